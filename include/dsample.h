@@ -10,7 +10,10 @@
  *
  * and the calls around them: ds_sample_ex (per-request ratios and iterations,
  * keep-ties mode), ds_reveal (confidence ranking and reveal), ds_merge_triples
- * (vocabulary-shard merge) and ds_log_softmax (dense log-probabilities). All are
+ * (vocabulary-shard merge) and ds_log_softmax (dense log-probabilities); and the
+ * serving head: ds_quantize_rows, ds_pack_i8 and ds_linear_i8 (hidden states to
+ * logits through an 8-bit vocabulary projection) and ds_sample_filtered (logits
+ * to tokens by temperature, top-k, top-p and min-p). All are
  * asynchronous on the caller's CUDA stream, allocate nothing and keep no state
  * between calls beyond a process-wide count of kernel launches
  * (ds_launch_count).
@@ -41,12 +44,16 @@ typedef enum {
 /* Bits OR-ed into *d_status by the kernels (device-detected input errors). */
 #define DS_DEV_ERR_LAYOUT 1u   /* sum(seq_lens) != P, or a negative seq_len */
 #define DS_DEV_ERR_NO_UNCOND 2u /* guidance != 0 for a request but u_logits == NULL */
-#define DS_DEV_ERR_PARAM 4u    /* temperature < 0 or NaN, or guidance NaN */
+#define DS_DEV_ERR_PARAM 4u    /* temperature < 0 or NaN, or guidance NaN; any parameter of ds_sample_filtered */
+#define DS_DEV_ERR_LOGITS 8u   /* ds_sample_filtered: a NaN or +inf among a row's logits */
+#define DS_DEV_ERR_TIMEOUT 16u /* ds_linear_i8: a wait inside the kernel ran out; the call's output is not valid */
 
 /* Limits of this build. */
 #define DS_MAX_ROWS 256          /* C: rows (codebooks) per call; the row index keys the noise */
 #define DS_MAX_ITERATION 16777215u /* iteration < 2^24; it keys the noise next to the row */
 #define DS_MAX_VOCAB 524281      /* largest V of ds_sample (16-CTA cluster, 32K elements per CTA) */
+#define DS_FILTERED_MAX_VOCAB 2097152 /* largest V of ds_sample_filtered: a row's mass stays below 2^53 */
+#define DS_LINEAR_MAX_K 131071   /* largest K of ds_linear_i8: K * 128 * 128 stays below 2^31 */
 
 /*
  * ds_sample -- sample every cell of a packed batch of guided logits.
@@ -263,6 +270,128 @@ ds_status ds_log_softmax(const void* logits, int32_t n, int32_t V, void* out, in
 ds_status ds_reveal(const float* scores, const int32_t* tokens, const int32_t* seq_lens,
                     const int32_t* reveal_counts, int32_t B, int32_t C, int32_t P, int32_t* canvas,
                     uint8_t* revealed, uint32_t* d_status, void* stream);
+
+/*
+ * ds_sample_filtered -- one token per row by temperature, top-k, top-p and
+ * min-p, from given uniform numbers.
+ *
+ * The serving sampler beside ds_sample: filters by count, by mass and by
+ * relative probability instead of by a ratio of the vocabulary, and the caller's
+ * own random numbers instead of keyed noise.
+ *
+ * Per row, with m = max x, r = min(1 / temperature, FLT_MAX) and the order
+ * (logit descending, id ascending; -0 and +0 tie), every logit has the integer
+ * weight w = rint(2^31 exp((x - m) r)), the exponential in fp32. Then
+ *   top_k   the first top_k of the order stay (<= 0 or >= V: all), of mass T;
+ *   top_p   of those, the ones with less than top_p * T before them;
+ *   min_p   of those, the ones with w >= min_p * 2^31;
+ * and the token is the first of the order whose running mass over what stays
+ * exceeds floor(u * mass). At least the first of the order always stays. Sums
+ * are exact, so a row's token depends on the row and its parameters alone, not
+ * on the batch. A token less probable than 2^-32 of the most probable one is
+ * never drawn.
+ *
+ * Arguments:
+ *   logits       device [n][V] of dtype, rows ld elements apart (ld >= V), any
+ *                alignment of the element type. -inf, or the type's lowest
+ *                value, masks a token.
+ *   dtype        DS_DTYPE_BF16 or DS_DTYPE_F32.
+ *   n, V         n >= 0 (0: nothing launched), 1 <= V <= DS_FILTERED_MAX_VOCAB.
+ *   temperature  device float [n], finite and >= 0; 0 returns the argmax
+ *                (smallest id on ties) whatever the filters.
+ *   top_k        device int32 [n], or NULL for none.
+ *   top_p        device float [n] in (0, 1], or NULL for 1.
+ *   min_p        device float [n] in [0, 1], or NULL for 0.
+ *   u            device float [n] in [0, 1).
+ *   out_tokens   device int32 [n].
+ *   out_logprobs device float [n]: x[token] - logsumexp(x) over the full,
+ *                unfiltered, untempered vocabulary, as ds_sample's.
+ *   d_status     device uint32 or NULL; the kernels OR DS_DEV_ERR_* bits into it.
+ *   stream       cudaStream_t.
+ * A row with nothing to draw (every logit -inf) gets token -1 and logprob NaN.
+ * So does a row with a parameter out of range (DS_DEV_ERR_PARAM) and one with a
+ * NaN or +inf (DS_DEV_ERR_LOGITS); other rows are not affected.
+ * Returns DS_OK, DS_ERR_INVALID_ARG, DS_ERR_UNSUPPORTED (V too large, ld > 2^40)
+ * or DS_ERR_CUDA.
+ */
+ds_status ds_sample_filtered(const void* logits, int32_t dtype, int32_t n, int32_t V, int64_t ld,
+                             const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                             const float* u, int32_t* out_tokens, float* out_logprobs, uint32_t* d_status,
+                             void* stream);
+
+/*
+ * ds_quantize_rows -- rows to 8-bit integers with one scale each, after an
+ * optional RMS norm.
+ *
+ *   y = x, or x * rsqrt(mean(x^2) + eps) * gain when gain is given (fp32)
+ *   scale = max|y| / 127,  q = rint(y * (127 / max|y|)) in [-127, 127]
+ * so that q * scale is y to within scale / 2. A row of zeros has scale 0. A row
+ * with a NaN or an infinity has scale NaN and q 0.
+ *
+ * Arguments:
+ *   x          device [n][K] of dtype, rows ld elements apart (ld >= K), any
+ *              alignment of the element type.
+ *   dtype      DS_DTYPE_BF16 or DS_DTYPE_F32.
+ *   n, K       n >= 0 (0: nothing launched), K >= 1.
+ *   gain       device float [K], or NULL for no norm (eps is then ignored).
+ *   out_q      device int8 [n][K], dense.
+ *   out_scale  device float [n].
+ *   stream     cudaStream_t.
+ * Returns DS_OK, DS_ERR_INVALID_ARG, DS_ERR_UNSUPPORTED (ld > 2^40) or DS_ERR_CUDA.
+ */
+ds_status ds_quantize_rows(const void* x, int32_t dtype, int32_t n, int32_t K, int64_t ld, const float* gain,
+                           float eps, int8_t* out_q, float* out_scale, void* stream);
+
+/* Bytes of the packed form of an int8 weight [N][K] (0: arguments out of range).
+ * Host-only, no CUDA call. */
+int64_t ds_packed_i8_bytes(int32_t N, int32_t K);
+
+/*
+ * ds_pack_i8 -- lay an int8 weight out for ds_linear_i8, once per weight.
+ *
+ *   w       device int8 [N][K], rows ldw bytes apart (ldw >= K), any alignment.
+ *   packed  device, ds_packed_i8_bytes(N, K) bytes, 16-byte aligned; its layout
+ *           is the library's own and may change between builds.
+ *   stream  cudaStream_t.
+ * Returns DS_OK, DS_ERR_INVALID_ARG, DS_ERR_UNSUPPORTED (K > DS_LINEAR_MAX_K,
+ * ldw > 2^40) or DS_ERR_CUDA.
+ */
+ds_status ds_pack_i8(const int8_t* w, int32_t N, int32_t K, int64_t ldw, void* packed, void* stream);
+
+/* Bytes of workspace that ds_linear_i8 needs for these sizes (0: none, or
+ * arguments out of range). Host-only, no CUDA call. */
+int64_t ds_linear_i8_workspace(int32_t n, int32_t N, int32_t K);
+
+/*
+ * ds_linear_i8 -- product of 8-bit integers with a scale for each row and
+ * channel: the vocabulary projection in front of the samplers.
+ *
+ *   out[i][j] = (sum over k of a[i][k] * w[j][k]) * a_scale[i] * w_scale[j]
+ *
+ * Products are exact and sums are kept in fp32: a sum is exact as long as its
+ * running value stays below 2^24, and rounded to fp32 beyond.
+ *
+ * Arguments:
+ *   a          device int8 [n][K], rows lda bytes apart (lda >= K), any alignment.
+ *   a_scale    device float [n].
+ *   packed     the weight as ds_pack_i8 laid it out for the same N and K.
+ *   w_scale    device float [N].
+ *   n, N, K    n >= 0 (0: nothing launched), N >= 1, 1 <= K <= DS_LINEAR_MAX_K.
+ *   out        device [n][N] of out_dtype, rows ldo elements apart (ldo >= N),
+ *              any alignment of the element type; what lies between the rows is
+ *              not written.
+ *   out_dtype  DS_DTYPE_BF16 (rounded to nearest even, once) or DS_DTYPE_F32.
+ *   workspace  device, workspace_bytes >= ds_linear_i8_workspace(n, N, K),
+ *              128-byte aligned (NULL when that is 0). Its contents need not be
+ *              kept between calls; calls that may run at once need one each.
+ *   d_status   device uint32 or NULL: DS_DEV_ERR_TIMEOUT.
+ *   stream     cudaStream_t.
+ * Returns DS_OK, DS_ERR_INVALID_ARG, DS_ERR_UNSUPPORTED (K, lda or ldo too
+ * large) or DS_ERR_CUDA.
+ */
+ds_status ds_linear_i8(const int8_t* a, int64_t lda, const float* a_scale, const void* packed, const float* w_scale,
+                       int32_t n, int32_t N, int32_t K, void* out, int32_t out_dtype, int64_t ldo, void* workspace,
+                       int64_t workspace_bytes, uint32_t* d_status, void* stream);
 
 /* Static description of a status code. Never NULL. */
 const char* ds_status_string(ds_status s);

@@ -1,0 +1,241 @@
+"""ds_quantize_rows, ds_pack_i8 and ds_linear_i8 against 64-bit arithmetic, and the whole head."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import vocab_wide_logit_gb300 as pkg
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def _dev():
+    assert torch.cuda.is_available(), "needs a GPU"
+    return torch.device("cuda", 0)
+
+
+# ------------------------------------------------------------------ quantisation
+def _check_quantised(x, gain, eps, q, scale):
+    """fp32 error of y * 127 / amax: the sum of squares (a tree over K terms), the root, three products and a quotient
+    stay below 16 roundings, so below 127 * 16 * 2^-24 = 1.3e-4 of a step; a q may be off its real value by half a step
+    and that."""
+    y = x.double()
+    if gain is not None:
+        y = y / torch.sqrt((y * y).mean(1, keepdim=True) + eps) * gain.double()
+    amax = y.abs().amax(1, keepdim=True)
+    real = torch.where(amax > 0, y * 127 / amax, torch.zeros_like(y))
+    assert int(q.abs().max()) <= 127
+    assert float((q.double() - real).abs().max()) <= 0.5 + 2e-4
+    np.testing.assert_allclose(scale.double().cpu().numpy(), (amax[:, 0] / 127).cpu().numpy(), rtol=16 * 2.0 ** -24,
+                               atol=0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,K", [(1, 1), (2, 3), (3, 31), (5, 64), (7, 257), (4, 1000), (33, 1024), (300, 2048), (3, 8191),
+                                 (2, 20001)])
+@pytest.mark.parametrize("norm", [False, True])
+def test_quantize_rows(n, K, dtype, norm):
+    dev = _dev()
+    g = torch.Generator().manual_seed(n + K)
+    x = (torch.randn((n, K), generator=g) * 3).to(DT[dtype]).to(dev)
+    if n > 2:
+        x[1] = 0
+        x[2] *= 1e-6
+    gain = (1 + 0.2 * torch.randn((K,), generator=g)).to(dev) if norm else None
+    q, scale = pkg.quantize_rows(x, gain=gain, eps=1e-5)
+    _check_quantised(x, gain, 1e-5, q, scale)
+    if n > 2:
+        assert float(scale[1]) == 0 and int(q[1].abs().max()) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K,pad,offset", [(64, 8, 0), (64, 3, 1), (1000, 1, 5), (1024, 0, 3)])
+def test_quantize_strided(K, pad, offset, dtype):
+    dev, n = _dev(), 9
+    g = torch.Generator().manual_seed(K)
+    buf = torch.randn((n * (K + pad) + offset,), generator=g).to(DT[dtype]).to(dev)
+    x = buf[offset:].view(n, K + pad)[:, :K]
+    q, scale = pkg.quantize_rows(x)
+    _check_quantised(x, None, 0.0, q, scale)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("norm", [False, True])
+def test_quantize_row_that_is_not_finite(bad, norm):
+    dev = _dev()
+    x = torch.randn((4, 500), generator=torch.Generator().manual_seed(1)).to(dev)
+    gain = torch.ones(500, device=dev) if norm else None
+    clean = pkg.quantize_rows(x, gain=gain)
+    x[2, 499] = bad
+    q, scale = pkg.quantize_rows(x, gain=gain)
+    assert torch.isnan(scale[2]) and int(q[2].abs().max()) == 0
+    for i in (0, 1, 3):
+        assert torch.equal(q[i], clean[0][i]) and scale[i] == clean[1][i]
+
+
+# ------------------------------------------------------------------ product
+def _operands(n, N, K, seed, kind="normal"):
+    g = torch.Generator().manual_seed(seed)
+    if kind == "normal":
+        a = torch.round(torch.randn((n, K), generator=g) * 36).clamp(-127, 127).to(torch.int8)
+        w = torch.round(torch.randn((N, K), generator=g) * 32).clamp(-127, 127).to(torch.int8)
+    elif kind == "all":  # every value of the type, -128 among them
+        a = torch.randint(-128, 128, (n, K), generator=g).to(torch.int8)
+        w = torch.randint(-128, 128, (N, K), generator=g).to(torch.int8)
+    else:  # the largest sums there are
+        a = torch.full((n, K), -128, dtype=torch.int8)
+        w = torch.full((N, K), -128, dtype=torch.int8)
+        w[1::2] = 127
+    sa = torch.rand((n,), generator=g) + 0.5
+    sw = (torch.rand((N,), generator=g) + 0.5) * 1e-3
+    return [t.to(_dev()) for t in (a, sa, w, sw)]
+
+
+def _exact(a, sa, w, sw):
+    s = a.double() @ w.double().t()
+    return s, s * sa.double()[:, None] * sw.double()[None]
+
+
+def _check(out, a, sa, w, sw, K):
+    """Sums are exact while their running value stays below 2^24; beyond, each of at most K additions rounds or
+    truncates by 2^-23 of it. Two products and the conversion round once each (2^-24), bf16 once more (7 stored bits: 2^-8)."""
+    s, want = _exact(a, sa, w, sw)
+    run = (a.double().abs() @ w.double().abs().t())
+    tol = torch.where(run < 2.0 ** 24, torch.zeros_like(run), run * K * 2.0 ** -23)
+    tol = tol * sa.double()[:, None] * sw.double()[None] + want.abs() * 4 * 2.0 ** -24
+    if out.dtype == torch.bfloat16:
+        tol = tol + want.abs() * 2.0 ** -8 * (1 + 2.0 ** -20)
+    off = (out.double() - want).abs()
+    assert bool((off <= tol).all()), float((off - tol).max())
+
+
+SIZES = [(1, 1, 1), (1, 128, 128), (2, 3, 5), (3, 129, 127), (5, 1025, 64), (7, 1025, 1000), (8, 8200, 1024), (16, 257, 2048),
+         (17, 300, 129), (33, 1025, 512), (64, 2000, 1024), (100, 513, 300), (128, 1025, 256), (129, 1025, 256),
+         (255, 640, 384), (256, 1025, 1024), (257, 1025, 1024), (600, 700, 640), (1030, 1025, 96)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,N,K", SIZES)
+def test_linear_i8(n, N, K, dtype):
+    a, sa, w, sw = _operands(n, N, K, n + N + K)
+    st = torch.zeros(1, dtype=torch.int32, device=_dev())
+    out = pkg.linear_i8(a, sa, pkg.pack_i8(w, sw), dtype=DT[dtype], d_status=st)
+    _check(out, a, sa, w, sw, K)
+    assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("n,N,K,kind", [(5, 300, 700, "all"), (40, 300, 1040, "all"), (200, 300, 4097, "all"),
+                                        (5, 130, 1000, "largest"), (70, 130, 5000, "largest"),
+                                        (300, 256, 1024, "largest")])
+def test_linear_i8_extremes(n, N, K, kind):
+    a, sa, w, sw = _operands(n, N, K, 3, kind)
+    out = pkg.linear_i8(a, sa, pkg.pack_i8(w, sw), dtype=torch.float32)
+    _check(out, a, sa, w, sw, K)
+
+
+@pytest.mark.parametrize("n", [1, 6, 40, 150, 300])
+def test_linear_i8_many_channel_blocks(n):
+    """More channel blocks than the GPU has SMs, so that a CTA takes several."""
+    a, sa, w, sw = _operands(n, 41000, 192, 11)
+    out = pkg.linear_i8(a, sa, pkg.pack_i8(w, sw), dtype=torch.float32)
+    _check(out, a, sa, w, sw, 192)
+
+
+@pytest.mark.parametrize("n,N,K,pa,pw,po", [(3, 200, 100, 1, 3, 5), (20, 200, 100, 28, 0, 1), (140, 333, 129, 7, 7, 3)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_linear_i8_strides(n, N, K, pa, pw, po, dtype):
+    """Operands and results whose rows lie apart, at odd addresses; what lies between them is left alone."""
+    dev = _dev()
+    a, sa, w, sw = _operands(n, N, K, 5)
+    ab = torch.full((n * (K + pa) + 1,), 77, dtype=torch.int8, device=dev)
+    av = ab[1:].view(n, K + pa)[:, :K]
+    av.copy_(a)
+    wb = torch.full((N * (K + pw) + 3,), 77, dtype=torch.int8, device=dev)
+    wv = wb[3:].view(N, K + pw)[:, :K]
+    wv.copy_(w)
+    ob = torch.full((n * (N + po) + 1,), 5.0, dtype=DT[dtype], device=dev)
+    ov = ob[1:].view(n, N + po)
+    out = pkg.linear_i8(av, sa, pkg.pack_i8(wv, sw), out=ov[:, :N])
+    _check(out, a, sa, w, sw, K)
+    assert bool((ov[:, N:] == 5.0).all()) and float(ob[0]) == 5.0
+
+
+def test_linear_i8_repeats_and_streams():
+    """One packed weight used from two streams at once; equal inputs give equal bits."""
+    a, sa, w, sw = _operands(50, 3000, 768, 21)
+    b, sb, _, _ = _operands(13, 3000, 768, 22)
+    p = pkg.pack_i8(w, sw)
+    want = pkg.linear_i8(a, sa, p), pkg.linear_i8(b, sb, p)
+    torch.cuda.synchronize()
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(5):
+        got.append((pkg.linear_i8(a, sa, p, stream=s[0]), pkg.linear_i8(b, sb, p, stream=s[1])))
+    torch.cuda.synchronize()
+    for g in got:
+        assert torch.equal(g[0], want[0]) and torch.equal(g[1], want[1])
+
+
+def test_linear_i8_scale_that_is_not_finite_stays_in_its_row():
+    a, sa, w, sw = _operands(20, 300, 256, 31)
+    p = pkg.pack_i8(w, sw)
+    want = pkg.linear_i8(a, sa, p)
+    sa[7] = math.nan
+    out = pkg.linear_i8(a, sa, p)
+    assert bool(torch.isnan(out[7]).all())
+    assert torch.equal(out[:7], want[:7]) and torch.equal(out[8:], want[8:])
+
+
+def test_empty_calls():
+    dev = _dev()
+    _, _, w, sw = _operands(1, 10, 20, 1)
+    out = pkg.linear_i8(torch.empty((0, 20), dtype=torch.int8, device=dev), torch.empty(0, device=dev),
+                        pkg.pack_i8(w, sw))
+    assert tuple(out.shape) == (0, 10)
+    q, s = pkg.quantize_rows(torch.empty((0, 20), device=dev))
+    assert tuple(q.shape) == (0, 20) and s.numel() == 0
+
+
+# ------------------------------------------------------------------ together
+@pytest.mark.parametrize("n,N,K", [(1, 1025, 512), (9, 4097, 768), (150, 1025, 1024)])
+def test_head_close_to_the_unquantised_product(n, N, K):
+    """Each operand is off by at most half a step of amax / 127 uniformly, so a logit's error is about
+    sqrt(K) * (rms of the other operand) * step / sqrt(12) for each; eight times that covers the largest of them."""
+    dev = _dev()
+    g = torch.Generator().manual_seed(n)
+    h = torch.randn((n, K), generator=g).to(torch.bfloat16).to(dev)
+    W = (torch.randn((N, K), generator=g) / math.sqrt(K)).to(dev)
+    gain = (1 + 0.1 * torch.randn((K,), generator=g)).to(dev)
+    head = pkg.Int8Head.from_weight(W, gain=gain)
+    out = head.logits(h, dtype=torch.float32).double()
+    y = h.double()
+    y = y / torch.sqrt((y * y).mean(1, keepdim=True) + 1e-6) * gain.double()
+    want = y @ W.double().t()
+    step_y = y.abs().amax(1, keepdim=True) / 127
+    step_w = W.double().abs().amax(1)[None] / 127
+    rms = lambda t: t.double().square().mean(1).sqrt()  # noqa: E731
+    sd = math.sqrt(K / 12) * (step_y * rms(W)[None] + rms(y)[:, None] * step_w)
+    assert float(((out - want).abs() / sd).max()) <= 8
+
+    one = torch.ones(n, device=dev)
+    tok, lp = head.sample(h, one * 0, one * 0)
+    assert torch.equal(tok.long(), head.logits(h).float().argmax(1))
+    want_lp = torch.log_softmax(head.logits(h).double(), 1).gather(1, tok.long()[:, None])[:, 0]
+    assert float((lp.double() - want_lp).abs().max()) <= 1e-4
+
+
+def test_head_reports_a_bad_hidden_state():
+    dev = _dev()
+    g = torch.Generator().manual_seed(4)
+    h = torch.randn((5, 256), generator=g).to(dev)
+    head = pkg.Int8Head.from_weight(torch.randn((600, 256), generator=g).to(dev))
+    h[3, 9] = math.nan
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    one = torch.ones(5, device=dev)
+    tok, lp = head.sample(h, one, one * 0.5, d_status=st)
+    assert int(st.item()) == pkg.DS_DEV_ERR_LOGITS
+    assert int(tok[3]) == -1 and bool(torch.isnan(lp[3]))
+    assert bool((tok[[0, 1, 2, 4]] >= 0).all())

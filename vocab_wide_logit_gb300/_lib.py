@@ -18,10 +18,15 @@ DS_ERR_CUDA = 3
 DS_DEV_ERR_LAYOUT = 1
 DS_DEV_ERR_NO_UNCOND = 2
 DS_DEV_ERR_PARAM = 4
+DS_DEV_ERR_LOGITS = 8
+DS_DEV_ERR_TIMEOUT = 16
 DS_MAX_VOCAB = 524281
+DS_FILTERED_MAX_VOCAB = 2097152
+DS_LINEAR_MAX_K = 131071
 
 EXPORTED = ("ds_sample", "ds_greedy_lse", "ds_status_string", "ds_top_k", "ds_merge_triples", "ds_log_softmax",
-            "ds_reveal", "ds_sample_ex", "ds_launch_count")
+            "ds_reveal", "ds_sample_ex", "ds_launch_count", "ds_sample_filtered", "ds_quantize_rows",
+            "ds_packed_i8_bytes", "ds_pack_i8", "ds_linear_i8_workspace", "ds_linear_i8")
 DS_FLAG_KEEP_TIES = 1
 DS_FLAG_SKIP_EXACT_PASS = 2
 DS_MARKED = -2
@@ -66,6 +71,19 @@ def load(path: str = LIB_PATH):
     L.ds_sample_ex.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, f32, u64, vp, u32, u32, vp, vp, vp,
                                vp]
     L.ds_sample_ex.restype = ctypes.c_int
+    i64 = ctypes.c_int64
+    L.ds_sample_filtered.argtypes = [vp, i32, i32, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.ds_sample_filtered.restype = ctypes.c_int
+    L.ds_quantize_rows.argtypes = [vp, i32, i32, i32, i64, vp, f32, vp, vp, vp]
+    L.ds_quantize_rows.restype = ctypes.c_int
+    L.ds_packed_i8_bytes.argtypes = [i32, i32]
+    L.ds_packed_i8_bytes.restype = i64
+    L.ds_pack_i8.argtypes = [vp, i32, i32, i64, vp, vp]
+    L.ds_pack_i8.restype = ctypes.c_int
+    L.ds_linear_i8_workspace.argtypes = [i32, i32, i32]
+    L.ds_linear_i8_workspace.restype = i64
+    L.ds_linear_i8.argtypes = [vp, i64, vp, vp, vp, i32, i32, i32, vp, i32, i64, vp, i64, vp, vp]
+    L.ds_linear_i8.restype = ctypes.c_int
     _lib = L
     return L
 
@@ -175,4 +193,84 @@ def ds_reveal(scores, tokens, seq_lens, reveal_counts, canvas, revealed=None, d_
                           int(P), _ptr(canvas), _ptr(revealed), _ptr(d_status), _stream(stream))
     if check and rc != DS_OK:
         raise DsError("ds_reveal", rc)
+    return rc
+
+
+def _dtype_code(t):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return DS_DTYPE_BF16
+    if t.dtype == torch.float32:
+        return DS_DTYPE_F32
+    raise TypeError("bfloat16 or float32 expected, got %s" % t.dtype)
+
+
+def ds_sample_filtered(logits, temperature, u, out_tokens, out_logprobs, top_k=None, top_p=None, min_p=None,
+                       d_status=None, n=None, V=None, ld=None, stream=None, check=True):
+    """Call ds_sample_filtered: logits [n, V] bfloat16 or float32 (rows ld elements apart), temperature / u / top_p /
+    min_p float32 [n], top_k int32 [n], out_tokens int32 [n], out_logprobs float32 [n]."""
+    if n is None:
+        n, V = logits.shape
+    if ld is None:
+        ld = logits.stride(0) if n > 1 else V
+    rc = load().ds_sample_filtered(logits.data_ptr(), _dtype_code(logits), n, V, ld, _ptr(temperature), _ptr(top_k),
+                                   _ptr(top_p), _ptr(min_p), _ptr(u), _ptr(out_tokens), _ptr(out_logprobs),
+                                   _ptr(d_status), _stream(stream))
+    if check and rc != DS_OK:
+        raise DsError("ds_sample_filtered", rc)
+    return rc
+
+
+def ds_quantize_rows(x, out_q, out_scale, gain=None, eps=1e-6, n=None, K=None, ld=None, stream=None, check=True):
+    """Call ds_quantize_rows: x [n, K] bfloat16 or float32, gain float32 [K] or None, out_q int8 [n, K] dense,
+    out_scale float32 [n]."""
+    if n is None:
+        n, K = x.shape
+    if ld is None:
+        ld = x.stride(0) if n > 1 else K
+    rc = load().ds_quantize_rows(x.data_ptr(), _dtype_code(x), n, K, ld, _ptr(gain), float(eps), _ptr(out_q),
+                                 _ptr(out_scale), _stream(stream))
+    if check and rc != DS_OK:
+        raise DsError("ds_quantize_rows", rc)
+    return rc
+
+
+def packed_i8_bytes(N: int, K: int) -> int:
+    return int(load().ds_packed_i8_bytes(int(N), int(K)))
+
+
+def linear_i8_workspace(n: int, N: int, K: int) -> int:
+    return int(load().ds_linear_i8_workspace(int(n), int(N), int(K)))
+
+
+def ds_pack_i8(w, packed, N=None, K=None, ldw=None, stream=None, check=True):
+    """Call ds_pack_i8: w int8 [N, K], packed uint8 [ds_packed_i8_bytes(N, K)]."""
+    if N is None:
+        N, K = w.shape
+    if ldw is None:
+        ldw = w.stride(0) if N > 1 else K
+    rc = load().ds_pack_i8(_ptr(w), N, K, ldw, _ptr(packed), _stream(stream))
+    if check and rc != DS_OK:
+        raise DsError("ds_pack_i8", rc)
+    return rc
+
+
+def ds_linear_i8(a, a_scale, packed, w_scale, out, N, K, workspace=None, d_status=None, n=None, lda=None, ldo=None,
+                 out_dtype=None, workspace_bytes=None, stream=None, check=True):
+    """Call ds_linear_i8: a int8 [n, K], a_scale float32 [n], packed uint8 (ds_pack_i8), w_scale float32 [N], out
+    [n, N] bfloat16 or float32, workspace uint8 of ds_linear_i8_workspace(n, N, K) bytes or None."""
+    if n is None:
+        n = a.shape[0]
+    if lda is None:
+        lda = a.stride(0) if n > 1 else K
+    if ldo is None:
+        ldo = out.stride(0) if n > 1 else N
+    if out_dtype is None:
+        out_dtype = _dtype_code(out)
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    rc = load().ds_linear_i8(a.data_ptr(), lda, _ptr(a_scale), _ptr(packed), _ptr(w_scale), n, N, K, _ptr(out),
+                             out_dtype, ldo, _ptr(workspace), workspace_bytes, _ptr(d_status), _stream(stream))
+    if check and rc != DS_OK:
+        raise DsError("ds_linear_i8", rc)
     return rc

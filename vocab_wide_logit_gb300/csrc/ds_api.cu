@@ -250,4 +250,82 @@ ds_status ds_reveal(const float* scores, const int32_t* tokens, const int32_t* s
   return e == cudaSuccess ? DS_OK : DS_ERR_CUDA;
 }
 
+ds_status ds_sample_filtered(const void* logits, int32_t dtype, int32_t n, int32_t V, int64_t ld,
+                             const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                             const float* u, int32_t* out_tokens, float* out_logprobs, uint32_t* d_status,
+                             void* stream) {
+  if (n < 0 || V < 1 || ld < V) return DS_ERR_INVALID_ARG;
+  if (dtype != DS_DTYPE_F32 && dtype != DS_DTYPE_BF16) return DS_ERR_INVALID_ARG;
+  if (n == 0) return DS_OK;
+  if (!logits || !temperature || !u || !out_tokens || !out_logprobs) return DS_ERR_INVALID_ARG;
+  const uintptr_t words = reinterpret_cast<uintptr_t>(temperature) | reinterpret_cast<uintptr_t>(top_k) |
+                          reinterpret_cast<uintptr_t>(top_p) | reinterpret_cast<uintptr_t>(min_p) |
+                          reinterpret_cast<uintptr_t>(u) | reinterpret_cast<uintptr_t>(out_tokens) |
+                          reinterpret_cast<uintptr_t>(out_logprobs) | reinterpret_cast<uintptr_t>(d_status);
+  if ((words & 3) || (reinterpret_cast<uintptr_t>(logits) & (dtype == DS_DTYPE_F32 ? 3 : 1))) return DS_ERR_INVALID_ARG;
+  if (V > DS_FILTERED_MAX_VOCAB || ld > (1LL << 40)) return DS_ERR_UNSUPPORTED;
+  const ds::FilteredArgs a = {logits, ld,    n, V, temperature, top_k,       top_p,
+                              min_p,  u, out_tokens, out_logprobs, d_status};
+  const cudaError_t e = ds::launch_sample_filtered(a, dtype == DS_DTYPE_F32, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DS_OK : DS_ERR_CUDA;
+}
+
+ds_status ds_quantize_rows(const void* x, int32_t dtype, int32_t n, int32_t K, int64_t ld, const float* gain,
+                           float eps, int8_t* out_q, float* out_scale, void* stream) {
+  if (n < 0 || K < 1 || ld < K) return DS_ERR_INVALID_ARG;
+  if (dtype != DS_DTYPE_F32 && dtype != DS_DTYPE_BF16) return DS_ERR_INVALID_ARG;
+  if (gain && !(eps >= 0.f && eps < INFINITY)) return DS_ERR_INVALID_ARG;
+  if (n == 0) return DS_OK;
+  if (!x || !out_q || !out_scale) return DS_ERR_INVALID_ARG;
+  if (((reinterpret_cast<uintptr_t>(gain) | reinterpret_cast<uintptr_t>(out_scale)) & 3) ||
+      (reinterpret_cast<uintptr_t>(x) & (dtype == DS_DTYPE_F32 ? 3 : 1)))
+    return DS_ERR_INVALID_ARG;
+  if (ld > (1LL << 40)) return DS_ERR_UNSUPPORTED;
+  const cudaError_t e = ds::launch_quantize_rows(x, dtype == DS_DTYPE_F32, n, K, ld, gain, eps, out_q, out_scale,
+                                                 static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DS_OK : DS_ERR_CUDA;
+}
+
+int64_t ds_packed_i8_bytes(int32_t N, int32_t K) {
+  if (N < 1 || K < 1 || K > DS_LINEAR_MAX_K) return 0;
+  const int64_t rows = ((int64_t)N + ds::kPackRows - 1) / ds::kPackRows * ds::kPackRows;
+  return rows * (((int64_t)K + ds::kPackK - 1) / ds::kPackK * ds::kPackK);
+}
+
+ds_status ds_pack_i8(const int8_t* w, int32_t N, int32_t K, int64_t ldw, void* packed, void* stream) {
+  if (N < 1 || K < 1 || ldw < K || !w || !packed) return DS_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(packed) & 15) return DS_ERR_INVALID_ARG;
+  if (K > DS_LINEAR_MAX_K || ldw > (1LL << 40)) return DS_ERR_UNSUPPORTED;
+  const cudaError_t e =
+      ds::launch_pack_i8(w, N, K, ldw, static_cast<uint8_t*>(packed), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DS_OK : DS_ERR_CUDA;
+}
+
+int64_t ds_linear_i8_workspace(int32_t n, int32_t N, int32_t K) {
+  if (n < 1 || N < 1 || K < 1 || K > DS_LINEAR_MAX_K) return 0;
+  return ds::linear_i8_workspace(n, N, K);
+}
+
+ds_status ds_linear_i8(const int8_t* a, int64_t lda, const float* a_scale, const void* packed, const float* w_scale,
+                       int32_t n, int32_t N, int32_t K, void* out, int32_t out_dtype, int64_t ldo, void* workspace,
+                       int64_t workspace_bytes, uint32_t* d_status, void* stream) {
+  if (n < 0 || N < 1 || K < 1 || lda < K || ldo < N) return DS_ERR_INVALID_ARG;
+  if (out_dtype != DS_DTYPE_F32 && out_dtype != DS_DTYPE_BF16) return DS_ERR_INVALID_ARG;
+  if (K > DS_LINEAR_MAX_K || lda > (1LL << 40) || ldo > (1LL << 40)) return DS_ERR_UNSUPPORTED;
+  if (n == 0) return DS_OK;
+  if (!a || !a_scale || !packed || !w_scale || !out) return DS_ERR_INVALID_ARG;
+  if (((reinterpret_cast<uintptr_t>(a_scale) | reinterpret_cast<uintptr_t>(w_scale) |
+        reinterpret_cast<uintptr_t>(d_status)) & 3) ||
+      (reinterpret_cast<uintptr_t>(packed) & 15) ||
+      (reinterpret_cast<uintptr_t>(out) & (out_dtype == DS_DTYPE_F32 ? 3 : 1)))
+    return DS_ERR_INVALID_ARG;
+  const int64_t need = ds::linear_i8_workspace(n, N, K);
+  if (need > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 127)))
+    return DS_ERR_INVALID_ARG;
+  const ds::LinearArgs g = {a, lda, a_scale, static_cast<const uint8_t*>(packed), w_scale, n, N, K, out, ldo,
+                            workspace, d_status};
+  const cudaError_t e = ds::launch_linear_i8(g, out_dtype == DS_DTYPE_BF16, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DS_OK : DS_ERR_CUDA;
+}
+
 }  // extern "C"

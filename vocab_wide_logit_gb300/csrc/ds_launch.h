@@ -67,4 +67,49 @@ bool log_softmax_fused_fits(int V);
 cudaError_t launch_log_softmax_fused(const uint16_t* x, int n, int V, float* out_max, float* out_lse,
                                      int* out_argmax, void* out, bool bf16_out, cudaStream_t st, bool* refused);
 
+// Filtered sampling of n rows of V logits, ld elements apart.
+struct FilteredArgs {
+  const void* x;  // bf16 or fp32
+  int64_t ld;
+  int32_t n, V;
+  const float* temperature;
+  const int32_t* top_k;  // or null
+  const float* top_p;    // or null
+  const float* min_p;    // or null
+  const float* u;
+  int32_t* out_tokens;
+  float* out_logprobs;
+  uint32_t* d_status;
+};
+cudaError_t launch_sample_filtered(const FilteredArgs& a, bool f32, cudaStream_t st);
+
+// Rows of x (optionally RMS-normalised) to int8 with one scale per row.
+cudaError_t launch_quantize_rows(const void* x, bool f32, int n, int K, int64_t ld, const float* gain, float eps,
+                                 int8_t* q, float* scale, cudaStream_t st);
+
+// The packed form of an int8 weight [N][K]: blocks of kPackRows channels x
+// kPackK inputs, 16 KB each, block (channels / kPackRows, inputs / kPackK) at
+// index (channel block) * (input blocks) + (input block). In a block, channel r
+// has 128 bytes at r * 128; its 16-byte chunk c stands at chunk c ^ (r & 7), so
+// that eight threads reading the same chunk of eight channels meet no bank
+// twice. Bytes hold w + 128, channels and inputs beyond N and K hold 128 (zero).
+constexpr int kPackRows = 128;
+constexpr int kPackK = 128;
+cudaError_t launch_pack_i8(const int8_t* w, int N, int K, int64_t ldw, uint8_t* packed, cudaStream_t st);
+
+struct LinearArgs {
+  const int8_t* a;
+  int64_t lda;
+  const float* a_scale;
+  const uint8_t* packed;
+  const float* w_scale;
+  int32_t n, N, K;
+  void* out;
+  int64_t ldo;
+  void* workspace;
+  uint32_t* d_status;
+};
+long long linear_i8_workspace(int n, int N, int K);
+cudaError_t launch_linear_i8(const LinearArgs& a, bool bf16_out, cudaStream_t st);
+
 }  // namespace ds
