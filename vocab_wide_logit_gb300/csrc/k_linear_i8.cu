@@ -1,6 +1,7 @@
 // k_linear_i8.cu -- product of 8-bit integers scaled by row and channel:
 // out[i][j] = (sum_k a[i][k] w[j][k]) * a_scale[i] * w_scale[j].
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "ds_device.cuh"
 #include "ds_launch.h"
@@ -8,8 +9,6 @@
 namespace ds {
 
 namespace {
-
-constexpr int kLiRows = 8;  // rows of a per CTA
 
 __device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
@@ -43,48 +42,385 @@ __global__ void __launch_bounds__(256) k_pack_i8(const int8_t* w, int N, int K, 
   }
 }
 
-// One thread per channel, kLiRows rows of a: exact sums by four-way integer dot products.
-template <typename OUT>
-__global__ void __launch_bounds__(kPackRows) k_linear_i8(LinearArgs g) {
+// The rows of a as fp16 in the order that the product reads: [row tile][block of
+// 64 inputs][row][128 bytes], 16-byte chunk c of row i at chunk c ^ (i & 7) (the
+// 128-byte swizzle of the matrix descriptors). Rows past n and inputs past K are
+// zero: a zero weight does not cancel a NaN left in the workspace.
+__global__ void __launch_bounds__(256) k_expand_i8(const int8_t* a, long long lda, int n, int K, int rows, int tiles,
+                                                   int kb64, uint4* out) {
   pdl_wait();
   pdl_release();
-  __shared__ int as[kLiRows][kPackK / 4];
-  const int kb = (g.K + kPackK - 1) / kPackK;
-  const int r = threadIdx.x;
-  const long long j = (long long)blockIdx.x * kPackRows + r;
-  for (int i0 = blockIdx.y * kLiRows; i0 < g.n; i0 += gridDim.y * kLiRows) {
-    int acc[kLiRows] = {};
-    for (int b = 0; b < kb; ++b) {
-      __syncthreads();
-      for (int e = r; e < kLiRows * kPackK; e += kPackRows) {
-        const int i = i0 + e / kPackK, k = b * kPackK + e % kPackK;
-        reinterpret_cast<int8_t*>(as)[e] = (i < g.n && k < g.K) ? g.a[(long long)i * g.lda + k] : (int8_t)0;
-      }
-      __syncthreads();
-      const uint4* blk =
-          reinterpret_cast<const uint4*>(g.packed + ((long long)blockIdx.x * kb + b) * (kPackRows * kPackK)) + r * 8;
+  const long long chunks = (long long)tiles * kb64 * rows * 8;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < chunks; i += (long long)gridDim.x * 256) {
+    const int c = (int)(i & 7);
+    const long long q = i >> 3;
+    const int r = (int)(q % rows);
+    const int b = (int)(q / rows % kb64);
+    const long long row = q / rows / kb64 * rows + r;
+    const int k0 = b * 64 + ((c ^ (r & 7)) << 3);
+    __half h[8];
+    const int8_t* src = a + row * lda + k0;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const uint4 v = blk[c ^ (r & 7)];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int i = 0; i < kLiRows; ++i) acc[i] = __dp4a((int)(w[q] ^ 0x80808080u), as[i][c * 4 + q], acc[i]);
-      }
-    }
-    if (j < g.N) {
-      const float sw = g.w_scale[j];
-#pragma unroll
-      for (int i = 0; i < kLiRows; ++i)
-        if (i0 + i < g.n)
-          store_out(static_cast<OUT*>(g.out) + (long long)(i0 + i) * g.ldo + j,
-                    (float)acc[i] * g.a_scale[i0 + i] * sw);
-    }
+    for (int j = 0; j < 8; ++j) h[j] = __int2half_rn((row < n && k0 + j < K) ? (int)src[j] : 0);
+    out[i] = *reinterpret_cast<const uint4*>(h);
   }
 }
 
-long long linear_i8_workspace(int, int, int) { return 0; }
+namespace {
+
+// ------------------------------------------------------------ tensor-core helpers
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void mbar_init(uint64_t* b, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* b) {
+  asm volatile("{\n.reg .b64 t;\nmbarrier.arrive.shared::cta.b64 t, [%0];\n}" ::"r"(smem_u32(b)) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint64_t* b, uint32_t bytes) {
+  asm volatile("{\n.reg .b64 t;\nmbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1;\n}" ::"r"(smem_u32(b)),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Every wait gives up after a while: it raises the CTA's stop flag, which ends
+// the other waits too, and the caller leaves its loop.
+__device__ __noinline__ bool mbar_wait_slow(uint64_t* b, uint32_t parity, volatile int* stop) {
+  for (int i = 0; i < (1 << 20); ++i) {
+    if (mbar_try(b, parity)) return true;
+    if (*stop) return false;
+  }
+  *stop = 1;
+  return false;
+}
+__device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity, volatile int* stop) {
+  return mbar_try(b, parity) || mbar_wait_slow(b, parity, stop);
+}
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// D[128][N] (+)= A[128][16] B[N][16]^T: A in tensor memory, B in shared memory.
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tc_ld16(uint32_t addr, float (&f)[16]) {
+  uint32_t v[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]);
+}
+
+// Matrix descriptor of a K-major tile with 128-byte swizzle: 8-row groups 1024
+// bytes apart.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t addr) {
+  return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// Four biased bytes b = w + 128 to four fp16 values w: 0x6400 | b is 1024 + b,
+// and 1024 + b - 1152 is exact.
+__device__ __forceinline__ void widen4(uint32_t b, uint32_t& lo, uint32_t& hi) {
+  const __half2 bias = __half2half2(__ushort_as_half((unsigned short)0x6480));
+  uint32_t l, h;
+  asm("prmt.b32 %0, %1, %2, 0x4140;" : "=r"(l) : "r"(b), "r"(0x64646464u));
+  asm("prmt.b32 %0, %1, %2, 0x4342;" : "=r"(h) : "r"(b), "r"(0x64646464u));
+  const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&l), bias), y = __hsub2(*reinterpret_cast<__half2*>(&h), bias);
+  lo = *reinterpret_cast<const uint32_t*>(&x);
+  hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+constexpr int kTcEpi = 4;   // warps 0-3: results out of tensor memory
+constexpr int kTcCvt = 8;   // warps 4-11: int8 weights to fp16, two groups of four
+constexpr int kTcWarps = kTcEpi + kTcCvt + 3;  // then: weight loads, row loads, matrix instructions
+constexpr int kTcNT = kTcWarps * 32;
+constexpr int kTcBlock = kPackRows * kPackK;  // bytes of a weight block
+constexpr int kTcWSlots = 12;                 // most weight slots
+constexpr int kTcBSlots = 64;                 // most row-tile slots
+constexpr int kTcASlots = 4;                  // fp16 weight blocks in tensor memory, 64 columns each
+constexpr int kTcACol = 256;                  // their first column; accumulators are below
+constexpr size_t kTcSmem = 232448 - 2048;     // dynamic shared memory of a CTA, barriers apart
+
+// How a call of n rows is cut: row tiles of `rows` (a multiple of 16, at most
+// 256), their slots in shared memory, and whether all of a tile's slots stay
+// there for every channel block.
+struct TcPlan {
+  int rows, tiles, kb, b_slots, w_slots, resident;
+};
+
+}  // namespace
+
+static TcPlan tc_plan(int n, int K) {
+  TcPlan p;
+  p.tiles = (n + 255) / 256;
+  p.rows = ((n + p.tiles - 1) / p.tiles + 15) / 16 * 16;
+  p.kb = (K + kPackK - 1) / kPackK;
+  const long long slot = (long long)p.rows * 128, all = slot * 2 * p.kb, room = (long long)kTcSmem - 1024;
+  p.resident = p.tiles == 1 && 2 * p.kb <= kTcBSlots && all + 5 * kTcBlock <= room;
+  p.b_slots = p.resident ? 2 * p.kb : 4;
+  const long long w = (room - slot * p.b_slots) / kTcBlock;
+  p.w_slots = (int)(w < kTcWSlots ? w : kTcWSlots);
+  return p;
+}
+
+// One CTA per SM walks tiles of 128 channels x `rows` rows of a.
+template <typename OUT>
+__global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan p) {
+  extern __shared__ uint8_t dyn[];
+  __shared__ uint64_t w_full[kTcWSlots], w_empty[kTcWSlots], b_full[kTcBSlots], b_empty[kTcBSlots];
+  __shared__ uint64_t a_full[kTcASlots], a_empty[kTcASlots], d_full[2], d_empty[2], drained;
+  __shared__ uint32_t tmem_base;
+  __shared__ int stop_flag;
+  volatile int* stop = &stop_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* bs = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
+  const uint32_t b_bytes = (uint32_t)p.rows * 128u;
+  uint8_t* ws = bs + (size_t)b_bytes * p.b_slots;
+  const int d_bufs = p.rows <= 128 ? 2 : 1;
+
+  if (threadIdx.x == 0) {
+    stop_flag = 0;
+    for (int i = 0; i < kTcWSlots; ++i) {
+      mbar_init(&w_full[i], 1);
+      mbar_init(&w_empty[i], 4);
+    }
+    for (int i = 0; i < kTcBSlots; ++i) {
+      mbar_init(&b_full[i], 1);
+      mbar_init(&b_empty[i], 1);
+    }
+    for (int i = 0; i < kTcASlots; ++i) {
+      mbar_init(&a_full[i], 4);
+      mbar_init(&a_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&d_full[i], 1);
+      mbar_init(&d_empty[i], 4);
+    }
+    mbar_init(&drained, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_base))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  pdl_wait();
+  pdl_release();
+
+  const int kb = p.kb;
+  const long long n_tiles = (long long)((g.N + kPackRows - 1) / kPackRows) * p.tiles;
+
+  if (warp == kTcEpi + kTcCvt) {
+    // ---- weight blocks, in the order they are used
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (long long t = blockIdx.x; ok && t < n_tiles; t += gridDim.x) {
+        const uint8_t* src = g.packed + (t / p.tiles) * kb * (long long)kTcBlock;
+        for (int b = 0; b < kb; ++b, ++it) {
+          const uint32_t s = it % p.w_slots, round = it / p.w_slots;
+          if (round > 0 && !mbar_wait(&w_empty[s], (round - 1) & 1, stop)) {
+            ok = false;
+            break;
+          }
+          mbar_expect(&w_full[s], kTcBlock);
+          bulk_load(ws + (size_t)s * kTcBlock, src + (long long)b * kTcBlock, kTcBlock, &w_full[s]);
+        }
+      }
+      // given up: no copy may be in flight when the CTA leaves
+      if (!ok)
+        for (uint32_t j = it > (uint32_t)p.w_slots ? it - p.w_slots : 0; j < it; ++j)
+          for (int i = 0; i < (1 << 20) && !mbar_try(&w_full[j % p.w_slots], (j / p.w_slots) & 1); ++i) {
+          }
+    }
+  } else if (warp == kTcEpi + kTcCvt + 1) {
+    // ---- row tiles
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      const uint8_t* base = static_cast<const uint8_t*>(g.workspace);
+      for (long long t = blockIdx.x; ok && t < n_tiles; t += gridDim.x) {
+        if (p.resident && it > 0) break;
+        const uint8_t* src = base + (t % p.tiles) * (2 * kb) * (long long)b_bytes;
+        for (int b = 0; b < 2 * kb; ++b, ++it) {
+          const uint32_t s = it % p.b_slots, round = it / p.b_slots;
+          if (round > 0 && !mbar_wait(&b_empty[s], (round - 1) & 1, stop)) {
+            ok = false;
+            break;
+          }
+          mbar_expect(&b_full[s], b_bytes);
+          bulk_load(bs + (size_t)s * b_bytes, src + (long long)b * b_bytes, b_bytes, &b_full[s]);
+        }
+      }
+      if (!ok)
+        for (uint32_t j = it > (uint32_t)p.b_slots ? it - p.b_slots : 0; j < it; ++j)
+          for (int i = 0; i < (1 << 20) && !mbar_try(&b_full[j % p.b_slots], (j / p.b_slots) & 1); ++i) {
+          }
+    }
+  } else if (warp == kTcEpi + kTcCvt + 2) {
+    // ---- matrix instructions, by one thread
+    if (lane == 0) {
+      // fp32 accumulators, fp16 operands, M = 128, N = rows
+      const uint32_t idesc = (1u << 4) | ((uint32_t)(p.rows >> 3) << 17) | ((uint32_t)(kPackRows >> 4) << 24);
+      uint32_t ia = 0, ib = 0, id = 0;
+      bool ok = true;
+      for (long long t = blockIdx.x; ok && t < n_tiles; t += gridDim.x, ++id) {
+        const uint32_t buf = id % d_bufs, use = id / d_bufs;
+        if (use > 0 && !mbar_wait(&d_empty[buf], (use - 1) & 1, stop)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + buf * 128u;
+        const bool loaded = p.resident && id > 0;  // the row tile is there already
+        for (int b = 0; ok && b < kb; ++b, ++ia) {
+          const uint32_t sa = ia % kTcASlots;
+          ok = mbar_wait(&a_full[sa], (ia / kTcASlots) & 1, stop);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t acol = tmem + kTcACol + sa * 64u;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t sb = p.resident ? (uint32_t)(2 * b + h) : ib % p.b_slots;
+            if (!loaded) {
+              ok = mbar_wait(&b_full[sb], p.resident ? 0u : (ib / p.b_slots) & 1, stop);
+              if (!ok) break;
+            }
+            const uint64_t bd = sw128_desc(smem_u32(bs) + sb * b_bytes);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc_mma(d, acol + (uint32_t)(h * 32 + k * 8), bd + (uint64_t)(k * 2), idesc, (b | h | k) ? 1u : 0u);
+            if (!p.resident) tc_commit(&b_empty[sb]);
+            ++ib;
+          }
+          if (ok) tc_commit(&a_empty[sa]);
+        }
+        if (ok) tc_commit(&d_full[buf]);
+      }
+      if (!ok || *stop) {
+        // given up: let the instructions in flight finish before tensor memory is freed
+        tc_commit(&drained);
+        for (int i = 0; i < (1 << 16) && !mbar_try(&drained, 0); ++i) {
+        }
+      }
+    }
+  } else if (warp >= kTcEpi) {
+    // ---- weights to fp16: a group of four warps takes every second block, a
+    // thread one channel of it
+    const int group = (warp - kTcEpi) >> 2, quad = warp & 3;
+    const int row = quad * 32 + lane;
+    uint32_t it = 0;
+    bool ok = true;
+    for (long long t = blockIdx.x; ok && t < n_tiles; t += gridDim.x) {
+      for (int b = 0; b < kb; ++b, ++it) {
+        if ((int)(it & 1) != group) continue;
+        const uint32_t s = it % p.w_slots, sa = it % kTcASlots, use = it / kTcASlots;
+        ok = __all_sync(0xffffffffu, mbar_wait(&w_full[s], (it / p.w_slots) & 1, stop));
+        if (!ok) break;
+        const uint8_t* src = ws + (size_t)s * kTcBlock + row * 128;
+        uint32_t v[2][32];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 x = *reinterpret_cast<const uint4*>(src + ((c ^ (row & 7)) << 4));
+          uint32_t* o = &v[c >> 2][(c & 3) * 8];
+          widen4(x.x, o[0], o[1]);
+          widen4(x.y, o[2], o[3]);
+          widen4(x.z, o[4], o[5]);
+          widen4(x.w, o[6], o[7]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&w_empty[s]);
+        if (use > 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&a_empty[sa], (use - 1) & 1, stop));
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const uint32_t dst = tmem + ((uint32_t)(quad * 32) << 16) + kTcACol + sa * 64u;
+        tc_st32(dst, v[0]);
+        tc_st32(dst + 32, v[1]);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&a_full[sa]);
+      }
+    }
+  } else {
+    // ---- results: a thread has one channel, a column of tensor memory is one row of a
+    const int quad = warp;
+    uint32_t id = 0;
+    for (long long t = blockIdx.x; t < n_tiles; t += gridDim.x, ++id) {
+      const uint32_t buf = id % d_bufs, use = id / d_bufs;
+      if (!__all_sync(0xffffffffu, mbar_wait(&d_full[buf], use & 1, stop))) break;
+      tc_fence_after();
+      if (__any_sync(0xffffffffu, *stop)) break;
+      const long long j = t / p.tiles * kPackRows + quad * 32 + lane;
+      const long long i0 = t % p.tiles * (long long)p.rows;
+      const float sw = j < g.N ? g.w_scale[j] : 0.f;
+      const uint32_t src = tmem + ((uint32_t)(quad * 32) << 16) + buf * 128u;
+      OUT* out = static_cast<OUT*>(g.out) + i0 * g.ldo + j;
+      for (int c = 0; c < p.rows; c += 16) {
+        float f[16];
+        tc_ld16(src + c, f);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (i0 + c + i < g.n && j < g.N)
+            store_out(out + (long long)(c + i) * g.ldo, f[i] * __ldg(g.a_scale + i0 + c + i) * sw);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&d_empty[buf]);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  if (threadIdx.x == 0 && stop_flag) report(g.d_status, DS_DEV_ERR_TIMEOUT);
+}
+
+long long linear_i8_workspace(int n, int N, int K) {
+  const TcPlan p = tc_plan(n, K);
+  return (long long)p.tiles * p.rows * p.kb * kPackK * 2;
+}
 
 cudaError_t launch_pack_i8(const int8_t* w, int N, int K, int64_t ldw, uint8_t* packed, cudaStream_t st) {
   const int sms = device_sms();
@@ -106,18 +442,37 @@ cudaError_t launch_pack_i8(const int8_t* w, int N, int K, int64_t ldw, uint8_t* 
 }
 
 cudaError_t launch_linear_i8(const LinearArgs& g, bool bf16_out, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  const int by = (g.n + kLiRows - 1) / kLiRows;
-  cfg.gridDim = dim3((unsigned)((g.N + kPackRows - 1LL) / kPackRows), (unsigned)(by < 65535 ? by : 65535));
-  cfg.blockDim = dim3(kPackRows);
-  cfg.stream = st;
+  const int sms = device_sms();
+  if (sms <= 0) return cudaErrorUnknown;
+  const TcPlan p = tc_plan(g.n, g.K);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = bf16_out ? cudaLaunchKernelEx(&cfg, k_linear_i8<__nv_bfloat16>, g)
-                                 : cudaLaunchKernelEx(&cfg, k_linear_i8<float>, g);
+
+  const long long chunks = (long long)p.tiles * 2 * p.kb * p.rows * 8, want = (chunks + 255) / 256;
+  cfg.gridDim = dim3((unsigned)(want < sms * 8LL ? want : sms * 8LL));
+  cfg.blockDim = dim3(256);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, k_expand_i8, g.a, (long long)g.lda, g.n, g.K, p.rows, p.tiles, 2 * p.kb,
+                                     static_cast<uint4*>(g.workspace));
+  if (e != cudaSuccess) return e;
+  note_launch();
+
+  auto kern = bf16_out ? k_linear_i8_tc<__nv_bfloat16> : k_linear_i8_tc<float>;
+  const int attr_ok = cached(reinterpret_cast<const void*>(kern), -1, [&](int) {
+    const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
+    if (r != cudaSuccess) (void)cudaGetLastError();
+    return r == cudaSuccess ? 1 : 0;
+  });
+  if (attr_ok <= 0) return cudaErrorUnknown;
+  const long long tiles = (long long)((g.N + kPackRows - 1) / kPackRows) * p.tiles;
+  cfg.gridDim = dim3((unsigned)(tiles < sms ? tiles : sms));
+  cfg.blockDim = dim3(kTcNT);
+  cfg.dynamicSmemBytes = kTcSmem;
+  e = cudaLaunchKernelEx(&cfg, kern, g, p);
   if (e == cudaSuccess) note_launch();
   return e;
 }
