@@ -144,6 +144,15 @@ def test_linear_i8_many_channel_blocks(n):
     _check(out, a, sa, w, sw, 192)
 
 
+@pytest.mark.parametrize("n,N,K", [(24, 41000, 2048), (48, 41000, 2048), (200, 25000, 1500), (300, 25000, 1100),
+                                   (9, 25000, 4224)])
+def test_linear_i8_many_blocks_each_way(n, N, K):
+    """Each ring of shared and tensor memory wraps many times, with few and many slots."""
+    a, sa, w, sw = _operands(n, N, K, 12)
+    out = pkg.linear_i8(a, sa, pkg.pack_i8(w, sw), dtype=torch.float32)
+    _check(out, a, sa, w, sw, K)
+
+
 @pytest.mark.parametrize("n,N,K,pa,pw,po", [(3, 200, 100, 1, 3, 5), (20, 200, 100, 28, 0, 1), (140, 333, 129, 7, 7, 3)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_linear_i8_strides(n, N, K, pa, pw, po, dtype):

@@ -111,6 +111,26 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
+// True in one thread of the (converged) warp. The compiler knows the branch to be
+// taken by one thread, which keeps the operands of the matrix instructions in
+// uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
+// A slot of a ring and the parity of its current use.
+struct Ring {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void next(uint32_t slots) {
+    if (++slot == slots) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
@@ -136,16 +156,23 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&v)[32]) 
       "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
       : "memory");
 }
-__device__ __forceinline__ void tc_ld16(uint32_t addr, float (&f)[16]) {
-  uint32_t v[16];
+// The next 32 columns of this thread's lane, `columns` of them read (16 or 32).
+__device__ __forceinline__ void tc_ld32(uint32_t addr, int columns, float (&f)[32]) {
+  uint32_t v[32];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
         "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
       : "r"(addr));
+  if (columns > 16)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(addr + 16));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]);
+  for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
 }
 
 // Matrix descriptor of a K-major tile with 128-byte swizzle: 8-row groups 1024
@@ -172,7 +199,7 @@ constexpr int kTcWarps = kTcEpi + kTcCvt + 3;  // then: weight loads, row loads,
 constexpr int kTcNT = kTcWarps * 32;
 constexpr int kTcBlock = kPackRows * kPackK;  // bytes of a weight block
 constexpr int kTcWSlots = 12;                 // most weight slots
-constexpr int kTcBSlots = 64;                 // most row-tile slots
+constexpr int kTcBSlots = 32;                 // most row-tile slots
 constexpr int kTcASlots = 4;                  // fp16 weight blocks in tensor memory, 64 columns each
 constexpr int kTcACol = 256;                  // their first column; accumulators are below
 constexpr size_t kTcSmem = 232448 - 2048;     // dynamic shared memory of a CTA, barriers apart
@@ -191,13 +218,19 @@ static TcPlan tc_plan(int n, int K) {
   p.tiles = (n + 255) / 256;
   p.rows = ((n + p.tiles - 1) / p.tiles + 15) / 16 * 16;
   p.kb = (K + kPackK - 1) / kPackK;
-  const long long slot = (long long)p.rows * 128, all = slot * 2 * p.kb, room = (long long)kTcSmem - 1024;
-  p.resident = p.tiles == 1 && 2 * p.kb <= kTcBSlots && all + 5 * kTcBlock <= room;
+  const long long room = (long long)kTcSmem - 1024;  // the tiles start on 1024 bytes
+  const long long slot = (long long)p.rows * 128, all = slot * 2 * p.kb;
+  p.resident = p.tiles == 1 && 2 * p.kb <= kTcBSlots && all + 6 * kTcBlock <= room;
   p.b_slots = p.resident ? 2 * p.kb : 4;
-  const long long w = (room - slot * p.b_slots) / kTcBlock;
+  // An even number: the two converting groups take blocks in turn, and each has
+  // to meet every use of the slots it waits on, or a parity of two uses ago
+  // would look like the current one.
+  const long long w = (room - slot * p.b_slots) / kTcBlock & ~1ll;
   p.w_slots = (int)(w < kTcWSlots ? w : kTcWSlots);
   return p;
 }
+
+static_assert(kTcWSlots % 2 == 0 && kTcASlots % 2 == 0, "each converting group keeps its slots");
 
 // One CTA per SM walks tiles of 128 channels x `rows` rows of a.
 template <typename OUT>
@@ -206,9 +239,10 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
   __shared__ uint64_t w_full[kTcWSlots], w_empty[kTcWSlots], b_full[kTcBSlots], b_empty[kTcBSlots];
   __shared__ uint64_t a_full[kTcASlots], a_empty[kTcASlots], d_full[2], d_empty[2], drained;
   __shared__ uint32_t tmem_base;
+  __shared__ float a_scale[256];
   __shared__ int stop_flag;
   volatile int* stop = &stop_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   uint8_t* bs = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
   const uint32_t b_bytes = (uint32_t)p.rows * 128u;
   uint8_t* ws = bs + (size_t)b_bytes * p.b_slots;
@@ -299,40 +333,44 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
     }
   } else if (warp == kTcEpi + kTcCvt + 2) {
     // ---- matrix instructions, by one thread
-    if (lane == 0) {
+    if (elect_one()) {
       // fp32 accumulators, fp16 operands, M = 128, N = rows
       const uint32_t idesc = (1u << 4) | ((uint32_t)(p.rows >> 3) << 17) | ((uint32_t)(kPackRows >> 4) << 24);
-      uint32_t ia = 0, ib = 0, id = 0;
-      bool ok = true;
-      for (long long t = blockIdx.x; ok && t < n_tiles; t += gridDim.x, ++id) {
-        const uint32_t buf = id % d_bufs, use = id / d_bufs;
-        if (use > 0 && !mbar_wait(&d_empty[buf], (use - 1) & 1, stop)) break;
+      const uint64_t b_desc = sw128_desc(smem_u32(bs));
+      const uint32_t b_step = b_bytes >> 4;
+      Ring ra, rb, rd;
+      bool ok = true, loaded = false;
+      for (long long t = blockIdx.x; ok && t < n_tiles; t += gridDim.x) {
+        if (!mbar_wait(&d_empty[rd.slot], rd.phase ^ 1u, stop)) break;
         tc_fence_after();
-        const uint32_t d = tmem + buf * 128u;
-        const bool loaded = p.resident && id > 0;  // the row tile is there already
-        for (int b = 0; ok && b < kb; ++b, ++ia) {
-          const uint32_t sa = ia % kTcASlots;
-          ok = mbar_wait(&a_full[sa], (ia / kTcASlots) & 1, stop);
+        const uint32_t d = tmem + rd.slot * 128u;
+        uint32_t accumulate = 0;
+        for (int b = 0; ok && b < kb; ++b) {
+          ok = mbar_wait(&a_full[ra.slot], ra.phase, stop);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t acol = tmem + kTcACol + sa * 64u;
+          const uint32_t acol = tmem + kTcACol + ra.slot * 64u;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t sb = p.resident ? (uint32_t)(2 * b + h) : ib % p.b_slots;
             if (!loaded) {
-              ok = mbar_wait(&b_full[sb], p.resident ? 0u : (ib / p.b_slots) & 1, stop);
+              ok = mbar_wait(&b_full[rb.slot], rb.phase, stop);
               if (!ok) break;
             }
-            const uint64_t bd = sw128_desc(smem_u32(bs) + sb * b_bytes);
+            const uint64_t bd = b_desc + (uint64_t)(rb.slot * b_step);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc_mma(d, acol + (uint32_t)(h * 32 + k * 8), bd + (uint64_t)(k * 2), idesc, (b | h | k) ? 1u : 0u);
-            if (!p.resident) tc_commit(&b_empty[sb]);
-            ++ib;
+            for (int k = 0; k < 4; ++k) {
+              tc_mma(d, acol + (uint32_t)(h * 32 + k * 8), bd + (uint64_t)(k * 2), idesc, accumulate);
+              accumulate = 1;
+            }
+            if (!p.resident) tc_commit(&b_empty[rb.slot]);
+            rb.next(p.b_slots);
           }
-          if (ok) tc_commit(&a_empty[sa]);
+          if (ok) tc_commit(&a_empty[ra.slot]);
+          ra.next(kTcASlots);
         }
-        if (ok) tc_commit(&d_full[buf]);
+        if (ok) tc_commit(&d_full[rd.slot]);
+        rd.next(d_bufs);
+        loaded = p.resident;  // a resident row tile has a slot for each of its blocks: the ring is back at the first
       }
       if (!ok || *stop) {
         // given up: let the instructions in flight finish before tensor memory is freed
@@ -384,29 +422,41 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
   } else {
     // ---- results: a thread has one channel, a column of tensor memory is one row of a
     const int quad = warp;
-    uint32_t id = 0;
-    for (long long t = blockIdx.x; t < n_tiles; t += gridDim.x, ++id) {
-      const uint32_t buf = id % d_bufs, use = id / d_bufs;
-      if (!__all_sync(0xffffffffu, mbar_wait(&d_full[buf], use & 1, stop))) break;
+    Ring rd;
+    long long scales = -1;  // row tile whose scales are in shared memory
+    for (long long t = blockIdx.x; t < n_tiles; t += gridDim.x) {
+      const long long j = t / p.tiles * kPackRows + quad * 32 + lane, tile = t % p.tiles, i0 = tile * p.rows;
+      if (tile != scales) {
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        for (int i = threadIdx.x; i < p.rows; i += 128) a_scale[i] = i0 + i < g.n ? g.a_scale[i0 + i] : 0.f;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        scales = tile;
+      }
+      const float sw = j < g.N ? g.w_scale[j] : 0.f;
+      if (!__all_sync(0xffffffffu, mbar_wait(&d_full[rd.slot], rd.phase, stop))) break;
       tc_fence_after();
       if (__any_sync(0xffffffffu, *stop)) break;
-      const long long j = t / p.tiles * kPackRows + quad * 32 + lane;
-      const long long i0 = t % p.tiles * (long long)p.rows;
-      const float sw = j < g.N ? g.w_scale[j] : 0.f;
-      const uint32_t src = tmem + ((uint32_t)(quad * 32) << 16) + buf * 128u;
+      const uint32_t src = tmem + ((uint32_t)(quad * 32) << 16) + rd.slot * 128u;
       OUT* out = static_cast<OUT*>(g.out) + i0 * g.ldo + j;
-      for (int c = 0; c < p.rows; c += 16) {
-        float f[16];
-        tc_ld16(src + c, f);
+      for (int c = 0; c < p.rows; c += 32, out += 32 * g.ldo) {
+        float f[32];
+        tc_ld32(src + c, p.rows - c, f);
+        const int left = (int)(g.n - i0) - c < p.rows - c ? (int)(g.n - i0) - c : p.rows - c;
+        if (j < g.N) {
+          if (left >= 32) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          if (i0 + c + i < g.n && j < g.N)
-            store_out(out + (long long)(c + i) * g.ldo, f[i] * __ldg(g.a_scale + i0 + c + i) * sw);
+            for (int i = 0; i < 32; ++i) store_out(out + i * g.ldo, f[i] * a_scale[c + i] * sw);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i < left) store_out(out + i * g.ldo, f[i] * a_scale[c + i] * sw);
+          }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&d_empty[buf]);
+      if (lane == 0) mbar_arrive(&d_empty[rd.slot]);
+      rd.next(d_bufs);
     }
   }
 
