@@ -40,6 +40,7 @@ struct Logit<uint16_t> {
   static __device__ __forceinline__ float get(const uint16_t* p, long long i) {
     return __uint_as_float((uint32_t)__ldg(p + i) << 16);
   }
+  static __device__ __forceinline__ float load(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
   static __device__ __forceinline__ uint32_t key(float x) { return order_key(x == 0.f ? 0.f : x) >> 16; }
   static __device__ __forceinline__ float value(uint32_t k) {
     return __uint_as_float(((k & 0x8000u) ? k ^ 0x8000u : ~k) << 16);
@@ -48,6 +49,7 @@ struct Logit<uint16_t> {
 template <>
 struct Logit<float> {
   static __device__ __forceinline__ float get(const float* p, long long i) { return __ldg(p + i); }
+  static __device__ __forceinline__ float load(const float* p) { return *p; }
   static __device__ __forceinline__ uint32_t key(float x) { return order_key(x == 0.f ? 0.f : x); }
   static __device__ __forceinline__ float value(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
@@ -269,9 +271,9 @@ __global__ void __launch_bounds__(kSfNT) k_sample_filtered_rows(FilteredArgs a) 
 //
 // A cluster of cs CTAs holds a row in shared memory, a contiguous slice each, and
 // answers the three questions from histograms over bins of x:
-//   max     m, the smallest logit that is no mask, and a cut x1 below which about
-//           half of the threads' maxima lie, so that some thousand logits at most
-//           are above it while NT / 4 at least are
+//   max     m, the smallest logit that is no mask, and a cut x1: the least of
+//           GROUPS groups' maxima, so that GROUPS logits at least are above it
+//           and, of independent ones, about ln(GROUPS) times as many
 //   weigh   sum exp(x - m); the mass of the row (unless a small top-k makes it
 //           needless); and for the logits >= x1, the ones that decide nearly
 //           every row, count and mass in bins linear in x
@@ -281,7 +283,7 @@ __global__ void __launch_bounds__(kSfNT) k_sample_filtered_rows(FilteredArgs a) 
 //   gather  the logits of those bins, a few dozen, come to rank 0, which sorts
 //           them and answers exactly.
 // A row whose boundary bins hold more than CAP logits (ties) is finished by
-// row_exact. So a logit costs two exponentials and its share of three walks over
+// row_exact. So a logit costs two exponentials and its share of two walks over
 // shared memory, an atomic only above x1.
 namespace {
 
@@ -292,13 +294,14 @@ struct SfShared {
   uint32_t pc[NB];                   // rank 0: count through each bin
   u64 list[CAP];                     // rank 0: gathered (key, ~id)
   u64 incl[CAP];                     // rank 0: running mass through each of them
-  u64 red[NT / 32];
-  float fred[3][NT / 32];
+  u64 full;                          // the slice's copy is done
+  u64 red[NT / 32], red2[NT / 32];
+  float fred[3][NT / 32], sred[2][NT / 32];
   uint32_t marks[NB / 32];
-  u64 part_total, part_floor;  // read by rank 0
-  float part_max, part_min, part_cut, part_sum;
-  float row[4];
-  int part_odd;
+  // each CTA's partials, pushed by it to everyone (max) or to rank 0 (weigh)
+  float part_max[16], part_min[16], part_cut[16], part_sum[16];
+  u64 part_total[16], part_floor[16];
+  int part_odd[16];
   int command, gate, n_list, first_id;
   u64 known_total, known_floor;
   float known_sum;
@@ -309,29 +312,13 @@ struct SfShared {
 
 enum Command { kDone, kGather, kTail, kExact };
 
-// v of the lane of rank `want` (0: largest) among the first `lanes` lanes.
-__device__ __forceinline__ float warp_nth_largest(float v, int lane, int lanes, int want) {
-  int rank = 0;
-  for (int j = 0; j < lanes; ++j) {
-    const float o = __shfl_sync(0xffffffffu, v, j);
-    rank += (o > v) || (o == v && j < lane);
-  }
-  const unsigned at = __ballot_sync(0xffffffffu, lane < lanes && rank == want);
-  return __shfl_sync(0xffffffffu, v, at ? __ffs(at) - 1 : 0);
-}
-
 // Index of the first element of the ascending array that is >= t (n if none), by one warp.
 template <typename U>
 __device__ __forceinline__ int warp_lower_bound(const U* v, int n, U t, int lane) {
   const int step = n / 32;
   const int seg = __popc(__ballot_sync(0xffffffffu, v[(lane + 1) * step - 1] < t));
   if (seg == 32) return n;
-  int at = seg * step;
-  for (int o = 0; o < step; o += 32) {
-    const unsigned below = __ballot_sync(0xffffffffu, o + lane < step && v[seg * step + o + lane] < t);
-    at += __popc(below);
-  }
-  return at;
+  return seg * step + __popc(__ballot_sync(0xffffffffu, lane < step && v[seg * step + lane] < t));
 }
 
 template <typename T>
@@ -352,15 +339,43 @@ struct Chunk<float> {
   }
 };
 
-__device__ __forceinline__ void sf_cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
-               : "memory");
+template <int N>
+__device__ __forceinline__ float max_of(const float (&f)[N]) {
+  float c = f[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) c = fmaxf(c, f[i]);
+  return c;
+}
+
+__device__ __forceinline__ u64 warp_sum_u64(u64 v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+__device__ __forceinline__ float warp_min_r(float v) { return -warp_max_r(-v); }
+
+__device__ __forceinline__ uint32_t sf_smem(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// Waits for the slice's copy; gives up after a while (false).
+__device__ __forceinline__ bool sf_wait(u64* bar, uint32_t parity) {
+  for (int i = 0; i < (1 << 20); ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(sf_smem(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
 }
 
 }  // namespace
 
-template <typename T, int NT, int NB, int CAP>
-__global__ void __launch_bounds__(NT, 1024 / NT) k_sample_filtered(FilteredArgs a) {
+template <typename T, int NT, int NB, int CAP, int GROUPS>
+__global__ void __launch_bounds__(NT, 1024 / NT)
+    k_sample_filtered(FilteredArgs a, int slice_chunks) {
   constexpr int EPC = Chunk<T>::N, NBT = NB / 2, NW = NT / 32;
   using Shared = SfShared<NT, NB, CAP>;
   extern __shared__ uint4 slice[];
@@ -370,12 +385,26 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample_filtered(FilteredArgs 
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const long long n_clusters = (long long)gridDim.x / cs, cid = (long long)blockIdx.x / cs;
   Shared* lead = cl.map_shared_rank(&sh, 0);
-  auto sync = [&] {
-    if (cs == 1)
+  // behind the slice: each warp's queue of its chunks that hold a logit >= x1, room for all of them
+  const int walk = ((slice_chunks + NT - 1) / NT) * 32;
+  uint16_t* queue = reinterpret_cast<uint16_t*>(slice + slice_chunks) + wid * walk;
+  auto cta_sync = [&] {
+    if (NT == 32)
+      __syncwarp();
+    else
       __syncthreads();
+  };
+  auto sync = [&] {
+    if (NT == 32 || cs == 1)
+      cta_sync();
     else
       cl.sync();
   };
+  if (tid == 0) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(sf_smem(&sh.full)) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  sync();  // every CTA of the cluster runs before any writes into another's shared memory
   pdl_wait();
   pdl_release();
 
@@ -396,19 +425,29 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample_filtered(FilteredArgs 
     g.q_hi = (int)((long long)(rank + 1) * g.nq / cs);
     return g;
   };
+  // One bulk copy of the row's slice, started when nobody reads the last one any more.
   auto start_copy = [&](long long n) {
-    if (n < a.n) {
+    if (tid == 0 && n < a.n) {
       const Slice g = slice_of(n);
-      for (int q = g.q_lo + tid; q < g.q_hi; q += NT) sf_cp_async16(&slice[q - g.q_lo], g.base + q);
+      const uint32_t bytes = (uint32_t)(g.q_hi - g.q_lo) * 16u;
+      asm volatile("{\n.reg .b64 t;\nmbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1;\n}" ::"r"(sf_smem(&sh.full)),
+                   "r"(bytes)
+                   : "memory");
+      if (bytes)
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                sf_smem(slice)),
+            "l"(g.base + g.q_lo), "r"(bytes), "r"(sf_smem(&sh.full))
+            : "memory");
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
   };
   start_copy(cid);
 
-  for (long long n = cid; n < a.n; n += n_clusters) {
+  uint32_t parity = 0;
+  for (long long n = cid; n < a.n; n += n_clusters, parity ^= 1u) {
     const Slice g = slice_of(n);
     const RowParams q = row_params(a, n);
-    // the logits of chunk j of this thread's walk; ids outside the row read as -inf
+    // the logits of chunk j; ids outside the row read as -inf
     auto values = [&](int j, float (&f)[EPC]) {
       Chunk<T>::get(slice[j - g.q_lo], f);
       if (j == 0 || j == g.nq - 1) {
@@ -424,131 +463,225 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample_filtered(FilteredArgs 
       sh.n_list = 0;
       sh.first_id = INT_MAX;
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");  // a thread reads only the chunks that it copied
+    if (!sf_wait(&sh.full, parity)) report(a.d_status, DS_DEV_ERR_TIMEOUT);
 
     // ---- max
     float mx = -kInf, mn = kInf;
     for (int j = g.q_lo + tid; j < g.q_hi; j += NT) {
       float f[EPC];
       values(j, f);
+      mx = fmaxf(mx, max_of(f));
 #pragma unroll
-      for (int i = 0; i < EPC; ++i) {
-        mx = fmaxf(mx, f[i]);
-        if (f[i] > -3e37f) mn = fminf(mn, f[i]);
-      }
+      for (int i = 0; i < EPC; ++i) mn = fminf(mn, f[i] > -3e37f ? f[i] : kInf);
     }
+    float m, lo, cut;
     {
-      const float wm = warp_max(mx), wn = -warp_max(-mn), wc = warp_nth_largest(mx, lane, 32, 15);
-      if (lane == 0) {
-        sh.fred[0][wid] = wm;
-        sh.fred[1][wid] = wn;
-        sh.fred[2][wid] = wc;
-      }
-      __syncthreads();
-      if (wid == 0) {
-        const float bm = warp_max(lane < NW ? sh.fred[0][lane] : -kInf);
-        const float bn = -warp_max(lane < NW ? -sh.fred[1][lane] : -kInf);
-        const float bc = warp_nth_largest(lane < NW ? sh.fred[2][lane] : -kInf, lane, NW, NW / 2 - 1);
+      float grp = mx;
+#pragma unroll
+      for (int o = 1; o < NT / GROUPS; o <<= 1) grp = fmaxf(grp, __shfl_xor_sync(0xffffffffu, grp, o));
+      m = warp_max_r(mx);
+      lo = warp_min_r(mn);
+      cut = warp_min_r(grp);
+      if (NW > 1) {
         if (lane == 0) {
-          sh.part_max = bm;
-          sh.part_min = bn;
-          sh.part_cut = bc;
+          sh.fred[0][wid] = m;
+          sh.fred[1][wid] = lo;
+          sh.fred[2][wid] = cut;
+        }
+        cta_sync();
+        if (cs == 1) {
+          m = warp_max_r(sh.fred[0][lane % NW]);
+          lo = warp_min_r(sh.fred[1][lane % NW]);
+          cut = warp_min_r(sh.fred[2][lane % NW]);
+        } else {
+          if (wid == 0) {
+            m = warp_max_r(sh.fred[0][lane % NW]);
+            lo = warp_min_r(sh.fred[1][lane % NW]);
+            cut = warp_min_r(sh.fred[2][lane % NW]);
+            if (lane < cs) {
+              Shared* peer = cl.map_shared_rank(&sh, lane);
+              peer->part_max[rank] = m;
+              peer->part_min[rank] = lo;
+              peer->part_cut[rank] = cut;
+            }
+          }
+          sync();
+          m = warp_max_r(sh.part_max[lane % cs]);
+          lo = warp_min_r(sh.part_min[lane % cs]);
+          cut = warp_max_r(sh.part_cut[lane % cs]);
         }
       }
-      sync();
-      if (wid == 0) {
-        const Shared* o = lane < cs ? cl.map_shared_rank(&sh, lane) : &sh;
-        const float m = warp_max(o->part_max), lo = -warp_max(-o->part_min), cut = warp_max(o->part_cut);
-        if (lane == 0) {
-          sh.row[0] = m;
-          sh.row[1] = fminf(lo, m);
-          sh.row[2] = cut;
-        }
-      }
-      __syncthreads();
     }
-    const float m = sh.row[0];
     // No logit below x_low has a weight: w > 0 needs (x - m) r > -22.2, and the
     // rest is room for the rounding of x_low. Masks are told from logits by
     // their size, which needs a range that ends above them.
     const float lowest = (m - 24.f * q.tau) - fabsf(m) * 2.4e-7f;
-    const float x_low = lowest > -3e37f ? fmaxf(sh.row[1], lowest) : fmaxf(lowest, -3.402823466e38f);
-    const float x1 = fmaxf(sh.row[2], x_low);  // splits the rest
+    const float x_low = lowest > -3e37f ? fmaxf(fminf(lo, m), lowest) : fmaxf(lowest, -3.402823466e38f);
+    const float x1 = fmaxf(cut, x_low);  // splits the rest
     const float sc1 = fminf((float)NBT / (m - x1), 3.402823466e38f);
     const float sc2 = fminf((float)(NB - NBT) / (x1 - x_low), 3.402823466e38f);
     auto bin_of = [&](float x) {  // for x_low <= x <= m
       return x >= x1 ? min(NBT - 1, __float2int_rz((m - x) * sc1))
                      : min(NB - 1, NBT + min(NB, __float2int_rz((x1 - x) * sc2)));
     };
-    const bool drawn = !q.bad && q.tau > 0.f && m > -kInf && m < kInf;
-    const bool greedy = !q.bad && q.tau == 0.f && m > -kInf && m < kInf;
-    // A top-k of at most NT / 4 ends above x1: the mass below is then not asked for.
-    const bool whole = drawn && !(q.k && q.k <= NT / 4);
-    const double floor_w = (double)q.mp * (double)kSfOne;
-    const uint32_t floor_i = (uint32_t)ceil(floor_w);
+    const bool finite = m > -kInf && m < kInf;
+    const bool drawn = !q.bad && q.tau > 0.f && finite;
+    const bool greedy = !q.bad && q.tau == 0.f && finite;
+    // A top-k of at most GROUPS ends above x1: the mass below is then not asked for.
+    const bool whole = drawn && !(q.k && q.k <= GROUPS);
+    const bool floored = q.mp > 0.f;
+    const uint32_t floor_i = (uint32_t)ceil((double)q.mp * (double)kSfOne);
+    // one logit of chunk j
+    auto value = [&](int j, int i) {
+      const int e = EPC * j - g.dc + i;
+      const float x = Logit<T>::load(reinterpret_cast<const T*>(slice) + (EPC * (j - g.q_lo) + i));
+      return e >= 0 && e < a.V ? x : -kInf;
+    };
+    auto add_bins = [&](float x, uint32_t w) {
+      if (w) {
+        const int b = bin_of(x);
+        atomicAdd(&sh.cnt[b], 1u);
+        atomicAdd(&sh.lo[b], w & 0xffffu);
+        if (w >> 16) atomicAdd(&sh.hi[b], w >> 16);
+      }
+    };
 
     // ---- weigh
     float s = 0.f;
     u64 total = 0, above_floor = 0;
-    int odd = 0, first = INT_MAX;
-    for (int j = g.q_lo + tid; j < g.q_hi; j += NT) {
+    int first = INT_MAX, odd = 0;
+    int queued = 0;
+    for (int j0 = g.q_lo + wid * 32; j0 < g.q_hi; j0 += NT) {
+      const int j = j0 + lane;
       float f[EPC];
-      values(j, f);
+      if (j < g.q_hi) {
+        values(j, f);
+      } else {
 #pragma unroll
-      for (int i = 0; i < EPC; ++i) {
-        const float x = f[i];
-        odd |= !(x < kInf);
-        s += ex2_approx((x - m) * kLog2e);
-        if (greedy && x == m) first = min(first, EPC * j - g.dc + i);
-        if (drawn && x >= (whole ? x_low : x1)) {
-          const uint32_t w = sf_weight(x, m, q.r);
+        for (int i = 0; i < EPC; ++i) f[i] = -kInf;
+      }
+      const float c = max_of(f);
+      float part = 0.f;
+#pragma unroll
+      for (int i = 0; i < EPC; ++i) part += ex2_approx((f[i] - m) * kLog2e);
+      s += part;
+      if (whole) {
+#pragma unroll
+        for (int i = 0; i < EPC; ++i) {
+          const uint32_t w = sf_weight(f[i], m, q.r);
           total += w;
-          if (w >= floor_i) above_floor += w;
-          if (x >= x1 && w) {
-            const int b = bin_of(x);
-            atomicAdd(&sh.cnt[b], 1u);
-            atomicAdd(&sh.lo[b], w & 0xffffu);
-            atomicAdd(&sh.hi[b], w >> 16);
-          }
+          if (floored) above_floor += w >= floor_i ? w : 0u;
         }
       }
+      const unsigned high = __ballot_sync(0xffffffffu, drawn && c >= x1);
+      if (drawn && c >= x1) queue[queued + __popc(high & ((1u << lane) - 1u))] = (uint16_t)(j - g.q_lo);
+      queued += __popc(high);
+      if (greedy && c == m) {
+#pragma unroll
+        for (int i = 0; i < EPC; ++i)
+          if (f[i] == m) first = min(first, EPC * j - g.dc + i);
+      }
+      if (!finite) {
+#pragma unroll
+        for (int i = 0; i < EPC; ++i) odd |= !(f[i] < kInf);
+      }
     }
+    // The queued chunks, a logit per lane: in the walk itself a few lanes at a
+    // time would weigh while the others wait.
+    __syncwarp();
+    // Four logits of the queued chunks per lane, -inf past their end.
+    auto four_queued = [&](int i0, float (&x)[4], int (&j)[4]) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) j[u] = g.q_lo + queue[min(i0 + lane / EPC + u * (32 / EPC), queued - 1)];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        x[u] = value(j[u], lane % EPC);
+        if (i0 + lane / EPC + u * (32 / EPC) >= queued) x[u] = -kInf;
+      }
+    };
+    for (int i0 = 0; i0 < queued; i0 += 128 / EPC) {
+      float x[4];
+      int j[4];
+      four_queued(i0, x, j);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (x[u] >= x1) {
+          const uint32_t w = sf_weight(x[u], m, q.r);
+          add_bins(x[u], w);
+          if (!whole && floored) above_floor += w >= floor_i ? w : 0u;
+        }
+    }
+    __syncwarp();
+    // A NaN, or +inf under a finite maximum, makes the sum NaN.
     s = warp_sum(s);
-    total = block_sum<NT>(total, sh.red);
-    above_floor = block_sum<NT>(above_floor, sh.red);
-    odd = __syncthreads_or(odd);
-    if (lane == 0) sh.fred[0][wid] = s;
+    odd |= finite && !(s < kInf);
+    odd = __any_sync(0xffffffffu, odd);
+    if (whole) total = warp_sum_u64(total);
+    if (floored) above_floor = warp_sum_u64(above_floor);
     if (greedy) {
       first = warp_min_i(first);
       if (lane == 0 && first != INT_MAX) atomicMin(&lead->first_id, first);
     }
-    __syncthreads();
-    if (tid == 0) {
-      s = 0.f;
-      for (int i = 0; i < NW; ++i) s += sh.fred[0][i];
-      sh.part_sum = s;
-      sh.part_total = total;
-      sh.part_floor = above_floor;
-      sh.part_odd = odd;
+    if (lane == 0) {
+      sh.red[wid] = total;
+      sh.red2[wid] = above_floor;
+      sh.sred[0][wid] = s;
+      sh.sred[1][wid] = __int_as_float(odd);
+    }
+    cta_sync();
+    if (wid == 0) {
+      const bool in = lane < NW;
+      total = warp_sum_u64(in ? sh.red[lane] : 0);
+      above_floor = warp_sum_u64(in ? sh.red2[lane] : 0);
+      s = warp_sum(in ? sh.sred[0][lane] : 0.f);
+      odd = __any_sync(0xffffffffu, in && __float_as_int(sh.sred[1][lane]));
+      if (lane == 0) {
+        lead->part_total[rank] = total;
+        lead->part_floor[rank] = above_floor;
+        lead->part_sum[rank] = s;
+        lead->part_odd[rank] = odd;
+      }
     }
     sync();
 
-    // Sums the cluster's bins [b0, b0 + NB / 2) into rank 0's pm and pc, a share of them per CTA.
-    auto merge_bins = [&](int b0) {
-      for (int i = rank * NT + tid; i < NB / 2; i += cs * NT) {
-        const int b = b0 + i;
-        uint32_t c = 0;
-        u64 mass = 0;
+    if (!drawn) {
+      start_copy(n + n_clusters);
+      if (rank == 0 && tid == 0) {
+        int bits = 0;
+        float sum = 0.f;
         for (int o = 0; o < cs; ++o) {
-          const Shared* peer = cl.map_shared_rank(&sh, o);
-          c += peer->cnt[b];
-          mass += (u64)peer->lo[b] + ((u64)peer->hi[b] << 16);
+          bits |= sh.part_odd[o];
+          sum += sh.part_sum[o];
         }
-        lead->pc[b] = c;
-        lead->pm[b] = mass;
+        const bool ok = greedy && !bits;
+        if (q.bad || bits) report(a.d_status, q.bad ? DS_DEV_ERR_PARAM : DS_DEV_ERR_LOGITS);
+        a.out_tokens[n] = ok ? sh.first_id : -1;
+        a.out_logprobs[n] = ok ? m - (m + logf(sum)) : __int_as_float(0x7fffffff);
+      }
+      continue;  // the partials are read before this CTA meets the others again
+    }
+
+    // Sums the cluster's bins [b0, b0 + NB / 2) into rank 0's pm and pc: a share
+    // of the bins per CTA, a thread per bin and peer, so that the reads of other
+    // CTAs' memory are one round trip.
+    auto merge_bins = [&](int b0) {
+      for (int i = tid; i < NBT; i += NT) {
+        const int b = b0 + rank * (NBT / cs) + i / cs;
+        const Shared* peer = cl.map_shared_rank(&sh, i % cs);
+        uint32_t c = peer->cnt[b];
+        u64 mass = (u64)peer->lo[b] + ((u64)peer->hi[b] << 16);
+        for (int o = 1; o < cs; o <<= 1) {
+          c += __shfl_xor_sync(0xffffffffu, c, o);
+          mass += __shfl_xor_sync(0xffffffffu, mass, o);
+        }
+        if (i % cs == 0) {
+          lead->pc[b] = c;
+          lead->pm[b] = mass;
+        }
       }
     };
-    // Rank 0: running sums of those bins, continuing from (m0, c0).
+    // Rank 0: running sums of those bins, continuing from (m0, c0). Alone in its
+    // cluster, it takes them as they are.
     auto scan_bins = [&](int b0, u64 m0, uint32_t c0) {
       constexpr int PER = (NBT + NT - 1) / NT;
       u64 mass[PER], sm = 0;
@@ -556,8 +689,12 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample_filtered(FilteredArgs 
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int b = tid * PER + i;
-        mass[i] = b < NBT ? sh.pm[b0 + b] : 0;
-        c[i] = b < NBT ? sh.pc[b0 + b] : 0;
+        mass[i] = 0;
+        c[i] = 0;
+        if (b < NBT) {
+          mass[i] = cs == 1 ? (u64)sh.lo[b0 + b] + ((u64)sh.hi[b0 + b] << 16) : sh.pm[b0 + b];
+          c[i] = cs == 1 ? sh.cnt[b0 + b] : sh.pc[b0 + b];
+        }
         sm += mass[i];
         sc += c[i];
       }
@@ -572,17 +709,20 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample_filtered(FilteredArgs 
           ic += uc;
         }
       }
-      __syncthreads();
-      if (lane == 31) {
-        sh.red[wid] = im;
-        sh.fred[0][wid] = __uint_as_float(ic);
-      }
-      __syncthreads();
       u64 bm = m0 + im - sm;
       uint32_t bc = c0 + ic - sc;
-      for (int w = 0; w < wid; ++w) {
-        bm += sh.red[w];
-        bc += __float_as_uint(sh.fred[0][w]);
+      if (NW > 1) {
+        if (lane == 31) {
+          sh.red[wid] = im;
+          sh.fred[0][wid] = __uint_as_float(ic);
+        }
+        cta_sync();
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+          if (w < wid) {
+            bm += sh.red[w];
+            bc += __float_as_uint(sh.fred[0][w]);
+          }
       }
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
@@ -594,7 +734,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample_filtered(FilteredArgs 
           sh.pc[b0 + b] = bc;
         }
       }
-      __syncthreads();
+      cta_sync();
     };
     // Rank 0, warp 0: which bins the boundaries can lie in (see the kernel's comment).
     auto decide = [&](bool tail) {
@@ -604,10 +744,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample_filtered(FilteredArgs 
       const bool complete = tail || !whole || known == all;
       uint32_t mark = 0;  // lane l: bins [32 l, 32 l + 32)
       auto mark_range = [&](int b0, int b1) {
-        for (int wd = lane; wd < NB / 32; wd += 32) {
-          const int lo = max(b0 - 32 * wd, 0), hi = min(b1 - 32 * wd, 31);
-          if (lo <= hi) mark |= (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
-        }
+        const int from = max(b0 - 32 * lane, 0), to = min(b1 - 32 * lane, 31);
+        if (lane < NB / 32 && from <= to) mark |= (0xffffffffu << from) & (0xffffffffu >> (31 - to));
       };
       u64 t_lo, t_hi;  // bounds of the kept mass
       int kb = -1;
@@ -625,73 +763,51 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample_filtered(FilteredArgs 
         t_lo = t_hi = whole ? all : known;
       }
       if (q.p < 1.f) {
-        const u64 n_lo = need_of(q.p, t_lo), n_hi = need_of(q.p, t_hi);
+        const u64 n_hi = need_of(q.p, t_hi), n_lo = t_lo == t_hi ? n_hi : need_of(q.p, t_lo);
         if (n_hi > known) return complete ? (int)kExact : (int)kTail;
         const int b0 = warp_lower_bound<u64>(sh.pm, nb, n_lo > 0 ? n_lo : 1, lane);
-        const int b1 = warp_lower_bound<u64>(sh.pm, nb, n_hi, lane);
+        const int b1 = n_lo == n_hi ? b0 : warp_lower_bound<u64>(sh.pm, nb, n_hi, lane);
         mark_range(b0, b1);
         t_lo = b0 ? sh.pm[b0 - 1] : 0;
         t_hi = sh.pm[b1];
       }
-      if (q.mp > 0.f) {
+      if (floored) {
         t_lo = fl < t_lo ? fl : t_lo;
         t_hi = fl < t_hi ? fl : t_hi;
       }
-      const u64 d_lo = target_of(q.u, t_lo), d_hi = target_of(q.u, t_hi);
+      const u64 d_hi = target_of(q.u, t_hi), d_lo = t_lo == t_hi ? d_hi : target_of(q.u, t_lo);
       if (d_hi >= known) return complete ? (int)kExact : (int)kTail;
-      mark_range(warp_lower_bound<u64>(sh.pm, nb, d_lo + 1, lane), warp_lower_bound<u64>(sh.pm, nb, d_hi + 1, lane));
+      const int b0 = warp_lower_bound<u64>(sh.pm, nb, d_lo + 1, lane);
+      mark_range(b0, d_lo == d_hi ? b0 : warp_lower_bound<u64>(sh.pm, nb, d_hi + 1, lane));
       int listed = 0;
-      for (uint32_t w = lane < NB / 32 ? mark : 0u; w; w &= w - 1) {
+      for (uint32_t w = mark; w; w &= w - 1) {
         const int b = 32 * lane + __ffs(w) - 1;
         listed += (int)(sh.pc[b] - (b ? sh.pc[b - 1] : 0u));
       }
       if (warp_sum_i(listed) > CAP) return (int)kExact;
       if (lane < NB / 32) sh.marks[lane] = mark;
+      const bool low = __any_sync(0xffffffffu, lane >= NBT / 32 && mark);
       if (lane == 0) {
         sh.kb = kb;
+        sh.gate = low;
       }
-      const bool low = __any_sync(0xffffffffu, lane >= NBT / 32 && lane < NB / 32 && mark);
-      if (lane == 0) sh.gate = low;
       return (int)kGather;
     };
 
-    if (!drawn) {
-      start_copy(n + n_clusters);
-      if (rank == 0 && tid == 0) {
-        int bits = 0;
-        float sum = 0.f;
-        for (int o = 0; o < cs; ++o) {
-          const Shared* peer = cl.map_shared_rank(&sh, o);
-          bits |= peer->part_odd;
-          sum += peer->part_sum;
-        }
-        const bool ok = greedy && !bits;
-        if (q.bad || bits) report(a.d_status, q.bad ? DS_DEV_ERR_PARAM : DS_DEV_ERR_LOGITS);
-        a.out_tokens[n] = ok ? sh.first_id : -1;
-        a.out_logprobs[n] = ok ? m - (m + logf(sum)) : __int_as_float(0x7fffffff);
-      }
-      sync();  // the partials are read before the next row writes them
-      continue;
-    }
-
-    merge_bins(0);
+    if (cs > 1) merge_bins(0);
     if (rank == 0 && wid == 0) {
-      const Shared* peer = lane < cs ? cl.map_shared_rank(&sh, lane) : nullptr;
-      u64 t = peer ? peer->part_total : 0, fl = peer ? peer->part_floor : 0;
-      float sum = peer ? peer->part_sum : 0.f;
-      int bits = peer ? peer->part_odd : 0;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        t += __shfl_xor_sync(0xffffffffu, t, o);
-        fl += __shfl_xor_sync(0xffffffffu, fl, o);
-        bits |= __shfl_xor_sync(0xffffffffu, bits, o);
+      if (cs > 1) {
+        const bool in = lane < cs;
+        total = warp_sum_u64(in ? sh.part_total[lane] : 0);
+        above_floor = warp_sum_u64(in ? sh.part_floor[lane] : 0);
+        s = warp_sum(in ? sh.part_sum[lane] : 0.f);
+        odd = __any_sync(0xffffffffu, in && sh.part_odd[lane]);
       }
-      sum = warp_sum(sum);
       if (lane == 0) {
-        sh.known_total = t;
-        sh.known_floor = fl;
-        sh.known_sum = sum;
-        sh.known_odd = bits;
+        sh.known_total = total;
+        sh.known_floor = above_floor;
+        sh.known_sum = s;
+        sh.known_odd = odd;
       }
     }
     sync();
@@ -705,58 +821,72 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample_filtered(FilteredArgs 
         if (wid == 0) {
           const int c = sh.known_odd ? (int)kDone : decide(tail);
           __syncwarp();
-          for (int o = 0; o < cs; ++o) {
+          for (int o = 1; o < cs; ++o) {
             Shared* peer = cl.map_shared_rank(&sh, o);
-            if (o && lane < NB / 32) peer->marks[lane] = sh.marks[lane];
+            if (lane < NB / 32) peer->marks[lane] = sh.marks[lane];
             if (lane == 0) {
               peer->gate = sh.gate;
               peer->command = c;
             }
           }
+          if (lane == 0) sh.command = c;
         }
       }
       sync();
       command = sh.command;
       if (command != kTail) break;
-      for (int j = g.q_lo + tid; j < g.q_hi; j += NT) {
-        float f[EPC];
-        values(j, f);
+      const int logits = (g.q_hi - g.q_lo) * EPC;
+      for (int e0 = tid; e0 < logits; e0 += 4 * NT) {
+        float x[4];
+        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < EPC; ++i) {
-          const float x = f[i];
-          if (x >= x_low && x < x1) {
-            const uint32_t w = sf_weight(x, m, q.r);
-            if (w) {
-              const int b = bin_of(x);
-              atomicAdd(&sh.cnt[b], 1u);
-              atomicAdd(&sh.lo[b], w & 0xffffu);
-              atomicAdd(&sh.hi[b], w >> 16);
-            }
-          }
+        for (int u = 0; u < 4; ++u) {
+          const int e = e0 + u * NT;
+          x[u] = e < logits ? value(g.q_lo + e / EPC, e % EPC) : -kInf;
         }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) w[u] = sf_weight(x[u], m, q.r);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (x[u] >= x_low && x[u] < x1) add_bins(x[u], w[u]);
       }
       sync();
-      merge_bins(NBT);
-      sync();
+      if (cs > 1) {
+        merge_bins(NBT);
+        sync();
+      }
     }
     if (command == kGather) {
-      const float gate = sh.gate ? x_low : x1;
-      for (int j = g.q_lo + tid; j < g.q_hi; j += NT) {
-        float f[EPC];
-        values(j, f);
+      auto take = [&](float x, int j, int i) {
+        const int b = bin_of(x);
+        if (((sh.marks[b >> 5] >> (b & 31)) & 1u) && sf_weight(x, m, q.r)) {
+          const int at = atomicAdd(&lead->n_list, 1);
+          if (at < CAP)
+            lead->list[at] = ((u64)Logit<T>::key(x) << 32) | (u64)(0xffffffffu - (uint32_t)(EPC * j - g.dc + i));
+        }
+      };
+      if (!sh.gate) {
+        for (int i0 = 0; i0 < queued; i0 += 128 / EPC) {
+          float x[4];
+          int j[4];
+          four_queued(i0, x, j);
 #pragma unroll
-        for (int i = 0; i < EPC; ++i) {
-          const float x = f[i];
-          if (x >= gate) {
-            const int b = bin_of(x);
-            if ((sh.marks[b >> 5] >> (b & 31)) & 1u) {
-              if (sf_weight(x, m, q.r)) {
-                const int at = atomicAdd(&lead->n_list, 1);
-                if (at < CAP)
-                  lead->list[at] =
-                      ((u64)Logit<T>::key(x) << 32) | (u64)(0xffffffffu - (uint32_t)(EPC * j - g.dc + i));
-              }
-            }
+          for (int u = 0; u < 4; ++u)
+            if (x[u] >= x1) take(x[u], j[u], lane % EPC);
+        }
+      } else {
+        const int logits = (g.q_hi - g.q_lo) * EPC;
+        for (int e0 = tid; e0 < logits; e0 += 4 * NT) {
+          float x[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int e = e0 + u * NT;
+            x[u] = e < logits ? value(g.q_lo + e / EPC, e % EPC) : -kInf;
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int e = e0 + u * NT;
+            if (x[u] >= x_low) take(x[u], g.q_lo + e / EPC, e % EPC);
           }
         }
       }
@@ -782,23 +912,34 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample_filtered(FilteredArgs 
       }
     } else {
       const int len = sh.n_list;
-      int pow2 = 32;
-      while (pow2 < len) pow2 *= 2;
-      for (int i = len + tid; i < pow2; i += NT) sh.list[i] = 0;
-      __syncthreads();
-      // bitonic sort, descending
-      for (int size = 2; size <= pow2; size *= 2)
-        for (int d = size / 2; d > 0; d /= 2) {
-          for (int i = tid; i < pow2 / 2; i += NT) {
-            const int x = 2 * i - (i & (d - 1)), y = x + d;
-            const u64 u = sh.list[x], v = sh.list[y];
-            if ((u < v) == ((x & size) == 0)) {
-              sh.list[x] = v;
-              sh.list[y] = u;
+      if (len <= 32) {
+        if (wid == 0) {
+          // bitonic sort in registers, descending
+          u64 e = lane < len ? sh.list[lane] : 0;
+#pragma unroll
+          for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+            for (int d = size / 2; d > 0; d /= 2) {
+              const u64 o = __shfl_xor_sync(0xffffffffu, e, d);
+              const bool keep_max = ((lane & d) == 0) == ((lane & size) == 0);
+              e = (e > o) == keep_max ? e : o;
             }
-          }
-          __syncthreads();
+          if (lane < len) sh.list[lane] = e;
+          __syncwarp();
         }
+      } else {
+        // each entry to the place that the number of larger ones gives; all differ
+        for (int i = tid; i < len; i += NT) {
+          const u64 e = sh.list[i];
+          int place = 0;
+#pragma unroll 8
+          for (int o = 0; o < len; ++o) place += sh.list[o] > e;
+          sh.incl[place] = e;
+        }
+        cta_sync();
+        for (int i = tid; i < len; i += NT) sh.list[i] = sh.incl[i];
+        cta_sync();
+      }
       if (wid == 0) {
         // running mass through each listed logit: through its bin's predecessor, plus the listed ones of its bin
         u64 sum = 0, off = 0, kept = 0;
@@ -842,7 +983,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample_filtered(FilteredArgs 
             const unsigned hit = __ballot_sync(0xffffffffu, j + lane < len && sh.incl[j + lane] >= t);
             if (hit) return j + __ffs(hit) - 1;
           }
-          return len - 1;  // not reached: the boundary's bin is listed
+          return max(len - 1, 0);  // not reached: the boundary's bin is listed
         };
         u64 all;
         if (sh.kb >= 0)
@@ -850,7 +991,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample_filtered(FilteredArgs 
         else
           all = whole ? sh.known_total : sh.pm[NBT - 1];
         if (q.p < 1.f) all = sh.incl[first_at_least(need_of(q.p, all))];
-        if (q.mp > 0.f) all = sh.known_floor < all ? sh.known_floor : all;
+        if (floored) all = sh.known_floor < all ? sh.known_floor : all;
         const int at = first_at_least(target_of(q.u, all) + 1);
         if (lane == 0) {
           const u64 e = sh.list[at];
@@ -859,23 +1000,24 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample_filtered(FilteredArgs 
         }
       }
     }
-    __syncthreads();  // the lists are free
+    cta_sync();  // the lists are free
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
   sync();  // no CTA leaves while a peer may still use its shared memory
 }
 
 namespace {
 
-constexpr int kSfSmallV = 4096;             // rows up to here: 128-thread CTAs
+constexpr int kSfSmallV = 2048;   // rows up to here, when there are enough to fill the GPU: a warp each
+constexpr int kSfMediumV = 8192;  // rows up to here: 128-thread CTAs
 constexpr long long kSfSlice = 64 << 10;    // bytes of a row per CTA, two CTAs per SM
 constexpr long long kSfSliceMax = 128 << 10;  // one CTA per SM; at most 65536 logits, which the bins' 32-bit sums allow
 constexpr long long kSfSliceMin = 8 << 10;
 
 // Launches the cluster kernel; *refused when no cluster of that shape fits.
-template <typename T, int NT, int NB, int CAP>
-cudaError_t launch_on_chip(const FilteredArgs& a, int cs, size_t smem, cudaStream_t st, bool* refused) {
-  auto kern = k_sample_filtered<T, NT, NB, CAP>;
+template <typename T, int NT, int NB, int CAP, int GROUPS>
+cudaError_t launch_on_chip(const FilteredArgs& a, int cs, int chunks, cudaStream_t st, bool* refused) {
+  const size_t smem = (size_t)chunks * 16 + (size_t)((chunks + NT - 1) / NT * NT) * 2;  // a slice and its queues
+  auto kern = k_sample_filtered<T, NT, NB, CAP, GROUPS>;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = smem;
@@ -888,23 +1030,26 @@ cudaError_t launch_on_chip(const FilteredArgs& a, int cs, size_t smem, cudaStrea
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
+  // A CTA alone is launched without a cluster: as clusters of one, only eight of them run on an SM.
+  if (cs == 1) attr[0] = attr[1];
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = cs == 1 ? 1 : 2;
   const void* site = reinterpret_cast<const void*>(kern);
   const int ok = cached(site, -1, [&](int) {
-    cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSfSliceMax + 32);
+    cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kSfSliceMax + kSfSliceMax / 8 + 2048));
     if (r == cudaSuccess) r = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (r != cudaSuccess) (void)cudaGetLastError();
     return r == cudaSuccess ? 1 : 0;
   });
   const int fit = ok <= 0 ? 0 : cached(site, (long long)smem * 32 + cs, [&](int) {
     int v = 0;
-    const cudaError_t r = cudaOccupancyMaxActiveClusters(&v, kern, &cfg);
+    const cudaError_t r = cs == 1 ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kern, NT, smem)
+                                  : cudaOccupancyMaxActiveClusters(&v, kern, &cfg);
     if (r != cudaSuccess) {
       (void)cudaGetLastError();
       return 0;
     }
-    return v;
+    return cs == 1 ? v * device_sms() : v;
   });
   if (fit < 1) {
     *refused = true;
@@ -912,7 +1057,7 @@ cudaError_t launch_on_chip(const FilteredArgs& a, int cs, size_t smem, cudaStrea
   }
   const long long clusters = a.n < fit ? a.n : fit;
   cfg.gridDim = dim3((unsigned)(clusters * cs));
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, chunks);
   if (e == cudaSuccess) note_launch();
   return e;
 }
@@ -925,8 +1070,11 @@ static cudaError_t launch_filtered(const FilteredArgs& a, cudaStream_t st) {
   if (sms <= 0) return cudaErrorUnknown;
   const long long bytes = (long long)a.V * sizeof(T) + 16;
   bool refused = false;
-  if (a.V <= kSfSmallV) {
-    const cudaError_t e = launch_on_chip<T, 128, 128, 256>(a, 1, (size_t)(bytes + 15) / 16 * 16, st, &refused);
+  if (a.V <= kSfSmallV && a.n >= sms * 8LL) {
+    const cudaError_t e = launch_on_chip<T, 32, 128, 128, 32>(a, 1, (int)((bytes + 15) / 16), st, &refused);
+    if (!refused) return e;
+  } else if (a.V <= kSfMediumV) {
+    const cudaError_t e = launch_on_chip<T, 128, 256, 256, 32>(a, 1, (int)((bytes + 15) / 16), st, &refused);
     if (!refused) return e;
   } else {
     int cs = 1;
@@ -935,7 +1083,7 @@ static cudaError_t launch_filtered(const FilteredArgs& a, cudaStream_t st) {
     while (cs < 8 && (long long)a.n * cs * 2 <= sms && bytes > cs * 2 * kSfSliceMin) cs *= 2;
     const long long slice = (bytes / 16 + cs) / cs * 16 + 16;
     if (slice <= kSfSliceMax) {
-      const cudaError_t e = launch_on_chip<T, 512, 1024, 1024>(a, cs, (size_t)slice, st, &refused);
+      const cudaError_t e = launch_on_chip<T, 512, 1024, 1024, 128>(a, cs, (int)(slice / 16), st, &refused);
       if (!refused) return e;
     }
   }
