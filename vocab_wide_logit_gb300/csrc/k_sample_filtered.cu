@@ -28,7 +28,6 @@ namespace {
 
 using u64 = unsigned long long;
 
-constexpr int kSfNT = 512;
 constexpr float kSfOne = 2147483648.f;  // 2^31, the weight of the row's maximum
 
 // A logit's value, and its order key: larger logit, larger key, -0 folded onto
@@ -62,11 +61,67 @@ __device__ __forceinline__ uint32_t sf_weight(float x, float m, float r) {
   return __float2uint_rn(__fmul_rn(expf(__fmul_rn(__fsub_rn(x, m), r)), kSfOne));
 }
 
-// Where a running measure passes its target.
-struct Cut {
-  uint32_t key;
-  u64 before;  // measure of the elements above `key`
-  u64 each;    // measure of one element at `key`
+// 16 bytes of logits as fp32.
+template <typename T>
+struct Chunk;
+template <>
+struct Chunk<uint16_t> {
+  static constexpr int N = 8;
+  static constexpr uint32_t NEG_INF = 0xff80ff80u;
+  static __device__ __forceinline__ void get(const uint4& v, float (&f)[8]) { unpack8(v, f); }
+};
+template <>
+struct Chunk<float> {
+  static constexpr int N = 4;
+  static constexpr uint32_t NEG_INF = 0xff800000u;
+  static __device__ __forceinline__ void get(const uint4& v, float (&f)[4]) {
+    f[0] = __uint_as_float(v.x);
+    f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z);
+    f[3] = __uint_as_float(v.w);
+  }
+};
+
+// A row as 16-byte chunks: chunk 0 starts at the row's first element rounded down
+// to 16 bytes, so that loads stay inside the 16-byte blocks that hold the row.
+template <typename T>
+struct Row {
+  static constexpr int EPC = Chunk<T>::N;
+  const uint4* base;
+  int dc, nq, V;  // elements before the row in chunk 0, chunks, length
+  __device__ __forceinline__ Row(const T* row, int V_) : V(V_) {
+    const uintptr_t ad = reinterpret_cast<uintptr_t>(row);
+    base = reinterpret_cast<const uint4*>(ad & ~(uintptr_t)15);
+    dc = (int)((ad & 15) / sizeof(T));
+    nq = (dc + V + EPC - 1) / EPC;
+  }
+  __device__ __forceinline__ int id(int j, int i) const { return EPC * j - dc + i; }
+  // the logits of chunk j; ids outside the row read as -inf
+  __device__ __forceinline__ void values(const uint4& raw, int j, float (&f)[EPC]) const {
+    Chunk<T>::get(raw, f);
+    if (j == 0 || j == nq - 1) {
+#pragma unroll
+      for (int i = 0; i < EPC; ++i)
+        if (id(j, i) < 0 || id(j, i) >= V) f[i] = -kInf;
+    }
+  }
+  // Calls body(j, chunk) for the chunks of [from, to) that this lane has, U loads
+  // at a time; all lanes of the warp together, with -inf past the end.
+  template <int NT, int U, typename Load, typename Body>
+  __device__ __forceinline__ void walk(int from, int to, Load load, Body body) const {
+#pragma unroll 1
+    for (int j0 = from + (int)(threadIdx.x & ~31u); j0 < to; j0 += U * NT) {
+      uint4 raw[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = j0 + u * NT + (int)(threadIdx.x & 31u);
+        raw[u] = make_uint4(Chunk<T>::NEG_INF, Chunk<T>::NEG_INF, Chunk<T>::NEG_INF, Chunk<T>::NEG_INF);
+        if (j < to) raw[u] = load(j);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) body(j0 + u * NT + (int)(threadIdx.x & 31u), raw[u]);
+    }
+  }
 };
 
 template <int NT>
@@ -82,45 +137,148 @@ __device__ __forceinline__ u64 block_sum(u64 v, u64* red) {
   return s;
 }
 
-// What is summed: 1 for each element (its rank), or its weight.
-enum Measure { kCount, kMass };
-
-// Measure of the row's elements with key >= lo.
+// The mass of a row's logits with weight >= floor_w.
 template <typename T, int NT>
-__device__ u64 row_measure(const T* row, int V, Measure what, uint32_t lo, float m, float r, u64* red) {
+__device__ u64 row_mass(const Row<T>& row, uint32_t floor_w, float m, float r, u64* red) {
   u64 s = 0;
-  for (int i = threadIdx.x; i < V; i += NT) {
-    const float x = Logit<T>::get(row, i);
-    if (Logit<T>::key(x) >= lo) s += (what == kCount) ? 1ull : (u64)sf_weight(x, m, r);
-  }
+  row.template walk<NT, 2>(
+      0, row.nq, [&](int j) { return __ldg(row.base + j); },
+      [&](int j, const uint4& raw) {
+        float f[Chunk<T>::N];
+        row.values(raw, j, f);
+#pragma unroll
+        for (int i = 0; i < Chunk<T>::N; ++i) {
+          const uint32_t w = sf_weight(f[i], m, r);
+          s += w >= floor_w ? w : 0u;
+        }
+      });
   return block_sum<NT>(s, red);
 }
 
-// The first element whose running measure passes t (t < the whole row's
-// measure), by bisection on its key: the largest key whose inclusive measure is
-// above t.
-template <typename T, int NT>
-__device__ Cut row_select(const T* row, int V, Measure what, u64 t, float m, float r, u64* red) {
-  uint32_t lo = Logit<T>::key(-kInf), hi = Logit<T>::key(m);  // measure(lo) > t; the answer lies in [lo, hi]
-  u64 above = 0;                                              // measure of the keys above hi
-  while (lo < hi) {
-    const uint32_t mid = hi - (hi - lo) / 2;  // in (lo, hi]
-    const u64 s = row_measure<T, NT>(row, V, what, mid, m, r, red);
-    if (s > t) {
-      lo = mid;
-    } else {
-      above = s;
-      hi = mid - 1;
+// Where a running measure passes its target.
+struct Cut {
+  uint32_t key;
+  u64 before;        // mass of the logits above `key`
+  u64 count_before;  // and their number
+  u64 each;          // weight of a logit at `key`
+};
+
+// Scratch of a search: counts, and masses as three sums of 11, 10 and 11 bits of
+// the weights, which 2^21 logits cannot overflow.
+template <int NB>
+struct Bins {
+  uint32_t *cnt, *w0, *w1, *w2;  // [NB]
+  u64* red;                      // [NT / 32]
+  u64* out;                      // [4]
+};
+
+// The first logit with a weight whose running count (by_count) or mass passes t,
+// t below the row's: a radix search on the key, NB ways a pass. One CTA.
+template <typename T, int NT, int NB>
+__device__ __noinline__ Cut row_select(const Row<T> row, bool by_count, u64 t, float m, float r, const Bins<NB> b) {
+  constexpr int NW = NT / 32, PER = NB / NT > 0 ? NB / NT : 1;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  uint32_t lo = Logit<T>::key(-kInf), hi = Logit<T>::key(m);
+  u64 mass0 = 0, count0 = 0;  // of the logits above hi
+  for (;;) {
+    int s = 0;
+    while (((hi - lo) >> s) >= (uint32_t)NB) ++s;
+    __syncthreads();
+    for (int i = tid; i < NB; i += NT) b.cnt[i] = b.w0[i] = b.w1[i] = b.w2[i] = 0;
+    __syncthreads();
+    row.template walk<NT, 2>(
+        0, row.nq, [&](int j) { return __ldg(row.base + j); },
+        [&](int j, const uint4& raw) {
+          float f[Chunk<T>::N];
+          row.values(raw, j, f);
+#pragma unroll
+          for (int i = 0; i < Chunk<T>::N; ++i) {
+            const uint32_t key = Logit<T>::key(f[i]);
+            const uint32_t w = sf_weight(f[i], m, r);
+            const bool in = key >= lo && key <= hi && w;
+            // a warp whose logits all fall on one bin adds them up first: ties are what this search is for
+            const unsigned who = __ballot_sync(0xffffffffu, in);
+            if (!who) continue;
+            const int bin = in ? (int)((hi - key) >> s) : -1;
+            const int first = __shfl_sync(0xffffffffu, bin, __ffs(who) - 1);
+            if (__all_sync(0xffffffffu, !in || bin == first)) {
+              const uint32_t a = __reduce_add_sync(0xffffffffu, in ? w & 0x7ffu : 0u);
+              const uint32_t c = __reduce_add_sync(0xffffffffu, in ? w >> 11 & 0x3ffu : 0u);
+              const uint32_t d = __reduce_add_sync(0xffffffffu, in ? w >> 21 : 0u);
+              if (lane == 0) {
+                atomicAdd(&b.cnt[first], (uint32_t)__popc(who));
+                atomicAdd(&b.w0[first], a);
+                atomicAdd(&b.w1[first], c);
+                atomicAdd(&b.w2[first], d);
+              }
+            } else if (in) {
+              atomicAdd(&b.cnt[bin], 1u);
+              atomicAdd(&b.w0[bin], w & 0x7ffu);
+              atomicAdd(&b.w1[bin], w >> 11 & 0x3ffu);
+              atomicAdd(&b.w2[bin], w >> 21);
+            }
+          }
+        });
+    __syncthreads();
+    // running sums; the thread that meets t writes what it found
+    u64 sc = 0, sm = 0;
+    for (int i = 0; i < PER; ++i) {
+      const int k = tid * PER + i;
+      if (k < NB) {
+        sc += b.cnt[k];
+        sm += (u64)b.w0[k] + ((u64)b.w1[k] << 11) + ((u64)b.w2[k] << 21);
+      }
+    }
+    u64 ic = sc, im = sm;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 uc = __shfl_up_sync(0xffffffffu, ic, o), um = __shfl_up_sync(0xffffffffu, im, o);
+      if (lane >= o) {
+        ic += uc;
+        im += um;
+      }
+    }
+    u64 bc = count0 + ic - sc, bm = mass0 + im - sm;
+    if (lane == 31) b.red[wid] = ic;
+    __syncthreads();
+    for (int w = 0; w < wid && w < NW; ++w) bc += b.red[w];
+    __syncthreads();
+    if (lane == 31) b.red[wid] = im;
+    if (tid == 0) b.out[3] = 0;
+    __syncthreads();
+    for (int w = 0; w < wid && w < NW; ++w) bm += b.red[w];
+    for (int i = 0; i < PER; ++i) {
+      const int k = tid * PER + i;
+      if (k >= NB) break;
+      const u64 c = b.cnt[k], mass = (u64)b.w0[k] + ((u64)b.w1[k] << 11) + ((u64)b.w2[k] << 21);
+      const u64 at = by_count ? bc : bm, step = by_count ? c : mass;
+      if (at <= t && t < at + step) {
+        b.out[0] = (u64)k;
+        b.out[1] = bc;
+        b.out[2] = bm;
+        b.out[3] = 1;
+      }
+      bc += c;
+      bm += mass;
+    }
+    __syncthreads();
+    Cut c = {hi, mass0, count0, 1};
+    if (!b.out[3]) return c;  // not reached: t is below the row's measure
+    hi -= (uint32_t)b.out[0] << s;
+    if (hi - lo > (1u << s) - 1u) lo = hi - ((1u << s) - 1u);
+    count0 = b.out[1];
+    mass0 = b.out[2];
+    if (s == 0) {
+      c.key = hi;
+      c.before = mass0;
+      c.count_before = count0;
+      c.each = (u64)sf_weight(Logit<T>::value(hi), m, r);
+      return c;
     }
   }
-  Cut c;
-  c.key = lo;
-  c.before = above;
-  c.each = what == kCount ? 1ull : (u64)sf_weight(Logit<T>::value(lo), m, r);
-  return c;
 }
 
-// Id of the j-th (from 0) element with the given key, in id order.
+// Id of the j-th (from 0) logit with the given key, in id order. One CTA.
 template <typename T, int NT>
 __device__ int row_nth(const T* row, int V, uint32_t key, u64 j, u64* red, int* slot) {
   const int per = (V + NT - 1) / NT;
@@ -147,16 +305,11 @@ __device__ int row_nth(const T* row, int V, uint32_t key, u64 j, u64* red, int* 
   return *slot;
 }
 
-// Mass of the prefix that ends with the first element whose running measure passes t.
-__device__ __forceinline__ u64 cut_mass_through(const Cut& c, u64 t) {
-  const u64 j = (t - c.before) / c.each;
-  return c.before + (j + 1) * c.each;
-}
-
 // A row's filter parameters, and what its kernels share of it.
 struct RowParams {
   float tau, p, mp, u, r;
-  int k;  // 0: no top-k
+  int k;             // 0: no top-k
+  uint32_t floor_w;  // min-p keeps the weights from here
   bool bad;
 };
 
@@ -171,6 +324,7 @@ __device__ __forceinline__ RowParams row_params(const FilteredArgs& a, long long
   q.bad = !(q.tau >= 0.f && q.tau < kInf) || !(q.u >= 0.f && q.u < 1.f) || !(q.p > 0.f && q.p <= 1.f) ||
           !(q.mp >= 0.f && q.mp <= 1.f);
   q.r = fminf(__frcp_rn(q.tau), 3.402823466e38f);
+  q.floor_w = (uint32_t)ceil((double)q.mp * (double)kSfOne);
   return q;
 }
 
@@ -178,139 +332,98 @@ __device__ __forceinline__ RowParams row_params(const FilteredArgs& a, long long
 __device__ __forceinline__ u64 need_of(float p, u64 total) { return (u64)ceil((double)p * (double)total); }
 __device__ __forceinline__ u64 target_of(float u, u64 total) { return (u64)floor((double)u * (double)total); }
 
-// The row's token by bisection on the keys, one CTA re-reading the row for every
-// question. Slow (some 50 passes) and without any assumption on the row: it
-// finishes the rows whose ties are too many for the lists of the fast kernel.
-template <typename T, int NT>
-__device__ __noinline__ int row_exact(const T* row, int V, const RowParams& q, float m, u64* red, int* slot) {
+// The row's token, each question by a search over the row, which one CTA re-reads
+// some ten times. It assumes nothing of the row: it finishes those whose ties are
+// too many for the lists of the fast kernel.
+template <typename T, int NT, int NB>
+__device__ __noinline__ int row_exact(const T* p, int V, const RowParams& q, float m, const Bins<NB>& b, int* slot) {
+  const Row<T> row(p, V);
   const float r = q.r;
-  u64 total = row_measure<T, NT>(row, V, kMass, 0u, m, r, red);
+  u64 total = row_mass<T, NT>(row, 0u, m, r, b.red);
   if (q.k) {
-    const Cut c = row_select<T, NT>(row, V, kCount, (u64)q.k - 1, m, r, red);
-    const u64 above = row_measure<T, NT>(row, V, kMass, c.key + 1u, m, r, red);
-    total = above + ((u64)q.k - c.before) * sf_weight(Logit<T>::value(c.key), m, r);
+    // a top-k that reaches the logits without a weight leaves the mass as it is
+    const Cut c = row_select<T, NT, NB>(row, true, (u64)q.k - 1, m, r, b);
+    if (b.out[3]) total = c.before + ((u64)q.k - c.count_before) * c.each;
   }
+  auto through = [&](const Cut& c, u64 t) { return c.before + ((t - c.before) / c.each + 1) * c.each; };
   if (q.p < 1.f) {
     // kept while the mass before is below p * total: through the first whose running mass reaches it
     const u64 need = need_of(q.p, total);
-    if (need < total) total = cut_mass_through(row_select<T, NT>(row, V, kMass, need - 1, m, r, red), need - 1);
+    if (need < total) total = through(row_select<T, NT, NB>(row, false, need - 1, m, r, b), need - 1);
   }
   if (q.mp > 0.f) {
-    const double floor_w = (double)q.mp * (double)kSfOne;
-    u64 sum = 0;
-    for (int i = threadIdx.x; i < V; i += NT) {
-      const uint32_t w = sf_weight(Logit<T>::get(row, i), m, r);
-      if ((double)w >= floor_w) sum += w;
-    }
-    sum = block_sum<NT>(sum, red);
+    const u64 sum = row_mass<T, NT>(row, q.floor_w, m, r, b.red);
     total = sum < total ? sum : total;
   }
   const u64 t = target_of(q.u, total);
-  const Cut c = row_select<T, NT>(row, V, kMass, t, m, r, red);
-  return row_nth<T, NT>(row, V, c.key, (t - c.before) / c.each, red, slot);
+  const Cut c = row_select<T, NT, NB>(row, false, t, m, r, b);
+  return row_nth<T, NT>(p, V, c.key, (t - c.before) / c.each, b.red, slot);
 }
 
 }  // namespace
 
-// One CTA per row, re-read from global memory: rows too long for a cluster's shared memory.
-template <typename T>
-__global__ void __launch_bounds__(kSfNT) k_sample_filtered_rows(FilteredArgs a) {
-  pdl_wait();
-  pdl_release();
-  __shared__ u64 red[kSfNT / 32];
-  __shared__ float fred[kSfNT / 32];
-  __shared__ int slot;
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  for (long long n = blockIdx.x; n < a.n; n += gridDim.x) {
-    const T* row = static_cast<const T*>(a.x) + n * a.ld;
-    const int V = a.V;
-    float m = -kInf;
-    for (int i = tid; i < V; i += kSfNT) m = fmaxf(m, Logit<T>::get(row, i));
-    m = warp_max(m);
-    __syncthreads();
-    if (lane == 0) fred[wid] = m;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kSfNT / 32; ++i) m = fmaxf(m, fred[i]);
-    // The sum is NaN when the row holds a NaN or +inf (inf - inf), or nothing but -inf.
-    float s = 0.f;
-    int odd = 0;  // a NaN or +inf
-    for (int i = tid; i < V; i += kSfNT) {
-      const float x = Logit<T>::get(row, i);
-      odd |= !(x < kInf);
-      s += expf(x - m);
-    }
-    s = warp_sum(s);
-    odd = __syncthreads_or(odd);
-    if (lane == 0) fred[wid] = s;
-    __syncthreads();
-    s = 0.f;
-#pragma unroll
-    for (int i = 0; i < kSfNT / 32; ++i) s += fred[i];
-    const float lse = m + logf(s);
-
-    const RowParams q = row_params(a, n);
-    int token = -1;
-    float lp = __int_as_float(0x7fffffff);
-    if (q.bad || odd || m == -kInf) {
-      if (tid == 0 && (q.bad || odd)) report(a.d_status, q.bad ? DS_DEV_ERR_PARAM : DS_DEV_ERR_LOGITS);
-    } else {
-      token = q.tau == 0.f ? row_nth<T, kSfNT>(row, V, Logit<T>::key(m), 0, red, &slot)
-                           : row_exact<T, kSfNT>(row, V, q, m, red, &slot);
-      lp = Logit<T>::get(row, token) - lse;
-    }
-    if (tid == 0) {
-      a.out_tokens[n] = token;
-      a.out_logprobs[n] = lp;
-    }
-    __syncthreads();
-  }
-}
-
-// ---------------------------------------------------------------- the row on chip
+// ---------------------------------------------------------------- the fast kernel
 //
-// A cluster of cs CTAs holds a row in shared memory, a contiguous slice each, and
-// answers the three questions from histograms over bins of x:
+// A cluster of cs CTAs takes a row, a contiguous slice each, and answers the
+// three questions from histograms over bins of x. A short slice is held in shared
+// memory (RESIDENT), the next row's copied there while this one is answered; a
+// long one is read from HBM for the first walk and from L2 for the second.
 //   max     m, the smallest logit that is no mask, and a cut x1: the least of
 //           GROUPS groups' maxima, so that GROUPS logits at least are above it
 //           and, of independent ones, about ln(GROUPS) times as many
-//   weigh   sum exp(x - m); the mass of the row (unless a small top-k makes it
-//           needless); and for the logits >= x1, the ones that decide nearly
-//           every row, count and mass in bins linear in x
+//   weigh   sum exp(x - m), and (unless a small top-k makes it needless) the
+//           tempered sum, both in fp32; and for the logits >= x1, the ones that
+//           decide nearly every row, exact count and mass in bins linear in x
 //   decide  the CTA of rank 0 sums up the bins and finds those where the top-k,
-//           top-p and draw boundaries can lie. If one lies below x1, the rest of
-//           the row gets bins too.
+//           top-p, min-p and draw boundaries can lie, given what the tempered
+//           sum says of the row's mass. If one lies below x1, the cut is lowered
+//           and the bins are made again.
 //   gather  the logits of those bins, a few dozen, come to rank 0, which sorts
 //           them and answers exactly.
+// The row's mass is used through "which logit does top_p T (or u T) fall on", so
+// bounds on it nearly always do: a_i = ex2(fl(y log2 e)) on the weight's own
+// y = fl(fl(x - m) r) is off by |y| 7.3e-8 <= 1.6e-6 for the rounding of the
+// product, 2.4e-7 for ex2.approx and 1.2e-7 for expf, relatively (kSfSlack); the
+// sum, a tree over 8 logits, a thread's chunks in turn and a tree over threads and
+// CTAs, by 2^-24 for each of these steps (kSfRounding); and each weight's rounding
+// to an integer by half a unit. Where the boundary's logits are too light for
+// that, the cluster weighs the rest of the row exactly (kWeigh), and where it
+// falls between two listed logits all the same, rank 0 does.
 // A row whose boundary bins hold more than CAP logits (ties) is finished by
-// row_exact. So a logit costs two exponentials and its share of two walks over
-// shared memory, an atomic only above x1.
+// row_exact. So a logit costs two ex2 and its share of two walks over the
+// row; an exact weight and an atomic only above x1.
 namespace {
 
-template <int NT, int NB, int CAP>
+template <int NT, int NB, int CAP, int QCAP>
 struct SfShared {
   uint32_t cnt[NB], lo[NB], hi[NB];  // this CTA's bins: count, and mass as two sums of 16-bit halves
   u64 pm[NB];                        // rank 0: mass through each bin
   uint32_t pc[NB];                   // rank 0: count through each bin
   u64 list[CAP];                     // rank 0: gathered (key, ~id)
-  u64 incl[CAP];                     // rank 0: running mass through each of them
+  u64 incl[CAP];                     // this CTA's gathered ones; rank 0: running mass through each listed one
+  uint16_t queue[NT / 32][QCAP];     // each warp's chunks that hold a logit >= x1, by their place in its walk
   u64 full;                          // the slice's copy is done
-  u64 red[NT / 32], red2[NT / 32];
+  u64 red[NT / 32];
   float fred[3][NT / 32], sred[2][NT / 32];
+  int ired[3][NT / 32];
   uint32_t marks[NB / 32];
   // each CTA's partials, pushed by it to everyone (max) or to rank 0 (weigh)
   float part_max[16], part_min[16], part_cut[16], part_sum[16];
-  u64 part_total[16], part_floor[16];
-  int part_odd[16];
-  int command, gate, n_list, first_id;
-  u64 known_total, known_floor;
+  float part_tempered[16];
+  u64 part_total[16];
+  int part_odd[16], part_floor[16], part_below[16];
+  int command, n_list, n_mine, mine_at, first_id;
+  u64 t_lo, t_hi;  // bounds of the row's mass
   float known_sum;
-  int known_odd;
-  int kb;
+  int known_odd, known_floor, known_below;
+  int kb, again, crowded;
+  u64 found[4];
   int slot;
 };
 
-enum Command { kDone, kGather, kTail, kExact };
+enum Command { kDone, kGather, kWeigh, kLower, kExact };
+
+constexpr double kSfSlack = 2.2e-6, kSfRounding = 6e-8;
 
 // Index of the first element of the ascending array that is >= t (n if none), by one warp.
 template <typename U>
@@ -320,24 +433,6 @@ __device__ __forceinline__ int warp_lower_bound(const U* v, int n, U t, int lane
   if (seg == 32) return n;
   return seg * step + __popc(__ballot_sync(0xffffffffu, lane < step && v[seg * step + lane] < t));
 }
-
-template <typename T>
-struct Chunk;  // 16 bytes of logits as fp32
-template <>
-struct Chunk<uint16_t> {
-  static constexpr int N = 8;
-  static __device__ __forceinline__ void get(const uint4& v, float (&f)[8]) { unpack8(v, f); }
-};
-template <>
-struct Chunk<float> {
-  static constexpr int N = 4;
-  static __device__ __forceinline__ void get(const uint4& v, float (&f)[4]) {
-    f[0] = __uint_as_float(v.x);
-    f[1] = __uint_as_float(v.y);
-    f[2] = __uint_as_float(v.z);
-    f[3] = __uint_as_float(v.w);
-  }
-};
 
 template <int N>
 __device__ __forceinline__ float max_of(const float (&f)[N]) {
@@ -373,11 +468,10 @@ __device__ __forceinline__ bool sf_wait(u64* bar, uint32_t parity) {
 
 }  // namespace
 
-template <typename T, int NT, int NB, int CAP, int GROUPS>
-__global__ void __launch_bounds__(NT, 1024 / NT)
-    k_sample_filtered(FilteredArgs a, int slice_chunks) {
-  constexpr int EPC = Chunk<T>::N, NBT = NB / 2, NW = NT / 32;
-  using Shared = SfShared<NT, NB, CAP>;
+template <typename T, int NT, int NB, int CAP, int GROUPS, int QCAP, bool RESIDENT>
+__global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT) k_sample_filtered(FilteredArgs a) {
+  constexpr int EPC = Chunk<T>::N, NW = NT / 32, U = RESIDENT ? 1 : 4;
+  using Shared = SfShared<NT, NB, CAP, QCAP>;
   extern __shared__ uint4 slice[];
   __shared__ Shared sh;
   cg::cluster_group cl = cg::this_cluster();
@@ -385,9 +479,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT)
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const long long n_clusters = (long long)gridDim.x / cs, cid = (long long)blockIdx.x / cs;
   Shared* lead = cl.map_shared_rank(&sh, 0);
-  // behind the slice: each warp's queue of its chunks that hold a logit >= x1, room for all of them
-  const int walk = ((slice_chunks + NT - 1) / NT) * 32;
-  uint16_t* queue = reinterpret_cast<uint16_t*>(slice + slice_chunks) + wid * walk;
+  uint16_t* queue = sh.queue[wid];
   auto cta_sync = [&] {
     if (NT == 32)
       __syncwarp();
@@ -408,28 +500,15 @@ __global__ void __launch_bounds__(NT, 1024 / NT)
   pdl_wait();
   pdl_release();
 
-  // This CTA's slice of a row: chunks [q_lo, q_hi) of the row's 16-byte chunks
-  // (chunk 0 starts at the row's first element rounded down to 16 bytes; the
-  // copies stay inside the 16-byte blocks that hold the row).
-  struct Slice {
-    const uint4* base;
-    int dc, nq, q_lo, q_hi;
-  };
-  auto slice_of = [&](long long n) {
-    Slice g;
-    const uintptr_t ad = reinterpret_cast<uintptr_t>(static_cast<const T*>(a.x) + n * a.ld);
-    g.base = reinterpret_cast<const uint4*>(ad & ~(uintptr_t)15);
-    g.dc = (int)((ad & 15) / sizeof(T));
-    g.nq = (g.dc + a.V + EPC - 1) / EPC;
-    g.q_lo = (int)((long long)rank * g.nq / cs);
-    g.q_hi = (int)((long long)(rank + 1) * g.nq / cs);
-    return g;
-  };
+  // This CTA's slice of a row: chunks [q_lo, q_hi).
+  auto row_of = [&](long long n) { return Row<T>(static_cast<const T*>(a.x) + n * a.ld, a.V); };
+  auto from_of = [&](const Row<T>& g, int r) { return (int)((long long)r * g.nq / cs); };
   // One bulk copy of the row's slice, started when nobody reads the last one any more.
   auto start_copy = [&](long long n) {
-    if (tid == 0 && n < a.n) {
-      const Slice g = slice_of(n);
-      const uint32_t bytes = (uint32_t)(g.q_hi - g.q_lo) * 16u;
+    if (RESIDENT && tid == 0 && n < a.n) {
+      const Row<T> g = row_of(n);
+      const int from = from_of(g, rank);
+      const uint32_t bytes = (uint32_t)(from_of(g, rank + 1) - from) * 16u;
       asm volatile("{\n.reg .b64 t;\nmbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1;\n}" ::"r"(sf_smem(&sh.full)),
                    "r"(bytes)
                    : "memory");
@@ -437,7 +516,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT)
         asm volatile(
             "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                 sf_smem(slice)),
-            "l"(g.base + g.q_lo), "r"(bytes), "r"(sf_smem(&sh.full))
+            "l"(g.base + from), "r"(bytes), "r"(sf_smem(&sh.full))
             : "memory");
     }
   };
@@ -445,35 +524,30 @@ __global__ void __launch_bounds__(NT, 1024 / NT)
 
   uint32_t parity = 0;
   for (long long n = cid; n < a.n; n += n_clusters, parity ^= 1u) {
-    const Slice g = slice_of(n);
+    const Row<T> g = row_of(n);
+    const int q_lo = from_of(g, rank), q_hi = from_of(g, rank + 1);
     const RowParams q = row_params(a, n);
-    // the logits of chunk j; ids outside the row read as -inf
-    auto values = [&](int j, float (&f)[EPC]) {
-      Chunk<T>::get(slice[j - g.q_lo], f);
-      if (j == 0 || j == g.nq - 1) {
-#pragma unroll
-        for (int i = 0; i < EPC; ++i) {
-          const int e = EPC * j - g.dc + i;
-          if (e < 0 || e >= a.V) f[i] = -kInf;
-        }
-      }
+    auto walk = [&](auto body) {
+      g.template walk<NT, U>(
+          q_lo, q_hi, [&](int j) { return RESIDENT ? slice[j - q_lo] : __ldg(g.base + j); }, body);
     };
     for (int i = tid; i < NB; i += NT) sh.cnt[i] = sh.lo[i] = sh.hi[i] = 0;
     if (tid == 0) {
-      sh.n_list = 0;
+      sh.n_list = sh.n_mine = 0;
       sh.first_id = INT_MAX;
+      sh.crowded = 0;
     }
-    if (!sf_wait(&sh.full, parity)) report(a.d_status, DS_DEV_ERR_TIMEOUT);
+    if (RESIDENT && !sf_wait(&sh.full, parity)) report(a.d_status, DS_DEV_ERR_TIMEOUT);
 
     // ---- max
     float mx = -kInf, mn = kInf;
-    for (int j = g.q_lo + tid; j < g.q_hi; j += NT) {
+    walk([&](int j, const uint4& raw) {
       float f[EPC];
-      values(j, f);
+      g.values(raw, j, f);
       mx = fmaxf(mx, max_of(f));
 #pragma unroll
       for (int i = 0; i < EPC; ++i) mn = fminf(mn, f[i] > -3e37f ? f[i] : kInf);
-    }
+    });
     float m, lo, cut;
     {
       float grp = mx;
@@ -517,24 +591,21 @@ __global__ void __launch_bounds__(NT, 1024 / NT)
     // their size, which needs a range that ends above them.
     const float lowest = (m - 24.f * q.tau) - fabsf(m) * 2.4e-7f;
     const float x_low = lowest > -3e37f ? fmaxf(fminf(lo, m), lowest) : fmaxf(lowest, -3.402823466e38f);
-    const float x1 = fmaxf(cut, x_low);  // splits the rest
-    const float sc1 = fminf((float)NBT / (m - x1), 3.402823466e38f);
-    const float sc2 = fminf((float)(NB - NBT) / (x1 - x_low), 3.402823466e38f);
-    auto bin_of = [&](float x) {  // for x_low <= x <= m
-      return x >= x1 ? min(NBT - 1, __float2int_rz((m - x) * sc1))
-                     : min(NB - 1, NBT + min(NB, __float2int_rz((x1 - x) * sc2)));
-    };
+    float x1 = fmaxf(cut, x_low);
+    float per_x = fminf((float)NB / (m - x1), 3.402823466e38f);
+    auto bin_of = [&](float x) { return min(NB - 1, __float2int_rz((m - x) * per_x)); };  // for x1 <= x <= m
     const bool finite = m > -kInf && m < kInf;
     const bool drawn = !q.bad && q.tau > 0.f && finite;
     const bool greedy = !q.bad && q.tau == 0.f && finite;
     // A top-k of at most GROUPS ends above x1: the mass below is then not asked for.
     const bool whole = drawn && !(q.k && q.k <= GROUPS);
+    const bool tempered = whole && x1 > x_low && q.r != 1.f;
     const bool floored = q.mp > 0.f;
-    const uint32_t floor_i = (uint32_t)ceil((double)q.mp * (double)kSfOne);
     // one logit of chunk j
     auto value = [&](int j, int i) {
-      const int e = EPC * j - g.dc + i;
-      const float x = Logit<T>::load(reinterpret_cast<const T*>(slice) + (EPC * (j - g.q_lo) + i));
+      const float x = RESIDENT ? Logit<T>::load(reinterpret_cast<const T*>(slice) + (EPC * (j - q_lo) + i))
+                               : Logit<T>::get(reinterpret_cast<const T*>(g.base), (long long)EPC * j + i);
+      const int e = g.id(j, i);
       return e >= 0 && e < a.V ? x : -kInf;
     };
     auto add_bins = [&](float x, uint32_t w) {
@@ -547,100 +618,157 @@ __global__ void __launch_bounds__(NT, 1024 / NT)
     };
 
     // ---- weigh
-    float s = 0.f;
-    u64 total = 0, above_floor = 0;
+    float s = 0.f, st = 0.f;
     int first = INT_MAX, odd = 0;
+    const float2 neg_m = make_float2(-m, -m), l2e = make_float2(kLog2e, kLog2e), rr = make_float2(q.r, q.r);
     int queued = 0;
-    for (int j0 = g.q_lo + wid * 32; j0 < g.q_hi; j0 += NT) {
-      const int j = j0 + lane;
+    // chunks with a logit above the cut go to the warp's queue
+    auto enqueue = [&](int j, bool high) {
+      const unsigned who = __ballot_sync(0xffffffffu, high);
+      const int at = queued + __popc(who & ((1u << lane) - 1u));
+      if (high && at < QCAP) queue[at] = (uint16_t)((j - q_lo) / NT * 32 + lane);
+      queued += __popc(who);
+    };
+    walk([&](int j, const uint4& raw) {
       float f[EPC];
-      if (j < g.q_hi) {
-        values(j, f);
-      } else {
-#pragma unroll
-        for (int i = 0; i < EPC; ++i) f[i] = -kInf;
-      }
+      g.values(raw, j, f);
       const float c = max_of(f);
-      float part = 0.f;
+      float2 d[EPC / 2], e[EPC / 2];
 #pragma unroll
-      for (int i = 0; i < EPC; ++i) part += ex2_approx((f[i] - m) * kLog2e);
-      s += part;
-      if (whole) {
+      for (int i = 0; i < EPC / 2; ++i) d[i] = __fadd2_rn(make_float2(f[2 * i], f[2 * i + 1]), neg_m);
+      auto sum_of_ex2 = [&]() {
 #pragma unroll
-        for (int i = 0; i < EPC; ++i) {
-          const uint32_t w = sf_weight(f[i], m, q.r);
-          total += w;
-          if (floored) above_floor += w >= floor_i ? w : 0u;
+        for (int i = 0; i < EPC / 2; ++i) {
+          e[i] = __fmul2_rn(e[i], l2e);
+          e[i] = make_float2(ex2_approx(e[i].x), ex2_approx(e[i].y));
         }
+#pragma unroll
+        for (int o = 1; o < EPC / 2; o *= 2)
+#pragma unroll
+          for (int i = 0; i + o < EPC / 2; i += 2 * o) e[i] = __fadd2_rn(e[i], e[i + o]);
+        return e[0].x + e[0].y;
+      };
+#pragma unroll
+      for (int i = 0; i < EPC / 2; ++i) e[i] = d[i];
+      s += sum_of_ex2();
+      if (tempered) {
+#pragma unroll
+        for (int i = 0; i < EPC / 2; ++i) e[i] = __fmul2_rn(d[i], rr);
+        st += sum_of_ex2();
       }
-      const unsigned high = __ballot_sync(0xffffffffu, drawn && c >= x1);
-      if (drawn && c >= x1) queue[queued + __popc(high & ((1u << lane) - 1u))] = (uint16_t)(j - g.q_lo);
-      queued += __popc(high);
+      enqueue(j, drawn && c >= x1);
       if (greedy && c == m) {
 #pragma unroll
         for (int i = 0; i < EPC; ++i)
-          if (f[i] == m) first = min(first, EPC * j - g.dc + i);
+          if (f[i] == m) first = min(first, g.id(j, i));
       }
       if (!finite) {
 #pragma unroll
         for (int i = 0; i < EPC; ++i) odd |= !(f[i] < kInf);
       }
-    }
+    });
     // The queued chunks, a logit per lane: in the walk itself a few lanes at a
-    // time would weigh while the others wait.
-    __syncwarp();
+    // time would weigh while the others wait. A warp whose queue did not hold them
+    // all (most of its chunks are high then) walks its chunks again.
+    auto queued_chunk = [&](int i) {
+      const int at = queue[i];
+      return q_lo + wid * 32 + at / 32 * NT + at % 32;
+    };
     // Four logits of the queued chunks per lane, -inf past their end.
     auto four_queued = [&](int i0, float (&x)[4], int (&j)[4]) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) j[u] = g.q_lo + queue[min(i0 + lane / EPC + u * (32 / EPC), queued - 1)];
+      for (int u = 0; u < 4; ++u) j[u] = queued_chunk(min(i0 + lane / EPC + u * (32 / EPC), queued - 1));
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         x[u] = value(j[u], lane % EPC);
         if (i0 + lane / EPC + u * (32 / EPC) >= queued) x[u] = -kInf;
       }
     };
-    for (int i0 = 0; i0 < queued; i0 += 128 / EPC) {
-      float x[4];
-      int j[4];
-      four_queued(i0, x, j);
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (x[u] >= x1) {
-          const uint32_t w = sf_weight(x[u], m, q.r);
-          add_bins(x[u], w);
-          if (!whole && floored) above_floor += w >= floor_i ? w : 0u;
+    // min-p: the last bin with a logit that stays, and whether one above x1 does not
+    int floor_bin = -1, below = 0;
+    auto bin_queued = [&] {
+      __syncwarp();
+      floor_bin = -1;
+      below = 0;
+      auto add = [&](float x, uint32_t w) {
+        if (x >= x1) {
+          add_bins(x, w);
+          if (floored) {
+            if (w >= q.floor_w)
+              floor_bin = max(floor_bin, bin_of(x));
+            else
+              below = 1;
+          }
         }
-    }
-    __syncwarp();
+      };
+      if (queued <= QCAP) {
+        for (int i0 = 0; i0 < queued; i0 += 128 / EPC) {
+          float x[4];
+          uint32_t w[4];
+          int j[4];
+          four_queued(i0, x, j);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) w[u] = sf_weight(x[u], m, q.r);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) add(x[u], w[u]);
+        }
+      } else {
+        walk([&](int j, const uint4& raw) {
+          float f[EPC];
+          uint32_t w[EPC];
+          g.values(raw, j, f);
+#pragma unroll
+          for (int i = 0; i < EPC; ++i) w[i] = sf_weight(f[i], m, q.r);
+#pragma unroll
+          for (int i = 0; i < EPC; ++i) add(f[i], w[i]);
+        });
+      }
+      __syncwarp();
+      if (floored) {
+        floor_bin = __reduce_max_sync(0xffffffffu, floor_bin);
+        below = __any_sync(0xffffffffu, below);
+      }
+      if (lane == 0) {
+        sh.ired[1][wid] = floor_bin;
+        sh.ired[2][wid] = below;
+      }
+    };
+    bin_queued();
     // A NaN, or +inf under a finite maximum, makes the sum NaN.
     s = warp_sum(s);
     odd |= finite && !(s < kInf);
     odd = __any_sync(0xffffffffu, odd);
-    if (whole) total = warp_sum_u64(total);
-    if (floored) above_floor = warp_sum_u64(above_floor);
+    if (tempered) st = warp_sum(st);
     if (greedy) {
       first = warp_min_i(first);
       if (lane == 0 && first != INT_MAX) atomicMin(&lead->first_id, first);
     }
     if (lane == 0) {
-      sh.red[wid] = total;
-      sh.red2[wid] = above_floor;
       sh.sred[0][wid] = s;
-      sh.sred[1][wid] = __int_as_float(odd);
+      sh.sred[1][wid] = st;
+      sh.ired[0][wid] = odd;
     }
     cta_sync();
+    // this CTA's share of what rank 0 needs to know, pushed there
+    auto push_bins_info = [&] {
+      floor_bin = __reduce_max_sync(0xffffffffu, lane < NW ? sh.ired[1][lane] : -1);
+      below = __any_sync(0xffffffffu, lane < NW && sh.ired[2][lane]);
+      if (lane == 0) {
+        lead->part_floor[rank] = floor_bin;
+        lead->part_below[rank] = below;
+      }
+    };
     if (wid == 0) {
       const bool in = lane < NW;
-      total = warp_sum_u64(in ? sh.red[lane] : 0);
-      above_floor = warp_sum_u64(in ? sh.red2[lane] : 0);
       s = warp_sum(in ? sh.sred[0][lane] : 0.f);
-      odd = __any_sync(0xffffffffu, in && __float_as_int(sh.sred[1][lane]));
+      st = warp_sum(in ? sh.sred[1][lane] : 0.f);
+      odd = __any_sync(0xffffffffu, in && sh.ired[0][lane]);
       if (lane == 0) {
-        lead->part_total[rank] = total;
-        lead->part_floor[rank] = above_floor;
         lead->part_sum[rank] = s;
+        lead->part_tempered[rank] = st;
         lead->part_odd[rank] = odd;
       }
+      push_bins_info();
     }
     sync();
 
@@ -661,15 +789,16 @@ __global__ void __launch_bounds__(NT, 1024 / NT)
       continue;  // the partials are read before this CTA meets the others again
     }
 
-    // Sums the cluster's bins [b0, b0 + NB / 2) into rank 0's pm and pc: a share
-    // of the bins per CTA, a thread per bin and peer, so that the reads of other
-    // CTAs' memory are one round trip.
-    auto merge_bins = [&](int b0) {
-      for (int i = tid; i < NBT; i += NT) {
-        const int b = b0 + rank * (NBT / cs) + i / cs;
+    // Sums the cluster's bins into rank 0's pm and pc: a share of the bins per CTA,
+    // a thread per bin and peer, so that the reads of other CTAs' memory are one
+    // round trip. A CTA's bin of more than 2^16 logits may have overflowed.
+    auto merge_bins = [&] {
+      for (int i = tid; i < NB; i += NT) {
+        const int b = rank * (NB / cs) + i / cs;
         const Shared* peer = cl.map_shared_rank(&sh, i % cs);
         uint32_t c = peer->cnt[b];
         u64 mass = (u64)peer->lo[b] + ((u64)peer->hi[b] << 16);
+        if (c > 65536u) lead->crowded = 1;
         for (int o = 1; o < cs; o <<= 1) {
           c += __shfl_xor_sync(0xffffffffu, c, o);
           mass += __shfl_xor_sync(0xffffffffu, mass, o);
@@ -680,10 +809,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT)
         }
       }
     };
-    // Rank 0: running sums of those bins, continuing from (m0, c0). Alone in its
-    // cluster, it takes them as they are.
-    auto scan_bins = [&](int b0, u64 m0, uint32_t c0) {
-      constexpr int PER = (NBT + NT - 1) / NT;
+    // Rank 0: running sums of the bins. Alone in its cluster, it takes them as they are.
+    auto scan_bins = [&] {
+      constexpr int PER = (NB + NT - 1) / NT;
       u64 mass[PER], sm = 0;
       uint32_t c[PER], sc = 0;
 #pragma unroll
@@ -691,9 +819,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT)
         const int b = tid * PER + i;
         mass[i] = 0;
         c[i] = 0;
-        if (b < NBT) {
-          mass[i] = cs == 1 ? (u64)sh.lo[b0 + b] + ((u64)sh.hi[b0 + b] << 16) : sh.pm[b0 + b];
-          c[i] = cs == 1 ? sh.cnt[b0 + b] : sh.pc[b0 + b];
+        if (b < NB) {
+          mass[i] = cs == 1 ? (u64)sh.lo[b] + ((u64)sh.hi[b] << 16) : sh.pm[b];
+          c[i] = cs == 1 ? sh.cnt[b] : sh.pc[b];
+          if (cs == 1 && c[i] > 65536u) sh.crowded = 1;
         }
         sm += mass[i];
         sc += c[i];
@@ -709,76 +838,99 @@ __global__ void __launch_bounds__(NT, 1024 / NT)
           ic += uc;
         }
       }
-      u64 bm = m0 + im - sm;
-      uint32_t bc = c0 + ic - sc;
+      u64 bm = im - sm;
+      uint32_t bc = ic - sc;
       if (NW > 1) {
         if (lane == 31) {
           sh.red[wid] = im;
           sh.fred[0][wid] = __uint_as_float(ic);
         }
         cta_sync();
-#pragma unroll
-        for (int w = 0; w < NW; ++w)
-          if (w < wid) {
-            bm += sh.red[w];
-            bc += __float_as_uint(sh.fred[0][w]);
-          }
+        const u64 wm = lane < wid ? sh.red[lane] : 0;
+        const uint32_t wc = lane < wid ? __float_as_uint(sh.fred[0][lane]) : 0u;
+        bm += warp_sum_u64(wm);
+        bc += __reduce_add_sync(0xffffffffu, wc);
       }
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int b = tid * PER + i;
         bm += mass[i];
         bc += c[i];
-        if (b < NBT) {
-          sh.pm[b0 + b] = bm;
-          sh.pc[b0 + b] = bc;
+        if (b < NB) {
+          sh.pm[b] = bm;
+          sh.pc[b] = bc;
         }
       }
       cta_sync();
     };
     // Rank 0, warp 0: which bins the boundaries can lie in (see the kernel's comment).
-    auto decide = [&](bool tail) {
-      const int nb = tail ? NB : NBT;
-      const u64 known = sh.pm[nb - 1], all = sh.known_total, fl = sh.known_floor;
+    // `weighed`: t_lo = t_hi is the row's mass.
+    auto decide = [&](bool weighed) {
+      const int nb = NB;
+      const u64 known = sh.pm[nb - 1];
       const uint32_t count = sh.pc[nb - 1];
-      const bool complete = tail || !whole || known == all;
+      const bool complete = !whole || x1 <= x_low;  // nothing that is asked for lies below x1
+      if (sh.crowded) return (int)kExact;
       uint32_t mark = 0;  // lane l: bins [32 l, 32 l + 32)
       auto mark_range = [&](int b0, int b1) {
         const int from = max(b0 - 32 * lane, 0), to = min(b1 - 32 * lane, 31);
         if (lane < NB / 32 && from <= to) mark |= (0xffffffffu << from) & (0xffffffffu >> (31 - to));
       };
-      u64 t_lo, t_hi;  // bounds of the kept mass
+      // a width that the logits of the bin are too light for
+      auto light = [&](int b, u64 width) {
+        const u64 mass = sh.pm[b] - (b ? sh.pm[b - 1] : 0);
+        const uint32_t c = sh.pc[b] - (b ? sh.pc[b - 1] : 0u);
+        return width > 0 && width * 4 * c > mass;
+      };
+      if (complete) {
+        if (lane == 0) sh.t_lo = sh.t_hi = known;
+        weighed = true;
+        __syncwarp();
+      }
+      u64 t_lo = sh.t_lo, t_hi = sh.t_hi;  // bounds of the kept mass
+      bool loose = !weighed;               // they differ by what is not known of the row's mass
       int kb = -1;
       if (q.k && (uint32_t)q.k <= count) {
         kb = warp_lower_bound<uint32_t>(sh.pc, nb, (uint32_t)q.k, lane);
-        t_hi = sh.pm[kb];
-        t_lo = t_hi;
+        t_lo = t_hi = sh.pm[kb];
+        loose = false;
         if (sh.pc[kb] != (uint32_t)q.k) {
           t_lo = kb ? sh.pm[kb - 1] : 0;
           mark_range(kb, kb);
         }
       } else if (q.k && !complete) {
-        return (int)kTail;
-      } else {
-        t_lo = t_hi = whole ? all : known;
+        return (int)kLower;
       }
       if (q.p < 1.f) {
         const u64 n_hi = need_of(q.p, t_hi), n_lo = t_lo == t_hi ? n_hi : need_of(q.p, t_lo);
-        if (n_hi > known) return complete ? (int)kExact : (int)kTail;
+        if (n_hi > known) return complete ? (int)kExact : (int)kLower;
         const int b0 = warp_lower_bound<u64>(sh.pm, nb, n_lo > 0 ? n_lo : 1, lane);
         const int b1 = n_lo == n_hi ? b0 : warp_lower_bound<u64>(sh.pm, nb, n_hi, lane);
+        if (loose && light(b1, n_hi - n_lo)) return (int)kWeigh;
+        loose = false;
         mark_range(b0, b1);
         t_lo = b0 ? sh.pm[b0 - 1] : 0;
         t_hi = sh.pm[b1];
       }
       if (floored) {
-        t_lo = fl < t_lo ? fl : t_lo;
-        t_hi = fl < t_hi ? fl : t_hi;
+        // the mass of what min-p keeps ends in floor_bin, or beyond what is known
+        const int fb = sh.known_floor;
+        const bool ends = complete || sh.known_below;
+        const u64 f_lo = !ends ? known : fb > 0 ? sh.pm[fb - 1] : 0, f_hi = ends ? sh.pm[max(fb, 0)] : t_hi;
+        if (f_lo < t_hi) {
+          if (!ends) return (int)kLower;
+          mark_range(fb, fb);
+          if (f_hi <= t_lo) loose = false;
+          t_lo = f_lo < t_lo ? f_lo : t_lo;
+          t_hi = f_hi < t_hi ? f_hi : t_hi;
+        }
       }
       const u64 d_hi = target_of(q.u, t_hi), d_lo = t_lo == t_hi ? d_hi : target_of(q.u, t_lo);
-      if (d_hi >= known) return complete ? (int)kExact : (int)kTail;
+      if (d_hi >= known) return complete ? (int)kExact : (int)kLower;
       const int b0 = warp_lower_bound<u64>(sh.pm, nb, d_lo + 1, lane);
-      mark_range(b0, d_lo == d_hi ? b0 : warp_lower_bound<u64>(sh.pm, nb, d_hi + 1, lane));
+      const int b1 = d_lo == d_hi ? b0 : warp_lower_bound<u64>(sh.pm, nb, d_hi + 1, lane);
+      if (loose && light(b1, d_hi - d_lo)) return (int)kWeigh;
+      mark_range(b0, b1);
       int listed = 0;
       for (uint32_t w = mark; w; w &= w - 1) {
         const int b = 32 * lane + __ffs(w) - 1;
@@ -786,86 +938,115 @@ __global__ void __launch_bounds__(NT, 1024 / NT)
       }
       if (warp_sum_i(listed) > CAP) return (int)kExact;
       if (lane < NB / 32) sh.marks[lane] = mark;
-      const bool low = __any_sync(0xffffffffu, lane >= NBT / 32 && mark);
-      if (lane == 0) {
-        sh.kb = kb;
-        sh.gate = low;
-      }
+      if (lane == 0) sh.kb = kb;
       return (int)kGather;
     };
 
-    if (cs > 1) merge_bins(0);
+    if (cs > 1) merge_bins();
     if (rank == 0 && wid == 0) {
-      if (cs > 1) {
-        const bool in = lane < cs;
-        total = warp_sum_u64(in ? sh.part_total[lane] : 0);
-        above_floor = warp_sum_u64(in ? sh.part_floor[lane] : 0);
-        s = warp_sum(in ? sh.part_sum[lane] : 0.f);
-        odd = __any_sync(0xffffffffu, in && sh.part_odd[lane]);
-      }
+      const bool in = lane < cs;
+      s = warp_sum(in ? sh.part_sum[lane] : 0.f);
+      st = warp_sum(in ? sh.part_tempered[lane] : 0.f);
+      odd = __any_sync(0xffffffffu, in && sh.part_odd[lane]);
       if (lane == 0) {
-        sh.known_total = total;
-        sh.known_floor = above_floor;
+        const double t = (double)(tempered ? st : s) * (double)kSfOne;
+        const double slack = t * (kSfSlack + kSfRounding * (21 + (q_hi - q_lo + NT - 1) / NT)) + 0.5 * (double)a.V;
+        sh.t_lo = t > slack ? (u64)(t - slack) : 0;
+        sh.t_hi = (u64)(t + slack) + 1;
         sh.known_sum = s;
         sh.known_odd = odd;
       }
     }
     sync();
     int command;
-    for (bool tail = false;; tail = true) {
+    bool weighed = false, fresh = true;
+    for (int lowered = 0;;) {
       if (rank == 0) {
-        if (tail)
-          scan_bins(NBT, sh.pm[NBT - 1], sh.pc[NBT - 1]);
-        else
-          scan_bins(0, 0, 0);
+        if (fresh) scan_bins();
         if (wid == 0) {
-          const int c = sh.known_odd ? (int)kDone : decide(tail);
+          const int fb = __reduce_max_sync(0xffffffffu, lane < cs ? sh.part_floor[lane] : -1);
+          const bool be = __any_sync(0xffffffffu, lane < cs && sh.part_below[lane]);
+          if (lane == 0) {
+            sh.known_floor = fb;
+            sh.known_below = be;
+          }
+          __syncwarp();
+          const int c = sh.known_odd ? (int)kDone : decide(weighed);
           __syncwarp();
           for (int o = 1; o < cs; ++o) {
             Shared* peer = cl.map_shared_rank(&sh, o);
             if (lane < NB / 32) peer->marks[lane] = sh.marks[lane];
-            if (lane == 0) {
-              peer->gate = sh.gate;
-              peer->command = c;
-            }
+            if (lane == 0) peer->command = c;
           }
           if (lane == 0) sh.command = c;
         }
       }
       sync();
       command = sh.command;
-      if (command != kTail) break;
-      const int logits = (g.q_hi - g.q_lo) * EPC;
-      for (int e0 = tid; e0 < logits; e0 += 4 * NT) {
-        float x[4];
-        uint32_t w[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int e = e0 + u * NT;
-          x[u] = e < logits ? value(g.q_lo + e / EPC, e % EPC) : -kInf;
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) w[u] = sf_weight(x[u], m, q.r);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (x[u] >= x_low && x[u] < x1) add_bins(x[u], w[u]);
-      }
-      sync();
-      if (cs > 1) {
-        merge_bins(NBT);
+      if (command == kLower) {
+        // A lower cut: a quarter further from the maximum each time, which in the
+        // tail of normal logits holds some four times as many, and at last all.
+        x1 = lowered < 4 ? fmaxf(x_low, x1 - 0.27f * (m - x1)) : x_low;
+        ++lowered;
+        per_x = fminf((float)NB / (m - x1), 3.402823466e38f);
+        for (int i = tid; i < NB; i += NT) sh.cnt[i] = sh.lo[i] = sh.hi[i] = 0;
+        cta_sync();
+        queued = 0;
+        walk([&](int j, const uint4& raw) {
+          float f[EPC];
+          g.values(raw, j, f);
+          enqueue(j, max_of(f) >= x1);
+        });
+        bin_queued();
+        cta_sync();
+        if (wid == 0) push_bins_info();
         sync();
+        if (cs > 1) {
+          merge_bins();
+          sync();
+        }
+        fresh = true;
+      } else if (command == kWeigh) {
+        // the mass of the rest of the row, exactly
+        u64 total = 0;
+        walk([&](int j, const uint4& raw) {
+          float f[EPC];
+          g.values(raw, j, f);
+#pragma unroll
+          for (int i = 0; i < EPC; ++i) {
+            const uint32_t w = sf_weight(f[i], m, q.r);
+            total += f[i] < x1 ? w : 0u;
+          }
+        });
+        total = warp_sum_u64(total);
+        if (lane == 0) sh.red[wid] = total;
+        cta_sync();
+        if (wid == 0) {
+          total = warp_sum_u64(lane < NW ? sh.red[lane] : 0);
+          if (lane == 0) lead->part_total[rank] = total;
+        }
+        sync();
+        if (rank == 0 && wid == 0) {
+          total = warp_sum_u64(lane < cs ? sh.part_total[lane] : 0);
+          if (lane == 0) sh.t_lo = sh.t_hi = sh.pm[NB - 1] + total;
+          __syncwarp();
+        }
+        weighed = true;
+        fresh = false;
+      } else {
+        break;
       }
     }
     if (command == kGather) {
       auto take = [&](float x, int j, int i) {
         const int b = bin_of(x);
         if (((sh.marks[b >> 5] >> (b & 31)) & 1u) && sf_weight(x, m, q.r)) {
-          const int at = atomicAdd(&lead->n_list, 1);
+          const int at = atomicAdd(&sh.n_mine, 1);
           if (at < CAP)
-            lead->list[at] = ((u64)Logit<T>::key(x) << 32) | (u64)(0xffffffffu - (uint32_t)(EPC * j - g.dc + i));
+            sh.incl[at] = ((u64)Logit<T>::key(x) << 32) | (u64)(0xffffffffu - (uint32_t)g.id(j, i));
         }
       };
-      if (!sh.gate) {
+      if (queued <= QCAP) {
         for (int i0 = 0; i0 < queued; i0 += 128 / EPC) {
           float x[4];
           int j[4];
@@ -875,20 +1056,25 @@ __global__ void __launch_bounds__(NT, 1024 / NT)
             if (x[u] >= x1) take(x[u], j[u], lane % EPC);
         }
       } else {
-        const int logits = (g.q_hi - g.q_lo) * EPC;
-        for (int e0 = tid; e0 < logits; e0 += 4 * NT) {
-          float x[4];
+        walk([&](int j, const uint4& raw) {
+          float f[EPC];
+          g.values(raw, j, f);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int e = e0 + u * NT;
-            x[u] = e < logits ? value(g.q_lo + e / EPC, e % EPC) : -kInf;
-          }
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int e = e0 + u * NT;
-            if (x[u] >= x_low) take(x[u], g.q_lo + e / EPC, e % EPC);
-          }
-        }
+          for (int i = 0; i < EPC; ++i)
+            if (f[i] >= x1) take(f[i], j, i);
+        });
+      }
+      // to rank 0's list, in one piece
+      cta_sync();
+      const int mine = min(sh.n_mine, CAP);
+      if (cs == 1) {
+        if (tid == 0) sh.n_list = mine;
+        for (int i = tid; i < mine; i += NT) sh.list[i] = sh.incl[i];
+      } else if (mine) {
+        if (tid == 0) sh.mine_at = atomicAdd(&lead->n_list, mine);
+        cta_sync();
+        for (int i = tid; i < mine; i += NT)
+          if (sh.mine_at + i < CAP) lead->list[sh.mine_at + i] = sh.incl[i];
       }
       sync();
     }
@@ -905,7 +1091,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT)
       }
     } else if (command == kExact) {
       const T* row = static_cast<const T*>(a.x) + n * a.ld;
-      const int token = row_exact<T, NT>(row, a.V, q, m, sh.red, &sh.slot);
+      const Bins<NB> bins = {sh.cnt, sh.lo, sh.hi, sh.pc, sh.red, sh.found};
+      const int token = row_exact<T, NT, NB>(row, a.V, q, m, bins, &sh.slot);
       if (tid == 0) {
         a.out_tokens[n] = token;
         a.out_logprobs[n] = Logit<T>::get(row, token) - lse;
@@ -940,9 +1127,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT)
         for (int i = tid; i < len; i += NT) sh.list[i] = sh.incl[i];
         cta_sync();
       }
+      u64 kept = 0;  // mass through the last of the top-k
       if (wid == 0) {
         // running mass through each listed logit: through its bin's predecessor, plus the listed ones of its bin
-        u64 sum = 0, off = 0, kept = 0;
+        u64 sum = 0, off = 0;
         int off_at = 0, off_count = 0, last_bin = -1;
         for (int j = 0; j < len; j += 32) {
           const bool in = j + lane < len;
@@ -977,27 +1165,58 @@ __global__ void __launch_bounds__(NT, 1024 / NT)
           off_at = __shfl_sync(0xffffffffu, at_use, 31);
           last_bin = __shfl_sync(0xffffffffu, b, 31);
         }
-        __syncwarp();
-        auto first_at_least = [&](u64 t) {
-          for (int j = 0; j < len; j += 32) {
-            const unsigned hit = __ballot_sync(0xffffffffu, j + lane < len && sh.incl[j + lane] >= t);
-            if (hit) return j + __ffs(hit) - 1;
+      }
+      for (;;) {
+        if (wid == 0) {
+          auto first_at_least = [&](u64 t) {
+            for (int j = 0; j < len; j += 32) {
+              const unsigned hit = __ballot_sync(0xffffffffu, j + lane < len && sh.incl[j + lane] >= t);
+              if (hit) return j + __ffs(hit) - 1;
+            }
+            return max(len - 1, 0);  // not reached: the boundary's bin is listed
+          };
+          u64 lo_t = sh.t_lo, hi_t = sh.t_hi;
+          if (sh.kb >= 0) lo_t = hi_t = sh.pc[sh.kb] == (uint32_t)q.k ? sh.pm[sh.kb] : kept;
+          if (q.p < 1.f) {
+            const int hi_at = first_at_least(need_of(q.p, hi_t));
+            const int lo_at = lo_t == hi_t ? hi_at : first_at_least(need_of(q.p, lo_t));
+            hi_t = sh.incl[hi_at];
+            lo_t = sh.incl[lo_at];
           }
-          return max(len - 1, 0);  // not reached: the boundary's bin is listed
-        };
-        u64 all;
-        if (sh.kb >= 0)
-          all = sh.pc[sh.kb] == (uint32_t)q.k ? sh.pm[sh.kb] : kept;
-        else
-          all = whole ? sh.known_total : sh.pm[NBT - 1];
-        if (q.p < 1.f) all = sh.incl[first_at_least(need_of(q.p, all))];
-        if (floored) all = sh.known_floor < all ? sh.known_floor : all;
-        const int at = first_at_least(target_of(q.u, all) + 1);
-        if (lane == 0) {
-          const u64 e = sh.list[at];
-          a.out_tokens[n] = (int)(0xffffffffu - (uint32_t)e);
-          a.out_logprobs[n] = Logit<T>::value((uint32_t)(e >> 32)) - lse;
+          if (floored) {
+            // through the last listed logit that min-p keeps
+            u64 f = ~0ull;
+            const int fb = sh.known_floor;
+            if ((sh.marks[max(fb, 0) >> 5] >> (max(fb, 0) & 31)) & 1u) {
+              for (int j = 0; j < len; j += 32) {
+                bool stays = false;
+                if (j + lane < len) {
+                  const float x = Logit<T>::value((uint32_t)(sh.list[j + lane] >> 32));
+                  stays = bin_of(x) == fb && sf_weight(x, m, q.r) >= q.floor_w;
+                }
+                const unsigned st_ = __ballot_sync(0xffffffffu, stays);
+                if (st_) f = sh.incl[j + 31 - __clz(st_)];
+              }
+            }
+            lo_t = f < lo_t ? f : lo_t;
+            hi_t = f < hi_t ? f : hi_t;
+          }
+          const int at = first_at_least(target_of(q.u, hi_t) + 1);
+          const int lo_at = lo_t == hi_t ? at : first_at_least(target_of(q.u, lo_t) + 1);
+          if (lane == 0) {
+            sh.again = at != lo_at;
+            const u64 e = sh.list[at];
+            a.out_tokens[n] = (int)(0xffffffffu - (uint32_t)e);
+            a.out_logprobs[n] = Logit<T>::value((uint32_t)(e >> 32)) - lse;
+          }
         }
+        cta_sync();
+        if (!sh.again) break;
+        // the bounds fall on two logits: weigh the whole row here
+        const u64 sum = row_mass<T, NT>(g, 0u, m, q.r, sh.red);
+        cta_sync();
+        if (tid == 0) sh.t_lo = sh.t_hi = sum;
+        cta_sync();
       }
     }
     cta_sync();  // the lists are free
@@ -1008,40 +1227,33 @@ __global__ void __launch_bounds__(NT, 1024 / NT)
 namespace {
 
 constexpr int kSfSmallV = 2048;   // rows up to here, when there are enough to fill the GPU: a warp each
-constexpr int kSfMediumV = 8192;  // rows up to here: 128-thread CTAs
-constexpr long long kSfSlice = 64 << 10;    // bytes of a row per CTA, two CTAs per SM
-constexpr long long kSfSliceMax = 128 << 10;  // one CTA per SM; at most 65536 logits, which the bins' 32-bit sums allow
+constexpr int kSfMediumV = 8192;  // rows up to here: 128-thread CTAs, held in shared memory
 constexpr long long kSfSliceMin = 8 << 10;
 
-// Launches the cluster kernel; *refused when no cluster of that shape fits.
-template <typename T, int NT, int NB, int CAP, int GROUPS>
-cudaError_t launch_on_chip(const FilteredArgs& a, int cs, int chunks, cudaStream_t st, bool* refused) {
-  const size_t smem = (size_t)chunks * 16 + (size_t)((chunks + NT - 1) / NT * NT) * 2;  // a slice and its queues
-  auto kern = k_sample_filtered<T, NT, NB, CAP, GROUPS>;
+// Launches the fast kernel with cs CTAs per row; *refused when no cluster of that shape fits.
+template <typename T, int NT, int NB, int CAP, int GROUPS, int QCAP, bool RESIDENT>
+cudaError_t launch_fast(const FilteredArgs& a, int cs, cudaStream_t st, bool* refused) {
+  auto kern = k_sample_filtered<T, NT, NB, CAP, GROUPS, QCAP, RESIDENT>;
+  // a resident slice: the most chunks that a row's 16-byte blocks can make, shared out
+  const long long chunks = ((long long)a.V * sizeof(T) + 46 - 2 * sizeof(T)) / 16;
+  const size_t smem = RESIDENT ? (size_t)((chunks + cs - 1) / cs) * 16 : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.gridDim = dim3((unsigned)cs);
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)cs;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  // A CTA alone is launched without a cluster: as clusters of one, only eight of them run on an SM.
-  if (cs == 1) attr[0] = attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cs;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
+  // A CTA alone is launched without a cluster: as clusters of one, only eight of them run on an SM.
   cfg.numAttrs = cs == 1 ? 1 : 2;
   const void* site = reinterpret_cast<const void*>(kern);
-  const int ok = cached(site, -1, [&](int) {
-    cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kSfSliceMax + kSfSliceMax / 8 + 2048));
-    if (r == cudaSuccess) r = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (r != cudaSuccess) (void)cudaGetLastError();
-    return r == cudaSuccess ? 1 : 0;
-  });
-  const int fit = ok <= 0 ? 0 : cached(site, (long long)smem * 32 + cs, [&](int) {
+  const int fit = cached(site, (long long)smem * 32 + cs, [&](int) {
     int v = 0;
     const cudaError_t r = cs == 1 ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kern, NT, smem)
                                   : cudaOccupancyMaxActiveClusters(&v, kern, &cfg);
@@ -1057,7 +1269,7 @@ cudaError_t launch_on_chip(const FilteredArgs& a, int cs, int chunks, cudaStream
   }
   const long long clusters = a.n < fit ? a.n : fit;
   cfg.gridDim = dim3((unsigned)(clusters * cs));
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, chunks);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
   if (e == cudaSuccess) note_launch();
   return e;
 }
@@ -1068,36 +1280,24 @@ template <typename T>
 static cudaError_t launch_filtered(const FilteredArgs& a, cudaStream_t st) {
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorUnknown;
-  const long long bytes = (long long)a.V * sizeof(T) + 16;
   bool refused = false;
+  cudaError_t e;
   if (a.V <= kSfSmallV && a.n >= sms * 8LL) {
-    const cudaError_t e = launch_on_chip<T, 32, 128, 128, 32>(a, 1, (int)((bytes + 15) / 16), st, &refused);
-    if (!refused) return e;
+    e = launch_fast<T, 32, 128, 128, 32, 192, true>(a, 1, st, &refused);
   } else if (a.V <= kSfMediumV) {
-    const cudaError_t e = launch_on_chip<T, 128, 256, 256, 32>(a, 1, (int)((bytes + 15) / 16), st, &refused);
-    if (!refused) return e;
+    e = launch_fast<T, 128, 256, 256, 32, 128, true>(a, 1, st, &refused);
   } else {
+    // a CTA per row, or as many as the SMs that the rows leave, down to 8 KB of a row each
     int cs = 1;
-    while (cs < 16 && bytes > cs * kSfSlice) cs *= 2;
-    // few rows: more CTAs per row, down to 8 KB each
-    while (cs < 8 && (long long)a.n * cs * 2 <= sms && bytes > cs * 2 * kSfSliceMin) cs *= 2;
-    const long long slice = (bytes / 16 + cs) / cs * 16 + 16;
-    if (slice <= kSfSliceMax) {
-      const cudaError_t e = launch_on_chip<T, 512, 1024, 1024, 128>(a, cs, (int)(slice / 16), st, &refused);
-      if (!refused) return e;
-    }
+    while (cs < 8 && a.n * cs * 2LL <= sms && (long long)a.V * sizeof(T) >= cs * 2 * kSfSliceMin) cs *= 2;
+    e = launch_fast<T, 512, 1024, 512, 128, 8192 / (512 / 32), false>(a, cs, st, &refused);
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.n < sms * 4LL ? a.n : sms * 4LL));
-  cfg.blockDim = dim3(kSfNT);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_sample_filtered_rows<T>, a);
-  if (e == cudaSuccess) note_launch();
+  // No cluster of that size fits (another program's share of the GPU): a CTA per row always does.
+  if (refused) {
+    refused = false;
+    e = launch_fast<T, 512, 1024, 512, 128, 8192 / (512 / 32), false>(a, 1, st, &refused);
+    if (refused) return cudaErrorLaunchOutOfResources;
+  }
   return e;
 }
 
