@@ -106,11 +106,14 @@ struct Row {
     }
   }
   // Calls body(j, chunk) for the chunks of [from, to) that this lane has, U loads
-  // at a time; all lanes of the warp together, with -inf past the end.
-  template <int NT, int U, typename Load, typename Body>
+  // at a time; all lanes of the warp together, with -inf past the end. BACK: from
+  // the end.
+  template <int NT, int U, bool BACK, typename Load, typename Body>
   __device__ __forceinline__ void walk(int from, int to, Load load, Body body) const {
+    const int rounds = (to - from + U * NT - 1) / (U * NT);
 #pragma unroll 1
-    for (int j0 = from + (int)(threadIdx.x & ~31u); j0 < to; j0 += U * NT) {
+    for (int it = 0; it < rounds; ++it) {
+      const int j0 = from + (BACK ? rounds - 1 - it : it) * (U * NT) + (int)(threadIdx.x & ~31u);
       uint4 raw[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -141,7 +144,7 @@ __device__ __forceinline__ u64 block_sum(u64 v, u64* red) {
 template <typename T, int NT>
 __device__ u64 row_mass(const Row<T>& row, uint32_t floor_w, float m, float r, u64* red) {
   u64 s = 0;
-  row.template walk<NT, 2>(
+  row.template walk<NT, 2, false>(
       0, row.nq, [&](int j) { return __ldg(row.base + j); },
       [&](int j, const uint4& raw) {
         float f[Chunk<T>::N];
@@ -186,7 +189,7 @@ __device__ __noinline__ Cut row_select(const Row<T> row, bool by_count, u64 t, f
     __syncthreads();
     for (int i = tid; i < NB; i += NT) b.cnt[i] = b.w0[i] = b.w1[i] = b.w2[i] = 0;
     __syncthreads();
-    row.template walk<NT, 2>(
+    row.template walk<NT, 2, false>(
         0, row.nq, [&](int j) { return __ldg(row.base + j); },
         [&](int j, const uint4& raw) {
           float f[Chunk<T>::N];
@@ -394,14 +397,14 @@ __device__ __noinline__ int row_exact(const T* p, int V, const RowParams& q, flo
 // row; an exact weight and an atomic only above x1.
 namespace {
 
-template <int NT, int NB, int CAP, int QCAP>
+template <int NT, int NB, int CAP, int QCAP>  // QCAP 0: no queue
 struct SfShared {
   uint32_t cnt[NB], lo[NB], hi[NB];  // this CTA's bins: count, and mass as two sums of 16-bit halves
   u64 pm[NB];                        // rank 0: mass through each bin
   uint32_t pc[NB];                   // rank 0: count through each bin
   u64 list[CAP];                     // rank 0: gathered (key, ~id)
   u64 incl[CAP];                     // this CTA's gathered ones; rank 0: running mass through each listed one
-  uint16_t queue[NT / 32][QCAP];     // each warp's chunks that hold a logit >= x1, by their place in its walk
+  uint16_t queue[NT / 32][QCAP > 0 ? QCAP : 1];  // each warp's chunks that hold a logit >= x1, by their place in its walk
   u64 full;                          // the slice's copy is done
   u64 red[NT / 32];
   float fred[3][NT / 32], sred[2][NT / 32];
@@ -468,8 +471,8 @@ __device__ __forceinline__ bool sf_wait(u64* bar, uint32_t parity) {
 
 }  // namespace
 
-template <typename T, int NT, int NB, int CAP, int GROUPS, int QCAP, bool RESIDENT>
-__global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT) k_sample_filtered(FilteredArgs a) {
+template <typename T, int NT, int NB, int CAP, int GROUPS, int QCAP, int ECAP, bool RESIDENT>
+__global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT) k_sample_filtered(FilteredArgs a, int slice_chunks) {
   constexpr int EPC = Chunk<T>::N, NW = NT / 32, U = RESIDENT ? 1 : 4;
   using Shared = SfShared<NT, NB, CAP, QCAP>;
   extern __shared__ uint4 slice[];
@@ -480,6 +483,9 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
   const long long n_clusters = (long long)gridDim.x / cs, cid = (long long)blockIdx.x / cs;
   Shared* lead = cl.map_shared_rank(&sh, 0);
   uint16_t* queue = sh.queue[wid];
+  // behind the slice: the logits >= x1 of each warp's walk, and their places in the row's chunks
+  float* high_x = reinterpret_cast<float*>(slice + slice_chunks) + wid * 2 * ECAP;
+  int* high_at = reinterpret_cast<int*>(high_x + ECAP);
   auto cta_sync = [&] {
     if (NT == 32)
       __syncwarp();
@@ -527,10 +533,10 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
     const Row<T> g = row_of(n);
     const int q_lo = from_of(g, rank), q_hi = from_of(g, rank + 1);
     const RowParams q = row_params(a, n);
-    auto walk = [&](auto body) {
-      g.template walk<NT, U>(
-          q_lo, q_hi, [&](int j) { return RESIDENT ? slice[j - q_lo] : __ldg(g.base + j); }, body);
-    };
+    auto load = [&](int j) { return RESIDENT ? slice[j - q_lo] : __ldg(g.base + j); };
+    auto walk = [&](auto body) { g.template walk<NT, U, false>(q_lo, q_hi, load, body); };
+    // The second walk goes back: of a batch of rows larger than L2, what was read last is still there.
+    auto walk_back = [&](auto body) { g.template walk<NT, U, !RESIDENT>(q_lo, q_hi, load, body); };
     for (int i = tid; i < NB; i += NT) sh.cnt[i] = sh.lo[i] = sh.hi[i] = 0;
     if (tid == 0) {
       sh.n_list = sh.n_mine = 0;
@@ -601,13 +607,6 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
     const bool whole = drawn && !(q.k && q.k <= GROUPS);
     const bool tempered = whole && x1 > x_low && q.r != 1.f;
     const bool floored = q.mp > 0.f;
-    // one logit of chunk j
-    auto value = [&](int j, int i) {
-      const float x = RESIDENT ? Logit<T>::load(reinterpret_cast<const T*>(slice) + (EPC * (j - q_lo) + i))
-                               : Logit<T>::get(reinterpret_cast<const T*>(g.base), (long long)EPC * j + i);
-      const int e = g.id(j, i);
-      return e >= 0 && e < a.V ? x : -kInf;
-    };
     auto add_bins = [&](float x, uint32_t w) {
       if (w) {
         const int b = bin_of(x);
@@ -622,14 +621,54 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
     int first = INT_MAX, odd = 0;
     const float2 neg_m = make_float2(-m, -m), l2e = make_float2(kLog2e, kLog2e), rr = make_float2(q.r, q.r);
     int queued = 0;
-    // chunks with a logit above the cut go to the warp's queue
-    auto enqueue = [&](int j, bool high) {
+    int have = 0;  // logits >= x1 of this warp's walk; more than fit: the walk itself is repeated for them
+    auto keep = [&](bool high, float x, int at) {
       const unsigned who = __ballot_sync(0xffffffffu, high);
-      const int at = queued + __popc(who & ((1u << lane) - 1u));
-      if (high && at < QCAP) queue[at] = (uint16_t)((j - q_lo) / NT * 32 + lane);
-      queued += __popc(who);
+      const int slot = have + __popc(who & ((1u << lane) - 1u));
+      if (high && slot < ECAP) {
+        high_x[slot] = x;
+        high_at[slot] = at;
+      }
+      have += __popc(who);
     };
-    walk([&](int j, const uint4& raw) {
+    // Of a short row every logit is looked at in the walk; of a long one, chunks
+    // with a high logit are queued, so that the walk pays a ballot a chunk.
+    auto collect = [&](int j, const float (&f)[EPC], bool high) {
+      const unsigned who = __ballot_sync(0xffffffffu, high);
+      if (RESIDENT) {
+        if (who) {
+#pragma unroll
+          for (int i = 0; i < EPC; ++i) keep(high && f[i] >= x1, f[i], EPC * j + i);
+        }
+      } else {
+        const int at = queued + __popc(who & ((1u << lane) - 1u));
+        if (high && at < QCAP) queue[at] = (uint16_t)((j - q_lo) / NT * 32 + lane);
+        queued += __popc(who);
+      }
+    };
+    auto collect_queued = [&] {
+      __syncwarp();
+      if (RESIDENT) return;
+      have = queued <= QCAP ? 0 : ECAP + 1;
+      if (have) return;
+      for (int i0 = 0; i0 < queued; i0 += 128 / EPC) {
+        float x[4];
+        int at[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int k = queue[min(i0 + lane / EPC + u * (32 / EPC), queued - 1)];
+          at[u] = EPC * (q_lo + wid * 32 + k / 32 * NT + k % 32) + lane % EPC;
+          x[u] = Logit<T>::get(reinterpret_cast<const T*>(g.base), at[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int id = at[u] - g.dc;
+          keep(x[u] >= x1 && i0 + lane / EPC + u * (32 / EPC) < queued && id >= 0 && id < a.V, x[u], at[u]);
+        }
+      }
+      __syncwarp();
+    };
+    walk_back([&](int j, const uint4& raw) {
       float f[EPC];
       g.values(raw, j, f);
       const float c = max_of(f);
@@ -656,7 +695,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
         for (int i = 0; i < EPC / 2; ++i) e[i] = __fmul2_rn(d[i], rr);
         st += sum_of_ex2();
       }
-      enqueue(j, drawn && c >= x1);
+      collect(j, f, drawn && c >= x1);
       if (greedy && c == m) {
 #pragma unroll
         for (int i = 0; i < EPC; ++i)
@@ -667,27 +706,10 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
         for (int i = 0; i < EPC; ++i) odd |= !(f[i] < kInf);
       }
     });
-    // The queued chunks, a logit per lane: in the walk itself a few lanes at a
-    // time would weigh while the others wait. A warp whose queue did not hold them
-    // all (most of its chunks are high then) walks its chunks again.
-    auto queued_chunk = [&](int i) {
-      const int at = queue[i];
-      return q_lo + wid * 32 + at / 32 * NT + at % 32;
-    };
-    // Four logits of the queued chunks per lane, -inf past their end.
-    auto four_queued = [&](int i0, float (&x)[4], int (&j)[4]) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) j[u] = queued_chunk(min(i0 + lane / EPC + u * (32 / EPC), queued - 1));
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        x[u] = value(j[u], lane % EPC);
-        if (i0 + lane / EPC + u * (32 / EPC) >= queued) x[u] = -kInf;
-      }
-    };
     // min-p: the last bin with a logit that stays, and whether one above x1 does not
     int floor_bin = -1, below = 0;
-    auto bin_queued = [&] {
-      __syncwarp();
+    auto bin_high = [&] {
+      collect_queued();
       floor_bin = -1;
       below = 0;
       auto add = [&](float x, uint32_t w) {
@@ -701,17 +723,8 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
           }
         }
       };
-      if (queued <= QCAP) {
-        for (int i0 = 0; i0 < queued; i0 += 128 / EPC) {
-          float x[4];
-          uint32_t w[4];
-          int j[4];
-          four_queued(i0, x, j);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) w[u] = sf_weight(x[u], m, q.r);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) add(x[u], w[u]);
-        }
+      if (have <= ECAP) {
+        for (int i = lane; i < have; i += 32) add(high_x[i], sf_weight(high_x[i], m, q.r));
       } else {
         walk([&](int j, const uint4& raw) {
           float f[EPC];
@@ -733,7 +746,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
         sh.ired[2][wid] = below;
       }
     };
-    bin_queued();
+    bin_high();
     // A NaN, or +inf under a finite maximum, makes the sum NaN.
     s = warp_sum(s);
     odd |= finite && !(s < kInf);
@@ -991,13 +1004,13 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
         per_x = fminf((float)NB / (m - x1), 3.402823466e38f);
         for (int i = tid; i < NB; i += NT) sh.cnt[i] = sh.lo[i] = sh.hi[i] = 0;
         cta_sync();
-        queued = 0;
+        queued = have = 0;
         walk([&](int j, const uint4& raw) {
           float f[EPC];
           g.values(raw, j, f);
-          enqueue(j, max_of(f) >= x1);
+          collect(j, f, max_of(f) >= x1);
         });
-        bin_queued();
+        bin_high();
         cta_sync();
         if (wid == 0) push_bins_info();
         sync();
@@ -1038,30 +1051,23 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
       }
     }
     if (command == kGather) {
-      auto take = [&](float x, int j, int i) {
+      auto take = [&](float x, int at) {
         const int b = bin_of(x);
         if (((sh.marks[b >> 5] >> (b & 31)) & 1u) && sf_weight(x, m, q.r)) {
-          const int at = atomicAdd(&sh.n_mine, 1);
-          if (at < CAP)
-            sh.incl[at] = ((u64)Logit<T>::key(x) << 32) | (u64)(0xffffffffu - (uint32_t)g.id(j, i));
+          const int slot = atomicAdd(&sh.n_mine, 1);
+          if (slot < CAP)
+            sh.incl[slot] = ((u64)Logit<T>::key(x) << 32) | (u64)(0xffffffffu - (uint32_t)(at - g.dc));
         }
       };
-      if (queued <= QCAP) {
-        for (int i0 = 0; i0 < queued; i0 += 128 / EPC) {
-          float x[4];
-          int j[4];
-          four_queued(i0, x, j);
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (x[u] >= x1) take(x[u], j[u], lane % EPC);
-        }
+      if (have <= ECAP) {
+        for (int i = lane; i < have; i += 32) take(high_x[i], high_at[i]);
       } else {
         walk([&](int j, const uint4& raw) {
           float f[EPC];
           g.values(raw, j, f);
 #pragma unroll
           for (int i = 0; i < EPC; ++i)
-            if (f[i] >= x1) take(f[i], j, i);
+            if (f[i] >= x1) take(f[i], EPC * j + i);
         });
       }
       // to rank 0's list, in one piece
@@ -1231,12 +1237,12 @@ constexpr int kSfMediumV = 8192;  // rows up to here: 128-thread CTAs, held in s
 constexpr long long kSfSliceMin = 8 << 10;
 
 // Launches the fast kernel with cs CTAs per row; *refused when no cluster of that shape fits.
-template <typename T, int NT, int NB, int CAP, int GROUPS, int QCAP, bool RESIDENT>
+template <typename T, int NT, int NB, int CAP, int GROUPS, int QCAP, int ECAP, bool RESIDENT>
 cudaError_t launch_fast(const FilteredArgs& a, int cs, cudaStream_t st, bool* refused) {
-  auto kern = k_sample_filtered<T, NT, NB, CAP, GROUPS, QCAP, RESIDENT>;
+  auto kern = k_sample_filtered<T, NT, NB, CAP, GROUPS, QCAP, ECAP, RESIDENT>;
   // a resident slice: the most chunks that a row's 16-byte blocks can make, shared out
-  const long long chunks = ((long long)a.V * sizeof(T) + 46 - 2 * sizeof(T)) / 16;
-  const size_t smem = RESIDENT ? (size_t)((chunks + cs - 1) / cs) * 16 : 0;
+  const int chunks = RESIDENT ? (int)((((long long)a.V * sizeof(T) + 46 - 2 * sizeof(T)) / 16 + cs - 1) / cs) : 0;
+  const size_t smem = (size_t)chunks * 16 + (size_t)(NT / 32) * ECAP * 8;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = smem;
@@ -1253,7 +1259,12 @@ cudaError_t launch_fast(const FilteredArgs& a, int cs, cudaStream_t st, bool* re
   // A CTA alone is launched without a cluster: as clusters of one, only eight of them run on an SM.
   cfg.numAttrs = cs == 1 ? 1 : 2;
   const void* site = reinterpret_cast<const void*>(kern);
-  const int fit = cached(site, (long long)smem * 32 + cs, [&](int) {
+  const int ok = cached(site, -1, [&](int) {
+    const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 << 10);
+    if (r != cudaSuccess) (void)cudaGetLastError();
+    return r == cudaSuccess ? 1 : 0;
+  });
+  const int fit = ok <= 0 ? 0 : cached(site, (long long)smem * 32 + cs, [&](int) {
     int v = 0;
     const cudaError_t r = cs == 1 ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kern, NT, smem)
                                   : cudaOccupancyMaxActiveClusters(&v, kern, &cfg);
@@ -1269,7 +1280,7 @@ cudaError_t launch_fast(const FilteredArgs& a, int cs, cudaStream_t st, bool* re
   }
   const long long clusters = a.n < fit ? a.n : fit;
   cfg.gridDim = dim3((unsigned)(clusters * cs));
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, chunks);
   if (e == cudaSuccess) note_launch();
   return e;
 }
@@ -1283,19 +1294,19 @@ static cudaError_t launch_filtered(const FilteredArgs& a, cudaStream_t st) {
   bool refused = false;
   cudaError_t e;
   if (a.V <= kSfSmallV && a.n >= sms * 8LL) {
-    e = launch_fast<T, 32, 128, 128, 32, 192, true>(a, 1, st, &refused);
+    e = launch_fast<T, 32, 128, 128, 32, 0, 256, true>(a, 1, st, &refused);
   } else if (a.V <= kSfMediumV) {
-    e = launch_fast<T, 128, 256, 256, 32, 128, true>(a, 1, st, &refused);
+    e = launch_fast<T, 128, 256, 256, 32, 0, 256, true>(a, 1, st, &refused);
   } else {
     // a CTA per row, or as many as the SMs that the rows leave, down to 8 KB of a row each
     int cs = 1;
     while (cs < 8 && a.n * cs * 2LL <= sms && (long long)a.V * sizeof(T) >= cs * 2 * kSfSliceMin) cs *= 2;
-    e = launch_fast<T, 512, 1024, 512, 128, 8192 / (512 / 32), false>(a, cs, st, &refused);
+    e = launch_fast<T, 512, 1024, 512, 128, 512, 256, false>(a, cs, st, &refused);
   }
   // No cluster of that size fits (another program's share of the GPU): a CTA per row always does.
   if (refused) {
     refused = false;
-    e = launch_fast<T, 512, 1024, 512, 128, 8192 / (512 / 32), false>(a, 1, st, &refused);
+    e = launch_fast<T, 512, 1024, 512, 128, 512, 256, false>(a, 1, st, &refused);
     if (refused) return cudaErrorLaunchOutOfResources;
   }
   return e;
