@@ -424,7 +424,11 @@ struct SfShared {
   int slot;
 };
 
-enum Command { kDone, kGather, kWeigh, kLower, kExact };
+// kOnce does every row. kFirst leaves the rows whose boundaries lie below the first
+// cut, or need the row's mass exactly, marked; kMarked does those.
+enum Pass { kOnce, kFirst, kMarked };
+
+enum Command { kDone, kGather, kWeigh, kLower, kExact, kMark };
 
 constexpr double kSfSlack = 2.2e-6, kSfRounding = 6e-8;
 
@@ -472,7 +476,7 @@ __device__ __forceinline__ bool sf_wait(u64* bar, uint32_t parity) {
 }  // namespace
 
 template <typename T, int NT, int NB, int CAP, int GROUPS, int QCAP, int ECAP, bool RESIDENT>
-__global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT) k_sample_filtered(FilteredArgs a, int slice_chunks) {
+__global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT) k_sample_filtered(FilteredArgs a, int slice_chunks, Pass pass) {
   constexpr int EPC = Chunk<T>::N, NW = NT / 32, U = RESIDENT ? 1 : 4;
   using Shared = SfShared<NT, NB, CAP, QCAP>;
   extern __shared__ uint4 slice[];
@@ -530,6 +534,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
 
   uint32_t parity = 0;
   for (long long n = cid; n < a.n; n += n_clusters, parity ^= 1u) {
+    if (!RESIDENT && pass == kMarked && a.out_tokens[n] != kStreamMark) continue;
     const Row<T> g = row_of(n);
     const int q_lo = from_of(g, rank), q_hi = from_of(g, rank + 1);
     const RowParams q = row_params(a, n);
@@ -984,7 +989,8 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
             sh.known_below = be;
           }
           __syncwarp();
-          const int c = sh.known_odd ? (int)kDone : decide(weighed);
+          int c = sh.known_odd ? (int)kDone : decide(weighed);
+          if (pass == kFirst && c != kDone && c != kGather) c = kMark;
           __syncwarp();
           for (int o = 1; o < cs; ++o) {
             Shared* peer = cl.map_shared_rank(&sh, o);
@@ -1089,7 +1095,9 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
 
     // ---- rank 0 answers
     const float lse = m + logf(sh.known_sum);
-    if (command == kDone) {
+    if (command == kMark) {
+      if (tid == 0) a.out_tokens[n] = kStreamMark;
+    } else if (command == kDone) {
       if (tid == 0) {
         report(a.d_status, DS_DEV_ERR_LOGITS);
         a.out_tokens[n] = -1;
@@ -1238,7 +1246,7 @@ constexpr long long kSfSliceMin = 8 << 10;
 
 // Launches the fast kernel with cs CTAs per row; *refused when no cluster of that shape fits.
 template <typename T, int NT, int NB, int CAP, int GROUPS, int QCAP, int ECAP, bool RESIDENT>
-cudaError_t launch_fast(const FilteredArgs& a, int cs, cudaStream_t st, bool* refused) {
+cudaError_t launch_fast(const FilteredArgs& a, int cs, Pass pass, cudaStream_t st, bool* refused) {
   auto kern = k_sample_filtered<T, NT, NB, CAP, GROUPS, QCAP, ECAP, RESIDENT>;
   // a resident slice: the most chunks that a row's 16-byte blocks can make, shared out
   const int chunks = RESIDENT ? (int)((((long long)a.V * sizeof(T) + 46 - 2 * sizeof(T)) / 16 + cs - 1) / cs) : 0;
@@ -1280,7 +1288,7 @@ cudaError_t launch_fast(const FilteredArgs& a, int cs, cudaStream_t st, bool* re
   }
   const long long clusters = a.n < fit ? a.n : fit;
   cfg.gridDim = dim3((unsigned)(clusters * cs));
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, chunks);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, chunks, pass);
   if (e == cudaSuccess) note_launch();
   return e;
 }
@@ -1294,22 +1302,29 @@ static cudaError_t launch_filtered(const FilteredArgs& a, cudaStream_t st) {
   bool refused = false;
   cudaError_t e;
   if (a.V <= kSfSmallV && a.n >= sms * 8LL) {
-    e = launch_fast<T, 32, 128, 128, 32, 0, 256, true>(a, 1, st, &refused);
+    e = launch_fast<T, 32, 128, 128, 32, 0, 256, true>(a, 1, kOnce, st, &refused);
   } else if (a.V <= kSfMediumV) {
-    e = launch_fast<T, 128, 256, 256, 32, 0, 256, true>(a, 1, st, &refused);
+    e = launch_fast<T, 128, 256, 256, 32, 0, 256, true>(a, 1, kOnce, st, &refused);
   } else {
-    // a CTA per row, or as many as the SMs that the rows leave, down to 8 KB of a row each
+    // A CTA per row, or as many as the SMs that the rows leave, down to 8 KB of a
+    // row each. A CTA alone would hold the call up with a row that takes several
+    // more walks: such rows get eight CTAs each in a second pass.
     int cs = 1;
     while (cs < 8 && a.n * cs * 2LL <= sms && (long long)a.V * sizeof(T) >= cs * 2 * kSfSliceMin) cs *= 2;
-    e = launch_fast<T, 512, 1024, 512, 128, 512, 256, false>(a, cs, st, &refused);
+    e = launch_fast<T, 512, 1024, 512, 128, 384, 256, false>(a, cs, cs > 1 ? kOnce : kFirst, st, &refused);
+    if (!refused && e == cudaSuccess && cs == 1) {
+      e = launch_fast<T, 512, 1024, 512, 128, 384, 256, false>(a, 8, kMarked, st, &refused);
+      if (refused) {
+        refused = false;
+        e = launch_fast<T, 512, 1024, 512, 128, 384, 256, false>(a, 1, kMarked, st, &refused);
+      }
+    } else if (refused) {
+      // no cluster of that size fits beside another program's work: a CTA per row does
+      refused = false;
+      e = launch_fast<T, 512, 1024, 512, 128, 384, 256, false>(a, 1, kOnce, st, &refused);
+    }
   }
-  // No cluster of that size fits (another program's share of the GPU): a CTA per row always does.
-  if (refused) {
-    refused = false;
-    e = launch_fast<T, 512, 1024, 512, 128, 512, 256, false>(a, 1, st, &refused);
-    if (refused) return cudaErrorLaunchOutOfResources;
-  }
-  return e;
+  return refused ? cudaErrorLaunchOutOfResources : e;
 }
 
 cudaError_t launch_sample_filtered(const FilteredArgs& a, bool f32, cudaStream_t st) {
