@@ -153,6 +153,20 @@ def test_every_spread_and_filter_alone(sigma, V, dtype):
         assert np.array_equal(tok, _integer_definition(x, *par))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,V", [(1300, 33), (1300, 1025), (1301, 2048), (1300, 2049), (700, 5003), (160, 9001),
+                                 (100, 70001)])
+@pytest.mark.parametrize("kind", ["normal", "few", "masked", "equal"])
+def test_batches_that_fill_the_gpu(n, V, kind, dtype):
+    """Enough rows that each gets one warp or one CTA, and several in turn; rows that take further passes among them."""
+    x = _logits(n, V, 3.0, V, DT[dtype], kind)
+    x[::7] *= 0.01
+    x = x.to(_dev())
+    par = _params(n, V)
+    tok, _ = _run(x, *par)
+    assert np.array_equal(tok, _integer_definition(x, *par))
+
+
 def test_filters_left_out_are_off():
     n, V = 16, 1025
     x = _logits(n, V, 2.0, 1, torch.bfloat16).to(_dev())

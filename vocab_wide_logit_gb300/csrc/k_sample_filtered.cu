@@ -424,8 +424,9 @@ struct SfShared {
   int slot;
 };
 
-// kOnce does every row. kFirst leaves the rows whose boundaries lie below the first
-// cut, or need the row's mass exactly, marked; kMarked does those.
+// kOnce does every row. kFirst, a kernel of its own without the code for them,
+// leaves the rows whose boundaries lie below the first cut, need the row's mass
+// exactly or overflow a list marked; kMarked does those.
 enum Pass { kOnce, kFirst, kMarked };
 
 enum Command { kDone, kGather, kWeigh, kLower, kExact, kMark };
@@ -475,8 +476,8 @@ __device__ __forceinline__ bool sf_wait(u64* bar, uint32_t parity) {
 
 }  // namespace
 
-template <typename T, int NT, int NB, int CAP, int GROUPS, int QCAP, int ECAP, bool RESIDENT>
-__global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT) k_sample_filtered(FilteredArgs a, int slice_chunks, Pass pass) {
+template <typename T, int NT, int NB, int CAP, int GROUPS, int QCAP, int ECAP, bool RESIDENT, Pass PASS>
+__global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT) k_sample_filtered(FilteredArgs a, int slice_chunks) {
   constexpr int EPC = Chunk<T>::N, NW = NT / 32, U = RESIDENT ? 1 : 4;
   using Shared = SfShared<NT, NB, CAP, QCAP>;
   extern __shared__ uint4 slice[];
@@ -530,11 +531,23 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
             : "memory");
     }
   };
-  start_copy(cid);
+  // The first row from n on that this cluster has to do: 32 are looked at at a time.
+  auto row_from = [&](long long n) {
+    if constexpr (PASS == kMarked) {
+      for (; n < a.n; n += 32 * n_clusters) {
+        const long long i = n + lane * n_clusters;
+        const unsigned marked = __ballot_sync(0xffffffffu, i < a.n && a.out_tokens[i] == kStreamMark);
+        if (marked) return n + (__ffs(marked) - 1) * n_clusters;
+      }
+    }
+    return n;
+  };
+  long long next = row_from(cid);
+  start_copy(next);
 
   uint32_t parity = 0;
-  for (long long n = cid; n < a.n; n += n_clusters, parity ^= 1u) {
-    if (!RESIDENT && pass == kMarked && a.out_tokens[n] != kStreamMark) continue;
+  for (long long n; (n = next) < a.n; parity ^= 1u) {
+    next = row_from(n + n_clusters);
     const Row<T> g = row_of(n);
     const int q_lo = from_of(g, rank), q_hi = from_of(g, rank + 1);
     const RowParams q = row_params(a, n);
@@ -602,7 +615,12 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
     // their size, which needs a range that ends above them.
     const float lowest = (m - 24.f * q.tau) - fabsf(m) * 2.4e-7f;
     const float x_low = lowest > -3e37f ? fmaxf(fminf(lo, m), lowest) : fmaxf(lowest, -3.402823466e38f);
-    float x1 = fmaxf(cut, x_low);
+    // The first cut; for a row of the second pass, of which most lie below it, the
+    // next one, or no cut where the row is short.
+    // A warp's own row starts a little lower, and lower still for a top-k that
+    // would end below (15510 x 1025, 12% of the rows with k = 200: 148 -> 129 us).
+    const float further = PASS == kMarked ? (RESIDENT ? 1e30f : 0.27f) : NT == 32 ? (q.k > 64 ? 0.3f : 0.1f) : 0.f;
+    float x1 = fmaxf(cut - further * (m - cut), x_low);
     float per_x = fminf((float)NB / (m - x1), 3.402823466e38f);
     auto bin_of = [&](float x) { return min(NB - 1, __float2int_rz((m - x) * per_x)); };  // for x1 <= x <= m
     const bool finite = m > -kInf && m < kInf;
@@ -730,6 +748,8 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
       };
       if (have <= ECAP) {
         for (int i = lane; i < have; i += 32) add(high_x[i], sf_weight(high_x[i], m, q.r));
+      } else if constexpr (PASS == kFirst) {
+        if (lane == 0) lead->crowded = 1;
       } else {
         walk([&](int j, const uint4& raw) {
           float f[EPC];
@@ -761,26 +781,32 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
       first = warp_min_i(first);
       if (lane == 0 && first != INT_MAX) atomicMin(&lead->first_id, first);
     }
-    if (lane == 0) {
-      sh.sred[0][wid] = s;
-      sh.sred[1][wid] = st;
-      sh.ired[0][wid] = odd;
-    }
-    cta_sync();
     // this CTA's share of what rank 0 needs to know, pushed there
     auto push_bins_info = [&] {
-      floor_bin = __reduce_max_sync(0xffffffffu, lane < NW ? sh.ired[1][lane] : -1);
-      below = __any_sync(0xffffffffu, lane < NW && sh.ired[2][lane]);
+      if (NW > 1) {
+        floor_bin = __reduce_max_sync(0xffffffffu, lane < NW ? sh.ired[1][lane] : -1);
+        below = __any_sync(0xffffffffu, lane < NW && sh.ired[2][lane]);
+      }
       if (lane == 0) {
         lead->part_floor[rank] = floor_bin;
         lead->part_below[rank] = below;
       }
     };
+    if (NW > 1) {
+      if (lane == 0) {
+        sh.sred[0][wid] = s;
+        sh.sred[1][wid] = st;
+        sh.ired[0][wid] = odd;
+      }
+      cta_sync();
+    }
     if (wid == 0) {
-      const bool in = lane < NW;
-      s = warp_sum(in ? sh.sred[0][lane] : 0.f);
-      st = warp_sum(in ? sh.sred[1][lane] : 0.f);
-      odd = __any_sync(0xffffffffu, in && sh.ired[0][lane]);
+      if (NW > 1) {
+        const bool in = lane < NW;
+        s = warp_sum(in ? sh.sred[0][lane] : 0.f);
+        st = warp_sum(in ? sh.sred[1][lane] : 0.f);
+        odd = __any_sync(0xffffffffu, in && sh.ired[0][lane]);
+      }
       if (lane == 0) {
         lead->part_sum[rank] = s;
         lead->part_tempered[rank] = st;
@@ -791,7 +817,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
     sync();
 
     if (!drawn) {
-      start_copy(n + n_clusters);
+      start_copy(next);
       if (rank == 0 && tid == 0) {
         int bits = 0;
         float sum = 0.f;
@@ -898,7 +924,8 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
       auto light = [&](int b, u64 width) {
         const u64 mass = sh.pm[b] - (b ? sh.pm[b - 1] : 0);
         const uint32_t c = sh.pc[b] - (b ? sh.pc[b - 1] : 0u);
-        return width > 0 && width * 4 * c > mass;
+        // a row of the second pass is not tried with bounds again
+        return width > 0 && (PASS == kMarked || width * 4 * c > mass);
       };
       if (complete) {
         if (lane == 0) sh.t_lo = sh.t_hi = known;
@@ -962,10 +989,12 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
 
     if (cs > 1) merge_bins();
     if (rank == 0 && wid == 0) {
-      const bool in = lane < cs;
-      s = warp_sum(in ? sh.part_sum[lane] : 0.f);
-      st = warp_sum(in ? sh.part_tempered[lane] : 0.f);
-      odd = __any_sync(0xffffffffu, in && sh.part_odd[lane]);
+      if (cs > 1) {
+        const bool in = lane < cs;
+        s = warp_sum(in ? sh.part_sum[lane] : 0.f);
+        st = warp_sum(in ? sh.part_tempered[lane] : 0.f);
+        odd = __any_sync(0xffffffffu, in && sh.part_odd[lane]);
+      }
       if (lane == 0) {
         const double t = (double)(tempered ? st : s) * (double)kSfOne;
         const double slack = t * (kSfSlack + kSfRounding * (21 + (q_hi - q_lo + NT - 1) / NT)) + 0.5 * (double)a.V;
@@ -990,7 +1019,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
           }
           __syncwarp();
           int c = sh.known_odd ? (int)kDone : decide(weighed);
-          if (pass == kFirst && c != kDone && c != kGather) c = kMark;
+          if (PASS == kFirst && c != kDone && c != kGather) c = kMark;
           __syncwarp();
           for (int o = 1; o < cs; ++o) {
             Shared* peer = cl.map_shared_rank(&sh, o);
@@ -1002,6 +1031,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
       }
       sync();
       command = sh.command;
+      if (PASS == kFirst || (command != kLower && command != kWeigh)) break;
       if (command == kLower) {
         // A lower cut: a quarter further from the maximum each time, which in the
         // tail of normal logits holds some four times as many, and at last all.
@@ -1025,7 +1055,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
           sync();
         }
         fresh = true;
-      } else if (command == kWeigh) {
+      } else {
         // the mass of the rest of the row, exactly
         u64 total = 0;
         walk([&](int j, const uint4& raw) {
@@ -1052,8 +1082,6 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
         }
         weighed = true;
         fresh = false;
-      } else {
-        break;
       }
     }
     if (command == kGather) {
@@ -1067,7 +1095,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
       };
       if (have <= ECAP) {
         for (int i = lane; i < have; i += 32) take(high_x[i], high_at[i]);
-      } else {
+      } else if constexpr (PASS != kFirst) {
         walk([&](int j, const uint4& raw) {
           float f[EPC];
           g.values(raw, j, f);
@@ -1090,12 +1118,12 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
       }
       sync();
     }
-    start_copy(n + n_clusters);
+    start_copy(next);
     if (rank != 0) continue;
 
     // ---- rank 0 answers
     const float lse = m + logf(sh.known_sum);
-    if (command == kMark) {
+    if (PASS == kFirst && command == kMark) {
       if (tid == 0) a.out_tokens[n] = kStreamMark;
     } else if (command == kDone) {
       if (tid == 0) {
@@ -1103,7 +1131,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
         a.out_tokens[n] = -1;
         a.out_logprobs[n] = __int_as_float(0x7fffffff);
       }
-    } else if (command == kExact) {
+    } else if (PASS != kFirst && command == kExact) {
       const T* row = static_cast<const T*>(a.x) + n * a.ld;
       const Bins<NB> bins = {sh.cnt, sh.lo, sh.hi, sh.pc, sh.red, sh.found};
       const int token = row_exact<T, NT, NB>(row, a.V, q, m, bins, &sh.slot);
@@ -1113,6 +1141,16 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
       }
     } else {
       const int len = sh.n_list;
+      if (len == 1) {
+        // every boundary falls on it
+        if (tid == 0) {
+          const u64 e = sh.list[0];
+          a.out_tokens[n] = (int)(0xffffffffu - (uint32_t)e);
+          a.out_logprobs[n] = Logit<T>::value((uint32_t)(e >> 32)) - lse;
+        }
+        cta_sync();
+        continue;
+      }
       if (len <= 32) {
         if (wid == 0) {
           // bitonic sort in registers, descending
@@ -1220,10 +1258,11 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : NT == 128 ? 6 : 1024 / NT)
           if (lane == 0) {
             sh.again = at != lo_at;
             const u64 e = sh.list[at];
-            a.out_tokens[n] = (int)(0xffffffffu - (uint32_t)e);
+            a.out_tokens[n] = PASS == kFirst && at != lo_at ? kStreamMark : (int)(0xffffffffu - (uint32_t)e);
             a.out_logprobs[n] = Logit<T>::value((uint32_t)(e >> 32)) - lse;
           }
         }
+        if (PASS == kFirst) break;
         cta_sync();
         if (!sh.again) break;
         // the bounds fall on two logits: weigh the whole row here
@@ -1245,9 +1284,9 @@ constexpr int kSfMediumV = 8192;  // rows up to here: 128-thread CTAs, held in s
 constexpr long long kSfSliceMin = 8 << 10;
 
 // Launches the fast kernel with cs CTAs per row; *refused when no cluster of that shape fits.
-template <typename T, int NT, int NB, int CAP, int GROUPS, int QCAP, int ECAP, bool RESIDENT>
-cudaError_t launch_fast(const FilteredArgs& a, int cs, Pass pass, cudaStream_t st, bool* refused) {
-  auto kern = k_sample_filtered<T, NT, NB, CAP, GROUPS, QCAP, ECAP, RESIDENT>;
+template <typename T, int NT, int NB, int CAP, int GROUPS, int QCAP, int ECAP, bool RESIDENT, Pass PASS>
+cudaError_t launch_fast(const FilteredArgs& a, int cs, cudaStream_t st, bool* refused) {
+  auto kern = k_sample_filtered<T, NT, NB, CAP, GROUPS, QCAP, ECAP, RESIDENT, PASS>;
   // a resident slice: the most chunks that a row's 16-byte blocks can make, shared out
   const int chunks = RESIDENT ? (int)((((long long)a.V * sizeof(T) + 46 - 2 * sizeof(T)) / 16 + cs - 1) / cs) : 0;
   const size_t smem = (size_t)chunks * 16 + (size_t)(NT / 32) * ECAP * 8;
@@ -1286,9 +1325,15 @@ cudaError_t launch_fast(const FilteredArgs& a, int cs, Pass pass, cudaStream_t s
     *refused = true;
     return cudaSuccess;
   }
-  const long long clusters = a.n < fit ? a.n : fit;
+  // Marked rows are few and fall anywhere: short shares, handed out as clusters
+  // come free. A CTA per short row (15510 x 1025: the pass took 88 us with a
+  // resident grid, 41 us so); three shares per resident cluster for long ones,
+  // whose empty CTAs cost more (256 x 248320, one marked row / a tenth marked:
+  // 66 / 174 us with one share, 71 / 144 with three, 81 / 135 with eight).
+  const long long most = PASS != kMarked ? fit : RESIDENT ? 1ll << 20 : 3ll * fit;
+  const long long clusters = a.n < most ? a.n : most;
   cfg.gridDim = dim3((unsigned)(clusters * cs));
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, chunks, pass);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, chunks);
   if (e == cudaSuccess) note_launch();
   return e;
 }
@@ -1302,26 +1347,28 @@ static cudaError_t launch_filtered(const FilteredArgs& a, cudaStream_t st) {
   bool refused = false;
   cudaError_t e;
   if (a.V <= kSfSmallV && a.n >= sms * 8LL) {
-    e = launch_fast<T, 32, 128, 128, 32, 0, 256, true>(a, 1, kOnce, st, &refused);
+    e = launch_fast<T, 32, 128, 64, 32, 0, 320, true, kFirst>(a, 1, st, &refused);
+    if (!refused && e == cudaSuccess) e = launch_fast<T, 128, 256, 256, 32, 0, 256, true, kMarked>(a, 1, st, &refused);
   } else if (a.V <= kSfMediumV) {
-    e = launch_fast<T, 128, 256, 256, 32, 0, 256, true>(a, 1, kOnce, st, &refused);
+    e = launch_fast<T, 128, 256, 256, 32, 0, 256, true, kOnce>(a, 1, st, &refused);
   } else {
     // A CTA per row, or as many as the SMs that the rows leave, down to 8 KB of a
     // row each. A CTA alone would hold the call up with a row that takes several
     // more walks: such rows get eight CTAs each in a second pass.
     int cs = 1;
     while (cs < 8 && a.n * cs * 2LL <= sms && (long long)a.V * sizeof(T) >= cs * 2 * kSfSliceMin) cs *= 2;
-    e = launch_fast<T, 512, 1024, 512, 128, 384, 256, false>(a, cs, cs > 1 ? kOnce : kFirst, st, &refused);
-    if (!refused && e == cudaSuccess && cs == 1) {
-      e = launch_fast<T, 512, 1024, 512, 128, 384, 256, false>(a, 8, kMarked, st, &refused);
-      if (refused) {
-        refused = false;
-        e = launch_fast<T, 512, 1024, 512, 128, 384, 256, false>(a, 1, kMarked, st, &refused);
-      }
-    } else if (refused) {
+    if (cs == 1) {
+      e = launch_fast<T, 512, 1024, 512, 128, 384, 256, false, kFirst>(a, 1, st, &refused);
+      if (refused || e != cudaSuccess) return refused ? cudaErrorLaunchOutOfResources : e;
+      e = launch_fast<T, 512, 1024, 512, 128, 384, 256, false, kMarked>(a, 8, st, &refused);
+    } else {
+      e = launch_fast<T, 512, 1024, 512, 128, 384, 256, false, kOnce>(a, cs, st, &refused);
+    }
+    if (refused) {
       // no cluster of that size fits beside another program's work: a CTA per row does
       refused = false;
-      e = launch_fast<T, 512, 1024, 512, 128, 384, 256, false>(a, 1, kOnce, st, &refused);
+      e = cs == 1 ? launch_fast<T, 512, 1024, 512, 128, 384, 256, false, kMarked>(a, 1, st, &refused)
+                  : launch_fast<T, 512, 1024, 512, 128, 384, 256, false, kOnce>(a, 1, st, &refused);
     }
   }
   return refused ? cudaErrorLaunchOutOfResources : e;
