@@ -193,8 +193,8 @@ __device__ __forceinline__ void widen4(uint32_t b, uint32_t& lo, uint32_t& hi) {
   hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
-constexpr int kTcEpi = 4;   // warps 0-3: results out of tensor memory
-constexpr int kTcCvt = 8;   // warps 4-11: int8 weights to fp16, two groups of four
+constexpr int kTcEpi = 8;   // warps 0-7: results out of tensor memory, two per lane quarter
+constexpr int kTcCvt = 8;   // warps 8-15: int8 weights to fp16, two groups of four
 constexpr int kTcWarps = kTcEpi + kTcCvt + 3;  // then: weight loads, row loads, matrix instructions
 constexpr int kTcNT = kTcWarps * 32;
 constexpr int kTcBlock = kPackRows * kPackK;  // bytes of a weight block
@@ -202,6 +202,7 @@ constexpr int kTcWSlots = 12;                 // most weight slots
 constexpr int kTcBSlots = 32;                 // most row-tile slots
 constexpr int kTcASlots = 4;                  // fp16 weight blocks in tensor memory, 64 columns each
 constexpr int kTcACol = 256;                  // their first column; accumulators are below
+constexpr int kTcSms = 152;  // SMs that calls are cut for
 constexpr size_t kTcSmem = 232448 - 2048;     // dynamic shared memory of a CTA, barriers apart
 
 // How a call of n rows is cut: row tiles of `rows` (a multiple of 16, at most
@@ -213,11 +214,32 @@ struct TcPlan {
 
 }  // namespace
 
-static TcPlan tc_plan(int n, int K) {
+// Estimated cycles of a call cut into `tiles` row tiles. Measured: an instruction
+// takes rows / 2 cycles, but 100 at least (its weights come from tensor memory);
+// a tile's results take 1500 and 10 a row, which overlap with the next tile's
+// instructions only where two accumulators fit (rows <= 128).
+static long long tc_cycles(int n, int N, int kb, int tiles, int rows) {
+  const long long ctas = ((N + kPackRows - 1LL) / kPackRows) * tiles, waves = (ctas + kTcSms - 1) / kTcSms;
+  const long long mma = 8LL * kb * (rows > 200 ? rows / 2 : 100), out = 1500 + 10LL * rows;
+  return waves * (rows > 128 ? mma + out : mma > out ? mma : out);
+}
+
+static TcPlan tc_plan(int n, int N, int K) {
   TcPlan p;
-  p.tiles = (n + 255) / 256;
-  p.rows = ((n + p.tiles - 1) / p.tiles + 15) / 16 * 16;
   p.kb = (K + kPackK - 1) / kPackK;
+  // as few row tiles as fit, or a few more where that fills the last wave better
+  const int least = (n + 255) / 256;
+  long long best = 0;
+  for (int tiles = least; tiles <= least + 8; ++tiles) {
+    const int rows = ((n + tiles - 1) / tiles + 15) / 16 * 16;
+    if ((long long)rows * (tiles - 1) >= n) continue;  // its last tile would be empty
+    const long long c = tc_cycles(n, N, p.kb, tiles, rows);
+    if (tiles == least || c < best) {
+      best = c;
+      p.tiles = tiles;
+      p.rows = rows;
+    }
+  }
   const long long room = (long long)kTcSmem - 1024;  // the tiles start on 1024 bytes
   const long long slot = (long long)p.rows * 128, all = slot * 2 * p.kb;
   p.resident = p.tiles == 1 && 2 * p.kb <= kTcBSlots && all + 6 * kTcBlock <= room;
@@ -264,7 +286,7 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&d_full[i], 1);
-      mbar_init(&d_empty[i], 4);
+      mbar_init(&d_empty[i], kTcEpi);
     }
     mbar_init(&drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -421,15 +443,15 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
     }
   } else {
     // ---- results: a thread has one channel, a column of tensor memory is one row of a
-    const int quad = warp;
+    const int quad = warp & 3, half = warp >> 2;
     Ring rd;
     long long scales = -1;  // row tile whose scales are in shared memory
     for (long long t = blockIdx.x; t < n_tiles; t += gridDim.x) {
       const long long j = t / p.tiles * kPackRows + quad * 32 + lane, tile = t % p.tiles, i0 = tile * p.rows;
       if (tile != scales) {
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        for (int i = threadIdx.x; i < p.rows; i += 128) a_scale[i] = i0 + i < g.n ? g.a_scale[i0 + i] : 0.f;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        for (int i = threadIdx.x; i < p.rows; i += kTcEpi * 32) a_scale[i] = i0 + i < g.n ? g.a_scale[i0 + i] : 0.f;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
         scales = tile;
       }
       const float sw = j < g.N ? g.w_scale[j] : 0.f;
@@ -437,8 +459,9 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
       tc_fence_after();
       if (__any_sync(0xffffffffu, *stop)) break;
       const uint32_t src = tmem + ((uint32_t)(quad * 32) << 16) + rd.slot * 128u;
-      OUT* out = static_cast<OUT*>(g.out) + i0 * g.ldo + j;
-      for (int c = 0; c < p.rows; c += 32, out += 32 * g.ldo) {
+      // the two warps of a quarter take 32 columns in turn
+      OUT* out = static_cast<OUT*>(g.out) + (i0 + 32 * half) * g.ldo + j;
+      for (int c = 32 * half; c < p.rows; c += 64, out += 64 * g.ldo) {
         float f[32];
         tc_ld32(src + c, p.rows - c, f);
         const int left = (int)(g.n - i0) - c < p.rows - c ? (int)(g.n - i0) - c : p.rows - c;
@@ -468,7 +491,7 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
 }
 
 long long linear_i8_workspace(int n, int N, int K) {
-  const TcPlan p = tc_plan(n, K);
+  const TcPlan p = tc_plan(n, N, K);
   return (long long)p.tiles * p.rows * p.kb * kPackK * 2;
 }
 
@@ -494,7 +517,7 @@ cudaError_t launch_pack_i8(const int8_t* w, int N, int K, int64_t ldw, uint8_t* 
 cudaError_t launch_linear_i8(const LinearArgs& g, bool bf16_out, cudaStream_t st) {
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorUnknown;
-  const TcPlan p = tc_plan(g.n, g.K);
+  const TcPlan p = tc_plan(g.n, g.N, g.K);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
