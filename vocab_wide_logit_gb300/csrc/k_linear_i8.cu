@@ -205,6 +205,18 @@ constexpr int kTcACol = 256;                  // their first column; accumulator
 constexpr int kTcSms = 152;  // SMs that calls are cut for
 constexpr size_t kTcSmem = 232448 - 2048;     // dynamic shared memory of a CTA, barriers apart
 
+// The warps that read results: all of them meet, and whether one of their threads says so.
+__device__ __forceinline__ void epi_sync() { asm volatile("barrier.sync 1, %0;" ::"n"(kTcEpi * 32) : "memory"); }
+__device__ __forceinline__ bool epi_any(bool p) {
+  uint32_t any;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.red.or.pred q, 1, %2, p;\nselp.u32 %0, 1, 0, q;\n}"
+      : "=r"(any)
+      : "r"((uint32_t)p), "n"(kTcEpi * 32)
+      : "memory");
+  return any != 0;
+}
+
 // How a call of n rows is cut: row tiles of `rows` (a multiple of 16, at most
 // 256), their slots in shared memory, and whether all of a tile's slots stay
 // there for every channel block.
@@ -447,24 +459,25 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
     Ring rd;
     long long scales = -1;  // row tile whose scales are in shared memory
     for (long long t = blockIdx.x; t < n_tiles; t += gridDim.x) {
-      const long long j = t / p.tiles * kPackRows + quad * 32 + lane, tile = t % p.tiles, i0 = tile * p.rows;
+      const long long j = t / p.tiles * kPackRows + quad * 32 + lane;
+      const long long tile = t % p.tiles, i0 = tile * p.rows;
+      const float sw = j < g.N ? g.w_scale[j] : 0.f;
+      const bool gone = !mbar_wait(&d_full[rd.slot], rd.phase, stop) || *stop;
+      if (epi_any(gone)) break;  // all of these warps or none: they meet at barriers below
+      tc_fence_after();
       if (tile != scales) {
-        asm volatile("bar.sync 1, 256;" ::: "memory");
         for (int i = threadIdx.x; i < p.rows; i += kTcEpi * 32) a_scale[i] = i0 + i < g.n ? g.a_scale[i0 + i] : 0.f;
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        epi_sync();
         scales = tile;
       }
-      const float sw = j < g.N ? g.w_scale[j] : 0.f;
-      if (!__all_sync(0xffffffffu, mbar_wait(&d_full[rd.slot], rd.phase, stop))) break;
-      tc_fence_after();
-      if (__any_sync(0xffffffffu, *stop)) break;
       const uint32_t src = tmem + ((uint32_t)(quad * 32) << 16) + rd.slot * 128u;
+      const int rows = (int)(g.n - i0 < p.rows ? g.n - i0 : p.rows);  // of this tile
       // the two warps of a quarter take 32 columns in turn
       OUT* out = static_cast<OUT*>(g.out) + (i0 + 32 * half) * g.ldo + j;
       for (int c = 32 * half; c < p.rows; c += 64, out += 64 * g.ldo) {
         float f[32];
         tc_ld32(src + c, p.rows - c, f);
-        const int left = (int)(g.n - i0) - c < p.rows - c ? (int)(g.n - i0) - c : p.rows - c;
+        const int left = rows - c;
         if (j < g.N) {
           if (left >= 32) {
 #pragma unroll
