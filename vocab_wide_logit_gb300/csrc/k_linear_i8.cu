@@ -156,21 +156,34 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&v)[32]) 
       "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
       : "memory");
 }
-// The next 32 columns of this thread's lane, `columns` of them read (16 or 32).
-__device__ __forceinline__ void tc_ld32(uint32_t addr, int columns, float (&f)[32]) {
-  uint32_t v[32];
+// 16 columns of this thread's lane, and the wait for them. The wait names the
+// registers, so that no use of them moves above it.
+__device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t* v) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
         "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
       : "r"(addr));
-  if (columns > 16)
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
-          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-        : "r"(addr + 16));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_ld16_wait(uint32_t* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+               :
+               : "memory");
+}
+// The next 32 columns, `columns` of them read (16 or 32).
+__device__ __forceinline__ void tc_ld32(uint32_t addr, int columns, float (&f)[32]) {
+  uint32_t v[32];
+  tc_ld16(addr, v);
+  if (columns > 16) {
+    tc_ld16(addr + 16, v + 16);
+  } else {
+#pragma unroll
+    for (int i = 16; i < 32; ++i) v[i] = 0u;
+  }
+  tc_ld16_wait(v);
+  tc_ld16_wait(v + 16);
 #pragma unroll
   for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
 }
