@@ -479,6 +479,7 @@ __device__ __forceinline__ bool sf_wait(u64* bar, uint32_t parity) {
 template <typename T, int NT, int NB, int CAP, int GROUPS, int QCAP, int ECAP, bool RESIDENT, Pass PASS>
 __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT) k_sample_filtered(FilteredArgs a, int slice_chunks) {
   constexpr int EPC = Chunk<T>::N, NW = NT / 32, U = RESIDENT ? 1 : 4;
+  constexpr bool ONE_WALK = PASS == kFirst && !RESIDENT;  // one CTA a row
   using Shared = SfShared<NT, NB, CAP, QCAP>;
   extern __shared__ uint4 slice[];
   __shared__ Shared sh;
@@ -563,15 +564,115 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
     }
     if (RESIDENT && !sf_wait(&sh.full, parity)) report(a.d_status, DS_DEV_ERR_TIMEOUT);
 
-    // ---- max
-    float mx = -kInf, mn = kInf;
-    walk([&](int j, const uint4& raw) {
-      float f[EPC];
-      g.values(raw, j, f);
-      mx = fmaxf(mx, max_of(f));
+    // ---- the sums of a chunk and its largest logit, relative to `ref`
+    float s = 0.f, st = 0.f;
+    const float2 l2e = make_float2(kLog2e, kLog2e), rr = make_float2(q.r, q.r);
+    auto sum_chunk = [&](const float (&f)[EPC], float ref, bool also_tempered) {
+      const float2 neg = make_float2(-ref, -ref);
+      float2 d[EPC / 2], e[EPC / 2];
 #pragma unroll
-      for (int i = 0; i < EPC; ++i) mn = fminf(mn, f[i] > -3e37f ? f[i] : kInf);
-    });
+      for (int i = 0; i < EPC / 2; ++i) d[i] = __fadd2_rn(make_float2(f[2 * i], f[2 * i + 1]), neg);
+      auto sum_of_ex2 = [&]() {
+#pragma unroll
+        for (int i = 0; i < EPC / 2; ++i) {
+          e[i] = __fmul2_rn(e[i], l2e);
+          e[i] = make_float2(ex2_approx(e[i].x), ex2_approx(e[i].y));
+        }
+#pragma unroll
+        for (int o = 1; o < EPC / 2; o *= 2)
+#pragma unroll
+          for (int i = 0; i + o < EPC / 2; i += 2 * o) e[i] = __fadd2_rn(e[i], e[i + o]);
+        return e[0].x + e[0].y;
+      };
+#pragma unroll
+      for (int i = 0; i < EPC / 2; ++i) e[i] = d[i];
+      s += sum_of_ex2();
+      if (also_tempered) {
+#pragma unroll
+        for (int i = 0; i < EPC / 2; ++i) e[i] = __fmul2_rn(d[i], rr);
+        st += sum_of_ex2();
+      }
+    };
+
+    // ---- the logits above the cut
+    float x1 = 0.f;
+    int queued = 0;
+    int have = 0;  // logits >= x1 of this warp's walk; more than fit: the walk itself is repeated for them
+    // ONE_WALK: a warp has 32-chunk blocks in a row, from this chunk on
+    const int warp_from = q_lo + (int)((long long)wid * ((q_hi - q_lo + 31) / 32) / NW) * 32;
+    const int warp_to = min(q_hi, q_lo + (int)((long long)(wid + 1) * ((q_hi - q_lo + 31) / 32) / NW) * 32);
+    auto keep = [&](bool high, float x, int at) {
+      const unsigned who = __ballot_sync(0xffffffffu, high);
+      const int slot = have + __popc(who & ((1u << lane) - 1u));
+      if (high && slot < ECAP) {
+        high_x[slot] = x;
+        high_at[slot] = at;
+      }
+      have += __popc(who);
+    };
+    // Of a short row every logit is looked at in the walk; of a long one, chunks
+    // with a high logit are queued, so that the walk pays a ballot a chunk.
+    auto collect = [&](int j, const float (&f)[EPC], bool high) {
+      const unsigned who = __ballot_sync(0xffffffffu, high);
+      if (RESIDENT) {
+        if (who) {
+#pragma unroll
+          for (int i = 0; i < EPC; ++i) keep(high && f[i] >= x1, f[i], EPC * j + i);
+        }
+      } else {
+        const int at = queued + __popc(who & ((1u << lane) - 1u));
+        if (high && at < QCAP) queue[at] = (uint16_t)(ONE_WALK ? j - warp_from : (j - q_lo) / NT * 32 + lane);
+        queued += __popc(who);
+      }
+    };
+    auto collect_queued = [&] {
+      __syncwarp();
+      if (RESIDENT) return;
+      have = queued <= QCAP ? 0 : ECAP + 1;
+      if (have) return;
+      for (int i0 = 0; i0 < queued; i0 += 128 / EPC) {
+        float x[4];
+        int at[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int k = queue[min(i0 + lane / EPC + u * (32 / EPC), queued - 1)];
+          at[u] = EPC * (ONE_WALK ? warp_from + k : q_lo + wid * 32 + k / 32 * NT + k % 32) + lane % EPC;
+          x[u] = Logit<T>::get(reinterpret_cast<const T*>(g.base), at[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int id = at[u] - g.dc;
+          keep(x[u] >= x1 && i0 + lane / EPC + u * (32 / EPC) < queued && id >= 0 && id < a.V, x[u], at[u]);
+        }
+      }
+      __syncwarp();
+    };
+
+    // ---- max (ONE_WALK: of a sample, the first blocks of every warp's share)
+    float mx = -kInf, mn = kInf;
+    uint4 sample[ONE_WALK ? U : 1];
+    if constexpr (ONE_WALK) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = warp_from + 32 * u + lane;
+        sample[u] = make_uint4(Chunk<T>::NEG_INF, Chunk<T>::NEG_INF, Chunk<T>::NEG_INF, Chunk<T>::NEG_INF);
+        if (j < warp_to) sample[u] = load(j);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float f[EPC];
+        g.values(sample[u], warp_from + 32 * u + lane, f);
+        mx = fmaxf(mx, max_of(f));
+      }
+    } else {
+      walk([&](int j, const uint4& raw) {
+        float f[EPC];
+        g.values(raw, j, f);
+        mx = fmaxf(mx, max_of(f));
+#pragma unroll
+        for (int i = 0; i < EPC; ++i) mn = fminf(mn, f[i] > -3e37f ? f[i] : kInf);
+      });
+    }
     float m, lo, cut;
     {
       float grp = mx;
@@ -610,6 +711,42 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
         }
       }
     }
+    // ---- ONE_WALK: the sums relative to the sample's maximum, the queue, and the maximum itself
+    const float ref = m;
+    if constexpr (ONE_WALK) {
+      // Where the sample is much of the row, few logits of it lie above its cut.
+      x1 = cut > -kInf && 4 * 32 * U * NW > q_hi - q_lo ? cut - 0.27f * (m - cut) : cut;
+      cut = x1;
+      const bool may_temper = q.r != 1.f && !(q.k && q.k <= 8 * GROUPS);
+      auto body = [&](int j, const uint4& raw) {
+        float f[EPC];
+        g.values(raw, j, f);
+        const float c = max_of(f);
+        mx = fmaxf(mx, c);
+        sum_chunk(f, ref, may_temper);
+        collect(j, f, c >= x1 && c > -kInf);
+      };
+#pragma unroll
+      for (int u = 0; u < U; ++u) body(warp_from + 32 * u + lane, sample[u]);
+#pragma unroll 1
+      for (int j0 = warp_from + 32 * U; j0 < warp_to; j0 += 32 * U) {
+        uint4 raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int j = j0 + 32 * u + lane;
+          raw[u] = make_uint4(Chunk<T>::NEG_INF, Chunk<T>::NEG_INF, Chunk<T>::NEG_INF, Chunk<T>::NEG_INF);
+          if (j < warp_to) raw[u] = load(j);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) body(j0 + 32 * u + lane, raw[u]);
+      }
+      m = warp_max_r(mx);
+      cta_sync();  // the sample's maxima are read
+      if (lane == 0) sh.fred[0][wid] = m;
+      cta_sync();
+      m = warp_max_r(sh.fred[0][lane % NW]);
+      lo = -3.402823466e38f;  // not looked for: a row that needs it goes to the second pass
+    }
     // No logit below x_low has a weight: w > 0 needs (x - m) r > -22.2, and the
     // rest is room for the rounding of x_low. Masks are told from logits by
     // their size, which needs a range that ends above them.
@@ -620,15 +757,17 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
     // A warp's own row starts a little lower, and lower still for a top-k that
     // would end below (15510 x 1025, 12% of the rows with k = 200: 148 -> 129 us).
     const float further = PASS == kMarked ? (RESIDENT ? 1e30f : 0.27f) : NT == 32 ? (q.k > 64 ? 0.3f : 0.1f) : 0.f;
-    float x1 = fmaxf(cut - further * (m - cut), x_low);
+    x1 = fmaxf(ONE_WALK ? cut : cut - further * (m - cut), x_low);
     float per_x = fminf((float)NB / (m - x1), 3.402823466e38f);
     auto bin_of = [&](float x) { return min(NB - 1, __float2int_rz((m - x) * per_x)); };  // for x1 <= x <= m
     const bool finite = m > -kInf && m < kInf;
     const bool drawn = !q.bad && q.tau > 0.f && finite;
     const bool greedy = !q.bad && q.tau == 0.f && finite;
-    // A top-k of at most GROUPS ends above x1: the mass below is then not asked for.
-    const bool whole = drawn && !(q.k && q.k <= GROUPS);
-    const bool tempered = whole && x1 > x_low && q.r != 1.f;
+    // A top-k of at most GROUPS ends above x1: the mass below is then not asked
+    // for. A longer one most likely does: its row is left to the second pass if not.
+    const bool sure = q.k && q.k <= GROUPS;
+    const bool whole = drawn && !(q.k && q.k <= (ONE_WALK ? 8 * GROUPS : GROUPS));
+    const bool tempered = whole && (ONE_WALK || x1 > x_low) && q.r != 1.f;
     const bool floored = q.mp > 0.f;
     auto add_bins = [&](float x, uint32_t w) {
       if (w) {
@@ -639,96 +778,29 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
       }
     };
 
+
     // ---- weigh
-    float s = 0.f, st = 0.f;
     int first = INT_MAX, odd = 0;
-    const float2 neg_m = make_float2(-m, -m), l2e = make_float2(kLog2e, kLog2e), rr = make_float2(q.r, q.r);
-    int queued = 0;
-    int have = 0;  // logits >= x1 of this warp's walk; more than fit: the walk itself is repeated for them
-    auto keep = [&](bool high, float x, int at) {
-      const unsigned who = __ballot_sync(0xffffffffu, high);
-      const int slot = have + __popc(who & ((1u << lane) - 1u));
-      if (high && slot < ECAP) {
-        high_x[slot] = x;
-        high_at[slot] = at;
-      }
-      have += __popc(who);
-    };
-    // Of a short row every logit is looked at in the walk; of a long one, chunks
-    // with a high logit are queued, so that the walk pays a ballot a chunk.
-    auto collect = [&](int j, const float (&f)[EPC], bool high) {
-      const unsigned who = __ballot_sync(0xffffffffu, high);
-      if (RESIDENT) {
-        if (who) {
-#pragma unroll
-          for (int i = 0; i < EPC; ++i) keep(high && f[i] >= x1, f[i], EPC * j + i);
+    if constexpr (!ONE_WALK) {
+      walk_back([&](int j, const uint4& raw) {
+        float f[EPC];
+        g.values(raw, j, f);
+        const float c = max_of(f);
+        sum_chunk(f, ref, tempered);
+        collect(j, f, drawn && c >= x1);
+        if (greedy && c == m) {
+  #pragma unroll
+          for (int i = 0; i < EPC; ++i)
+            if (f[i] == m) first = min(first, g.id(j, i));
         }
-      } else {
-        const int at = queued + __popc(who & ((1u << lane) - 1u));
-        if (high && at < QCAP) queue[at] = (uint16_t)((j - q_lo) / NT * 32 + lane);
-        queued += __popc(who);
-      }
-    };
-    auto collect_queued = [&] {
-      __syncwarp();
-      if (RESIDENT) return;
-      have = queued <= QCAP ? 0 : ECAP + 1;
-      if (have) return;
-      for (int i0 = 0; i0 < queued; i0 += 128 / EPC) {
-        float x[4];
-        int at[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int k = queue[min(i0 + lane / EPC + u * (32 / EPC), queued - 1)];
-          at[u] = EPC * (q_lo + wid * 32 + k / 32 * NT + k % 32) + lane % EPC;
-          x[u] = Logit<T>::get(reinterpret_cast<const T*>(g.base), at[u]);
+        if (!finite) {
+  #pragma unroll
+          for (int i = 0; i < EPC; ++i) odd |= !(f[i] < kInf);
         }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int id = at[u] - g.dc;
-          keep(x[u] >= x1 && i0 + lane / EPC + u * (32 / EPC) < queued && id >= 0 && id < a.V, x[u], at[u]);
-        }
-      }
-      __syncwarp();
-    };
-    walk_back([&](int j, const uint4& raw) {
-      float f[EPC];
-      g.values(raw, j, f);
-      const float c = max_of(f);
-      float2 d[EPC / 2], e[EPC / 2];
-#pragma unroll
-      for (int i = 0; i < EPC / 2; ++i) d[i] = __fadd2_rn(make_float2(f[2 * i], f[2 * i + 1]), neg_m);
-      auto sum_of_ex2 = [&]() {
-#pragma unroll
-        for (int i = 0; i < EPC / 2; ++i) {
-          e[i] = __fmul2_rn(e[i], l2e);
-          e[i] = make_float2(ex2_approx(e[i].x), ex2_approx(e[i].y));
-        }
-#pragma unroll
-        for (int o = 1; o < EPC / 2; o *= 2)
-#pragma unroll
-          for (int i = 0; i + o < EPC / 2; i += 2 * o) e[i] = __fadd2_rn(e[i], e[i + o]);
-        return e[0].x + e[0].y;
-      };
-#pragma unroll
-      for (int i = 0; i < EPC / 2; ++i) e[i] = d[i];
-      s += sum_of_ex2();
-      if (tempered) {
-#pragma unroll
-        for (int i = 0; i < EPC / 2; ++i) e[i] = __fmul2_rn(d[i], rr);
-        st += sum_of_ex2();
-      }
-      collect(j, f, drawn && c >= x1);
-      if (greedy && c == m) {
-#pragma unroll
-        for (int i = 0; i < EPC; ++i)
-          if (f[i] == m) first = min(first, g.id(j, i));
-      }
-      if (!finite) {
-#pragma unroll
-        for (int i = 0; i < EPC; ++i) odd |= !(f[i] < kInf);
-      }
-    });
+      });
+    } else {
+      odd = m == kInf;
+    }
     // min-p: the last bin with a logit that stays, and whether one above x1 does not
     int floor_bin = -1, below = 0;
     auto bin_high = [&] {
@@ -771,10 +843,22 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
         sh.ired[2][wid] = below;
       }
     };
-    bin_high();
+    if (!ONE_WALK || drawn) {
+      bin_high();
+    } else {
+      collect_queued();
+      if (greedy) {
+        if (have > ECAP && lane == 0) sh.crowded = 1;
+        for (int i = lane; i < min(have, ECAP); i += 32)
+          if (high_x[i] == m) first = min(first, high_at[i] - g.dc);
+      }
+    }
     // A NaN, or +inf under a finite maximum, makes the sum NaN.
     s = warp_sum(s);
     odd |= finite && !(s < kInf);
+    // What one walk cannot settle: a sample without a logit, a maximum so far
+    // above the sample's that the sums overflow.
+    if (ONE_WALK && lane == 0 && (!(ref > -kInf) || s == kInf || (tempered && !(st < kInf)))) sh.crowded = 1;
     odd = __any_sync(0xffffffffu, odd);
     if (tempered) st = warp_sum(st);
     if (greedy) {
@@ -826,9 +910,13 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
           sum += sh.part_sum[o];
         }
         const bool ok = greedy && !bits;
-        if (q.bad || bits) report(a.d_status, q.bad ? DS_DEV_ERR_PARAM : DS_DEV_ERR_LOGITS);
-        a.out_tokens[n] = ok ? sh.first_id : -1;
-        a.out_logprobs[n] = ok ? m - (m + logf(sum)) : __int_as_float(0x7fffffff);
+        if (ONE_WALK && !q.bad && sh.crowded) {
+          a.out_tokens[n] = kStreamMark;
+        } else {
+          if (q.bad || bits) report(a.d_status, q.bad ? DS_DEV_ERR_PARAM : DS_DEV_ERR_LOGITS);
+          a.out_tokens[n] = ok ? sh.first_id : -1;
+          a.out_logprobs[n] = ok ? m - (ref + logf(sum)) : __int_as_float(0x7fffffff);
+        }
       }
       continue;  // the partials are read before this CTA meets the others again
     }
@@ -913,7 +1001,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
       const int nb = NB;
       const u64 known = sh.pm[nb - 1];
       const uint32_t count = sh.pc[nb - 1];
-      const bool complete = !whole || x1 <= x_low;  // nothing that is asked for lies below x1
+      const bool complete = sure || x1 <= x_low;  // nothing that is asked for lies below x1
       if (sh.crowded) return (int)kExact;
       uint32_t mark = 0;  // lane l: bins [32 l, 32 l + 32)
       auto mark_range = [&](int b0, int b1) {
@@ -996,8 +1084,16 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
         odd = __any_sync(0xffffffffu, in && sh.part_odd[lane]);
       }
       if (lane == 0) {
-        const double t = (double)(tempered ? st : s) * (double)kSfOne;
-        const double slack = t * (kSfSlack + kSfRounding * (21 + (q_hi - q_lo + NT - 1) / NT)) + 0.5 * (double)a.V;
+        // relative to the maximum: of one walk, ref is the sample's
+        double t = (double)(tempered ? st : s) * (double)kSfOne, rel = kSfSlack;
+        if (ONE_WALK) {
+          // The exponents are taken from ref: three roundings of (x - ref) r beside two of (x - m) r, both
+          // 15 at most in the mean (ln V), (m - ref) r further off here; and the factor's own.
+          const double off = (double)((m - ref) * q.r);
+          t *= exp(-off);
+          rel += kSfRounding * (2 * 15 + 3 * (15 + off) + off);
+        }
+        const double slack = t * (rel + kSfRounding * (21 + (q_hi - q_lo + NT - 1) / NT)) + 0.5 * (double)a.V;
         sh.t_lo = t > slack ? (u64)(t - slack) : 0;
         sh.t_hi = (u64)(t + slack) + 1;
         sh.known_sum = s;
@@ -1018,7 +1114,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
             sh.known_below = be;
           }
           __syncwarp();
-          int c = sh.known_odd ? (int)kDone : decide(weighed);
+          int c = sh.known_odd && !(ONE_WALK && sh.crowded) ? (int)kDone : decide(weighed);
           if (PASS == kFirst && c != kDone && c != kGather) c = kMark;
           __syncwarp();
           for (int o = 1; o < cs; ++o) {
@@ -1122,7 +1218,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
     if (rank != 0) continue;
 
     // ---- rank 0 answers
-    const float lse = m + logf(sh.known_sum);
+    const float lse = ref + logf(sh.known_sum);
     if (PASS == kFirst && command == kMark) {
       if (tid == 0) a.out_tokens[n] = kStreamMark;
     } else if (command == kDone) {
@@ -1358,7 +1454,7 @@ static cudaError_t launch_filtered(const FilteredArgs& a, cudaStream_t st) {
     int cs = 1;
     while (cs < 8 && a.n * cs * 2LL <= sms && (long long)a.V * sizeof(T) >= cs * 2 * kSfSliceMin) cs *= 2;
     if (cs == 1) {
-      e = launch_fast<T, 512, 1024, 512, 128, 384, 256, false, kFirst>(a, 1, st, &refused);
+      e = launch_fast<T, 512, 1024, 512, 32, 384, 256, false, kFirst>(a, 1, st, &refused);
       if (refused || e != cudaSuccess) return refused ? cudaErrorLaunchOutOfResources : e;
       e = launch_fast<T, 512, 1024, 512, 128, 384, 256, false, kMarked>(a, 8, st, &refused);
     } else {
