@@ -407,7 +407,7 @@ struct SfShared {
   uint16_t queue[NT / 32][QCAP > 0 ? QCAP : 1];  // each warp's chunks that hold a logit >= x1, by their place in its walk
   u64 full;                          // the slice's copy is done
   u64 red[NT / 32];
-  float fred[3][NT / 32], sred[2][NT / 32];
+  float fred[3][NT / 32], sred[2][NT / 32], groups[32];
   int ired[3][NT / 32];
   uint32_t marks[NB / 32];
   // each CTA's partials, pushed by it to everyone (max) or to rank 0 (weigh)
@@ -420,6 +420,7 @@ struct SfShared {
   float known_sum;
   int known_odd, known_floor, known_below;
   int kb, again, crowded;
+  float hint;  // a lower cut that the boundary most likely lies above
   u64 found[4];
   int slot;
 };
@@ -480,6 +481,7 @@ template <typename T, int NT, int NB, int CAP, int GROUPS, int QCAP, int ECAP, b
 __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT) k_sample_filtered(FilteredArgs a, int slice_chunks) {
   constexpr int EPC = Chunk<T>::N, NW = NT / 32, U = RESIDENT ? 1 : 4;
   constexpr bool ONE_WALK = PASS == kFirst && !RESIDENT;  // one CTA a row
+  static_assert(!ONE_WALK || GROUPS == 32, "a warp picks among the groups' maxima");
   using Shared = SfShared<NT, NB, CAP, QCAP>;
   extern __shared__ uint4 slice[];
   __shared__ Shared sh;
@@ -504,13 +506,26 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
     else
       cl.sync();
   };
+  pdl_wait();
+  pdl_release();
+  // The first row from n on that this cluster has to do: 32 are looked at at a time.
+  auto row_from = [&](long long n) {
+    if constexpr (PASS == kMarked) {
+      for (; n < a.n; n += 32 * n_clusters) {
+        const long long i = n + lane * n_clusters;
+        const unsigned marked = __ballot_sync(0xffffffffu, i < a.n && a.out_tokens[i] == kStreamMark);
+        if (marked) return n + (__ffs(marked) - 1) * n_clusters;
+      }
+    }
+    return n;
+  };
+  long long next = row_from(cid);
+  if (PASS == kMarked && next >= a.n) return;  // nothing marked among this cluster's rows: all of its CTAs leave
   if (tid == 0) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(sf_smem(&sh.full)) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   sync();  // every CTA of the cluster runs before any writes into another's shared memory
-  pdl_wait();
-  pdl_release();
 
   // This CTA's slice of a row: chunks [q_lo, q_hi).
   auto row_of = [&](long long n) { return Row<T>(static_cast<const T*>(a.x) + n * a.ld, a.V); };
@@ -532,18 +547,6 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
             : "memory");
     }
   };
-  // The first row from n on that this cluster has to do: 32 are looked at at a time.
-  auto row_from = [&](long long n) {
-    if constexpr (PASS == kMarked) {
-      for (; n < a.n; n += 32 * n_clusters) {
-        const long long i = n + lane * n_clusters;
-        const unsigned marked = __ballot_sync(0xffffffffu, i < a.n && a.out_tokens[i] == kStreamMark);
-        if (marked) return n + (__ffs(marked) - 1) * n_clusters;
-      }
-    }
-    return n;
-  };
-  long long next = row_from(cid);
   start_copy(next);
 
   uint32_t parity = 0;
@@ -673,9 +676,9 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
         for (int i = 0; i < EPC; ++i) mn = fminf(mn, f[i] > -3e37f ? f[i] : kInf);
       });
     }
-    float m, lo, cut;
+    float m, lo, cut, grp;
     {
-      float grp = mx;
+      grp = mx;
 #pragma unroll
       for (int o = 1; o < NT / GROUPS; o <<= 1) grp = fmaxf(grp, __shfl_xor_sync(0xffffffffu, grp, o));
       m = warp_max_r(mx);
@@ -714,6 +717,16 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
     // ---- ONE_WALK: the sums relative to the sample's maximum, the queue, and the maximum itself
     const float ref = m;
     if constexpr (ONE_WALK) {
+      // The cut is the third least of the groups' maxima: the least scatters so much
+      // that one row in sixty had more logits above it than the lists hold.
+      if (lane % (NT / GROUPS) == 0) sh.groups[tid / (NT / GROUPS)] = grp;
+      cta_sync();
+      float v = sh.groups[lane];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        cut = warp_min_r(v);
+        if (__ffs(__ballot_sync(0xffffffffu, v == cut)) - 1 == lane) v = kInf;
+      }
       // Where the sample is much of the row, few logits of it lie above its cut.
       x1 = cut > -kInf && 4 * 32 * U * NW > q_hi - q_lo ? cut - 0.27f * (m - cut) : cut;
       cut = x1;
@@ -752,12 +765,13 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
     // their size, which needs a range that ends above them.
     const float lowest = (m - 24.f * q.tau) - fabsf(m) * 2.4e-7f;
     const float x_low = lowest > -3e37f ? fmaxf(fminf(lo, m), lowest) : fmaxf(lowest, -3.402823466e38f);
-    // The first cut; for a row of the second pass, of which most lie below it, the
-    // next one, or no cut where the row is short.
+    // The first cut; none for a short row of the second pass.
     // A warp's own row starts a little lower, and lower still for a top-k that
     // would end below (15510 x 1025, 12% of the rows with k = 200: 148 -> 129 us).
-    const float further = PASS == kMarked ? (RESIDENT ? 1e30f : 0.27f) : NT == 32 ? (q.k > 64 ? 0.3f : 0.1f) : 0.f;
-    x1 = fmaxf(ONE_WALK ? cut : cut - further * (m - cut), x_low);
+    const float further = PASS == kMarked ? (RESIDENT ? 1e30f : 0.f) : NT == 32 ? (q.k > 64 ? 0.3f : 0.1f) : 0.f;
+    x1 = ONE_WALK ? cut : cut - further * (m - cut);
+    if (PASS == kMarked && !RESIDENT) x1 = fminf(x1, a.out_logprobs[n]);  // the first pass's hint, +inf for none
+    x1 = fmaxf(x1, x_low);
     float per_x = fminf((float)NB / (m - x1), 3.402823466e38f);
     auto bin_of = [&](float x) { return min(NB - 1, __float2int_rz((m - x) * per_x)); };  // for x1 <= x <= m
     const bool finite = m > -kInf && m < kInf;
@@ -765,7 +779,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
     const bool greedy = !q.bad && q.tau == 0.f && finite;
     // A top-k of at most GROUPS ends above x1: the mass below is then not asked
     // for. A longer one most likely does: its row is left to the second pass if not.
-    const bool sure = q.k && q.k <= GROUPS;
+    const bool sure = q.k && q.k <= (ONE_WALK ? GROUPS - 2 : GROUPS);
     const bool whole = drawn && !(q.k && q.k <= (ONE_WALK ? 8 * GROUPS : GROUPS));
     const bool tempered = whole && (ONE_WALK || x1 > x_low) && q.r != 1.f;
     const bool floored = q.mp > 0.f;
@@ -912,6 +926,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
         const bool ok = greedy && !bits;
         if (ONE_WALK && !q.bad && sh.crowded) {
           a.out_tokens[n] = kStreamMark;
+          a.out_logprobs[n] = kInf;
         } else {
           if (q.bad || bits) report(a.d_status, q.bad ? DS_DEV_ERR_PARAM : DS_DEV_ERR_LOGITS);
           a.out_tokens[n] = ok ? sh.first_id : -1;
@@ -1002,6 +1017,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
       const u64 known = sh.pm[nb - 1];
       const uint32_t count = sh.pc[nb - 1];
       const bool complete = sure || x1 <= x_low;  // nothing that is asked for lies below x1
+      if (PASS == kFirst && lane == 0) sh.hint = kInf;  // none
       if (sh.crowded) return (int)kExact;
       uint32_t mark = 0;  // lane l: bins [32 l, 32 l + 32)
       auto mark_range = [&](int b0, int b1) {
@@ -1020,6 +1036,22 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
         weighed = true;
         __syncwarp();
       }
+      // Goes on below x1: with what mass missing, by the fall of the mass from one
+      // quarter of the bins to the next.
+      auto lower = [&](u64 target) {
+        if (PASS == kFirst && !RESIDENT) {
+          const float q3 = (float)(sh.pm[NB * 3 / 4 - 1] - sh.pm[NB / 2 - 1]), q4 = (float)(known - sh.pm[NB * 3 / 4 - 1]);
+          const float fall = fminf(q4 / q3, 0.98f);
+          float missing = 1.2f * (float)(target - known), step = q4;
+          int quarters = 1;
+          for (; quarters < 24 && missing > 0.f; ++quarters) {
+            step *= fall;
+            missing -= step;
+          }
+          if (lane == 0) sh.hint = missing > 0.f ? -kInf : x1 - 0.25f * (float)quarters * (m - x1);
+        }
+        return (int)kLower;
+      };
       u64 t_lo = sh.t_lo, t_hi = sh.t_hi;  // bounds of the kept mass
       bool loose = !weighed;               // they differ by what is not known of the row's mass
       int kb = -1;
@@ -1036,7 +1068,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
       }
       if (q.p < 1.f) {
         const u64 n_hi = need_of(q.p, t_hi), n_lo = t_lo == t_hi ? n_hi : need_of(q.p, t_lo);
-        if (n_hi > known) return complete ? (int)kExact : (int)kLower;
+        if (n_hi > known) return complete ? (int)kExact : lower(n_hi);
         const int b0 = warp_lower_bound<u64>(sh.pm, nb, n_lo > 0 ? n_lo : 1, lane);
         const int b1 = n_lo == n_hi ? b0 : warp_lower_bound<u64>(sh.pm, nb, n_hi, lane);
         if (loose && light(b1, n_hi - n_lo)) return (int)kWeigh;
@@ -1059,7 +1091,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
         }
       }
       const u64 d_hi = target_of(q.u, t_hi), d_lo = t_lo == t_hi ? d_hi : target_of(q.u, t_lo);
-      if (d_hi >= known) return complete ? (int)kExact : (int)kLower;
+      if (d_hi >= known) return complete ? (int)kExact : lower(d_hi + 1);
       const int b0 = warp_lower_bound<u64>(sh.pm, nb, d_lo + 1, lane);
       const int b1 = d_lo == d_hi ? b0 : warp_lower_bound<u64>(sh.pm, nb, d_hi + 1, lane);
       if (loose && light(b1, d_hi - d_lo)) return (int)kWeigh;
@@ -1220,7 +1252,10 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
     // ---- rank 0 answers
     const float lse = ref + logf(sh.known_sum);
     if (PASS == kFirst && command == kMark) {
-      if (tid == 0) a.out_tokens[n] = kStreamMark;
+      if (tid == 0) {
+        a.out_tokens[n] = kStreamMark;
+        a.out_logprobs[n] = sh.hint;
+      }
     } else if (command == kDone) {
       if (tid == 0) {
         report(a.d_status, DS_DEV_ERR_LOGITS);
@@ -1354,11 +1389,11 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
           if (lane == 0) {
             sh.again = at != lo_at;
             const u64 e = sh.list[at];
-            a.out_tokens[n] = PASS == kFirst && at != lo_at ? kStreamMark : (int)(0xffffffffu - (uint32_t)e);
+            a.out_tokens[n] = PASS == kFirst && RESIDENT && at != lo_at ? kStreamMark : (int)(0xffffffffu - (uint32_t)e);
             a.out_logprobs[n] = Logit<T>::value((uint32_t)(e >> 32)) - lse;
           }
         }
-        if (PASS == kFirst) break;
+        if (PASS == kFirst && RESIDENT) break;
         cta_sync();
         if (!sh.again) break;
         // the bounds fall on two logits: weigh the whole row here
@@ -1403,7 +1438,7 @@ cudaError_t launch_fast(const FilteredArgs& a, int cs, cudaStream_t st, bool* re
   cfg.numAttrs = cs == 1 ? 1 : 2;
   const void* site = reinterpret_cast<const void*>(kern);
   const int ok = cached(site, -1, [&](int) {
-    const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 << 10);
+    const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 << 10);
     if (r != cudaSuccess) (void)cudaGetLastError();
     return r == cudaSuccess ? 1 : 0;
   });
@@ -1423,10 +1458,10 @@ cudaError_t launch_fast(const FilteredArgs& a, int cs, cudaStream_t st, bool* re
   }
   // Marked rows are few and fall anywhere: short shares, handed out as clusters
   // come free. A CTA per short row (15510 x 1025: the pass took 88 us with a
-  // resident grid, 41 us so); three shares per resident cluster for long ones,
-  // whose empty CTAs cost more (256 x 248320, one marked row / a tenth marked:
-  // 66 / 174 us with one share, 71 / 144 with three, 81 / 135 with eight).
-  const long long most = PASS != kMarked ? fit : RESIDENT ? 1ll << 20 : 3ll * fit;
+  // resident grid, 41 us so); eight shares per resident cluster for long ones,
+  // whose empty CTAs cost more (256 x 248320, none / an eighth marked: 49 / 144
+  // us with three shares, 52 / 123 us with eight).
+  const long long most = PASS != kMarked ? fit : RESIDENT ? 1ll << 20 : 8ll * fit;
   const long long clusters = a.n < most ? a.n : most;
   cfg.gridDim = dim3((unsigned)(clusters * cs));
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, chunks);
@@ -1456,15 +1491,15 @@ static cudaError_t launch_filtered(const FilteredArgs& a, cudaStream_t st) {
     if (cs == 1) {
       e = launch_fast<T, 512, 1024, 512, 32, 384, 256, false, kFirst>(a, 1, st, &refused);
       if (refused || e != cudaSuccess) return refused ? cudaErrorLaunchOutOfResources : e;
-      e = launch_fast<T, 512, 1024, 512, 128, 384, 256, false, kMarked>(a, 8, st, &refused);
+      e = launch_fast<T, 512, 1024, 512, 128, 384, 512, false, kMarked>(a, 8, st, &refused);
     } else {
-      e = launch_fast<T, 512, 1024, 512, 128, 384, 256, false, kOnce>(a, cs, st, &refused);
+      e = launch_fast<T, 512, 1024, 512, 128, 384, 512, false, kOnce>(a, cs, st, &refused);
     }
     if (refused) {
       // no cluster of that size fits beside another program's work: a CTA per row does
       refused = false;
-      e = cs == 1 ? launch_fast<T, 512, 1024, 512, 128, 384, 256, false, kMarked>(a, 1, st, &refused)
-                  : launch_fast<T, 512, 1024, 512, 128, 384, 256, false, kOnce>(a, 1, st, &refused);
+      e = cs == 1 ? launch_fast<T, 512, 1024, 512, 128, 384, 512, false, kMarked>(a, 1, st, &refused)
+                  : launch_fast<T, 512, 1024, 512, 128, 384, 512, false, kOnce>(a, 1, st, &refused);
     }
   }
   return refused ? cudaErrorLaunchOutOfResources : e;
