@@ -11,9 +11,9 @@
  * and the calls around them: ds_sample_ex (per-request ratios and iterations,
  * keep-ties mode), ds_reveal (confidence ranking and reveal), ds_merge_triples
  * (vocabulary-shard merge) and ds_log_softmax (dense log-probabilities); and the
- * serving head: ds_quantize_rows, ds_pack_i8 and ds_linear_i8 (hidden states to
- * logits through an 8-bit vocabulary projection) and ds_sample_filtered (logits
- * to tokens by temperature, top-k, top-p and min-p). All are
+ * serving head: ds_quantize_rows, ds_pack_i8, ds_linear_i8 and ds_head_i8 (hidden
+ * states to logits through an 8-bit vocabulary projection) and ds_sample_filtered
+ * (logits to tokens by temperature, top-k, top-p and min-p). All are
  * asynchronous on the caller's CUDA stream, allocate nothing and keep no state
  * between calls beyond a process-wide count of kernel launches
  * (ds_launch_count).
@@ -392,6 +392,26 @@ int64_t ds_linear_i8_workspace(int32_t n, int32_t N, int32_t K);
 ds_status ds_linear_i8(const int8_t* a, int64_t lda, const float* a_scale, const void* packed, const float* w_scale,
                        int32_t n, int32_t N, int32_t K, void* out, int32_t out_dtype, int64_t ldo, void* workspace,
                        int64_t workspace_bytes, uint32_t* d_status, void* stream);
+
+/* Bytes of workspace that ds_head_i8 needs for these sizes (0: arguments out of
+ * range). Host-only, no CUDA call. */
+int64_t ds_head_i8_workspace(int32_t n, int32_t N, int32_t K);
+
+/*
+ * ds_head_i8 -- hidden states to logits: ds_quantize_rows, then ds_linear_i8 on
+ * its result, bit for bit, without the int8 rows in between.
+ *
+ * Arguments as of those two calls (x [n][K] of dtype, rows ld apart; gain [K] or
+ * NULL with eps; packed and w_scale of an [N][K] weight; out [n][N] of out_dtype,
+ * rows ldo apart). workspace: device, workspace_bytes >= ds_head_i8_workspace(n,
+ * N, K), 128-byte aligned, contents not kept between calls. A row with a NaN or
+ * an infinity gives a row of NaN. d_status: DS_DEV_ERR_TIMEOUT, or NULL.
+ * Returns DS_OK, DS_ERR_INVALID_ARG, DS_ERR_UNSUPPORTED (K, ld or ldo too large)
+ * or DS_ERR_CUDA.
+ */
+ds_status ds_head_i8(const void* x, int32_t dtype, int32_t n, int32_t K, int64_t ld, const float* gain, float eps,
+                     const void* packed, const float* w_scale, int32_t N, void* out, int32_t out_dtype, int64_t ldo,
+                     void* workspace, int64_t workspace_bytes, uint32_t* d_status, void* stream);
 
 /* Static description of a status code. Never NULL. */
 const char* ds_status_string(ds_status s);

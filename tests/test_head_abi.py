@@ -73,6 +73,28 @@ def test_pack_and_linear(lib):
     assert call(ldo=(1 << 40) + 1) == UNSUPPORTED
 
 
+def test_head_i8(lib):
+    n, N, K = 20, 1000, 512
+    need = lib.ds_head_i8_workspace(n, N, K)
+    assert need > lib.ds_linear_i8_workspace(n, N, K)
+
+    def call(x=FAKE, dtype=BF16, n=n, K=K, ld=K, gain=None, eps=1e-6, p=FAKE, sw=FAKE, N=N, out=FAKE, out_dtype=BF16, ldo=N,
+             ws=FAKE, wb=1 << 40, st=None):
+        return lib.ds_head_i8(x, dtype, n, K, ld, gain, eps, p, sw, N, out, out_dtype, ldo, ws, wb, st, None)
+
+    assert call(n=0) == OK
+    for bad in (dict(n=-1), dict(N=0), dict(K=0), dict(ld=K - 1), dict(ldo=N - 1), dict(dtype=4), dict(out_dtype=-1),
+                dict(x=None), dict(p=None), dict(sw=None), dict(out=None), dict(x=ODD), dict(x=HALF, dtype=F32),
+                dict(gain=HALF), dict(gain=FAKE, eps=-1.0), dict(sw=HALF), dict(st=HALF), dict(out=ODD),
+                dict(out=HALF, out_dtype=F32), dict(p=ctypes.c_void_p(0x100008)), dict(ws=None), dict(wb=need - 1),
+                dict(ws=ctypes.c_void_p(0x100010))):
+        assert call(**bad) == INVALID, bad
+    assert call(K=_lib.DS_LINEAR_MAX_K + 1, ld=1 << 20) == UNSUPPORTED
+    assert call(ld=(1 << 40) + 1) == UNSUPPORTED
+    for bad in ((0, 5, 5), (5, 0, 5), (5, 5, 0), (5, 5, _lib.DS_LINEAR_MAX_K + 1)):
+        assert pkg.head_i8_workspace(*bad) == 0
+
+
 def test_sizes(lib):
     assert pkg.packed_i8_bytes(1, 1) == 128 * 128
     assert pkg.packed_i8_bytes(129, 300) == 256 * 384
@@ -125,6 +147,18 @@ def test_wrappers_refuse_on_the_gpu():
         args.update(bad)
         with pytest.raises(ValueError):
             pkg.linear_i8(**args)
+    with pytest.raises(ValueError):
+        pkg.linear_i8(a, None, p)
+    with pytest.raises(ValueError):
+        pkg.linear_i8(a, v, p, dtype=torch.float16)
+    head = pkg.Int8Head(w, sw)
+    for bad in (x[:, :15], x.half(), x[:, ::2], x.cpu()):
+        with pytest.raises(ValueError):
+            head.logits(bad)
+    with pytest.raises(ValueError):
+        head.logits(x, out=torch.empty((4, 7), device=dev))
+    with pytest.raises(ValueError):
+        pkg.Int8Head(w, sw, gain=v)
     with pytest.raises(ValueError):
         pkg.quantize_rows(x, gain=v)
     with pytest.raises(ValueError):

@@ -236,6 +236,45 @@ def test_head_close_to_the_unquantised_product(n, N, K):
     assert float((lp.double() - want_lp).abs().max()) <= 1e-4
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,N,K,norm", [(1, 1025, 512, True), (3, 300, 77, False), (17, 4097, 1000, True),
+                                        (40, 700, 8200, True), (130, 1025, 2049, False), (300, 513, 9001, True)])
+def test_head_is_quantise_then_product(n, N, K, norm, dtype):
+    """One call, or quantised rows and then the product: the same bits, whatever the workspace held."""
+    dev = _dev()
+    g = torch.Generator().manual_seed(n + K)
+    x = (torch.randn((n, K), generator=g) * 2).to(DT[dtype]).to(dev)
+    if n > 2:
+        x[1] = 0
+        x[2, K // 2] = math.nan
+    gain = (1 + 0.1 * torch.randn((K,), generator=g)).to(dev) if norm else None
+    _, _, w, sw = _operands(1, N, K, 5)
+    head = pkg.Int8Head(w, sw, gain=gain, eps=1e-5)
+    q, scale = pkg.quantize_rows(x, gain=gain, eps=1e-5)
+    want = pkg.linear_i8(q, scale, head.weight, dtype=torch.float32)
+    junk = torch.full((pkg.head_i8_workspace(n, N, K) // 4 + 64,), math.nan, device=dev)
+    del junk  # the next workspace is likely these bytes
+    got = head.logits(x, dtype=torch.float32)
+    assert torch.equal(torch.nan_to_num(got, nan=123.0), torch.nan_to_num(want, nan=123.0))
+    assert bool(torch.isnan(got[2]).all()) if n > 2 else bool(torch.isfinite(got).all())
+
+
+def test_head_strided_and_other_stream():
+    dev = _dev()
+    g = torch.Generator().manual_seed(8)
+    buf = torch.randn((9, 131), generator=g).to(torch.bfloat16).to(dev)
+    x = buf[:, 1:128]
+    _, _, w, sw = _operands(1, 500, 127, 6)
+    head = pkg.Int8Head(w, sw)
+    want = head.logits(x.contiguous())
+    assert torch.equal(head.logits(x), want)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = head.logits(x, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
+
+
 def test_head_reports_a_bad_hidden_state():
     dev = _dev()
     g = torch.Generator().manual_seed(4)

@@ -26,7 +26,8 @@ DS_LINEAR_MAX_K = 131071
 
 EXPORTED = ("ds_sample", "ds_greedy_lse", "ds_status_string", "ds_top_k", "ds_merge_triples", "ds_log_softmax",
             "ds_reveal", "ds_sample_ex", "ds_launch_count", "ds_sample_filtered", "ds_quantize_rows",
-            "ds_packed_i8_bytes", "ds_pack_i8", "ds_linear_i8_workspace", "ds_linear_i8")
+            "ds_packed_i8_bytes", "ds_pack_i8", "ds_linear_i8_workspace", "ds_linear_i8", "ds_head_i8_workspace",
+            "ds_head_i8")
 DS_FLAG_KEEP_TIES = 1
 DS_FLAG_SKIP_EXACT_PASS = 2
 DS_MARKED = -2
@@ -84,6 +85,10 @@ def load(path: str = LIB_PATH):
     L.ds_linear_i8_workspace.restype = i64
     L.ds_linear_i8.argtypes = [vp, i64, vp, vp, vp, i32, i32, i32, vp, i32, i64, vp, i64, vp, vp]
     L.ds_linear_i8.restype = ctypes.c_int
+    L.ds_head_i8_workspace.argtypes = [i32, i32, i32]
+    L.ds_head_i8_workspace.restype = i64
+    L.ds_head_i8.argtypes = [vp, i32, i32, i32, i64, vp, f32, vp, vp, i32, vp, i32, i64, vp, i64, vp, vp]
+    L.ds_head_i8.restype = ctypes.c_int
     _lib = L
     return L
 
@@ -196,6 +201,12 @@ def ds_reveal(scores, tokens, seq_lens, reveal_counts, canvas, revealed=None, d_
     return rc
 
 
+def raw_stream():
+    """Handle of the current stream of the current device, without making a stream object for it."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
 def _dtype_code(t):
     import torch
     if t.dtype == torch.bfloat16:
@@ -241,6 +252,32 @@ def packed_i8_bytes(N: int, K: int) -> int:
 
 def linear_i8_workspace(n: int, N: int, K: int) -> int:
     return int(load().ds_linear_i8_workspace(int(n), int(N), int(K)))
+
+
+def head_i8_workspace(n: int, N: int, K: int) -> int:
+    return int(load().ds_head_i8_workspace(int(n), int(N), int(K)))
+
+
+def ds_head_i8(x, packed, w_scale, out, workspace, N, gain=None, eps=1e-6, d_status=None, n=None, K=None, ld=None,
+               ldo=None, out_dtype=None, workspace_bytes=None, stream=None, check=True):
+    """Call ds_head_i8: x [n, K] bfloat16 or float32, packed / w_scale of an [N, K] weight, out [n, N] bfloat16 or
+    float32, workspace uint8 of ds_head_i8_workspace(n, N, K) bytes."""
+    if n is None:
+        n, K = x.shape
+    if ld is None:
+        ld = x.stride(0) if n > 1 else K
+    if ldo is None:
+        ldo = out.stride(0) if n > 1 else N
+    if out_dtype is None:
+        out_dtype = _dtype_code(out)
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    rc = load().ds_head_i8(x.data_ptr(), _dtype_code(x), n, K, ld, _ptr(gain), float(eps), _ptr(packed), _ptr(w_scale),
+                           N, _ptr(out), out_dtype, ldo, _ptr(workspace), workspace_bytes, _ptr(d_status),
+                           _stream(stream))
+    if check and rc != DS_OK:
+        raise DsError("ds_head_i8", rc)
+    return rc
 
 
 def ds_pack_i8(w, packed, N=None, K=None, ldw=None, stream=None, check=True):

@@ -282,7 +282,7 @@ ds_status ds_quantize_rows(const void* x, int32_t dtype, int32_t n, int32_t K, i
     return DS_ERR_INVALID_ARG;
   if (ld > (1LL << 40)) return DS_ERR_UNSUPPORTED;
   const cudaError_t e = ds::launch_quantize_rows(x, dtype == DS_DTYPE_F32, n, K, ld, gain, eps, out_q, out_scale,
-                                                 static_cast<cudaStream_t>(stream));
+                                                 nullptr, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DS_OK : DS_ERR_CUDA;
 }
 
@@ -298,6 +298,41 @@ ds_status ds_pack_i8(const int8_t* w, int32_t N, int32_t K, int64_t ldw, void* p
   if (K > DS_LINEAR_MAX_K || ldw > (1LL << 40)) return DS_ERR_UNSUPPORTED;
   const cudaError_t e =
       ds::launch_pack_i8(w, N, K, ldw, static_cast<uint8_t*>(packed), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DS_OK : DS_ERR_CUDA;
+}
+
+int64_t ds_head_i8_workspace(int32_t n, int32_t N, int32_t K) {
+  if (n < 1 || N < 1 || K < 1 || K > DS_LINEAR_MAX_K) return 0;
+  return ds::linear_i8_workspace(n, N, K) + (int64_t)n * 4;  // the rows' scales behind their tiles
+}
+
+ds_status ds_head_i8(const void* x, int32_t dtype, int32_t n, int32_t K, int64_t ld, const float* gain, float eps,
+                     const void* packed, const float* w_scale, int32_t N, void* out, int32_t out_dtype, int64_t ldo,
+                     void* workspace, int64_t workspace_bytes, uint32_t* d_status, void* stream) {
+  if (n < 0 || N < 1 || K < 1 || ld < K || ldo < N) return DS_ERR_INVALID_ARG;
+  if (dtype != DS_DTYPE_F32 && dtype != DS_DTYPE_BF16) return DS_ERR_INVALID_ARG;
+  if (out_dtype != DS_DTYPE_F32 && out_dtype != DS_DTYPE_BF16) return DS_ERR_INVALID_ARG;
+  if (gain && !(eps >= 0.f && eps < INFINITY)) return DS_ERR_INVALID_ARG;
+  if (K > DS_LINEAR_MAX_K || ld > (1LL << 40) || ldo > (1LL << 40)) return DS_ERR_UNSUPPORTED;
+  if (n == 0) return DS_OK;
+  if (!x || !packed || !w_scale || !out) return DS_ERR_INVALID_ARG;
+  if (((reinterpret_cast<uintptr_t>(gain) | reinterpret_cast<uintptr_t>(w_scale) |
+        reinterpret_cast<uintptr_t>(d_status)) & 3) ||
+      (reinterpret_cast<uintptr_t>(x) & (dtype == DS_DTYPE_F32 ? 3 : 1)) ||
+      (reinterpret_cast<uintptr_t>(packed) & 15) ||
+      (reinterpret_cast<uintptr_t>(out) & (out_dtype == DS_DTYPE_F32 ? 3 : 1)))
+    return DS_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < ds_head_i8_workspace(n, N, K) || (reinterpret_cast<uintptr_t>(workspace) & 127))
+    return DS_ERR_INVALID_ARG;
+  float* scale = reinterpret_cast<float*>(static_cast<char*>(workspace) + ds::linear_i8_workspace(n, N, K));
+  const ds::I8Tiles tiles = ds::linear_i8_tiles(n, N, K, workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = ds::launch_quantize_rows(x, dtype == DS_DTYPE_F32, n, K, ld, gain, eps, nullptr, scale, &tiles, st);
+  if (e == cudaSuccess) {
+    const ds::LinearArgs g = {nullptr, 0, scale, static_cast<const uint8_t*>(packed), w_scale, n, N, K, out, ldo,
+                              workspace, d_status};
+    e = ds::launch_linear_i8(g, out_dtype == DS_DTYPE_BF16, st);
+  }
   return e == cudaSuccess ? DS_OK : DS_ERR_CUDA;
 }
 

@@ -83,9 +83,19 @@ struct FilteredArgs {
 };
 cudaError_t launch_sample_filtered(const FilteredArgs& a, bool f32, cudaStream_t st);
 
-// Rows of x (optionally RMS-normalised) to int8 with one scale per row.
+// The left operand of the product of 8-bit integers as fp16: [row tile][block of
+// 64 inputs][row][128 bytes], 16-byte chunk c of row i at chunk c ^ (i & 7) (the
+// 128-byte swizzle of the matrix descriptors). Rows and inputs past the end are
+// zero: a zero weight does not cancel a NaN left in the workspace.
+struct I8Tiles {
+  void* out;
+  int rows, tiles, kb;  // rows of a tile, tiles, blocks of 64 inputs
+};
+
+// Rows of x (optionally RMS-normalised) to int8 with one scale per row: to q, or
+// as such tiles when given.
 cudaError_t launch_quantize_rows(const void* x, bool f32, int n, int K, int64_t ld, const float* gain, float eps,
-                                 int8_t* q, float* scale, cudaStream_t st);
+                                 int8_t* q, float* scale, const I8Tiles* tiles, cudaStream_t st);
 
 // The packed form of an int8 weight [N][K]: blocks of kPackRows channels x
 // kPackK inputs, 16 KB each, block (channels / kPackRows, inputs / kPackK) at
@@ -110,6 +120,8 @@ struct LinearArgs {
   uint32_t* d_status;
 };
 long long linear_i8_workspace(int n, int N, int K);
+I8Tiles linear_i8_tiles(int n, int N, int K, void* workspace);
+// With g.a null the workspace holds the tiles already.
 cudaError_t launch_linear_i8(const LinearArgs& a, bool bf16_out, cudaStream_t st);
 
 }  // namespace ds

@@ -42,14 +42,12 @@ __global__ void __launch_bounds__(256) k_pack_i8(const int8_t* w, int N, int K, 
   }
 }
 
-// The rows of a as fp16 in the order that the product reads: [row tile][block of
-// 64 inputs][row][128 bytes], 16-byte chunk c of row i at chunk c ^ (i & 7) (the
-// 128-byte swizzle of the matrix descriptors). Rows past n and inputs past K are
-// zero: a zero weight does not cancel a NaN left in the workspace.
-__global__ void __launch_bounds__(256) k_expand_i8(const int8_t* a, long long lda, int n, int K, int rows, int tiles,
-                                                   int kb64, uint4* out) {
+// The rows of a as the fp16 tiles that the product reads.
+__global__ void __launch_bounds__(256) k_expand_i8(const int8_t* a, long long lda, int n, int K, I8Tiles t) {
   pdl_wait();
   pdl_release();
+  const int rows = t.rows, tiles = t.tiles, kb64 = t.kb;
+  uint4* out = static_cast<uint4*>(t.out);
   const long long chunks = (long long)tiles * kb64 * rows * 8;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < chunks; i += (long long)gridDim.x * 256) {
     const int c = (int)(i & 7);
@@ -521,6 +519,11 @@ long long linear_i8_workspace(int n, int N, int K) {
   return (long long)p.tiles * p.rows * p.kb * kPackK * 2;
 }
 
+I8Tiles linear_i8_tiles(int n, int N, int K, void* workspace) {
+  const TcPlan p = tc_plan(n, N, K);
+  return {workspace, p.rows, p.tiles, 2 * p.kb};
+}
+
 cudaError_t launch_pack_i8(const int8_t* w, int N, int K, int64_t ldw, uint8_t* packed, cudaStream_t st) {
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorUnknown;
@@ -552,13 +555,16 @@ cudaError_t launch_linear_i8(const LinearArgs& g, bool bf16_out, cudaStream_t st
   cfg.attrs = attr;
   cfg.numAttrs = 1;
 
-  const long long chunks = (long long)p.tiles * 2 * p.kb * p.rows * 8, want = (chunks + 255) / 256;
-  cfg.gridDim = dim3((unsigned)(want < sms * 8LL ? want : sms * 8LL));
-  cfg.blockDim = dim3(256);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, k_expand_i8, g.a, (long long)g.lda, g.n, g.K, p.rows, p.tiles, 2 * p.kb,
-                                     static_cast<uint4*>(g.workspace));
-  if (e != cudaSuccess) return e;
-  note_launch();
+  cudaError_t e;
+  if (g.a) {
+    const long long chunks = (long long)p.tiles * 2 * p.kb * p.rows * 8, want = (chunks + 255) / 256;
+    cfg.gridDim = dim3((unsigned)(want < sms * 8LL ? want : sms * 8LL));
+    cfg.blockDim = dim3(256);
+    e = cudaLaunchKernelEx(&cfg, k_expand_i8, g.a, (long long)g.lda, g.n, g.K,
+                           linear_i8_tiles(g.n, g.N, g.K, g.workspace));
+    if (e != cudaSuccess) return e;
+    note_launch();
+  }
 
   auto kern = bf16_out ? k_linear_i8_tc<__nv_bfloat16> : k_linear_i8_tc<float>;
   const int attr_ok = cached(reinterpret_cast<const void*>(kern), -1, [&](int) {
