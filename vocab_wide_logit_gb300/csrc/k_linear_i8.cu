@@ -323,7 +323,9 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  pdl_wait();
+  // Launched while the kernel that makes the row tiles runs, which in turn started
+  // after everything before it on the stream was done: the weights are there, and
+  // only what that kernel writes is waited for.
   pdl_release();
 
   const int kb = p.kb;
@@ -355,6 +357,7 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
   } else if (warp == kTcEpi + kTcCvt + 1) {
     // ---- row tiles
     if (lane == 0) {
+      pdl_wait();
       uint32_t it = 0;
       bool ok = true;
       const uint8_t* base = static_cast<const uint8_t*>(g.workspace);
@@ -469,6 +472,7 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
     const int quad = warp & 3, half = warp >> 2;
     Ring rd;
     long long scales = -1;  // row tile whose scales are in shared memory
+    pdl_wait();
     for (long long t = blockIdx.x; t < n_tiles; t += gridDim.x) {
       const long long j = t / p.tiles * kPackRows + quad * 32 + lane;
       const long long tile = t % p.tiles, i0 = tile * p.rows;
