@@ -397,7 +397,7 @@ __device__ __noinline__ int row_exact(const T* p, int V, const RowParams& q, flo
 // row; an exact weight and an atomic only above x1.
 namespace {
 
-template <int NT, int NB, int CAP, int QCAP>  // QCAP 0: no queue
+template <int NT, int NB, int CAP, int QCAP, int CS>  // QCAP 0: no queue; CS: most CTAs of a cluster
 struct SfShared {
   uint32_t cnt[NB], lo[NB], hi[NB];  // this CTA's bins: count, and mass as two sums of 16-bit halves
   u64 pm[NB];                        // rank 0: mass through each bin
@@ -411,10 +411,10 @@ struct SfShared {
   int ired[3][NT / 32];
   uint32_t marks[NB / 32];
   // each CTA's partials, pushed by it to everyone (max) or to rank 0 (weigh)
-  float part_max[16], part_min[16], part_cut[16], part_sum[16];
-  float part_tempered[16];
-  u64 part_total[16];
-  int part_odd[16], part_floor[16], part_below[16];
+  float part_max[CS], part_min[CS], part_cut[CS], part_sum[CS];
+  float part_tempered[CS];
+  u64 part_total[CS];
+  int part_odd[CS], part_floor[CS], part_below[CS];
   int command, n_list, n_mine, mine_at, first_id;
   u64 t_lo, t_hi;  // bounds of the row's mass
   float known_sum;
@@ -478,11 +478,11 @@ __device__ __forceinline__ bool sf_wait(u64* bar, uint32_t parity) {
 }  // namespace
 
 template <typename T, int NT, int NB, int CAP, int GROUPS, int QCAP, int ECAP, bool RESIDENT, Pass PASS>
-__global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT) k_sample_filtered(FilteredArgs a, int slice_chunks) {
+__global__ void __launch_bounds__(NT, NT == 32 ? 28 : NT == 128 ? 6 : 1024 / NT) k_sample_filtered(FilteredArgs a, int slice_chunks) {
   constexpr int EPC = Chunk<T>::N, NW = NT / 32, U = RESIDENT ? 1 : 4;
   constexpr bool ONE_WALK = PASS == kFirst && !RESIDENT;  // one CTA a row
   static_assert(!ONE_WALK || GROUPS == 32, "a warp picks among the groups' maxima");
-  using Shared = SfShared<NT, NB, CAP, QCAP>;
+  using Shared = SfShared<NT, NB, CAP, QCAP, RESIDENT || ONE_WALK ? 1 : 8>;
   extern __shared__ uint4 slice[];
   __shared__ Shared sh;
   cg::cluster_group cl = cg::this_cluster();
@@ -492,8 +492,11 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
   Shared* lead = cl.map_shared_rank(&sh, 0);
   uint16_t* queue = sh.queue[wid];
   // behind the slice: the logits >= x1 of each warp's walk, and their places in the row's chunks
+  // (of a slice in shared memory the places alone, room for every logit of the walk)
   float* high_x = reinterpret_cast<float*>(slice + slice_chunks) + wid * 2 * ECAP;
   int* high_at = reinterpret_cast<int*>(high_x + ECAP);
+  uint16_t* high_place =
+      reinterpret_cast<uint16_t*>(slice + slice_chunks) + wid * ((slice_chunks + NT - 1) / NT * 32 * EPC);
   auto cta_sync = [&] {
     if (NT == 32)
       __syncwarp();
@@ -607,11 +610,17 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
     auto keep = [&](bool high, float x, int at) {
       const unsigned who = __ballot_sync(0xffffffffu, high);
       const int slot = have + __popc(who & ((1u << lane) - 1u));
-      if (high && slot < ECAP) {
+      if (RESIDENT) {
+        if (high) high_place[slot] = (uint16_t)(at - EPC * q_lo);
+      } else if (high && slot < ECAP) {
         high_x[slot] = x;
         high_at[slot] = at;
       }
       have += __popc(who);
+    };
+    auto kept_place = [&](int i) { return RESIDENT ? EPC * q_lo + (int)high_place[i] : high_at[i]; };
+    auto kept_value = [&](int i) {
+      return RESIDENT ? Logit<T>::load(reinterpret_cast<const T*>(slice) + high_place[i]) : high_x[i];
     };
     // Of a short row every logit is looked at in the walk; of a long one, chunks
     // with a high logit are queued, so that the walk pays a ballot a chunk.
@@ -768,7 +777,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
     // The first cut; none for a short row of the second pass.
     // A warp's own row starts a little lower, and lower still for a top-k that
     // would end below (15510 x 1025, 12% of the rows with k = 200: 148 -> 129 us).
-    const float further = PASS == kMarked ? (RESIDENT ? 1e30f : 0.f) : NT == 32 ? (q.k > 64 ? 0.3f : 0.1f) : 0.f;
+    const float further = PASS == kMarked ? (RESIDENT ? 1e30f : 0.f) : NT == 32 ? (q.k > 64 ? .35f : .15f) : 0.f;
     x1 = ONE_WALK ? cut : cut - further * (m - cut);
     if (PASS == kMarked && !RESIDENT) x1 = fminf(x1, a.out_logprobs[n]);  // the first pass's hint, +inf for none
     x1 = fmaxf(x1, x_low);
@@ -832,8 +841,8 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
           }
         }
       };
-      if (have <= ECAP) {
-        for (int i = lane; i < have; i += 32) add(high_x[i], sf_weight(high_x[i], m, q.r));
+      if (RESIDENT || have <= ECAP) {
+        for (int i = lane; i < have; i += 32) add(kept_value(i), sf_weight(kept_value(i), m, q.r));
       } else if constexpr (PASS == kFirst) {
         if (lane == 0) lead->crowded = 1;
       } else {
@@ -1221,8 +1230,8 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
             sh.incl[slot] = ((u64)Logit<T>::key(x) << 32) | (u64)(0xffffffffu - (uint32_t)(at - g.dc));
         }
       };
-      if (have <= ECAP) {
-        for (int i = lane; i < have; i += 32) take(high_x[i], high_at[i]);
+      if (RESIDENT || have <= ECAP) {
+        for (int i = lane; i < have; i += 32) take(kept_value(i), kept_place(i));
       } else if constexpr (PASS != kFirst) {
         walk([&](int j, const uint4& raw) {
           float f[EPC];
@@ -1410,8 +1419,15 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : NT == 128 ? 6 : 1024 / NT)
 
 namespace {
 
+// Which kernel a call runs. Measured (us, rows x V of bf16, mixed parameters):
+//   a warp per row          8000 x 2048    95    2000 x 4000  68   8000 x 4000 181
+//   128 threads, resident                        2000 x 4000  50   8000 x 4000 156   600 x 16000  62   4 x 16000 21
+//   512 threads, streamed   600 x 16000   107    2000 x 32000 233  300 x 64000  58   1000 x 64000 163
+//   256 threads, streamed   100 x 32000 29 (41)  2000 x 32000 149  300 x 64000  66   1000 x 64000 136
 constexpr int kSfSmallV = 2048;   // rows up to here, when there are enough to fill the GPU: a warp each
 constexpr int kSfMediumV = 8192;  // rows up to here: 128-thread CTAs, held in shared memory
+constexpr long long kSfMediumBytes = 32 << 10;  // and, when there are enough to fill the GPU, up to here
+constexpr long long kSfLongBytes = 128 << 10;   // streamed rows up to here: 256 threads, two CTAs in a second pass
 constexpr long long kSfSliceMin = 8 << 10;
 
 // Launches the fast kernel with cs CTAs per row; *refused when no cluster of that shape fits.
@@ -1420,7 +1436,8 @@ cudaError_t launch_fast(const FilteredArgs& a, int cs, cudaStream_t st, bool* re
   auto kern = k_sample_filtered<T, NT, NB, CAP, GROUPS, QCAP, ECAP, RESIDENT, PASS>;
   // a resident slice: the most chunks that a row's 16-byte blocks can make, shared out
   const int chunks = RESIDENT ? (int)((((long long)a.V * sizeof(T) + 46 - 2 * sizeof(T)) / 16 + cs - 1) / cs) : 0;
-  const size_t smem = (size_t)chunks * 16 + (size_t)(NT / 32) * ECAP * 8;
+  const size_t smem = RESIDENT ? (size_t)chunks * 16 + (size_t)((chunks + NT - 1) / NT) * NT * (16 / sizeof(T)) * 2
+                               : (size_t)(NT / 32) * ECAP * 8;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = smem;
@@ -1457,11 +1474,10 @@ cudaError_t launch_fast(const FilteredArgs& a, int cs, cudaStream_t st, bool* re
     return cudaSuccess;
   }
   // Marked rows are few and fall anywhere: short shares, handed out as clusters
-  // come free. A CTA per short row (15510 x 1025: the pass took 88 us with a
-  // resident grid, 41 us so); eight shares per resident cluster for long ones,
-  // whose empty CTAs cost more (256 x 248320, none / an eighth marked: 49 / 144
-  // us with three shares, 52 / 123 us with eight).
-  const long long most = PASS != kMarked ? fit : RESIDENT ? 1ll << 20 : 8ll * fit;
+  // come free (15510 x 1025: one, two, four or eight shares per resident CTA 133,
+  // 126, 126, 128 us). Empty CTAs of long rows cost more: 256 x 248320, none / an
+  // eighth marked, 49 / 144 us with three shares per cluster, 52 / 123 us with eight.
+  const long long most = PASS != kMarked ? fit : RESIDENT ? 4ll * fit : 8ll * fit;
   const long long clusters = a.n < most ? a.n : most;
   cfg.gridDim = dim3((unsigned)(clusters * cs));
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, chunks);
@@ -1478,20 +1494,22 @@ static cudaError_t launch_filtered(const FilteredArgs& a, cudaStream_t st) {
   bool refused = false;
   cudaError_t e;
   if (a.V <= kSfSmallV && a.n >= sms * 8LL) {
-    e = launch_fast<T, 32, 128, 64, 32, 0, 320, true, kFirst>(a, 1, st, &refused);
-    if (!refused && e == cudaSuccess) e = launch_fast<T, 128, 256, 256, 32, 0, 256, true, kMarked>(a, 1, st, &refused);
-  } else if (a.V <= kSfMediumV) {
-    e = launch_fast<T, 128, 256, 256, 32, 0, 256, true, kOnce>(a, 1, st, &refused);
+    e = launch_fast<T, 32, 64, 64, 32, 0, 0, true, kFirst>(a, 1, st, &refused);
+    if (!refused && e == cudaSuccess) e = launch_fast<T, 128, 256, 256, 32, 0, 0, true, kMarked>(a, 1, st, &refused);
+  } else if (a.V <= kSfMediumV || (a.n >= sms && (long long)a.V * sizeof(T) <= kSfMediumBytes)) {
+    e = launch_fast<T, 128, 256, 256, 32, 0, 0, true, kOnce>(a, 1, st, &refused);
   } else {
     // A CTA per row, or as many as the SMs that the rows leave, down to 8 KB of a
     // row each. A CTA alone would hold the call up with a row that takes several
-    // more walks: such rows get eight CTAs each in a second pass.
+    // more walks: such rows get two or eight CTAs each in a second pass.
+    const long long bytes = (long long)a.V * sizeof(T);
     int cs = 1;
-    while (cs < 8 && a.n * cs * 2LL <= sms && (long long)a.V * sizeof(T) >= cs * 2 * kSfSliceMin) cs *= 2;
+    while (cs < 8 && a.n * cs * 2LL <= sms && bytes >= cs * 2 * kSfSliceMin) cs *= 2;
     if (cs == 1) {
-      e = launch_fast<T, 512, 1024, 512, 32, 384, 256, false, kFirst>(a, 1, st, &refused);
+      e = bytes <= kSfLongBytes ? launch_fast<T, 256, 512, 512, 32, 384, 256, false, kFirst>(a, 1, st, &refused)
+                                : launch_fast<T, 512, 1024, 512, 32, 384, 256, false, kFirst>(a, 1, st, &refused);
       if (refused || e != cudaSuccess) return refused ? cudaErrorLaunchOutOfResources : e;
-      e = launch_fast<T, 512, 1024, 512, 128, 384, 512, false, kMarked>(a, 8, st, &refused);
+      e = launch_fast<T, 512, 1024, 512, 128, 384, 512, false, kMarked>(a, bytes <= kSfLongBytes ? 2 : 8, st, &refused);
     } else {
       e = launch_fast<T, 512, 1024, 512, 128, 384, 512, false, kOnce>(a, cs, st, &refused);
     }
