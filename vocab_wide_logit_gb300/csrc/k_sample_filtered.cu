@@ -790,7 +790,10 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 28 : NT == 128 ? 6 : 1024 / NT)
     // for. A longer one most likely does: its row is left to the second pass if not.
     const bool sure = q.k && q.k <= (ONE_WALK ? GROUPS - 2 : GROUPS);
     const bool whole = drawn && !(q.k && q.k <= (ONE_WALK ? 8 * GROUPS : GROUPS));
-    const bool tempered = whole && (ONE_WALK || x1 > x_low) && q.r != 1.f;
+    // A row of the second pass is weighed exactly at once: bounds did not do, or will not that far down.
+    const bool exact = PASS == kMarked && whole && x1 > x_low;
+    const bool tempered = PASS != kMarked && whole && (ONE_WALK || x1 > x_low) && q.r != 1.f;
+    u64 mass = 0;
     const bool floored = q.mp > 0.f;
     auto add_bins = [&](float x, uint32_t w) {
       if (w) {
@@ -810,14 +813,18 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 28 : NT == 128 ? 6 : 1024 / NT)
         g.values(raw, j, f);
         const float c = max_of(f);
         sum_chunk(f, ref, tempered);
+        if (exact) {
+#pragma unroll
+          for (int i = 0; i < EPC; ++i) mass += sf_weight(f[i], m, q.r);
+        }
         collect(j, f, drawn && c >= x1);
         if (greedy && c == m) {
-  #pragma unroll
+#pragma unroll
           for (int i = 0; i < EPC; ++i)
             if (f[i] == m) first = min(first, g.id(j, i));
         }
         if (!finite) {
-  #pragma unroll
+#pragma unroll
           for (int i = 0; i < EPC; ++i) odd |= !(f[i] < kInf);
         }
       });
@@ -899,11 +906,13 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 28 : NT == 128 ? 6 : 1024 / NT)
         lead->part_below[rank] = below;
       }
     };
+    if (exact) mass = warp_sum_u64(mass);
     if (NW > 1) {
       if (lane == 0) {
         sh.sred[0][wid] = s;
         sh.sred[1][wid] = st;
         sh.ired[0][wid] = odd;
+        if (PASS == kMarked) sh.red[wid] = mass;
       }
       cta_sync();
     }
@@ -913,8 +922,10 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 28 : NT == 128 ? 6 : 1024 / NT)
         s = warp_sum(in ? sh.sred[0][lane] : 0.f);
         st = warp_sum(in ? sh.sred[1][lane] : 0.f);
         odd = __any_sync(0xffffffffu, in && sh.ired[0][lane]);
+        if (exact) mass = warp_sum_u64(in ? sh.red[lane] : 0);
       }
       if (lane == 0) {
+        if (PASS == kMarked) lead->part_total[rank] = mass;
         lead->part_sum[rank] = s;
         lead->part_tempered[rank] = st;
         lead->part_odd[rank] = odd;
@@ -1037,8 +1048,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 28 : NT == 128 ? 6 : 1024 / NT)
       auto light = [&](int b, u64 width) {
         const u64 mass = sh.pm[b] - (b ? sh.pm[b - 1] : 0);
         const uint32_t c = sh.pc[b] - (b ? sh.pc[b - 1] : 0u);
-        // a row of the second pass is not tried with bounds again
-        return width > 0 && (PASS == kMarked || width * 4 * c > mass);
+        return width > 0 && width * 4 * c > mass;
       };
       if (complete) {
         if (lane == 0) sh.t_lo = sh.t_hi = known;
@@ -1123,6 +1133,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 28 : NT == 128 ? 6 : 1024 / NT)
         s = warp_sum(in ? sh.part_sum[lane] : 0.f);
         st = warp_sum(in ? sh.part_tempered[lane] : 0.f);
         odd = __any_sync(0xffffffffu, in && sh.part_odd[lane]);
+        if (exact) mass = warp_sum_u64(in ? sh.part_total[lane] : 0);
       }
       if (lane == 0) {
         // relative to the maximum: of one walk, ref is the sample's
@@ -1137,13 +1148,14 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 28 : NT == 128 ? 6 : 1024 / NT)
         const double slack = t * (rel + kSfRounding * (21 + (q_hi - q_lo + NT - 1) / NT)) + 0.5 * (double)a.V;
         sh.t_lo = t > slack ? (u64)(t - slack) : 0;
         sh.t_hi = (u64)(t + slack) + 1;
+        if (exact) sh.t_lo = sh.t_hi = mass;
         sh.known_sum = s;
         sh.known_odd = odd;
       }
     }
     sync();
     int command;
-    bool weighed = false, fresh = true;
+    bool weighed = exact, fresh = true;
     for (int lowered = 0;;) {
       if (rank == 0) {
         if (fresh) scan_bins();
