@@ -335,6 +335,20 @@ __device__ __forceinline__ RowParams row_params(const FilteredArgs& a, long long
 __device__ __forceinline__ u64 need_of(float p, u64 total) { return (u64)ceil((double)p * (double)total); }
 __device__ __forceinline__ u64 target_of(float u, u64 total) { return (u64)floor((double)u * (double)total); }
 
+// Integers around f * total (0 <= f <= 1, total < 2^53): both functions above lie
+// between them. FP64 runs at a sixty-fourth of FP32's rate, and where a boundary
+// may lie is asked up to eight times a row.
+__device__ __forceinline__ u64 fraction_low(float f, u64 total) {
+  const u64 bits = (u64)(f * 4294967296.f);  // f has 24 bits: exact from 2^-8 on, less by under 2^-32 below
+  const u64 x = bits >> 32 ? total : __umul64hi(total, bits << 32);
+  return x > 2 ? x - 2 : 0;
+}
+__device__ __forceinline__ u64 fraction_high(float f, u64 total) {
+  const u64 bits = (u64)(f * 4294967296.f) + 1;
+  const u64 x = bits >> 32 ? total : __umul64hi(total, bits << 32);
+  return x + 3 < total ? x + 3 : total;
+}
+
 // The row's token, each question by a search over the row, which one CTA re-reads
 // some ten times. It assumes nothing of the row: it finishes those whose ties are
 // too many for the lists of the fast kernel.
@@ -432,7 +446,7 @@ enum Pass { kOnce, kFirst, kMarked };
 
 enum Command { kDone, kGather, kWeigh, kLower, kExact, kMark };
 
-constexpr double kSfSlack = 2.2e-6, kSfRounding = 6e-8;
+constexpr float kSfSlack = 2.2e-6f, kSfRounding = 6e-8f;
 
 // Index of the first element of the ascending array that is >= t (n if none), by one warp.
 template <typename U>
@@ -642,17 +656,18 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 28 : NT == 128 ? 6 : 1024 / NT)
       if (RESIDENT) return;
       have = queued <= QCAP ? 0 : ECAP + 1;
       if (have) return;
-      for (int i0 = 0; i0 < queued; i0 += 128 / EPC) {
-        float x[4];
-        int at[4];
+      constexpr int B = 4;  // loads in flight
+      for (int i0 = 0; i0 < queued; i0 += 32 * B / EPC) {
+        float x[B];
+        int at[B];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < B; ++u) {
           const int k = queue[min(i0 + lane / EPC + u * (32 / EPC), queued - 1)];
           at[u] = EPC * (ONE_WALK ? warp_from + k : q_lo + wid * 32 + k / 32 * NT + k % 32) + lane % EPC;
           x[u] = Logit<T>::get(reinterpret_cast<const T*>(g.base), at[u]);
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < B; ++u) {
           const int id = at[u] - g.dc;
           keep(x[u] >= x1 && i0 + lane / EPC + u * (32 / EPC) < queued && id >= 0 && id < a.V, x[u], at[u]);
         }
@@ -1086,10 +1101,10 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 28 : NT == 128 ? 6 : 1024 / NT)
         return (int)kLower;
       }
       if (q.p < 1.f) {
-        const u64 n_hi = need_of(q.p, t_hi), n_lo = t_lo == t_hi ? n_hi : need_of(q.p, t_lo);
+        const u64 n_hi = fraction_high(q.p, t_hi), n_lo = fraction_low(q.p, t_lo);
         if (n_hi > known) return complete ? (int)kExact : lower(n_hi);
         const int b0 = warp_lower_bound<u64>(sh.pm, nb, n_lo > 0 ? n_lo : 1, lane);
-        const int b1 = n_lo == n_hi ? b0 : warp_lower_bound<u64>(sh.pm, nb, n_hi, lane);
+        const int b1 = n_hi <= sh.pm[b0] ? b0 : warp_lower_bound<u64>(sh.pm, nb, n_hi, lane);
         if (loose && light(b1, n_hi - n_lo)) return (int)kWeigh;
         loose = false;
         mark_range(b0, b1);
@@ -1109,10 +1124,13 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 28 : NT == 128 ? 6 : 1024 / NT)
           t_hi = f_hi < t_hi ? f_hi : t_hi;
         }
       }
-      const u64 d_hi = target_of(q.u, t_hi), d_lo = t_lo == t_hi ? d_hi : target_of(q.u, t_lo);
+      // the draw's target is below the kept mass
+      u64 d_hi = fraction_high(q.u, t_hi), d_lo = fraction_low(q.u, t_lo);
+      if (d_hi >= t_hi && t_hi) d_hi = t_hi - 1;
+      if (d_lo > d_hi) d_lo = d_hi;
       if (d_hi >= known) return complete ? (int)kExact : lower(d_hi + 1);
       const int b0 = warp_lower_bound<u64>(sh.pm, nb, d_lo + 1, lane);
-      const int b1 = d_lo == d_hi ? b0 : warp_lower_bound<u64>(sh.pm, nb, d_hi + 1, lane);
+      const int b1 = d_hi < sh.pm[b0] ? b0 : warp_lower_bound<u64>(sh.pm, nb, d_hi + 1, lane);
       if (loose && light(b1, d_hi - d_lo)) return (int)kWeigh;
       mark_range(b0, b1);
       int listed = 0;
@@ -1136,18 +1154,18 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 28 : NT == 128 ? 6 : 1024 / NT)
         if (exact) mass = warp_sum_u64(in ? sh.part_total[lane] : 0);
       }
       if (lane == 0) {
-        // relative to the maximum: of one walk, ref is the sample's
-        double t = (double)(tempered ? st : s) * (double)kSfOne, rel = kSfSlack;
+        float t = (tempered ? st : s) * kSfOne, rel = kSfSlack;
         if (ONE_WALK) {
-          // The exponents are taken from ref: three roundings of (x - ref) r beside two of (x - m) r, both
-          // 15 at most in the mean (ln V), (m - ref) r further off here; and the factor's own.
-          const double off = (double)((m - ref) * q.r);
-          t *= exp(-off);
-          rel += kSfRounding * (2 * 15 + 3 * (15 + off) + off);
+          // The exponents are taken from ref, the sample's maximum: three roundings of (x - ref) r beside two of
+          // (x - m) r, both 15 at most in the mean (ln V), (m - ref) r further off here; and the factor's own.
+          const float off = (m - ref) * q.r;
+          t *= expf(-off);
+          rel += kSfRounding * (2.f * 15.f + 3.f * (15.f + off) + off + 4.f);
         }
-        const double slack = t * (rel + kSfRounding * (21 + (q_hi - q_lo + NT - 1) / NT)) + 0.5 * (double)a.V;
-        sh.t_lo = t > slack ? (u64)(t - slack) : 0;
-        sh.t_hi = (u64)(t + slack) + 1;
+        rel += kSfRounding * (float)(25 + (q_hi - q_lo + NT - 1) / NT);
+        const u64 mid = (u64)t, slack = (u64)(t * rel) + (u64)(a.V / 2) + 2;
+        sh.t_lo = mid > slack ? mid - slack : 0;
+        sh.t_hi = mid + slack;
         if (exact) sh.t_lo = sh.t_hi = mass;
         sh.known_sum = s;
         sh.known_odd = odd;
