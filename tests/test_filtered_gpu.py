@@ -156,11 +156,13 @@ def test_every_spread_and_filter_alone(sigma, V, dtype):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n,V", [(1300, 33), (1300, 1025), (1301, 2048), (1300, 2049), (700, 5003), (160, 9001),
                                  (80, 20000), (100, 70001)])
-@pytest.mark.parametrize("kind", ["normal", "few", "masked", "equal"])
+@pytest.mark.parametrize("kind", ["normal", "few", "masked", "equal", "peaked"])
 def test_batches_that_fill_the_gpu(n, V, kind, dtype):
     """Enough rows that each gets one warp or one CTA, and several in turn; rows that take further passes among them."""
     x = _logits(n, V, 3.0, V, DT[dtype], kind)
     x[::7] *= 0.01
+    if kind == "peaked":  # further yet than a sum of exponentials reaches from the other logits
+        x[3::11] = torch.where(x[3::11] > 30, x[3::11] + 200, x[3::11])
     x = x.to(_dev())
     par = _params(n, V)
     tok, _ = _run(x, *par)

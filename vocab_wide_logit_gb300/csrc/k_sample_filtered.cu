@@ -382,9 +382,8 @@ __device__ __noinline__ int row_exact(const T* p, int V, const RowParams& q, flo
 // ---------------------------------------------------------------- the fast kernel
 //
 // A cluster of cs CTAs takes a row, a contiguous slice each, and answers the
-// three questions from histograms over bins of x. A short slice is held in shared
-// memory (RESIDENT), the next row's copied there while this one is answered; a
-// long one is read from HBM for the first walk and from L2 for the second.
+// three questions from histograms over bins of x. A short row is held in shared
+// memory (RESIDENT), the next one copied there while this one is answered.
 //   max     m, the smallest logit that is no mask, and a cut x1: the least of
 //           GROUPS groups' maxima, so that GROUPS logits at least are above it
 //           and, of independent ones, about ln(GROUPS) times as many
@@ -407,8 +406,24 @@ __device__ __noinline__ int row_exact(const T* p, int V, const RowParams& q, flo
 // that, the cluster weighs the rest of the row exactly (kWeigh), and where it
 // falls between two listed logits all the same, rank 0 does.
 // A row whose boundary bins hold more than CAP logits (ties) is finished by
-// row_exact. So a logit costs two ex2 and its share of two walks over the
-// row; an exact weight and an atomic only above x1.
+// row_exact. So a logit costs two ex2 and its share of two walks over the row; an
+// exact weight and an atomic only above x1.
+//
+// Batches that fill the GPU take a warp (short rows) or a CTA (long ones) per row
+// and leave the few rows that need more to a second launch (kFirst, kMarked): the
+// first kernel then has none of that code, and a slow row holds nobody up. A long
+// row's CTA reads it once (ONE_WALK): the cut and a reference for the sums come
+// from a sixteenth of the row, and the logits that turn out high are read again
+// singly. Splitting every row over a cluster instead took 203 us where this takes
+// 82 (256 rows x 248320, top-p: each cluster barrier waits for the slowest CTA of
+// a row's latency-bound steps); two walks per CTA 96 us, the second from HBM again
+// because 256 rows do not fit L2.
+//
+// What bounds it: long rows HBM first, then the latency of the steps behind the
+// walk (52 us for 256 x 248320 with a top-k, 19 of them at the copy rate); short
+// rows instructions and their fetch (3100 per row of 1025 at 56% of the issue
+// rate, 109 us for 15510 rows of 1025); single rows the barriers (9 us for 1025,
+// 19 us for 248320).
 namespace {
 
 template <int NT, int NB, int CAP, int QCAP, int CS>  // QCAP 0: no queue; CS: most CTAs of a cluster
@@ -819,7 +834,6 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 28 : NT == 128 ? 6 : 1024 / NT)
       }
     };
 
-
     // ---- weigh
     int first = INT_MAX, odd = 0;
     if constexpr (!ONE_WALK) {
@@ -901,11 +915,11 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 28 : NT == 128 ? 6 : 1024 / NT)
     // A NaN, or +inf under a finite maximum, makes the sum NaN.
     s = warp_sum(s);
     odd |= finite && !(s < kInf);
+    if (tempered) st = warp_sum(st);
     // What one walk cannot settle: a sample without a logit, a maximum so far
     // above the sample's that the sums overflow.
     if (ONE_WALK && lane == 0 && (!(ref > -kInf) || s == kInf || (tempered && !(st < kInf)))) sh.crowded = 1;
     odd = __any_sync(0xffffffffu, odd);
-    if (tempered) st = warp_sum(st);
     if (greedy) {
       first = warp_min_i(first);
       if (lane == 0 && first != INT_MAX) atomicMin(&lead->first_id, first);
@@ -938,6 +952,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 28 : NT == 128 ? 6 : 1024 / NT)
         st = warp_sum(in ? sh.sred[1][lane] : 0.f);
         odd = __any_sync(0xffffffffu, in && sh.ired[0][lane]);
         if (exact) mass = warp_sum_u64(in ? sh.red[lane] : 0);
+        if (ONE_WALK && lane == 0 && (s == kInf || (tempered && !(st < kInf)))) sh.crowded = 1;
       }
       if (lane == 0) {
         if (PASS == kMarked) lead->part_total[rank] = mass;
@@ -1323,17 +1338,12 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 28 : NT == 128 ? 6 : 1024 / NT)
       }
       if (len <= 32) {
         if (wid == 0) {
-          // bitonic sort in registers, descending
-          u64 e = lane < len ? sh.list[lane] : 0;
-#pragma unroll
-          for (int size = 2; size <= 32; size *= 2)
-#pragma unroll
-            for (int d = size / 2; d > 0; d /= 2) {
-              const u64 o = __shfl_xor_sync(0xffffffffu, e, d);
-              const bool keep_max = ((lane & d) == 0) == ((lane & size) == 0);
-              e = (e > o) == keep_max ? e : o;
-            }
-          if (lane < len) sh.list[lane] = e;
+          // each entry to the place that the number of larger ones gives; all differ
+          const u64 v = lane < len ? sh.list[lane] : 0;
+          int place = 0;
+          for (int o = 0; o < len; ++o) place += sh.list[o] > v;
+          __syncwarp();
+          if (lane < len) sh.list[place] = v;
           __syncwarp();
         }
       } else {
