@@ -8,9 +8,14 @@
 // as the fp16 tiles that the product of 8-bit integers reads (launch_linear_i8),
 // which saves that call its own pass over them.
 //
-// Bound by latency at decoding sizes: a load, two block reductions and a store;
-// 2.2 us for a row of 1024, 2.5 us for 24 rows of 2048 on the device.
+// Bound by latency at decoding sizes, a load, two block reductions and a store:
+// 1.8 us for a row of 1024, 1.9 us for 24 rows of 2048, 2.2 us for 256 (bf16, with a
+// gain). Wide batches are bound by instructions: 8192 rows of 4096 take 35 us,
+// 2.9 TB/s. A thread keeps 1, 2 or 4 chunks by K: with 4 throughout, 8192 x 4096
+// took 90 us for the registers it held.
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "ds_device.cuh"
 #include "ds_launch.h"
@@ -20,7 +25,6 @@ namespace ds {
 namespace {
 
 constexpr int kQrNT = 256;
-constexpr int kQrHeld = 4;  // chunks of a row that a thread keeps
 
 __device__ __forceinline__ float qr_get(const uint16_t* p, long long i) {
   return __uint_as_float((uint32_t)__ldg(p + i) << 16);
@@ -51,8 +55,9 @@ __device__ __forceinline__ void qr_chunk(const float* row, int c, int K, bool wi
 }  // namespace
 
 // TILES: rows of fp16 tiles, grid rows up to the last tile's end (zero past n, zero past K).
-template <typename T, bool TILES>
-__global__ void __launch_bounds__(kQrNT) k_quantize_rows(const void* x, int n, int K, long long ld, const float* gain,
+// HELD: chunks of a row that a thread keeps.
+template <typename T, bool TILES, int HELD>
+__global__ void __launch_bounds__(kQrNT, HELD == 4 ? 3 : HELD == 2 ? 4 : 5) k_quantize_rows(const void* x, int n, int K, long long ld, const float* gain,
                                                          float eps, int8_t* q, float* scale, I8Tiles tiles) {
   pdl_wait();
   pdl_release();
@@ -64,21 +69,10 @@ __global__ void __launch_bounds__(kQrNT) k_quantize_rows(const void* x, int n, i
     const T* row = static_cast<const T*>(x) + i * ld;
     const bool live = i < n;
     const bool wide = (reinterpret_cast<uintptr_t>(row) & 15) == 0;
-    float held[kQrHeld][8];
-    auto get = [&](int s, int c, float (&f)[8]) {  // the s-th chunk of this thread, chunk c of the row
-      if (s < kQrHeld) {
+    const bool wide_gain = (reinterpret_cast<uintptr_t>(gain) & 15) == 0;
+    float held[HELD][8];
 #pragma unroll
-        for (int h = 0; h < kQrHeld; ++h)
-          if (h == s) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = held[h][e];
-          }
-      } else {
-        qr_chunk(row, c, K, wide, f);
-      }
-    };
-#pragma unroll
-    for (int h = 0; h < kQrHeld; ++h) {
+    for (int h = 0; h < HELD; ++h) {
       const int c = tid + h * kQrNT;
       if (live && 8 * c < K) {
         qr_chunk(row, c, K, wide, held[h]);
@@ -88,15 +82,15 @@ __global__ void __launch_bounds__(kQrNT) k_quantize_rows(const void* x, int n, i
       }
     }
     float f = 1.f;
-    int bad = 0;
+    bool bad = false;
     if (gain) {
       float s = 0.f;
 #pragma unroll
-      for (int h = 0; h < kQrHeld; ++h)
+      for (int h = 0; h < HELD; ++h)
 #pragma unroll
         for (int e = 0; e < 8; ++e) s = __fmaf_rn(held[h][e], held[h][e], s);
       if (live)
-        for (int c = tid + kQrHeld * kQrNT; 8 * c < K; c += kQrNT) {
+        for (int c = tid + HELD * kQrNT; 8 * c < K; c += kQrNT) {
           float v[8];
           qr_chunk(row, c, K, wide, v);
 #pragma unroll
@@ -113,72 +107,75 @@ __global__ void __launch_bounds__(kQrNT) k_quantize_rows(const void* x, int n, i
     }
     auto normed = [&](int c, float (&v)[8]) {
       if (gain) {
+        float w[8];
+        qr_chunk(gain, c, K, wide_gain, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 8 * c + e < K ? v[e] * f * __ldg(gain + 8 * c + e) : 0.f;
+        for (int e = 0; e < 8; ++e) v[e] = v[e] * f * w[e];
       }
     };
-    float amax = 0.f;
+    // max |y| as bits: of numbers without sign they are in the numbers' order, infinities and NaN last
+    uint32_t top = 0;
 #pragma unroll
-    for (int h = 0; h < kQrHeld; ++h) {
+    for (int h = 0; h < HELD; ++h) {
       const int c = tid + h * kQrNT;
       if (8 * c < K) normed(c, held[h]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        bad |= !(fabsf(held[h][e]) < kInf);
-        amax = fmaxf(amax, fabsf(held[h][e]));
-      }
+      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(held[h][e]) & 0x7fffffffu);
     }
     if (live)
-      for (int c = tid + kQrHeld * kQrNT; 8 * c < K; c += kQrNT) {
+      for (int c = tid + HELD * kQrNT; 8 * c < K; c += kQrNT) {
         float v[8];
         qr_chunk(row, c, K, wide, v);
         normed(c, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          bad |= !(fabsf(v[e]) < kInf);
-          amax = fmaxf(amax, fabsf(v[e]));
-        }
+        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
       }
-    amax = warp_max(amax);
-    if (lane == 0) red[1][wid] = amax;
-    bad = __syncthreads_or(bad);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) red[1][wid] = __uint_as_float(top);
+    __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kQrNT / 32; ++w) amax = fmaxf(amax, red[1][w]);
-    const float inv = (bad || amax == 0.f) ? 0.f : fminf(127.f / amax, 3.402823466e38f);
-    int s = 0;
-    for (int c = tid; c < chunks; c += kQrNT, ++s) {
-      float v[8];
-      get(s, c, v);
-      if (s >= kQrHeld) {
-        if (!live)
+    for (int w = 0; w < kQrNT / 32; ++w) top = max(top, __float_as_uint(red[1][w]));
+    const float amax = __uint_as_float(top);
+    bad = bad || top >= 0x7f800000u;
+    const float inv = (bad || top == 0u) ? 0.f : fminf(127.f / amax, 3.402823466e38f);
+    auto put = [&](int c, const float (&v)[8]) {
+      // |y inv| <= 127 (1 + 2^-23): added to 1.5 2^23 it is rounded to the nearest integer, which the low
+      // bits then hold
+      float w[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = 0.f;
-        normed(c, v);
-      }
-      int w[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = bad ? 0 : __float2int_rn(fminf(fmaxf(v[e] * inv, -127.f), 127.f));
+      for (int e = 0; e < 8; ++e) w[e] = bad ? 12582912.f : __fadd_rn(__fmul_rn(v[e], inv), 12582912.f);
       if (TILES) {
         const int r = (int)(i % tiles.rows);
         const long long block = (i / tiles.rows) * tiles.kb + (c >> 3);
-        __half h[8];
+        __half2 h[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[e] = __int2half_rn(w[e]);
+        for (int e = 0; e < 4; ++e) h[e] = __floats2half2_rn(w[2 * e] - 12582912.f, w[2 * e + 1] - 12582912.f);
         reinterpret_cast<uint4*>(tiles.out)[(block * tiles.rows + r) * 8 + ((c & 7) ^ (r & 7))] =
             *reinterpret_cast<const uint4*>(h);
       } else if ((K & 7) == 0 && (reinterpret_cast<uintptr_t>(q) & 7) == 0) {
         uint32_t lo = 0, hi = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          lo |= (uint32_t)(uint8_t)(int8_t)w[e] << (8 * e);
-          hi |= (uint32_t)(uint8_t)(int8_t)w[4 + e] << (8 * e);
+          lo |= (__float_as_uint(w[e]) & 0xffu) << (8 * e);
+          hi |= (__float_as_uint(w[4 + e]) & 0xffu) << (8 * e);
         }
         *reinterpret_cast<uint2*>(q + i * K + 8 * c) = make_uint2(lo, hi);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (8 * c + e < K) q[i * K + 8 * c + e] = (int8_t)w[e];
+          if (8 * c + e < K) q[i * K + 8 * c + e] = (int8_t)(__float_as_uint(w[e]) & 0xffu);
       }
+    };
+#pragma unroll
+    for (int h = 0; h < HELD; ++h)
+      if (tid + h * kQrNT < chunks) put(tid + h * kQrNT, held[h]);
+    for (int c = tid + HELD * kQrNT; c < chunks; c += kQrNT) {
+      float v[8] = {};
+      if (live && 8 * c < K) {
+        qr_chunk(row, c, K, wide, v);
+        normed(c, v);
+      }
+      put(c, v);
     }
     if (tid == 0 && live) scale[i] = bad ? __int_as_float(0x7fffffff) : amax / 127.f;
     __syncthreads();  // red is free
@@ -199,8 +196,13 @@ cudaError_t launch_quantize_rows(const void* x, bool f32, int n, int K, int64_t 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto kern = tiles ? (f32 ? k_quantize_rows<float, true> : k_quantize_rows<uint16_t, true>)
-                    : (f32 ? k_quantize_rows<float, false> : k_quantize_rows<uint16_t, false>);
+  auto pick = [&](auto held) {
+    constexpr int H = decltype(held)::value;
+    return tiles ? (f32 ? k_quantize_rows<float, true, H> : k_quantize_rows<uint16_t, true, H>)
+                 : (f32 ? k_quantize_rows<float, false, H> : k_quantize_rows<uint16_t, false, H>);
+  };
+  auto kern = K <= 8 * kQrNT ? pick(std::integral_constant<int, 1>{})
+                             : K <= 16 * kQrNT ? pick(std::integral_constant<int, 2>{}) : pick(std::integral_constant<int, 4>{});
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, x, n, K, (long long)ld, gain, eps, q, scale,
                                            tiles ? *tiles : I8Tiles{nullptr, 0, 0, 0});
   if (e == cudaSuccess) note_launch();
