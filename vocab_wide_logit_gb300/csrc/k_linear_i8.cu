@@ -89,6 +89,17 @@ __device__ __forceinline__ bool mbar_try(uint64_t* b, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+// Arrives at the barrier of the pair's first CTA. What it reports are finished
+// bulk copies and tensor-memory accesses (the tcgen05 fences order those), never
+// this thread's own writes, so nothing is released to the cluster: that would
+// wait for every result this CTA has on its way to memory (1600 cycles and more
+// per arrival, 248 us where this takes 160 for 256 rows x 248320 x 2048).
+__device__ __forceinline__ void mbar_arrive_first(uint64_t* b) {
+  asm volatile(
+      "{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %0, 0;\nmbarrier.arrive.shared::cluster.b64 _, [a];\n}" ::"r"(
+          smem_u32(b))
+      : "memory");
+}
 // Every wait gives up after a while: it raises the CTA's stop flag, which ends
 // the other waits too, and the caller leaves its loop.
 __device__ __noinline__ bool mbar_wait_slow(uint64_t* b, uint32_t parity, volatile int* stop) {
@@ -129,20 +140,38 @@ struct Ring {
   }
 };
 
+// The barrier (of both CTAs of a pair) hears of the instructions so far when they are done.
+template <bool PAIR>
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
+  if (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((unsigned short)3)
+        : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// D[128][N] (+)= A[128][16] B[N][16]^T: A in tensor memory, B in shared memory.
+// D[128][N] (+)= A[128][16] B[N][16]^T: A in tensor memory, B in shared memory. A
+// pair: D[256][N], each CTA with its 128 rows of D and A and its half of B.
+template <bool PAIR>
 __device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
+  if (PAIR)
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&v)[32]) {
   asm volatile(
@@ -213,6 +242,7 @@ constexpr int kTcWSlots = 12;                 // most weight slots
 constexpr int kTcBSlots = 32;                 // most row-tile slots
 constexpr int kTcASlots = 4;                  // fp16 weight blocks in tensor memory, 64 columns each
 constexpr int kTcACol = 256;                  // their first column; accumulators are below
+constexpr int kTcPairRows = 128;  // row tiles above this: a pair of CTAs
 constexpr int kTcSms = 152;  // SMs that calls are cut for
 constexpr size_t kTcSmem = 232448 - 2048;     // dynamic shared memory of a CTA, barriers apart
 
@@ -228,11 +258,22 @@ __device__ __forceinline__ bool epi_any(bool p) {
   return any != 0;
 }
 
+// The CTA's threads, or the pair's, meet.
+template <bool PAIR>
+__device__ __forceinline__ void all_sync() {
+  if (PAIR) {
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+  } else {
+    __syncthreads();
+  }
+}
+
 // How a call of n rows is cut: row tiles of `rows` (a multiple of 16, at most
 // 256), their slots in shared memory, and whether all of a tile's slots stay
 // there for every channel block.
 struct TcPlan {
-  int rows, tiles, kb, b_slots, w_slots, resident;
+  int rows, tiles, kb, b_slots, w_slots, resident, pair;
 };
 
 }  // namespace
@@ -254,19 +295,21 @@ static TcPlan tc_plan(int n, int N, int K) {
   const int least = (n + 255) / 256;
   long long best = 0;
   for (int tiles = least; tiles <= least + 8; ++tiles) {
-    const int rows = ((n + tiles - 1) / tiles + 15) / 16 * 16;
+    const int each = (n + tiles - 1) / tiles, pair = each > kTcPairRows, step = pair ? 32 : 16;
+    const int rows = (each + step - 1) / step * step;
     if ((long long)rows * (tiles - 1) >= n) continue;  // its last tile would be empty
     const long long c = tc_cycles(n, N, p.kb, tiles, rows);
     if (tiles == least || c < best) {
       best = c;
       p.tiles = tiles;
       p.rows = rows;
+      p.pair = pair;
     }
   }
   const long long room = (long long)kTcSmem - 1024;  // the tiles start on 1024 bytes
-  const long long slot = (long long)p.rows * 128, all = slot * 2 * p.kb;
-  p.resident = p.tiles == 1 && 2 * p.kb <= kTcBSlots && all + 6 * kTcBlock <= room;
-  p.b_slots = p.resident ? 2 * p.kb : 4;
+  const long long slot = (long long)p.rows * (p.pair ? 64 : 128), all = slot * 2 * p.kb;
+  p.resident = !p.pair && p.tiles == 1 && 2 * p.kb <= kTcBSlots && all + 6 * kTcBlock <= room;
+  p.b_slots = p.resident ? 2 * p.kb : p.pair ? 8 : 4;
   // An even number: the two converting groups take blocks in turn, and each has
   // to meet every use of the slots it waits on, or a parity of two uses ago
   // would look like the current one.
@@ -278,18 +321,19 @@ static TcPlan tc_plan(int n, int N, int K) {
 static_assert(kTcWSlots % 2 == 0 && kTcASlots % 2 == 0, "each converting group keeps its slots");
 
 // One CTA per SM walks tiles of 128 channels x `rows` rows of a.
-template <typename OUT>
+template <typename OUT, bool PAIR>
 __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan p) {
   extern __shared__ uint8_t dyn[];
   __shared__ uint64_t w_full[kTcWSlots], w_empty[kTcWSlots], b_full[kTcBSlots], b_empty[kTcBSlots];
-  __shared__ uint64_t a_full[kTcASlots], a_empty[kTcASlots], d_full[2], d_empty[2], drained;
+  __shared__ uint64_t a_full[kTcASlots], a_empty[kTcASlots], peer_full[kTcASlots], d_full[2], d_empty[2], drained;
   __shared__ uint32_t tmem_base;
   __shared__ float a_scale[256];
   __shared__ int stop_flag;
   volatile int* stop = &stop_flag;
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   uint8_t* bs = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
-  const uint32_t b_bytes = (uint32_t)p.rows * 128u;
+  const uint32_t rank = PAIR ? blockIdx.x & 1u : 0u;
+  const uint32_t b_bytes = (uint32_t)p.rows * (PAIR ? 64u : 128u);  // this CTA's rows of a tile's 64 inputs
   uint8_t* ws = bs + (size_t)b_bytes * p.b_slots;
   const int d_bufs = p.rows <= 128 ? 2 : 1;
 
@@ -306,21 +350,28 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
     for (int i = 0; i < kTcASlots; ++i) {
       mbar_init(&a_full[i], 4);
       mbar_init(&a_empty[i], 1);
+      mbar_init(&peer_full[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&d_full[i], 1);
-      mbar_init(&d_empty[i], kTcEpi);
+      mbar_init(&d_empty[i], PAIR ? 2 * kTcEpi : kTcEpi);
     }
     mbar_init(&drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_base))
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_base))
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_base))
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
   }
   tc_fence_before();
-  __syncthreads();
+  all_sync<PAIR>();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   // Launched while the kernel that makes the row tiles runs, which in turn started
@@ -329,23 +380,27 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
   pdl_release();
 
   const int kb = p.kb;
-  const long long n_tiles = (long long)((g.N + kPackRows - 1) / kPackRows) * p.tiles;
+  const int blocks = (g.N + kPackRows - 1) / kPackRows;
+  const long long n_tiles = (long long)(PAIR ? (blocks + 1) / 2 : blocks) * p.tiles;
+  const long long t0 = PAIR ? blockIdx.x >> 1 : blockIdx.x, t_step = PAIR ? gridDim.x >> 1 : gridDim.x;
 
   if (warp == kTcEpi + kTcCvt) {
     // ---- weight blocks, in the order they are used
     if (lane == 0) {
       uint32_t it = 0;
+      Ring rw;
       bool ok = true;
-      for (long long t = blockIdx.x; ok && t < n_tiles; t += gridDim.x) {
-        const uint8_t* src = g.packed + (t / p.tiles) * kb * (long long)kTcBlock;
-        for (int b = 0; b < kb; ++b, ++it) {
-          const uint32_t s = it % p.w_slots, round = it / p.w_slots;
-          if (round > 0 && !mbar_wait(&w_empty[s], (round - 1) & 1, stop)) {
+      for (long long t = t0; ok && t < n_tiles; t += t_step) {
+        // the second CTA of the last pair may have no channels of its own: it reads the first's
+        const long long own = PAIR ? min(2 * (t / p.tiles) + rank, blocks - 1LL) : t / p.tiles;
+        const uint8_t* src = g.packed + own * kb * (long long)kTcBlock;
+        for (int b = 0; b < kb; ++b, ++it, rw.next(p.w_slots)) {
+          if (it >= (uint32_t)p.w_slots && !mbar_wait(&w_empty[rw.slot], rw.phase ^ 1u, stop)) {
             ok = false;
             break;
           }
-          mbar_expect(&w_full[s], kTcBlock);
-          bulk_load(ws + (size_t)s * kTcBlock, src + (long long)b * kTcBlock, kTcBlock, &w_full[s]);
+          mbar_expect(&w_full[rw.slot], kTcBlock);
+          bulk_load(ws + rw.slot * kTcBlock, src + (long long)b * kTcBlock, kTcBlock, &w_full[rw.slot]);
         }
       }
       // given up: no copy may be in flight when the CTA leaves
@@ -359,19 +414,20 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
     if (lane == 0) {
       pdl_wait();
       uint32_t it = 0;
+      Ring rb;
       bool ok = true;
       const uint8_t* base = static_cast<const uint8_t*>(g.workspace);
-      for (long long t = blockIdx.x; ok && t < n_tiles; t += gridDim.x) {
+      for (long long t = t0; ok && t < n_tiles; t += t_step) {
         if (p.resident && it > 0) break;
-        const uint8_t* src = base + (t % p.tiles) * (2 * kb) * (long long)b_bytes;
-        for (int b = 0; b < 2 * kb; ++b, ++it) {
-          const uint32_t s = it % p.b_slots, round = it / p.b_slots;
-          if (round > 0 && !mbar_wait(&b_empty[s], (round - 1) & 1, stop)) {
+        const uint32_t tile_bytes = (uint32_t)p.rows * 128u;
+        const uint8_t* src = base + (t % p.tiles) * (2 * kb) * (long long)tile_bytes + rank * b_bytes;
+        for (int b = 0; b < 2 * kb; ++b, ++it, rb.next(p.b_slots)) {
+          if (it >= (uint32_t)p.b_slots && !mbar_wait(&b_empty[rb.slot], rb.phase ^ 1u, stop)) {
             ok = false;
             break;
           }
-          mbar_expect(&b_full[s], b_bytes);
-          bulk_load(bs + (size_t)s * b_bytes, src + (long long)b * b_bytes, b_bytes, &b_full[s]);
+          mbar_expect(&b_full[rb.slot], b_bytes);
+          bulk_load(bs + rb.slot * b_bytes, src + (long long)b * tile_bytes, b_bytes, &b_full[rb.slot]);
         }
       }
       if (!ok)
@@ -381,20 +437,40 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
     }
   } else if (warp == kTcEpi + kTcCvt + 2) {
     // ---- matrix instructions, by one thread
-    if (elect_one()) {
-      // fp32 accumulators, fp16 operands, M = 128, N = rows
-      const uint32_t idesc = (1u << 4) | ((uint32_t)(p.rows >> 3) << 17) | ((uint32_t)(kPackRows >> 4) << 24);
+    if (PAIR && rank == 1) {
+      // the pair's first CTA issues them; this one says when its operands are there
+      if (elect_one()) {
+        Ring ra, rb;
+        bool ok = true;
+        for (long long t = t0; ok && t < n_tiles; t += t_step)
+          for (int b = 0; ok && b < kb; ++b) {
+            ok = mbar_wait(&a_full[ra.slot], ra.phase, stop);
+            tc_fence_after();
+            for (int h = 0; ok && h < 2; ++h) {
+              ok = mbar_wait(&b_full[rb.slot], rb.phase, stop);
+              rb.next(p.b_slots);
+            }
+            tc_fence_before();
+            if (ok) mbar_arrive_first(&peer_full[ra.slot]);
+            ra.next(kTcASlots);
+          }
+      }
+    } else if (elect_one()) {
+      // fp32 accumulators, fp16 operands, M = 128 or 256, N = rows
+      const uint32_t idesc =
+          (1u << 4) | ((uint32_t)(p.rows >> 3) << 17) | ((uint32_t)((PAIR ? 2 : 1) * kPackRows >> 4) << 24);
       const uint64_t b_desc = sw128_desc(smem_u32(bs));
       const uint32_t b_step = b_bytes >> 4;
       Ring ra, rb, rd;
       bool ok = true, loaded = false;
-      for (long long t = blockIdx.x; ok && t < n_tiles; t += gridDim.x) {
+      for (long long t = t0; ok && t < n_tiles; t += t_step) {
         if (!mbar_wait(&d_empty[rd.slot], rd.phase ^ 1u, stop)) break;
         tc_fence_after();
         const uint32_t d = tmem + rd.slot * 128u;
         uint32_t accumulate = 0;
         for (int b = 0; ok && b < kb; ++b) {
-          ok = mbar_wait(&a_full[ra.slot], ra.phase, stop);
+          ok = mbar_wait(&a_full[ra.slot], ra.phase, stop) &&
+               (!PAIR || mbar_wait(&peer_full[ra.slot], ra.phase, stop));
           if (!ok) break;
           tc_fence_after();
           const uint32_t acol = tmem + kTcACol + ra.slot * 64u;
@@ -407,22 +483,22 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
             const uint64_t bd = b_desc + (uint64_t)(rb.slot * b_step);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              tc_mma(d, acol + (uint32_t)(h * 32 + k * 8), bd + (uint64_t)(k * 2), idesc, accumulate);
+              tc_mma<PAIR>(d, acol + (uint32_t)(h * 32 + k * 8), bd + (uint64_t)(k * 2), idesc, accumulate);
               accumulate = 1;
             }
-            if (!p.resident) tc_commit(&b_empty[rb.slot]);
+            if (!p.resident) tc_commit<PAIR>(&b_empty[rb.slot]);
             rb.next(p.b_slots);
           }
-          if (ok) tc_commit(&a_empty[ra.slot]);
+          if (ok) tc_commit<PAIR>(&a_empty[ra.slot]);
           ra.next(kTcASlots);
         }
-        if (ok) tc_commit(&d_full[rd.slot]);
+        if (ok) tc_commit<PAIR>(&d_full[rd.slot]);
         rd.next(d_bufs);
         loaded = p.resident;  // a resident row tile has a slot for each of its blocks: the ring is back at the first
       }
       if (!ok || *stop) {
         // given up: let the instructions in flight finish before tensor memory is freed
-        tc_commit(&drained);
+        tc_commit<PAIR>(&drained);
         for (int i = 0; i < (1 << 16) && !mbar_try(&drained, 0); ++i) {
         }
       }
@@ -432,13 +508,13 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
     // thread one channel of it
     const int group = (warp - kTcEpi) >> 2, quad = warp & 3;
     const int row = quad * 32 + lane;
-    uint32_t it = 0;
+    uint32_t it = 0, s = group, s_phase = 0;  // s: the slot of this group's block, every second of the even ring
     bool ok = true;
-    for (long long t = blockIdx.x; ok && t < n_tiles; t += gridDim.x) {
+    for (long long t = t0; ok && t < n_tiles; t += t_step) {
       for (int b = 0; b < kb; ++b, ++it) {
         if ((int)(it & 1) != group) continue;
-        const uint32_t s = it % p.w_slots, sa = it % kTcASlots, use = it / kTcASlots;
-        ok = __all_sync(0xffffffffu, mbar_wait(&w_full[s], (it / p.w_slots) & 1, stop));
+        const uint32_t sa = it % kTcASlots, use = it / kTcASlots;
+        ok = __all_sync(0xffffffffu, mbar_wait(&w_full[s], s_phase, stop));
         if (!ok) break;
         const uint8_t* src = ws + (size_t)s * kTcBlock + row * 128;
         uint32_t v[2][32];
@@ -453,6 +529,11 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&w_empty[s]);
+        s += 2;
+        if (s >= (uint32_t)p.w_slots) {
+          s -= p.w_slots;
+          s_phase ^= 1u;
+        }
         if (use > 0) {
           ok = __all_sync(0xffffffffu, mbar_wait(&a_empty[sa], (use - 1) & 1, stop));
           if (!ok) break;
@@ -473,8 +554,8 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
     Ring rd;
     long long scales = -1;  // row tile whose scales are in shared memory
     pdl_wait();
-    for (long long t = blockIdx.x; t < n_tiles; t += gridDim.x) {
-      const long long j = t / p.tiles * kPackRows + quad * 32 + lane;
+    for (long long t = t0; t < n_tiles; t += t_step) {
+      const long long j = (PAIR ? 2 * (t / p.tiles) + rank : t / p.tiles) * kPackRows + quad * 32 + lane;
       const long long tile = t % p.tiles, i0 = tile * p.rows;
       const float sw = j < g.N ? g.w_scale[j] : 0.f;
       const bool gone = !mbar_wait(&d_full[rd.slot], rd.phase, stop) || *stop;
@@ -506,15 +587,25 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&d_empty[rd.slot]);
+      if (lane == 0) {
+        if (PAIR)
+          mbar_arrive_first(&d_empty[rd.slot]);
+        else
+          mbar_arrive(&d_empty[rd.slot]);
+      }
       rd.next(d_bufs);
     }
   }
 
   tc_fence_before();
-  __syncthreads();
+  all_sync<PAIR>();  // of a pair, neither leaves while the other may still use its memory
   tc_fence_after();
-  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  if (warp == 0) {
+    if (PAIR)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
   if (threadIdx.x == 0 && stop_flag) report(g.d_status, DS_DEV_ERR_TIMEOUT);
 }
 
@@ -551,7 +642,7 @@ cudaError_t launch_linear_i8(const LinearArgs& g, bool bf16_out, cudaStream_t st
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorUnknown;
   const TcPlan p = tc_plan(g.n, g.N, g.K);
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
@@ -570,17 +661,27 @@ cudaError_t launch_linear_i8(const LinearArgs& g, bool bf16_out, cudaStream_t st
     note_launch();
   }
 
-  auto kern = bf16_out ? k_linear_i8_tc<__nv_bfloat16> : k_linear_i8_tc<float>;
-  const int attr_ok = cached(reinterpret_cast<const void*>(kern), -1, [&](int) {
-    const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
-    if (r != cudaSuccess) (void)cudaGetLastError();
-    return r == cudaSuccess ? 1 : 0;
-  });
-  if (attr_ok <= 0) return cudaErrorUnknown;
-  const long long tiles = (long long)((g.N + kPackRows - 1) / kPackRows) * p.tiles;
-  cfg.gridDim = dim3((unsigned)(tiles < sms ? tiles : sms));
+  auto kern = p.pair ? (bf16_out ? k_linear_i8_tc<__nv_bfloat16, true> : k_linear_i8_tc<float, true>)
+                     : (bf16_out ? k_linear_i8_tc<__nv_bfloat16, false> : k_linear_i8_tc<float, false>);
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.numAttrs = p.pair ? 2 : 1;
+  cfg.gridDim = dim3(2);
   cfg.blockDim = dim3(kTcNT);
   cfg.dynamicSmemBytes = kTcSmem;
+  const int fit = cached(reinterpret_cast<const void*>(kern), -1, [&](int) {
+    int v = 0;
+    cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
+    if (r == cudaSuccess && p.pair) r = cudaOccupancyMaxActiveClusters(&v, kern, &cfg);
+    if (r != cudaSuccess) (void)cudaGetLastError();
+    return r != cudaSuccess ? 0 : p.pair ? v : sms;
+  });
+  if (fit <= 0) return cudaErrorUnknown;
+  const long long blocks = (g.N + kPackRows - 1) / kPackRows;
+  const long long tiles = (p.pair ? (blocks + 1) / 2 : blocks) * p.tiles, ctas = tiles < fit ? tiles : fit;
+  cfg.gridDim = dim3((unsigned)(p.pair ? 2 * ctas : ctas));
   e = cudaLaunchKernelEx(&cfg, kern, g, p);
   if (e == cudaSuccess) note_launch();
   return e;
