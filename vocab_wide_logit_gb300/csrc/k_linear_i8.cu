@@ -129,6 +129,27 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// The tiles of a CTA (or pair): channel blocks (or pairs of them) outermost, row
+// tiles innermost, one tile in `step`. Without a division between tiles.
+struct Walk {
+  long long t;
+  const uint32_t step, tiles;
+  const int d_block, d_tile;
+  int block, tile;
+  __device__ __forceinline__ Walk(uint32_t first, uint32_t step_, uint32_t tiles_)
+      : t(first), step(step_), tiles(tiles_), d_block((int)(step_ / tiles_)), d_tile((int)(step_ % tiles_)),
+        block((int)(first / tiles_)), tile((int)(first % tiles_)) {}
+  __device__ __forceinline__ void next() {
+    t += step;
+    block += d_block;
+    tile += d_tile;
+    if (tile >= (int)tiles) {
+      tile -= (int)tiles;
+      ++block;
+    }
+  }
+};
+
 // A slot of a ring and the parity of its current use.
 struct Ring {
   uint32_t slot = 0, phase = 0;
@@ -213,6 +234,18 @@ __device__ __forceinline__ void tc_ld32(uint32_t addr, int columns, float (&f)[3
   tc_ld16_wait(v + 16);
 #pragma unroll
   for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+}
+
+// Two results, scaled and rounded to bf16.
+__device__ __forceinline__ __nv_bfloat162 scaled2(uint32_t x, uint32_t y, float sx, float sy, float sw) {
+  uint32_t r;
+  asm("{\n.reg .b64 v, s, w;\n.reg .f32 a, b;\n"
+      "mov.b64 v, {%1, %2};\nmov.b64 s, {%3, %4};\nmov.b64 w, {%5, %5};\n"
+      "mul.rn.f32x2 v, v, s;\nmul.rn.f32x2 v, v, w;\n"
+      "mov.b64 {a, b}, v;\ncvt.rn.bf16x2.f32 %0, b, a;\n}"
+      : "=r"(r)
+      : "r"(x), "r"(y), "f"(sx), "f"(sy), "f"(sw));
+  return *reinterpret_cast<const __nv_bfloat162*>(&r);
 }
 
 // Matrix descriptor of a K-major tile with 128-byte swizzle: 8-row groups 1024
@@ -327,7 +360,7 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
   __shared__ uint64_t w_full[kTcWSlots], w_empty[kTcWSlots], b_full[kTcBSlots], b_empty[kTcBSlots];
   __shared__ uint64_t a_full[kTcASlots], a_empty[kTcASlots], peer_full[kTcASlots], d_full[2], d_empty[2], drained;
   __shared__ uint32_t tmem_base;
-  __shared__ float a_scale[256];
+  __shared__ __align__(16) float a_scale[256];
   __shared__ int stop_flag;
   volatile int* stop = &stop_flag;
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -382,7 +415,7 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
   const int kb = p.kb;
   const int blocks = (g.N + kPackRows - 1) / kPackRows;
   const long long n_tiles = (long long)(PAIR ? (blocks + 1) / 2 : blocks) * p.tiles;
-  const long long t0 = PAIR ? blockIdx.x >> 1 : blockIdx.x, t_step = PAIR ? gridDim.x >> 1 : gridDim.x;
+  const uint32_t t0 = PAIR ? blockIdx.x >> 1 : blockIdx.x, t_step = PAIR ? gridDim.x >> 1 : gridDim.x;
 
   if (warp == kTcEpi + kTcCvt) {
     // ---- weight blocks, in the order they are used
@@ -390,10 +423,10 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
       uint32_t it = 0;
       Ring rw;
       bool ok = true;
-      for (long long t = t0; ok && t < n_tiles; t += t_step) {
+      for (Walk at(t0, t_step, p.tiles); ok && at.t < n_tiles; at.next()) {
         // the second CTA of the last pair may have no channels of its own: it reads the first's
-        const long long own = PAIR ? min(2 * (t / p.tiles) + rank, blocks - 1LL) : t / p.tiles;
-        const uint8_t* src = g.packed + own * kb * (long long)kTcBlock;
+        const int own = PAIR ? min(2 * at.block + (int)rank, blocks - 1) : at.block;
+        const uint8_t* src = g.packed + (long long)own * kb * kTcBlock;
         for (int b = 0; b < kb; ++b, ++it, rw.next(p.w_slots)) {
           if (it >= (uint32_t)p.w_slots && !mbar_wait(&w_empty[rw.slot], rw.phase ^ 1u, stop)) {
             ok = false;
@@ -417,10 +450,10 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
       Ring rb;
       bool ok = true;
       const uint8_t* base = static_cast<const uint8_t*>(g.workspace);
-      for (long long t = t0; ok && t < n_tiles; t += t_step) {
+      for (Walk at(t0, t_step, p.tiles); ok && at.t < n_tiles; at.next()) {
         if (p.resident && it > 0) break;
         const uint32_t tile_bytes = (uint32_t)p.rows * 128u;
-        const uint8_t* src = base + (t % p.tiles) * (2 * kb) * (long long)tile_bytes + rank * b_bytes;
+        const uint8_t* src = base + (long long)at.tile * (2 * kb) * tile_bytes + rank * b_bytes;
         for (int b = 0; b < 2 * kb; ++b, ++it, rb.next(p.b_slots)) {
           if (it >= (uint32_t)p.b_slots && !mbar_wait(&b_empty[rb.slot], rb.phase ^ 1u, stop)) {
             ok = false;
@@ -442,7 +475,7 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
       if (elect_one()) {
         Ring ra, rb;
         bool ok = true;
-        for (long long t = t0; ok && t < n_tiles; t += t_step)
+        for (Walk at(t0, t_step, p.tiles); ok && at.t < n_tiles; at.next())
           for (int b = 0; ok && b < kb; ++b) {
             ok = mbar_wait(&a_full[ra.slot], ra.phase, stop);
             tc_fence_after();
@@ -463,7 +496,7 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
       const uint32_t b_step = b_bytes >> 4;
       Ring ra, rb, rd;
       bool ok = true, loaded = false;
-      for (long long t = t0; ok && t < n_tiles; t += t_step) {
+      for (Walk at(t0, t_step, p.tiles); ok && at.t < n_tiles; at.next()) {
         if (!mbar_wait(&d_empty[rd.slot], rd.phase ^ 1u, stop)) break;
         tc_fence_after();
         const uint32_t d = tmem + rd.slot * 128u;
@@ -510,7 +543,7 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
     const int row = quad * 32 + lane;
     uint32_t it = 0, s = group, s_phase = 0;  // s: the slot of this group's block, every second of the even ring
     bool ok = true;
-    for (long long t = t0; ok && t < n_tiles; t += t_step) {
+    for (Walk at(t0, t_step, p.tiles); ok && at.t < n_tiles; at.next()) {
       for (int b = 0; b < kb; ++b, ++it) {
         if ((int)(it & 1) != group) continue;
         const uint32_t sa = it % kTcASlots, use = it / kTcASlots;
@@ -552,46 +585,89 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
     // ---- results: a thread has one channel, a column of tensor memory is one row of a
     const int quad = warp & 3, half = warp >> 2;
     Ring rd;
-    long long scales = -1;  // row tile whose scales are in shared memory
+    int scales = -1;  // row tile whose scales are in shared memory
     pdl_wait();
-    for (long long t = t0; t < n_tiles; t += t_step) {
-      const long long j = (PAIR ? 2 * (t / p.tiles) + rank : t / p.tiles) * kPackRows + quad * 32 + lane;
-      const long long tile = t % p.tiles, i0 = tile * p.rows;
+    for (Walk at(t0, t_step, p.tiles); at.t < n_tiles; at.next()) {
+      const long long j = (PAIR ? 2LL * at.block + rank : (long long)at.block) * kPackRows + quad * 32 + lane;
+      const long long i0 = (long long)at.tile * p.rows;
       const float sw = j < g.N ? g.w_scale[j] : 0.f;
       const bool gone = !mbar_wait(&d_full[rd.slot], rd.phase, stop) || *stop;
       if (epi_any(gone)) break;  // all of these warps or none: they meet at barriers below
       tc_fence_after();
-      if (tile != scales) {
+      if (at.tile != scales) {
         for (int i = threadIdx.x; i < p.rows; i += kTcEpi * 32) a_scale[i] = i0 + i < g.n ? g.a_scale[i0 + i] : 0.f;
         epi_sync();
-        scales = tile;
+        scales = at.tile;
       }
       const uint32_t src = tmem + ((uint32_t)(quad * 32) << 16) + rd.slot * 128u;
       const int rows = (int)(g.n - i0 < p.rows ? g.n - i0 : p.rows);  // of this tile
       // the two warps of a quarter take 32 columns in turn
       OUT* out = static_cast<OUT*>(g.out) + (i0 + 32 * half) * g.ldo + j;
-      for (int c = 32 * half; c < p.rows; c += 64, out += 64 * g.ldo) {
-        float f[32];
-        tc_ld32(src + c, p.rows - c, f);
-        const int left = rows - c;
-        if (j < g.N) {
-          if (left >= 32) {
+      auto freed = [&] {  // the accumulator may be written again
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR)
+            mbar_arrive_first(&d_empty[rd.slot]);
+          else
+            mbar_arrive(&d_empty[rd.slot]);
+        }
+      };
+      if constexpr (PAIR && sizeof(OUT) == 2) {
+        // There is one accumulator: all of it into registers first, rounded, and to
+        // memory beside the next tile's instructions.
+        __nv_bfloat162 held[4][16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) store_out(out + i * g.ldo, f[i] * a_scale[c + i] * sw);
-          } else {
+        for (int q = 0; q < 4; ++q) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i < left) store_out(out + i * g.ldo, f[i] * a_scale[c + i] * sw);
+          for (int h = 0; h < 2; ++h) {
+            const int c = 32 * half + 64 * q + 16 * h;
+            if (c < p.rows) {
+              uint32_t v[16];
+              tc_ld16(src + c, v);
+              tc_ld16_wait(v);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float4 sa = reinterpret_cast<const float4*>(a_scale + c)[i];
+                held[q][8 * h + 2 * i] = scaled2(v[4 * i], v[4 * i + 1], sa.x, sa.y, sw);
+                held[q][8 * h + 2 * i + 1] = scaled2(v[4 * i + 2], v[4 * i + 3], sa.z, sa.w, sw);
+              }
+            }
           }
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (PAIR)
-          mbar_arrive_first(&d_empty[rd.slot]);
-        else
-          mbar_arrive(&d_empty[rd.slot]);
+        freed();
+        if (j < g.N) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int left = rows - (32 * half + 64 * q);
+            OUT* o = out + 64 * q * g.ldo;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (2 * i < left) *o = held[q][i].x;
+              o += g.ldo;
+              if (2 * i + 1 < left) *o = held[q][i].y;
+              o += g.ldo;
+              asm volatile("" : "+l"(o));  // stepped, not 32 row offsets kept in registers
+            }
+          }
+        }
+      } else {
+        for (int c = 32 * half; c < p.rows; c += 64, out += 64 * g.ldo) {
+          float f[32];
+          tc_ld32(src + c, p.rows - c, f);
+          const int left = rows - c;
+          if (j < g.N) {
+            if (left >= 32) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) store_out(out + i * g.ldo, f[i] * a_scale[c + i] * sw);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i < left) store_out(out + i * g.ldo, f[i] * a_scale[c + i] * sw);
+            }
+          }
+        }
+        freed();
       }
       rd.next(d_bufs);
     }
