@@ -36,7 +36,7 @@ def _vec(name, t, n, dtype, index):
     """The address of a contiguous device vector, None for None."""
     if t is None:
         return None
-    if t.dim() != 1 or t.numel() != n or t.dtype != dtype or t.get_device() != index or not t.is_contiguous():
+    if t.dim() != 1 or t.numel() != n or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
         _bad(name, "a contiguous %s tensor [%d] on cuda:%d" % (dtype, n, index), t)
     return t.data_ptr()
 
@@ -74,10 +74,14 @@ def sample_filtered(logits, temperature, u, top_k=None, top_p=None, min_p=None, 
     st = _status(d_status, index)
     if out_tokens is None:
         out_tokens = torch.empty(n, dtype=_I32, device=logits.device)
+        tok = out_tokens.data_ptr()
+    else:
+        tok = _vec("out_tokens", out_tokens, n, _I32, index)
     if out_logprobs is None:
         out_logprobs = torch.empty_like(temperature)
-    tok = _vec("out_tokens", out_tokens, n, _I32, index)
-    lp = _vec("out_logprobs", out_logprobs, n, _F32, index)
+        lp = out_logprobs.data_ptr()
+    else:
+        lp = _vec("out_logprobs", out_logprobs, n, _F32, index)
     _check("ds_sample_filtered", _lib.load().ds_sample_filtered(
         logits.data_ptr(), _CODE[logits.dtype], n, V, ld, tau, k, p, mp, up, tok, lp, st, _lib.raw_stream()))
     return out_tokens, out_logprobs
@@ -97,7 +101,9 @@ def quantize_rows(x, gain=None, eps=1e-6, out=None, out_scale=None, stream=None)
         _bad("out", "a contiguous int8 tensor [%d, %d] on cuda:%d" % (n, K, index), out)
     if out_scale is None:
         out_scale = torch.empty(n, dtype=_F32, device=x.device)
-    sp = _vec("out_scale", out_scale, n, _F32, index)
+        sp = out_scale.data_ptr()
+    else:
+        sp = _vec("out_scale", out_scale, n, _F32, index)
     _check("ds_quantize_rows", _lib.load().ds_quantize_rows(x.data_ptr(), _CODE[x.dtype], n, K, ld, gp, eps,
                                                             out.data_ptr(), sp, _lib.raw_stream()))
     return out, out_scale
