@@ -206,6 +206,23 @@ def test_a_row_does_not_depend_on_its_batch():
     assert np.array_equal(again, whole)
 
 
+def test_offsets_beyond_32_bits():
+    """More than 2^31 logits, apart by more than a row: the last rows are those of a call of their own."""
+    n, V, ld = 8650, 248320, 248323
+    buf = torch.empty(n * ld, dtype=torch.bfloat16, device=_dev())
+    assert buf.numel() > 2 ** 31
+    for i in range(0, buf.numel(), 1 << 28):
+        buf[i:i + (1 << 28)].normal_(0, 4)
+    x = buf.view(n, ld)[:, :V]
+    par = _params(n, 21)
+    tok, lp = _run(x, *par)
+    for i in (0, 4321, n - 40):
+        part = [v[i:i + 40] for v in par]
+        t, l = _run(x[i:i + 40].contiguous(), *part)
+        assert np.array_equal(tok[i:i + 40], t) and np.allclose(lp[i:i + 40], l, rtol=0, atol=1e-5, equal_nan=True)
+        assert np.array_equal(t, _integer_definition(x[i:i + 40], *part))
+
+
 @pytest.mark.parametrize("V", [11, 1025, 9000])
 def test_draws_follow_the_distribution(V):
     """u over an even grid: each kept token is drawn in proportion to its mass, to within two grid steps."""

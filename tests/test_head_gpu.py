@@ -153,6 +153,33 @@ def test_linear_i8_many_blocks_each_way(n, N, K):
     _check(out, a, sa, w, sw, K)
 
 
+@pytest.mark.parametrize("n,N,K", [(130, 25000, 640), (256, 41000, 300), (200, 20011, 1500), (777, 20100, 640),
+                                   (1939, 8300, 256), (330, 129, 2100)])
+def test_linear_i8_wide_tiles(n, N, K):
+    """Row tiles above 128, bf16: several tiles for each pair of CTAs, an odd number of channel blocks, ragged ends."""
+    a, sa, w, sw = _operands(n, N, K, 13)
+    out = pkg.linear_i8(a, sa, pkg.pack_i8(w, sw))
+    _check(out, a, sa, w, sw, K)
+
+
+@pytest.mark.parametrize("n", [2, 140])
+def test_linear_i8_longest_sum(n):
+    a, sa, w, sw = _operands(n, 130, 131071, 14)
+    out = pkg.linear_i8(a, sa, pkg.pack_i8(w, sw), dtype=torch.float32)
+    _check(out, a, sa, w, sw, 131071)
+
+
+def test_linear_i8_offsets_beyond_32_bits():
+    """Results of more than 2^32 bytes and 2^31 elements: the last rows are those of a call of their own."""
+    a, sa, w, sw = _operands(8800, 248320, 64, 15)
+    weight = pkg.pack_i8(w, sw)
+    out = pkg.linear_i8(a, sa, weight)
+    assert out.numel() > 2 ** 31
+    for i in (0, 4300, 8650):
+        assert torch.equal(out[i:i + 150], pkg.linear_i8(a[i:i + 150], sa[i:i + 150], weight))
+        _check(out[i:i + 150], a[i:i + 150], sa[i:i + 150], w, sw, 64)
+
+
 @pytest.mark.parametrize("n,N,K,pa,pw,po", [(3, 200, 100, 1, 3, 5), (20, 200, 100, 28, 0, 1), (140, 333, 129, 7, 7, 3)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_linear_i8_strides(n, N, K, pa, pw, po, dtype):

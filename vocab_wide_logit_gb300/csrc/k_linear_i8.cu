@@ -1,5 +1,39 @@
 // k_linear_i8.cu -- product of 8-bit integers scaled by row and channel:
 // out[i][j] = (sum_k a[i][k] w[j][k]) * a_scale[i] * w_scale[j].
+//
+// The mathematics. Integers of 8 bits are exact in fp16 and their products (at most
+// 2^14) in fp32, so the tensor cores' fp16 products with fp32 sums are the integer
+// product as long as a running sum stays below 2^24. The 8-bit integer rate of this
+// GPU is far below its fp16 rate, so nothing is lost by that.
+//
+// The layout. The weight is the large operand and is read once, as 8 bits. It is
+// packed once into blocks of 128 channels x 128 inputs (16 KB, consecutive in memory),
+// which bulk copies bring into a ring in shared memory. Warps widen a block (a byte
+// permutation and a subtraction for two values) and write it to tensor memory as the
+// instruction's first operand, which costs no shared memory and no second pass. The
+// rows of a are the second operand: a short kernel before this one writes them as
+// fp16 tiles in the swizzled order that the instruction reads, or ds_quantize_rows
+// does so itself. So one instruction has 128 channels x `rows` rows x 16 inputs.
+// Each of loads, widening, instructions and results has warps of its own, joined by
+// mbarriers, and the weight loads start before the row tiles are there.
+//   rows <= 128  a CTA per 128 channels. Two accumulators, so that results go out
+//                beside the next tile's instructions. A row tile that fits stays in
+//                shared memory for all channel blocks.
+//   rows > 128   a pair of CTAs per 256 channels, one instruction for both, each with
+//                half of the row tile: 96 KB instead of 160 KB through shared memory
+//                per block of 128 inputs. One CTA alone took 1150-1190 cycles per block
+//                of 1024 of instructions and 172 us where the pair takes 151 (256 rows
+//                x 248320 x 2048; 777 x 20011 x 4096: 122 and 97 us).
+//
+// What bounds it (bf16 out, K and the rest as stated):
+//   24 x 248320 x 2048    82 us with its ds_quantize_rows, 522 MB at 6.4 TB/s: HBM
+//   256 x 248320 x 2048   149 us, 260 GFLOP at 1.75 PFLOP/s, tensor pipe 78% busy; the
+//                         rest is reading the accumulator, 128 KB in 2300-2600 cycles
+//                         per tile (tensor memory gives about 50 bytes a cycle), and the
+//                         handing over to the next tile
+//   777 x 20011 x 4096    97 us, 1.31 PFLOP/s: the same, and 316 tiles on 76 pairs
+//   1939 x 8200 x 1024    33 us: tiles of 8 blocks, a third of the time between them
+//   one row x 8200 x 1024 9 us with its ds_quantize_rows: latency, 65 tiles on 152 SMs
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -312,9 +346,12 @@ struct TcPlan {
 }  // namespace
 
 // Estimated cycles of a call cut into `tiles` row tiles. Measured: an instruction
-// takes rows / 2 cycles, but 100 at least (its weights come from tensor memory);
-// a tile's results take 1500 and 10 a row, which overlap with the next tile's
-// instructions only where two accumulators fit (rows <= 128).
+// takes rows / 2 cycles, but 100 at least (its 4 KB of weights come from tensor
+// memory); between tiles lie 1500 cycles and 10 a row, beside the next tile's
+// instructions only where two accumulators fit (rows <= 128). The choices that it
+// makes and the next ones: 1939 x 8200 x 1024 in 9, 8, 11 tiles 33.4, 35.3, 37.4 us;
+// 777 x 20011 x 4096 in 4, 5, 7 tiles 97, 111, 135 us; 256 x 248320 x 2048 in 1, 2
+// tiles 151, 220 us.
 static long long tc_cycles(int n, int N, int kb, int tiles, int rows) {
   const long long ctas = ((N + kPackRows - 1LL) / kPackRows) * tiles, waves = (ctas + kTcSms - 1) / kTcSms;
   const long long mma = 8LL * kb * (rows > 200 ? rows / 2 : 100), out = 1500 + 10LL * rows;
@@ -353,7 +390,8 @@ static TcPlan tc_plan(int n, int N, int K) {
 
 static_assert(kTcWSlots % 2 == 0 && kTcASlots % 2 == 0, "each converting group keeps its slots");
 
-// One CTA per SM walks tiles of 128 channels x `rows` rows of a.
+// One CTA per SM, or one pair of CTAs per two, walks tiles of 128 or 256 channels x
+// `rows` rows of a.
 template <typename OUT, bool PAIR>
 __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan p) {
   extern __shared__ uint8_t dyn[];

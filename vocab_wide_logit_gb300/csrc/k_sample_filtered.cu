@@ -415,14 +415,14 @@ __device__ __noinline__ int row_exact(const T* p, int V, const RowParams& q, flo
 // row's CTA reads it once (ONE_WALK): the cut and a reference for the sums come
 // from a sixteenth of the row, and the logits that turn out high are read again
 // singly. Splitting every row over a cluster instead took 203 us where this takes
-// 82 (256 rows x 248320, top-p: each cluster barrier waits for the slowest CTA of
+// 80 (256 rows x 248320, top-p: each cluster barrier waits for the slowest CTA of
 // a row's latency-bound steps); two walks per CTA 96 us, the second from HBM again
 // because 256 rows do not fit L2.
 //
 // What bounds it: long rows HBM first, then the latency of the steps behind the
-// walk (52 us for 256 x 248320 with a top-k, 19 of them at the copy rate); short
+// walk (51 us for 256 x 248320 with a top-k, 19 of them at the copy rate); short
 // rows instructions and their fetch (3100 per row of 1025 at 56% of the issue
-// rate, 109 us for 15510 rows of 1025); single rows the barriers (9 us for 1025,
+// rate, 107 us for 15510 rows of 1025); single rows the barriers (9 us for 1025,
 // 19 us for 248320).
 namespace {
 
