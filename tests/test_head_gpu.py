@@ -314,3 +314,40 @@ def test_head_reports_a_bad_hidden_state():
     assert int(st.item()) == pkg.DS_DEV_ERR_LOGITS
     assert int(tok[3]) == -1 and bool(torch.isnan(lp[3]))
     assert bool((tok[[0, 1, 2, 4]] >= 0).all())
+
+
+def test_short_way_and_checked_way_agree():
+    """Calls that make their outputs go past the interpreter, others through it: the same answers, the same refusals."""
+    dev = _dev()
+    n, N, K = 5, 700, 192
+    a, sa, w, sw = _operands(n, N, K, 16)
+    weight = pkg.pack_i8(w, sw)
+    h = (torch.randn((n, K), generator=torch.Generator().manual_seed(1)) * 2).to(dev)
+    head = pkg.Int8Head(w, sw, gain=torch.ones(K, device=dev))
+    tau, u = torch.ones(n, device=dev), torch.arange(n, device=dev) / n
+    k = torch.full((n,), 20, dtype=torch.int32, device=dev)
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    for dtype in (torch.bfloat16, torch.float32):
+        out = pkg.linear_i8(a, sa, weight, dtype=dtype)
+        assert out.dtype == dtype and torch.equal(out, pkg.linear_i8(a, sa, weight, dtype=dtype, d_status=st))
+        x = head.logits(h.to(dtype), dtype=dtype)
+        assert x.dtype == dtype and torch.equal(x, head.logits(h.to(dtype), dtype=dtype, d_status=st))
+        s = pkg.sample_filtered(x, tau, u, top_k=k)
+        t = pkg.sample_filtered(x, tau, u, top_k=k, d_status=st)
+        assert torch.equal(s[0], t[0]) and torch.equal(s[1], t[1]) and s[0].dtype == torch.int32
+    assert int(st.item()) == 0
+    for bad in (dict(temperature=tau.double()), dict(temperature=tau[:4]), dict(temperature=None), dict(u=u.cpu()), dict(u=None),
+                dict(u=torch.zeros((n, 2), device=dev)[:, 0]),
+                dict(u=u.view(n, 1)), dict(top_k=k.long()), dict(top_p=k), dict(min_p=tau.half()), dict(logits=x.t()),
+                dict(logits=x[0]), dict(logits=x.half()), dict(logits=x.cpu())):
+        with pytest.raises(ValueError):
+            pkg.sample_filtered(**dict(dict(logits=x, temperature=tau, u=u), **bad))
+    for args in ((a.int(), sa, weight), (a[:, :100], sa, weight), (a, sa[:3], weight), (a, None, weight), (a, sa.double(), weight),
+                 (a.cpu(), sa, weight)):
+        with pytest.raises(ValueError):
+            pkg.linear_i8(*args)
+    for x in (h[:, :100], h.half(), h[0], h.cpu()):
+        with pytest.raises(ValueError):
+            head.logits(x)
+    with pytest.raises(ValueError):
+        pkg.linear_i8(a, sa, weight, dtype=torch.float16)

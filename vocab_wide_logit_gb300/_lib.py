@@ -6,6 +6,7 @@ stream into a handle. There is no fallback: if the library is missing the
 import of a call raises.
 """
 import ctypes
+import importlib.util
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -35,6 +36,7 @@ DS_DTYPE_F32 = 0
 DS_DTYPE_BF16 = 1
 
 _lib = None
+_calls = None
 
 
 class DsError(RuntimeError):
@@ -199,6 +201,24 @@ def ds_reveal(scores, tokens, seq_lens, reveal_counts, canvas, revealed=None, d_
     if check and rc != DS_OK:
         raise DsError("ds_reveal", rc)
     return rc
+
+
+def calls():
+    """The module that runs the serving head's calls on torch tensors (csrc/py_calls.cpp), bound to the library."""
+    global _calls
+    if _calls is None:
+        L, path = load(), os.path.join(os.path.dirname(LIB_PATH), "ds_calls.so")
+        if not os.path.exists(path):
+            raise OSError("ds_calls.so not built at %s: run __graft_entry__.build() or "
+                          "python vocab_wide_logit_gb300/build.py" % path)
+        import torch  # noqa: F401  (its libraries are what the module links to)
+        spec = importlib.util.spec_from_file_location("ds_calls", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.ds_sample_filtered, L.ds_linear_i8_workspace, L.ds_linear_i8, L.ds_head_i8_workspace, L.ds_head_i8)))
+        _calls = module
+    return _calls
 
 
 def raw_stream():

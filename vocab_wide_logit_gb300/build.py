@@ -1,18 +1,21 @@
-"""Build libdsample.so in-tree for sm_103a with nvcc (no CMake, no torch extension).
+"""Build libdsample.so in-tree for sm_103a with nvcc (no CMake), and ds_calls.so, its short way from torch tensors.
 
 The Gumbel bound table is generated first, then each translation unit is
 compiled in parallel and linked into vocab_wide_logit_gb300/_build/libdsample.so.
 """
 import concurrent.futures
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libdsample.so")
+CALLS = os.path.join(OUT, "ds_calls.so")
 INCLUDE = os.path.join(ROOT, "include")
 SOURCES = ["ds_api.cu", "k_greedy.cu", "k_sample_warp.cu", "k_sample_cluster.cu", "k_sample_stream.cu",
            "k_merge.cu", "k_reveal.cu", "k_log_softmax.cu", "k_sample_filtered.cu", "k_quantize.cu",
@@ -35,6 +38,16 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _calls_command(src, out):
+    """g++ for the CPython module, against the headers and libraries of the installed torch and CUDA runtime."""
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    inc = [INCLUDE, os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    return (["g++", "-std=c++17", "-O2", "-fPIC", "-shared"] + ["-I" + i for i in inc] + [src, "-o", out,
+            "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
     os.makedirs(OUT, exist_ok=True)
     table = os.path.join(OUT, "gumbel_bounds.inc")
@@ -53,6 +66,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         o = os.path.join(OUT, src.replace(".cu", ".o"))
         if force or ptxas_verbose or _stale(o, [s] + common):
             jobs.append([nvcc()] + flags + ["-c", s, "-o", o])
+    src = os.path.join(CSRC, "py_calls.cpp")
+    calls = CALLS + ".tmp%d" % os.getpid()
+    new_calls = force or _stale(CALLS, [src, os.path.join(INCLUDE, "dsample.h"), os.path.abspath(__file__)])
+    cuda_jobs = len(jobs)
+    if new_calls:
+        jobs.append(_calls_command(src, calls))
     if jobs:
         with concurrent.futures.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
             results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
@@ -60,9 +79,11 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             if verbose or ptxas_verbose or r.returncode != 0:
                 sys.stderr.write(r.stdout + r.stderr)
             if r.returncode != 0:
-                raise RuntimeError("nvcc failed: " + " ".join(cmd))
+                raise RuntimeError("compiler failed: " + " ".join(cmd))
     objs = [os.path.join(OUT, s.replace(".cu", ".o")) for s in SOURCES]
-    if force or jobs or _stale(LIB, objs):
+    if new_calls:
+        os.replace(calls, CALLS)
+    if force or cuda_jobs or _stale(LIB, objs):
         tmp = LIB + ".tmp%d" % os.getpid()
         subprocess.run([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart"], check=True)
         os.replace(tmp, LIB)

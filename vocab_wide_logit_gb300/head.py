@@ -3,8 +3,9 @@ temperature, top-k, top-p and min-p.
 
 Functions allocate their outputs and check their tensors (a tensor of another type or shape would be read as if it
 were the expected one); the compute is in the library. Outputs and workspaces are allocated on the stream that the
-call runs on. At decoding sizes a call takes about as long to issue as to run, so the checks are plain comparisons
-and the library is called with plain integers.
+call runs on. At decoding sizes a call takes about as long to issue as to run, so the usual calls (outputs made here, no
+status word) go through _lib.calls(), which checks and launches without the interpreter and hands everything else back;
+here the checks are plain comparisons and the library is called with plain integers.
 """
 import torch
 
@@ -63,6 +64,10 @@ def sample_filtered(logits, temperature, u, top_k=None, top_p=None, min_p=None, 
     if stream is not None:
         with torch.cuda.stream(stream):
             return sample_filtered(logits, temperature, u, top_k, top_p, min_p, out_tokens, out_logprobs, d_status)
+    if out_tokens is None and out_logprobs is None and d_status is None:
+        r = _lib.calls().sample(logits, temperature, u, top_k, top_p, min_p)
+        if r is not None:
+            return r if type(r) is tuple else _check("ds_sample_filtered", r)
     n, V, ld, index = _rows("logits", logits, _CODE)
     if temperature is None or u is None:
         raise ValueError("temperature and u are needed")
@@ -148,6 +153,10 @@ def linear_i8(a, a_scale, weight, out=None, dtype=torch.bfloat16, d_status=None,
     if stream is not None:
         with torch.cuda.stream(stream):
             return linear_i8(a, a_scale, weight, out, dtype, d_status)
+    if out is None and d_status is None and dtype in _CODE:
+        r = _lib.calls().linear(a, a_scale, weight.packed, weight.scale, weight.N, weight.K, _CODE[dtype])
+        if r is not None:
+            return _check("ds_linear_i8", r) if type(r) is int else r
     n, K, lda, index = _rows("a", a, (_I8,))
     N = weight.N
     if K != weight.K or index != weight.packed.get_device():
@@ -186,6 +195,11 @@ class Int8Head:
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.logits(hidden, out, dtype, d_status)
+        if out is None and d_status is None and dtype in _CODE:
+            w = self.weight
+            r = _lib.calls().head(hidden, self.gain, w.packed, w.scale, w.N, w.K, _CODE[dtype], self.eps)
+            if r is not None:
+                return _check("ds_head_i8", r) if type(r) is int else r
         n, K, ld, index = _rows("hidden", hidden, _CODE)
         weight, gain = self.weight, self.gain
         if K != weight.K or index != weight.packed.get_device():
