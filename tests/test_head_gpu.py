@@ -335,6 +335,11 @@ def test_short_way_and_checked_way_agree():
         s = pkg.sample_filtered(x, tau, u, top_k=k)
         t = pkg.sample_filtered(x, tau, u, top_k=k, d_status=st)
         assert torch.equal(s[0], t[0]) and torch.equal(s[1], t[1]) and s[0].dtype == torch.int32
+        for gain in (None, head.gain):
+            q, s = pkg.quantize_rows(h.to(dtype), gain=gain, eps=1e-5)
+            r = torch.empty_like(s)
+            p, _ = pkg.quantize_rows(h.to(dtype), gain=gain, eps=1e-5, out_scale=r)
+            assert torch.equal(q, p) and torch.equal(s, r) and q.dtype == torch.int8
     assert int(st.item()) == 0
     for bad in (dict(temperature=tau.double()), dict(temperature=tau[:4]), dict(temperature=None), dict(u=u.cpu()), dict(u=None),
                 dict(u=torch.zeros((n, 2), device=dev)[:, 0]),
@@ -349,5 +354,8 @@ def test_short_way_and_checked_way_agree():
     for x in (h[:, :100], h.half(), h[0], h.cpu()):
         with pytest.raises(ValueError):
             head.logits(x)
+    for x, gain in ((h.half(), None), (h[0], None), (h.t(), None), (h, sa), (h, torch.ones(K)), (h.cpu(), None)):
+        with pytest.raises(ValueError):
+            pkg.quantize_rows(x, gain=gain)
     with pytest.raises(ValueError):
         pkg.linear_i8(a, sa, weight, dtype=torch.float16)

@@ -216,7 +216,8 @@ def calls():
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-            L.ds_sample_filtered, L.ds_linear_i8_workspace, L.ds_linear_i8, L.ds_head_i8_workspace, L.ds_head_i8)))
+            L.ds_sample_filtered, L.ds_linear_i8_workspace, L.ds_linear_i8, L.ds_head_i8_workspace, L.ds_head_i8,
+            L.ds_quantize_rows)))
         _calls = module
     return _calls
 

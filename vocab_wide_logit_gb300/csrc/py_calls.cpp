@@ -21,6 +21,7 @@
 namespace {
 
 decltype(&ds_sample_filtered) p_sample = nullptr;
+decltype(&ds_quantize_rows) p_quantize = nullptr;
 decltype(&ds_linear_i8_workspace) p_linear_ws = nullptr;
 decltype(&ds_linear_i8) p_linear = nullptr;
 decltype(&ds_head_i8_workspace) p_head_ws = nullptr;
@@ -68,6 +69,15 @@ at::TensorOptions on(int device, at::ScalarType t) {
 
 void* stream(int device) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream(); }
 
+PyObject* both(at::Tensor first, at::Tensor second) {
+  PyObject* a = THPVariable_Wrap(std::move(first));
+  PyObject* b = a ? THPVariable_Wrap(std::move(second)) : nullptr;
+  PyObject* r = b ? PyTuple_Pack(2, a, b) : nullptr;
+  Py_XDECREF(a);
+  Py_XDECREF(b);
+  return r;
+}
+
 // sample(logits, temperature, u, top_k, top_p, min_p) -> (tokens, logprobs)
 PyObject* sample(PyObject*, PyObject* const* v, Py_ssize_t count) {
   HANDLE_TH_ERRORS
@@ -83,13 +93,24 @@ PyObject* sample(PyObject*, PyObject* const* v, Py_ssize_t count) {
   const ds_status rc = p_sample(x.p, c, (int32_t)x.n, (int32_t)x.k, x.ld, (const float*)tau, (const int32_t*)k,
                                 (const float*)p, (const float*)mp, (const float*)u, (int32_t*)tok.data_ptr(),
                                 (float*)lp.data_ptr(), nullptr, stream(x.device));
-  if (rc != DS_OK) return PyLong_FromLong(rc);
-  PyObject* a = THPVariable_Wrap(std::move(tok));
-  PyObject* b = a ? THPVariable_Wrap(std::move(lp)) : nullptr;
-  PyObject* r = b ? PyTuple_Pack(2, a, b) : nullptr;
-  Py_XDECREF(a);
-  Py_XDECREF(b);
-  return r;
+  return rc != DS_OK ? PyLong_FromLong(rc) : both(std::move(tok), std::move(lp));
+  END_HANDLE_TH_ERRORS
+}
+
+// quantize(x, gain, eps) -> (q, scale)
+PyObject* quantize(PyObject*, PyObject* const* v, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
+  Rows x;
+  int32_t c;
+  void* gain;
+  const at::Tensor* t = count == 3 && p_quantize ? tensor(v[0]) : nullptr;
+  if (!rows(t, &x) || !code(t->scalar_type(), &c) || !vec(v[1], x.k, at::kFloat, x.device, true, &gain)) Py_RETURN_NONE;
+  const double eps = PyFloat_AsDouble(v[2]);
+  if (PyErr_Occurred()) return nullptr;
+  at::Tensor q = at::empty({x.n, x.k}, on(x.device, at::kChar)), scale = at::empty({x.n}, on(x.device, at::kFloat));
+  const ds_status rc = p_quantize(x.p, c, (int32_t)x.n, (int32_t)x.k, x.ld, (const float*)gain, (float)eps,
+                                  (int8_t*)q.data_ptr(), (float*)scale.data_ptr(), stream(x.device));
+  return rc != DS_OK ? PyLong_FromLong(rc) : both(std::move(q), std::move(scale));
   END_HANDLE_TH_ERRORS
 }
 
@@ -162,12 +183,12 @@ PyObject* head(PyObject*, PyObject* const* v, Py_ssize_t count) {
 
 // bind(addresses of the entry points)
 PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t count) {
-  void* p[5];
-  if (count != 5) {
-    PyErr_SetString(PyExc_TypeError, "bind() takes five addresses");
+  void* p[6];
+  if (count != 6) {
+    PyErr_SetString(PyExc_TypeError, "bind() takes six addresses");
     return nullptr;
   }
-  for (int i = 0; i < 5; ++i) {
+  for (int i = 0; i < 6; ++i) {
     p[i] = PyLong_AsVoidPtr(v[i]);
     if (PyErr_Occurred()) return nullptr;
   }
@@ -176,6 +197,7 @@ PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t count) {
   p_linear = reinterpret_cast<decltype(p_linear)>(p[2]);
   p_head_ws = reinterpret_cast<decltype(p_head_ws)>(p[3]);
   p_head = reinterpret_cast<decltype(p_head)>(p[4]);
+  p_quantize = reinterpret_cast<decltype(p_quantize)>(p[5]);
   Py_RETURN_NONE;
 }
 
@@ -183,6 +205,7 @@ PyMethodDef methods[] = {
     {"sample", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(sample)), METH_FASTCALL, nullptr},
     {"linear", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(linear)), METH_FASTCALL, nullptr},
     {"head", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(head)), METH_FASTCALL, nullptr},
+    {"quantize", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(quantize)), METH_FASTCALL, nullptr},
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "ds_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -98,6 +98,10 @@ def quantize_rows(x, gain=None, eps=1e-6, out=None, out_scale=None, stream=None)
     if stream is not None:
         with torch.cuda.stream(stream):
             return quantize_rows(x, gain, eps, out, out_scale)
+    if out is None and out_scale is None:
+        r = _lib.calls().quantize(x, gain, eps)
+        if r is not None:
+            return r if type(r) is tuple else _check("ds_quantize_rows", r)
     n, K, ld, index = _rows("x", x, _CODE)
     gp = _vec("gain", gain, K, _F32, index)
     if out is None:
