@@ -1,0 +1,117 @@
+"""Serving-head calls with tensors of another device, or of sizes that the library's 32-bit counts cannot hold: refused
+on the host before anything is launched. Stand-ins for the tensors and for the library; no GPU is used."""
+import types
+
+import pytest
+import torch
+
+import vocab_wide_logit_gb300 as pkg
+from vocab_wide_logit_gb300 import _lib, head
+
+
+class Tensor:
+    """What the wrappers ask of a device tensor."""
+
+    def __init__(self, shape, dtype, index=0, address=0x100000):
+        self.shape, self.dtype, self.index, self.address = tuple(shape), dtype, index, address
+        self.is_cuda, self.device = True, torch.device("cuda", index)
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        n = 1
+        for s in self.shape:
+            n *= s
+        return n
+
+    def stride(self, i=None):
+        s = [1]
+        for n in self.shape[:0:-1]:
+            s.insert(0, s[0] * n)
+        return tuple(s) if i is None else s[i]
+
+    def get_device(self):
+        return self.index
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return self.address
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def is_floating_point(self):
+        return self.dtype.is_floating_point
+
+
+F32, BF16, I8, I32 = torch.float32, torch.bfloat16, torch.int8, torch.int32
+
+
+@pytest.fixture
+def launched(monkeypatch):
+    """The names of the library's entry points that a call reached, with device 0 current."""
+    names = []
+
+    def entry(name):
+        def call(*args):
+            names.append(name)
+            return 64 if name.endswith("workspace") or name.endswith("bytes") else _lib.DS_OK
+        return call
+
+    lib = types.SimpleNamespace(**{name: entry(name) for name in _lib.EXPORTED})
+    none = types.SimpleNamespace(**{name: lambda *a: None for name in ("sample", "quantize", "linear", "head")})
+    monkeypatch.setattr(_lib, "load", lambda *a: lib)
+    monkeypatch.setattr(_lib, "calls", lambda: none)
+    monkeypatch.setattr(_lib, "raw_stream", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(cuda_stream=0))
+    make = lambda *shape, dtype=F32, device=None: Tensor(  # noqa: E731
+        shape[0] if isinstance(shape[0], (tuple, list)) else shape, dtype, device.index)
+    monkeypatch.setattr(torch, "empty", make)
+    monkeypatch.setattr(torch, "empty_like", lambda t: Tensor(t.shape, t.dtype, t.index))
+    return names
+
+
+def _weight(N, K, index):
+    w = object.__new__(pkg.PackedI8)
+    w.N, w.K, w.packed, w.scale = N, K, Tensor((N * K,), torch.uint8, index), Tensor((N,), F32, index)
+    return w
+
+
+def _head(N, K, index):
+    h = object.__new__(pkg.Int8Head)
+    h.weight, h.gain, h.eps = _weight(N, K, index), None, 1e-6
+    return h
+
+
+def _all_calls(index, n=4, V=16, K=32, N=24):
+    t = lambda shape, dtype: Tensor(shape, dtype, index)  # noqa: E731
+    v = t((n,), F32)
+    return {
+        "sample": lambda: pkg.sample_filtered(t((n, V), BF16), v, v),
+        "sample, outputs given": lambda: pkg.sample_filtered(t((n, V), F32), v, v, out_tokens=t((n,), I32), out_logprobs=v),
+        "sample, status": lambda: pkg.sample_filtered(t((n, V), F32), v, v, d_status=t((1,), I32)),
+        "quantize": lambda: pkg.quantize_rows(t((n, K), BF16)),
+        "quantize, outputs given": lambda: pkg.quantize_rows(t((n, K), BF16), out=t((n, K), I8), out_scale=v),
+        "linear": lambda: pkg.linear_i8(t((n, K), I8), v, _weight(N, K, index)),
+        "linear, output given": lambda: pkg.linear_i8(t((n, K), I8), v, _weight(N, K, index), out=t((n, N), BF16)),
+        "logits": lambda: _head(N, K, index).logits(t((n, K), BF16)),
+        "head": lambda: _head(N, K, index).sample(t((n, K), BF16), v, v),
+        "pack": lambda: pkg.pack_i8(t((N, K), I8), t((N,), F32)),
+    }
+
+
+@pytest.mark.parametrize("name", sorted(_all_calls(0)))
+def test_tensors_of_the_current_device_are_launched(launched, name):
+    _all_calls(0)[name]()
+    assert launched
+
+
+@pytest.mark.parametrize("name", sorted(_all_calls(0)))
+def test_tensors_of_another_device_are_refused(launched, name):
+    with pytest.raises(ValueError, match="current device"):
+        _all_calls(1)[name]()
+    assert not launched

@@ -21,9 +21,12 @@ def _bad(name, want, t):
 
 
 def _rows(name, t, codes):
-    """(rows, columns, elements between rows, device index) of a device matrix whose rows are dense."""
+    """(rows, columns, elements between rows, device index) of a matrix on the current device whose rows are dense. The
+    launch goes to that device's stream, where the addresses of another device's tensors would fault or race."""
     if t.dim() != 2 or t.dtype not in codes or not t.is_cuda:
         _bad(name, "a 2-d cuda tensor of %s" % "/".join(str(d) for d in codes), t)
+    if t.get_device() != torch.cuda.current_device():
+        _bad(name, "a tensor on the current device (cuda:%d, or that of the given stream)" % torch.cuda.current_device(), t)
     n, k = t.shape
     ld, step = t.stride()
     if n <= 1:
@@ -123,12 +126,12 @@ class PackedI8:
     calls on several streams may share it."""
 
     def __init__(self, w, scale, stream=None):
-        N, K, ld, index = _rows("w", w, (_I8,))
         if scale is None:
             raise ValueError("scale is needed")
-        _vec("scale", scale, N, _F32, index)
-        self.N, self.K, self.scale = N, K, scale
         with torch.cuda.stream(stream):
+            N, K, ld, index = _rows("w", w, (_I8,))
+            _vec("scale", scale, N, _F32, index)
+            self.N, self.K, self.scale = N, K, scale
             self.packed = torch.empty(_lib.packed_i8_bytes(N, K), dtype=_U8, device=w.device)
             _lib.ds_pack_i8(w, self.packed, N, K, ld)
 
