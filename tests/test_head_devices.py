@@ -115,3 +115,15 @@ def test_tensors_of_another_device_are_refused(launched, name):
     with pytest.raises(ValueError, match="current device"):
         _all_calls(1)[name]()
     assert not launched
+
+
+@pytest.mark.parametrize("n,K", [(2 ** 32 + 5, 1), (2 ** 31, 2), (3, 2 ** 32 + 8)])
+def test_sizes_beyond_32_bits_are_refused(launched, n, K):
+    """The library counts rows and columns in 32 bits: 2^32 + 5 rows would be read as 5, the rest left unwritten."""
+    v = Tensor((n,), F32)
+    for call in (lambda: pkg.sample_filtered(Tensor((n, K), BF16), v, v), lambda: pkg.quantize_rows(Tensor((n, K), BF16)),
+                 lambda: pkg.linear_i8(Tensor((n, K), I8), v, _weight(24, K, 0)),
+                 lambda: pkg.pack_i8(Tensor((n, K), I8), v), lambda: _head(24, K, 0).logits(Tensor((n, K), BF16))):
+        with pytest.raises(ValueError, match="2147483647"):
+            call()
+    assert not launched

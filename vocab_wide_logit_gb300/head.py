@@ -12,6 +12,7 @@ import torch
 from . import _lib
 
 _F32, _I32, _I8, _U8, _BF16 = torch.float32, torch.int32, torch.int8, torch.uint8, torch.bfloat16
+_INT_MAX = 2 ** 31 - 1
 _CODE = {_F32: _lib.DS_DTYPE_F32, _BF16: _lib.DS_DTYPE_BF16}
 
 
@@ -28,6 +29,8 @@ def _rows(name, t, codes):
     if t.get_device() != torch.cuda.current_device():
         _bad(name, "a tensor on the current device (cuda:%d, or that of the given stream)" % torch.cuda.current_device(), t)
     n, k = t.shape
+    if n > _INT_MAX or k > _INT_MAX:  # would lose their upper bits on the way into the library
+        _bad(name, "at most %d rows and columns" % _INT_MAX, t)
     ld, step = t.stride()
     if n <= 1:
         ld = k
