@@ -67,7 +67,7 @@ def launched(monkeypatch):
     monkeypatch.setattr(_lib, "calls", lambda: none)
     monkeypatch.setattr(_lib, "raw_stream", lambda: 0)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(cuda_stream=0))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(cuda_stream=0, device_index=0))
     make = lambda *shape, dtype=F32, device=None: Tensor(  # noqa: E731
         shape[0] if isinstance(shape[0], (tuple, list)) else shape, dtype, device.index)
     monkeypatch.setattr(torch, "empty", make)
@@ -127,3 +127,41 @@ def test_sizes_beyond_32_bits_are_refused(launched, n, K):
         with pytest.raises(ValueError, match="2147483647"):
             call()
     assert not launched
+
+
+def _named_calls(index, B=2, C=3, P=4, V=16, N=24, K=32):
+    """The calls under the C names, which take the current stream when none is given."""
+    t = lambda shape, dtype=F32: Tensor(shape, dtype, index)  # noqa: E731
+    ids, per, cells, v = t((B,), I32), t((B,)), t((C, P)), t((P,))
+    return {
+        "sample": lambda **kw: pkg.ds_sample(ids, t((C, P, V), BF16), None, ids, per, per, 0.5, 0, 0, t((C, P), I32), cells,
+                                             **kw),
+        "sample_ex": lambda **kw: pkg.ds_sample(ids, t((C, P, V), BF16), None, ids, per, per, 0.5, 0, 0, t((C, P), I32),
+                                                cells, top_ratios=per, **kw),
+        "greedy": lambda **kw: pkg.ds_greedy_lse(t((P, V), BF16), v, v, t((P,), I32), **kw),
+        "merge": lambda **kw: pkg.ds_merge_triples(t((P, 2, 3)), v, v, t((P,), I32), **kw),
+        "log_softmax": lambda **kw: pkg.ds_log_softmax(t((P, V), BF16), t((P, V)), v, v, t((P,), I32), **kw),
+        "reveal": lambda **kw: pkg.ds_reveal(cells, t((C, P), I32), ids, ids, t((C, P), I32), **kw),
+        "filtered": lambda **kw: pkg.ds_sample_filtered(t((P, V)), v, v, t((P,), I32), v, **kw),
+        "quantize": lambda **kw: pkg.ds_quantize_rows(t((P, K), BF16), t((P, K), I8), v, **kw),
+        "pack": lambda **kw: pkg.ds_pack_i8(t((N, K), I8), t((N * K,), torch.uint8), **kw),
+        "linear": lambda **kw: pkg.ds_linear_i8(t((P, K), I8), v, t((N * K,), torch.uint8), t((N,)), t((P, N)), N, K, **kw),
+        "head": lambda **kw: pkg.ds_head_i8(t((P, K), BF16), t((N * K,), torch.uint8), t((N,)), t((P, N)),
+                                            t((64,), torch.uint8), N, **kw),
+    }
+
+
+@pytest.mark.parametrize("name", sorted(_named_calls(0)))
+def test_calls_by_c_name_keep_to_the_device_of_their_stream(launched, monkeypatch, name):
+    def stream(i):
+        return types.SimpleNamespace(cuda_stream=0, device_index=i)
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: stream(0))
+    with pytest.raises(ValueError, match="stream"):
+        _named_calls(1)[name]()
+    with pytest.raises(ValueError, match="stream"):
+        _named_calls(0)[name](stream=stream(1))
+    assert not launched
+    _named_calls(0)[name]()
+    _named_calls(0)[name](stream=stream(0))
+    assert len(launched) == 2

@@ -112,10 +112,15 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream):
+def _stream(stream, t):
+    """Handle of the stream (None: the current one) that a call on t is launched on. The addresses of another device's
+    tensors would fault or race there."""
     import torch
     if stream is None:
         stream = torch.cuda.current_stream()
+    if t is not None and t.is_cuda and t.get_device() != stream.device_index:
+        raise ValueError("a tensor on cuda:%d for a stream of cuda:%d (the current stream unless one is given)"
+                         % (t.get_device(), stream.device_index))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -137,14 +142,14 @@ def ds_sample(request_ids, c_logits, u_logits, seq_lens, guidance, temperature, 
         rc = load().ds_sample(_ptr(request_ids), _ptr(c_logits), _ptr(u_logits), _ptr(seq_lens), int(B),
                               int(C), int(P), int(V), _ptr(guidance), _ptr(temperature), float(top_ratio),
                               int(seed) & (2 ** 64 - 1), int(iteration), _ptr(out_tokens), _ptr(out_logprobs),
-                              _ptr(d_status), _stream(stream))
+                              _ptr(d_status), _stream(stream, c_logits))
         name = "ds_sample"
     else:
         rc = load().ds_sample_ex(_ptr(request_ids), _ptr(c_logits), _ptr(u_logits), _ptr(seq_lens), int(B),
                                  int(C), int(P), int(V), _ptr(guidance), _ptr(temperature), _ptr(top_ratios),
                                  float(top_ratio), int(seed) & (2 ** 64 - 1), _ptr(iterations), int(iteration),
                                  flags, _ptr(out_tokens), _ptr(out_logprobs),
-                                 _ptr(d_status), _stream(stream))
+                                 _ptr(d_status), _stream(stream, c_logits))
         name = "ds_sample_ex"
     if check and rc != DS_OK:
         raise DsError(name, rc)
@@ -156,7 +161,7 @@ def ds_greedy_lse(logits, out_max, out_lse, out_argmax, n=None, V=None, stream=N
     if n is None:
         n, V = logits.shape
     rc = load().ds_greedy_lse(_ptr(logits), int(n), int(V), _ptr(out_max), _ptr(out_lse), _ptr(out_argmax),
-                              _stream(stream))
+                              _stream(stream, logits))
     if check and rc != DS_OK:
         raise DsError("ds_greedy_lse", rc)
     return rc
@@ -167,7 +172,7 @@ def ds_merge_triples(triples, out_max, out_lse, out_argmax, n=None, shards=None,
     if n is None:
         n, shards = triples.shape[0], triples.shape[1]
     rc = load().ds_merge_triples(_ptr(triples), int(n), int(shards), _ptr(out_max), _ptr(out_lse),
-                                 _ptr(out_argmax), _stream(stream))
+                                 _ptr(out_argmax), _stream(stream, triples))
     if check and rc != DS_OK:
         raise DsError("ds_merge_triples", rc)
     return rc
@@ -182,7 +187,7 @@ def ds_log_softmax(logits, out, out_max, out_lse, out_argmax, out_dtype=None, n=
     if out_dtype is None:
         out_dtype = DS_DTYPE_BF16 if out.dtype == torch.bfloat16 else DS_DTYPE_F32
     rc = load().ds_log_softmax(_ptr(logits), int(n), int(V), _ptr(out), int(out_dtype), _ptr(out_max),
-                               _ptr(out_lse), _ptr(out_argmax), _stream(stream))
+                               _ptr(out_lse), _ptr(out_argmax), _stream(stream, logits))
     if check and rc != DS_OK:
         raise DsError("ds_log_softmax", rc)
     return rc
@@ -197,7 +202,7 @@ def ds_reveal(scores, tokens, seq_lens, reveal_counts, canvas, revealed=None, d_
     if B is None:
         B = seq_lens.shape[0]
     rc = load().ds_reveal(_ptr(scores), _ptr(tokens), _ptr(seq_lens), _ptr(reveal_counts), int(B), int(C),
-                          int(P), _ptr(canvas), _ptr(revealed), _ptr(d_status), _stream(stream))
+                          int(P), _ptr(canvas), _ptr(revealed), _ptr(d_status), _stream(stream, scores))
     if check and rc != DS_OK:
         raise DsError("ds_reveal", rc)
     return rc
@@ -247,7 +252,7 @@ def ds_sample_filtered(logits, temperature, u, out_tokens, out_logprobs, top_k=N
         ld = logits.stride(0) if n > 1 else V
     rc = load().ds_sample_filtered(logits.data_ptr(), _dtype_code(logits), n, V, ld, _ptr(temperature), _ptr(top_k),
                                    _ptr(top_p), _ptr(min_p), _ptr(u), _ptr(out_tokens), _ptr(out_logprobs),
-                                   _ptr(d_status), _stream(stream))
+                                   _ptr(d_status), _stream(stream, logits))
     if check and rc != DS_OK:
         raise DsError("ds_sample_filtered", rc)
     return rc
@@ -261,7 +266,7 @@ def ds_quantize_rows(x, out_q, out_scale, gain=None, eps=1e-6, n=None, K=None, l
     if ld is None:
         ld = x.stride(0) if n > 1 else K
     rc = load().ds_quantize_rows(x.data_ptr(), _dtype_code(x), n, K, ld, _ptr(gain), float(eps), _ptr(out_q),
-                                 _ptr(out_scale), _stream(stream))
+                                 _ptr(out_scale), _stream(stream, x))
     if check and rc != DS_OK:
         raise DsError("ds_quantize_rows", rc)
     return rc
@@ -295,7 +300,7 @@ def ds_head_i8(x, packed, w_scale, out, workspace, N, gain=None, eps=1e-6, d_sta
         workspace_bytes = workspace.numel() * workspace.element_size()
     rc = load().ds_head_i8(x.data_ptr(), _dtype_code(x), n, K, ld, _ptr(gain), float(eps), _ptr(packed), _ptr(w_scale),
                            N, _ptr(out), out_dtype, ldo, _ptr(workspace), workspace_bytes, _ptr(d_status),
-                           _stream(stream))
+                           _stream(stream, x))
     if check and rc != DS_OK:
         raise DsError("ds_head_i8", rc)
     return rc
@@ -307,7 +312,7 @@ def ds_pack_i8(w, packed, N=None, K=None, ldw=None, stream=None, check=True):
         N, K = w.shape
     if ldw is None:
         ldw = w.stride(0) if N > 1 else K
-    rc = load().ds_pack_i8(_ptr(w), N, K, ldw, _ptr(packed), _stream(stream))
+    rc = load().ds_pack_i8(_ptr(w), N, K, ldw, _ptr(packed), _stream(stream, w))
     if check and rc != DS_OK:
         raise DsError("ds_pack_i8", rc)
     return rc
@@ -328,7 +333,7 @@ def ds_linear_i8(a, a_scale, packed, w_scale, out, N, K, workspace=None, d_statu
     if workspace_bytes is None:
         workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = load().ds_linear_i8(a.data_ptr(), lda, _ptr(a_scale), _ptr(packed), _ptr(w_scale), n, N, K, _ptr(out),
-                             out_dtype, ldo, _ptr(workspace), workspace_bytes, _ptr(d_status), _stream(stream))
+                             out_dtype, ldo, _ptr(workspace), workspace_bytes, _ptr(d_status), _stream(stream, a))
     if check and rc != DS_OK:
         raise DsError("ds_linear_i8", rc)
     return rc
