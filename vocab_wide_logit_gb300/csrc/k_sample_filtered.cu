@@ -808,9 +808,10 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 28 : NT == 128 ? 6 : 1024 / NT)
     // A warp's own row starts a little lower, and lower still for a top-k that
     // would end below (15510 x 1025, 12% of the rows with k = 200: 148 -> 129 us).
     const float further = PASS == kMarked ? (RESIDENT ? 1e30f : 0.f) : NT == 32 ? (q.k > 64 ? .35f : .15f) : 0.f;
-    x1 = ONE_WALK ? cut : cut - further * (m - cut);
+    // Without a cut (in each CTA a group without a logit) all of the row is above it.
+    x1 = ONE_WALK || !(cut > -kInf) ? cut : cut - further * (m - cut);
     if (PASS == kMarked && !RESIDENT) x1 = fminf(x1, a.out_logprobs[n]);  // the first pass's hint, +inf for none
-    x1 = fmaxf(x1, x_low);
+    x1 = fmaxf(x1, x_low);  // never above m: the bins hold the maximum at least
     float per_x = fminf((float)NB / (m - x1), 3.402823466e38f);
     auto bin_of = [&](float x) { return min(NB - 1, __float2int_rz((m - x) * per_x)); };  // for x1 <= x <= m
     const bool finite = m > -kInf && m < kInf;
@@ -1068,7 +1069,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 28 : NT == 128 ? 6 : 1024 / NT)
       const uint32_t count = sh.pc[nb - 1];
       const bool complete = sure || x1 <= x_low;  // nothing that is asked for lies below x1
       if (PASS == kFirst && lane == 0) sh.hint = kInf;  // none
-      if (sh.crowded) return (int)kExact;
+      if (sh.crowded || !known) return (int)kExact;  // a search among empty bins would end behind the last
       uint32_t mark = 0;  // lane l: bins [32 l, 32 l + 32)
       auto mark_range = [&](int b0, int b1) {
         const int from = max(b0 - 32 * lane, 0), to = min(b1 - 32 * lane, 31);
