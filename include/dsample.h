@@ -46,7 +46,7 @@ typedef enum {
 #define DS_DEV_ERR_NO_UNCOND 2u /* guidance != 0 for a request but u_logits == NULL */
 #define DS_DEV_ERR_PARAM 4u    /* temperature < 0 or NaN, or guidance NaN; any parameter of ds_sample_filtered */
 #define DS_DEV_ERR_LOGITS 8u   /* ds_sample_filtered: a NaN or +inf among a row's logits */
-#define DS_DEV_ERR_TIMEOUT 16u /* ds_linear_i8: a wait inside the kernel ran out; the call's output is not valid */
+#define DS_DEV_ERR_TIMEOUT 16u /* ds_linear_i8, ds_head_i8: a wait inside the kernel ran out; results not made are NaN */
 
 /* Limits of this build. */
 #define DS_MAX_ROWS 256          /* C: rows (codebooks) per call; the row index keys the noise */
@@ -384,7 +384,7 @@ int64_t ds_linear_i8_workspace(int32_t n, int32_t N, int32_t K);
  *   workspace  device, workspace_bytes >= ds_linear_i8_workspace(n, N, K),
  *              128-byte aligned (NULL when that is 0). Its contents need not be
  *              kept between calls; calls that may run at once need one each.
- *   d_status   device uint32 or NULL: DS_DEV_ERR_TIMEOUT.
+ *   d_status   device uint32 or NULL: DS_DEV_ERR_TIMEOUT, and NaN for the results not made.
  *   stream     cudaStream_t.
  * Returns DS_OK, DS_ERR_INVALID_ARG, DS_ERR_UNSUPPORTED (K, lda or ldo too
  * large) or DS_ERR_CUDA.
@@ -405,7 +405,8 @@ int64_t ds_head_i8_workspace(int32_t n, int32_t N, int32_t K);
  * NULL with eps; packed and w_scale of an [N][K] weight; out [n][N] of out_dtype,
  * rows ldo apart). workspace: device, workspace_bytes >= ds_head_i8_workspace(n,
  * N, K), 128-byte aligned, contents not kept between calls. A row with a NaN or
- * an infinity gives a row of NaN. d_status: DS_DEV_ERR_TIMEOUT, or NULL.
+ * an infinity gives a row of NaN. d_status: DS_DEV_ERR_TIMEOUT (and NaN for the
+ * results not made), or NULL.
  * Returns DS_OK, DS_ERR_INVALID_ARG, DS_ERR_UNSUPPORTED (K, ld or ldo too large)
  * or DS_ERR_CUDA.
  */

@@ -32,6 +32,17 @@ int cached(const void* site, long long param, F init) {
 // SM count of the current device (cached).
 int device_sms();
 
+// How often a wait inside a serving-head kernel asks before it gives up, and the
+// instruction that asks. Another build (no second time, and without the suspension
+// that try_wait may add) makes waits run out, to test what is left then.
+#ifndef DS_WAIT_TRIES
+#define DS_WAIT_TRIES (1 << 20)
+#define DS_WAIT_TRY "try_wait"
+#endif
+// A kernel that has given up asks this often for its own copies and instructions
+// in flight before it leaves.
+constexpr int kDrainTries = 1 << 20;
+
 constexpr int kWarpKernelThreads = 128;
 constexpr int kStreamMark = DS_MARKED_TOKEN;  // out_tokens marker left by a fast pass for the exact one
 

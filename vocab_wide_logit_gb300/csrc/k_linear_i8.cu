@@ -117,7 +117,7 @@ __device__ __forceinline__ void mbar_expect(uint64_t* b, uint32_t bytes) {
 __device__ __forceinline__ bool mbar_try(uint64_t* b, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+      "{\n.reg .pred p;\nmbarrier." DS_WAIT_TRY ".parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
       : "=r"(ok)
       : "r"(smem_u32(b)), "r"(parity)
       : "memory");
@@ -134,10 +134,18 @@ __device__ __forceinline__ void mbar_arrive_first(uint64_t* b) {
           smem_u32(b))
       : "memory");
 }
+// Raises the stop flag of the pair's other CTA as well.
+__device__ __forceinline__ void tell_peer(int* flag, uint32_t peer) {
+  asm volatile("{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %0, %1;\nst.shared::cluster.u32 [a], %2;\n}" ::"r"(
+                   smem_u32(flag)),
+               "r"(peer), "r"(1)
+               : "memory");
+}
 // Every wait gives up after a while: it raises the CTA's stop flag, which ends
-// the other waits too, and the caller leaves its loop.
+// the other waits too, and the caller leaves its loop. What the CTA has started is
+// then still waited for (mbar_drain), and the results that it owes become NaN.
 __device__ __noinline__ bool mbar_wait_slow(uint64_t* b, uint32_t parity, volatile int* stop) {
-  for (int i = 0; i < (1 << 20); ++i) {
+  for (int i = 0; i < DS_WAIT_TRIES; ++i) {
     if (mbar_try(b, parity)) return true;
     if (*stop) return false;
   }
@@ -146,6 +154,16 @@ __device__ __noinline__ bool mbar_wait_slow(uint64_t* b, uint32_t parity, volati
 }
 __device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity, volatile int* stop) {
   return mbar_try(b, parity) || mbar_wait_slow(b, parity, stop);
+}
+// No copy or matrix instruction may be in flight when the CTA leaves its shared
+// and tensor memory.
+__device__ __forceinline__ void mbar_drain(uint64_t* b, uint32_t parity) {
+  for (int i = 0; i < kDrainTries && !mbar_try(b, parity); ++i) {
+  }
+}
+// The same for the last uses of a ring that was used n times.
+__device__ __noinline__ void ring_drain(uint64_t* full, uint32_t slots, uint32_t n) {
+  for (uint32_t i = n > slots ? n - slots : 0; i < n; ++i) mbar_drain(&full[i % slots], (i / slots) & 1u);
 }
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -400,6 +418,7 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
   __shared__ uint32_t tmem_base;
   __shared__ __align__(16) float a_scale[256];
   __shared__ int stop_flag;
+  __shared__ uint32_t started[3];  // weight blocks, blocks of row tiles, tiles handed on, once their warp is done
   volatile int* stop = &stop_flag;
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   uint8_t* bs = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
@@ -474,11 +493,7 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
           bulk_load(ws + rw.slot * kTcBlock, src + (long long)b * kTcBlock, kTcBlock, &w_full[rw.slot]);
         }
       }
-      // given up: no copy may be in flight when the CTA leaves
-      if (!ok)
-        for (uint32_t j = it > (uint32_t)p.w_slots ? it - p.w_slots : 0; j < it; ++j)
-          for (int i = 0; i < (1 << 20) && !mbar_try(&w_full[j % p.w_slots], (j / p.w_slots) & 1); ++i) {
-          }
+      started[0] = it;
     }
   } else if (warp == kTcEpi + kTcCvt + 1) {
     // ---- row tiles
@@ -501,10 +516,7 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
           bulk_load(bs + rb.slot * b_bytes, src + (long long)b * tile_bytes, b_bytes, &b_full[rb.slot]);
         }
       }
-      if (!ok)
-        for (uint32_t j = it > (uint32_t)p.b_slots ? it - p.b_slots : 0; j < it; ++j)
-          for (int i = 0; i < (1 << 20) && !mbar_try(&b_full[j % p.b_slots], (j / p.b_slots) & 1); ++i) {
-          }
+      started[1] = it;
     }
   } else if (warp == kTcEpi + kTcCvt + 2) {
     // ---- matrix instructions, by one thread
@@ -513,6 +525,7 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
       if (elect_one()) {
         Ring ra, rb;
         bool ok = true;
+        started[2] = 0;
         for (Walk at(t0, t_step, p.tiles); ok && at.t < n_tiles; at.next())
           for (int b = 0; ok && b < kb; ++b) {
             ok = mbar_wait(&a_full[ra.slot], ra.phase, stop);
@@ -533,9 +546,11 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
       const uint64_t b_desc = sw128_desc(smem_u32(bs));
       const uint32_t b_step = b_bytes >> 4;
       Ring ra, rb, rd;
+      uint32_t handed = 0;  // tiles
       bool ok = true, loaded = false;
       for (Walk at(t0, t_step, p.tiles); ok && at.t < n_tiles; at.next()) {
-        if (!mbar_wait(&d_empty[rd.slot], rd.phase ^ 1u, stop)) break;
+        ok = mbar_wait(&d_empty[rd.slot], rd.phase ^ 1u, stop);
+        if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + rd.slot * 128u;
         uint32_t accumulate = 0;
@@ -563,15 +578,17 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
           if (ok) tc_commit<PAIR>(&a_empty[ra.slot]);
           ra.next(kTcASlots);
         }
-        if (ok) tc_commit<PAIR>(&d_full[rd.slot]);
+        if (ok) {
+          tc_commit<PAIR>(&d_full[rd.slot]);
+          ++handed;
+        }
         rd.next(d_bufs);
         loaded = p.resident;  // a resident row tile has a slot for each of its blocks: the ring is back at the first
       }
-      if (!ok || *stop) {
-        // given up: let the instructions in flight finish before tensor memory is freed
-        tc_commit<PAIR>(&drained);
-        for (int i = 0; i < (1 << 16) && !mbar_try(&drained, 0); ++i) {
-        }
+      started[2] = handed;
+      if (!ok) {
+        tc_commit<PAIR>(&drained);  // of a tile that was not handed on
+        mbar_drain(&drained, 0);
       }
     }
   } else if (warp >= kTcEpi) {
@@ -625,8 +642,10 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
     Ring rd;
     int scales = -1;  // row tile whose scales are in shared memory
     pdl_wait();
-    for (Walk at(t0, t_step, p.tiles); at.t < n_tiles; at.next()) {
-      const long long j = (PAIR ? 2LL * at.block + rank : (long long)at.block) * kPackRows + quad * 32 + lane;
+    Walk at(t0, t_step, p.tiles);
+    auto channel = [&] { return (PAIR ? 2LL * at.block + rank : (long long)at.block) * kPackRows + quad * 32 + lane; };
+    for (; at.t < n_tiles; at.next()) {
+      const long long j = channel();
       const long long i0 = (long long)at.tile * p.rows;
       const float sw = j < g.N ? g.w_scale[j] : 0.f;
       const bool gone = !mbar_wait(&d_full[rd.slot], rd.phase, stop) || *stop;
@@ -709,10 +728,25 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
       }
       rd.next(d_bufs);
     }
+    // given up: the rest of this CTA's results
+    for (; at.t < n_tiles; at.next()) {
+      const long long j = channel(), i0 = (long long)at.tile * p.rows;
+      if (j < g.N)
+        for (long long i = i0 + half; i < g.n && i < i0 + p.rows; i += 2)
+          store_out(static_cast<OUT*>(g.out) + i * g.ldo + j, __int_as_float(0x7fffffff));
+    }
   }
 
   tc_fence_before();
+  if (PAIR && *stop) tell_peer(&stop_flag, rank ^ 1u);
   all_sync<PAIR>();  // of a pair, neither leaves while the other may still use its memory
+  if (*stop) {
+    // Given up, and whoever did may have left the others' work in flight.
+    if (threadIdx.x == 0) ring_drain(w_full, p.w_slots, started[0]);
+    if (threadIdx.x == 32) ring_drain(b_full, p.b_slots, started[1]);
+    if (threadIdx.x == 64) ring_drain(d_full, d_bufs, started[2]);
+    all_sync<PAIR>();
+  }
   tc_fence_after();
   if (warp == 0) {
     if (PAIR)
