@@ -46,7 +46,9 @@ typedef enum {
 #define DS_DEV_ERR_NO_UNCOND 2u /* guidance != 0 for a request but u_logits == NULL */
 #define DS_DEV_ERR_PARAM 4u    /* temperature < 0 or NaN, or guidance NaN; any parameter of ds_sample_filtered */
 #define DS_DEV_ERR_LOGITS 8u   /* ds_sample_filtered: a NaN or +inf among a row's logits */
-#define DS_DEV_ERR_TIMEOUT 16u /* ds_linear_i8, ds_head_i8: a wait inside the kernel ran out; results not made are NaN */
+/* A wait inside a kernel ran out: ds_linear_i8 and ds_head_i8 leave NaN for the
+ * results not made, ds_sample_filtered token -1 and logprob NaN. */
+#define DS_DEV_ERR_TIMEOUT 16u
 
 /* Limits of this build. */
 #define DS_MAX_ROWS 256          /* C: rows (codebooks) per call; the row index keys the noise */
@@ -309,8 +311,9 @@ ds_status ds_reveal(const float* scores, const int32_t* tokens, const int32_t* s
  *   d_status     device uint32 or NULL; the kernels OR DS_DEV_ERR_* bits into it.
  *   stream       cudaStream_t.
  * A row with nothing to draw (every logit -inf) gets token -1 and logprob NaN.
- * So does a row with a parameter out of range (DS_DEV_ERR_PARAM) and one with a
- * NaN or +inf (DS_DEV_ERR_LOGITS); other rows are not affected.
+ * So does a row with a parameter out of range (DS_DEV_ERR_PARAM), one with a NaN
+ * or +inf (DS_DEV_ERR_LOGITS), and one whose copy to the chip was not there in
+ * time (DS_DEV_ERR_TIMEOUT); other rows are not affected.
  * Returns DS_OK, DS_ERR_INVALID_ARG, DS_ERR_UNSUPPORTED (V too large, ld > 2^40)
  * or DS_ERR_CUDA.
  */

@@ -25,7 +25,7 @@ def impatient(tmp_path_factory):
                           "--expt-relaxed-constexpr", "-DDS_WAIT_TRIES=0", '-DDS_WAIT_TRY="test_wait"']
     objs, jobs = [], []
     for src in build.SOURCES:
-        own = src in ("k_linear_i8.cu",)
+        own = src in ("k_linear_i8.cu", "k_sample_filtered.cu")
         obj = os.path.join(str(out) if own else build.OUT, src.replace(".cu", ".o"))
         objs.append(obj)
         if own:
@@ -94,3 +94,31 @@ def test_head_that_gives_up(use, n):
     tok, lp = pkg.sample_filtered(out, torch.ones(n, device=w.device), torch.full((n,), 0.5, device=w.device))
     hit = torch.isnan(out).any(1)  # the sampler reports such rows
     assert bool((tok[hit] == -1).all()) and all(math.isnan(v) for v in lp[hit].tolist())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sampler_that_gives_up(use, dtype):
+    """Rows held in shared memory, by 128 threads each or by a warp each with a second launch behind it: a row whose copy
+    was not waited for has token -1 and logprob NaN, and no row has another token than its own. A short row's copy is
+    often there when it is asked for, so that a call may lose nothing, but not all of them together."""
+    lost_rows = 0
+    for n, V in [(1, 1025), (40, 1025), (15510, 1025), (1300, 2048), (3000, 5003), (160, 8001),
+                 (20000, 8001)]:  # the last: more than L2 holds
+        g = torch.Generator().manual_seed(n)
+        dev = torch.device("cuda", 0)
+        x = (torch.randn((n, V), generator=g) * 3).to(DT[dtype]).to(dev)
+        tau = torch.where(torch.arange(n) % 3 == 0, 0.0, 0.8).to(dev)
+        u, p = torch.rand((n,), generator=g).to(dev), torch.full((n,), 0.9, device=dev)
+        k = torch.where(torch.arange(n) % 5 == 0, 200, 0).to(torch.int32).to(dev)
+        want, want_lp = pkg.sample_filtered(x, tau, u, top_k=k, top_p=p)
+        tok, lp = torch.full((n,), 7, dtype=torch.int32, device=dev), torch.full((n,), 7.0, device=dev)
+        st = torch.zeros(1, dtype=torch.int32, device=dev)
+        use(lambda: pkg.ds_sample_filtered(x, tau, u, tok, lp, top_k=k, top_p=p, d_status=st))
+        lost = torch.isnan(lp)
+        assert int(st.item()) == (pkg.DS_DEV_ERR_TIMEOUT if bool(lost.any()) else 0)
+        assert bool((tok[lost] == -1).all())
+        assert torch.equal(tok[~lost], want[~lost]) and torch.equal(lp[~lost], want_lp[~lost])
+        again, _ = pkg.sample_filtered(x, tau, u, top_k=k, top_p=p)
+        assert torch.equal(again, want)
+        lost_rows += int(lost.sum())
+    assert lost_rows

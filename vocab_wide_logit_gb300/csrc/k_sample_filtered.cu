@@ -444,6 +444,7 @@ struct SfShared {
   float part_tempered[CS];
   u64 part_total[CS];
   int part_odd[CS], part_floor[CS], part_below[CS];
+  int gave_up;  // a warp's wait for the slice ran out
   int command, n_list, n_mine, mine_at, first_id;
   u64 t_lo, t_hi;  // bounds of the row's mass
   float known_sum;
@@ -491,11 +492,11 @@ __device__ __forceinline__ float warp_min_r(float v) { return -warp_max_r(-v); }
 __device__ __forceinline__ uint32_t sf_smem(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
 // Waits for the slice's copy; gives up after a while (false).
-__device__ __forceinline__ bool sf_wait(u64* bar, uint32_t parity) {
-  for (int i = 0; i < (1 << 20); ++i) {
+__device__ __forceinline__ bool sf_wait(u64* bar, uint32_t parity, int tries = DS_WAIT_TRIES) {
+  for (int i = 0; i <= tries; ++i) {
     uint32_t ok;
     asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+        "{\n.reg .pred p;\nmbarrier." DS_WAIT_TRY ".parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok)
         : "r"(sf_smem(bar)), "r"(parity)
         : "memory");
@@ -554,6 +555,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 28 : NT == 128 ? 6 : 1024 / NT)
   long long next = row_from(cid);
   if (PASS == kMarked && next >= a.n) return;  // nothing marked among this cluster's rows: all of its CTAs leave
   if (tid == 0) {
+    sh.gave_up = 0;
     asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(sf_smem(&sh.full)) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -597,7 +599,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 28 : NT == 128 ? 6 : 1024 / NT)
       sh.first_id = INT_MAX;
       sh.crowded = 0;
     }
-    if (RESIDENT && !sf_wait(&sh.full, parity)) report(a.d_status, DS_DEV_ERR_TIMEOUT);
+    bool gave_up = RESIDENT && !sf_wait(&sh.full, parity);
 
     // ---- the sums of a chunk and its largest logit, relative to `ref`
     float s = 0.f, st = 0.f;
@@ -723,6 +725,10 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 28 : NT == 128 ? 6 : 1024 / NT)
       m = warp_max_r(mx);
       lo = warp_min_r(mn);
       cut = warp_min_r(grp);
+      if (RESIDENT) {
+        gave_up = __any_sync(0xffffffffu, gave_up);
+        if (NW > 1 && gave_up && lane == 0) sh.gave_up = 1;
+      }
       if (NW > 1) {
         if (lane == 0) {
           sh.fred[0][wid] = m;
@@ -752,6 +758,21 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 28 : NT == 128 ? 6 : 1024 / NT)
           cut = warp_max_r(sh.part_cut[lane % cs]);
         }
       }
+    }
+    if (RESIDENT && (NW > 1 ? sh.gave_up : (int)gave_up)) {
+      // The copy of this row never came: neither it nor this CTA's further rows are
+      // answered. A later launch has nothing to do for them.
+      if (tid == 0) {
+        report(a.d_status, DS_DEV_ERR_TIMEOUT);
+        (void)sf_wait(&sh.full, parity, kDrainTries);  // not while it is still to be written
+      }
+      for (long long i = n; i < a.n; i = row_from(i + n_clusters)) {
+        if (tid == 0) {
+          a.out_tokens[i] = -1;
+          a.out_logprobs[i] = __int_as_float(0x7fffffff);
+        }
+      }
+      break;
     }
     // ---- ONE_WALK: the sums relative to the sample's maximum, the queue, and the maximum itself
     const float ref = m;
