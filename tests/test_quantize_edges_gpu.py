@@ -1,0 +1,50 @@
+"""ds_quantize_rows and the head where fp32's range ends: rows close to zero, squares that leave the range, no eps, and
+rows of nearly 2^31 elements."""
+import math
+
+import pytest
+import torch
+
+import vocab_wide_logit_gb300 as pkg
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+STEP = 2.0 ** -149  # the smallest fp32 number: what a scale below 2^-126 is rounded to a multiple of
+
+
+def _check(x, gain, eps, q, scale):
+    """The definition in 64 bits. fp32 arithmetic: 16 roundings of 2^-24 at most, so 127 * 16 * 2^-24 = 1.3e-4 of a step
+    beside the half that rounding to an integer may take; a row whose y lies below 2^-126 has further errors of one STEP for each
+    of three products, 127 * 3 of them in the largest."""
+    y = x.double()
+    if gain is not None:
+        y = y / torch.sqrt((y * y).mean(1, keepdim=True) + eps)
+        y = torch.where(x.double().abs().amax(1, keepdim=True) > 0, y, torch.zeros_like(y)) * gain.double()
+    amax = y.abs().amax(1, keepdim=True)
+    real = torch.where(amax > 0, y * 127 / amax, torch.zeros_like(y))
+    room = torch.where(amax > 0, 0.5 + 2e-4 + (6 * 127 * STEP / amax if gain is not None else 0.0), torch.zeros_like(amax))
+    assert int(q.abs().max()) <= 127
+    assert bool(((q.double() - real).abs() <= room).all())
+    want = amax[:, 0] / 127
+    assert bool(((scale.double() - want).abs() <= want * 16 * 2.0 ** -24 + STEP * (4 if gain is not None else 0.5)).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [5, 64, 1000, 8192, 20001])
+@pytest.mark.parametrize("norm", [False, True])
+def test_rows_close_to_zero(K, dtype, norm):
+    """127 / max|y| is beyond fp32 below 3.7e-37."""
+    dev = torch.device("cuda", 0)
+    sizes = [1e-36, 3.7e-37, 3e-37, 1e-37, 1e-38, 2e-39, 1e-41, 3e-44]
+    x = torch.randn((len(sizes), K), generator=torch.Generator().manual_seed(K))
+    x = x / x.abs().amax(1, keepdim=True) * torch.tensor(sizes, dtype=torch.float64)[:, None]
+    x = x.to(DT[dtype]).to(dev)
+    assert bool((x.abs().amax(1) > 0).all()) or dtype == "bf16"  # whose smallest number is 9e-41: the last two rows are zeros
+    gain = (1 + 0.2 * torch.randn((K,), generator=torch.Generator().manual_seed(1))).to(dev) if norm else None
+    eps = 1.0 if norm else 0.0  # y is then x times the gain
+    q, scale = pkg.quantize_rows(x, gain=gain, eps=eps)
+    _check(x, gain, eps, q, scale)
+    head = pkg.Int8Head(torch.eye(K, dtype=torch.int8, device=dev)[:64].contiguous(), torch.ones(min(K, 64), device=dev),
+                        gain=gain, eps=eps)
+    assert torch.equal(head.logits(x, dtype=torch.float32), q[:, :64].float() * scale[:, None])

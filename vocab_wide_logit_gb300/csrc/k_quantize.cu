@@ -137,7 +137,16 @@ __global__ void __launch_bounds__(kQrNT, HELD == 4 ? 3 : HELD == 2 ? 4 : 5) k_qu
     for (int w = 0; w < kQrNT / 32; ++w) top = max(top, __float_as_uint(red[1][w]));
     const float amax = __uint_as_float(top);
     bad = bad || top >= 0x7f800000u;
-    const float inv = (bad || top == 0u) ? 0.f : fminf(127.f / amax, 3.402823466e38f);
+    // 127 / max|y| is beyond fp32 below 3.7e-37: such a row is taken 2^64 times as large, exactly
+    const bool small = amax < 4e-37f;
+    const float lift = small ? 18446744073709551616.f : 1.f;
+    const float inv = (bad || top == 0u) ? 0.f : 127.f / (amax * lift);
+    if (small) {
+#pragma unroll
+      for (int h = 0; h < HELD; ++h)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) held[h][e] *= lift;
+    }
     auto put = [&](int c, const float (&v)[8]) {
       // |y inv| <= 127 (1 + 2^-23): added to 1.5 2^23 it is rounded to the nearest integer, which the low
       // bits then hold
@@ -174,6 +183,8 @@ __global__ void __launch_bounds__(kQrNT, HELD == 4 ? 3 : HELD == 2 ? 4 : 5) k_qu
       if (live && 8 * c < K) {
         qr_chunk(row, c, K, wide, v);
         normed(c, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= lift;
       }
       put(c, v);
     }
