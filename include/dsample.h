@@ -329,8 +329,9 @@ ds_status ds_sample_filtered(const void* logits, int32_t dtype, int32_t n, int32
  *   y = x, or x * rsqrt(mean(x^2) + eps) * gain when gain is given (fp32)
  *   scale = max|y| / 127,  q = rint(y * (127 / max|y|)) in [-127, 127]
  * so that q * scale is y to within scale / 2 (and 127 * 2^-150 where the scale is
- * below 2^-126, fp32's least normal number). A row of zeros has scale 0. A row
- * with a NaN or an infinity has scale NaN and q 0.
+ * below 2^-126, fp32's least normal number). A row of zeros has scale 0, whatever
+ * eps; squares that leave fp32's range do no harm. A row with a NaN or an infinity
+ * in x or y has scale NaN and q 0.
  *
  * Arguments:
  *   x          device [n][K] of dtype, rows ld elements apart (ld >= K), any

@@ -48,3 +48,29 @@ def test_rows_close_to_zero(K, dtype, norm):
     head = pkg.Int8Head(torch.eye(K, dtype=torch.int8, device=dev)[:64].contiguous(), torch.ones(min(K, 64), device=dev),
                         gain=gain, eps=eps)
     assert torch.equal(head.logits(x, dtype=torch.float32), q[:, :64].float() * scale[:, None])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [5, 64, 1000, 8192, 20001])
+@pytest.mark.parametrize("eps", [0.0, 1e-44, 1e-38, 9e-38, 1e-6, 3e38])
+def test_norm_of_rows_whose_squares_leave_the_range(K, eps, dtype):
+    """A row of zeros without eps, squares below 2^-126 and above 2^128, and a sum of them that passes 2^128 with eps."""
+    dev = torch.device("cuda", 0)
+    sizes = [0.0, 1e-44, 1e-40, 1e-38, 1e-30, 1e-22, 1e-19, 1e-18, 1.0, 1e18, 1.7e19, 3e19, 1e25, 1e38, 3e38]
+    x = torch.randn((len(sizes), K), generator=torch.Generator().manual_seed(K))
+    x = x / x.abs().amax(1, keepdim=True) * torch.tensor(sizes, dtype=torch.float64)[:, None]
+    x[12, 1:] *= 1e-40  # one large value among small ones
+    x = x.to(DT[dtype]).to(dev)
+    gain = (1 + 0.2 * torch.randn((K,), generator=torch.Generator().manual_seed(1))).to(dev)
+    q, scale = pkg.quantize_rows(x, gain=gain, eps=eps)
+    _check(x, gain, float(torch.tensor(eps)), q, scale)  # the fp32 number that the call takes: 1e-44 is 9.8e-45
+    assert float(scale[0]) == 0 and int(q[0].abs().max()) == 0
+    w = torch.ones((3, K), dtype=torch.int8, device=dev)
+    head = pkg.Int8Head(w, torch.ones(3, device=dev), gain=gain, eps=eps)
+    assert torch.equal(head.logits(x, dtype=torch.float32),
+                       pkg.linear_i8(q, scale, head.weight, dtype=torch.float32))
+    x[3, K - 1], x[13, 0] = math.nan, math.inf
+    q2, scale2 = pkg.quantize_rows(x, gain=gain, eps=eps)
+    keep = [i for i in range(len(sizes)) if i not in (3, 13)]
+    assert torch.equal(q2[keep], q[keep]) and torch.equal(scale2[keep], scale[keep])
+    assert bool(torch.isnan(scale2[[3, 13]]).all()) and int(q2[[3, 13]].abs().max()) == 0

@@ -81,9 +81,13 @@ __global__ void __launch_bounds__(kQrNT, HELD == 4 ? 3 : HELD == 2 ? 4 : 5) k_qu
         for (int e = 0; e < 8; ++e) held[h][e] = 0.f;
       }
     }
-    float f = 1.f;
-    bool bad = false;
-    if (gain) {
+    float f = 1.f, pre = 1.f;  // pre: a power of two that x is taken times, in `held` already
+    auto rest = [&](int c, float (&v)[8]) {
+      qr_chunk(row, c, K, wide, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= pre;
+    };
+    auto squares = [&] {
       float s = 0.f;
 #pragma unroll
       for (int h = 0; h < HELD; ++h)
@@ -92,7 +96,7 @@ __global__ void __launch_bounds__(kQrNT, HELD == 4 ? 3 : HELD == 2 ? 4 : 5) k_qu
       if (live)
         for (int c = tid + HELD * kQrNT; 8 * c < K; c += kQrNT) {
           float v[8];
-          qr_chunk(row, c, K, wide, v);
+          rest(c, v);
 #pragma unroll
           for (int e = 0; e < 8; ++e) s = __fmaf_rn(v[e], v[e], s);
         }
@@ -102,8 +106,46 @@ __global__ void __launch_bounds__(kQrNT, HELD == 4 ? 3 : HELD == 2 ? 4 : 5) k_qu
       s = 0.f;
 #pragma unroll
       for (int w = 0; w < kQrNT / 32; ++w) s += red[0][w];
-      f = rsqrtf(s / (float)K + eps);
-      bad = !(s < kInf);  // a NaN, an infinity, or squares that overflow
+      return s;
+    };
+    if (gain) {
+      const float v = squares() / (float)K + eps;
+      f = rsqrtf(v);
+      // Squares lose bits below 2^-126, which matters where their mean is that small,
+      // and overflow from 1.8e19 on: the row is then taken times a power of two that
+      // brings the larger of max|x| and sqrt(eps) to between 1 and 4.
+      if (!(v >= 1e-37f && v < kInf)) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int h = 0; h < HELD; ++h)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(held[h][e]) & 0x7fffffffu);
+        if (live)
+          for (int c = tid + HELD * kQrNT; 8 * c < K; c += kQrNT) {
+            float w[8];
+            rest(c, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(w[e]) & 0x7fffffffu);
+          }
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0) red[1][wid] = __uint_as_float(top);
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kQrNT / 32; ++w) top = max(top, __float_as_uint(red[1][w]));
+        const float most = fmaxf(__uint_as_float(top), sqrtf(eps));
+        if (top >= 0x7f800000u) {
+          f = 1.f;  // a NaN or an infinity, which y has then too
+        } else if (most == 0.f) {
+          f = 0.f;  // zeros, without eps
+        } else {
+          pre = __uint_as_float((uint32_t)max(1, 254 - max(1, (int)(__float_as_uint(most) >> 23))) << 23);
+#pragma unroll
+          for (int h = 0; h < HELD; ++h)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) held[h][e] *= pre;
+          f = rsqrtf(squares() / (float)K + eps * pre * pre);
+        }
+      }
     }
     auto normed = [&](int c, float (&v)[8]) {
       if (gain) {
@@ -125,7 +167,7 @@ __global__ void __launch_bounds__(kQrNT, HELD == 4 ? 3 : HELD == 2 ? 4 : 5) k_qu
     if (live)
       for (int c = tid + HELD * kQrNT; 8 * c < K; c += kQrNT) {
         float v[8];
-        qr_chunk(row, c, K, wide, v);
+        rest(c, v);
         normed(c, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
@@ -136,7 +178,7 @@ __global__ void __launch_bounds__(kQrNT, HELD == 4 ? 3 : HELD == 2 ? 4 : 5) k_qu
 #pragma unroll
     for (int w = 0; w < kQrNT / 32; ++w) top = max(top, __float_as_uint(red[1][w]));
     const float amax = __uint_as_float(top);
-    bad = bad || top >= 0x7f800000u;
+    const bool bad = top >= 0x7f800000u;
     // 127 / max|y| is beyond fp32 below 3.7e-37: such a row is taken 2^64 times as large, exactly
     const bool small = amax < 4e-37f;
     const float lift = small ? 18446744073709551616.f : 1.f;
@@ -181,7 +223,7 @@ __global__ void __launch_bounds__(kQrNT, HELD == 4 ? 3 : HELD == 2 ? 4 : 5) k_qu
     for (int c = tid + HELD * kQrNT; c < chunks; c += kQrNT) {
       float v[8] = {};
       if (live && 8 * c < K) {
-        qr_chunk(row, c, K, wide, v);
+        rest(c, v);
         normed(c, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= lift;
