@@ -74,3 +74,24 @@ def test_norm_of_rows_whose_squares_leave_the_range(K, eps, dtype):
     keep = [i for i in range(len(sizes)) if i not in (3, 13)]
     assert torch.equal(q2[keep], q[keep]) and torch.equal(scale2[keep], scale[keep])
     assert bool(torch.isnan(scale2[[3, 13]]).all()) and int(q2[[3, 13]].abs().max()) == 0
+
+
+def test_the_longest_row():
+    """2^31 - 1 elements: the chunk behind the last one starts at 2^31."""
+    dev, K = torch.device("cuda", 0), 2 ** 31 - 1
+    x = torch.empty((1, K), dtype=torch.bfloat16, device=dev)
+    parts = [slice(i, min(i + (1 << 28), K)) for i in range(0, K, 1 << 28)]
+    for i, p in enumerate(parts):
+        x[0, p].normal_(0, 1 + i, generator=torch.Generator(device=dev).manual_seed(i))
+    x[0, K - 1] = 100.0  # the largest, and the last
+    q, scale = pkg.quantize_rows(x)
+    assert int(q[0, K - 1]) == 127 and float(scale[0]) == float(torch.tensor(100.0) / 127)
+    for p in parts:  # half a step, and the 16 roundings that _check allows
+        assert float((q[0, p].float() * (100 / 127) - x[0, p].float()).abs().max()) <= (0.5 + 2e-4) * 100 / 127 * (1 + 1e-6)
+    one = torch.ones(K, device=dev)
+    qn, sn = pkg.quantize_rows(x, gain=one, eps=0.0)
+    rms = (sum(float(x[0, p].double().square().sum()) for p in parts) / K) ** 0.5
+    # a thread adds 2^23 squares in turn, each addition off by 2^-24 of its running sum at most, which is half of
+    # the whole in the mean: 2^23 2^-24 / 2 = 1/4 of the sum at worst, 0.16 of its root
+    assert abs(float(sn[0]) / (100.0 / 127 / rms) - 1) <= 0.16
+    assert int(qn[0, K - 1]) == 127

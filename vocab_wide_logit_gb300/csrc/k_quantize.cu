@@ -33,7 +33,7 @@ __device__ __forceinline__ float qr_get(const float* p, long long i) { return __
 
 // 8 elements from chunk c on, zero past K.
 __device__ __forceinline__ void qr_chunk(const uint16_t* row, int c, int K, bool wide, float (&f)[8]) {
-  if (wide && 8 * c + 8 <= K) {
+  if (wide && c < K / 8) {
     unpack8(__ldg(reinterpret_cast<const uint4*>(row) + c), f);
   } else {
 #pragma unroll
@@ -41,7 +41,7 @@ __device__ __forceinline__ void qr_chunk(const uint16_t* row, int c, int K, bool
   }
 }
 __device__ __forceinline__ void qr_chunk(const float* row, int c, int K, bool wide, float (&f)[8]) {
-  if (wide && 8 * c + 8 <= K) {
+  if (wide && c < K / 8) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(row) + 2 * c);
     const float4 b = __ldg(reinterpret_cast<const float4*>(row) + 2 * c + 1);
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
@@ -63,7 +63,8 @@ __global__ void __launch_bounds__(kQrNT, HELD == 4 ? 3 : HELD == 2 ? 4 : 5) k_qu
   pdl_release();
   __shared__ float red[2][kQrNT / 32];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int chunks = TILES ? tiles.kb * 8 : (K + 7) / 8;  // of 8 inputs; a tile's row goes on to its last block's end
+  const int parts = (int)((K + 7LL) / 8);  // chunks of 8 inputs: counted, as 8 c passes 32 bits behind a row of 2^31 - 1
+  const int chunks = TILES ? tiles.kb * 8 : parts;  // a tile's row goes on to its last block's end
   const long long rows = TILES ? (long long)tiles.rows * tiles.tiles : n;
   for (long long i = blockIdx.x; i < rows; i += gridDim.x) {
     const T* row = static_cast<const T*>(x) + i * ld;
@@ -74,7 +75,7 @@ __global__ void __launch_bounds__(kQrNT, HELD == 4 ? 3 : HELD == 2 ? 4 : 5) k_qu
 #pragma unroll
     for (int h = 0; h < HELD; ++h) {
       const int c = tid + h * kQrNT;
-      if (live && 8 * c < K) {
+      if (live && c < parts) {
         qr_chunk(row, c, K, wide, held[h]);
       } else {
 #pragma unroll
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(kQrNT, HELD == 4 ? 3 : HELD == 2 ? 4 : 5) k_qu
 #pragma unroll
         for (int e = 0; e < 8; ++e) s = __fmaf_rn(held[h][e], held[h][e], s);
       if (live)
-        for (int c = tid + HELD * kQrNT; 8 * c < K; c += kQrNT) {
+        for (int c = tid + HELD * kQrNT; c < parts; c += kQrNT) {
           float v[8];
           rest(c, v);
 #pragma unroll
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(kQrNT, HELD == 4 ? 3 : HELD == 2 ? 4 : 5) k_qu
 #pragma unroll
           for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(held[h][e]) & 0x7fffffffu);
         if (live)
-          for (int c = tid + HELD * kQrNT; 8 * c < K; c += kQrNT) {
+          for (int c = tid + HELD * kQrNT; c < parts; c += kQrNT) {
             float w[8];
             rest(c, w);
 #pragma unroll
@@ -160,12 +161,12 @@ __global__ void __launch_bounds__(kQrNT, HELD == 4 ? 3 : HELD == 2 ? 4 : 5) k_qu
 #pragma unroll
     for (int h = 0; h < HELD; ++h) {
       const int c = tid + h * kQrNT;
-      if (8 * c < K) normed(c, held[h]);
+      if (c < parts) normed(c, held[h]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(held[h][e]) & 0x7fffffffu);
     }
     if (live)
-      for (int c = tid + HELD * kQrNT; 8 * c < K; c += kQrNT) {
+      for (int c = tid + HELD * kQrNT; c < parts; c += kQrNT) {
         float v[8];
         rest(c, v);
         normed(c, v);
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(kQrNT, HELD == 4 ? 3 : HELD == 2 ? 4 : 5) k_qu
       if (tid + h * kQrNT < chunks) put(tid + h * kQrNT, held[h]);
     for (int c = tid + HELD * kQrNT; c < chunks; c += kQrNT) {
       float v[8] = {};
-      if (live && 8 * c < K) {
+      if (live && c < parts) {
         rest(c, v);
         normed(c, v);
 #pragma unroll
