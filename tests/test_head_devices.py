@@ -165,3 +165,14 @@ def test_calls_by_c_name_keep_to_the_device_of_their_stream(launched, monkeypatc
     _named_calls(0)[name]()
     _named_calls(0)[name](stream=stream(0))
     assert len(launched) == 2
+
+
+@pytest.mark.parametrize("n", [1, 129, 10 ** 9, 2 ** 31 - 300, 2 ** 31 - 256, 2 ** 31 - 255, 2 ** 31 - 1])
+def test_workspace_holds_every_row(n):
+    """A row of up to 128 inputs takes 256 bytes there, and the last rows of a count close to 2^31 do too."""
+    from vocab_wide_logit_gb300 import build
+    build.build()
+    for N in (1, 128, 2 ** 31 - 1):
+        assert n * 256 <= pkg.linear_i8_workspace(n, N, 1) <= n * 256 + 256 * 256 * 2
+        assert pkg.head_i8_workspace(n, N, 1) == pkg.linear_i8_workspace(n, N, 1) + 4 * n
+        assert pkg.packed_i8_bytes(N, 1) == (N + 127) // 128 * 128 * 128

@@ -288,7 +288,7 @@ ds_status ds_quantize_rows(const void* x, int32_t dtype, int32_t n, int32_t K, i
 
 int64_t ds_packed_i8_bytes(int32_t N, int32_t K) {
   if (N < 1 || K < 1 || K > DS_LINEAR_MAX_K) return 0;
-  const int64_t rows = ((int64_t)N + ds::kPackRows - 1) / ds::kPackRows * ds::kPackRows;
+  const int64_t rows = (int64_t)ds::channel_blocks(N) * ds::kPackRows;
   return rows * (((int64_t)K + ds::kPackK - 1) / ds::kPackK * ds::kPackK);
 }
 

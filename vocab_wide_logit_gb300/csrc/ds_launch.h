@@ -116,6 +116,8 @@ cudaError_t launch_quantize_rows(const void* x, bool f32, int n, int K, int64_t 
 // twice. Bytes hold w + 128, channels and inputs beyond N and K hold 128 (zero).
 constexpr int kPackRows = 128;
 constexpr int kPackK = 128;
+__host__ __device__ constexpr int channel_blocks(int N) { return (int)((N + (kPackRows - 1LL)) / kPackRows); }
+static_assert(channel_blocks(2147483647) == 16777216, "counted beyond 32 bits");
 cudaError_t launch_pack_i8(const int8_t* w, int N, int K, int64_t ldw, uint8_t* packed, cudaStream_t st);
 
 struct LinearArgs {

@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(256) k_pack_i8(const int8_t* w, int N, int K, 
   pdl_wait();
   pdl_release();
   const int kb = (K + kPackK - 1) / kPackK;
-  const long long chunks = (long long)((N + kPackRows - 1) / kPackRows) * kb * (kPackRows * kPackK / 16);
+  const long long chunks = (long long)channel_blocks(N) * kb * (kPackRows * kPackK / 16);
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < chunks; i += (long long)gridDim.x * 256) {
     const int c = (int)(i & 7), r = (int)((i >> 3) & (kPackRows - 1));
     const long long b = i >> 10;
@@ -371,7 +371,7 @@ struct TcPlan {
 // 777 x 20011 x 4096 in 4, 5, 7 tiles 97, 111, 135 us; 256 x 248320 x 2048 in 1, 2
 // tiles 151, 220 us.
 static long long tc_cycles(int n, int N, int kb, int tiles, int rows) {
-  const long long ctas = ((N + kPackRows - 1LL) / kPackRows) * tiles, waves = (ctas + kTcSms - 1) / kTcSms;
+  const long long ctas = (long long)channel_blocks(N) * tiles, waves = (ctas + kTcSms - 1) / kTcSms;
   const long long mma = 8LL * kb * (rows > 200 ? rows / 2 : 100), out = 1500 + 10LL * rows;
   return waves * (rows > 128 ? mma + out : mma > out ? mma : out);
 }
@@ -380,10 +380,10 @@ static TcPlan tc_plan(int n, int N, int K) {
   TcPlan p;
   p.kb = (K + kPackK - 1) / kPackK;
   // as few row tiles as fit, or a few more where that fills the last wave better
-  const int least = (n + 255) / 256;
+  const int least = (int)((n + 255LL) / 256);
   long long best = 0;
   for (int tiles = least; tiles <= least + 8; ++tiles) {
-    const int each = (n + tiles - 1) / tiles, pair = each > kTcPairRows, step = pair ? 32 : 16;
+    const int each = (int)(((long long)n + tiles - 1) / tiles), pair = each > kTcPairRows, step = pair ? 32 : 16;
     const int rows = (each + step - 1) / step * step;
     if ((long long)rows * (tiles - 1) >= n) continue;  // its last tile would be empty
     const long long c = tc_cycles(n, N, p.kb, tiles, rows);
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kTcNT, 1) k_linear_i8_tc(LinearArgs g, TcPlan 
   pdl_release();
 
   const int kb = p.kb;
-  const int blocks = (g.N + kPackRows - 1) / kPackRows;
+  const int blocks = channel_blocks(g.N);
   const long long n_tiles = (long long)(PAIR ? (blocks + 1) / 2 : blocks) * p.tiles;
   const uint32_t t0 = PAIR ? blockIdx.x >> 1 : blockIdx.x, t_step = PAIR ? gridDim.x >> 1 : gridDim.x;
 
@@ -770,7 +770,7 @@ I8Tiles linear_i8_tiles(int n, int N, int K, void* workspace) {
 cudaError_t launch_pack_i8(const int8_t* w, int N, int K, int64_t ldw, uint8_t* packed, cudaStream_t st) {
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorUnknown;
-  const long long chunks = (long long)((N + kPackRows - 1) / kPackRows) * ((K + kPackK - 1) / kPackK) * 1024;
+  const long long chunks = (long long)channel_blocks(N) * ((K + kPackK - 1) / kPackK) * 1024;
   const long long want = (chunks + 255) / 256;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(want < sms * 16LL ? want : sms * 16LL));
@@ -827,7 +827,7 @@ cudaError_t launch_linear_i8(const LinearArgs& g, bool bf16_out, cudaStream_t st
     return r != cudaSuccess ? 0 : p.pair ? v : sms;
   });
   if (fit <= 0) return cudaErrorUnknown;
-  const long long blocks = (g.N + kPackRows - 1) / kPackRows;
+  const long long blocks = channel_blocks(g.N);
   const long long tiles = (p.pair ? (blocks + 1) / 2 : blocks) * p.tiles, ctas = tiles < fit ? tiles : fit;
   cfg.gridDim = dim3((unsigned)(p.pair ? 2 * ctas : ctas));
   e = cudaLaunchKernelEx(&cfg, kern, g, p);
