@@ -1,7 +1,8 @@
 """Build libdsample.so in-tree for sm_103a with nvcc (no CMake), and ds_calls.so, its short way from torch tensors.
 
 The Gumbel bound table is generated first, then each translation unit is
-compiled in parallel and linked into vocab_wide_logit_gb300/_build/libdsample.so.
+compiled in parallel and linked into vocab_wide_logit_gb300/_build/libdsample.so,
+which needs nvcc alone. Where torch is installed, ds_calls.so is built beside it.
 """
 import concurrent.futures
 import importlib.util
@@ -39,8 +40,12 @@ def _stale(target, deps):
 
 
 def _calls_command(src, out):
-    """g++ for the CPython module, against the headers and libraries of the installed torch and CUDA runtime."""
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    """g++ for the CPython module, against the headers and libraries of the installed torch and CUDA runtime; None
+    without torch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    torch = spec.submodule_search_locations[0]
     cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
     inc = [INCLUDE, os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
@@ -67,26 +72,31 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         if force or ptxas_verbose or _stale(o, [s] + common):
             jobs.append([nvcc()] + flags + ["-c", s, "-o", o])
     src = os.path.join(CSRC, "py_calls.cpp")
-    calls = CALLS + ".tmp%d" % os.getpid()
-    new_calls = force or _stale(CALLS, [src, os.path.join(INCLUDE, "dsample.h"), os.path.abspath(__file__)])
-    cuda_jobs = len(jobs)
-    if new_calls:
-        jobs.append(_calls_command(src, calls))
-    if jobs:
-        with concurrent.futures.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
-            results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
-        for cmd, r in zip(jobs, results):
+    tmp_calls = CALLS + ".tmp%d" % os.getpid()
+    calls = None
+    if force or _stale(CALLS, [src, os.path.join(INCLUDE, "dsample.h"), os.path.abspath(__file__)]):
+        calls = _calls_command(src, tmp_calls)
+        if calls is None:
+            sys.stderr.write("torch is not installed: ds_calls.so (calls on torch tensors) is not built\n")
+    failed = []
+    commands = jobs + ([calls] if calls else [])
+    if commands:
+        with concurrent.futures.ThreadPoolExecutor(max_workers=len(commands)) as ex:
+            results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), commands))
+        for cmd, r in zip(commands, results):
             if verbose or ptxas_verbose or r.returncode != 0:
                 sys.stderr.write(r.stdout + r.stderr)
             if r.returncode != 0:
-                raise RuntimeError("compiler failed: " + " ".join(cmd))
+                failed.append(cmd)
     objs = [os.path.join(OUT, s.replace(".cu", ".o")) for s in SOURCES]
-    if new_calls:
-        os.replace(calls, CALLS)
-    if force or cuda_jobs or _stale(LIB, objs):
+    if not any(cmd in failed for cmd in jobs) and (force or jobs or _stale(LIB, objs)):
         tmp = LIB + ".tmp%d" % os.getpid()
         subprocess.run([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart"], check=True)
         os.replace(tmp, LIB)
+    if calls and calls not in failed:
+        os.replace(tmp_calls, CALLS)
+    if failed:
+        raise RuntimeError("compiler failed: " + "; ".join(" ".join(cmd) for cmd in failed))
     return LIB
 
 
