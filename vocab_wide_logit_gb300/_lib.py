@@ -217,6 +217,15 @@ def calls():
             raise OSError("ds_calls.so not built at %s: run __graft_entry__.build() or "
                           "python vocab_wide_logit_gb300/build.py" % path)
         import torch  # noqa: F401  (its libraries are what the module links to)
+        from .build import torch_identity
+        try:
+            with open(os.path.splitext(path)[0] + ".torch") as f:
+                built_with = f.read()
+        except OSError:
+            built_with = None
+        if built_with != torch_identity():
+            raise OSError("%s was built for another torch: run __graft_entry__.build() or "
+                          "python vocab_wide_logit_gb300/build.py" % path)
         spec = importlib.util.spec_from_file_location("ds_calls", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)

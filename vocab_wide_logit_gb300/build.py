@@ -39,6 +39,24 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def torch_identity():
+    """What ds_calls.so depends on of the installed torch: its version file (None without torch)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    with open(os.path.join(spec.submodule_search_locations[0], "version.py")) as f:
+        return f.read()
+
+
+def _calls_torch():
+    """The torch_identity() that ds_calls.so was built with, None when that is not known."""
+    try:
+        with open(os.path.splitext(CALLS)[0] + ".torch") as f:
+            return f.read()
+    except OSError:
+        return None
+
+
 def _calls_command(src, out):
     """g++ for the CPython module, against the headers and libraries of the installed torch and CUDA runtime; None
     without torch."""
@@ -73,8 +91,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             jobs.append([nvcc()] + flags + ["-c", s, "-o", o])
     src = os.path.join(CSRC, "py_calls.cpp")
     tmp_calls = CALLS + ".tmp%d" % os.getpid()
-    calls = None
-    if force or _stale(CALLS, [src, os.path.join(INCLUDE, "dsample.h"), os.path.abspath(__file__)]):
+    calls, identity = None, torch_identity()
+    deps = [src, os.path.join(INCLUDE, "dsample.h"), os.path.abspath(__file__)]
+    if force or _stale(CALLS, deps) or _calls_torch() != identity:
         calls = _calls_command(src, tmp_calls)
         if calls is None:
             sys.stderr.write("torch is not installed: ds_calls.so (calls on torch tensors) is not built\n")
@@ -95,6 +114,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         os.replace(tmp, LIB)
     if calls and calls not in failed:
         os.replace(tmp_calls, CALLS)
+        with open(os.path.splitext(CALLS)[0] + ".torch", "w") as f:
+            f.write(identity)
     if failed:
         raise RuntimeError("compiler failed: " + "; ".join(" ".join(cmd) for cmd in failed))
     return LIB
