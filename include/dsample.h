@@ -55,7 +55,7 @@ typedef enum {
 #define DS_MAX_ITERATION 16777215u /* iteration < 2^24; it keys the noise next to the row */
 #define DS_MAX_VOCAB 524281      /* largest V of ds_sample (16-CTA cluster, 32K elements per CTA) */
 #define DS_FILTERED_MAX_VOCAB 2097152 /* largest V of ds_sample_filtered: a row's mass stays below 2^53 */
-#define DS_LINEAR_MAX_K 131071   /* largest K of ds_linear_i8: K * 128 * 128 stays below 2^31 */
+#define DS_LINEAR_MAX_K 131071   /* largest K of ds_linear_i8: sums beyond 2^24 are off by a thousandth at most */
 
 /*
  * ds_sample -- sample every cell of a packed batch of guided logits.
@@ -373,8 +373,11 @@ int64_t ds_linear_i8_workspace(int32_t n, int32_t N, int32_t K);
  *
  *   out[i][j] = (sum over k of a[i][k] * w[j][k]) * a_scale[i] * w_scale[j]
  *
- * Products are exact and sums are kept in fp32: a sum is exact as long as its
- * running value stays below 2^24, and rounded to fp32 beyond.
+ * Products are exact and sums are kept in fp32, 16 inputs a step: a sum is exact
+ * as long as its running value stays below 2^24 - 2^18 (whatever the operands up to
+ * K = 1024). Beyond, each step may drop what lies below the running sum's fp32
+ * spacing, so that the sum is off by less than (K / 16 + 1) 2^-23 of the largest
+ * running value.
  *
  * Arguments:
  *   a          device int8 [n][K], rows lda bytes apart (lda >= K), any alignment.

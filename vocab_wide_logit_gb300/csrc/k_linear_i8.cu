@@ -3,8 +3,11 @@
 //
 // The mathematics. Integers of 8 bits are exact in fp16 and their products (at most
 // 2^14) in fp32, so the tensor cores' fp16 products with fp32 sums are the integer
-// product as long as a running sum stays below 2^24. The 8-bit integer rate of this
-// GPU is far below its fp16 rate, so nothing is lost by that.
+// product as long as a running sum stays below 2^24. Beyond, an instruction (16
+// inputs) truncates: with operands of one sign and the largest size, 1.8e-4 of the
+// sum is lost at K = 131071, 1.1e-4 at 16384 and one unit at 1041. The 8-bit integer
+// rate of this GPU is far below its fp16 rate; rows and weights of a model have both
+// signs, and their sums stay below 2^24 at any K allowed.
 //
 // The layout. The weight is the large operand and is read once, as 8 bits. It is
 // packed once into blocks of 128 channels x 128 inputs (16 KB, consecutive in memory),
