@@ -25,18 +25,19 @@
 //   rows > 128   a pair of CTAs per 256 channels, one instruction for both, each with
 //                half of the row tile: 96 KB instead of 160 KB through shared memory
 //                per block of 128 inputs. One CTA alone took 1150-1190 cycles per block
-//                of 1024 of instructions and 172 us where the pair takes 151 (256 rows
-//                x 248320 x 2048; 777 x 20011 x 4096: 122 and 97 us).
+//                of 1024 of instructions and 172 us where the pair takes 150 (256 rows
+//                x 248320 x 2048; 777 x 20011 x 4096: 122 and 94 us).
 //
 // What bounds it (bf16 out, K and the rest as stated):
 //   24 x 248320 x 2048    82 us with its ds_quantize_rows, 522 MB at 6.4 TB/s: HBM
-//   256 x 248320 x 2048   149 us, 260 GFLOP at 1.75 PFLOP/s, tensor pipe 78% busy; the
+//   256 x 248320 x 2048   150 us, 260 GFLOP at 1.74 PFLOP/s, tensor pipe 79% busy; the
 //                         rest is reading the accumulator, 128 KB in 2300-2600 cycles
-//                         per tile (tensor memory gives about 50 bytes a cycle), and the
-//                         handing over to the next tile
-//   777 x 20011 x 4096    97 us, 1.31 PFLOP/s: the same, and 316 tiles on 76 pairs
-//   1939 x 8200 x 1024    33 us: tiles of 8 blocks, a third of the time between them
-//   one row x 8200 x 1024 9 us with its ds_quantize_rows: latency, 65 tiles on 152 SMs
+//                         per tile, and the handing over to the next tile. A warp has
+//                         one load of 2 KB in flight and waits for it, so that this may
+//                         be latency as well as tensor memory's rate: not told apart
+//   777 x 20011 x 4096    94 us, 1.35 PFLOP/s: the same, and 316 tiles on 76 pairs
+//   1939 x 8200 x 1024    32 us: tiles of 8 blocks, a third of the time between them
+//   one row x 8200 x 1024 8.5 us with its ds_quantize_rows: latency, 65 tiles on 152 SMs
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -9,10 +9,12 @@
 // which saves that call its own pass over them.
 //
 // Bound by latency at decoding sizes, a load, two block reductions and a store:
-// 1.8 us for a row of 1024, 1.9 us for 24 rows of 2048, 2.2 us for 256 (bf16, with a
-// gain). Wide batches are bound by instructions: 8192 rows of 4096 take 35 us,
-// 2.9 TB/s. A thread keeps 1, 2 or 4 chunks by K: with 4 throughout, 8192 x 4096
-// took 90 us for the registers it held.
+// 1.8 us for a row of 1024, 1.9 us for 24 rows of 2048, 2.1 us for 256 (bf16, with a
+// gain). Wide batches: 8192 rows of 4096 take 35 us, 2.9 TB/s. 24 instructions an
+// input fill 61% of the issue slots, and a CTA has none of the next row's loads in
+// flight across a row's two reductions, which the profile shows as the longest
+// stall. A thread keeps 1, 2 or 4 chunks by K: with 4 throughout, 8192 x 4096 took
+// 90 us for the registers it held.
 #include <cuda_fp16.h>
 
 #include <type_traits>

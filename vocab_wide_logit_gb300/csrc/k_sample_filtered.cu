@@ -199,7 +199,7 @@ __device__ __noinline__ Cut row_select(const Row<T> row, bool by_count, u64 t, f
             const uint32_t key = Logit<T>::key(f[i]);
             const uint32_t w = sf_weight(f[i], m, r);
             const bool in = key >= lo && key <= hi && w;
-            // a warp whose logits all fall on one bin adds them up first: ties are what this search is for
+            // a warp whose logits all fall on one bin adds them up first: ties are one thing this search is for
             const unsigned who = __ballot_sync(0xffffffffu, in);
             if (!who) continue;
             const int bin = in ? (int)((hi - key) >> s) : -1;
@@ -350,8 +350,8 @@ __device__ __forceinline__ u64 fraction_high(float f, u64 total) {
 }
 
 // The row's token, each question by a search over the row, which one CTA re-reads
-// some ten times. It assumes nothing of the row: it finishes those whose ties are
-// too many for the lists of the fast kernel.
+// some ten times. It assumes nothing of the row: it finishes those whose boundaries
+// meet too many logits for the lists of the fast kernel, by ties or in a flat row.
 template <typename T, int NT, int NB>
 __device__ __noinline__ int row_exact(const T* p, int V, const RowParams& q, float m, const Bins<NB>& b, int* slot) {
   const Row<T> row(p, V);
@@ -405,9 +405,10 @@ __device__ __noinline__ int row_exact(const T* p, int V, const RowParams& q, flo
 // to an integer by half a unit. Where the boundary's logits are too light for
 // that, the cluster weighs the rest of the row exactly (kWeigh), and where it
 // falls between two listed logits all the same, rank 0 does.
-// A row whose boundary bins hold more than CAP logits (ties) is finished by
-// row_exact. So a logit costs two ex2 and its share of two walks over the row; an
-// exact weight and an atomic only above x1.
+// A row whose boundary bins hold more than CAP logits is finished by row_exact, in
+// one CTA: rows of ties, and flat rows, whose nucleus or draw reaches so far down
+// that a bin of x there holds that many. Every other row's logit costs two ex2 and
+// its share of two walks over the row; an exact weight and an atomic only above x1.
 //
 // Batches that fill the GPU take a warp (short rows) or a CTA (long ones) per row
 // and leave the few rows that need more to a second launch (kFirst, kMarked): the
@@ -422,8 +423,10 @@ __device__ __noinline__ int row_exact(const T* p, int V, const RowParams& q, flo
 // What bounds it: long rows HBM first, then the latency of the steps behind the
 // walk (51 us for 256 x 248320 with a top-k, 19 of them at the copy rate); short
 // rows instructions and their fetch (3100 per row of 1025 at 56% of the issue
-// rate, 107 us for 15510 rows of 1025); single rows the barriers (9 us for 1025,
-// 19 us for 248320).
+// rate, 110 us for 15510 rows of 1025); single rows the barriers (9 us for 1025,
+// 19 us for 248320). Flat rows row_exact, a CTA a row: 256 x 248320, top-p 0.9 of
+// normal logits of spread 4, 3, 2, 1: 0.27, 1.1, 4.7, 6.3 ms (bf16), 0.29, 0.39, 4.2,
+// 10.0 ms (fp32).
 namespace {
 
 template <int NT, int NB, int CAP, int QCAP, int CS>  // QCAP 0: no queue; CS: most CTAs of a cluster
@@ -828,6 +831,8 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 28 : NT == 128 ? 6 : 1024 / NT)
     // The first cut; none for a short row of the second pass.
     // A warp's own row starts a little lower, and lower still for a top-k that
     // would end below (15510 x 1025, 12% of the rows with k = 200: 148 -> 129 us).
+    // These shares, like the other steps of the cut, were fitted to normal logits of
+    // spread 3 and 4. They decide how many walks a row takes, never its answer.
     const float further = PASS == kMarked ? (RESIDENT ? 1e30f : 0.f) : NT == 32 ? (q.k > 64 ? .35f : .15f) : 0.f;
     // Without a cut (in each CTA a group without a logit) all of the row is above it.
     x1 = ONE_WALK || !(cut > -kInf) ? cut : cut - further * (m - cut);
