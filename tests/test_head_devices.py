@@ -176,3 +176,10 @@ def test_workspace_holds_every_row(n):
         assert n * 256 <= pkg.linear_i8_workspace(n, N, 1) <= n * 256 + 256 * 256 * 2
         assert pkg.head_i8_workspace(n, N, 1) == pkg.linear_i8_workspace(n, N, 1) + 4 * n
         assert pkg.packed_i8_bytes(N, 1) == (N + 127) // 128 * 128 * 128
+
+
+@pytest.mark.parametrize("name", sorted(_named_calls(0)))
+def test_any_object_with_a_stream_handle_will_do(launched, name):
+    """A stream of another library: a handle, and no word of its device."""
+    _named_calls(0)[name](stream=types.SimpleNamespace(cuda_stream=7))
+    assert launched

@@ -118,9 +118,10 @@ def _stream(stream, t):
     import torch
     if stream is None:
         stream = torch.cuda.current_stream()
-    if t is not None and t.is_cuda and t.get_device() != stream.device_index:
+    index = getattr(stream, "device_index", None)  # another library's stream may not say
+    if t is not None and index is not None and t.is_cuda and t.get_device() != index:
         raise ValueError("a tensor on cuda:%d for a stream of cuda:%d (the current stream unless one is given)"
-                         % (t.get_device(), stream.device_index))
+                         % (t.get_device(), index))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
