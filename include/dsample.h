@@ -13,7 +13,9 @@
  * (vocabulary-shard merge) and ds_log_softmax (dense log-probabilities); and the
  * serving head: ds_quantize_rows, ds_pack_i8, ds_linear_i8 and ds_head_i8 (hidden
  * states to logits through an 8-bit vocabulary projection) and ds_sample_filtered
- * (logits to tokens by temperature, top-k, top-p and min-p). All are
+ * (logits to tokens by temperature, top-k, top-p and min-p), ds_add_adapters
+ * (each request's low-rank adapter on the logits), ds_score_tokens and
+ * ds_score_tokens_grad (log-probabilities of given tokens, and their gradient). All are
  * asynchronous on the caller's CUDA stream, allocate nothing and keep no state
  * between calls beyond a process-wide count of kernel launches
  * (ds_launch_count).
@@ -44,8 +46,9 @@ typedef enum {
 /* Bits OR-ed into *d_status by the kernels (device-detected input errors). */
 #define DS_DEV_ERR_LAYOUT 1u   /* sum(seq_lens) != P, or a negative seq_len */
 #define DS_DEV_ERR_NO_UNCOND 2u /* guidance != 0 for a request but u_logits == NULL */
-#define DS_DEV_ERR_PARAM 4u    /* temperature < 0 or NaN, or guidance NaN; any parameter of ds_sample_filtered */
-#define DS_DEV_ERR_LOGITS 8u   /* ds_sample_filtered: a NaN or +inf among a row's logits */
+#define DS_DEV_ERR_PARAM 4u    /* temperature < 0 or NaN, or guidance NaN; any parameter of ds_sample_filtered;
+                                  a token >= V or an adapter >= L */
+#define DS_DEV_ERR_LOGITS 8u   /* ds_sample_filtered, ds_score_tokens: a NaN or +inf among a row's logits */
 /* A wait inside a kernel ran out: ds_linear_i8 and ds_head_i8 leave NaN for the
  * results not made, ds_sample_filtered token -1 and logprob NaN. */
 #define DS_DEV_ERR_TIMEOUT 16u
@@ -56,6 +59,9 @@ typedef enum {
 #define DS_MAX_VOCAB 524281      /* largest V of ds_sample (16-CTA cluster, 32K elements per CTA) */
 #define DS_FILTERED_MAX_VOCAB 2097152 /* largest V of ds_sample_filtered: a row's mass stays below 2^53 */
 #define DS_LINEAR_MAX_K 131071   /* largest K of ds_linear_i8: sums beyond 2^24 are off by a thousandth at most */
+#define DS_SCORE_MAX_TOP 128     /* most alternatives of ds_score_tokens */
+#define DS_ADAPTERS_MAX 8192     /* most adapters of ds_add_adapters */
+#define DS_ADAPTERS_MAX_RANK 128 /* their largest rank */
 
 /*
  * ds_sample -- sample every cell of a packed batch of guided logits.
@@ -421,6 +427,122 @@ int64_t ds_head_i8_workspace(int32_t n, int32_t N, int32_t K);
 ds_status ds_head_i8(const void* x, int32_t dtype, int32_t n, int32_t K, int64_t ld, const float* gain, float eps,
                      const void* packed, const float* w_scale, int32_t N, void* out, int32_t out_dtype, int64_t ldo,
                      void* workspace, int64_t workspace_bytes, uint32_t* d_status, void* stream);
+
+/*
+ * ds_score_tokens -- log-probabilities of given tokens, with the row's
+ * log-sum-exp and entropy, the token's rank and the most likely alternatives.
+ *
+ * Per row of logits x, over the full vocabulary at temperature 1, with the order
+ * (logit descending, id ascending; -0 and +0 tie):
+ *   lse = logsumexp(x),  logprob = x[token] - lse,
+ *   entropy = -sum of p log p with p = exp(x - lse) (nats; p = 0 counts nothing),
+ *   rank = how many tokens come before the given one in the order (0: the argmax),
+ *   top alternatives = the first `top` of the order.
+ *
+ * Arguments:
+ *   logits       device [n][V] of dtype, rows ld elements apart (ld >= V), any
+ *                alignment of the element type. -inf, or the type's lowest
+ *                value, masks a token.
+ *   dtype        DS_DTYPE_BF16 or DS_DTYPE_F32.
+ *   n, V         n >= 0 (0: nothing launched), V >= 1.
+ *   tokens       device int32 [n]. A negative one stands for none (a padded row,
+ *                a row that ds_sample_filtered had nothing to draw from): logprob
+ *                NaN, rank -1, the row's other results as usual. One >= V gives
+ *                the same and DS_DEV_ERR_PARAM.
+ *   top          0 <= top <= min(V, DS_SCORE_MAX_TOP).
+ *   out_logprobs device float [n].
+ *   out_lse, out_entropy, out_ranks
+ *                device float [n], float [n], int32 [n]; each may be NULL.
+ *   out_top_ids, out_top_logprobs
+ *                device int32 [n][top] and float [n][top], dense; not used (and
+ *                may be NULL) when top is 0.
+ *   d_status     device uint32 or NULL; the kernels OR DS_DEV_ERR_* bits into it.
+ *   stream       cudaStream_t.
+ * A row with nothing in it (every logit -inf) has lse -inf, logprob, entropy and
+ * alternatives' logprobs NaN, rank and alternatives' ids -1. So has one with a NaN
+ * or +inf, with lse NaN and DS_DEV_ERR_LOGITS. Other rows are not affected.
+ * Returns DS_OK, DS_ERR_INVALID_ARG, DS_ERR_UNSUPPORTED (top > DS_SCORE_MAX_TOP,
+ * ld > 2^40) or DS_ERR_CUDA.
+ */
+ds_status ds_score_tokens(const void* logits, int32_t dtype, int32_t n, int32_t V, int64_t ld, const int32_t* tokens,
+                          int32_t top, float* out_logprobs, float* out_lse, float* out_entropy, int32_t* out_ranks,
+                          int32_t* out_top_ids, float* out_top_logprobs, uint32_t* d_status, void* stream);
+
+/*
+ * ds_score_tokens_grad -- gradient of ds_score_tokens' log-probabilities and
+ * entropies with respect to the logits.
+ *
+ *   out[j] = g_logprob ([j == token] - p_j) - g_entropy p_j (log p_j + entropy),
+ *   p_j = exp(x_j - lse)
+ * in fp32, rounded once to dtype.
+ *
+ * Arguments (logits, dtype, n, V, ld, tokens, d_status, stream as there):
+ *   lse, entropy device float [n], as ds_score_tokens wrote them; entropy may be
+ *                NULL without g_entropy. lse is taken as it is: its half ulp, 2^-24 of
+ *                its size, is p's relative error.
+ *   g_logprobs, g_entropy
+ *                device float [n], the loss's gradient by each row's results;
+ *                one of them may be NULL for none.
+ *   out          device [n][V] of dtype, rows ldo elements apart (ldo >= V). May
+ *                be the logits themselves (with ldo == ld); any other overlap of
+ *                the two is not allowed. What lies between the rows is not written.
+ * A row without a token (negative, or >= V, which sets DS_DEV_ERR_PARAM) takes its
+ * g_logprob as 0 whatever it is. A row with nothing in it (lse -inf) gets zeros;
+ * one with lse NaN gets NaN.
+ * Returns DS_OK, DS_ERR_INVALID_ARG, DS_ERR_UNSUPPORTED (ld or ldo > 2^40) or
+ * DS_ERR_CUDA.
+ */
+ds_status ds_score_tokens_grad(const void* logits, int32_t dtype, int32_t n, int32_t V, int64_t ld,
+                               const int32_t* tokens, const float* lse, const float* entropy, const float* g_logprobs,
+                               const float* g_entropy, void* out, int64_t ldo, uint32_t* d_status, void* stream);
+
+/* Bytes of workspace that ds_add_adapters needs for these sizes (0: arguments out
+ * of range). Host-only, no CUDA call. */
+int64_t ds_add_adapters_workspace(int32_t n, int32_t L, int32_t R);
+
+/*
+ * ds_add_adapters -- a low-rank adapter of each row's own, added to the logits of
+ * a projection that all rows share.
+ *
+ *   out[i] = base[i] + scale[q] * B[q] (A[q] y[i]),  q = ids[i],
+ *   y = x, or x * rsqrt(mean(x^2) + eps) * gain when gain is given
+ * in fp32, rounded once to dtype; products of the adapters' bf16 with fp32 values
+ * lose nothing above 2^-23 of them.
+ *
+ * Arguments:
+ *   base         device [n][N] of dtype, rows ldb elements apart (ldb >= N), any
+ *                alignment of the element type.
+ *   dtype        DS_DTYPE_BF16 or DS_DTYPE_F32, of base and out.
+ *   n, N         n >= 0 (0: nothing launched), N >= 1.
+ *   x            device [n][K] of x_dtype, rows ldx elements apart (ldx >= K), any
+ *                alignment of the element type: the hidden states that the
+ *                projection was fed, before its norm when gain is given.
+ *   gain, eps    as for ds_quantize_rows.
+ *   a, b         device bf16 [L][R][K] and [L][N][R], dense; 2-byte alignment
+ *                (16 bytes and R a multiple of 8 are the fast case). A program
+ *                may keep L slots and rewrite one while no call that uses it runs;
+ *                adapters of a lower rank are filled up with zeros.
+ *   scale        device float [L].
+ *   L, R         1 <= L <= DS_ADAPTERS_MAX, 1 <= R <= DS_ADAPTERS_MAX_RANK.
+ *   ids          device int32 [n], rows of an adapter in any order; a negative one
+ *                stands for none (out[i] = base[i]). One >= L gives a row of NaN
+ *                and DS_DEV_ERR_PARAM.
+ *   out          device [n][N] of dtype, rows ldo elements apart (ldo >= N). May be
+ *                base itself (with ldo == ldb); any other overlap of the two is not
+ *                allowed. What lies between the rows is not written.
+ *   workspace    device, workspace_bytes >= ds_add_adapters_workspace(n, L, R),
+ *                128-byte aligned. Its contents need not be kept between calls;
+ *                calls that may run at once need one each.
+ *   d_status     device uint32 or NULL.
+ *   stream       cudaStream_t.
+ * A row of x with a NaN or an infinity gives a row of NaN.
+ * Returns DS_OK, DS_ERR_INVALID_ARG, DS_ERR_UNSUPPORTED (L, R, ldb, ldx or ldo too
+ * large) or DS_ERR_CUDA.
+ */
+ds_status ds_add_adapters(const void* base, int32_t dtype, int32_t n, int32_t N, int64_t ldb, const void* x,
+                          int32_t x_dtype, int32_t K, int64_t ldx, const float* gain, float eps, const void* a,
+                          const void* b, const float* scale, int32_t L, int32_t R, const int32_t* ids, void* out,
+                          int64_t ldo, void* workspace, int64_t workspace_bytes, uint32_t* d_status, void* stream);
 
 /* Static description of a status code. Never NULL. */
 const char* ds_status_string(ds_status s);

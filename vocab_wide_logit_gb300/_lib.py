@@ -24,11 +24,14 @@ DS_DEV_ERR_TIMEOUT = 16
 DS_MAX_VOCAB = 524281
 DS_FILTERED_MAX_VOCAB = 2097152
 DS_LINEAR_MAX_K = 131071
+DS_SCORE_MAX_TOP = 128
+DS_ADAPTERS_MAX = 8192
+DS_ADAPTERS_MAX_RANK = 128
 
 EXPORTED = ("ds_sample", "ds_greedy_lse", "ds_status_string", "ds_top_k", "ds_merge_triples", "ds_log_softmax",
             "ds_reveal", "ds_sample_ex", "ds_launch_count", "ds_sample_filtered", "ds_quantize_rows",
             "ds_packed_i8_bytes", "ds_pack_i8", "ds_linear_i8_workspace", "ds_linear_i8", "ds_head_i8_workspace",
-            "ds_head_i8")
+            "ds_head_i8", "ds_score_tokens", "ds_score_tokens_grad", "ds_add_adapters_workspace", "ds_add_adapters")
 DS_FLAG_KEEP_TIES = 1
 DS_FLAG_SKIP_EXACT_PASS = 2
 DS_MARKED = -2
@@ -91,6 +94,15 @@ def load(path: str = LIB_PATH):
     L.ds_head_i8_workspace.restype = i64
     L.ds_head_i8.argtypes = [vp, i32, i32, i32, i64, vp, f32, vp, vp, i32, vp, i32, i64, vp, i64, vp, vp]
     L.ds_head_i8.restype = ctypes.c_int
+    L.ds_score_tokens.argtypes = [vp, i32, i32, i32, i64, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.ds_score_tokens.restype = ctypes.c_int
+    L.ds_score_tokens_grad.argtypes = [vp, i32, i32, i32, i64, vp, vp, vp, vp, vp, vp, i64, vp, vp]
+    L.ds_score_tokens_grad.restype = ctypes.c_int
+    L.ds_add_adapters_workspace.argtypes = [i32, i32, i32]
+    L.ds_add_adapters_workspace.restype = i64
+    L.ds_add_adapters.argtypes = [vp, i32, i32, i32, i64, vp, i32, i32, i64, vp, f32, vp, vp, vp, i32, i32, vp, vp, i64,
+                                  vp, i64, vp, vp]
+    L.ds_add_adapters.restype = ctypes.c_int
     _lib = L
     return L
 
@@ -346,4 +358,70 @@ def ds_linear_i8(a, a_scale, packed, w_scale, out, N, K, workspace=None, d_statu
                              out_dtype, ldo, _ptr(workspace), workspace_bytes, _ptr(d_status), _stream(stream, a))
     if check and rc != DS_OK:
         raise DsError("ds_linear_i8", rc)
+    return rc
+
+
+def ds_score_tokens(logits, tokens, out_logprobs, out_lse=None, out_entropy=None, out_ranks=None, out_top_ids=None,
+                    out_top_logprobs=None, top=None, d_status=None, n=None, V=None, ld=None, stream=None, check=True):
+    """Call ds_score_tokens: logits [n, V] bfloat16 or float32 (rows ld elements apart), tokens int32 [n], out_logprobs /
+    out_lse / out_entropy float32 [n], out_ranks int32 [n], out_top_ids int32 and out_top_logprobs float32 [n, top]."""
+    if n is None:
+        n, V = logits.shape
+    if ld is None:
+        ld = logits.stride(0) if n > 1 else V
+    if top is None:
+        top = 0 if out_top_ids is None else out_top_ids.shape[1]
+    rc = load().ds_score_tokens(logits.data_ptr(), _dtype_code(logits), n, V, ld, _ptr(tokens), top, _ptr(out_logprobs),
+                                _ptr(out_lse), _ptr(out_entropy), _ptr(out_ranks), _ptr(out_top_ids),
+                                _ptr(out_top_logprobs), _ptr(d_status), _stream(stream, logits))
+    if check and rc != DS_OK:
+        raise DsError("ds_score_tokens", rc)
+    return rc
+
+
+def ds_score_tokens_grad(logits, tokens, lse, out, entropy=None, g_logprobs=None, g_entropy=None, d_status=None, n=None,
+                         V=None, ld=None, ldo=None, stream=None, check=True):
+    """Call ds_score_tokens_grad: logits and out [n, V] of one type, tokens int32 [n], lse / entropy / g_logprobs /
+    g_entropy float32 [n]."""
+    if n is None:
+        n, V = logits.shape
+    if ld is None:
+        ld = logits.stride(0) if n > 1 else V
+    if ldo is None:
+        ldo = out.stride(0) if n > 1 else V
+    rc = load().ds_score_tokens_grad(logits.data_ptr(), _dtype_code(logits), n, V, ld, _ptr(tokens), _ptr(lse),
+                                     _ptr(entropy), _ptr(g_logprobs), _ptr(g_entropy), _ptr(out), ldo, _ptr(d_status),
+                                     _stream(stream, logits))
+    if check and rc != DS_OK:
+        raise DsError("ds_score_tokens_grad", rc)
+    return rc
+
+
+def add_adapters_workspace(n: int, L: int, R: int) -> int:
+    return int(load().ds_add_adapters_workspace(int(n), int(L), int(R)))
+
+
+def ds_add_adapters(base, x, a, b, scale, ids, out, workspace, gain=None, eps=1e-6, d_status=None, n=None, N=None,
+                    K=None, L=None, R=None, ldb=None, ldx=None, ldo=None, workspace_bytes=None, stream=None, check=True):
+    """Call ds_add_adapters: base and out [n, N] of one type, x [n, K], a bfloat16 [L, R, K], b bfloat16 [L, N, R], scale
+    float32 [L], ids int32 [n], gain float32 [K] or None, workspace uint8 of ds_add_adapters_workspace(n, L, R) bytes."""
+    if n is None:
+        n, N = base.shape
+    if K is None:
+        K = x.shape[1]
+    if L is None:
+        L, R = a.shape[:2]
+    if ldb is None:
+        ldb = base.stride(0) if n > 1 else N
+    if ldx is None:
+        ldx = x.stride(0) if n > 1 else K
+    if ldo is None:
+        ldo = out.stride(0) if n > 1 else N
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    rc = load().ds_add_adapters(base.data_ptr(), _dtype_code(base), n, N, ldb, x.data_ptr(), _dtype_code(x), K, ldx,
+                                _ptr(gain), float(eps), _ptr(a), _ptr(b), _ptr(scale), L, R, _ptr(ids), _ptr(out), ldo,
+                                _ptr(workspace), workspace_bytes, _ptr(d_status), _stream(stream, base))
+    if check and rc != DS_OK:
+        raise DsError("ds_add_adapters", rc)
     return rc

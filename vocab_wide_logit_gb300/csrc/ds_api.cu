@@ -363,4 +363,77 @@ ds_status ds_linear_i8(const int8_t* a, int64_t lda, const float* a_scale, const
   return e == cudaSuccess ? DS_OK : DS_ERR_CUDA;
 }
 
+ds_status ds_score_tokens(const void* logits, int32_t dtype, int32_t n, int32_t V, int64_t ld, const int32_t* tokens,
+                          int32_t top, float* out_logprobs, float* out_lse, float* out_entropy, int32_t* out_ranks,
+                          int32_t* out_top_ids, float* out_top_logprobs, uint32_t* d_status, void* stream) {
+  if (n < 0 || V < 1 || ld < V || top < 0 || top > V) return DS_ERR_INVALID_ARG;
+  if (dtype != DS_DTYPE_F32 && dtype != DS_DTYPE_BF16) return DS_ERR_INVALID_ARG;
+  if (top > DS_SCORE_MAX_TOP || ld > (1LL << 40)) return DS_ERR_UNSUPPORTED;
+  if (n == 0) return DS_OK;
+  if (!logits || !tokens || !out_logprobs || (top > 0 && (!out_top_ids || !out_top_logprobs))) return DS_ERR_INVALID_ARG;
+  const uintptr_t words = reinterpret_cast<uintptr_t>(tokens) | reinterpret_cast<uintptr_t>(out_logprobs) |
+                          reinterpret_cast<uintptr_t>(out_lse) | reinterpret_cast<uintptr_t>(out_entropy) |
+                          reinterpret_cast<uintptr_t>(out_ranks) | reinterpret_cast<uintptr_t>(out_top_ids) |
+                          reinterpret_cast<uintptr_t>(out_top_logprobs) | reinterpret_cast<uintptr_t>(d_status);
+  if ((words & 3) || (reinterpret_cast<uintptr_t>(logits) & (dtype == DS_DTYPE_F32 ? 3 : 1))) return DS_ERR_INVALID_ARG;
+  const ds::ScoreArgs a = {logits,      ld,        n,           V,           top,     tokens, out_logprobs, out_lse,
+                           out_entropy, out_ranks, out_top_ids, out_top_logprobs, d_status};
+  const cudaError_t e = ds::launch_score(a, dtype == DS_DTYPE_F32, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DS_OK : DS_ERR_CUDA;
+}
+
+ds_status ds_score_tokens_grad(const void* logits, int32_t dtype, int32_t n, int32_t V, int64_t ld,
+                               const int32_t* tokens, const float* lse, const float* entropy, const float* g_logprobs,
+                               const float* g_entropy, void* out, int64_t ldo, uint32_t* d_status, void* stream) {
+  if (n < 0 || V < 1 || ld < V || ldo < V) return DS_ERR_INVALID_ARG;
+  if (dtype != DS_DTYPE_F32 && dtype != DS_DTYPE_BF16) return DS_ERR_INVALID_ARG;
+  if (ld > (1LL << 40) || ldo > (1LL << 40)) return DS_ERR_UNSUPPORTED;
+  if (n == 0) return DS_OK;
+  if (!logits || !tokens || !lse || !out || (!g_logprobs && !g_entropy) || (g_entropy && !entropy))
+    return DS_ERR_INVALID_ARG;
+  if (logits == out && ld != ldo) return DS_ERR_INVALID_ARG;
+  const uintptr_t words = reinterpret_cast<uintptr_t>(tokens) | reinterpret_cast<uintptr_t>(lse) |
+                          reinterpret_cast<uintptr_t>(entropy) | reinterpret_cast<uintptr_t>(g_logprobs) |
+                          reinterpret_cast<uintptr_t>(g_entropy) | reinterpret_cast<uintptr_t>(d_status);
+  const uintptr_t rows = reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(out);
+  if ((words & 3) || (rows & (dtype == DS_DTYPE_F32 ? 3 : 1))) return DS_ERR_INVALID_ARG;
+  const ds::ScoreGradArgs a = {logits, ld, n, V, tokens, lse, entropy, g_logprobs, g_entropy, out, ldo, d_status};
+  const cudaError_t e = ds::launch_score_grad(a, dtype == DS_DTYPE_F32, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DS_OK : DS_ERR_CUDA;
+}
+
+int64_t ds_add_adapters_workspace(int32_t n, int32_t L, int32_t R) {
+  if (n < 1 || L < 1 || R < 1 || L > DS_ADAPTERS_MAX || R > DS_ADAPTERS_MAX_RANK) return 0;
+  return ds::adapters_workspace(n, L, R);
+}
+
+ds_status ds_add_adapters(const void* base, int32_t dtype, int32_t n, int32_t N, int64_t ldb, const void* x,
+                          int32_t x_dtype, int32_t K, int64_t ldx, const float* gain, float eps, const void* a,
+                          const void* b, const float* scale, int32_t L, int32_t R, const int32_t* ids, void* out,
+                          int64_t ldo, void* workspace, int64_t workspace_bytes, uint32_t* d_status, void* stream) {
+  if (n < 0 || N < 1 || K < 1 || L < 1 || R < 1 || ldb < N || ldx < K || ldo < N) return DS_ERR_INVALID_ARG;
+  if (dtype != DS_DTYPE_F32 && dtype != DS_DTYPE_BF16) return DS_ERR_INVALID_ARG;
+  if (x_dtype != DS_DTYPE_F32 && x_dtype != DS_DTYPE_BF16) return DS_ERR_INVALID_ARG;
+  if (gain && !(eps >= 0.f && eps < INFINITY)) return DS_ERR_INVALID_ARG;
+  if (L > DS_ADAPTERS_MAX || R > DS_ADAPTERS_MAX_RANK || ldb > (1LL << 40) || ldx > (1LL << 40) || ldo > (1LL << 40))
+    return DS_ERR_UNSUPPORTED;
+  if (n == 0) return DS_OK;
+  if (!base || !x || !a || !b || !scale || !ids || !out) return DS_ERR_INVALID_ARG;
+  if (base == out && ldb != ldo) return DS_ERR_INVALID_ARG;
+  const uintptr_t words = reinterpret_cast<uintptr_t>(gain) | reinterpret_cast<uintptr_t>(scale) |
+                          reinterpret_cast<uintptr_t>(ids) | reinterpret_cast<uintptr_t>(d_status);
+  const uintptr_t logits = reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(out);
+  const uintptr_t halves = reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b);
+  if ((words & 3) || (halves & 1) || (logits & (dtype == DS_DTYPE_F32 ? 3 : 1)) ||
+      (reinterpret_cast<uintptr_t>(x) & (x_dtype == DS_DTYPE_F32 ? 3 : 1)))
+    return DS_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < ds::adapters_workspace(n, L, R) || (reinterpret_cast<uintptr_t>(workspace) & 127))
+    return DS_ERR_INVALID_ARG;
+  const ds::AdapterArgs g = {base, ldb, x, ldx, gain, eps, static_cast<const uint16_t*>(a),
+                             static_cast<const uint16_t*>(b), scale, ids, n, N, K, L, R, out, ldo, workspace, d_status};
+  const cudaError_t e = ds::launch_add_adapters(g, x_dtype == DS_DTYPE_F32, dtype == DS_DTYPE_F32,
+                                                static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DS_OK : DS_ERR_CUDA;
+}
+
 }  // extern "C"

@@ -137,4 +137,56 @@ I8Tiles linear_i8_tiles(int n, int N, int K, void* workspace);
 // With g.a null the workspace holds the tiles already.
 cudaError_t launch_linear_i8(const LinearArgs& a, bool bf16_out, cudaStream_t st);
 
+// Scores of given tokens in n rows of V logits, ld elements apart.
+struct ScoreArgs {
+  const void* x;  // bf16 or fp32
+  int64_t ld;
+  int32_t n, V, top;
+  const int32_t* tokens;
+  float* out_logprobs;
+  float* out_lse;      // or null
+  float* out_entropy;  // or null
+  int32_t* out_ranks;  // or null
+  int32_t* out_top_ids;     // null without alternatives
+  float* out_top_logprobs;  // the same
+  uint32_t* d_status;
+};
+cudaError_t launch_score(const ScoreArgs& a, bool f32, cudaStream_t st);
+
+struct ScoreGradArgs {
+  const void* x;  // bf16 or fp32, as the result
+  int64_t ld;
+  int32_t n, V;
+  const int32_t* tokens;
+  const float* lse;
+  const float* entropy;     // null without g_entropy
+  const float* g_logprobs;  // or null
+  const float* g_entropy;   // or null
+  void* out;
+  int64_t ldo;
+  uint32_t* d_status;
+};
+cudaError_t launch_score_grad(const ScoreGradArgs& a, bool f32, cudaStream_t st);
+
+// Low-rank adapters added to n rows of N logits.
+struct AdapterArgs {
+  const void* base;  // bf16 or fp32, as the result
+  int64_t ldb;
+  const void* x;  // bf16 or fp32
+  int64_t ldx;
+  const float* gain;  // or null
+  float eps;
+  const uint16_t* a;  // [L][R][K]
+  const uint16_t* b;  // [L][N][R]
+  const float* scale;
+  const int32_t* ids;
+  int32_t n, N, K, L, R;
+  void* out;
+  int64_t ldo;
+  void* workspace;
+  uint32_t* d_status;
+};
+long long adapters_workspace(int n, int L, int R);
+cudaError_t launch_add_adapters(const AdapterArgs& a, bool x_f32, bool f32, cudaStream_t st);
+
 }  // namespace ds

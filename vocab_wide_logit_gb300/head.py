@@ -1,5 +1,5 @@
-"""The serving head: hidden states to logits through an 8-bit vocabulary projection, and logits to tokens by
-temperature, top-k, top-p and min-p.
+"""The serving head: hidden states to logits through an 8-bit vocabulary projection and each request's low-rank adapter,
+and logits to tokens by temperature, top-k, top-p and min-p.
 
 Functions allocate their outputs and check their tensors (a tensor of another type or shape would be read as if it
 were the expected one); the compute is in the library. Outputs and workspaces are allocated on the stream that the
@@ -185,6 +185,88 @@ def linear_i8(a, a_scale, weight, out=None, dtype=torch.bfloat16, d_status=None,
     return out
 
 
+def _meet(given, ld, out, ldo):
+    """Whether two matrices of one shape and type share memory."""
+    n, columns = given.shape
+    size = given.element_size()
+    apart = (out.data_ptr() - given.data_ptr()) // size
+    if apart >= (n - 1) * ld + columns or -apart >= (n - 1) * ldo + columns:
+        return False
+    # rows of one buffer side by side
+    return not (n > 1 and ld == ldo and columns <= apart % ld <= ld - columns)
+
+
+def _like(out, given, ld, index):
+    """(tensor, elements between rows) of a result of the shape and type of `given`, whose rows are ld apart: a new one, or
+    one that is `given` or shares no memory with it."""
+    n, columns = given.shape
+    if out is None:
+        return torch.empty((n, columns), dtype=given.dtype, device=given.device), columns
+    rows, width, ldo, at = _rows("out", out, (given.dtype,))
+    if rows != n or width != columns or at != index:
+        _bad("out", "[%d, %d] on cuda:%d" % (n, columns, index), out)
+    if n and out.data_ptr() == given.data_ptr():
+        if ldo != ld:
+            _bad("out", "rows %d elements apart, as those of the tensor that it overwrites" % ld, out)
+    elif n and _meet(given, ld, out, ldo):
+        _bad("out", "the input itself or memory of its own", out)
+    return out, ldo
+
+
+class Adapters:
+    """Low-rank adapters of one projection, in stacks: a bfloat16 [L, R, K], b bfloat16 [L, N, R], scale float32 [L], all
+    contiguous on one device. Adapter i adds scale[i] * b[i] @ (a[i] @ y) to the projection of y. The tensors are used as
+    they are, so that a program may rewrite the adapter in a slot between calls; one of a lower rank is filled up with
+    zeros. Holds no workspace: calls on several streams may share it."""
+
+    def __init__(self, a, b, scale):
+        for name, t, what in (("a", a, "[L, R, K]"), ("b", b, "[L, N, R]")):
+            if t.dim() != 3 or t.dtype != _BF16 or not t.is_cuda or not t.is_contiguous() or not t.numel():
+                _bad(name, "a contiguous cuda bfloat16 tensor %s" % what, t)
+        self.L, self.R, self.K = a.shape
+        self.N = b.shape[1]
+        if b.shape[0] != self.L or b.shape[2] != self.R or b.get_device() != a.get_device():
+            _bad("b", "[%d, N, %d] on %s" % (self.L, self.R, a.device), b)
+        if scale is None:
+            raise ValueError("scale is needed")
+        _vec("scale", scale, self.L, _F32, a.get_device())
+        if self.L > _lib.DS_ADAPTERS_MAX or self.R > _lib.DS_ADAPTERS_MAX_RANK or max(self.N, self.K) > _INT_MAX:
+            raise ValueError("at most %d adapters of rank %d at most, got %d of rank %d" % (
+                _lib.DS_ADAPTERS_MAX, _lib.DS_ADAPTERS_MAX_RANK, self.L, self.R))
+        self.a, self.b, self.scale = a, b, scale
+
+
+def add_adapters(base, hidden, adapters, ids, gain=None, eps=1e-6, out=None, d_status=None, stream=None):
+    """Each row's low-rank adapter added to the logits of a projection that all rows share: base [n, N] (bfloat16 or
+    float32) + scale B (A y) with the Adapters entry ids[row] (int32 [n], any order, -1 for none), y the hidden states
+    [n, K] (bfloat16 or float32), RMS-normed with gain (float32 [K]) and eps when that is given. Computed in float32 and
+    rounded once to base's type. out: such a tensor (rows may lie apart), base itself to add in place; allocated when
+    None. An id beyond the stack gives a row of NaN and a bit in d_status."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return add_adapters(base, hidden, adapters, ids, gain, eps, out, d_status)
+    n, N, ldb, index = _rows("base", base, _CODE)
+    rows, K, ldx, at = _rows("hidden", hidden, _CODE)
+    if rows != n or K != adapters.K or at != index:
+        _bad("hidden", "[%d, %d] on cuda:%d" % (n, adapters.K, index), hidden)
+    if N != adapters.N or adapters.a.get_device() != index:
+        _bad("base", "[n, %d] on %s" % (adapters.N, adapters.a.device), base)
+    if ids is None:
+        raise ValueError("ids are needed")
+    ip = _vec("ids", ids, n, _I32, index)
+    gp = _vec("gain", gain, K, _F32, index)
+    st = _status(d_status, index)
+    out, ldo = _like(out, base, ldb, index)
+    lib = _lib.load()
+    need = lib.ds_add_adapters_workspace(n, adapters.L, adapters.R)
+    ws = torch.empty(need, dtype=_U8, device=base.device)
+    _check("ds_add_adapters", lib.ds_add_adapters(
+        base.data_ptr(), _CODE[base.dtype], n, N, ldb, hidden.data_ptr(), _CODE[hidden.dtype], K, ldx, gp, eps,
+        adapters.a.data_ptr(), adapters.b.data_ptr(), adapters.scale.data_ptr(), adapters.L, adapters.R, ip,
+        out.data_ptr(), ldo, ws.data_ptr(), need, st, _lib.raw_stream()))
+    return out
+
+
 class Int8Head:
     """A model's output head in 8 bits: the final RMS norm (when gain is given), the vocabulary projection and the
     sampler. w int8 [N, K] with scale float32 [N]; from_weight() quantises a bfloat16 or float32 weight."""
@@ -200,11 +282,25 @@ class Int8Head:
         q, scale = quantize_rows(w)
         return cls(q, scale, gain=gain, eps=eps)
 
-    def logits(self, hidden, out=None, dtype=torch.bfloat16, d_status=None, stream=None):
-        """Logits [n, N] of hidden states [n, K] (bfloat16 or float32): quantize_rows() and linear_i8() in one call."""
+    def logits(self, hidden, out=None, dtype=torch.bfloat16, d_status=None, stream=None, adapters=None, adapter_ids=None):
+        """Logits [n, N] of hidden states [n, K] (bfloat16 or float32): quantize_rows() and linear_i8() in one call. With
+        Adapters and an id per row (int32 [n], -1 for none) add_adapters() adds to them in place; bfloat16 logits are
+        then rounded twice, before the sum and after it (float32 ones in effect once)."""
         if stream is not None:
             with torch.cuda.stream(stream):
-                return self.logits(hidden, out, dtype, d_status)
+                return self.logits(hidden, out, dtype, d_status, None, adapters, adapter_ids)
+        if adapters is not None:
+            # checked before the projection runs: a refused call leaves out as it was
+            if adapter_ids is None:
+                raise ValueError("adapter_ids are needed")
+            n, K, _, index = _rows("hidden", hidden, _CODE)
+            _vec("adapter_ids", adapter_ids, n, _I32, index)
+            if adapters.N != self.weight.N or adapters.K != self.weight.K or adapters.a.get_device() != index:
+                _bad("adapters", "of a projection [%d, %d] on cuda:%d" % (self.weight.N, self.weight.K, index), adapters.b)
+            out = self.logits(hidden, out, dtype, d_status)
+            return add_adapters(out, hidden, adapters, adapter_ids, self.gain, self.eps, out, d_status)
+        if adapter_ids is not None:
+            raise ValueError("adapter_ids without adapters")
         if out is None and d_status is None and dtype in _CODE:
             w = self.weight
             r = _lib.calls().head(hidden, self.gain, w.packed, w.scale, w.N, w.K, _CODE[dtype], self.eps)
@@ -225,7 +321,16 @@ class Int8Head:
                                             ws.data_ptr(), need, st, _lib.raw_stream()))
         return out
 
-    def sample(self, hidden, temperature, u, top_k=None, top_p=None, min_p=None, d_status=None, stream=None):
+    def sample(self, hidden, temperature, u, top_k=None, top_p=None, min_p=None, d_status=None, stream=None, adapters=None,
+               adapter_ids=None):
         """Hidden states [n, K] to (tokens, logprobs): logits() then sample_filtered()."""
-        return sample_filtered(self.logits(hidden, d_status=d_status, stream=stream), temperature, u, top_k=top_k,
-                               top_p=top_p, min_p=min_p, d_status=d_status, stream=stream)
+        logits = self.logits(hidden, d_status=d_status, stream=stream, adapters=adapters, adapter_ids=adapter_ids)
+        return sample_filtered(logits, temperature, u, top_k=top_k, top_p=top_p, min_p=min_p, d_status=d_status,
+                               stream=stream)
+
+    def score(self, hidden, tokens, top=0, d_status=None, stream=None, adapters=None, adapter_ids=None):
+        """Hidden states [n, K] and a given token per row (int32 [n], -1 for none) to TokenScores: logits() then
+        score_tokens()."""
+        from .score import score_tokens
+        logits = self.logits(hidden, d_status=d_status, stream=stream, adapters=adapters, adapter_ids=adapter_ids)
+        return score_tokens(logits, tokens, top=top, d_status=d_status, stream=stream)
