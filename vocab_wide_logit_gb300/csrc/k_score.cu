@@ -1,132 +1,880 @@
 // k_score.cu -- log-probabilities of given tokens, with log-sum-exp, entropy, rank
 // and the most likely alternatives.
 //
-// Per row, with m = max x, e_j = exp(x_j - m) and s = sum e:
-//   lse = m + log s,  logprob = x_token - lse,  H = log s - (sum e_j (x_j - m)) / s,
+// Per row, with m = max x, e_j = exp(x_j - m), s = sum e_j and t = sum e_j (x_j - m):
+//   lse = m + log s,  logprob = x_token - lse,  H = log s - t / s,
 //   rank = how many come before the token by (x descending, id ascending),
-// and the first `top` of that order. One CTA per row, the row read once for m, once
-// for the sums and once for each alternative.
+// and the first `top` of that order, all from one read of the row.
+//
+// Sums: m is a running maximum, s and t are rescaled when it moves. Two bf16 logits
+// cost one packed maximum, one packed clamp (which keeps -inf out of the product in t:
+// at 256 below m an exponential is 0 already), two exponentials, four packed fp32
+// instructions and, for the rank, a packed comparison and a packed sum.
+//
+// Alternatives: a logit is among the first `top` only if its thread's own maximum
+// is: of the groups of threads (a warp's lanes, or 64 or more groups of a block)
+// the maxima are ranked, and the top-th of them bounds the top-th logit from below.
+// What reaches the bound, a few more than `top` for rows in any usual order, is
+// listed, from the registers or a second look at those threads' shares, and ranked by
+// counting who comes before whom. The bound is a pair (logit, chunk of 16 bytes), so
+// that ties (a masked row's -inf above all) list a few chunks and not the row. A list that
+// is long all the same is cut at its exact top-th entry, found bit by bit.
+#include <climits>
+#include <cooperative_groups.h>
+
 #include "ds_device.cuh"
 #include "ds_launch.h"
+
+namespace cg = cooperative_groups;
 
 namespace ds {
 
 namespace {
 
-constexpr int kThreads = 256;
+typedef unsigned long long u64;
+constexpr uint32_t kMinusInf2 = 0xff80ff80u;  // two bf16 of -inf
+constexpr uint32_t kMinusInf = 0xff800000u;
 
+// ---------------------------------------------------------------- packed bf16
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {  // a NaN stays
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t gt2(uint32_t a, uint32_t b) {  // 1 or 0, as bf16
+  uint32_t r;
+  asm("set.gt.bf16x2.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t ge2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("set.ge.bf16x2.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t add2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf2(float f) {  // f rounded, in both halves
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(r) : "f"(f));
+  return r;
+}
+
+// ---------------------------------------------------------------- a row's logits
 template <bool F32>
-__device__ __forceinline__ float load(const void* row, long long i) {
-  if constexpr (F32)
-    return static_cast<const float*>(row)[i];
-  else
-    return __uint_as_float((uint32_t) static_cast<const uint16_t*>(row)[i] << 16);
-}
-
-// The order (x descending, id ascending; -0 and +0 tie) as an integer.
-__device__ __forceinline__ unsigned long long order_of(float x, int id) {
-  return ((unsigned long long)order_key(x + 0.f) << 32) | (uint32_t)~id;
-}
-
-struct Sum {
-  __device__ float operator()(float p, float q) const { return p + q; }
-};
-struct Max {
-  template <typename T>
-  __device__ T operator()(T p, T q) const {
-    return p > q ? p : q;
+struct Row {
+  static constexpr int E = F32 ? 4 : 8;     // logits of a 16-byte chunk
+  static constexpr int kSize = F32 ? 4 : 2;
+  const char* at;    // the row
+  const char* base;  // its first chunk
+  int dc;            // logits of the first chunk that are before the row
+  int nq;            // chunks
+  __device__ __forceinline__ Row(const ScoreArgs& a, int row) {
+    at = static_cast<const char*>(a.x) + (long long)row * a.ld * kSize;
+    const uintptr_t p = reinterpret_cast<uintptr_t>(at);
+    base = reinterpret_cast<const char*>(p & ~(uintptr_t)15);
+    dc = (int)(p & 15) / kSize;
+    nq = (int)(((long long)dc + a.V + E - 1) / E);
+  }
+  __device__ __forceinline__ uint4 chunk(int q) const { return ld_stream16(base + 16LL * q); }
+  __device__ __forceinline__ float logit(int id) const {
+    if constexpr (F32)
+      return __ldg(reinterpret_cast<const float*>(at) + id);
+    else
+      return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t*>(at) + id) << 16);
   }
 };
 
-template <typename T, typename F>
-__device__ T cta_reduce(T v, F f) {
-  __shared__ T part[kThreads / 32];
-  __syncthreads();
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = part[0];
-  for (int i = 1; i < kThreads / 32; ++i) v = f(v, part[i]);
-  return v;
+template <bool F32>
+__device__ __forceinline__ float logit_of(const uint4& v, int i) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (F32)
+    return __uint_as_float(w[i]);
+  else
+    return (i & 1) ? bf_hi(w[i >> 1]) : bf_lo(w[i >> 1]);
 }
 
 template <bool F32>
-__global__ void __launch_bounds__(kThreads) k_score(const ScoreArgs a) {
+__device__ __forceinline__ uint4 nothing() {
+  const uint32_t w = F32 ? kMinusInf : kMinusInf2;
+  return make_uint4(w, w, w, w);
+}
+
+// The logits of a chunk that are not the row's become -inf.
+template <bool F32>
+__device__ __forceinline__ void mask_edges(uint4& v, int q, int dc, int V) {
+  constexpr int E = Row<F32>::E;
+  const long long id0 = (long long)q * E - dc;
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    if (id0 + i >= 0 && id0 + i < V) continue;
+    if constexpr (F32)
+      w[i] = kMinusInf;
+    else
+      w[i >> 1] = (i & 1) ? ((w[i >> 1] & 0x0000ffffu) | 0xff800000u) : ((w[i >> 1] & 0xffff0000u) | 0x0000ff80u);
+  }
+  v = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <bool F32>
+__device__ __forceinline__ float chunk_max(const uint4& v) {
+  if constexpr (F32) {
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+  } else {
+    const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+    return fmaxf(bf_lo(m), bf_hi(m));
+  }
+}
+
+template <bool F32, int U>
+__device__ __forceinline__ float chunks_max(const uint4 (&v)[U]) {
+  if constexpr (F32) {
+    float m = chunk_max<F32>(v[0]);
+#pragma unroll
+    for (int u = 1; u < U; ++u) m = fmaxf(m, chunk_max<F32>(v[u]));
+    return m;
+  } else {
+    uint32_t m = max2(max2(v[0].x, v[0].y), max2(v[0].z, v[0].w));
+#pragma unroll
+    for (int u = 1; u < U; ++u) m = max2(m, max2(max2(v[u].x, v[u].y), max2(v[u].z, v[u].w)));
+    return fmaxf(bf_lo(m), bf_hi(m));
+  }
+}
+
+// Adds exp(x - m) and exp(x - m) (x - m) of a chunk to s and t; m is finite and not
+// below any x. A NaN shows in s.
+template <bool F32>
+__device__ __forceinline__ void add_sums(const uint4& v, float m, uint32_t low2, float2& s, float2& t) {
+  const float2 nm = make_float2(-m, -m), l2e = make_float2(kLog2e, kLog2e);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (F32) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float2 d = __fadd2_rn(make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])), nm);
+      const float2 a = __fmul2_rn(d, l2e);
+      const float2 e = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+      s = __fadd2_rn(s, e);
+      d = make_float2(fmaxf(d.x, -256.f), fmaxf(d.y, -256.f));
+      t = __ffma2_rn(e, d, t);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t c = max2_nan(w[i], low2);
+      const float2 d = __fadd2_rn(make_float2(bf_lo(c), bf_hi(c)), nm);
+      const float2 a = __fmul2_rn(d, l2e);
+      const float2 e = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+      s = __fadd2_rn(s, e);
+      t = __ffma2_rn(e, d, t);
+    }
+  }
+}
+// The same where m is so low that nothing finite lies 256 below it.
+template <bool F32>
+__device__ __noinline__ void add_sums_low(uint4 v, float m, float2& s, float2& t) {
+  for (int i = 0; i < Row<F32>::E; ++i) {
+    const float d = logit_of<F32>(v, i) - m, e = ex2_approx(d * kLog2e);
+    s.x += e;
+    t.x += e > 0.f ? e * d : 0.f;
+  }
+}
+// What the clamp of bf16 logits may not fall below: more than 200 under m, whatever
+// the rounding to bf16 (2^-9 of it, an eighth of the distance for large m).
+__device__ __forceinline__ uint32_t low_of(float m) { return bf2(m - fmaxf(256.f, fabsf(m) * 0.015625f)); }
+__device__ __forceinline__ bool is_low(float m) { return m < -1e38f; }
+
+// How many logits of a chunk come before the token: those above x_token, and in
+// chunks in front of the token's those equal to it. (In the token's own chunk those
+// are counted apart, once a row.)
+template <bool F32>
+__device__ __forceinline__ int count_before(const uint4& v, bool front, float xt) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  int n = 0;
+  if constexpr (F32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n += front ? __uint_as_float(w[i]) >= xt : __uint_as_float(w[i]) > xt;
+  } else {
+    const uint32_t x2 = bf2(xt);
+    uint32_t c = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c = add2(c, front ? ge2(w[i], x2) : gt2(w[i], x2));
+    n = (int)(bf_lo(c) + bf_hi(c));
+  }
+  return n;
+}
+template <bool F32, int U, bool FRONT>
+__device__ __forceinline__ int count_all(const uint4 (&v)[U], float xt) {
+  int n = 0;
+  if constexpr (F32) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) n += count_before<F32>(v[u], FRONT, xt);
+  } else {
+    static_assert(U * 4 <= 128, "sums of ones in bf16 are exact up to 256");
+    const uint32_t x2 = bf2(xt);
+    uint32_t c = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c = add2(c, FRONT ? ge2(w[i], x2) : gt2(w[i], x2));
+    }
+    n = (int)(bf_lo(c) + bf_hi(c));
+  }
+  return n;
+}
+
+// The order (x descending, id or chunk ascending; -0 and +0 tie) as an integer. No
+// logit gives 0.
+__device__ __forceinline__ u64 order_of(float x, int id) {
+  return ((u64)order_key(x + 0.f) << 32) | (uint32_t)~id;
+}
+__device__ __forceinline__ int id_of(u64 key) { return (int)~(uint32_t)key; }
+__device__ __forceinline__ float logit_of_key(u64 key) {
+  const uint32_t k = (uint32_t)(key >> 32);
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+// ---------------------------------------------------------------- a row's results
+struct Sums {
+  float m, s, t;
+  int before;
+};
+
+struct Given {
+  int token;   // -1: none
+  float x;     // its logit; +inf without one (nothing counts as before)
+  int chunk;   // its chunk; 0 without one
+};
+template <bool F32>
+__device__ __forceinline__ Given given_token(const ScoreArgs& a, int row, const Row<F32>& x) {
+  const int tok = a.tokens[row];
+  Given g{-1, kInf, 0};
+  if (tok >= 0 && tok < a.V) {
+    g.token = tok;
+    g.x = x.logit(tok);
+    g.chunk = (int)(((long long)tok + x.dc) / Row<F32>::E);
+  }
+  return g;
+}
+// What `before` lacks or has too much: ties in front of the token in its own chunk;
+// the padding in front of the row, which ties with a token of -inf.
+template <bool F32>
+__device__ __forceinline__ int rank_mend(const Row<F32>& x, const Given& g) {
+  if (g.token < 0) return 0;
+  int n = g.x == -kInf && g.chunk > 0 ? -x.dc : 0;
+  const int first = max(0, (int)((long long)g.chunk * Row<F32>::E - x.dc));
+  for (int id = first; id < g.token; ++id) n += x.logit(id) == g.x;
+  return n;
+}
+
+// Writes the row's four numbers; returns lse, NaN when nothing may be listed.
+__device__ __forceinline__ float write_row(const ScoreArgs& a, int row, const Sums& r, const Given& g) {
+  const float nan = __int_as_float(0x7fffffff);
+  const bool bad = !(r.s < kInf) || r.m == kInf;  // a NaN or +inf among the logits
+  const bool none = bad || r.m == -kInf;
+  const float log_s = logf(r.s);
+  const float lse = bad ? nan : none ? -kInf : r.m + log_s;
+  a.out_logprobs[row] = none || g.token < 0 ? nan : (g.x - r.m) - log_s;
+  if (a.out_lse) a.out_lse[row] = lse;
+  if (a.out_entropy) a.out_entropy[row] = none ? nan : log_s - r.t / r.s;
+  if (a.out_ranks) a.out_ranks[row] = none || g.token < 0 ? -1 : r.before;
+  const uint32_t bits = (a.tokens[row] >= a.V ? DS_DEV_ERR_PARAM : 0u) | (bad ? DS_DEV_ERR_LOGITS : 0u);
+  if (bits) report(a.d_status, bits);
+  return none ? nan : lse;
+}
+// Alternative number r; key 0 for none.
+__device__ __forceinline__ void write_top(const ScoreArgs& a, int row, int r, u64 key, const Sums& sums, bool none) {
+  const long long at = (long long)row * a.top + r;
+  a.out_top_ids[at] = none ? -1 : id_of(key);
+  a.out_top_logprobs[at] = none ? __int_as_float(0x7fffffff) : (logit_of_key(key) - sums.m) - logf(sums.s);
+}
+__device__ __forceinline__ bool is_none(const Sums& r) { return !(r.s < kInf) || r.m == kInf || r.m == -kInf; }
+
+// ---------------------------------------------------------------- a warp per row
+// Rows of up to 32 C chunks, held in registers: 700 instructions for 1025 bf16
+// logits and 8 alternatives.
+constexpr int kWarps = 4;
+constexpr int kWarpList = 256;  // candidates a row may list: 32 lanes' chunks of 8
+constexpr int kWarpTop = 32;    // alternatives: a lane's maximum each
+constexpr int kLongList = 64;   // entries from which the exact cut is cheaper than ranking all
+
+// The top-th largest of n unique keys.
+__device__ __noinline__ u64 warp_cut(const u64* list, int n, int top) {
+  const int lane = threadIdx.x & 31;
+  u64 cut = 0;
+  for (int bit = 63; bit >= 0; --bit) {
+    const u64 trial = cut | (1ull << bit);
+    int c = 0;
+    for (int i = lane; i < n; i += 32) c += list[i] >= trial;
+    c = warp_sum_i(c);
+    if (c >= top) cut = trial;
+    if (c == top) break;
+  }
+  return cut;
+}
+
+// Which logits of a chunk are at or above f, a bit each.
+template <bool F32>
+__device__ __forceinline__ uint32_t reaching(const uint4& v, float f) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t bits = 0;
+  if constexpr (F32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bits |= (uint32_t)(__uint_as_float(w[i]) >= f) << i;
+  } else {
+    const uint32_t f2 = bf2(f);
+    uint32_t c = 0;  // a one is 0x3f80: its bit 7
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c |= (ge2(w[i], f2) & 0x00800080u) >> (7 - 2 * i);
+    bits = (c | (c >> 15)) & 0xffu;
+  }
+  return bits;
+}
+// Logit i of a chunk in registers.
+template <bool F32>
+__device__ __forceinline__ float pick(const uint4& v, int i) {
+  const int k = F32 ? i : i >> 1;
+  const uint32_t lo = (k & 1) ? v.y : v.x, hi = (k & 1) ? v.w : v.z, w = (k & 2) ? hi : lo;
+  if constexpr (F32)
+    return __uint_as_float(w);
+  else
+    return (i & 1) ? bf_hi(w) : bf_lo(w);
+}
+
+// The first `top` of a row, listed in no order, when its order puts the largest
+// into few lanes: the exact cut, then the list, from memory. Returns how many.
+template <bool F32>
+__device__ __noinline__ int warp_list_exact(const Row<F32> x, int V, int top, u64* list) {
+  const int lane = threadIdx.x & 31;
+  u64 cut = 0;
+  for (int bit = 63; bit >= 0; --bit) {
+    const u64 trial = cut | (1ull << bit);
+    int c = 0;
+    for (int id = lane; id < V; id += 32) c += order_of(x.logit(id), id) >= trial;
+    c = warp_sum_i(c);
+    if (c >= top) cut = trial;
+    if (c == top) break;
+  }
+  int listed = 0;
+  for (int id0 = 0; id0 < V; id0 += 32) {
+    const u64 o = id0 + lane < V ? order_of(x.logit(id0 + lane), id0 + lane) : 0;
+    const bool in = o != 0 && o >= cut;
+    const unsigned who = __ballot_sync(0xffffffffu, in);
+    const int pos = listed + __popc(who & ((1u << lane) - 1));
+    if (in && pos < kWarpList) list[pos] = o;
+    listed += __popc(who);
+  }
+  __syncwarp();
+  return min(listed, kWarpList);
+}
+
+template <bool F32, int C>
+__global__ void __launch_bounds__(kWarps * 32) k_score_warp(const ScoreArgs a) {
+  constexpr int E = Row<F32>::E;
+  __shared__ u64 lists[kWarps][kWarpList];
   pdl_release();
   pdl_wait();
-  const float nan = __int_as_float(0x7fffffff);
-  for (int row = blockIdx.x; row < a.n; row += gridDim.x) {
-    const char* x = static_cast<const char*>(a.x) + (long long)row * a.ld * (F32 ? 4 : 2);
-    const int token = a.tokens[row];
-    const bool given = token >= 0 && token < a.V;
-    const float at = given ? load<F32>(x, token) : 0.f;
-    float m = -kInf;
-    int bad = 0;
-    for (long long i = threadIdx.x; i < a.V; i += kThreads) {
-      const float v = load<F32>(x, i);
-      bad |= !(v < kInf);
-      m = fmaxf(m, v);
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const long long row_l = (long long)blockIdx.x * kWarps + wid;
+  if (row_l >= a.n) return;
+  const int row = (int)row_l;
+  const Row<F32> x(a, row);
+  uint4 v[C];
+#pragma unroll
+  for (int u = 0; u < C; ++u) {
+    const int q = lane + 32 * u;
+    v[u] = q < x.nq ? x.chunk(q) : nothing<F32>();
+  }
+  const Given g = given_token(a, row, x);
+  // the row's first and last chunk reach beyond it
+  if (lane == 0) mask_edges<F32>(v[0], 0, x.dc, a.V);
+#pragma unroll
+  for (int u = 0; u < C; ++u)
+    if (lane + 32 * u == x.nq - 1) mask_edges<F32>(v[u], lane + 32 * u, x.dc, a.V);
+
+  float best = -kInf;  // the lane's maximum and its first chunk
+  int at = lane;
+  Sums r{-kInf, 0.f, 0.f, 0};
+#pragma unroll
+  for (int u = 0; u < C; ++u) {
+    const float c = chunk_max<F32>(v[u]);
+    if (c > best) {
+      best = c;
+      at = lane + 32 * u;
     }
-    m = cta_reduce(m, Max());
-    bad = __syncthreads_or(bad);
-    float s = 0.f, t = 0.f;
-    int before = 0;
-    for (long long i = threadIdx.x; i < a.V; i += kThreads) {
-      const float v = load<F32>(x, i), d = v - m, e = __expf(d);
-      s += e;
-      t += e > 0.f ? e * d : 0.f;
-      before += v > at || (v == at && i < token);
-    }
-    s = cta_reduce(s, Sum());
-    t = cta_reduce(t, Sum());
-    const int rank = (int)cta_reduce((float)(before >> 12), Sum()) * 4096 + (int)cta_reduce((float)(before & 4095), Sum());
-    const bool none = bad || m == -kInf;
-    const float lse = bad ? nan : none ? -kInf : m + logf(s);
-    if (threadIdx.x == 0) {
-      a.out_logprobs[row] = none || !given ? nan : at - lse;
-      if (a.out_lse) a.out_lse[row] = lse;
-      if (a.out_entropy) a.out_entropy[row] = none ? nan : logf(s) - t / s;
-      if (a.out_ranks) a.out_ranks[row] = none || !given ? -1 : rank;
-      const uint32_t bits = (token >= a.V ? DS_DEV_ERR_PARAM : 0u) | (bad ? DS_DEV_ERR_LOGITS : 0u);
-      if (bits) report(a.d_status, bits);
-    }
-    unsigned long long last = ~0ull;
-    for (int j = 0; j < a.top; ++j) {
-      unsigned long long best = 0;
-      if (!none)
-        for (long long i = threadIdx.x; i < a.V; i += kThreads) {
-          const unsigned long long o = order_of(load<F32>(x, i), (int)i);
-          if (o < last && o > best) best = o;
-        }
-      best = cta_reduce(best, Max());
-      last = best;
-      if (threadIdx.x == 0) {
-        const int id = none ? -1 : (int)~(uint32_t)best;
-        a.out_top_ids[(long long)row * a.top + j] = id;
-        a.out_top_logprobs[(long long)row * a.top + j] = none ? nan : load<F32>(x, id) - lse;
+    const int q = lane + 32 * u;
+    if (q < x.nq) r.before += count_before<F32>(v[u], q < g.chunk, g.x);
+  }
+  r.m = warp_max_r(best);
+  float2 s = make_float2(0.f, 0.f), t = s;
+  if (is_low(r.m)) {
+    if (r.m != -kInf)
+#pragma unroll
+      for (int u = 0; u < C; ++u) add_sums_low<F32>(v[u], r.m, s, t);
+  } else {
+    const uint32_t low2 = low_of(r.m);
+#pragma unroll
+    for (int u = 0; u < C; ++u) add_sums<F32>(v[u], r.m, low2, s, t);
+  }
+  r.s = warp_sum(s.x + s.y);
+  r.t = warp_sum(t.x + t.y);
+  if (r.m == -kInf) {  // a row of NaN and -inf alone
+    float seen = 0.f;
+#pragma unroll
+    for (int u = 0; u < C; ++u)
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float f = logit_of<F32>(v[u], i);
+        if (f != f) seen = f;
       }
+    r.s = warp_sum(seen);
+  }
+  r.before = warp_sum_i(r.before);
+  if (lane == 0) {
+    r.before += rank_mend(x, g);
+    write_row(a, row, r, g);
+  }
+  if (a.top == 0) return;
+  const bool none = is_none(r);
+  if (none) {
+    for (int i = lane; i < a.top; i += 32) write_top(a, row, i, 0, r, true);
+    return;
+  }
+
+  // the bound: the top-th of the lanes' maxima, by (logit, chunk)
+  uint32_t key = lane < x.nq ? order_key(best + 0.f) : 0u, bound = 0;
+  int bound_at = INT_MAX;
+  if (x.nq >= a.top) {
+    int left = a.top;
+    uint32_t rest = key;
+    while (true) {
+      bound = __reduce_max_sync(0xffffffffu, rest);
+      const bool mine = rest == bound;
+      const int c = __popc(__ballot_sync(0xffffffffu, mine));
+      if (c >= left) {
+        // of those that tie, the left-th chunk
+        unsigned chunk = mine ? (unsigned)at : UINT_MAX;
+        for (; left > 0; --left) {
+          bound_at = (int)__reduce_min_sync(0xffffffffu, chunk);
+          if (chunk == (unsigned)bound_at) chunk = UINT_MAX;
+        }
+        break;
+      }
+      left -= c;
+      if (mine) rest = 0;
     }
   }
+  // list what reaches it
+  u64* list = lists[wid];
+  int listed = 0;
+  const bool all = x.nq < a.top;
+  const u64 cut = all ? 0 : ((u64)bound << 32) | (uint32_t)~bound_at;
+  const float bound_x = all ? -kInf : logit_of_key(cut);
+  const bool any = lane < x.nq && (((u64)key << 32) | (uint32_t)~at) >= cut;
+#pragma unroll
+  for (int u = 0; u < C; ++u) {
+    const int q = lane + 32 * u;
+    const bool here = any && q < x.nq && chunk_max<F32>(v[u]) >= bound_x;
+    if (!__any_sync(0xffffffffu, here)) continue;
+    uint32_t reach = here ? reaching<F32>(v[u], bound_x) : 0;
+    while (__any_sync(0xffffffffu, reach != 0)) {
+      const int i = reach ? __ffs(reach) - 1 : 0, id = q * E - x.dc + i;
+      const uint32_t k = order_key(pick<F32>(v[u], i) + 0.f);
+      const bool in = reach && id >= 0 && id < a.V && (((u64)k << 32) | (uint32_t)~q) >= cut;
+      const unsigned who = __ballot_sync(0xffffffffu, in);
+      const int pos = listed + __popc(who & ((1u << lane) - 1));
+      if (in && pos < kWarpList) list[pos] = ((u64)k << 32) | (uint32_t)~id;
+      listed += __popc(who);
+      reach &= reach - 1;
+    }
+  }
+  __syncwarp();
+  u64 last = 0;
+  if (listed > kWarpList)
+    listed = warp_list_exact<F32>(x, a.V, a.top, list);
+  else if (listed > kLongList)
+    last = warp_cut(list, listed, a.top);
+  for (int i = lane; i < listed; i += 32) {
+    const u64 mine = list[i];
+    if (mine < last) continue;
+    int before = 0;
+    for (int j = 0; j < listed; ++j) before += list[j] > mine;
+    if (before < a.top) write_top(a, row, before, mine, r, false);
+  }
+}
+
+// ---------------------------------------------------------------- blocks per row
+// A row over a cluster of CTAs, each with a slice of it; one of them joins.
+constexpr int kMaxCluster = 16;
+// Candidates a slice may list: `top` chunks of 8 logits for each thread of a group.
+__host__ __device__ constexpr int list_size(int threads) { return threads >= 512 ? 2048 : 1024; }
+constexpr int kLong = 160;     // entries from which the exact cut is cheaper than ranking all
+constexpr int kUnroll = 4;     // chunks a thread has in flight, twice
+
+template <int NT>
+struct Shared {
+  u64 list[list_size(NT)];  // candidates; in the joining CTA then the survivors of all slices
+  u64 sorted[(NT >= 512 ? kMaxCluster : 1) * DS_SCORE_MAX_TOP];  // each slice's alternatives in order
+  u64 keys[256];                      // groups' maxima
+  Sums warps[NT / 32];
+  Sums slices[kMaxCluster];
+  Sums total;
+  u64 bound;
+  int count;
+  int bits[64];
+};
+
+__device__ __forceinline__ Sums join(const Sums& p, const Sums& q) {
+  Sums r;
+  r.m = fmaxf(p.m, q.m);
+  r.before = p.before + q.before;
+  // an empty side has s = t = 0 and m = -inf: no product with that difference
+  const float dp = p.m == -kInf ? 0.f : p.m - r.m, dq = q.m == -kInf ? 0.f : q.m - r.m;
+  const float fp = ex2_approx(dp * kLog2e), fq = ex2_approx(dq * kLog2e);
+  r.s = p.s * fp + q.s * fq;
+  // far below the other's maximum a part counts nothing, whatever the distance
+  r.t = (fp > 0.f ? (p.t + p.s * dp) * fp : 0.f) + (fq > 0.f ? (q.t + q.s * dq) * fq : 0.f);
+  return r;
+}
+__device__ __forceinline__ Sums warp_join(Sums p, int lanes) {
+  for (int o = lanes >> 1; o > 0; o >>= 1) {
+    Sums q;
+    q.m = __shfl_xor_sync(0xffffffffu, p.m, o);
+    q.s = __shfl_xor_sync(0xffffffffu, p.s, o);
+    q.t = __shfl_xor_sync(0xffffffffu, p.t, o);
+    q.before = __shfl_xor_sync(0xffffffffu, p.before, o);
+    p = join(p, q);
+  }
+  return p;
+}
+
+// The top-th largest of what count(trial) counts at or above trial, for a block; bits
+// are 64 zeros and stay used.
+template <typename F>
+__device__ __forceinline__ u64 block_cut(int* bits, int top, F count) {
+  u64 cut = 0;
+  for (int bit = 63; bit >= 0; --bit) {
+    const u64 trial = cut | (1ull << bit);
+    const int c = warp_sum_i(count(trial));
+    if ((threadIdx.x & 31) == 0 && c) atomicAdd(&bits[bit], c);
+    __syncthreads();
+    const int all = bits[bit];
+    if (all >= top) cut = trial;
+    if (all == top) break;
+  }
+  return cut;
+}
+
+template <bool F32, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a) {
+  constexpr int E = Row<F32>::E, U = kUnroll, kList = list_size(NT);
+  __shared__ Shared<NT> sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int cs = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  if (cs > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  pdl_release();
+  pdl_wait();
+  const int row = (int)(blockIdx.x / (unsigned)cs);
+  const Row<F32> x(a, row);
+  const int q_lo = (int)((long long)rank * x.nq / cs), q_hi = (int)((long long)(rank + 1) * x.nq / cs);
+
+  auto load = [&](uint4 (&v)[U], int q) {
+    if (q + (U - 1) * NT < q_hi) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = x.chunk(q + u * NT);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = q + u * NT < q_hi ? x.chunk(q + u * NT) : nothing<F32>();
+    }
+    // the row's first and last chunk reach beyond it
+    if (q == 0) mask_edges<F32>(v[0], 0, x.dc, a.V);
+    if (q + (U - 1) * NT >= x.nq - 1) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (q + u * NT == x.nq - 1) mask_edges<F32>(v[u], q + u * NT, x.dc, a.V);
+    }
+  };
+
+  uint4 v[U];
+  int q = q_lo + tid;
+  load(v, q);
+  if (tid < 64) sh.bits[tid] = 0;
+  if (tid == 0) sh.count = 0;
+  const Given g = given_token(a, row, x);
+  float m = -kInf, seen = 0.f;
+  uint32_t low2 = 0;
+  int at = q, before = 0;
+  float2 s = make_float2(0.f, 0.f), t = s;
+  while (q < q_hi) {
+    uint4 next[U];
+    const int qn = q + U * NT;
+    if (qn < q_hi) load(next, qn);
+    // the running maximum and the first chunk that has it
+    const float c = chunks_max<F32, U>(v);
+    if (c > m) {
+#pragma unroll
+      for (int u = U - 1; u >= 0; --u)
+        if (chunk_max<F32>(v[u]) == c) at = q + u * NT;
+      const float d = m - c, f = ex2_approx(d * kLog2e);
+      // nothing yet, or nothing that counts beside c: no product with an infinite distance
+      t = f > 0.f ? make_float2((t.x + s.x * d) * f, (t.y + s.y * d) * f) : make_float2(0.f, 0.f);
+      s = make_float2(s.x * f, s.y * f);
+      m = c;
+      low2 = low_of(m);
+    }
+    if (qn - NT < g.chunk && qn - NT < q_hi) {
+      before += count_all<F32, U, true>(v, g.x);
+    } else if (q > g.chunk) {
+      before += count_all<F32, U, false>(v, g.x);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (q + u * NT < q_hi) before += count_before<F32>(v[u], q + u * NT < g.chunk, g.x);
+    }
+    if (!is_low(m)) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) add_sums<F32>(v[u], m, low2, s, t);
+    } else if (m != -kInf) {
+      for (int u = 0; u < U; ++u) add_sums_low<F32>(v[u], m, s, t);
+    } else {  // -inf and NaN alone
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const float f = logit_of<F32>(v[u], i);
+          if (f != f) seen = f;
+        }
+    }
+    q = qn;
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = next[u];
+  }
+
+  // join the block's sums
+  {
+    Sums p{m, s.x + s.y + seen, t.x + t.y, before};
+    p = warp_join(p, 32);
+    if (lane == 0) sh.warps[wid] = p;
+  }
+  const int top = a.top;
+  const u64 own = q_lo + tid < q_hi ? ((u64)order_key(m + 0.f) << 32) | (uint32_t)~at : 0;
+  const int width = top <= 32 && NT > 64 ? NT / 64 : NT > 256 ? NT / 256 : 1;  // threads of a group
+  if (top > 0) {
+    u64 k = own;
+    for (int o = width >> 1; o > 0; o >>= 1) {
+      const u64 other = __shfl_xor_sync(0xffffffffu, k, o);
+      k = k > other ? k : other;
+    }
+    if ((tid & (width - 1)) == 0) sh.keys[tid / width] = k;
+  }
+  __syncthreads();
+  if (wid == NT / 32 - 1) {
+    Sums p = lane < NT / 32 ? sh.warps[lane] : Sums{-kInf, 0.f, 0.f, 0};
+    p = warp_join(p, 32);
+    if (lane == 0) sh.total = p;
+  }
+  if (top > 0) {
+    const int groups = NT / width;
+    if (tid < groups) {
+      // the top-th of the groups' maxima bounds the slice's top-th logit from below
+      const u64 k = sh.keys[tid];
+      int above = 0;
+      for (int j = 0; j < groups; ++j) above += sh.keys[j] > k || (sh.keys[j] == k && j < tid);
+      if (above == top - 1) sh.bound = k;
+    }
+    __syncthreads();
+    const u64 bound = sh.bound;
+    auto scan = [&](auto f) {  // the logits of this thread's share, when it has any that reach the bound
+      if (own == 0 || own < bound) return;
+      for (int p = q_lo + tid; p < q_hi; p += NT) {
+        const uint4 w = x.chunk(p);
+        if (((u64)order_key(chunk_max<F32>(w) + 0.f) << 32 | 0xffffffffu) < bound && p != 0 && p != x.nq - 1) continue;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const long long id = (long long)p * E - x.dc + i;
+          if (id < 0 || id >= a.V) continue;
+          const float l = logit_of<F32>(w, i);
+          if ((((u64)order_key(l + 0.f) << 32) | (uint32_t)~p) >= bound) f(order_of(l, (int)id));
+        }
+      }
+    };
+    auto put = [&](u64 key) {
+      const int pos = atomicAdd(&sh.count, 1);
+      if (pos < kList) sh.list[pos] = key;
+    };
+    scan(put);
+    __syncthreads();
+    u64 cut = 0;
+    int listed = sh.count;
+    if (listed > kList) {
+      // the largest logits met in few threads: the exact cut, then the list again
+      cut = block_cut(sh.bits, top, [&](u64 trial) {
+        int c = 0;
+        scan([&](u64 key) { c += key >= trial; });
+        return c;
+      });
+      __syncthreads();
+      if (tid == 0) sh.count = 0;
+      __syncthreads();
+      scan([&](u64 key) {
+        if (key >= cut) put(key);
+      });
+      __syncthreads();
+      listed = min(sh.count, kList);
+    } else if (listed > kLong) {
+      cut = block_cut(sh.bits, top, [&](u64 trial) {
+        int c = 0;
+        for (int i = tid; i < listed; i += NT) c += sh.list[i] >= trial;
+        return c;
+      });
+    }
+    // in order to the joining CTA, zeros behind the last
+    if (cs > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    u64* sorted = cs > 1 ? cluster.map_shared_rank(sh.sorted, 0) + rank * top : sh.sorted;
+    for (int i = tid; i < listed; i += NT) {
+      const u64 mine = sh.list[i];
+      if (mine < cut) continue;
+      int above = 0;
+      for (int j = 0; j < listed; ++j) above += sh.list[j] > mine;
+      if (above < top) sorted[above] = mine;
+    }
+    for (int i = listed + tid; i < top; i += NT) sorted[i] = 0;
+  } else {
+    __syncthreads();
+    if (cs > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  }
+  if (cs == 1) {
+    __syncthreads();
+    Sums r = sh.total;
+    if (tid == 0) {
+      r.before += rank_mend(x, g);
+      write_row(a, row, r, g);
+    }
+    const bool none = is_none(r);
+    for (int i = tid; i < top; i += NT) write_top(a, row, i, sh.sorted[i], r, none);
+    return;
+  }
+  if (tid == 0) *cluster.map_shared_rank(&sh.slices[rank], 0) = sh.total;
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (rank != 0) return;  // what it wrote is the joining CTA's, which is still there
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+
+  // every warp joins the slices' sums for itself
+  Sums r = lane < cs ? sh.slices[lane] : Sums{-kInf, 0.f, 0.f, 0};
+  r = warp_join(r, 32);
+  if (tid == 0) {
+    Sums w = r;
+    w.before += rank_mend(x, g);
+    write_row(a, row, w, g);
+  }
+  if (top == 0) return;
+  const bool none = is_none(r);
+  if (none) {
+    for (int i = tid; i < top; i += NT) write_top(a, row, i, 0, r, true);
+    return;
+  }
+  // bounds of the row's top-th: the largest of the slices' top-th entries, and, with
+  // c slices that have d entries at or above a key, c d >= top, that key
+  u64 bound;
+  {
+    const int d = (top + (cs >> 1) - 1) / (cs >> 1), c = (top + d - 1) / d;
+    const u64 kd = lane < cs ? sh.sorted[lane * top + d - 1] : 0, kt = lane < cs ? sh.sorted[lane * top + top - 1] : 0;
+    int above = 0;
+    u64 most = 0;
+    for (int j = 0; j < cs; ++j) {
+      const u64 other = __shfl_sync(0xffffffffu, kd, j), last = __shfl_sync(0xffffffffu, kt, j);
+      above += other > kd || (other == kd && j < lane);
+      most = most > last ? most : last;
+    }
+    const unsigned who = __ballot_sync(0xffffffffu, lane < cs && above == c - 1);
+    const u64 second = __shfl_sync(0xffffffffu, kd, __ffs(who) - 1);
+    bound = most > second ? most : second;
+  }
+  if (tid == 0) sh.count = 0;
+  if (tid < 64) sh.bits[tid] = 0;
+  __syncthreads();
+  for (int i = tid; i < cs * top; i += NT) {
+    const u64 key = sh.sorted[i];
+    if (key == 0 || key < bound) continue;
+    sh.list[atomicAdd(&sh.count, 1)] = key;  // at most cs top = kList
+  }
+  __syncthreads();
+  const int listed = sh.count;
+  u64 cut = 0;
+  if (listed > kLong)
+    cut = block_cut(sh.bits, top, [&](u64 trial) {
+      int c = 0;
+      for (int i = tid; i < listed; i += NT) c += sh.list[i] >= trial;
+      return c;
+    });
+  for (int i = tid; i < listed; i += NT) {
+    const u64 mine = sh.list[i];
+    if (mine < cut) continue;
+    int above = 0;
+    for (int j = 0; j < listed; ++j) above += sh.list[j] > mine;
+    if (above < top) write_top(a, row, above, mine, r, false);
+  }
+}
+static_assert(kMaxCluster * DS_SCORE_MAX_TOP <= list_size(512), "the survivors of all slices fit the list");
+
+template <typename K>
+cudaError_t launch(K kern, const ScoreArgs& a, long long blocks, int threads, int cs, cudaStream_t st) {
+  if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks, 1, 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cs;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cs > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  return cudaGetLastError();
+}
+
+template <bool F32>
+cudaError_t launch_rows(const ScoreArgs& a, cudaStream_t st) {
+  const int E = F32 ? 4 : 8;
+  const long long nq = ((long long)a.V + 2 * E - 2) / E;  // the most chunks a row has
+  if (a.top <= kWarpTop && nq <= 32 * 16) {
+    const long long blocks = ((long long)a.n + kWarps - 1) / kWarps;
+    const int c = (int)((nq + 31) / 32);
+    if (c <= 1) return launch(k_score_warp<F32, 1>, a, blocks, kWarps * 32, 1, st);
+    if (c <= 2) return launch(k_score_warp<F32, 2>, a, blocks, kWarps * 32, 1, st);
+    if (c <= 3) return launch(k_score_warp<F32, 3>, a, blocks, kWarps * 32, 1, st);
+    if (c <= 5) return launch(k_score_warp<F32, 5>, a, blocks, kWarps * 32, 1, st);
+    if (c <= 9) return launch(k_score_warp<F32, 9>, a, blocks, kWarps * 32, 1, st);
+    return launch(k_score_warp<F32, 16>, a, blocks, kWarps * 32, 1, st);
+  }
+  const int sms = device_sms();
+  if (sms <= 0) return cudaErrorUnknown;
+  if (nq <= 2048) return launch(k_score_block<F32, 128>, a, a.n, 128, 1, st);
+  // slices of at least 2048 chunks, more CTAs than SMs when the rows allow
+  int cs = 1;
+  while (cs < 8 && nq / (2 * cs) >= 2048 && (long long)a.n * cs < 4LL * sms) cs *= 2;
+  return launch(k_score_block<F32, 512>, a, (long long)a.n * cs, 512, cs, st);
 }
 
 }  // namespace
 
 cudaError_t launch_score(const ScoreArgs& a, bool f32, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.n, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e =
-      f32 ? cudaLaunchKernelEx(&cfg, k_score<true>, a) : cudaLaunchKernelEx(&cfg, k_score<false>, a);
-  if (e != cudaSuccess) return e;
-  note_launch();
-  return cudaGetLastError();
+  return f32 ? launch_rows<true>(a, st) : launch_rows<false>(a, st);
 }
 
 }  // namespace ds
