@@ -309,8 +309,13 @@ constexpr int kLongList = 64;   // entries from which the exact cut is cheaper t
 // The top-th largest of n unique keys.
 __device__ __noinline__ u64 warp_cut(const u64* list, int n, int top) {
   const int lane = threadIdx.x & 31;
-  u64 cut = 0;
-  for (int bit = 63; bit >= 0; --bit) {
+  const u64 any = list[0];
+  u64 d = 1;
+  for (int i = lane; i < n; i += 32) d |= list[i] ^ any;
+  d = ((u64)__reduce_or_sync(0xffffffffu, (uint32_t)(d >> 32)) << 32) | __reduce_or_sync(0xffffffffu, (uint32_t)d);
+  const int from = 63 - __clzll((long long)d);  // above it all of them agree
+  u64 cut = from == 63 ? 0 : any >> (from + 1) << (from + 1);
+  for (int bit = from; bit >= 0; --bit) {
     const u64 trial = cut | (1ull << bit);
     int c = 0;
     for (int i = lane; i < n; i += 32) c += list[i] >= trial;
@@ -527,7 +532,7 @@ struct Shared {
   Sums warps[NT / 32];
   Sums slices[kMaxCluster];
   Sums total;
-  u64 bound;
+  u64 bound, differ;
   int count;
   int bits[64];
 };
@@ -557,11 +562,11 @@ __device__ __forceinline__ Sums warp_join(Sums p, int lanes) {
 }
 
 // The top-th largest of what count(trial) counts at or above trial, for a block; bits
-// are 64 zeros and stay used.
+// are 64 zeros and stay used. All of them agree with `any` above bit `from`.
 template <typename F>
-__device__ __forceinline__ u64 block_cut(int* bits, int top, F count) {
-  u64 cut = 0;
-  for (int bit = 63; bit >= 0; --bit) {
+__device__ __forceinline__ u64 block_cut(int* bits, int top, u64 any, int from, F count) {
+  u64 cut = from == 63 ? 0 : any >> (from + 1) << (from + 1);
+  for (int bit = from; bit >= 0; --bit) {
     const u64 trial = cut | (1ull << bit);
     const int c = warp_sum_i(count(trial));
     if ((threadIdx.x & 31) == 0 && c) atomicAdd(&bits[bit], c);
@@ -571,6 +576,21 @@ __device__ __forceinline__ u64 block_cut(int* bits, int top, F count) {
     if (all == top) break;
   }
   return cut;
+}
+// The same for n listed keys; *differ is 0 and stays used.
+template <int NT>
+__device__ __forceinline__ u64 list_cut(const u64* list, int n, int* bits, u64* differ, int top) {
+  const u64 any = list[0];
+  u64 d = 0;
+  for (int i = threadIdx.x; i < n; i += NT) d |= list[i] ^ any;
+  const uint32_t hi = __reduce_or_sync(0xffffffffu, (uint32_t)(d >> 32)), lo = __reduce_or_sync(0xffffffffu, (uint32_t)d);
+  if ((threadIdx.x & 31) == 0) atomicOr(differ, ((u64)hi << 32) | lo);
+  __syncthreads();
+  return block_cut(bits, top, any, 63 - __clzll((long long)(*differ | 1)), [&](u64 trial) {
+    int c = 0;
+    for (int i = threadIdx.x; i < n; i += NT) c += list[i] >= trial;
+    return c;
+  });
 }
 
 template <bool F32, int NT>
@@ -608,11 +628,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
   int q = q_lo + tid;
   load(v, q);
   if (tid < 64) sh.bits[tid] = 0;
-  if (tid == 0) sh.count = 0;
+  if (tid == 0) sh.count = 0, sh.differ = 0;
   const Given g = given_token(a, row, x);
-  float m = -kInf, seen = 0.f;
+  float m = -kInf, second = -kInf, seen = 0.f;  // second: the largest of the other batches
   uint32_t low2 = 0;
-  int at = q, before = 0;
+  int at = q, at_batch = q, before = 0;
   float2 s = make_float2(0.f, 0.f), t = s;
   while (q < q_hi) {
     uint4 next[U];
@@ -620,7 +640,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
     if (qn < q_hi) load(next, qn);
     // the running maximum and the first chunk that has it
     const float c = chunks_max<F32, U>(v);
+    second = fmaxf(second, fminf(c, m));
     if (c > m) {
+      at_batch = q;
 #pragma unroll
       for (int u = U - 1; u >= 0; --u)
         if (chunk_max<F32>(v[u]) == c) at = q + u * NT;
@@ -693,18 +715,27 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
     }
     __syncthreads();
     const u64 bound = sh.bound;
-    auto scan = [&](auto f) {  // the logits of this thread's share, when it has any that reach the bound
+    // The logits of this thread's share that reach the bound: in its best batch, and in
+    // the others when one of them has any.
+    auto scan = [&](auto f) {
       if (own == 0 || own < bound) return;
-      for (int p = q_lo + tid; p < q_hi; p += NT) {
-        const uint4 w = x.chunk(p);
-        if (((u64)order_key(chunk_max<F32>(w) + 0.f) << 32 | 0xffffffffu) < bound && p != 0 && p != x.nq - 1) continue;
+      const bool one = (((u64)order_key(second + 0.f) << 32) | 0xffffffffu) < bound;
+      for (int p = one ? at_batch : q_lo + tid; p < q_hi; p += U * NT) {
+        uint4 w[U];
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const long long id = (long long)p * E - x.dc + i;
-          if (id < 0 || id >= a.V) continue;
-          const float l = logit_of<F32>(w, i);
-          if ((((u64)order_key(l + 0.f) << 32) | (uint32_t)~p) >= bound) f(order_of(l, (int)id));
+        for (int u = 0; u < U; ++u) w[u] = p + u * NT < q_hi ? x.chunk(p + u * NT) : nothing<F32>();
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if ((((u64)order_key(chunk_max<F32>(w[u]) + 0.f) << 32) | 0xffffffffu) < bound) continue;
+          const int q1 = p + u * NT;
+          if (q1 >= q_hi) break;
+          for (int i = 0; i < E; ++i) {
+            const long long id = (long long)q1 * E - x.dc + i;
+            const float l = pick<F32>(w[u], i);
+            if (id >= 0 && id < a.V && (((u64)order_key(l + 0.f) << 32) | (uint32_t)~q1) >= bound) f(order_of(l, (int)id));
+          }
         }
+        if (one) break;
       }
     };
     auto put = [&](u64 key) {
@@ -717,7 +748,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
     int listed = sh.count;
     if (listed > kList) {
       // the largest logits met in few threads: the exact cut, then the list again
-      cut = block_cut(sh.bits, top, [&](u64 trial) {
+      cut = block_cut(sh.bits, top, 0, 63, [&](u64 trial) {
         int c = 0;
         scan([&](u64 key) { c += key >= trial; });
         return c;
@@ -731,11 +762,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
       __syncthreads();
       listed = min(sh.count, kList);
     } else if (listed > kLong) {
-      cut = block_cut(sh.bits, top, [&](u64 trial) {
-        int c = 0;
-        for (int i = tid; i < listed; i += NT) c += sh.list[i] >= trial;
-        return c;
-      });
+      cut = list_cut<NT>(sh.list, listed, sh.bits, &sh.differ, top);
     }
     // in order to the joining CTA, zeros behind the last
     if (cs > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
@@ -799,7 +826,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
     const u64 second = __shfl_sync(0xffffffffu, kd, __ffs(who) - 1);
     bound = most > second ? most : second;
   }
-  if (tid == 0) sh.count = 0;
+  if (tid == 0) sh.count = 0, sh.differ = 0;
   if (tid < 64) sh.bits[tid] = 0;
   __syncthreads();
   for (int i = tid; i < cs * top; i += NT) {
@@ -811,11 +838,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
   const int listed = sh.count;
   u64 cut = 0;
   if (listed > kLong)
-    cut = block_cut(sh.bits, top, [&](u64 trial) {
-      int c = 0;
-      for (int i = tid; i < listed; i += NT) c += sh.list[i] >= trial;
-      return c;
-    });
+    cut = list_cut<NT>(sh.list, listed, sh.bits, &sh.differ, top);
   for (int i = tid; i < listed; i += NT) {
     const u64 mine = sh.list[i];
     if (mine < cut) continue;
@@ -865,9 +888,10 @@ cudaError_t launch_rows(const ScoreArgs& a, cudaStream_t st) {
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorUnknown;
   if (nq <= 2048) return launch(k_score_block<F32, 128>, a, a.n, 128, 1, st);
-  // slices of at least 2048 chunks, more CTAs than SMs when the rows allow
+  if (nq <= 4096) return launch(k_score_block<F32, 256>, a, a.n, 256, 1, st);
+  // slices of at least 4.5 chunks a thread while all CTAs run at once
   int cs = 1;
-  while (cs < 8 && nq / (2 * cs) >= 2048 && (long long)a.n * cs < 4LL * sms) cs *= 2;
+  while (cs < 8 && nq / (2 * cs) >= 2304 && 2LL * a.n * cs <= 2LL * sms) cs *= 2;
   return launch(k_score_block<F32, 512>, a, (long long)a.n * cs, 512, cs, st);
 }
 
