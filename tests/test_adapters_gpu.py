@@ -34,7 +34,8 @@ def _reference(base, hidden, ad, ids, gain, eps=EPS):
     """(what is right, how far off it may be) in float64.
 
     t = A y: K products and their sum, K + 8 roundings of at most 2^-24 of the sum of sizes; the norm's root adds (K / 32 +
-    16) / 2 of them and its products 3. B t: t in parts of 2^-24, then R products, at most (3 R / 16 + 4) additions that
+    16) / 2 of them and its products 3. For bf16 logits y and t lose 2^-18 each as sums of two bf16 parts (three lose 2^-27).
+    B t: then R products, at most (3 R / 16 + 4) additions that
     each lose 2^-23 of the running size where a matrix instruction makes them and R of 2^-24 where not. The sum with base
     rounds once, and to bf16 once more (half a step, 2^-8)."""
     y = hidden.double()
@@ -54,7 +55,7 @@ def _reference(base, hidden, ad, ids, gain, eps=EPS):
             size[mine] = (y[mine].abs() @ a.abs().t() * s.abs()) @ b.abs().t()
     tol = size * (down + 4 + 2 * (ad.R + 4)) * 2.0 ** -24 + out.abs() * 2.0 ** -23
     if base.dtype == torch.bfloat16:
-        tol = tol + out.abs() * 2.0 ** -8 * (1 + 2.0 ** -10)
+        tol = tol + size * 2.0 ** -17 + out.abs() * 2.0 ** -8 * (1 + 2.0 ** -10)
     return out, tol
 
 
