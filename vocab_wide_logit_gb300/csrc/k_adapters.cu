@@ -266,6 +266,7 @@ __global__ void __launch_bounds__(kDownThreads) k_adapters_down(const AdapterArg
   float ss0 = 0.f, ss1 = 0.f, odd0 = 0.f, odd1 = 0.f;
   // 32 inputs a step: lane q of a row's four takes 8 that lie together, four of them
   // for each of two instructions
+#pragma unroll 2
   for (int k0 = wid * 32; k0 < g.K; k0 += kDownWarps * 32) {
     const int k = k0 + 8 * q;
     float f0[8], f1[8];
@@ -416,10 +417,10 @@ __device__ __forceinline__ void st16(void* p, uint4 v) {
 }
 
 // RP: padded ranks. VEC: weights in one load a lane and step. NEAR: base and result
-// rows lie the same way to 16 bytes.
-template <bool F32, int RP, bool VEC, bool NEAR>
+// rows lie the same way to 16 bytes. SHIFT: some row starts between two chunks.
+template <bool F32, int RP, bool VEC, bool NEAR, bool SHIFT>
 __global__ void __launch_bounds__(kUpWarps * 32, RP <= 64 ? 2 : 1)
-    k_adapters_up(const AdapterArgs g, const Tile* tiles, const uint8_t* t_in, int any_shift) {
+    k_adapters_up(const AdapterArgs g, const Tile* tiles, const uint8_t* t_in) {
   using U = Up<F32>;
   constexpr int E = U::E, kSize = F32 ? 4 : 2, PARTS = F32 ? 3 : 2, STEPS = RP / 16;
   constexpr int kLoad = RP == 16 ? 4 : 8;  // weights of a lane and load: one instruction's, or two's
@@ -431,24 +432,27 @@ __global__ void __launch_bounds__(kUpWarps * 32, RP <= 64 ? 2 : 1)
   const int count = tile.count, a = tile.adapter;
   const long long block = (long long)blockIdx.x * kUpWarps + wid;  // of 16 chunks
   const long long c0 = block * U::kChannels;
-  if (count <= 0 || c0 >= (long long)g.N + E - 1) return;
+  if (count <= 0 || c0 >= (long long)g.N + (SHIFT ? E - 1 : 0)) return;
   if (a == kNone && g.out == g.base) return;
   float* mine = results + wid * kRows * U::kPitch;
   const int my_row = lane < count ? tile.rows[lane] : 0;
   char* out = static_cast<char*>(g.out);
   const char* base = static_cast<const char*>(g.base);
+  // how many logits of a row's first chunk are before it
+  auto shift_of = [&](long long row) {
+    return SHIFT ? (int)(reinterpret_cast<uintptr_t>(out + row * g.ldo * kSize) & 15) / kSize : 0;
+  };
 
   // lane l, turn i: chunk l % 16 of the tile's row 2 i + l / 16
   uint4 v[8];
   if (a != kBad) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+      if (2 * i >= count) break;
       const int r = 2 * i + (lane >> 4);
       const long long row = __shfl_sync(0xffffffffu, my_row, r);
-      if (r >= count) continue;
-      const int dc = (int)(reinterpret_cast<uintptr_t>(out + row * g.ldo * kSize) & 15) / kSize;
-      const long long id = c0 + (lane & 15) * E - dc;
-      if (id >= g.N) continue;
+      const long long id = c0 + (lane & 15) * E - shift_of(row);
+      if (r >= count || id >= g.N) continue;
       const char* p = base + (row * g.ldb + id) * kSize;
       if constexpr (NEAR) {
         v[i] = ld16(p);  // its edges may be other rows' bytes, of the same 16
@@ -476,47 +480,72 @@ __global__ void __launch_bounds__(kUpWarps * 32, RP <= 64 ? 2 : 1)
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) t[s][p] = t4[(s * 3 + p) * 32];
     }
-    // where the rows of this lane's sums start within 16 bytes
-    const long long row0 = __shfl_sync(0xffffffffu, my_row, gq), row1 = __shfl_sync(0xffffffffu, my_row, gq + 8);
-    const int dc0 = (int)(reinterpret_cast<uintptr_t>(out + row0 * g.ldo * kSize) & 15) / kSize;
-    const int dc1 = (int)(reinterpret_cast<uintptr_t>(out + row1 * g.ldo * kSize) & 15) / kSize;
+    const int dc0 = shift_of(__shfl_sync(0xffffffffu, my_row, gq)), dc1 = shift_of(__shfl_sync(0xffffffffu, my_row, gq + 8));
+    // this lane's two sums of a group of 8 channels go here, the group's place added
+    float* to0 = mine + gq * U::kPitch + 2 * q + dc0;
+    float* to1 = mine + (gq + 8) * U::kPitch + 2 * q + dc1;
     const uint16_t* w = g.b + (long long)a * g.N * g.R;
+    auto weights = [&](int n, uint32_t (&b)[RP / 8]) {  // of channels c0 + 8 n + gq
+      const long long ch = c0 + 8 * n + gq;
+      const bool there = (!SHIFT || ch >= 0) && ch < g.N;
+      const uint16_t* row = w + (there ? ch * g.R : 0);
+#pragma unroll
+      for (int h = 0; h < RP / (4 * kLoad); ++h) {
+        uint32_t part[kLoad / 2];
+        load_weights<kLoad, VEC>(row, 4 * kLoad * h + kLoad * q, there ? g.R : 0, part);
+#pragma unroll
+        for (int i = 0; i < kLoad / 2; ++i) b[h * (kLoad / 2) + i] = part[i];
+      }
+    };
+    auto multiply = [&](const uint32_t (&b)[RP / 8], float (&d)[4]) {
+      d[0] = d[1] = d[2] = d[3] = 0.f;
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+        for (int p = PARTS - 1; p >= 0; --p) {
+          if constexpr (RP <= 64)
+            mma(d, t[s][p], b[2 * s], b[2 * s + 1]);
+          else
+            mma(d, t4[(s * 3 + p) * 32], b[2 * s], b[2 * s + 1]);
+        }
+    };
     constexpr int kTurn = RP <= 64 ? 4 : 2;  // groups of 8 channels with their loads in flight
-    for (int n0 = any_shift ? -1 : 0; n0 < U::kChannels / 8; n0 += kTurn) {
+#pragma unroll 1
+    for (int n0 = 0; n0 < U::kChannels / 8; n0 += kTurn) {
       uint32_t b[kTurn][RP / 8];
 #pragma unroll
+      for (int j = 0; j < kTurn; ++j) weights(n0 + j, b[j]);
+#pragma unroll
       for (int j = 0; j < kTurn; ++j) {
-        const long long ch = c0 + 8 * (n0 + j) + gq;
-        const bool there = n0 + j < U::kChannels / 8 && ch >= 0 && ch < g.N;
-        const uint16_t* row = w + (there ? ch * g.R : 0);
-#pragma unroll
-        for (int h = 0; h < RP / (4 * kLoad); ++h) {
-          uint32_t part[kLoad / 2];
-          load_weights<kLoad, VEC>(row, 4 * kLoad * h + kLoad * q, there ? g.R : 0, part);
-#pragma unroll
-          for (int i = 0; i < kLoad / 2; ++i) b[j][h * (kLoad / 2) + i] = part[i];
+        float d[4];
+        multiply(b[j], d);
+        // up to 7 places behind the last chunk: the pitch has room, nobody reads them
+        const int at = 8 * (n0 + j);
+        if constexpr (SHIFT) {
+          to0[at] = d[0];
+          to0[at + 1] = d[1];
+        } else {
+          *reinterpret_cast<float2*>(to0 + at) = make_float2(d[0], d[1]);
+        }
+        if (count > 8) {
+          if constexpr (SHIFT) {
+            to1[at] = d[2];
+            to1[at + 1] = d[3];
+          } else {
+            *reinterpret_cast<float2*>(to1 + at) = make_float2(d[2], d[3]);
+          }
         }
       }
+    }
+    if constexpr (SHIFT) {  // the last channels in front of the block, where a row's chunks start earlier
+      uint32_t b[RP / 8];
+      float d[4];
+      weights(-1, b);
+      multiply(b, d);
 #pragma unroll
-      for (int j = 0; j < kTurn; ++j) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-          for (int p = PARTS - 1; p >= 0; --p) {
-            if constexpr (RP <= 64)
-              mma(d, t[s][p], b[j][2 * s], b[j][2 * s + 1]);
-            else
-              mma(d, t4[(s * 3 + p) * 32], b[j][2 * s], b[j][2 * s + 1]);
-          }
-        // to its place in the rows' chunks; what belongs to the neighbouring blocks is left out
-        const int at = 8 * (n0 + j) + 2 * q;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int p0 = at + e + dc0, p1 = at + e + dc1;
-          if (p0 >= 0 && p0 < U::kChannels) mine[gq * U::kPitch + p0] = d[e];
-          if (p1 >= 0 && p1 < U::kChannels) mine[(gq + 8) * U::kPitch + p1] = d[2 + e];
-        }
+      for (int e = 0; e < 2; ++e) {
+        if (2 * q + e + dc0 >= 8) to0[e - 8] = d[e];
+        if (2 * q + e + dc1 >= 8) to1[e - 8] = d[2 + e];
       }
     }
     __syncwarp();
@@ -524,14 +553,12 @@ __global__ void __launch_bounds__(kUpWarps * 32, RP <= 64 ? 2 : 1)
 
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
+    if (2 * i >= count) break;
     const int r = 2 * i + (lane >> 4);
     const long long row = __shfl_sync(0xffffffffu, my_row, r);
-    if (r >= count) continue;
-    char* o = out + row * g.ldo * kSize;
-    const int dc = (int)(reinterpret_cast<uintptr_t>(o) & 15) / kSize;
-    const long long id = c0 + (lane & 15) * E - dc;
-    if (id >= g.N) continue;
-    o += id * kSize;
+    const long long id = c0 + (lane & 15) * E - shift_of(row);
+    if (r >= count || id >= g.N) continue;
+    char* o = out + (row * g.ldo + id) * kSize;
     uint4 z = v[i];
     if (a == kBad) {
       const uint32_t nan = F32 ? 0x7fffffffu : 0x7fff7fffu;
@@ -548,7 +575,7 @@ __global__ void __launch_bounds__(kUpWarps * 32, RP <= 64 ? 2 : 1)
                        pack_bf(bf_lo(z.z) + h.x, bf_hi(z.z) + h.y), pack_bf(bf_lo(z.w) + h.z, bf_hi(z.w) + h.w));
       }
     }
-    if (id >= 0 && id + E <= g.N) {
+    if ((!SHIFT || id >= 0) && id + E <= g.N) {
       st16(o, z);
     } else {  // the ends of a row
       const uint32_t w[4] = {z.x, z.y, z.z, z.w};
@@ -596,37 +623,39 @@ cudaError_t launch_down(const AdapterArgs& g, long long most, Tile* tiles, uint8
   return e;
 }
 
-template <bool F32, int RP, bool VEC, bool NEAR>
-cudaError_t launch_up(const AdapterArgs& g, unsigned most, const Tile* tiles, const uint8_t* t, int shift, cudaStream_t st) {
+template <bool F32, int RP, bool VEC, bool NEAR, bool SHIFT>
+cudaError_t launch_up(const AdapterArgs& g, unsigned most, const Tile* tiles, const uint8_t* t, cudaStream_t st) {
   using U = Up<F32>;
-  auto kern = k_adapters_up<F32, RP, VEC, NEAR>;
+  auto kern = k_adapters_up<F32, RP, VEC, NEAR, SHIFT>;
   if (!allow_smem(kern, U::kSmem)) return cudaErrorUnknown;
   cudaLaunchAttribute attr;
-  const long long blocks = ((long long)g.N + U::E - 1 + U::kChannels - 1) / U::kChannels;
+  const long long blocks = ((long long)g.N + (SHIFT ? U::E - 1 : 0) + U::kChannels - 1) / U::kChannels;
   const dim3 grid((unsigned)((blocks + kUpWarps - 1) / kUpWarps), most, 1);
   const cudaLaunchConfig_t cfg = config(grid, kUpWarps * 32, U::kSmem, st, &attr);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, g, tiles, t, shift);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, g, tiles, t);
   if (e == cudaSuccess) note_launch();
   return e;
 }
-template <bool F32, int RP>
-cudaError_t launch_up_as(const AdapterArgs& g, bool vec, bool near, unsigned most, const Tile* tiles, const uint8_t* t, int shift,
+template <bool F32, int RP, bool VEC>
+cudaError_t launch_up_as(const AdapterArgs& g, bool near, bool shift, unsigned most, const Tile* tiles, const uint8_t* t,
                          cudaStream_t st) {
-  if (vec)
-    return near ? launch_up<F32, RP, true, true>(g, most, tiles, t, shift, st)
-                : launch_up<F32, RP, true, false>(g, most, tiles, t, shift, st);
-  return near ? launch_up<F32, RP, false, true>(g, most, tiles, t, shift, st)
-              : launch_up<F32, RP, false, false>(g, most, tiles, t, shift, st);
+  if (!near) return launch_up<F32, RP, VEC, false, true>(g, most, tiles, t, st);
+  return shift ? launch_up<F32, RP, VEC, true, true>(g, most, tiles, t, st)
+               : launch_up<F32, RP, VEC, true, false>(g, most, tiles, t, st);
 }
 template <bool F32>
-cudaError_t launch_up_ranks(const AdapterArgs& g, bool vec, bool near, unsigned most, const Tile* tiles, const uint8_t* t,
-                            int shift, cudaStream_t st) {
+cudaError_t launch_up_ranks(const AdapterArgs& g, bool vec, bool near, bool shift, unsigned most, const Tile* tiles,
+                            const uint8_t* t, cudaStream_t st) {
+#define DS_UP(RP)                                                            \
+  return vec ? launch_up_as<F32, RP, true>(g, near, shift, most, tiles, t, st) \
+             : launch_up_as<F32, RP, false>(g, near, shift, most, tiles, t, st)
   switch (padded(g.R)) {
-    case 16: return launch_up_as<F32, 16>(g, vec, near, most, tiles, t, shift, st);
-    case 32: return launch_up_as<F32, 32>(g, vec, near, most, tiles, t, shift, st);
-    case 64: return launch_up_as<F32, 64>(g, vec, near, most, tiles, t, shift, st);
-    default: return launch_up_as<F32, 128>(g, vec, near, most, tiles, t, shift, st);
+    case 16: DS_UP(16);
+    case 32: DS_UP(32);
+    case 64: DS_UP(64);
+    default: DS_UP(128);
   }
+#undef DS_UP
 }
 
 }  // namespace
@@ -663,13 +692,13 @@ cudaError_t launch_add_adapters(const AdapterArgs& g, bool x_f32, bool f32, cuda
   const bool vec = padded(g.R) == 16 ? g.R % 4 == 0 && (reinterpret_cast<uintptr_t>(g.b) & 7) == 0 : g.R % 8 == 0 && at16(g.b);
   const bool near = ((reinterpret_cast<uintptr_t>(g.base) ^ reinterpret_cast<uintptr_t>(g.out)) & 15) == 0 &&
                     (g.ldb - g.ldo) * s % 16 == 0;
-  const int shift = !at16(g.out) || g.ldo * s % 16 != 0;
+  const bool shift = !at16(g.out) || g.ldo * s % 16 != 0;
   // the grid's second dimension ends at 65535
   for (long long first = 0; first < most && e == cudaSuccess; first += 65535) {
     const unsigned some = (unsigned)(most - first < 65535 ? most - first : 65535);
     const uint8_t* ts = t + first * t_bytes(g.R);
-    e = f32 ? launch_up_ranks<true>(g, vec, near, some, tiles + first, ts, shift, st)
-            : launch_up_ranks<false>(g, vec, near, some, tiles + first, ts, shift, st);
+    e = f32 ? launch_up_ranks<true>(g, vec, near, shift, some, tiles + first, ts, st)
+            : launch_up_ranks<false>(g, vec, near, shift, some, tiles + first, ts, st);
   }
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
