@@ -515,7 +515,7 @@ int64_t ds_add_adapters_workspace(int32_t n, int32_t L, int32_t R);
  *   base         device [n][N] of dtype, rows ldb elements apart (ldb >= N), any
  *                alignment of the element type.
  *   dtype        DS_DTYPE_BF16 or DS_DTYPE_F32, of base and out.
- *   n, N         n >= 0 (0: nothing launched), N >= 1.
+ *   n, N         n >= 0 (0: nothing launched), 1 <= N <= 2^30.
  *   x            device [n][K] of x_dtype, rows ldx elements apart (ldx >= K), any
  *                alignment of the element type: the hidden states that the
  *                projection was fed, before its norm when gain is given.
@@ -538,7 +538,7 @@ int64_t ds_add_adapters_workspace(int32_t n, int32_t L, int32_t R);
  *   d_status     device uint32 or NULL.
  *   stream       cudaStream_t.
  * A row of x with a NaN or an infinity gives a row of NaN.
- * Returns DS_OK, DS_ERR_INVALID_ARG, DS_ERR_UNSUPPORTED (L, R, ldb, ldx or ldo too
+ * Returns DS_OK, DS_ERR_INVALID_ARG, DS_ERR_UNSUPPORTED (N, L, R, ldb, ldx or ldo too
  * large) or DS_ERR_CUDA.
  */
 ds_status ds_add_adapters(const void* base, int32_t dtype, int32_t n, int32_t N, int64_t ldb, const void* x,

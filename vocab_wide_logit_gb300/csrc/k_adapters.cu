@@ -10,20 +10,23 @@
 //                    each find their own tile.
 //   k_adapters_down  a CTA per tile and 32 ranks: t = scale A y by matrix instructions
 //                    (16 rows x 8 ranks x 16 inputs), the inputs split over 16 warps.
-//   k_adapters_up    a warp per tile and 256 bytes of each row's logits: t B^T by
-//                    matrix instructions (16 rows x 8 channels x 16 ranks), then base
-//                    and result in whole 16-byte chunks a row.
+//   k_adapters_up    CTAs that stay, each with an equal share of (tile, block of channels)
+//                    pairs: t B^T by matrix instructions (16 rows x 8 channels x 16
+//                    ranks), then base and result in whole 16-byte chunks a row.
 // The adapters' bf16 goes into the instructions as it is. The fp32 operand goes in as a
 // sum of bf16 parts, each the rest that the parts before it left: three of them (2^-27
 // of it is lost) for fp32 logits, two (2^-18) for bf16 logits, whose own rounding is
 // 2^-9. Sums are fp32.
 //
-// What bounds it is HBM: base, result and the weights once. The weights' bytes go
-// from memory to the registers that the instructions read, 8 or 16 bytes a lane, each
-// lane taking the ranks that lie together there as "its" four of an instruction's 16
-// (any order of the ranks is right that both operands share). Rows start at any
-// element: a tile of channels starts for each row at that row's own 16-byte boundary,
-// for which eight channels in front of the tile are computed twice.
+// What bounds it is HBM: base, result and the weights once. The weights of a block of
+// channels are one run of bytes whatever the rank, and come to shared memory with the
+// base's chunks by asynchronous copies of 16 bytes, three blocks ahead: with the loads
+// of a block in registers instead, 16 warps of 100 registers an SM left the memory
+// idle two thirds of the time. A lane takes the ranks that lie together, 8 or 16 bytes,
+// as "its" four of an instruction's 16 (any order of the ranks is right that both operands
+// share). Rows start at any element: a block of channels starts for each row at that
+// row's own 16-byte boundary, for which eight channels in front of the block are
+// computed twice.
 #include <cuda_bf16.h>
 
 #include "ds_device.cuh"
@@ -39,7 +42,7 @@ constexpr int kDownThreads = 512;
 constexpr int kDownWarps = kDownThreads / 32;
 constexpr int kDownRanks = 32;     // ranks of a CTA
 constexpr int kPlanThreads = 1024;
-constexpr int kUpWarps = 8;
+constexpr int kUpThreads = 256;
 constexpr int kNone = -1, kBad = -2;  // a tile of rows without an adapter, of ids beyond the stack
 
 // Rows of one adapter; count 0: no tile.
@@ -49,6 +52,12 @@ struct Tile {
   int32_t pad[14];
 };
 static_assert(sizeof(Tile) == 128, "tiles keep what follows them aligned");
+
+// What stands in front of the tiles.
+struct Head {
+  int32_t tiles;
+  int32_t pad[31];
+};
 
 // Ranks filled up with zeros: 16, or a power of two from 32.
 __host__ __device__ constexpr int padded(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
@@ -129,7 +138,7 @@ __device__ __forceinline__ void load_weights(const uint16_t* row, int i, int end
 // ---------------------------------------------------------------- tiles
 // More than 256 rows: counted, then dealt out. Which rows share a tile may differ from
 // run to run; a row's result does not depend on it.
-__global__ void __launch_bounds__(kPlanThreads) k_adapters_plan(const AdapterArgs g, Tile* tiles, int most) {
+__global__ void __launch_bounds__(kPlanThreads) k_adapters_plan(const AdapterArgs g, Head* head, Tile* tiles, int most) {
   extern __shared__ uint32_t counts[];  // rows of each kind (adapters, none, bad), then its first tile
   __shared__ int warp_sums[kPlanThreads / 32];
   pdl_release();
@@ -174,16 +183,18 @@ __global__ void __launch_bounds__(kPlanThreads) k_adapters_plan(const AdapterArg
     tiles[slot / kRows].rows[slot % kRows] = (int)i;
   }
   for (int i = all + tid; i < most; i += kPlanThreads) tiles[i].count = 0;
+  if (tid == 0) head->tiles = all;
 }
 
 // Up to 256 rows: tile number `want` of those that the rows' order makes, found by a CTA.
+// Returns how many there are.
 struct SelfPlan {
   int kinds[kSelfPlan];
   int leaders[kDownWarps];
   int at;  // the row that opens the tile
   int count;
 };
-__device__ __forceinline__ void self_plan(const AdapterArgs& g, int want, SelfPlan& s, Tile& tile) {
+__device__ __forceinline__ int self_plan(const AdapterArgs& g, int want, SelfPlan& s, Tile& tile) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   if (tid < kSelfPlan) s.kinds[tid] = tid < g.n ? kind_of(g.ids[tid], g.L) : kBad - 1;
   if (tid == 0) s.at = -1;
@@ -217,6 +228,9 @@ __device__ __forceinline__ void self_plan(const AdapterArgs& g, int want, SelfPl
   if (tid == 0) tile.count = c;
   if (tid < kRows && tid >= c) tile.rows[tid] = 0;
   __syncthreads();
+  int all = 0;
+  for (int i = 0; i < kDownWarps; ++i) all += s.leaders[i];
+  return all;
 }
 
 // ---------------------------------------------------------------- t = scale A y
@@ -232,14 +246,16 @@ struct Down {
 
 // PARTS: bf16 parts of an input. VEC: 16-byte loads.
 template <bool XF32, int PARTS, bool VEC>
-__global__ void __launch_bounds__(kDownThreads) k_adapters_down(const AdapterArgs g, Tile* tiles, uint8_t* t_out, int parts_out) {
+__global__ void __launch_bounds__(kDownThreads) k_adapters_down(const AdapterArgs g, Head* head, Tile* tiles, uint8_t* t_out,
+                                                                int parts_out) {
   extern __shared__ __align__(16) unsigned char raw[];
   Down& sh = *reinterpret_cast<Down*>(raw);
   pdl_release();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, gq = lane >> 2, q = lane & 3;
   if (g.n <= kSelfPlan) {
-    self_plan(g, blockIdx.x, sh.plan, sh.tile);
+    const int all = self_plan(g, blockIdx.x, sh.plan, sh.tile);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) head->tiles = all;
     if (blockIdx.y == 0 && tid < 2 + kRows)
       reinterpret_cast<int32_t*>(&tiles[blockIdx.x])[tid] = reinterpret_cast<const int32_t*>(&sh.tile)[tid];
   } else {
@@ -392,202 +408,303 @@ __global__ void __launch_bounds__(kDownThreads) k_adapters_down(const AdapterArg
 }
 
 // ---------------------------------------------------------------- base + t B^T
-// Logits that a warp makes of each row, 16 chunks of 16 bytes, and the pitch of its
-// results in shared memory (rows 8 banks apart).
-template <bool F32>
+// The kernel's sizes. RP: padded ranks.
+template <bool F32, int RP, bool SHIFT>
 struct Up {
-  static constexpr int E = F32 ? 4 : 8;
-  static constexpr int kChannels = 16 * E;
-  static constexpr int kPitch = kChannels + 8;
-  static constexpr int kSmem = kUpWarps * kRows * kPitch * 4;
+  static constexpr int E = F32 ? 4 : 8;                          // logits of a chunk
+  static constexpr int kChunks = (F32 ? RP <= 64 : RP <= 32) ? 32 : F32 || RP <= 64 ? 16 : 8;  // of a row and block
+  static constexpr int kChannels = kChunks * E;                  // of a block
+  static constexpr int kGroups = kChannels / 8;                  // of 8 channels
+  static constexpr int kFront = SHIFT ? 8 : 0;                   // channels in front of the block
+  static constexpr int kPitch = kChannels + 8;                   // rows of results lie 8 banks apart
+  // weights that may start at any 2 bytes, and base
+  static constexpr int kWeights = (kChannels + kFront) * RP * 2 + 32;
+  static constexpr int kStage = kWeights + kRows * kChunks * 16;
+  static constexpr int kResults = kRows * kPitch * 4;
+  static constexpr int kStages = 4 * kStage + kResults <= 110 * 1024 ? 4 : 3;
+  static constexpr int kSmem = kStages * kStage + kResults;
 };
 
-// Not through the read-only path: base may be the result.
-__device__ __forceinline__ uint4 ld16(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
-  return v;
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 __device__ __forceinline__ void st16(void* p, uint4 v) {
   asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
 }
 
-// RP: padded ranks. VEC: weights in one load a lane and step. NEAR: base and result
-// rows lie the same way to 16 bytes. SHIFT: some row starts between two chunks.
+// `COUNT` (4 or 8) weights in shared memory from rank i on, zeros from `end` on.
+template <int COUNT, bool VEC>
+__device__ __forceinline__ void shared_weights(const unsigned char* row, int i, int end, uint32_t* w) {
+  if constexpr (VEC) {
+    if (i >= end) {
+#pragma unroll
+      for (int j = 0; j < COUNT / 2; ++j) w[j] = 0;
+    } else if constexpr (COUNT == 8) {
+      const uint4 v = *reinterpret_cast<const uint4*>(row + 2 * i);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(row + 2 * i);
+      w[0] = v.x, w[1] = v.y;
+    }
+  } else {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
+#pragma unroll
+    for (int j = 0; j < COUNT / 2; ++j) {
+      const uint32_t lo = i + 2 * j < end ? p[i + 2 * j] : 0u, hi = i + 2 * j + 1 < end ? p[i + 2 * j + 1] : 0u;
+      w[j] = lo | (hi << 16);
+    }
+  }
+}
+
+// VEC: a lane's weights in one load. NEAR: base and result rows lie the same way to
+// 16 bytes. SHIFT: some row starts between two chunks.
 template <bool F32, int RP, bool VEC, bool NEAR, bool SHIFT>
-__global__ void __launch_bounds__(kUpWarps * 32, RP <= 64 ? 2 : 1)
-    k_adapters_up(const AdapterArgs g, const Tile* tiles, const uint8_t* t_in) {
-  using U = Up<F32>;
-  constexpr int E = U::E, kSize = F32 ? 4 : 2, PARTS = F32 ? 3 : 2, STEPS = RP / 16;
+__global__ void __launch_bounds__(kUpThreads, 2)
+    k_adapters_up(const AdapterArgs g, const Head* head, const Tile* tiles, const uint8_t* t_in, int blocks) {
+  using U = Up<F32, RP, SHIFT>;
+  constexpr int E = U::E, kSize = F32 ? 4 : 2, PARTS = F32 ? 3 : 2, STEPS = RP / 16, S = U::kStages, W = U::kChunks;
   constexpr int kLoad = RP == 16 ? 4 : 8;  // weights of a lane and load: one instruction's, or two's
-  extern __shared__ __align__(16) float results[];
+  constexpr int kTurns = (kRows * W + kUpThreads - 1) / kUpThreads;
+  extern __shared__ __align__(16) unsigned char smem[];
+  float* results = reinterpret_cast<float*>(smem + S * U::kStage);
+  const uint32_t smem_at = (uint32_t)__cvta_generic_to_shared(smem);
   pdl_release();
   pdl_wait();
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, gq = lane >> 2, q = lane & 3;
-  const Tile& tile = tiles[blockIdx.y];
-  const int count = tile.count, a = tile.adapter;
-  const long long block = (long long)blockIdx.x * kUpWarps + wid;  // of 16 chunks
-  const long long c0 = block * U::kChannels;
-  if (count <= 0 || c0 >= (long long)g.N + (SHIFT ? E - 1 : 0)) return;
-  if (a == kNone && g.out == g.base) return;
-  float* mine = results + wid * kRows * U::kPitch;
-  const int my_row = lane < count ? tile.rows[lane] : 0;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, gq = lane >> 2, q = lane & 3;
+  const long long total = (long long)head->tiles * blocks;
+  const long long lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
   char* out = static_cast<char*>(g.out);
   const char* base = static_cast<const char*>(g.base);
   // how many logits of a row's first chunk are before it
   auto shift_of = [&](long long row) {
     return SHIFT ? (int)(reinterpret_cast<uintptr_t>(out + row * g.ldo * kSize) & 15) / kSize : 0;
   };
+  // turn k of a thread: chunk tid % W of the tile's row tid / W + kPerTurn k
+  constexpr int kPerTurn = kUpThreads / W;
+  const int my_chunk = (tid % W) * E, my_row = tid / W;
+  const int row_bytes = g.R * 2;
+  // a block's first copied channel: with SHIFT those in front of it too
+  auto front = [&](int b) { return SHIFT && b > 0 ? 8 : 0; };
 
-  // lane l, turn i: chunk l % 16 of the tile's row 2 i + l / 16
-  uint4 v[8];
-  if (a != kBad) {
+  // Asks for blocks one after the other, on its own way through the tiles.
+  struct Ask {
+    int tile, block, count, adapter;
+    const char* weights;           // the adapter's, of channel 0
+    const char* base[kTurns];      // this thread's chunks of block 0
+    int shift[kTurns];
+  } ask;
+  ask.tile = -1;
+  int ask_at = (int)(lo / blocks);
+  ask.block = (int)(lo % blocks);
+  long long asked = lo;
+  auto issue = [&](int stage) {
+    if (asked < hi) {
+      if (ask.tile != ask_at) {
+        ask.tile = ask_at;
+        const Tile& tile = tiles[ask_at];
+        ask.count = tile.count;
+        ask.adapter = tile.adapter;
+        ask.weights = reinterpret_cast<const char*>(g.b) + (long long)max(ask.adapter, 0) * g.N * row_bytes;
+        if (!NEAR || ask.adapter == kBad || (ask.adapter == kNone && g.out == g.base)) ask.count = 0;  // no base
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (2 * i >= count) break;
-      const int r = 2 * i + (lane >> 4);
-      const long long row = __shfl_sync(0xffffffffu, my_row, r);
-      const long long id = c0 + (lane & 15) * E - shift_of(row);
-      if (r >= count || id >= g.N) continue;
-      const char* p = base + (row * g.ldb + id) * kSize;
-      if constexpr (NEAR) {
-        v[i] = ld16(p);  // its edges may be other rows' bytes, of the same 16
-      } else {
-        uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          if (id + e < 0 || id + e >= g.N) continue;
-          if constexpr (F32)
-            w[e] = reinterpret_cast<const volatile uint32_t*>(p)[e];
-          else
-            w[e >> 1] |= (uint32_t) reinterpret_cast<const volatile uint16_t*>(p)[e] << (16 * (e & 1));
+        for (int k = 0; k < kTurns; ++k) {
+          const int r = my_row + kPerTurn * k;
+          const long long row = r < ask.count ? tile.rows[r] : 0;
+          ask.shift[k] = shift_of(row);
+          ask.base[k] = base + (row * g.ldb + my_chunk - ask.shift[k]) * kSize;
         }
-        v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      const int c0 = ask.block * U::kChannels;
+      const uint32_t to = smem_at + stage * U::kStage + 16 * tid;
+      if (ask.adapter >= 0) {
+        const int f = front(ask.block), c1 = min(U::kChannels, g.N - c0);
+        const char* from = ask.weights + (long long)(c0 - f) * row_bytes;
+        const int off = (int)(reinterpret_cast<uintptr_t>(from) & 15);
+        const int bytes = off + (c1 + f) * row_bytes;
+        from += 16 * tid - off;
+#pragma unroll
+        for (int i = 0; i < (U::kWeights / 16 + kUpThreads - 1) / kUpThreads; ++i)
+          if (16 * (tid + i * kUpThreads) < bytes) copy16(to + 16 * i * kUpThreads, from + 16 * i * kUpThreads);
+      }
+#pragma unroll
+      for (int k = 0; k < kTurns; ++k) {
+        if (my_row + kPerTurn * k >= ask.count) break;
+        // the ends may be other rows' bytes, of the same 16
+        if (c0 + my_chunk - ask.shift[k] < g.N)
+          copy16(to + U::kWeights + 16 * k * kUpThreads, ask.base[k] + (long long)c0 * kSize);
+      }
+      if (++ask.block == blocks) ask.block = 0, ++ask_at;
+      ++asked;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue(i);
+
+  int at = (int)(lo / blocks), block = (int)(lo % blocks), stage = 0, ready = -1;
+  int count = 0, a = kNone, dc0 = 0, dc1 = 0;
+  bool idle = true;
+  const char* weights = nullptr;
+  char* to_out[kTurns];
+  const char* from_base[kTurns];  // without NEAR
+  int shift[kTurns];
+  const uint4* t4 = nullptr;
+  uint4 t[RP <= 64 ? STEPS : 1][PARTS];
+  for (long long item = lo; item < hi; ++item) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+    __syncthreads();
+    issue(stage == 0 ? S - 1 : stage - 1);
+    if (ready != at) {
+      ready = at;
+      const Tile& tile = tiles[at];
+      count = tile.count;
+      a = tile.adapter;
+      idle = a == kNone && g.out == g.base;
+      weights = reinterpret_cast<const char*>(g.b) + (long long)max(a, 0) * g.N * row_bytes;
+      t4 = reinterpret_cast<const uint4*>(t_in + at * t_bytes(g.R)) + lane;
+#pragma unroll
+      for (int k = 0; k < kTurns; ++k) {
+        const int r = my_row + kPerTurn * k;
+        const long long row = r < count ? tile.rows[r] : 0;
+        shift[k] = shift_of(row);
+        to_out[k] = out + (row * g.ldo + my_chunk - shift[k]) * kSize;
+        from_base[k] = base + (row * g.ldb + my_chunk - shift[k]) * kSize;
+      }
+      if (a >= 0) {
+        if constexpr (RP <= 64) {
+#pragma unroll
+          for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p) t[s][p] = t4[(s * 3 + p) * 32];
+        }
+        dc0 = gq < count ? shift_of(tile.rows[gq]) : 0;
+        dc1 = gq + 8 < count ? shift_of(tile.rows[gq + 8]) : 0;
       }
     }
-  }
-
-  if (a >= 0) {
-    const uint4* t4 = reinterpret_cast<const uint4*>(t_in + blockIdx.y * t_bytes(g.R)) + lane;
-    uint4 t[RP <= 64 ? STEPS : 1][PARTS];
-    if constexpr (RP <= 64) {
+    const int c0 = block * U::kChannels, left = g.N - c0;  // channels from here on
+    const unsigned char* here = smem + stage * U::kStage;
+    if (a >= 0) {
+      const int f = front(block);
+      const unsigned char* w = here + (int)((reinterpret_cast<uintptr_t>(weights) + (long long)(c0 - f) * row_bytes) & 15) +
+                               (f + gq) * row_bytes;
+      auto multiply = [&](int n, bool there, float (&d)[4]) {  // of channels c0 + 8 n + gq
+        const unsigned char* row = w + (there ? n * 8 * row_bytes : 0);
+        d[0] = d[1] = d[2] = d[3] = 0.f;
 #pragma unroll
-      for (int s = 0; s < STEPS; ++s)
+        for (int h = 0; h < RP / (4 * kLoad); ++h) {
+          uint32_t b[kLoad / 2];
+          shared_weights<kLoad, VEC>(row, 4 * kLoad * h + kLoad * q, there ? g.R : 0, b);
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p) t[s][p] = t4[(s * 3 + p) * 32];
-    }
-    const int dc0 = shift_of(__shfl_sync(0xffffffffu, my_row, gq)), dc1 = shift_of(__shfl_sync(0xffffffffu, my_row, gq + 8));
-    // this lane's two sums of a group of 8 channels go here, the group's place added
-    float* to0 = mine + gq * U::kPitch + 2 * q + dc0;
-    float* to1 = mine + (gq + 8) * U::kPitch + 2 * q + dc1;
-    const uint16_t* w = g.b + (long long)a * g.N * g.R;
-    auto weights = [&](int n, uint32_t (&b)[RP / 8]) {  // of channels c0 + 8 n + gq
-      const long long ch = c0 + 8 * n + gq;
-      const bool there = (!SHIFT || ch >= 0) && ch < g.N;
-      const uint16_t* row = w + (there ? ch * g.R : 0);
+          for (int i = 0; i < kLoad / 4; ++i) {
+            const int s = h * (kLoad / 4) + i;
 #pragma unroll
-      for (int h = 0; h < RP / (4 * kLoad); ++h) {
-        uint32_t part[kLoad / 2];
-        load_weights<kLoad, VEC>(row, 4 * kLoad * h + kLoad * q, there ? g.R : 0, part);
-#pragma unroll
-        for (int i = 0; i < kLoad / 2; ++i) b[h * (kLoad / 2) + i] = part[i];
-      }
-    };
-    auto multiply = [&](const uint32_t (&b)[RP / 8], float (&d)[4]) {
-      d[0] = d[1] = d[2] = d[3] = 0.f;
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-        for (int p = PARTS - 1; p >= 0; --p) {
-          if constexpr (RP <= 64)
-            mma(d, t[s][p], b[2 * s], b[2 * s + 1]);
-          else
-            mma(d, t4[(s * 3 + p) * 32], b[2 * s], b[2 * s + 1]);
+            for (int p = PARTS - 1; p >= 0; --p) {
+              if constexpr (RP <= 64)
+                mma(d, t[s][p], b[2 * i], b[2 * i + 1]);
+              else
+                mma(d, t4[(s * 3 + p) * 32], b[2 * i], b[2 * i + 1]);
+            }
+          }
         }
-    };
-    constexpr int kTurn = RP <= 64 ? 4 : 2;  // groups of 8 channels with their loads in flight
-#pragma unroll 1
-    for (int n0 = 0; n0 < U::kChannels / 8; n0 += kTurn) {
-      uint32_t b[kTurn][RP / 8];
-#pragma unroll
-      for (int j = 0; j < kTurn; ++j) weights(n0 + j, b[j]);
-#pragma unroll
-      for (int j = 0; j < kTurn; ++j) {
-        float d[4];
-        multiply(b[j], d);
+      };
+      // this lane's two sums of a group of 8 channels go here, the group's place added
+      float* to0 = results + gq * U::kPitch + 2 * q + dc0;
+      float* to1 = results + (gq + 8) * U::kPitch + 2 * q + dc1;
+      auto put = [&](int n, const float (&d)[4]) {
         // up to 7 places behind the last chunk: the pitch has room, nobody reads them
-        const int at = 8 * (n0 + j);
         if constexpr (SHIFT) {
-          to0[at] = d[0];
-          to0[at + 1] = d[1];
+          to0[8 * n] = d[0];
+          to0[8 * n + 1] = d[1];
         } else {
-          *reinterpret_cast<float2*>(to0 + at) = make_float2(d[0], d[1]);
+          *reinterpret_cast<float2*>(to0 + 8 * n) = make_float2(d[0], d[1]);
         }
         if (count > 8) {
           if constexpr (SHIFT) {
-            to1[at] = d[2];
-            to1[at + 1] = d[3];
+            to1[8 * n] = d[2];
+            to1[8 * n + 1] = d[3];
           } else {
-            *reinterpret_cast<float2*>(to1 + at) = make_float2(d[2], d[3]);
+            *reinterpret_cast<float2*>(to1 + 8 * n) = make_float2(d[2], d[3]);
+          }
+        }
+      };
+      constexpr int kMine = U::kGroups / 8;  // groups of a warp
+      static_assert(U::kGroups % 8 == 0, "the same number for each");
+      float d[kMine][4];
+      if (left >= U::kChannels) {
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) multiply(wid + 8 * j, true, d[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) multiply(wid + 8 * j, 8 * (wid + 8 * j) + gq < left, d[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) put(wid + 8 * j, d[j]);
+      if (SHIFT && wid == 7) {  // the last channels in front of the block, where a row's chunks start earlier
+        multiply(-1, f > 0 && gq - 8 < left, d[0]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (2 * q + e + dc0 >= 8) to0[e - 8] = d[0][e];
+          if (2 * q + e + dc1 >= 8) to1[e - 8] = d[0][2 + e];
+        }
+      }
+      __syncthreads();
+    }
+    if (!idle) {
+#pragma unroll
+      for (int k = 0; k < kTurns; ++k) {
+        if (my_row + kPerTurn * k >= count) break;
+        const int id = c0 + my_chunk - shift[k];
+        if (id >= g.N) continue;
+        uint4 z = make_uint4(0, 0, 0, 0);
+        if constexpr (NEAR) {
+          z = *reinterpret_cast<const uint4*>(here + U::kWeights + 16 * (tid + k * kUpThreads));
+        } else {
+          const char* p = from_base[k] + (long long)c0 * kSize;
+          uint32_t w4[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            if (id + e < 0 || id + e >= g.N) continue;
+            if constexpr (F32)
+              w4[e] = reinterpret_cast<const volatile uint32_t*>(p)[e];
+            else
+              w4[e >> 1] |= (uint32_t) reinterpret_cast<const volatile uint16_t*>(p)[e] << (16 * (e & 1));
+          }
+          z = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+        }
+        if (a == kBad) {
+          const uint32_t nan = F32 ? 0x7fffffffu : 0x7fff7fffu;
+          z = make_uint4(nan, nan, nan, nan);
+        } else if (a >= 0) {
+          const float4* s = reinterpret_cast<const float4*>(results + (my_row + kPerTurn * k) * U::kPitch + my_chunk);
+          if constexpr (F32) {
+            const float4 f = s[0];
+            z = make_uint4(__float_as_uint(__uint_as_float(z.x) + f.x), __float_as_uint(__uint_as_float(z.y) + f.y),
+                           __float_as_uint(__uint_as_float(z.z) + f.z), __float_as_uint(__uint_as_float(z.w) + f.w));
+          } else {
+            const float4 f = s[0], h = s[1];
+            z = make_uint4(pack_bf(bf_lo(z.x) + f.x, bf_hi(z.x) + f.y), pack_bf(bf_lo(z.y) + f.z, bf_hi(z.y) + f.w),
+                           pack_bf(bf_lo(z.z) + h.x, bf_hi(z.z) + h.y), pack_bf(bf_lo(z.w) + h.z, bf_hi(z.w) + h.w));
+          }
+        }
+        char* o = to_out[k] + (long long)c0 * kSize;
+        if ((!SHIFT || id >= 0) && g.N - id >= E) {
+          st16(o, z);
+        } else {  // the ends of a row
+          const uint32_t w4[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            if (id + e < 0 || id + e >= g.N) continue;
+            if constexpr (F32)
+              reinterpret_cast<uint32_t*>(o)[e] = w4[e];
+            else
+              reinterpret_cast<uint16_t*>(o)[e] = (uint16_t)(w4[e >> 1] >> (16 * (e & 1)));
           }
         }
       }
     }
-    if constexpr (SHIFT) {  // the last channels in front of the block, where a row's chunks start earlier
-      uint32_t b[RP / 8];
-      float d[4];
-      weights(-1, b);
-      multiply(b, d);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (2 * q + e + dc0 >= 8) to0[e - 8] = d[e];
-        if (2 * q + e + dc1 >= 8) to1[e - 8] = d[2 + e];
-      }
-    }
-    __syncwarp();
-  }
-
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (2 * i >= count) break;
-    const int r = 2 * i + (lane >> 4);
-    const long long row = __shfl_sync(0xffffffffu, my_row, r);
-    const long long id = c0 + (lane & 15) * E - shift_of(row);
-    if (r >= count || id >= g.N) continue;
-    char* o = out + (row * g.ldo + id) * kSize;
-    uint4 z = v[i];
-    if (a == kBad) {
-      const uint32_t nan = F32 ? 0x7fffffffu : 0x7fff7fffu;
-      z = make_uint4(nan, nan, nan, nan);
-    } else if (a >= 0) {
-      const float4* s = reinterpret_cast<const float4*>(mine + r * U::kPitch + (lane & 15) * E);
-      if constexpr (F32) {
-        const float4 f = s[0];
-        z = make_uint4(__float_as_uint(__uint_as_float(z.x) + f.x), __float_as_uint(__uint_as_float(z.y) + f.y),
-                       __float_as_uint(__uint_as_float(z.z) + f.z), __float_as_uint(__uint_as_float(z.w) + f.w));
-      } else {
-        const float4 f = s[0], h = s[1];
-        z = make_uint4(pack_bf(bf_lo(z.x) + f.x, bf_hi(z.x) + f.y), pack_bf(bf_lo(z.y) + f.z, bf_hi(z.y) + f.w),
-                       pack_bf(bf_lo(z.z) + h.x, bf_hi(z.z) + h.y), pack_bf(bf_lo(z.w) + h.z, bf_hi(z.w) + h.w));
-      }
-    }
-    if ((!SHIFT || id >= 0) && id + E <= g.N) {
-      st16(o, z);
-    } else {  // the ends of a row
-      const uint32_t w[4] = {z.x, z.y, z.z, z.w};
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        if (id + e < 0 || id + e >= g.N) continue;
-        if constexpr (F32)
-          reinterpret_cast<uint32_t*>(o)[e] = w[e];
-        else
-          reinterpret_cast<uint16_t*>(o)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-      }
-    }
+    if (++block == blocks) block = 0, ++at;
+    if (++stage == S) stage = 0;
   }
 }
 
@@ -612,43 +729,47 @@ bool allow_smem(K kern, int bytes) {
 }
 
 template <bool XF32, int PARTS, bool VEC>
-cudaError_t launch_down(const AdapterArgs& g, long long most, Tile* tiles, uint8_t* t, int parts, cudaStream_t st) {
+cudaError_t launch_down(const AdapterArgs& g, long long most, Head* head, Tile* tiles, uint8_t* t, int parts, cudaStream_t st) {
   auto kern = k_adapters_down<XF32, PARTS, VEC>;
   if (!allow_smem(kern, (int)sizeof(Down))) return cudaErrorUnknown;
   cudaLaunchAttribute attr;
   const dim3 grid((unsigned)most, (unsigned)((padded(g.R) + kDownRanks - 1) / kDownRanks), 1);
   const cudaLaunchConfig_t cfg = config(grid, kDownThreads, sizeof(Down), st, &attr);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, g, tiles, t, parts);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, g, head, tiles, t, parts);
   if (e == cudaSuccess) note_launch();
   return e;
 }
 
 template <bool F32, int RP, bool VEC, bool NEAR, bool SHIFT>
-cudaError_t launch_up(const AdapterArgs& g, unsigned most, const Tile* tiles, const uint8_t* t, cudaStream_t st) {
-  using U = Up<F32>;
+cudaError_t launch_up(const AdapterArgs& g, long long most, const Head* head, const Tile* tiles, const uint8_t* t,
+                      cudaStream_t st) {
+  using U = Up<F32, RP, SHIFT>;
+  static_assert(2 * U::kSmem <= 227 * 1024, "two CTAs an SM");
   auto kern = k_adapters_up<F32, RP, VEC, NEAR, SHIFT>;
-  if (!allow_smem(kern, U::kSmem)) return cudaErrorUnknown;
+  const int sms = device_sms();
+  if (sms <= 0 || !allow_smem(kern, U::kSmem)) return cudaErrorUnknown;
   cudaLaunchAttribute attr;
   const long long blocks = ((long long)g.N + (SHIFT ? U::E - 1 : 0) + U::kChannels - 1) / U::kChannels;
-  const dim3 grid((unsigned)((blocks + kUpWarps - 1) / kUpWarps), most, 1);
-  const cudaLaunchConfig_t cfg = config(grid, kUpWarps * 32, U::kSmem, st, &attr);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, g, tiles, t);
+  const long long items = most * blocks;
+  const dim3 grid((unsigned)(items < 2LL * sms ? items : 2LL * sms), 1, 1);
+  const cudaLaunchConfig_t cfg = config(grid, kUpThreads, U::kSmem, st, &attr);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, g, head, tiles, t, (int)blocks);
   if (e == cudaSuccess) note_launch();
   return e;
 }
 template <bool F32, int RP, bool VEC>
-cudaError_t launch_up_as(const AdapterArgs& g, bool near, bool shift, unsigned most, const Tile* tiles, const uint8_t* t,
-                         cudaStream_t st) {
-  if (!near) return launch_up<F32, RP, VEC, false, true>(g, most, tiles, t, st);
-  return shift ? launch_up<F32, RP, VEC, true, true>(g, most, tiles, t, st)
-               : launch_up<F32, RP, VEC, true, false>(g, most, tiles, t, st);
+cudaError_t launch_up_as(const AdapterArgs& g, bool near, bool shift, long long most, const Head* head, const Tile* tiles,
+                         const uint8_t* t, cudaStream_t st) {
+  if (!near) return launch_up<F32, RP, VEC, false, true>(g, most, head, tiles, t, st);
+  return shift ? launch_up<F32, RP, VEC, true, true>(g, most, head, tiles, t, st)
+               : launch_up<F32, RP, VEC, true, false>(g, most, head, tiles, t, st);
 }
 template <bool F32>
-cudaError_t launch_up_ranks(const AdapterArgs& g, bool vec, bool near, bool shift, unsigned most, const Tile* tiles,
-                            const uint8_t* t, cudaStream_t st) {
-#define DS_UP(RP)                                                            \
-  return vec ? launch_up_as<F32, RP, true>(g, near, shift, most, tiles, t, st) \
-             : launch_up_as<F32, RP, false>(g, near, shift, most, tiles, t, st)
+cudaError_t launch_up_ranks(const AdapterArgs& g, bool vec, bool near, bool shift, long long most, const Head* head,
+                            const Tile* tiles, const uint8_t* t, cudaStream_t st) {
+#define DS_UP(RP)                                                                    \
+  return vec ? launch_up_as<F32, RP, true>(g, near, shift, most, head, tiles, t, st) \
+             : launch_up_as<F32, RP, false>(g, near, shift, most, head, tiles, t, st)
   switch (padded(g.R)) {
     case 16: DS_UP(16);
     case 32: DS_UP(32);
@@ -660,46 +781,45 @@ cudaError_t launch_up_ranks(const AdapterArgs& g, bool vec, bool near, bool shif
 
 }  // namespace
 
-long long adapters_workspace(int n, int L, int R) { return tiles_of(n, L) * ((long long)sizeof(Tile) + t_bytes(R)); }
+long long adapters_workspace(int n, int L, int R) {
+  return (long long)sizeof(Head) + tiles_of(n, L) * ((long long)sizeof(Tile) + t_bytes(R));
+}
 
 cudaError_t launch_add_adapters(const AdapterArgs& g, bool x_f32, bool f32, cudaStream_t st) {
   const long long most = tiles_of(g.n, g.L);
-  Tile* tiles = static_cast<Tile*>(g.workspace);
+  Head* head = static_cast<Head*>(g.workspace);
+  Tile* tiles = reinterpret_cast<Tile*>(head + 1);
   uint8_t* t = reinterpret_cast<uint8_t*>(tiles + most);
   cudaLaunchAttribute attr;
   cudaError_t e = cudaSuccess;
   if (g.n > kSelfPlan) {
     const int smem = (g.L + 2) * 4;
     const cudaLaunchConfig_t cfg = config(dim3(1, 1, 1), kPlanThreads, (size_t)smem, st, &attr);
-    e = cudaLaunchKernelEx(&cfg, k_adapters_plan, g, tiles, (int)most);
+    e = cudaLaunchKernelEx(&cfg, k_adapters_plan, g, head, tiles, (int)most);
     if (e != cudaSuccess) return e;
     note_launch();
   }
   const auto at16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
   const int xs = x_f32 ? 4 : 2, s = f32 ? 4 : 2, parts = f32 ? 3 : 2;
   const bool x_vec = at16(g.x) && at16(g.a) && at16(g.gain) && g.K % 8 == 0 && g.ldx * xs % 16 == 0;
+#define DS_DOWN(XF32, PARTS)                                                                \
+  (x_vec ? launch_down<XF32, PARTS, true>(g, most, head, tiles, t, parts, st)               \
+         : launch_down<XF32, PARTS, false>(g, most, head, tiles, t, parts, st))
   if (!x_f32 && !g.gain)  // the inputs are bf16 themselves
-    e = x_vec ? launch_down<false, 1, true>(g, most, tiles, t, parts, st) : launch_down<false, 1, false>(g, most, tiles, t, parts, st);
-  else if (x_f32 && f32)
-    e = x_vec ? launch_down<true, 3, true>(g, most, tiles, t, parts, st) : launch_down<true, 3, false>(g, most, tiles, t, parts, st);
+    e = DS_DOWN(false, 1);
   else if (x_f32)
-    e = x_vec ? launch_down<true, 2, true>(g, most, tiles, t, parts, st) : launch_down<true, 2, false>(g, most, tiles, t, parts, st);
-  else if (f32)
-    e = x_vec ? launch_down<false, 3, true>(g, most, tiles, t, parts, st) : launch_down<false, 3, false>(g, most, tiles, t, parts, st);
+    e = f32 ? DS_DOWN(true, 3) : DS_DOWN(true, 2);
   else
-    e = x_vec ? launch_down<false, 2, true>(g, most, tiles, t, parts, st) : launch_down<false, 2, false>(g, most, tiles, t, parts, st);
+    e = f32 ? DS_DOWN(false, 3) : DS_DOWN(false, 2);
+#undef DS_DOWN
   if (e != cudaSuccess) return e;
+  // a lane's weights in one load: 8 bytes, every adapter's stack at such a boundary, or 16
   const bool vec = padded(g.R) == 16 ? g.R % 4 == 0 && (reinterpret_cast<uintptr_t>(g.b) & 7) == 0 : g.R % 8 == 0 && at16(g.b);
   const bool near = ((reinterpret_cast<uintptr_t>(g.base) ^ reinterpret_cast<uintptr_t>(g.out)) & 15) == 0 &&
                     (g.ldb - g.ldo) * s % 16 == 0;
   const bool shift = !at16(g.out) || g.ldo * s % 16 != 0;
-  // the grid's second dimension ends at 65535
-  for (long long first = 0; first < most && e == cudaSuccess; first += 65535) {
-    const unsigned some = (unsigned)(most - first < 65535 ? most - first : 65535);
-    const uint8_t* ts = t + first * t_bytes(g.R);
-    e = f32 ? launch_up_ranks<true>(g, vec, near, shift, some, tiles + first, ts, st)
-            : launch_up_ranks<false>(g, vec, near, shift, some, tiles + first, ts, st);
-  }
+  e = f32 ? launch_up_ranks<true>(g, vec, near, shift, most, head, tiles, t, st)
+          : launch_up_ranks<false>(g, vec, near, shift, most, head, tiles, t, st);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
