@@ -273,6 +273,18 @@ def test_no_rows():
     assert out.shape == (0, 50)
 
 
+def test_both_ways_of_a_call():
+    status = torch.zeros(1, dtype=torch.int32, device=_dev())
+    for dtype, x_dtype, norm in (("bf16", "bf16", True), ("f32", "f32", False)):
+        base, hidden, ad, ids, gain = _inputs(9, 700, 64, 8, 3, dtype, x_dtype, norm)
+        assert torch.equal(pkg.add_adapters(base, hidden, ad, ids, gain=gain, eps=EPS),
+                           pkg.add_adapters(base, hidden, ad, ids, gain=gain, eps=EPS, d_status=status))
+    for bad in (dict(ids=None), dict(ids=ids.long()), dict(ids=ids[:8]), dict(ids=ids.cpu()), dict(hidden=hidden[:, :63]),
+                dict(hidden=hidden[:8]), dict(base=base[:, :699]), dict(base=base.half()), dict(gain=torch.ones(63, device=_dev()))):
+        with pytest.raises(ValueError):
+            pkg.add_adapters(**{**dict(base=base, hidden=hidden, adapters=ad, ids=ids), **bad})
+
+
 def test_c_name():
     base, hidden, ad, ids, gain = _inputs(9, 700, 64, 8, 3, norm=True)
     out = torch.empty_like(base)

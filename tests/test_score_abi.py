@@ -1,5 +1,6 @@
 """Refusals of the scoring calls and of the adapters: bad arguments are turned away on the host, before any CUDA call."""
 import ctypes
+import types
 
 import pytest
 import torch
@@ -7,7 +8,20 @@ import torch
 import vocab_wide_logit_gb300 as pkg
 from vocab_wide_logit_gb300 import _lib
 
-from test_head_devices import BF16, F32, I32, Tensor, _head, launched  # noqa: F401  (a fixture)
+import test_head_devices
+from test_head_devices import BF16, F32, I32, Tensor, _head
+
+head_launched = test_head_devices.launched  # a fixture
+
+
+@pytest.fixture
+def launched(head_launched, monkeypatch):
+    """The same, with a ds_calls module that hands every call back."""
+    none = types.SimpleNamespace(**{name: lambda *a: None for name in ("sample", "quantize", "linear", "head", "score",
+                                                                       "score_grad", "adapters")})
+    monkeypatch.setattr(_lib, "calls", lambda: none)
+    return head_launched
+
 
 FAKE = ctypes.c_void_p(0x100000)  # never dereferenced: every call below fails validation first
 ODD = ctypes.c_void_p(0x100001)
@@ -102,20 +116,20 @@ def _all_calls(index, n=4, V=16, K=32):
 
 
 @pytest.mark.parametrize("name", sorted(_all_calls(0)))
-def test_tensors_of_the_current_device_are_launched(launched, name):  # noqa: F811
+def test_tensors_of_the_current_device_are_launched(launched, name):
     _all_calls(0)[name]()
     assert launched
 
 
 @pytest.mark.parametrize("name", sorted(_all_calls(0)))
-def test_tensors_of_another_device_are_refused(launched, name):  # noqa: F811
+def test_tensors_of_another_device_are_refused(launched, name):
     with pytest.raises(ValueError, match="current device"):
         _all_calls(1)[name]()
     assert not launched
 
 
 @pytest.mark.parametrize("n,V", [(2 ** 32 + 5, 1), (2 ** 31, 2), (3, 2 ** 32 + 8)])
-def test_sizes_beyond_32_bits_are_refused(launched, n, V):  # noqa: F811
+def test_sizes_beyond_32_bits_are_refused(launched, n, V):
     v, ids = Tensor((n,), F32), Tensor((n,), I32)
     for call in (lambda: pkg.score_tokens(Tensor((n, V), BF16), ids),
                  lambda: pkg.score_tokens_grad(Tensor((n, V), BF16), ids, v, g_logprobs=v),
@@ -125,7 +139,7 @@ def test_sizes_beyond_32_bits_are_refused(launched, n, V):  # noqa: F811
     assert not launched
 
 
-def test_wrong_tensors_are_refused(launched):  # noqa: F811
+def test_wrong_tensors_are_refused(launched):
     n, V, K = 4, 16, 32
 
     def t(*shape, dtype=F32, index=0, address=0x100000):
@@ -155,7 +169,7 @@ def test_wrong_tensors_are_refused(launched):  # noqa: F811
     assert not launched
 
 
-def test_results_beside_the_input_are_taken(launched):  # noqa: F811
+def test_results_beside_the_input_are_taken(launched):
     """Rows side by side in one buffer, and right behind the input."""
     n, V = 4, 16
     v, ids = Tensor((n,), F32), Tensor((n,), I32)
@@ -184,7 +198,7 @@ def test_stacks_are_checked():
         pkg.Adapters(torch.zeros((3, 8, 32), dtype=BF16), torch.zeros((3, 16, 8), dtype=BF16), torch.zeros(3))
 
 
-def test_by_c_name_on_another_device(launched):  # noqa: F811
+def test_by_c_name_on_another_device(launched):
     """The address of another device's tensor on the current stream."""
     t = lambda *shape, dtype=F32: Tensor(shape, dtype, 1)  # noqa: E731
     ids = t(4, dtype=I32)

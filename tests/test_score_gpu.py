@@ -391,6 +391,28 @@ def test_another_stream_and_a_graph():
         _check_grad(dx, y, t, r.lse, r.entropy, gl, gh)
 
 
+def test_both_ways_of_a_call():
+    """The calls that ds_calls runs, and the same through the checks in Python (as with a status word)."""
+    status = torch.zeros(1, dtype=torch.int32, device=_dev())
+    for n, V, dtype, top in ((5, 1025, "bf16", 4), (3, 9001, "f32", 0), (1, 40, "f32", 40)):
+        x, tokens = _inputs(n, V, dtype, n)
+        fast, slow = pkg.score_tokens(x, tokens, top=top), pkg.score_tokens(x, tokens, top=top, d_status=status)
+        assert type(fast) is type(slow) is pkg.TokenScores
+        for a, b in zip(fast, slow):
+            assert torch.equal(a, b) and a.dtype == b.dtype and a.shape == b.shape
+        gl = torch.randn(n, device=_dev())
+        assert torch.equal(pkg.score_tokens_grad(x, tokens, fast.lse, fast.entropy, gl, gl),
+                           pkg.score_tokens_grad(x, tokens, fast.lse, fast.entropy, gl, gl, d_status=status))
+    for bad in (dict(tokens=None), dict(tokens=tokens.long()), dict(tokens=tokens.cpu()), dict(top=41), dict(top=-1),
+                dict(logits=x.half()), dict(logits=x[:, ::2])):
+        with pytest.raises(ValueError):
+            pkg.score_tokens(**{**dict(logits=x, tokens=tokens, top=1), **bad})
+    for bad in (dict(lse=None), dict(lse=fast.lse.double()), dict(g_logprobs=None), dict(g_logprobs=None, g_entropy=gl),
+                dict(g_logprobs=gl.cpu())):
+        with pytest.raises(ValueError):
+            pkg.score_tokens_grad(**{**dict(logits=x, tokens=tokens, lse=fast.lse, g_logprobs=gl), **bad})
+
+
 def test_c_names():
     n, V, top = 4, 2000, 9
     x, tokens = _inputs(n, V, "f32", 5)

@@ -244,7 +244,8 @@ def calls():
         spec.loader.exec_module(module)
         module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
             L.ds_sample_filtered, L.ds_linear_i8_workspace, L.ds_linear_i8, L.ds_head_i8_workspace, L.ds_head_i8,
-            L.ds_quantize_rows)))
+            L.ds_quantize_rows, L.ds_score_tokens, L.ds_score_tokens_grad, L.ds_add_adapters_workspace,
+            L.ds_add_adapters)))
         _calls = module
     return _calls
 

@@ -7,8 +7,12 @@
 //        = gl 1[j = token] - p_j (gl + gh (x_j - lse + H)),
 // in fp32, rounded once to the type of the logits. Every logit is read once and
 // written once and nothing is shared between them but five numbers a row, so HBM
-// bounds it: the 16-byte chunks of all rows are one list, each thread takes four of
-// them 256 apart, which is the same for one long row and for many short ones.
+// bounds it, as long as a bf16 logit costs fewer than about ten instructions: packed
+// fp32 differences and products, the entropy's guard as one packed maximum (a logit
+// 256 below lse counts as that; its p is 0, and -inf stays out of a product with it),
+// the given token apart. The 16-byte chunks of all rows are one list, each thread takes
+// four of them 256 apart, which is the same for one long row and for many short ones;
+// a CTA whose chunks are one row's reads the row's numbers once.
 // A row whose lse is -inf (nothing in it) gets zeros; a logit of probability zero
 // gets exactly zero from the entropy, -inf among them.
 #include "ds_device.cuh"
@@ -42,82 +46,142 @@ __device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
   return r;
 }
 
-template <bool F32>
+// What a row's logits share.
+struct RowGrad {
+  float lse, gl, c, h;  // the gradient is -p (c + h (x - lse)), c = gl + gh H, h = gh
+  uint32_t low2;        // bf16: what x may not fall below, twice
+  int token;            // -1: none
+  bool dead, low;       // nothing in the row; lse so low that nothing finite lies 256 below it
+};
+template <bool ENT>
+__device__ __forceinline__ RowGrad row_grad(const ScoreGradArgs& a, int r) {
+  RowGrad g;
+  const int token = a.tokens[r];
+  g.token = token < a.V ? token : -1;
+  g.lse = a.lse[r];
+  g.gl = g.token >= 0 && a.g_logprobs ? a.g_logprobs[r] : 0.f;
+  g.c = g.gl;
+  g.h = 0.f;
+  g.dead = g.lse == -kInf;
+  g.low = g.lse < -1e38f;
+  if constexpr (ENT) {
+    g.h = a.g_entropy[r];
+    g.c = __fmaf_rn(g.h, a.entropy[r], g.gl);
+    // more than 200 below lse whatever the rounding to bf16 (2^-9 of it, an eighth of the distance for large lse)
+    const float low = g.lse - fmaxf(256.f, fabsf(g.lse) * 0.015625f);
+    g.low2 = pack_bf(low, low);
+  }
+  return g;
+}
+
+template <bool F32, bool ENT>
+__device__ __forceinline__ uint4 chunk_grad(const uint4& v, const RowGrad& g, int first) {
+  constexpr int E = F32 ? 4 : 8;
+  if (g.dead) return make_uint4(0, 0, 0, 0);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const float2 nl = make_float2(-g.lse, -g.lse), l2e = make_float2(kLog2e, kLog2e);
+  const float2 nc = make_float2(-g.c, -g.c), nh = make_float2(-g.h, -g.h);
+  float2 f[E / 2];
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    float2 x;
+    if constexpr (F32) {
+      x = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    } else {
+      uint32_t c = w[i];
+      if constexpr (ENT)
+        if (!g.low) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(c), "r"(g.low2));
+      x = make_float2(bf_lo(c), bf_hi(c));
+    }
+    float2 d = __fadd2_rn(x, nl);
+    const float2 t = __fmul2_rn(d, l2e);
+    const float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+    if constexpr (ENT) {
+      if (F32 || g.low) d = make_float2(fmaxf(d.x, -256.f), fmaxf(d.y, -256.f));
+      f[i] = __fmul2_rn(p, __ffma2_rn(nh, d, nc));
+    } else {
+      f[i] = __fmul2_rn(p, nc);
+    }
+  }
+  const int at = g.token - first;  // the given token's own part
+  if (g.token >= 0 && (unsigned)at < (unsigned)E) {
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      if (at == 2 * i) f[i].x += g.gl;
+      if (at == 2 * i + 1) f[i].y += g.gl;
+    }
+  }
+  if constexpr (F32)
+    return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
+  else
+    return make_uint4(pack_bf(f[0].x, f[0].y), pack_bf(f[1].x, f[1].y), pack_bf(f[2].x, f[2].y), pack_bf(f[3].x, f[3].y));
+}
+
+template <bool F32, bool ENT>
 __global__ void __launch_bounds__(kThreads) k_score_grad(const ScoreGradArgs a, int nq) {
-  constexpr int E = F32 ? 4 : 8;             // elements of a chunk
+  constexpr int E = F32 ? 4 : 8;  // elements of a chunk
   constexpr int kSize = F32 ? 4 : 2;
   pdl_release();
   pdl_wait();
   const long long first = (long long)blockIdx.x * (kThreads * kChunks);
   const long long row0 = first / nq;
   const uint32_t rem = (uint32_t)(first - row0 * nq);
+  auto write = [&](char* out, int id0, const uint4& z) {
+    if (id0 >= 0 && a.V - id0 >= E && (reinterpret_cast<uintptr_t>(out) & 15) == 0) {
+      st16(out, z);
+    } else {
+      const uint32_t w[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        if (id0 + i < 0 || i >= a.V - id0) continue;
+        if constexpr (F32)
+          reinterpret_cast<uint32_t*>(out)[i] = w[i];
+        else
+          reinterpret_cast<uint16_t*>(out)[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+      }
+    }
+  };
+  if (rem + kThreads * kChunks <= (uint32_t)nq) {
+    // one row
+    const char* x = static_cast<const char*>(a.x) + row0 * a.ld * kSize;
+    const int dc = (int)(reinterpret_cast<uintptr_t>(x) & 15) / kSize;
+    const int id0 = (int)((long long)(rem + threadIdx.x) * E - dc);
+    x += (long long)id0 * kSize;
+    uint4 v[kChunks];
+#pragma unroll
+    for (int u = 0; u < kChunks; ++u)
+      if (u * kThreads * E < a.V - id0) v[u] = ld16(x + u * kThreads * 16);
+    const RowGrad g = row_grad<ENT>(a, (int)row0);
+    char* out = static_cast<char*>(a.out) + (row0 * a.ldo + id0) * kSize;
+#pragma unroll
+    for (int u = 0; u < kChunks; ++u)
+      if (u * kThreads * E < a.V - id0)
+        write(out + u * kThreads * 16, id0 + u * kThreads * E, chunk_grad<F32, ENT>(v[u], g, id0 + u * kThreads * E));
+    if (rem == 0 && threadIdx.x == 0 && a.tokens[row0] >= a.V) report(a.d_status, DS_DEV_ERR_PARAM);
+    return;
+  }
   uint4 v[kChunks];
-  const char* row_at[kChunks];
-  int row[kChunks], q[kChunks];
+  int row[kChunks], at[kChunks];
 #pragma unroll
   for (int u = 0; u < kChunks; ++u) {
     const uint32_t i = rem + threadIdx.x + u * kThreads;
-    const uint32_t down = i < (uint32_t)nq ? 0u : i / (uint32_t)nq;
+    const uint32_t down = i < (uint32_t)nq ? 0u : i / (uint32_t)nq, q = i - down * (uint32_t)nq;
     const long long r = row0 + down;
-    row[u] = r < a.n ? (int)r : -1;
-    q[u] = (int)(i - down * (uint32_t)nq);
-    if (row[u] < 0) continue;
-    row_at[u] = static_cast<const char*>(a.x) + r * a.ld * kSize;
-    const uintptr_t at = reinterpret_cast<uintptr_t>(row_at[u]);
-    const int dc = (int)(at & 15) / kSize;
-    if ((long long)q[u] * E - dc >= a.V)
-      row[u] = -1;  // the chunk that only rows starting further into a chunk have
-    else
-      v[u] = ld16(reinterpret_cast<const char*>(at & ~(uintptr_t)15) + 16LL * q[u]);
+    row[u] = -1;
+    if (r >= a.n) continue;
+    const char* x = static_cast<const char*>(a.x) + r * a.ld * kSize;
+    const long long id0 = (long long)q * E - (int)(reinterpret_cast<uintptr_t>(x) & 15) / kSize;
+    if (id0 >= a.V) continue;  // the chunk that only rows starting further into a chunk have
+    row[u] = (int)r;
+    at[u] = (int)id0;
+    v[u] = ld16(x + id0 * kSize);
+    if (q == 0 && a.tokens[r] >= a.V) report(a.d_status, DS_DEV_ERR_PARAM);
   }
 #pragma unroll
   for (int u = 0; u < kChunks; ++u) {
     if (row[u] < 0) continue;
-    const int r = row[u];
-    const int token = a.tokens[r];
-    const float lse = a.lse[r];
-    const bool given = token >= 0 && token < a.V;
-    if (q[u] == 0 && token >= a.V) report(a.d_status, DS_DEV_ERR_PARAM);
-    const float gl = given && a.g_logprobs ? a.g_logprobs[r] : 0.f;
-    const float gh = a.g_entropy ? a.g_entropy[r] : 0.f;
-    const float shift = a.g_entropy ? a.entropy[r] : 0.f;
-    const bool dead = lse == -kInf;
-    const int dc = (int)(reinterpret_cast<uintptr_t>(row_at[u]) & 15) / kSize;
-    const int id0 = q[u] * E - dc;
-    float f[E];
-    if constexpr (F32) {
-      f[0] = __uint_as_float(v[u].x);
-      f[1] = __uint_as_float(v[u].y);
-      f[2] = __uint_as_float(v[u].z);
-      f[3] = __uint_as_float(v[u].w);
-    } else {
-      unpack8(v[u], f);
-    }
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float d = f[i] - lse;
-      const float p = ex2_approx(d * kLog2e);
-      // p = 0 has no part in the entropy; its d may be -inf
-      const float w = p == 0.f ? 0.f : p * __fmaf_rn(gh, d + shift, gl);
-      f[i] = dead ? 0.f : (id0 + i == token ? gl - w : -w);
-    }
-    char* out = static_cast<char*>(a.out) + (r * a.ldo + id0) * kSize;
-    if (id0 >= 0 && (long long)id0 + E <= a.V && (reinterpret_cast<uintptr_t>(out) & 15) == 0) {
-      if constexpr (F32)
-        st16(out, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
-      else
-        st16(out, make_uint4(pack_bf(f[0], f[1]), pack_bf(f[2], f[3]), pack_bf(f[4], f[5]), pack_bf(f[6], f[7])));
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const long long id = (long long)id0 + i;
-        if (id < 0 || id >= a.V) continue;
-        if constexpr (F32)
-          reinterpret_cast<float*>(out)[i] = f[i];
-        else
-          reinterpret_cast<uint16_t*>(out)[i] = (uint16_t)pack_bf(f[i], 0.f);
-      }
-    }
+    const RowGrad g = row_grad<ENT>(a, row[u]);
+    write(static_cast<char*>(a.out) + (row[u] * a.ldo + at[u]) * kSize, at[u], chunk_grad<F32, ENT>(v[u], g, at[u]));
   }
 }
 
@@ -137,8 +201,9 @@ cudaError_t launch_score_grad(const ScoreGradArgs& a, bool f32, cudaStream_t st)
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = f32 ? cudaLaunchKernelEx(&cfg, k_score_grad<true>, a, nq)
-                            : cudaLaunchKernelEx(&cfg, k_score_grad<false>, a, nq);
+  const auto kern = a.g_entropy ? (f32 ? k_score_grad<true, true> : k_score_grad<false, true>)
+                                : (f32 ? k_score_grad<true, false> : k_score_grad<false, false>);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, nq);
   if (e != cudaSuccess) return e;
   note_launch();
   return cudaGetLastError();

@@ -26,6 +26,10 @@ decltype(&ds_linear_i8_workspace) p_linear_ws = nullptr;
 decltype(&ds_linear_i8) p_linear = nullptr;
 decltype(&ds_head_i8_workspace) p_head_ws = nullptr;
 decltype(&ds_head_i8) p_head = nullptr;
+decltype(&ds_score_tokens) p_score = nullptr;
+decltype(&ds_score_tokens_grad) p_score_grad = nullptr;
+decltype(&ds_add_adapters_workspace) p_adapters_ws = nullptr;
+decltype(&ds_add_adapters) p_adapters = nullptr;
 
 const at::Tensor* tensor(PyObject* o) { return THPVariable_CheckExact(o) ? &THPVariable_Unpack(o) : nullptr; }
 
@@ -181,14 +185,99 @@ PyObject* head(PyObject*, PyObject* const* v, Py_ssize_t count) {
   END_HANDLE_TH_ERRORS
 }
 
+// score(logits, tokens, top) -> (logprobs, lse, entropy, ranks, top ids, top logprobs)
+PyObject* score(PyObject*, PyObject* const* v, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
+  Rows x;
+  int32_t c;
+  void* tokens;
+  const at::Tensor* t = count == 3 && p_score ? tensor(v[0]) : nullptr;
+  if (!rows(t, &x) || !code(t->scalar_type(), &c) || !vec(v[1], x.n, at::kInt, x.device, false, &tokens) ||
+      !PyLong_CheckExact(v[2]))
+    Py_RETURN_NONE;
+  const long top = PyLong_AsLong(v[2]);
+  if (top < 0 || top > x.k || top > DS_SCORE_MAX_TOP) {
+    PyErr_Clear();
+    Py_RETURN_NONE;
+  }
+  const at::TensorOptions f = on(x.device, at::kFloat), i = on(x.device, at::kInt);
+  at::Tensor r[6] = {at::empty({x.n}, f), at::empty({x.n}, f),      at::empty({x.n}, f),
+                     at::empty({x.n}, i), at::empty({x.n, top}, i), at::empty({x.n, top}, f)};
+  const ds_status rc = p_score(x.p, c, (int32_t)x.n, (int32_t)x.k, x.ld, (const int32_t*)tokens, (int32_t)top,
+                               (float*)r[0].data_ptr(), (float*)r[1].data_ptr(), (float*)r[2].data_ptr(),
+                               (int32_t*)r[3].data_ptr(), (int32_t*)r[4].data_ptr(), (float*)r[5].data_ptr(), nullptr,
+                               stream(x.device));
+  if (rc != DS_OK) return PyLong_FromLong(rc);
+  PyObject* all = PyTuple_New(6);
+  for (int j = 0; all && j < 6; ++j) {
+    PyObject* o = THPVariable_Wrap(std::move(r[j]));
+    if (!o) {
+      Py_CLEAR(all);
+      break;
+    }
+    PyTuple_SET_ITEM(all, j, o);
+  }
+  return all;
+  END_HANDLE_TH_ERRORS
+}
+
+// score_grad(logits, tokens, lse, entropy, g_logprobs, g_entropy) -> gradient
+PyObject* score_grad(PyObject*, PyObject* const* v, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
+  Rows x;
+  int32_t c;
+  void *tokens, *lse, *entropy, *gl, *gh;
+  const at::Tensor* t = count == 6 && p_score_grad ? tensor(v[0]) : nullptr;
+  if (!rows(t, &x) || !code(t->scalar_type(), &c) || !vec(v[1], x.n, at::kInt, x.device, false, &tokens) ||
+      !vec(v[2], x.n, at::kFloat, x.device, false, &lse) || !vec(v[3], x.n, at::kFloat, x.device, true, &entropy) ||
+      !vec(v[4], x.n, at::kFloat, x.device, true, &gl) || !vec(v[5], x.n, at::kFloat, x.device, true, &gh) ||
+      (!gl && !gh) || (gh && !entropy))
+    Py_RETURN_NONE;
+  at::Tensor out = at::empty({x.n, x.k}, on(x.device, t->scalar_type()));
+  const ds_status rc = p_score_grad(x.p, c, (int32_t)x.n, (int32_t)x.k, x.ld, (const int32_t*)tokens, (const float*)lse,
+                                    (const float*)entropy, (const float*)gl, (const float*)gh, out.data_ptr(), x.k,
+                                    nullptr, stream(x.device));
+  return rc != DS_OK ? PyLong_FromLong(rc) : THPVariable_Wrap(std::move(out));
+  END_HANDLE_TH_ERRORS
+}
+
+// adapters(base, hidden, a, b, scale, ids, gain, eps) -> base with the adapters' part; a, b and scale as the
+// Adapters that hold them were checked
+PyObject* adapters(PyObject*, PyObject* const* v, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
+  Rows base, x;
+  int32_t c, xc;
+  void *ids, *gain;
+  const bool all = count == 8 && p_adapters;
+  const at::Tensor *t = all ? tensor(v[0]) : nullptr, *h = all ? tensor(v[1]) : nullptr, *a = all ? tensor(v[2]) : nullptr,
+                   *b = all ? tensor(v[3]) : nullptr, *s = all ? tensor(v[4]) : nullptr;
+  if (!rows(t, &base) || !code(t->scalar_type(), &c) || !rows(h, &x) || !code(h->scalar_type(), &xc) || !a || !b || !s ||
+      a->dim() != 3 || b->dim() != 3 || a->get_device() != base.device || x.n != base.n || x.k != a->size(2) ||
+      base.k != b->size(1) || !vec(v[5], base.n, at::kInt, base.device, false, &ids) ||
+      !vec(v[6], x.k, at::kFloat, base.device, true, &gain))
+    Py_RETURN_NONE;
+  const double eps = PyFloat_AsDouble(v[7]);
+  if (PyErr_Occurred()) return nullptr;
+  const int32_t L = (int32_t)a->size(0), R = (int32_t)a->size(1);
+  at::Tensor out = at::empty({base.n, base.k}, on(base.device, t->scalar_type()));
+  const int64_t need = p_adapters_ws((int32_t)base.n, L, R);
+  at::Tensor ws = at::empty({need}, on(base.device, at::kByte));
+  const ds_status rc =
+      p_adapters(base.p, c, (int32_t)base.n, (int32_t)base.k, base.ld, x.p, xc, (int32_t)x.k, x.ld, (const float*)gain,
+                 (float)eps, a->const_data_ptr(), b->const_data_ptr(), (const float*)s->const_data_ptr(), L, R,
+                 (const int32_t*)ids, out.data_ptr(), base.k, ws.data_ptr(), need, nullptr, stream(base.device));
+  return rc != DS_OK ? PyLong_FromLong(rc) : THPVariable_Wrap(std::move(out));
+  END_HANDLE_TH_ERRORS
+}
+
 // bind(addresses of the entry points)
 PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t count) {
-  void* p[6];
-  if (count != 6) {
-    PyErr_SetString(PyExc_TypeError, "bind() takes six addresses");
+  void* p[10];
+  if (count != 10) {
+    PyErr_SetString(PyExc_TypeError, "bind() takes ten addresses");
     return nullptr;
   }
-  for (int i = 0; i < 6; ++i) {
+  for (int i = 0; i < 10; ++i) {
     p[i] = PyLong_AsVoidPtr(v[i]);
     if (PyErr_Occurred()) return nullptr;
   }
@@ -198,6 +287,10 @@ PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t count) {
   p_head_ws = reinterpret_cast<decltype(p_head_ws)>(p[3]);
   p_head = reinterpret_cast<decltype(p_head)>(p[4]);
   p_quantize = reinterpret_cast<decltype(p_quantize)>(p[5]);
+  p_score = reinterpret_cast<decltype(p_score)>(p[6]);
+  p_score_grad = reinterpret_cast<decltype(p_score_grad)>(p[7]);
+  p_adapters_ws = reinterpret_cast<decltype(p_adapters_ws)>(p[8]);
+  p_adapters = reinterpret_cast<decltype(p_adapters)>(p[9]);
   Py_RETURN_NONE;
 }
 
@@ -206,6 +299,9 @@ PyMethodDef methods[] = {
     {"linear", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(linear)), METH_FASTCALL, nullptr},
     {"head", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(head)), METH_FASTCALL, nullptr},
     {"quantize", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(quantize)), METH_FASTCALL, nullptr},
+    {"score", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(score)), METH_FASTCALL, nullptr},
+    {"score_grad", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(score_grad)), METH_FASTCALL, nullptr},
+    {"adapters", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(adapters)), METH_FASTCALL, nullptr},
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "ds_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -245,6 +245,10 @@ def add_adapters(base, hidden, adapters, ids, gain=None, eps=1e-6, out=None, d_s
     if stream is not None:
         with torch.cuda.stream(stream):
             return add_adapters(base, hidden, adapters, ids, gain, eps, out, d_status)
+    if out is None and d_status is None:
+        r = _lib.calls().adapters(base, hidden, adapters.a, adapters.b, adapters.scale, ids, gain, eps)
+        if r is not None:
+            return _check("ds_add_adapters", r) if type(r) is int else r
     n, N, ldb, index = _rows("base", base, _CODE)
     rows, K, ldx, at = _rows("hidden", hidden, _CODE)
     if rows != n or K != adapters.K or at != index:

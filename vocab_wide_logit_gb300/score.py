@@ -2,7 +2,7 @@
 alternatives, and the gradient of what was scored with respect to the logits.
 
 Functions check their tensors and allocate their outputs on the stream that the call runs on, as those of the serving
-head do; the compute is in the library. Nothing here is recorded by autograd: score_tokens_grad() is the backward pass,
+head do, and the usual calls go through _lib.calls() as theirs; the compute is in the library. Nothing here is recorded by autograd: score_tokens_grad() is the backward pass,
 called with what the forward pass returned.
 """
 from typing import NamedTuple
@@ -38,6 +38,10 @@ def score_tokens(logits, tokens, top=0, d_status=None, stream=None):
     if stream is not None:
         with torch.cuda.stream(stream):
             return score_tokens(logits, tokens, top, d_status)
+    if d_status is None:
+        r = _lib.calls().score(logits, tokens, top)
+        if r is not None:
+            return TokenScores._make(r) if type(r) is tuple else _check("ds_score_tokens", r)
     n, V, ld, index = _rows("logits", logits, _CODE)
     _count("top", top, min(V, _lib.DS_SCORE_MAX_TOP))
     if tokens is None:
@@ -63,6 +67,10 @@ def score_tokens_grad(logits, tokens, lse, entropy=None, g_logprobs=None, g_entr
     if stream is not None:
         with torch.cuda.stream(stream):
             return score_tokens_grad(logits, tokens, lse, entropy, g_logprobs, g_entropy, out, d_status)
+    if out is None and d_status is None:
+        r = _lib.calls().score_grad(logits, tokens, lse, entropy, g_logprobs, g_entropy)
+        if r is not None:
+            return _check("ds_score_tokens_grad", r) if type(r) is int else r
     n, V, ld, index = _rows("logits", logits, _CODE)
     if tokens is None or lse is None or (g_logprobs is None and g_entropy is None):
         raise ValueError("tokens, lse and g_logprobs or g_entropy are needed")
