@@ -186,6 +186,16 @@ __device__ __noinline__ void add_sums_low(uint4 v, float m, float2& s, float2& t
     t.x += e > 0.f ? e * d : 0.f;
   }
 }
+// NaN when one of a chunk is, else 0.
+template <bool F32>
+__device__ __noinline__ float nan_of(uint4 v) {
+  float n = 0.f;
+  for (int i = 0; i < Row<F32>::E; ++i) {
+    const float f = logit_of<F32>(v, i);
+    if (f != f) n = f;
+  }
+  return n;
+}
 // What the clamp of bf16 logits may not fall below: more than 200 under m, whatever
 // the rounding to bf16 (2^-9 of it, an eighth of the distance for large m).
 __device__ __forceinline__ uint32_t low_of(float m) { return bf2(m - fmaxf(256.f, fabsf(m) * 0.015625f)); }
@@ -210,22 +220,20 @@ __device__ __forceinline__ int count_before(const uint4& v, bool front, float xt
   }
   return n;
 }
-template <bool F32, int U, bool FRONT>
+// The same for chunks none of which is in front of the token's.
+template <bool F32, int U>
 __device__ __forceinline__ int count_all(const uint4 (&v)[U], float xt) {
   int n = 0;
   if constexpr (F32) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) n += count_before<F32>(v[u], FRONT, xt);
+    for (int u = 0; u < U; ++u) n += count_before<F32>(v[u], false, xt);
   } else {
     static_assert(U * 4 <= 128, "sums of ones in bf16 are exact up to 256");
     const uint32_t x2 = bf2(xt);
     uint32_t c = 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c = add2(c, FRONT ? ge2(w[i], x2) : gt2(w[i], x2));
-    }
+    for (int u = 0; u < U; ++u)
+      c = add2(c, add2(add2(gt2(v[u].x, x2), gt2(v[u].y, x2)), add2(gt2(v[u].z, x2), gt2(v[u].w, x2))));
     n = (int)(bf_lo(c) + bf_hi(c));
   }
   return n;
@@ -249,9 +257,9 @@ struct Sums {
 };
 
 struct Given {
-  int token;   // -1: none
-  float x;     // its logit; +inf without one (nothing counts as before)
-  int chunk;   // its chunk; 0 without one
+  int token;  // -1: none
+  float x;    // its logit; +inf without one (nothing counts as before)
+  int chunk;  // its chunk; 0 without one
 };
 template <bool F32>
 __device__ __forceinline__ Given given_token(const ScoreArgs& a, int row, const Row<F32>& x) {
@@ -264,15 +272,17 @@ __device__ __forceinline__ Given given_token(const ScoreArgs& a, int row, const 
   }
   return g;
 }
-// What `before` lacks or has too much: ties in front of the token in its own chunk;
-// the padding in front of the row, which ties with a token of -inf.
+// Lane i: logit i of the token's chunk when that is in front of the token, else NaN.
 template <bool F32>
-__device__ __forceinline__ int rank_mend(const Row<F32>& x, const Given& g) {
-  if (g.token < 0) return 0;
-  int n = g.x == -kInf && g.chunk > 0 ? -x.dc : 0;
-  const int first = max(0, (int)((long long)g.chunk * Row<F32>::E - x.dc));
-  for (int id = first; id < g.token; ++id) n += x.logit(id) == g.x;
-  return n;
+__device__ __forceinline__ float in_front(const Row<F32>& x, const Given& g) {
+  const int id = max(0, (int)((long long)g.chunk * Row<F32>::E - x.dc)) + (int)(threadIdx.x & 31);
+  return id < g.token ? x.logit(id) : __int_as_float(0x7fffffff);
+}
+// What `before` lacks or has too much: ties in front of the token in its own chunk;
+// the padding in front of the row, which ties with a token of -inf. For a whole warp.
+__device__ __forceinline__ int rank_mend(const Given& g, float near, int dc) {
+  const int n = __popc(__ballot_sync(0xffffffffu, near == g.x));
+  return n - (g.x == -kInf && g.chunk > 0 ? dc : 0);
 }
 
 // Writes the row's four numbers; returns lse, NaN when nothing may be listed.
@@ -399,6 +409,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_score_warp(const ScoreArgs a) {
     v[u] = q < x.nq ? x.chunk(q) : nothing<F32>();
   }
   const Given g = given_token(a, row, x);
+  const float near = in_front(x, g);
   // the row's first and last chunk reach beyond it
   if (lane == 0) mask_edges<F32>(v[0], 0, x.dc, a.V);
 #pragma unroll
@@ -431,22 +442,15 @@ __global__ void __launch_bounds__(kWarps * 32) k_score_warp(const ScoreArgs a) {
   }
   r.s = warp_sum(s.x + s.y);
   r.t = warp_sum(t.x + t.y);
-  if (r.m == -kInf) {  // a row of NaN and -inf alone
+  if (r.m == -kInf) {  // a row of NaN and -inf alone: s shows the NaN
     float seen = 0.f;
 #pragma unroll
-    for (int u = 0; u < C; ++u)
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const float f = logit_of<F32>(v[u], i);
-        if (f != f) seen = f;
-      }
+    for (int u = 0; u < C; ++u) seen += nan_of<F32>(v[u]);
     r.s = warp_sum(seen);
   }
   r.before = warp_sum_i(r.before);
-  if (lane == 0) {
-    r.before += rank_mend(x, g);
-    write_row(a, row, r, g);
-  }
+  r.before += rank_mend(g, near, x.dc);
+  if (lane == 0) write_row(a, row, r, g);
   if (a.top == 0) return;
   const bool none = is_none(r);
   if (none) {
@@ -593,6 +597,21 @@ __device__ __forceinline__ u64 list_cut(const u64* list, int n, int* bits, u64* 
   });
 }
 
+// f(key, how many of the list are above it) for each of n keys, 16 threads a key.
+template <int NT, typename F>
+__device__ __forceinline__ void rank_list(const u64* list, int n, u64 cut, F f) {
+  const int half = threadIdx.x >> 4, part = threadIdx.x & 15;
+  for (int i = half; (i & ~1) < n; i += NT / 16) {  // both halves of a warp, or neither
+    const u64 mine = i < n ? list[i] : 0;
+    int above = 0;
+    if (mine >= cut)
+      for (int j = part; j < n; j += 16) above += list[j] > mine;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
+    if (part == 0 && i < n && mine >= cut) f(mine, above);
+  }
+}
+
 template <bool F32, int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a) {
   constexpr int E = Row<F32>::E, U = kUnroll, kList = list_size(NT);
@@ -606,43 +625,43 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
   const int row = (int)(blockIdx.x / (unsigned)cs);
   const Row<F32> x(a, row);
   const int q_lo = (int)((long long)rank * x.nq / cs), q_hi = (int)((long long)(rank + 1) * x.nq / cs);
+  const int q_in = min(q_hi, x.nq - 1);  // chunks below it (but the row's first) lie within the row
 
-  auto load = [&](uint4 (&v)[U], int q) {
-    if (q + (U - 1) * NT < q_hi) {
+  auto load_edge = [&](uint4 (&v)[U], int q) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = x.chunk(q + u * NT);
-    } else {
-#pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = q + u * NT < q_hi ? x.chunk(q + u * NT) : nothing<F32>();
-    }
+    for (int u = 0; u < U; ++u) v[u] = q + u * NT < q_hi ? x.chunk(q + u * NT) : nothing<F32>();
     // the row's first and last chunk reach beyond it
     if (q == 0) mask_edges<F32>(v[0], 0, x.dc, a.V);
-    if (q + (U - 1) * NT >= x.nq - 1) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (q + u * NT == x.nq - 1) mask_edges<F32>(v[u], q + u * NT, x.dc, a.V);
-    }
+    for (int u = 0; u < U; ++u)
+      if (q + u * NT == x.nq - 1) mask_edges<F32>(v[u], q + u * NT, x.dc, a.V);
   };
 
-  uint4 v[U];
+  uint4 v[U], w[U];
   int q = q_lo + tid;
-  load(v, q);
+  load_edge(v, q);
   if (tid < 64) sh.bits[tid] = 0;
   if (tid == 0) sh.count = 0, sh.differ = 0;
   const Given g = given_token(a, row, x);
-  float m = -kInf, second = -kInf, seen = 0.f;  // second: the largest of the other batches
+  float m = -kInf, second = -kInf;  // second: the largest of the other batches
   uint32_t low2 = 0;
-  int at = q, at_batch = q, before = 0;
+  int at = q, before = 0;
+  bool usual = false;
   float2 s = make_float2(0.f, 0.f), t = s;
-  while (q < q_hi) {
-    uint4 next[U];
+  // takes a batch while the next one is on its way; false behind the last
+  auto step = [&](const uint4 (&v)[U], uint4 (&next)[U]) {
     const int qn = q + U * NT;
-    if (qn < q_hi) load(next, qn);
+    if (qn + (U - 1) * NT < q_in) {
+      const char* p = x.base + 16LL * qn;
+#pragma unroll
+      for (int u = 0; u < U; ++u) next[u] = ld_stream16(p + u * NT * 16);
+    } else if (qn < q_hi) {
+      load_edge(next, qn);
+    }
     // the running maximum and the first chunk that has it
     const float c = chunks_max<F32, U>(v);
     second = fmaxf(second, fminf(c, m));
     if (c > m) {
-      at_batch = q;
 #pragma unroll
       for (int u = U - 1; u >= 0; --u)
         if (chunk_max<F32>(v[u]) == c) at = q + u * NT;
@@ -652,38 +671,40 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
       s = make_float2(s.x * f, s.y * f);
       m = c;
       low2 = low_of(m);
+      usual = !is_low(m);
     }
-    if (qn - NT < g.chunk && qn - NT < q_hi) {
-      before += count_all<F32, U, true>(v, g.x);
-    } else if (q > g.chunk) {
-      before += count_all<F32, U, false>(v, g.x);
-    } else {
+    if (c >= g.x) {  // few batches reach a likely token
+      if (q >= g.chunk)
+        before += count_all<F32, U>(v, g.x);
+      else
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (q + u * NT < q_hi) before += count_before<F32>(v[u], q + u * NT < g.chunk, g.x);
+        for (int u = 0; u < U; ++u)
+          if (q + u * NT < q_hi) before += count_before<F32>(v[u], q + u * NT < g.chunk, g.x);
     }
-    if (!is_low(m)) {
+    if (usual) {
 #pragma unroll
       for (int u = 0; u < U; ++u) add_sums<F32>(v[u], m, low2, s, t);
     } else if (m != -kInf) {
       for (int u = 0; u < U; ++u) add_sums_low<F32>(v[u], m, s, t);
-    } else {  // -inf and NaN alone
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const float f = logit_of<F32>(v[u], i);
-          if (f != f) seen = f;
-        }
+    } else {  // -inf and NaN alone: s shows the NaN
+      for (int u = 0; u < U; ++u) s.x += nan_of<F32>(v[u]);
     }
     q = qn;
+    return qn < q_hi;
+  };
+  // (two turns with the batches' roles exchanged instead of moved: 31.5 us for 28.5 at 256 x
+  // 248320 without alternatives)
+  if (q < q_hi)
+#pragma unroll 1
+    while (step(v, w)) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = next[u];
-  }
+      for (int u = 0; u < U; ++u) v[u] = w[u];
+    }
 
+  const float near = wid == 0 ? in_front(x, g) : 0.f;
   // join the block's sums
   {
-    Sums p{m, s.x + s.y + seen, t.x + t.y, before};
+    Sums p{m, s.x + s.y, t.x + t.y, before};
     p = warp_join(p, 32);
     if (lane == 0) sh.warps[wid] = p;
   }
@@ -705,38 +726,62 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
     if (lane == 0) sh.total = p;
   }
   if (top > 0) {
-    const int groups = NT / width;
-    if (tid < groups) {
-      // the top-th of the groups' maxima bounds the slice's top-th logit from below
-      const u64 k = sh.keys[tid];
-      int above = 0;
-      for (int j = 0; j < groups; ++j) above += sh.keys[j] > k || (sh.keys[j] == k && j < tid);
-      if (above == top - 1) sh.bound = k;
+    // the top-th of the groups' maxima bounds the slice's top-th logit from below; the
+    // threads of a group share the comparisons
+    const int groups = NT / width, group = tid / width;
+    const u64 k = sh.keys[group];
+    int above = 0;
+    for (int j = tid & (width - 1); j < groups; j += width) above += sh.keys[j] > k || (sh.keys[j] == k && j < group);
+    for (int o = width >> 1; o > 0; o >>= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
+    if (above == top - 1) sh.bound = k;
+  }
+  __syncthreads();
+  if (cs == 1) {
+    Sums r = sh.total;
+    if (wid == 0) {
+      r.before += rank_mend(g, near, x.dc);
+      if (tid == 0) write_row(a, row, r, g);
     }
-    __syncthreads();
+    if (is_none(r)) {  // nothing to list
+      for (int i = tid; i < top; i += NT) write_top(a, row, i, 0, r, true);
+      return;
+    }
+    if (top == 0) return;
+  }
+  int listed = 0;
+  u64 cut = 0;
+  if (top > 0) {
     const u64 bound = sh.bound;
-    // The logits of this thread's share that reach the bound: in its best batch, and in
-    // the others when one of them has any.
-    auto scan = [&](auto f) {
-      if (own == 0 || own < bound) return;
-      const bool one = (((u64)order_key(second + 0.f) << 32) | 0xffffffffu) < bound;
-      for (int p = one ? at_batch : q_lo + tid; p < q_hi; p += U * NT) {
-        uint4 w[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) w[u] = p + u * NT < q_hi ? x.chunk(p + u * NT) : nothing<F32>();
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if ((((u64)order_key(chunk_max<F32>(w[u]) + 0.f) << 32) | 0xffffffffu) < bound) continue;
-          const int q1 = p + u * NT;
-          if (q1 >= q_hi) break;
-          for (int i = 0; i < E; ++i) {
-            const long long id = (long long)q1 * E - x.dc + i;
-            const float l = pick<F32>(w[u], i);
-            if (id >= 0 && id < a.V && (((u64)order_key(l + 0.f) << 32) | (uint32_t)~q1) >= bound) f(order_of(l, (int)id));
-          }
-        }
-        if (one) break;
+    const float bound_x = bound == 0 ? -kInf : logit_of_key(bound);
+    // The logits that reach the bound: in the best batch of each thread whose maximum does,
+    // and in all of the thread's share, taken by its whole warp, when another batch has any.
+    const int at_batch = q_lo + tid + (at - q_lo - tid) / (U * NT) * (U * NT);
+    const bool has = own != 0 && own >= bound;
+    // (a tie with the maximum comes after its batch)
+    const uint32_t earliest = second == m ? (uint32_t)~(at_batch + U * NT) : 0xffffffffu;
+    const bool one = (((u64)order_key(second + 0.f) << 32) | earliest) < bound;
+    auto visit = [&](const uint4& b, int q1, auto f) {
+      if ((((u64)order_key(chunk_max<F32>(b) + 0.f) << 32) | (uint32_t)~q1) < bound) return;
+      for (uint32_t reach = reaching<F32>(b, bound_x); reach; reach &= reach - 1) {
+        const int i = __ffs(reach) - 1;
+        const long long id = (long long)q1 * E - x.dc + i;
+        const uint32_t l = order_key(pick<F32>(b, i) + 0.f);
+        if (id >= 0 && id < a.V && (((u64)l << 32) | (uint32_t)~q1) >= bound) f(((u64)l << 32) | (uint32_t)~(int)id);
       }
+    };
+    auto scan = [&](auto f) {
+      if (has && one) {
+        uint4 b[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) b[u] = at_batch + u * NT < q_hi ? x.chunk(at_batch + u * NT) : nothing<F32>();
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (at_batch + u * NT < q_hi) visit(b[u], at_batch + u * NT, f);
+      }
+      for (unsigned all = __ballot_sync(0xffffffffu, has && !one); all; all &= all - 1)
+        for (long long p = q_lo + (tid & ~31) + __ffs(all) - 1 + (long long)lane * NT; p < q_hi; p += 32 * NT)
+          visit(x.chunk((int)p), (int)p, f);
+      __syncwarp();
     };
     auto put = [&](u64 key) {
       const int pos = atomicAdd(&sh.count, 1);
@@ -744,8 +789,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
     };
     scan(put);
     __syncthreads();
-    u64 cut = 0;
-    int listed = sh.count;
+    listed = sh.count;
     if (listed > kList) {
       // the largest logits met in few threads: the exact cut, then the list again
       cut = block_cut(sh.bits, top, 0, 63, [&](u64 trial) {
@@ -764,31 +808,23 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
     } else if (listed > kLong) {
       cut = list_cut<NT>(sh.list, listed, sh.bits, &sh.differ, top);
     }
-    // in order to the joining CTA, zeros behind the last
-    if (cs > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    u64* sorted = cs > 1 ? cluster.map_shared_rank(sh.sorted, 0) + rank * top : sh.sorted;
-    for (int i = tid; i < listed; i += NT) {
-      const u64 mine = sh.list[i];
-      if (mine < cut) continue;
-      int above = 0;
-      for (int j = 0; j < listed; ++j) above += sh.list[j] > mine;
-      if (above < top) sorted[above] = mine;
-    }
-    for (int i = listed + tid; i < top; i += NT) sorted[i] = 0;
-  } else {
-    __syncthreads();
-    if (cs > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   }
   if (cs == 1) {
-    __syncthreads();
-    Sums r = sh.total;
-    if (tid == 0) {
-      r.before += rank_mend(x, g);
-      write_row(a, row, r, g);
-    }
-    const bool none = is_none(r);
-    for (int i = tid; i < top; i += NT) write_top(a, row, i, sh.sorted[i], r, none);
+    const Sums r = sh.total;
+    rank_list<NT>(sh.list, listed, cut, [&](u64 key, int above) {
+      if (above < top) write_top(a, row, above, key, r, false);
+    });
     return;
+  }
+
+  // in order to the joining CTA, zeros behind the last
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  {
+    u64* sorted = cluster.map_shared_rank(sh.sorted, 0) + rank * top;
+    rank_list<NT>(sh.list, listed, cut, [&](u64 key, int above) {
+      if (above < top) sorted[above] = key;
+    });
+    for (int i = listed + tid; i < top; i += NT) sorted[i] = 0;
   }
   if (tid == 0) *cluster.map_shared_rank(&sh.slices[rank], 0) = sh.total;
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -798,14 +834,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
   // every warp joins the slices' sums for itself
   Sums r = lane < cs ? sh.slices[lane] : Sums{-kInf, 0.f, 0.f, 0};
   r = warp_join(r, 32);
-  if (tid == 0) {
-    Sums w = r;
-    w.before += rank_mend(x, g);
-    write_row(a, row, w, g);
+  if (wid == 0) {
+    Sums all = r;
+    all.before += rank_mend(g, near, x.dc);
+    if (tid == 0) write_row(a, row, all, g);
   }
   if (top == 0) return;
-  const bool none = is_none(r);
-  if (none) {
+  if (is_none(r)) {
     for (int i = tid; i < top; i += NT) write_top(a, row, i, 0, r, true);
     return;
   }
@@ -823,8 +858,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
       most = most > last ? most : last;
     }
     const unsigned who = __ballot_sync(0xffffffffu, lane < cs && above == c - 1);
-    const u64 second = __shfl_sync(0xffffffffu, kd, __ffs(who) - 1);
-    bound = most > second ? most : second;
+    const u64 second_bound = __shfl_sync(0xffffffffu, kd, __ffs(who) - 1);
+    bound = most > second_bound ? most : second_bound;
   }
   if (tid == 0) sh.count = 0, sh.differ = 0;
   if (tid < 64) sh.bits[tid] = 0;
@@ -832,20 +867,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
   for (int i = tid; i < cs * top; i += NT) {
     const u64 key = sh.sorted[i];
     if (key == 0 || key < bound) continue;
-    sh.list[atomicAdd(&sh.count, 1)] = key;  // at most cs top = kList
+    sh.list[atomicAdd(&sh.count, 1)] = key;  // at most cs top, which it holds
   }
   __syncthreads();
-  const int listed = sh.count;
-  u64 cut = 0;
-  if (listed > kLong)
-    cut = list_cut<NT>(sh.list, listed, sh.bits, &sh.differ, top);
-  for (int i = tid; i < listed; i += NT) {
-    const u64 mine = sh.list[i];
-    if (mine < cut) continue;
-    int above = 0;
-    for (int j = 0; j < listed; ++j) above += sh.list[j] > mine;
-    if (above < top) write_top(a, row, above, mine, r, false);
-  }
+  listed = sh.count;
+  cut = listed > kLong ? list_cut<NT>(sh.list, listed, sh.bits, &sh.differ, top) : 0;
+  rank_list<NT>(sh.list, listed, cut, [&](u64 key, int above) {
+    if (above < top) write_top(a, row, above, key, r, false);
+  });
 }
 static_assert(kMaxCluster * DS_SCORE_MAX_TOP <= list_size(512), "the survivors of all slices fit the list");
 
