@@ -74,7 +74,8 @@ SIZES = [(1, 1, 1, 1, 1), (1, 1025, 64, 16, 1), (2, 3, 5, 2, 2), (3, 31, 33, 3, 
          (8, 256, 256, 8, 2), (9, 257, 1000, 7, 4), (15, 1000, 64, 16, 5), (16, 1025, 512, 16, 1), (17, 1025, 72, 17, 4),
          (24, 5003, 2048, 16, 8), (31, 640, 1024, 32, 40), (33, 513, 96, 33, 3), (64, 2000, 333, 64, 9), (65, 8200, 1024, 8, 5),
          (100, 300, 200, 100, 7), (128, 1024, 128, 128, 3), (37, 701, 1001, 13, 6), (257, 1025, 512, 24, 6), (600, 264, 160, 48, 2),
-         (1939, 1025, 256, 8, 5), (40, 333, 5000, 127, 3), (1030, 77, 64, 1, 300), (4, 70001, 64, 16, 2)]
+         (1939, 1025, 256, 8, 5), (40, 333, 5000, 127, 3), (1030, 77, 64, 1, 300), (4, 70001, 64, 16, 2),
+         (32, 90, 40, 16, 3), (33, 90, 40, 16, 40), (8192, 33, 24, 5, 50), (8193, 33, 24, 5, 50), (20000, 17, 40, 16, 3)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

@@ -5,9 +5,9 @@
 //
 // Rows are gathered into tiles of up to 16 that have the same adapter, so that an
 // adapter's weights are read once for 16 rows in whatever order the rows come.
-//   k_adapters_plan  (more than 256 rows) one CTA counts the rows of each adapter and
-//                    deals them out to tiles; up to 256 rows the next kernel's CTAs
-//                    each find their own tile.
+//   k_adapters_plan  (more than 8192 rows) one CTA counts the rows of each adapter and
+//                    deals them out to tiles; up to 8192 rows the next kernel's CTAs each
+//                    find their own tile, which saves a launch (4 us).
 //   k_adapters_down  a CTA per tile and 32 ranks: t = scale A y by matrix instructions
 //                    (16 rows x 8 ranks x 16 inputs), the inputs split over 16 warps.
 //   k_adapters_up    CTAs that stay, each with an equal share of (tile, block of channels)
@@ -37,7 +37,7 @@ namespace ds {
 namespace {
 
 constexpr int kRows = 16;          // rows of a tile
-constexpr int kSelfPlan = 256;     // rows up to which k_adapters_down plans for itself
+constexpr int kSelfPlan = 8192;    // rows up to which k_adapters_down plans for itself
 constexpr int kDownThreads = 512;
 constexpr int kDownWarps = kDownThreads / 32;
 constexpr int kDownRanks = 32;     // ranks of a CTA
@@ -136,7 +136,7 @@ __device__ __forceinline__ void load_weights(const uint16_t* row, int i, int end
 }
 
 // ---------------------------------------------------------------- tiles
-// More than 256 rows: counted, then dealt out. Which rows share a tile may differ from
+// More than 8192 rows: counted, then dealt out. Which rows share a tile may differ from
 // run to run; a row's result does not depend on it.
 __global__ void __launch_bounds__(kPlanThreads) k_adapters_plan(const AdapterArgs g, Head* head, Tile* tiles, int most) {
   extern __shared__ uint32_t counts[];  // rows of each kind (adapters, none, bad), then its first tile
@@ -186,57 +186,100 @@ __global__ void __launch_bounds__(kPlanThreads) k_adapters_plan(const AdapterArg
   if (tid == 0) head->tiles = all;
 }
 
-// Up to 256 rows: tile number `want` of those that the rows' order makes, found by a CTA.
-// Returns how many there are.
+// Up to 32 rows: tile number `want` of those that the rows' order makes, found by a warp
+// alone, to rows[]. Returns how many there are.
+__device__ __forceinline__ int warp_plan(const AdapterArgs& g, int want, int32_t* rows, int& adapter, int& count) {
+  const int lane = threadIdx.x & 31;
+  const bool there = lane < g.n;
+  const int kind = there ? kind_of(g.ids[lane], g.L) : kBad - 1;
+  const int before = __popc(__match_any_sync(0xffffffffu, kind) & ((1u << lane) - 1));  // rows of the kind in front
+  unsigned leaders = __ballot_sync(0xffffffffu, there && before % kRows == 0);
+  const int all = __popc(leaders);
+  for (int i = 0; i < want; ++i) leaders &= leaders - 1;
+  const int leader = leaders ? __ffs(leaders) - 1 : 0;
+  adapter = __shfl_sync(0xffffffffu, kind, leader);
+  const int first = __shfl_sync(0xffffffffu, before, leader);
+  const bool in = leaders && there && kind == adapter && before / kRows == first / kRows;
+  if (lane < kRows) rows[lane] = 0;
+  __syncwarp();
+  if (in) rows[before % kRows] = lane;
+  count = __popc(__ballot_sync(0xffffffffu, in));
+  return all;
+}
+
+// Up to 8192 rows: the same by a CTA, the tiles in the order of the adapters, then those
+// without one, then the bad ones.
 struct SelfPlan {
-  int kinds[kSelfPlan];
-  int leaders[kDownWarps];
-  int at;  // the row that opens the tile
-  int count;
+  int sums[kDownWarps];
+  int adapter, part, count, all;
 };
-__device__ __forceinline__ int self_plan(const AdapterArgs& g, int want, SelfPlan& s, Tile& tile) {
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  if (tid < kSelfPlan) s.kinds[tid] = tid < g.n ? kind_of(g.ids[tid], g.L) : kBad - 1;
-  if (tid == 0) s.at = -1;
+__device__ __forceinline__ int block_plan(const AdapterArgs& g, int want, SelfPlan& s, uint32_t* counts, int32_t* rows, int& adapter,
+                                          int& count) {
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, kinds = g.L + 2;
+  for (int i = tid; i < kinds; i += kDownThreads) counts[i] = 0;
+  if (tid == 0) s.count = 0;
+  if (tid < kRows) rows[tid] = 0;
   __syncthreads();
-  const int kind = tid < g.n ? s.kinds[tid] : kBad - 1;
-  int before = 0;  // rows of this kind in front of this one
-  if (wid * 32 < g.n) {
-    const int4* four = reinterpret_cast<const int4*>(s.kinds);
-    for (int j = 0; j < wid * 8; ++j) {
-      const int4 v = four[j];
-      before += (v.x == kind) + (v.y == kind) + (v.z == kind) + (v.w == kind);
+  for (int i0 = wid * 32; i0 < g.n; i0 += kDownThreads) {
+    const int a = i0 + lane < g.n ? kind_of(g.ids[i0 + lane], g.L) : kBad - 1;
+    const unsigned same = __match_any_sync(0xffffffffu, a);
+    if (a > kBad - 1 && (same & ((1u << lane) - 1)) == 0) atomicAdd(&counts[a >= 0 ? a : g.L - 1 - a], (uint32_t)__popc(same));
+  }
+  __syncthreads();
+  const int per = (kinds + kDownThreads - 1) / kDownThreads, lo = tid * per, hi = min(lo + per, kinds);
+  int mine = 0;
+  for (int i = lo; i < hi; ++i) mine += (int)((counts[i] + kRows - 1) / kRows);
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) s.sums[wid] = incl;
+  __syncthreads();
+  int at = incl - mine, all = 0;
+  for (int i = 0; i < kDownWarps; ++i) {
+    at += i < wid ? s.sums[i] : 0;
+    all += s.sums[i];
+  }
+  if (want >= at && want < at + mine)
+    for (int i = lo; i < hi; ++i) {
+      const int t = (int)((counts[i] + kRows - 1) / kRows);
+      if (want >= at && want < at + t) {
+        s.adapter = i < g.L ? i : g.L - 1 - i;
+        s.part = want - at;
+        s.count = min(kRows, (int)counts[i] - s.part * kRows);
+      }
+      at += t;
     }
-    before += __popc(__match_any_sync(0xffffffffu, kind) & ((1u << lane) - 1));
+  __syncthreads();
+  adapter = s.adapter;
+  count = s.count;
+  if (count == 0) return all;
+  // its rows, a stretch of rows to each warp
+  const int stretch = (g.n + kDownThreads - 1) / kDownThreads * 32, i0 = wid * stretch, i1 = min(i0 + stretch, g.n);
+  int found = 0;
+  for (int i = i0; i < i1; i += 32)
+    found += __popc(__ballot_sync(0xffffffffu, i + lane < i1 && kind_of(g.ids[i + lane], g.L) == adapter));
+  if (lane == 0) s.sums[wid] = found;
+  __syncthreads();
+  int slot = -s.part * kRows;
+  for (int i = 0; i < wid; ++i) slot += s.sums[i];
+  for (int i = i0; i < i1; i += 32) {
+    const bool in = i + lane < i1 && kind_of(g.ids[i + lane], g.L) == adapter;
+    const unsigned who = __ballot_sync(0xffffffffu, in);
+    const int to = slot + __popc(who & ((1u << lane) - 1));
+    if (in && to >= 0 && to < kRows) rows[to] = i + lane;
+    slot += __popc(who);
   }
-  const bool leads = tid < g.n && before % kRows == 0;
-  const unsigned who = __ballot_sync(0xffffffffu, leads);
-  if (lane == 0) s.leaders[wid] = __popc(who);
   __syncthreads();
-  int number = __popc(who & ((1u << lane) - 1));
-  for (int i = 0; i < wid; ++i) number += s.leaders[i];
-  if (leads && number == want) {
-    s.at = tid;
-    s.count = before;
-    tile.adapter = kind;
-  }
-  __syncthreads();
-  const int at = s.at;
-  const bool in = at >= 0 && kind == s.kinds[max(at, 0)] && tid < g.n && before / kRows == s.count / kRows;
-  if (in) tile.rows[before % kRows] = tid;
-  const int c = __syncthreads_count(in);
-  if (tid == 0) tile.count = c;
-  if (tid < kRows && tid >= c) tile.rows[tid] = 0;
-  __syncthreads();
-  int all = 0;
-  for (int i = 0; i < kDownWarps; ++i) all += s.leaders[i];
   return all;
 }
 
 // ---------------------------------------------------------------- t = scale A y
 struct Down {
-  Tile tile;
   SelfPlan plan;
+  int32_t rows[kDownWarps][kRows];  // the tile's, a copy for each warp that finds it alone
   float t[kDownWarps][kRows][kDownRanks + 1];
   float squares[kDownWarps][kRows];
   float odd[kDownWarps][kRows];  // 0, or NaN where a row's input is not finite
@@ -244,8 +287,30 @@ struct Down {
   float factor[kRows];
 };
 
-// PARTS: bf16 parts of an input. VEC: 16-byte loads.
-template <bool XF32, int PARTS, bool VEC>
+// Eight inputs as they come from memory.
+template <bool F32>
+struct Raw {
+  uint4 v[F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const char* row, int k, int K) {
+    const uint4* p = reinterpret_cast<const uint4*>(row + (long long)k * (F32 ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < (F32 ? 2 : 1); ++i) v[i] = k < K ? __ldg(p + i) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void floats(float (&f)[8]) const {
+    if constexpr (F32) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        f[4 * i] = __uint_as_float(v[i].x), f[4 * i + 1] = __uint_as_float(v[i].y);
+        f[4 * i + 2] = __uint_as_float(v[i].z), f[4 * i + 3] = __uint_as_float(v[i].w);
+      }
+    } else {
+      unpack8(v[0], f);
+    }
+  }
+};
+
+// PARTS: bf16 parts of an input. VEC: 16-byte loads. GROUPS: of 8 ranks, 2 or 4.
+template <bool XF32, int PARTS, bool VEC, int GROUPS>
 __global__ void __launch_bounds__(kDownThreads) k_adapters_down(const AdapterArgs g, Head* head, Tile* tiles, uint8_t* t_out,
                                                                 int parts_out) {
   extern __shared__ __align__(16) unsigned char raw[];
@@ -253,56 +318,58 @@ __global__ void __launch_bounds__(kDownThreads) k_adapters_down(const AdapterArg
   pdl_release();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, gq = lane >> 2, q = lane & 3;
-  if (g.n <= kSelfPlan) {
-    const int all = self_plan(g, blockIdx.x, sh.plan, sh.tile);
-    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) head->tiles = all;
-    if (blockIdx.y == 0 && tid < 2 + kRows)
-      reinterpret_cast<int32_t*>(&tiles[blockIdx.x])[tid] = reinterpret_cast<const int32_t*>(&sh.tile)[tid];
+  const int32_t* rows = sh.rows[0];
+  int count, a, all = -1;
+  if (g.n <= 32) {
+    all = warp_plan(g, blockIdx.x, sh.rows[wid], a, count);
+    rows = sh.rows[wid];
+    __syncwarp();
+  } else if (g.n <= kSelfPlan) {
+    all = block_plan(g, blockIdx.x, sh.plan, reinterpret_cast<uint32_t*>(raw + sizeof(Down)), sh.rows[0], a, count);
   } else {
-    if (tid < 2 + kRows)
-      reinterpret_cast<int32_t*>(&sh.tile)[tid] = reinterpret_cast<const int32_t*>(&tiles[blockIdx.x])[tid];
+    const Tile& tile = tiles[blockIdx.x];
+    count = tile.count;
+    a = tile.adapter;
+    if (tid < kRows) sh.rows[0][tid] = tid < count ? tile.rows[tid] : 0;
     __syncthreads();
   }
-  const int count = sh.tile.count, a = sh.tile.adapter;
-  if (count <= 0) return;
-  if (a < 0) {
-    if (a == kBad && g.n <= kSelfPlan && blockIdx.y == 0 && tid == 0) report(g.d_status, DS_DEV_ERR_PARAM);
-    return;
+  if (all >= 0 && blockIdx.y == 0 && wid == 0) {
+    Tile& tile = tiles[blockIdx.x];
+    if (lane < kRows) tile.rows[lane] = rows[lane];
+    if (lane == 0) {
+      tile.adapter = a;
+      tile.count = count;
+      if (blockIdx.x == 0) head->tiles = all;
+      if (count > 0 && a == kBad) report(g.d_status, DS_DEV_ERR_PARAM);
+    }
   }
+  if (count <= 0 || a < 0) return;
   constexpr int kSize = XF32 ? 4 : 2;
   const char* x = static_cast<const char*>(g.x);
   const bool has0 = gq < count, has1 = gq + 8 < count;
-  const char* x0 = x + (has0 ? sh.tile.rows[gq] : 0) * g.ldx * kSize;
-  const char* x1 = x + (has1 ? sh.tile.rows[gq + 8] : 0) * g.ldx * kSize;
+  const char* x0 = x + rows[gq] * g.ldx * kSize;
+  const char* x1 = x + rows[gq + 8] * g.ldx * kSize;
+  const int K0 = has0 ? g.K : 0, K1 = has1 ? g.K : 0;
   const int rank0 = blockIdx.y * kDownRanks;
-  const int groups = min(kDownRanks, padded(g.R) - rank0) / 8;  // of 8 ranks: 2 or 4
   const uint16_t* w = g.a + ((long long)a * g.R + rank0) * g.K;
-
-  float d[4][4] = {};
-  float ss0 = 0.f, ss1 = 0.f, odd0 = 0.f, odd1 = 0.f;
-  // 32 inputs a step: lane q of a row's four takes 8 that lie together, four of them
-  // for each of two instructions
-#pragma unroll 2
-  for (int k0 = wid * 32; k0 < g.K; k0 += kDownWarps * 32) {
-    const int k = k0 + 8 * q;
-    float f0[8], f1[8];
-    load8<XF32, VEC>(x0, k, has0 ? g.K : 0, f0);
-    load8<XF32, VEC>(x1, k, has1 ? g.K : 0, f1);
-    uint32_t b[4][4];
+  const uint16_t* wr[GROUPS];
+  int Kw[GROUPS];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = 8 * j + gq;
-      const bool there = j < groups && rank0 + r < g.R;
-      load_weights<8, VEC>(w + (there ? (long long)r * g.K : 0), k, there ? g.K : 0, b[j]);
-    }
+  for (int j = 0; j < GROUPS; ++j) {
+    const int r = 8 * j + gq;
+    Kw[j] = rank0 + r < g.R ? g.K : 0;
+    wr[j] = w + (Kw[j] ? (long long)r * g.K : 0);
+  }
+
+  float d[GROUPS][4] = {};
+  float ss0 = 0.f, ss1 = 0.f, odd0 = 0.f, odd1 = 0.f;
+  auto take = [&](float (&f0)[8], float (&f1)[8], const float (&n8)[8], const uint32_t (&b)[GROUPS][4]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       odd0 = __fmaf_rn(f0[i], 0.f, odd0);
       odd1 = __fmaf_rn(f1[i], 0.f, odd1);
     }
     if (g.gain) {
-      float n8[8];
-      load8<true, VEC>(g.gain, k, g.K, n8);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         ss0 = __fmaf_rn(f0[i], f0[i], ss0);
@@ -329,12 +396,53 @@ __global__ void __launch_bounds__(kDownThreads) k_adapters_down(const AdapterArg
       for (int s = 0; s < 2; ++s) {
         const uint4 av = make_uint4(h0[2 * s], h1[2 * s], h0[2 * s + 1], h1[2 * s + 1]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma(d[j], av, b[j][2 * s], b[j][2 * s + 1]);
+        for (int j = 0; j < GROUPS; ++j) mma(d[j], av, b[j][2 * s], b[j][2 * s + 1]);
       }
+    }
+  };
+  // 32 inputs a step: lane q of a row's four takes 8 that lie together, four of them
+  // for each of two instructions
+  constexpr int kStep = kDownWarps * 32;
+  if constexpr (VEC) {
+    constexpr int kDepth = GROUPS == 2 && !XF32 ? 4 : 2;  // steps in flight
+    for (int k0 = wid * 32; k0 < g.K; k0 += kDepth * kStep) {
+      Raw<XF32> r0[kDepth], r1[kDepth];
+      Raw<true> rn[kDepth];
+      uint32_t b[kDepth][GROUPS][4];
+#pragma unroll
+      for (int i = 0; i < kDepth; ++i) {
+        const int k = k0 + i * kStep + 8 * q;
+        r0[i].load(x0, k, K0);
+        r1[i].load(x1, k, K1);
+#pragma unroll
+        for (int j = 0; j < GROUPS; ++j) load_weights<8, true>(wr[j], k, Kw[j], b[i][j]);
+        if (g.gain) rn[i].load(reinterpret_cast<const char*>(g.gain), k, g.K);
+      }
+#pragma unroll
+      for (int i = 0; i < kDepth; ++i) {
+        if (k0 + i * kStep >= g.K) break;
+        float f0[8], f1[8], n8[8];
+        r0[i].floats(f0);
+        r1[i].floats(f1);
+        rn[i].floats(n8);
+        take(f0, f1, n8, b[i]);
+      }
+    }
+  } else {
+    for (int k0 = wid * 32; k0 < g.K; k0 += kStep) {
+      const int k = k0 + 8 * q;
+      float f0[8], f1[8], n8[8];
+      uint32_t b[GROUPS][4];
+      load8<XF32, false>(x0, k, K0, f0);
+      load8<XF32, false>(x1, k, K1, f1);
+#pragma unroll
+      for (int j = 0; j < GROUPS; ++j) load_weights<8, false>(wr[j], k, Kw[j], b[j]);
+      load8<true, false>(g.gain, k, g.gain ? g.K : 0, n8);
+      take(f0, f1, n8, b);
     }
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < GROUPS; ++j) {
     sh.t[wid][gq][8 * j + 2 * q] = d[j][0];
     sh.t[wid][gq][8 * j + 2 * q + 1] = d[j][1];
     sh.t[wid][gq + 8][8 * j + 2 * q] = d[j][2];
@@ -354,46 +462,49 @@ __global__ void __launch_bounds__(kDownThreads) k_adapters_down(const AdapterArg
     sh.odd[wid][gq + 8] = odd1;
   }
   __syncthreads();
-  // each row's factor: scale, the norm's root, NaN for a row that is not finite
-  if (tid < kRows) {
-    float ss = 0.f, odd = 0.f;
-    for (int i = 0; i < kDownWarps; ++i) {
-      ss += sh.squares[i][tid];
-      odd += sh.odd[i][tid];
-    }
-    float f = 1.f;
-    if (g.gain) f = ss > 1e-25f && ss < 1e37f ? rsqrtf(ss / (float)g.K + g.eps) : -1.f;  // -1: below
-    sh.factor[tid] = odd != 0.f || odd != odd ? __int_as_float(0x7fffffff) : f;
-  }
-  __syncthreads();
-  if (g.gain) {
-    // squares that leave fp32's range, rows of zeros: the sum in 64 bits
-    for (int r = 0; r < count; ++r) {
-      if (sh.factor[r] != -1.f) continue;
-      const char* row = x + sh.tile.rows[r] * g.ldx * kSize;
-      double ss = 0;
-      for (int k = tid; k < g.K; k += kDownThreads) {
-        const double v = load<XF32>(row, k);
-        ss += v * v;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (lane == 0) sh.wide[wid] = ss;
-      __syncthreads();
-      ss = 0;
-      for (int i = 0; i < kDownWarps; ++i) ss += sh.wide[i];
-      __syncthreads();
-      if (tid == 0) sh.factor[r] = ss == 0 ? 0.f : (float)(1.0 / sqrt(ss / g.K + g.eps));
-    }
-    __syncthreads();
-  }
-  // a thread per row and rank
+  // a thread per row and rank; the row's factor is scale, the norm's root, NaN for a row
+  // that is not finite
   const int row = tid / kDownRanks, r = tid % kDownRanks, rank = rank0 + r;
-  if (r < groups * 8) {
-    float t = 0.f;
+  float t = 0.f, odd = 0.f, factor = 1.f;
+#pragma unroll
+  for (int i = 0; i < kDownWarps; ++i) odd += sh.odd[i][row];
+  if (r < GROUPS * 8)
 #pragma unroll
     for (int i = 0; i < kDownWarps; ++i) t += sh.t[i][row][r];
-    t = row < count ? t * (sh.factor[row] * g.scale[a]) : 0.f;
+  if (g.gain) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < kDownWarps; ++i) ss += sh.squares[i][row];
+    const bool usual = ss > 1e-25f && ss < 1e37f;
+    factor = rsqrtf(ss / (float)g.K + g.eps);
+    // squares that leave fp32's range, rows of zeros: the sum in 64 bits
+    if (__syncthreads_or(row < count && !usual && odd == 0.f)) {
+      if (r == 0) sh.factor[row] = row < count && !usual && odd == 0.f ? -1.f : factor;
+      __syncthreads();
+      for (int i = 0; i < count; ++i) {
+        if (sh.factor[i] != -1.f) continue;
+        const char* p = x + rows[i] * g.ldx * kSize;
+        double sum = 0;
+        for (int k = tid; k < g.K; k += kDownThreads) {
+          const double v = load<XF32>(p, k);
+          sum += v * v;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) sh.wide[wid] = sum;
+        __syncthreads();
+        sum = 0;
+        for (int j = 0; j < kDownWarps; ++j) sum += sh.wide[j];
+        __syncthreads();
+        if (tid == 0) sh.factor[i] = sum == 0 ? 0.f : (float)(1.0 / sqrt(sum / g.K + g.eps));
+      }
+      __syncthreads();
+      factor = sh.factor[row];
+    }
+  }
+  if (odd != 0.f || odd != odd) factor = __int_as_float(0x7fffffff);
+  if (r < GROUPS * 8) {
+    t = row < count ? t * (factor * g.scale[a]) : 0.f;
     // which step, lane and place holds this rank
     const int rp = padded(g.R);
     const int step = rp == 16 ? 0 : 2 * (rank / 32) + (rank >> 2) % 2, qt = rp == 16 ? rank / 4 : (rank % 32) / 8, e = rank % 4;
@@ -421,7 +532,8 @@ struct Up {
   static constexpr int kWeights = (kChannels + kFront) * RP * 2 + 32;
   static constexpr int kStage = kWeights + kRows * kChunks * 16;
   static constexpr int kResults = kRows * kPitch * 4;
-  static constexpr int kStages = 4 * kStage + kResults <= 110 * 1024 ? 4 : 3;
+  static constexpr int kCtas = RP == 16 ? 3 : 2;                 // of an SM
+  static constexpr int kStages = kCtas * (4 * kStage + kResults) <= 220 * 1024 ? 4 : 3;
   static constexpr int kSmem = kStages * kStage + kResults;
 };
 
@@ -460,7 +572,7 @@ __device__ __forceinline__ void shared_weights(const unsigned char* row, int i, 
 // VEC: a lane's weights in one load. NEAR: base and result rows lie the same way to
 // 16 bytes. SHIFT: some row starts between two chunks.
 template <bool F32, int RP, bool VEC, bool NEAR, bool SHIFT>
-__global__ void __launch_bounds__(kUpThreads, 2)
+__global__ void __launch_bounds__(kUpThreads, RP == 16 ? 3 : 2)
     k_adapters_up(const AdapterArgs g, const Head* head, const Tile* tiles, const uint8_t* t_in, int blocks) {
   using U = Up<F32, RP, SHIFT>;
   constexpr int E = U::E, kSize = F32 ? 4 : 2, PARTS = F32 ? 3 : 2, STEPS = RP / 16, S = U::kStages, W = U::kChunks;
@@ -728,30 +840,41 @@ bool allow_smem(K kern, int bytes) {
          }) == 1;
 }
 
-template <bool XF32, int PARTS, bool VEC>
+template <bool XF32, int PARTS, bool VEC, int GROUPS>
 cudaError_t launch_down(const AdapterArgs& g, long long most, Head* head, Tile* tiles, uint8_t* t, int parts, cudaStream_t st) {
-  auto kern = k_adapters_down<XF32, PARTS, VEC>;
-  if (!allow_smem(kern, (int)sizeof(Down))) return cudaErrorUnknown;
+  auto kern = k_adapters_down<XF32, PARTS, VEC, GROUPS>;
+  if (!allow_smem(kern, (int)sizeof(Down) + (DS_ADAPTERS_MAX + 2) * 4)) return cudaErrorUnknown;
   cudaLaunchAttribute attr;
   const dim3 grid((unsigned)most, (unsigned)((padded(g.R) + kDownRanks - 1) / kDownRanks), 1);
-  const cudaLaunchConfig_t cfg = config(grid, kDownThreads, sizeof(Down), st, &attr);
+  const size_t smem = sizeof(Down) + (g.n > 32 && g.n <= kSelfPlan ? (g.L + 2) * 4 : 0);
+  const cudaLaunchConfig_t cfg = config(grid, kDownThreads, smem, st, &attr);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, g, head, tiles, t, parts);
   if (e == cudaSuccess) note_launch();
   return e;
+}
+template <bool XF32, int PARTS>
+cudaError_t launch_down_as(const AdapterArgs& g, bool vec, long long most, Head* head, Tile* tiles, uint8_t* t, int parts,
+                           cudaStream_t st) {
+  if (g.R <= 16)
+    return vec ? launch_down<XF32, PARTS, true, 2>(g, most, head, tiles, t, parts, st)
+               : launch_down<XF32, PARTS, false, 2>(g, most, head, tiles, t, parts, st);
+  return vec ? launch_down<XF32, PARTS, true, 4>(g, most, head, tiles, t, parts, st)
+             : launch_down<XF32, PARTS, false, 4>(g, most, head, tiles, t, parts, st);
 }
 
 template <bool F32, int RP, bool VEC, bool NEAR, bool SHIFT>
 cudaError_t launch_up(const AdapterArgs& g, long long most, const Head* head, const Tile* tiles, const uint8_t* t,
                       cudaStream_t st) {
   using U = Up<F32, RP, SHIFT>;
-  static_assert(2 * U::kSmem <= 227 * 1024, "two CTAs an SM");
+  static_assert(U::kCtas * (U::kSmem + 1024) <= 228 * 1024, "CTAs an SM");
   auto kern = k_adapters_up<F32, RP, VEC, NEAR, SHIFT>;
   const int sms = device_sms();
   if (sms <= 0 || !allow_smem(kern, U::kSmem)) return cudaErrorUnknown;
   cudaLaunchAttribute attr;
   const long long blocks = ((long long)g.N + (SHIFT ? U::E - 1 : 0) + U::kChannels - 1) / U::kChannels;
   const long long items = most * blocks;
-  const dim3 grid((unsigned)(items < 2LL * sms ? items : 2LL * sms), 1, 1);
+  const long long ctas = (long long)U::kCtas * sms;
+  const dim3 grid((unsigned)(items < ctas ? items : ctas), 1, 1);
   const cudaLaunchConfig_t cfg = config(grid, kUpThreads, U::kSmem, st, &attr);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, g, head, tiles, t, (int)blocks);
   if (e == cudaSuccess) note_launch();
@@ -802,9 +925,7 @@ cudaError_t launch_add_adapters(const AdapterArgs& g, bool x_f32, bool f32, cuda
   const auto at16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
   const int xs = x_f32 ? 4 : 2, s = f32 ? 4 : 2, parts = f32 ? 3 : 2;
   const bool x_vec = at16(g.x) && at16(g.a) && at16(g.gain) && g.K % 8 == 0 && g.ldx * xs % 16 == 0;
-#define DS_DOWN(XF32, PARTS)                                                                \
-  (x_vec ? launch_down<XF32, PARTS, true>(g, most, head, tiles, t, parts, st)               \
-         : launch_down<XF32, PARTS, false>(g, most, head, tiles, t, parts, st))
+#define DS_DOWN(XF32, PARTS) launch_down_as<XF32, PARTS>(g, x_vec, most, head, tiles, t, parts, st)
   if (!x_f32 && !g.gain)  // the inputs are bf16 themselves
     e = DS_DOWN(false, 1);
   else if (x_f32)
