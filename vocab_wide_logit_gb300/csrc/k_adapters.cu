@@ -209,67 +209,125 @@ __device__ __forceinline__ int warp_plan(const AdapterArgs& g, int want, int32_t
 
 // Up to 8192 rows: the same by a CTA, the tiles in the order of the adapters, then those
 // without one, then the bad ones.
+constexpr int kFewKinds = 32;  // a lane each
 struct SelfPlan {
   int sums[kDownWarps];
-  int adapter, part, count, all;
+  int adapter, part, count;
+  int few[kDownWarps][kFewKinds];  // rows of each kind in each warp's stretch
 };
 __device__ __forceinline__ int block_plan(const AdapterArgs& g, int want, SelfPlan& s, uint32_t* counts, int32_t* rows, int& adapter,
                                           int& count) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, kinds = g.L + 2;
-  for (int i = tid; i < kinds; i += kDownThreads) counts[i] = 0;
-  if (tid == 0) s.count = 0;
-  if (tid < kRows) rows[tid] = 0;
-  __syncthreads();
-  for (int i0 = wid * 32; i0 < g.n; i0 += kDownThreads) {
-    const int a = i0 + lane < g.n ? kind_of(g.ids[i0 + lane], g.L) : kBad - 1;
-    const unsigned same = __match_any_sync(0xffffffffu, a);
-    if (a > kBad - 1 && (same & ((1u << lane) - 1)) == 0) atomicAdd(&counts[a >= 0 ? a : g.L - 1 - a], (uint32_t)__popc(same));
-  }
-  __syncthreads();
-  const int per = (kinds + kDownThreads - 1) / kDownThreads, lo = tid * per, hi = min(lo + per, kinds);
-  int mine = 0;
-  for (int i = lo; i < hi; ++i) mine += (int)((counts[i] + kRows - 1) / kRows);
-  int incl = mine;
+  // a stretch of rows to each warp, 32 at a time
+  constexpr int kTimes = kSelfPlan / kDownThreads;
+  const int times = (g.n + kDownThreads - 1) / kDownThreads, i0 = wid * times * 32 + lane;
+  int kind[kTimes];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) s.sums[wid] = incl;
-  __syncthreads();
-  int at = incl - mine, all = 0;
-  for (int i = 0; i < kDownWarps; ++i) {
-    at += i < wid ? s.sums[i] : 0;
-    all += s.sums[i];
-  }
-  if (want >= at && want < at + mine)
-    for (int i = lo; i < hi; ++i) {
-      const int t = (int)((counts[i] + kRows - 1) / kRows);
-      if (want >= at && want < at + t) {
-        s.adapter = i < g.L ? i : g.L - 1 - i;
-        s.part = want - at;
-        s.count = min(kRows, (int)counts[i] - s.part * kRows);
-      }
-      at += t;
+  for (int i = 0; i < kTimes; ++i) kind[i] = i < times && i0 + 32 * i < g.n ? g.ids[i0 + 32 * i] : 0;
+  if (tid < kRows) rows[tid] = 0;
+  auto index_of = [&](int kind) { return kind >= 0 ? kind : g.L - 1 - kind; };
+#pragma unroll
+  for (int i = 0; i < kTimes; ++i)
+    if (i < times) kind[i] = i0 + 32 * i < g.n ? kind_of(kind[i], g.L) : kBad - 1;
+  int all = 0, slot;  // slot: the place in the tile of the warp's first row of the kind
+  if (kinds <= kFewKinds) {
+    s.few[wid][lane] = 0;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kTimes; ++i) {
+      if (i >= times) break;
+      const unsigned same = __match_any_sync(0xffffffffu, kind[i]);
+      if (kind[i] >= kBad && (same & ((1u << lane) - 1)) == 0) s.few[wid][index_of(kind[i])] += __popc(same);
+      __syncwarp();
     }
-  __syncthreads();
-  adapter = s.adapter;
-  count = s.count;
-  if (count == 0) return all;
-  // its rows, a stretch of rows to each warp
-  const int stretch = (g.n + kDownThreads - 1) / kDownThreads * 32, i0 = wid * stretch, i1 = min(i0 + stretch, g.n);
-  int found = 0;
-  for (int i = i0; i < i1; i += 32)
-    found += __popc(__ballot_sync(0xffffffffu, i + lane < i1 && kind_of(g.ids[i + lane], g.L) == adapter));
-  if (lane == 0) s.sums[wid] = found;
-  __syncthreads();
-  int slot = -s.part * kRows;
-  for (int i = 0; i < wid; ++i) slot += s.sums[i];
-  for (int i = i0; i < i1; i += 32) {
-    const bool in = i + lane < i1 && kind_of(g.ids[i + lane], g.L) == adapter;
+    __syncthreads();
+    // every warp finds the tile for itself, a kind a lane
+    int rows_of = 0, before = 0;
+#pragma unroll
+    for (int i = 0; i < kDownWarps; ++i) {
+      const int c = s.few[i][lane];
+      rows_of += c;
+      before += i < wid ? c : 0;
+    }
+    const int mine = (rows_of + kRows - 1) / kRows;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    all = __shfl_sync(0xffffffffu, incl, 31);
+    const unsigned who = __ballot_sync(0xffffffffu, want >= incl - mine && want < incl);
+    if (!who) {
+      count = 0;
+      adapter = kNone;
+      return all;
+    }
+    const int owner = __ffs(who) - 1;
+    const int part = want - __shfl_sync(0xffffffffu, incl - mine, owner);
+    adapter = owner < g.L ? owner : g.L - 1 - owner;
+    count = min(kRows, __shfl_sync(0xffffffffu, rows_of, owner) - part * kRows);
+    slot = __shfl_sync(0xffffffffu, before, owner) - part * kRows;
+  } else {
+    for (int i = tid; i < kinds; i += kDownThreads) counts[i] = 0;
+    if (tid == 0) s.count = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kTimes; ++i) {
+      if (i >= times) break;
+      const unsigned same = __match_any_sync(0xffffffffu, kind[i]);
+      if (kind[i] >= kBad && (same & ((1u << lane) - 1)) == 0) atomicAdd(&counts[index_of(kind[i])], (uint32_t)__popc(same));
+    }
+    __syncthreads();
+    const int per = (kinds + kDownThreads - 1) / kDownThreads, lo = tid * per, hi = min(lo + per, kinds);
+    int mine = 0;
+    for (int i = lo; i < hi; ++i) mine += (int)((counts[i] + kRows - 1) / kRows);
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) s.sums[wid] = incl;
+    __syncthreads();
+    int at = incl - mine;
+    for (int i = 0; i < kDownWarps; ++i) {
+      at += i < wid ? s.sums[i] : 0;
+      all += s.sums[i];
+    }
+    if (want >= at && want < at + mine)
+      for (int i = lo; i < hi; ++i) {
+        const int t = (int)((counts[i] + kRows - 1) / kRows);
+        if (want >= at && want < at + t) {
+          s.adapter = i < g.L ? i : g.L - 1 - i;
+          s.part = want - at;
+          s.count = min(kRows, (int)counts[i] - s.part * kRows);
+        }
+        at += t;
+      }
+    __syncthreads();
+    adapter = s.adapter;
+    count = s.count;
+    if (count == 0) return all;
+    int found = 0;
+#pragma unroll
+    for (int i = 0; i < kTimes; ++i) {
+      if (i >= times) break;
+      found += __popc(__ballot_sync(0xffffffffu, kind[i] == adapter));
+    }
+    if (lane == 0) s.sums[wid] = found;
+    __syncthreads();
+    slot = -s.part * kRows;
+    for (int i = 0; i < wid; ++i) slot += s.sums[i];
+  }
+  __syncthreads();  // rows[] is zero
+#pragma unroll
+  for (int i = 0; i < kTimes; ++i) {
+    if (i >= times) break;
+    const bool in = kind[i] == adapter;
     const unsigned who = __ballot_sync(0xffffffffu, in);
     const int to = slot + __popc(who & ((1u << lane) - 1));
-    if (in && to >= 0 && to < kRows) rows[to] = i + lane;
+    if (in && to >= 0 && to < kRows) rows[to] = i0 + 32 * i;
     slot += __popc(who);
   }
   __syncthreads();
@@ -282,7 +340,6 @@ struct Down {
   int32_t rows[kDownWarps][kRows];  // the tile's, a copy for each warp that finds it alone
   float t[kDownWarps][kRows][kDownRanks + 1];
   float squares[kDownWarps][kRows];
-  float odd[kDownWarps][kRows];  // 0, or NaN where a row's input is not finite
   double wide[kDownWarps];
   float factor[kRows];
 };
@@ -362,36 +419,38 @@ __global__ void __launch_bounds__(kDownThreads) k_adapters_down(const AdapterArg
   }
 
   float d[GROUPS][4] = {};
-  float ss0 = 0.f, ss1 = 0.f, odd0 = 0.f, odd1 = 0.f;
+  float ss0 = 0.f, ss1 = 0.f;
+  const bool half = count <= 8;
   auto take = [&](float (&f0)[8], float (&f1)[8], const float (&n8)[8], const uint32_t (&b)[GROUPS][4]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      odd0 = __fmaf_rn(f0[i], 0.f, odd0);
-      odd1 = __fmaf_rn(f1[i], 0.f, odd1);
-    }
     if (g.gain) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         ss0 = __fmaf_rn(f0[i], f0[i], ss0);
-        ss1 = __fmaf_rn(f1[i], f1[i], ss1);
         f0[i] *= n8[i];
-        f1[i] *= n8[i];
+      }
+      if (!half) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          ss1 = __fmaf_rn(f1[i], f1[i], ss1);
+          f1[i] *= n8[i];
+        }
       }
     }
 #pragma unroll
     for (int p = 0; p < PARTS; ++p) {
-      uint32_t h0[4], h1[4];
+      uint32_t h0[4], h1[4] = {0, 0, 0, 0};
+      auto part = [&](float (&f)[8], uint32_t (&h)[4]) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        h0[i] = pack_bf(f0[2 * i], f0[2 * i + 1]);
-        h1[i] = pack_bf(f1[2 * i], f1[2 * i + 1]);
-        if (p + 1 < PARTS) {
-          f0[2 * i] -= bf_lo(h0[i]);
-          f0[2 * i + 1] -= bf_hi(h0[i]);
-          f1[2 * i] -= bf_lo(h1[i]);
-          f1[2 * i + 1] -= bf_hi(h1[i]);
+        for (int i = 0; i < 4; ++i) {
+          h[i] = pack_bf(f[2 * i], f[2 * i + 1]);
+          if (p + 1 < PARTS) {
+            f[2 * i] -= bf_lo(h[i]);
+            f[2 * i + 1] -= bf_hi(h[i]);
+          }
         }
-      }
+      };
+      part(f0, h0);
+      if (!half) part(f1, h1);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const uint4 av = make_uint4(h0[2 * s], h1[2 * s], h0[2 * s + 1], h1[2 * s + 1]);
@@ -452,22 +511,15 @@ __global__ void __launch_bounds__(kDownThreads) k_adapters_down(const AdapterArg
   for (int o = 1; o < 4; o <<= 1) {
     ss0 += __shfl_xor_sync(0xffffffffu, ss0, o);
     ss1 += __shfl_xor_sync(0xffffffffu, ss1, o);
-    odd0 += __shfl_xor_sync(0xffffffffu, odd0, o);
-    odd1 += __shfl_xor_sync(0xffffffffu, odd1, o);
   }
   if (q == 0) {
     sh.squares[wid][gq] = ss0;
     sh.squares[wid][gq + 8] = ss1;
-    sh.odd[wid][gq] = odd0;
-    sh.odd[wid][gq + 8] = odd1;
   }
   __syncthreads();
-  // a thread per row and rank; the row's factor is scale, the norm's root, NaN for a row
-  // that is not finite
+  // a thread per row and rank; the row's factor is scale and the norm's root
   const int row = tid / kDownRanks, r = tid % kDownRanks, rank = rank0 + r;
-  float t = 0.f, odd = 0.f, factor = 1.f;
-#pragma unroll
-  for (int i = 0; i < kDownWarps; ++i) odd += sh.odd[i][row];
+  float t = 0.f, factor = 1.f;
   if (r < GROUPS * 8)
 #pragma unroll
     for (int i = 0; i < kDownWarps; ++i) t += sh.t[i][row][r];
@@ -478,8 +530,8 @@ __global__ void __launch_bounds__(kDownThreads) k_adapters_down(const AdapterArg
     const bool usual = ss > 1e-25f && ss < 1e37f;
     factor = rsqrtf(ss / (float)g.K + g.eps);
     // squares that leave fp32's range, rows of zeros: the sum in 64 bits
-    if (__syncthreads_or(row < count && !usual && odd == 0.f)) {
-      if (r == 0) sh.factor[row] = row < count && !usual && odd == 0.f ? -1.f : factor;
+    if (__syncthreads_or(row < count && !usual)) {
+      if (r == 0) sh.factor[row] = row < count && !usual ? -1.f : factor;
       __syncthreads();
       for (int i = 0; i < count; ++i) {
         if (sh.factor[i] != -1.f) continue;
@@ -502,8 +554,9 @@ __global__ void __launch_bounds__(kDownThreads) k_adapters_down(const AdapterArg
       factor = sh.factor[row];
     }
   }
-  if (odd != 0.f || odd != odd) factor = __int_as_float(0x7fffffff);
   if (r < GROUPS * 8) {
+    // an infinity or NaN in x is in every t of its row, whatever the weights
+    if (!(fabsf(t) < kInf)) t = __int_as_float(0x7fffffff);
     t = row < count ? t * (factor * g.scale[a]) : 0.f;
     // which step, lane and place holds this rank
     const int rp = padded(g.R);
@@ -523,16 +576,22 @@ __global__ void __launch_bounds__(kDownThreads) k_adapters_down(const AdapterArg
 template <bool F32, int RP, bool SHIFT>
 struct Up {
   static constexpr int E = F32 ? 4 : 8;                          // logits of a chunk
-  static constexpr int kChunks = (F32 ? RP <= 64 : RP <= 32) ? 32 : F32 || RP <= 64 ? 16 : 8;  // of a row and block
+  static constexpr int kChunks = RP == 16 && (F32 || !SHIFT) ? 64 : (F32 ? RP <= 64 : RP <= 32) ? 32 : F32 || RP <= 64 ? 16 : 8;  // of a row and block
   static constexpr int kChannels = kChunks * E;                  // of a block
   static constexpr int kGroups = kChannels / 8;                  // of 8 channels
   static constexpr int kFront = SHIFT ? 8 : 0;                   // channels in front of the block
+  // Channels of a warp and block: 8 columns of as many instructions. Where two of each
+  // make whole chunks a lane and rows start on chunks, sums go straight from the lane that
+  // has them to the result; else through shared memory.
+  static constexpr int kMine = kGroups / 8;
+  static constexpr int kPieces = 2 * kMine / E;                  // chunks of a lane
+  static constexpr bool kDirect = !SHIFT && kPieces > 0;
   static constexpr int kPitch = kChannels + 8;                   // rows of results lie 8 banks apart
   // weights that may start at any 2 bytes, and base
   static constexpr int kWeights = (kChannels + kFront) * RP * 2 + 32;
   static constexpr int kStage = kWeights + kRows * kChunks * 16;
-  static constexpr int kResults = kRows * kPitch * 4;
-  static constexpr int kCtas = RP == 16 ? 3 : 2;                 // of an SM
+  static constexpr int kResults = kDirect ? 0 : kRows * kPitch * 4;
+  static constexpr int kCtas = RP == 16 && kChunks == 32 ? 3 : 2;  // of an SM
   static constexpr int kStages = kCtas * (4 * kStage + kResults) <= 220 * 1024 ? 4 : 3;
   static constexpr int kSmem = kStages * kStage + kResults;
 };
@@ -572,20 +631,26 @@ __device__ __forceinline__ void shared_weights(const unsigned char* row, int i, 
 // VEC: a lane's weights in one load. NEAR: base and result rows lie the same way to
 // 16 bytes. SHIFT: some row starts between two chunks.
 template <bool F32, int RP, bool VEC, bool NEAR, bool SHIFT>
-__global__ void __launch_bounds__(kUpThreads, RP == 16 ? 3 : 2)
+__global__ void __launch_bounds__(kUpThreads, (Up<F32, RP, SHIFT>::kCtas))
     k_adapters_up(const AdapterArgs g, const Head* head, const Tile* tiles, const uint8_t* t_in, int blocks) {
   using U = Up<F32, RP, SHIFT>;
   constexpr int E = U::E, kSize = F32 ? 4 : 2, PARTS = F32 ? 3 : 2, STEPS = RP / 16, S = U::kStages, W = U::kChunks;
   constexpr int kLoad = RP == 16 ? 4 : 8;  // weights of a lane and load: one instruction's, or two's
   constexpr int kTurns = (kRows * W + kUpThreads - 1) / kUpThreads;
   extern __shared__ __align__(16) unsigned char smem[];
-  float* results = reinterpret_cast<float*>(smem + S * U::kStage);
+  float* results = reinterpret_cast<float*>(smem + S * U::kStage);  // without kDirect
   const uint32_t smem_at = (uint32_t)__cvta_generic_to_shared(smem);
   pdl_release();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, gq = lane >> 2, q = lane & 3;
+  // this CTA's share: total / grid blocks, one more for the first ones
   const long long total = (long long)head->tiles * blocks;
-  const long long lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+  const bool few = total <= 0x7fffffffLL;  // 64-bit quotients take 100 ns each
+  const long long share = few ? (uint32_t)total / gridDim.x : total / gridDim.x;
+  const int more = (int)(total - share * gridDim.x);
+  const long long lo = share * blockIdx.x + min((int)blockIdx.x, more), hi = lo + share + ((int)blockIdx.x < more);
+  const int first_tile = few ? (int)((uint32_t)lo / (uint32_t)blocks) : (int)(lo / blocks);
+  const int first_block = (int)(lo - (long long)first_tile * blocks);
   char* out = static_cast<char*>(g.out);
   const char* base = static_cast<const char*>(g.base);
   // how many logits of a row's first chunk are before it
@@ -607,8 +672,8 @@ __global__ void __launch_bounds__(kUpThreads, RP == 16 ? 3 : 2)
     int shift[kTurns];
   } ask;
   ask.tile = -1;
-  int ask_at = (int)(lo / blocks);
-  ask.block = (int)(lo % blocks);
+  int ask_at = first_tile;
+  ask.block = first_block;
   long long asked = lo;
   auto issue = [&](int stage) {
     if (asked < hi) {
@@ -654,10 +719,12 @@ __global__ void __launch_bounds__(kUpThreads, RP == 16 ? 3 : 2)
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) issue(i);
 
-  int at = (int)(lo / blocks), block = (int)(lo % blocks), stage = 0, ready = -1;
+  int at = first_tile, block = first_block, stage = 0, ready = -1;
   int count = 0, a = kNone, dc0 = 0, dc1 = 0;
   bool idle = true;
   const char* weights = nullptr;
+  constexpr int kMine = U::kMine;
+  char* to_direct[2];  // kDirect: this lane's channels of block 0 in its two rows
   char* to_out[kTurns];
   const char* from_base[kTurns];  // without NEAR
   int shift[kTurns];
@@ -675,8 +742,15 @@ __global__ void __launch_bounds__(kUpThreads, RP == 16 ? 3 : 2)
       idle = a == kNone && g.out == g.base;
       weights = reinterpret_cast<const char*>(g.b) + (long long)max(a, 0) * g.N * row_bytes;
       t4 = reinterpret_cast<const uint4*>(t_in + at * t_bytes(g.R)) + lane;
+      if constexpr (U::kDirect) {
 #pragma unroll
-      for (int k = 0; k < kTurns; ++k) {
+        for (int k = 0; k < 2; ++k) {
+          const long long row = gq + 8 * k < count ? tile.rows[gq + 8 * k] : 0;
+          to_direct[k] = out + (row * g.ldo + 8 * kMine * wid + 2 * kMine * q) * kSize;
+        }
+      }
+#pragma unroll
+      for (int k = 0; !U::kDirect && k < kTurns; ++k) {
         const int r = my_row + kPerTurn * k;
         const long long row = r < count ? tile.rows[r] : 0;
         shift[k] = shift_of(row);
@@ -696,6 +770,78 @@ __global__ void __launch_bounds__(kUpThreads, RP == 16 ? 3 : 2)
     }
     const int c0 = block * U::kChannels, left = g.N - c0;  // channels from here on
     const unsigned char* here = smem + stage * U::kStage;
+    if constexpr (U::kDirect) {
+      if (!idle) {
+        // instruction j's column n is channel 2 kMine (n / 2) + 2 j + n % 2 of the warp's: a lane's
+        // two columns of all of them lie together
+        float d[kMine][4] = {};
+        if (a >= 0) {
+          const int first = 8 * kMine * wid + 2 * kMine * (gq >> 1) + (gq & 1);
+          const unsigned char* w = here + (int)((reinterpret_cast<uintptr_t>(weights) + (long long)c0 * row_bytes) & 15) +
+                                   first * row_bytes;
+#pragma unroll
+          for (int j = 0; j < kMine; ++j) {
+            const bool there = left >= U::kChannels || first + 2 * j < left;
+            const unsigned char* row = w + (there ? 2 * j * row_bytes : 0);
+#pragma unroll
+            for (int h = 0; h < RP / (4 * kLoad); ++h) {
+              uint32_t b[kLoad / 2];
+              shared_weights<kLoad, VEC>(row, 4 * kLoad * h + kLoad * q, there ? g.R : 0, b);
+#pragma unroll
+              for (int i = 0; i < kLoad / 4; ++i)
+#pragma unroll
+                for (int p = PARTS - 1; p >= 0; --p) mma(d[j], t[h * (kLoad / 4) + i][p], b[2 * i], b[2 * i + 1]);
+            }
+          }
+        }
+        const int id0 = c0 + 8 * kMine * wid + 2 * kMine * q;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (gq + 8 * k >= count) break;
+          const unsigned char* from = here + U::kWeights + 16 * ((gq + 8 * k) * W + U::kPieces * (4 * wid + q));
+          char* o = to_direct[k] + (long long)c0 * kSize;
+#pragma unroll
+          for (int c = 0; c < U::kPieces; ++c) {
+            const int id = id0 + c * E;
+            if (id >= g.N) break;
+            uint4 z = *reinterpret_cast<const uint4*>(from + 16 * c);
+            if (a == kBad) {
+              const uint32_t nan = F32 ? 0x7fffffffu : 0x7fff7fffu;
+              z = make_uint4(nan, nan, nan, nan);
+            } else if (a >= 0) {
+              uint32_t f[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+              for (int j = 0; j < E / 2; ++j) {
+                const float* s = &d[c * (E / 2) + j][2 * k];
+                if constexpr (F32) {
+                  f[2 * j] = __float_as_uint(__uint_as_float(f[2 * j]) + s[0]);
+                  f[2 * j + 1] = __float_as_uint(__uint_as_float(f[2 * j + 1]) + s[1]);
+                } else {
+                  f[j] = pack_bf(bf_lo(f[j]) + s[0], bf_hi(f[j]) + s[1]);
+                }
+              }
+              z = make_uint4(f[0], f[1], f[2], f[3]);
+            }
+            if (g.N - id >= E) {
+              st16(o + 16 * c, z);
+            } else {  // the end of a row
+              const uint32_t w4[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+              for (int e = 0; e < E; ++e) {
+                if (e >= g.N - id) break;
+                if constexpr (F32)
+                  reinterpret_cast<uint32_t*>(o + 16 * c)[e] = w4[e];
+                else
+                  reinterpret_cast<uint16_t*>(o + 16 * c)[e] = (uint16_t)(w4[e >> 1] >> (16 * (e & 1)));
+              }
+            }
+          }
+        }
+      }
+      if (++block == blocks) block = 0, ++at;
+      if (++stage == S) stage = 0;
+      continue;
+    }
     if (a >= 0) {
       const int f = front(block);
       const unsigned char* w = here + (int)((reinterpret_cast<uintptr_t>(weights) + (long long)(c0 - f) * row_bytes) & 15) +
@@ -740,7 +886,6 @@ __global__ void __launch_bounds__(kUpThreads, RP == 16 ? 3 : 2)
           }
         }
       };
-      constexpr int kMine = U::kGroups / 8;  // groups of a warp
       static_assert(U::kGroups % 8 == 0, "the same number for each");
       float d[kMine][4];
       if (left >= U::kChannels) {
