@@ -185,7 +185,19 @@ PyObject* head(PyObject*, PyObject* const* v, Py_ssize_t count) {
   END_HANDLE_TH_ERRORS
 }
 
-// score(logits, tokens, top) -> (logprobs, lse, entropy, ranks, top ids, top logprobs)
+// A contiguous tensor [n] or [n][columns] of 4-byte elements within the memory of another: a quarter of what an
+// allocation takes.
+at::Tensor within(const at::Tensor& memory, int64_t first, at::ScalarType type, int64_t n, int64_t columns = -1) {
+  auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(memory.storage()), memory.key_set(),
+                                                   c10::scalarTypeToTypeMeta(type));
+  impl->set_storage_offset(first);
+  const int64_t sizes[2] = {n, columns};
+  impl->set_sizes_contiguous(c10::IntArrayRef(sizes, columns < 0 ? 1 : 2));
+  return at::Tensor(std::move(impl));
+}
+
+// score(logits, tokens, top) -> (logprobs, lse, entropy, ranks, top ids, top logprobs); the first four share their
+// memory, and the last two, so that a program that keeps the former does not keep the latter
 PyObject* score(PyObject*, PyObject* const* v, Py_ssize_t count) {
   HANDLE_TH_ERRORS
   Rows x;
@@ -200,9 +212,11 @@ PyObject* score(PyObject*, PyObject* const* v, Py_ssize_t count) {
     PyErr_Clear();
     Py_RETURN_NONE;
   }
-  const at::TensorOptions f = on(x.device, at::kFloat), i = on(x.device, at::kInt);
-  at::Tensor r[6] = {at::empty({x.n}, f), at::empty({x.n}, f),      at::empty({x.n}, f),
-                     at::empty({x.n}, i), at::empty({x.n, top}, i), at::empty({x.n, top}, f)};
+  const at::Tensor four = at::empty({4 * x.n}, on(x.device, at::kFloat));
+  const at::Tensor two = top > 0 ? at::empty({2 * x.n * top}, on(x.device, at::kInt)) : four;
+  at::Tensor r[6] = {within(four, 0, at::kFloat, x.n),       within(four, x.n, at::kFloat, x.n),
+                     within(four, 2 * x.n, at::kFloat, x.n), within(four, 3 * x.n, at::kInt, x.n),
+                     within(two, 0, at::kInt, x.n, top),     within(two, top > 0 ? x.n * top : 0, at::kFloat, x.n, top)};
   const ds_status rc = p_score(x.p, c, (int32_t)x.n, (int32_t)x.k, x.ld, (const int32_t*)tokens, (int32_t)top,
                                (float*)r[0].data_ptr(), (float*)r[1].data_ptr(), (float*)r[2].data_ptr(),
                                (int32_t*)r[3].data_ptr(), (int32_t*)r[4].data_ptr(), (float*)r[5].data_ptr(), nullptr,
