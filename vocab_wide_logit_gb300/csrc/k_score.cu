@@ -312,8 +312,9 @@ __device__ __forceinline__ bool is_none(const Sums& r) { return !(r.s < kInf) ||
 // Rows of up to 32 C chunks, held in registers: 700 instructions for 1025 bf16
 // logits and 8 alternatives.
 constexpr int kWarps = 4;
-constexpr int kWarpList = 256;  // candidates a row may list: 32 lanes' chunks of 8
-constexpr int kWarpTop = 32;    // alternatives: a lane's maximum each
+constexpr int kWarpTop = 32;    // alternatives that are bounded by a lane's maximum each; more by a chunk's
+// Candidates a row may list: that many chunks of 8.
+__host__ __device__ constexpr int warp_list(bool many) { return 8 * (many ? DS_SCORE_MAX_TOP : kWarpTop); }
 constexpr int kLongList = 64;   // entries from which the exact cut is cheaper than ranking all
 
 // The top-th largest of n unique keys.
@@ -367,7 +368,7 @@ __device__ __forceinline__ float pick(const uint4& v, int i) {
 // The first `top` of a row, listed in no order, when its order puts the largest
 // into few lanes: the exact cut, then the list, from memory. Returns how many.
 template <bool F32>
-__device__ __noinline__ int warp_list_exact(const Row<F32> x, int V, int top, u64* list) {
+__device__ __noinline__ int warp_list_exact(const Row<F32> x, int V, int top, u64* list, int size) {
   const int lane = threadIdx.x & 31;
   u64 cut = 0;
   for (int bit = 63; bit >= 0; --bit) {
@@ -384,16 +385,32 @@ __device__ __noinline__ int warp_list_exact(const Row<F32> x, int V, int top, u6
     const bool in = o != 0 && o >= cut;
     const unsigned who = __ballot_sync(0xffffffffu, in);
     const int pos = listed + __popc(who & ((1u << lane) - 1));
-    if (in && pos < kWarpList) list[pos] = o;
+    if (in && pos < size) list[pos] = o;
     listed += __popc(who);
   }
   __syncwarp();
-  return min(listed, kWarpList);
+  return min(listed, size);
 }
 
-template <bool F32, int C>
+// Leaves of n listed keys those at or above the cut, in their order. Returns how many.
+__device__ __forceinline__ int warp_keep(u64* list, int n, u64 cut) {
+  const int lane = threadIdx.x & 31;
+  int kept = 0;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const u64 key = i0 + lane < n ? list[i0 + lane] : 0;
+    const bool in = key != 0 && key >= cut;
+    const unsigned who = __ballot_sync(0xffffffffu, in);
+    if (in) list[kept + __popc(who & ((1u << lane) - 1))] = key;
+    kept += __popc(who);
+    __syncwarp();
+  }
+  return kept;
+}
+
+// MANY: more than kWarpTop alternatives.
+template <bool F32, int C, bool MANY>
 __global__ void __launch_bounds__(kWarps * 32) k_score_warp(const ScoreArgs a) {
-  constexpr int E = Row<F32>::E;
+  constexpr int E = Row<F32>::E, kWarpList = warp_list(MANY);
   __shared__ u64 lists[kWarps][kWarpList];
   pdl_release();
   pdl_wait();
@@ -458,10 +475,35 @@ __global__ void __launch_bounds__(kWarps * 32) k_score_warp(const ScoreArgs a) {
     return;
   }
 
-  // the bound: the top-th of the lanes' maxima, by (logit, chunk)
+  // the bound: the top-th of the lanes' maxima, or of the chunks', by (logit, chunk)
   uint32_t key = lane < x.nq ? order_key(best + 0.f) : 0u, bound = 0;
   int bound_at = INT_MAX;
-  if (x.nq >= a.top) {
+  const bool all = x.nq < a.top;
+  if constexpr (MANY) {
+    uint32_t keys[C];
+#pragma unroll
+    for (int u = 0; u < C; ++u) keys[u] = lane + 32 * u < x.nq ? order_key(chunk_max<F32>(v[u]) + 0.f) : 0u;
+    auto count = [&](auto f) {
+      int c = 0;
+#pragma unroll
+      for (int u = 0; u < C; ++u) c += f(keys[u], lane + 32 * u);
+      return warp_sum_i(c);
+    };
+    if (!all) {
+      // bit by bit; of a bf16's key the upper half says it
+      for (int bit = 31; bit >= (F32 ? 0 : 16); --bit) {
+        const uint32_t trial = bound | (1u << bit);
+        if (count([&](uint32_t k, int) { return k >= trial; }) >= a.top) bound = trial;
+      }
+      if (!F32 && bound < 0x80000000u) bound |= 0xffffu;
+      // of those that tie, the chunks up to the one that makes them enough
+      const int left = a.top - count([&](uint32_t k, int) { return k > bound; });
+      int below = 0;  // the largest number such that fewer tie in front of it
+      for (int bit = 1 << 9; bit > 0; bit >>= 1)
+        if (count([&](uint32_t k, int q) { return k == bound && q < (below | bit); }) < left) below |= bit;
+      bound_at = below;
+    }
+  } else if (!all) {
     int left = a.top;
     uint32_t rest = key;
     while (true) {
@@ -484,10 +526,9 @@ __global__ void __launch_bounds__(kWarps * 32) k_score_warp(const ScoreArgs a) {
   // list what reaches it
   u64* list = lists[wid];
   int listed = 0;
-  const bool all = x.nq < a.top;
   const u64 cut = all ? 0 : ((u64)bound << 32) | (uint32_t)~bound_at;
   const float bound_x = all ? -kInf : logit_of_key(cut);
-  const bool any = lane < x.nq && (((u64)key << 32) | (uint32_t)~at) >= cut;
+  const bool any = lane < x.nq && (MANY || (((u64)key << 32) | (uint32_t)~at) >= cut);
 #pragma unroll
   for (int u = 0; u < C; ++u) {
     const int q = lane + 32 * u;
@@ -506,14 +547,12 @@ __global__ void __launch_bounds__(kWarps * 32) k_score_warp(const ScoreArgs a) {
     }
   }
   __syncwarp();
-  u64 last = 0;
   if (listed > kWarpList)
-    listed = warp_list_exact<F32>(x, a.V, a.top, list);
-  else if (listed > kLongList)
-    last = warp_cut(list, listed, a.top);
+    listed = warp_list_exact<F32>(x, a.V, a.top, list, kWarpList);
+  else if (listed > kLongList && listed > a.top)
+    listed = warp_keep(list, listed, warp_cut(list, listed, a.top));
   for (int i = lane; i < listed; i += 32) {
     const u64 mine = list[i];
-    if (mine < last) continue;
     int before = 0;
     for (int j = 0; j < listed; ++j) before += list[j] > mine;
     if (before < a.top) write_top(a, row, before, mine, r, false);
@@ -904,15 +943,21 @@ template <bool F32>
 cudaError_t launch_rows(const ScoreArgs& a, cudaStream_t st) {
   const int E = F32 ? 4 : 8;
   const long long nq = ((long long)a.V + 2 * E - 2) / E;  // the most chunks a row has
-  if (a.top <= kWarpTop && nq <= 32 * 16) {
+  if (nq <= 32 * 16) {
     const long long blocks = ((long long)a.n + kWarps - 1) / kWarps;
     const int c = (int)((nq + 31) / 32);
-    if (c <= 1) return launch(k_score_warp<F32, 1>, a, blocks, kWarps * 32, 1, st);
-    if (c <= 2) return launch(k_score_warp<F32, 2>, a, blocks, kWarps * 32, 1, st);
-    if (c <= 3) return launch(k_score_warp<F32, 3>, a, blocks, kWarps * 32, 1, st);
-    if (c <= 5) return launch(k_score_warp<F32, 5>, a, blocks, kWarps * 32, 1, st);
-    if (c <= 9) return launch(k_score_warp<F32, 9>, a, blocks, kWarps * 32, 1, st);
-    return launch(k_score_warp<F32, 16>, a, blocks, kWarps * 32, 1, st);
+#define DS_WARP(C, MANY) return launch(k_score_warp<F32, C, MANY>, a, blocks, kWarps * 32, 1, st)
+    if (a.top > kWarpTop) {
+      if (c <= 5) DS_WARP(5, true);
+      DS_WARP(16, true);
+    }
+    if (c <= 1) DS_WARP(1, false);
+    if (c <= 2) DS_WARP(2, false);
+    if (c <= 3) DS_WARP(3, false);
+    if (c <= 5) DS_WARP(5, false);
+    if (c <= 9) DS_WARP(9, false);
+    DS_WARP(16, false);
+#undef DS_WARP
   }
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorUnknown;
