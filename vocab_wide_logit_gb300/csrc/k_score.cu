@@ -111,15 +111,19 @@ __device__ __forceinline__ uint4 nothing() {
 template <bool F32>
 __device__ __forceinline__ void mask_edges(uint4& v, int q, int dc, int V) {
   constexpr int E = Row<F32>::E;
-  const long long id0 = (long long)q * E - dc;
+  // a bit for each logit of the row
+  const long long first = (long long)q * E - dc;
+  const int lo = first < 0 ? (int)-first : 0, hi = V - first < E ? (int)(V - first) : E;
+  const uint32_t keep = ((1u << hi) - 1u) & ~((1u << lo) - 1u);
   uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    if (id0 + i >= 0 && id0 + i < V) continue;
-    if constexpr (F32)
-      w[i] = kMinusInf;
-    else
-      w[i >> 1] = (i & 1) ? ((w[i >> 1] & 0x0000ffffu) | 0xff800000u) : ((w[i >> 1] & 0xffff0000u) | 0x0000ff80u);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (F32) {
+      w[i] = (keep >> i & 1u) ? w[i] : kMinusInf;
+    } else {
+      const uint32_t m = (0u - (keep >> (2 * i) & 1u)) & 0x0000ffffu | (0u - (keep >> (2 * i + 1) & 1u)) & 0xffff0000u;
+      w[i] = (w[i] & m) | (kMinusInf2 & ~m);
+    }
   }
   v = make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -285,12 +289,11 @@ __device__ __forceinline__ int rank_mend(const Given& g, float near, int dc) {
   return n - (g.x == -kInf && g.chunk > 0 ? dc : 0);
 }
 
-// Writes the row's four numbers; returns lse, NaN when nothing may be listed.
-__device__ __forceinline__ float write_row(const ScoreArgs& a, int row, const Sums& r, const Given& g) {
+// Writes the row's four numbers.
+__device__ __forceinline__ void write_row(const ScoreArgs& a, int row, const Sums& r, const Given& g, float log_s) {
   const float nan = __int_as_float(0x7fffffff);
   const bool bad = !(r.s < kInf) || r.m == kInf;  // a NaN or +inf among the logits
   const bool none = bad || r.m == -kInf;
-  const float log_s = logf(r.s);
   const float lse = bad ? nan : none ? -kInf : r.m + log_s;
   a.out_logprobs[row] = none || g.token < 0 ? nan : (g.x - r.m) - log_s;
   if (a.out_lse) a.out_lse[row] = lse;
@@ -298,13 +301,12 @@ __device__ __forceinline__ float write_row(const ScoreArgs& a, int row, const Su
   if (a.out_ranks) a.out_ranks[row] = none || g.token < 0 ? -1 : r.before;
   const uint32_t bits = (a.tokens[row] >= a.V ? DS_DEV_ERR_PARAM : 0u) | (bad ? DS_DEV_ERR_LOGITS : 0u);
   if (bits) report(a.d_status, bits);
-  return none ? nan : lse;
 }
 // Alternative number r; key 0 for none.
-__device__ __forceinline__ void write_top(const ScoreArgs& a, int row, int r, u64 key, const Sums& sums, bool none) {
+__device__ __forceinline__ void write_top(const ScoreArgs& a, int row, int r, u64 key, float m, float log_s, bool none) {
   const long long at = (long long)row * a.top + r;
   a.out_top_ids[at] = none ? -1 : id_of(key);
-  a.out_top_logprobs[at] = none ? __int_as_float(0x7fffffff) : (logit_of_key(key) - sums.m) - logf(sums.s);
+  a.out_top_logprobs[at] = none ? __int_as_float(0x7fffffff) : (logit_of_key(key) - m) - log_s;
 }
 __device__ __forceinline__ bool is_none(const Sums& r) { return !(r.s < kInf) || r.m == kInf || r.m == -kInf; }
 
@@ -467,11 +469,12 @@ __global__ void __launch_bounds__(kWarps * 32) k_score_warp(const ScoreArgs a) {
   }
   r.before = warp_sum_i(r.before);
   r.before += rank_mend(g, near, x.dc);
-  if (lane == 0) write_row(a, row, r, g);
+  const float log_s = logf(r.s);
+  if (lane == 0) write_row(a, row, r, g, log_s);
   if (a.top == 0) return;
   const bool none = is_none(r);
   if (none) {
-    for (int i = lane; i < a.top; i += 32) write_top(a, row, i, 0, r, true);
+    for (int i = lane; i < a.top; i += 32) write_top(a, row, i, 0, 0.f, 0.f, true);
     return;
   }
 
@@ -529,21 +532,41 @@ __global__ void __launch_bounds__(kWarps * 32) k_score_warp(const ScoreArgs a) {
   const u64 cut = all ? 0 : ((u64)bound << 32) | (uint32_t)~bound_at;
   const float bound_x = all ? -kInf : logit_of_key(cut);
   const bool any = lane < x.nq && (MANY || (((u64)key << 32) | (uint32_t)~at) >= cut);
+  if constexpr (C * E <= 64) {
+    // a bit for each logit of the lane that reaches the bound; the logits from memory again
+    u64 reach = 0;
 #pragma unroll
-  for (int u = 0; u < C; ++u) {
-    const int q = lane + 32 * u;
-    const bool here = any && q < x.nq && chunk_max<F32>(v[u]) >= bound_x;
-    if (!__any_sync(0xffffffffu, here)) continue;
-    uint32_t reach = here ? reaching<F32>(v[u], bound_x) : 0;
+    for (int u = 0; u < C; ++u) reach |= (u64)reaching<F32>(v[u], bound_x) << (E * u);
+    if (!any) reach = 0;
+    const int first = lane * E - x.dc;
     while (__any_sync(0xffffffffu, reach != 0)) {
-      const int i = reach ? __ffs(reach) - 1 : 0, id = q * E - x.dc + i;
-      const uint32_t k = order_key(pick<F32>(v[u], i) + 0.f);
-      const bool in = reach && id >= 0 && id < a.V && (((u64)k << 32) | (uint32_t)~q) >= cut;
+      const int i = reach ? __ffsll((long long)reach) - 1 : 0, q = lane + 32 * (i / E), id = first + 32 * E * (i / E) + i % E;
+      const bool in_row = reach && id >= 0 && id < a.V;
+      const uint32_t k = order_key((in_row ? x.logit(id) : 0.f) + 0.f);
+      const bool in = in_row && (((u64)k << 32) | (uint32_t)~q) >= cut;
       const unsigned who = __ballot_sync(0xffffffffu, in);
       const int pos = listed + __popc(who & ((1u << lane) - 1));
       if (in && pos < kWarpList) list[pos] = ((u64)k << 32) | (uint32_t)~id;
       listed += __popc(who);
       reach &= reach - 1;
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < C; ++u) {
+      const int q = lane + 32 * u;
+      const bool here = any && q < x.nq && chunk_max<F32>(v[u]) >= bound_x;
+      if (!__any_sync(0xffffffffu, here)) continue;
+      uint32_t reach = here ? reaching<F32>(v[u], bound_x) : 0;
+      while (__any_sync(0xffffffffu, reach != 0)) {
+        const int i = reach ? __ffs(reach) - 1 : 0, id = q * E - x.dc + i;
+        const uint32_t k = order_key(pick<F32>(v[u], i) + 0.f);
+        const bool in = reach && id >= 0 && id < a.V && (((u64)k << 32) | (uint32_t)~q) >= cut;
+        const unsigned who = __ballot_sync(0xffffffffu, in);
+        const int pos = listed + __popc(who & ((1u << lane) - 1));
+        if (in && pos < kWarpList) list[pos] = ((u64)k << 32) | (uint32_t)~id;
+        listed += __popc(who);
+        reach &= reach - 1;
+      }
     }
   }
   __syncwarp();
@@ -555,7 +578,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_score_warp(const ScoreArgs a) {
     const u64 mine = list[i];
     int before = 0;
     for (int j = 0; j < listed; ++j) before += list[j] > mine;
-    if (before < a.top) write_top(a, row, before, mine, r, false);
+    if (before < a.top) write_top(a, row, before, mine, r.m, log_s, false);
   }
 }
 
@@ -779,10 +802,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
     Sums r = sh.total;
     if (wid == 0) {
       r.before += rank_mend(g, near, x.dc);
-      if (tid == 0) write_row(a, row, r, g);
+      if (tid == 0) write_row(a, row, r, g, logf(r.s));
     }
     if (is_none(r)) {  // nothing to list
-      for (int i = tid; i < top; i += NT) write_top(a, row, i, 0, r, true);
+      for (int i = tid; i < top; i += NT) write_top(a, row, i, 0, 0.f, 0.f, true);
       return;
     }
     if (top == 0) return;
@@ -849,9 +872,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
     }
   }
   if (cs == 1) {
-    const Sums r = sh.total;
+    const float m_row = sh.total.m, log_s = logf(sh.total.s);
     rank_list<NT>(sh.list, listed, cut, [&](u64 key, int above) {
-      if (above < top) write_top(a, row, above, key, r, false);
+      if (above < top) write_top(a, row, above, key, m_row, log_s, false);
     });
     return;
   }
@@ -876,11 +899,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
   if (wid == 0) {
     Sums all = r;
     all.before += rank_mend(g, near, x.dc);
-    if (tid == 0) write_row(a, row, all, g);
+    if (tid == 0) write_row(a, row, all, g, logf(r.s));
   }
   if (top == 0) return;
   if (is_none(r)) {
-    for (int i = tid; i < top; i += NT) write_top(a, row, i, 0, r, true);
+    for (int i = tid; i < top; i += NT) write_top(a, row, i, 0, 0.f, 0.f, true);
     return;
   }
   // bounds of the row's top-th: the largest of the slices' top-th entries, and, with
@@ -911,8 +934,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
   __syncthreads();
   listed = sh.count;
   cut = listed > kLong ? list_cut<NT>(sh.list, listed, sh.bits, &sh.differ, top) : 0;
+  const float log_s = logf(r.s);
   rank_list<NT>(sh.list, listed, cut, [&](u64 key, int above) {
-    if (above < top) write_top(a, row, above, key, r, false);
+    if (above < top) write_top(a, row, above, key, r.m, log_s, false);
   });
 }
 static_assert(kMaxCluster * DS_SCORE_MAX_TOP <= list_size(512), "the survivors of all slices fit the list");
