@@ -366,6 +366,26 @@ struct Raw {
   }
 };
 
+// Eight bf16 from i on that start at any 2 bytes, as they are; zeros from `end` on: words
+// of 4 bytes, each of which has one of them.
+__device__ __forceinline__ void load_any(const uint16_t* row, int i, int end, uint32_t (&w)[4]) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row + i);
+  const int odd = (int)(at >> 1) & 1;
+  const uint32_t* p = reinterpret_cast<const uint32_t*>(at & ~(uintptr_t)3);
+  uint32_t f[5];
+#pragma unroll
+  for (int j = 0; j < 5; ++j) f[j] = i + 2 * j - odd < end && (j < 4 || odd) ? __ldg(p + j) : 0u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = odd ? __funnelshift_r(f[j], f[j + 1], 16) : f[j];
+  if (i + 8 > end) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (i + 2 * j >= end) w[j] = 0;
+      if (i + 2 * j + 1 >= end) w[j] &= 0xffffu;
+    }
+  }
+}
+
 // PARTS: bf16 parts of an input. VEC: 16-byte loads. GROUPS: of 8 ranks, 2 or 4.
 template <bool XF32, int PARTS, bool VEC, int GROUPS>
 __global__ void __launch_bounds__(kDownThreads) k_adapters_down(const AdapterArgs g, Head* head, Tile* tiles, uint8_t* t_out,
@@ -488,14 +508,23 @@ __global__ void __launch_bounds__(kDownThreads) k_adapters_down(const AdapterArg
       }
     }
   } else {
+#pragma unroll 2
     for (int k0 = wid * 32; k0 < g.K; k0 += kStep) {
       const int k = k0 + 8 * q;
       float f0[8], f1[8], n8[8];
       uint32_t b[GROUPS][4];
-      load8<XF32, false>(x0, k, K0, f0);
-      load8<XF32, false>(x1, k, K1, f1);
+      if constexpr (XF32) {
+        load8<true, false>(x0, k, K0, f0);
+        load8<true, false>(x1, k, K1, f1);
+      } else {
+        uint32_t w0[4], w1[4];
+        load_any(reinterpret_cast<const uint16_t*>(x0), k, K0, w0);
+        load_any(reinterpret_cast<const uint16_t*>(x1), k, K1, w1);
+        unpack8(make_uint4(w0[0], w0[1], w0[2], w0[3]), f0);
+        unpack8(make_uint4(w1[0], w1[1], w1[2], w1[3]), f1);
+      }
 #pragma unroll
-      for (int j = 0; j < GROUPS; ++j) load_weights<8, false>(wr[j], k, Kw[j], b[j]);
+      for (int j = 0; j < GROUPS; ++j) load_any(wr[j], k, Kw[j], b[j]);
       load8<true, false>(g.gain, k, g.gain ? g.K : 0, n8);
       take(f0, f1, n8, b);
     }

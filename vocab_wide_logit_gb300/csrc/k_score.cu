@@ -314,10 +314,12 @@ __device__ __forceinline__ bool is_none(const Sums& r) { return !(r.s < kInf) ||
 // Rows of up to 32 C chunks, held in registers: 700 instructions for 1025 bf16
 // logits and 8 alternatives.
 constexpr int kWarps = 4;
-constexpr int kWarpTop = 32;    // alternatives that are bounded by a lane's maximum each; more by a chunk's
-// Candidates a row may list: that many chunks of 8.
-__host__ __device__ constexpr int warp_list(bool many) { return 8 * (many ? DS_SCORE_MAX_TOP : kWarpTop); }
-constexpr int kLongList = 64;   // entries from which the exact cut is cheaper than ranking all
+// Alternatives that are bounded by a lane's maximum each, more by a chunk's: the 20th of 32
+// maxima lists 31 logits in the mean, the 32nd 130.
+constexpr int kWarpTop = 24;
+// Candidates a row may list: as many chunks of 8 as alternatives or lanes.
+__host__ __device__ constexpr int warp_list(bool many) { return 8 * (many ? DS_SCORE_MAX_TOP : 32); }
+constexpr int kLongList = 128;  // entries from which the exact cut is cheaper than ranking all
 
 // The top-th largest of n unique keys.
 __device__ __noinline__ u64 warp_cut(const u64* list, int n, int top) {
@@ -529,10 +531,13 @@ __global__ void __launch_bounds__(kWarps * 32) k_score_warp(const ScoreArgs a) {
   // list what reaches it
   u64* list = lists[wid];
   int listed = 0;
-  const u64 cut = all ? 0 : ((u64)bound << 32) | (uint32_t)~bound_at;
-  const float bound_x = all ? -kInf : logit_of_key(cut);
+  const u64 cut = ((u64)bound << 32) | (uint32_t)~bound_at;
+  const float bound_x = logit_of_key(cut);
   const bool any = lane < x.nq && (MANY || (((u64)key << 32) | (uint32_t)~at) >= cut);
-  if constexpr (C * E <= 64) {
+  if (all) {  // fewer chunks than alternatives
+    for (int id = lane; id < a.V; id += 32) list[id] = order_of(x.logit(id), id);
+    listed = a.V;
+  } else if constexpr (C > 2 && C * E <= 64) {
     // a bit for each logit of the lane that reaches the bound; the logits from memory again
     u64 reach = 0;
 #pragma unroll
@@ -589,12 +594,13 @@ constexpr int kMaxCluster = 16;
 __host__ __device__ constexpr int list_size(int threads) { return threads >= 512 ? 2048 : 1024; }
 constexpr int kLong = 160;     // entries from which the exact cut is cheaper than ranking all
 constexpr int kUnroll = 4;     // chunks a thread has in flight, twice
+constexpr int kFewTop = 32;    // alternatives for which 64 groups of threads are enough
 
 template <int NT>
 struct Shared {
   u64 list[list_size(NT)];  // candidates; in the joining CTA then the survivors of all slices
   u64 sorted[(NT >= 512 ? kMaxCluster : 1) * DS_SCORE_MAX_TOP];  // each slice's alternatives in order
-  u64 keys[256];                      // groups' maxima
+  u64 keys[64];             // groups' maxima
   Sums warps[NT / 32];
   Sums slices[kMaxCluster];
   Sums total;
@@ -772,14 +778,16 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
   }
   const int top = a.top;
   const u64 own = q_lo + tid < q_hi ? ((u64)order_key(m + 0.f) << 32) | (uint32_t)~at : 0;
-  const int width = top <= 32 && NT > 64 ? NT / 64 : NT > 256 ? NT / 256 : 1;  // threads of a group
-  if (top > 0) {
+  constexpr int kWidth = NT / 64;  // threads of a group
+  const bool few = top <= kFewTop;
+  if (top > 0 && few) {
     u64 k = own;
-    for (int o = width >> 1; o > 0; o >>= 1) {
+#pragma unroll
+    for (int o = kWidth >> 1; o > 0; o >>= 1) {
       const u64 other = __shfl_xor_sync(0xffffffffu, k, o);
       k = k > other ? k : other;
     }
-    if ((tid & (width - 1)) == 0) sh.keys[tid / width] = k;
+    if ((tid & (kWidth - 1)) == 0) sh.keys[tid / kWidth] = k;
   }
   __syncthreads();
   if (wid == NT / 32 - 1) {
@@ -787,15 +795,30 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
     p = warp_join(p, 32);
     if (lane == 0) sh.total = p;
   }
-  if (top > 0) {
-    // the top-th of the groups' maxima bounds the slice's top-th logit from below; the
-    // threads of a group share the comparisons
-    const int groups = NT / width, group = tid / width;
+  // The top-th of the groups' maxima bounds the slice's top-th logit from below; the
+  // threads of a group share the comparisons. For more alternatives the top-th of the
+  // threads' maxima, bit by bit (ranking 256 groups took 1.5 us more).
+  u64 bound = 0;
+  if (top > 0 && few) {
+    const int group = tid / kWidth;
     const u64 k = sh.keys[group];
     int above = 0;
-    for (int j = tid & (width - 1); j < groups; j += width) above += sh.keys[j] > k || (sh.keys[j] == k && j < group);
-    for (int o = width >> 1; o > 0; o >>= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
+#pragma unroll 8
+    for (int j = tid & (kWidth - 1); j < 64; j += kWidth) above += sh.keys[j] > k || (sh.keys[j] == k && j < group);
+#pragma unroll
+    for (int o = kWidth >> 1; o > 0; o >>= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
     if (above == top - 1) sh.bound = k;
+  } else if (top > 0 && __syncthreads_count(own != 0) >= top) {
+    for (int bit = 63; bit >= 0; --bit) {
+      if (!F32 && bit == 47) {  // of a bf16's key the upper half says it
+        if (!(bound >> 63)) bound |= 0xffffull << 32;
+        bit = 31;
+      }
+      const u64 trial = bound | (1ull << bit);
+      const int c = __syncthreads_count(own >= trial);
+      if (c >= top) bound = trial;
+      if (c == top) break;
+    }
   }
   __syncthreads();
   if (cs == 1) {
@@ -813,7 +836,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
   int listed = 0;
   u64 cut = 0;
   if (top > 0) {
-    const u64 bound = sh.bound;
+    if (few) bound = sh.bound;
     const float bound_x = bound == 0 ? -kInf : logit_of_key(bound);
     // The logits that reach the bound: in the best batch of each thread whose maximum does,
     // and in all of the thread's share, taken by its whole warp, when another batch has any.
@@ -906,9 +929,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
     for (int i = tid; i < top; i += NT) write_top(a, row, i, 0, 0.f, 0.f, true);
     return;
   }
-  // bounds of the row's top-th: the largest of the slices' top-th entries, and, with
+  // Bounds of the row's top-th: the largest of the slices' top-th entries, and, with
   // c slices that have d entries at or above a key, c d >= top, that key
-  u64 bound;
   {
     const int d = (top + (cs >> 1) - 1) / (cs >> 1), c = (top + d - 1) / d;
     const u64 kd = lane < cs ? sh.sorted[lane * top + d - 1] : 0, kt = lane < cs ? sh.sorted[lane * top + top - 1] : 0;
@@ -973,20 +995,26 @@ cudaError_t launch_rows(const ScoreArgs& a, cudaStream_t st) {
 #define DS_WARP(C, MANY) return launch(k_score_warp<F32, C, MANY>, a, blocks, kWarps * 32, 1, st)
     if (a.top > kWarpTop) {
       if (c <= 5) DS_WARP(5, true);
+      if (c <= 9) DS_WARP(9, true);
       DS_WARP(16, true);
     }
     if (c <= 1) DS_WARP(1, false);
     if (c <= 2) DS_WARP(2, false);
     if (c <= 3) DS_WARP(3, false);
     if (c <= 5) DS_WARP(5, false);
+    if (c <= 7) DS_WARP(7, false);
     if (c <= 9) DS_WARP(9, false);
+    if (c <= 12) DS_WARP(12, false);
     DS_WARP(16, false);
 #undef DS_WARP
   }
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorUnknown;
-  if (nq <= 2048) return launch(k_score_block<F32, 128>, a, a.n, 128, 1, st);
-  if (nq <= 4096) return launch(k_score_block<F32, 256>, a, a.n, 256, 1, st);
+  // (128 alternatives from the maxima of 128 threads would list half the row)
+  if (a.top <= kFewTop) {
+    if (nq <= 2048) return launch(k_score_block<F32, 128>, a, a.n, 128, 1, st);
+    if (nq <= 4096) return launch(k_score_block<F32, 256>, a, a.n, 256, 1, st);
+  }
   // slices of at least 4.5 chunks a thread while all CTAs run at once
   int cs = 1;
   while (cs < 8 && nq / (2 * cs) >= 2304 && 2LL * a.n * cs <= 2LL * sms) cs *= 2;
