@@ -612,19 +612,22 @@ struct Up {
   // Channels of a warp and block: 8 columns of as many instructions. Where two of each
   // make whole chunks a lane and rows start on chunks, sums go straight from the lane that
   // has them to the result; else through shared memory.
-  static constexpr int kMine = kGroups / 8;
+  // With 128 ranks half of the warps take half of the ranks each: t stays in registers.
+  static constexpr int kHalves = RP == 128 ? 2 : 1, kWarps = 8 / kHalves;
+  static constexpr int kMine = kGroups / kWarps;
   static constexpr int kPieces = 2 * kMine / E;                  // chunks of a lane
-  static constexpr bool kDirect = !SHIFT && kPieces > 0;
+  static constexpr bool kDirect = !SHIFT && kPieces > 0 && kHalves == 1;
   static constexpr int kPitch = kChannels + 8;                   // rows of results lie 8 banks apart
   // weights that may start at any 2 bytes, and base
   static constexpr int kWeights = (kChannels + kFront) * RP * 2 + 32;
   static constexpr int kStage = kWeights + kRows * kChunks * 16;
-  static constexpr int kResults = kDirect ? 0 : kRows * kPitch * 4;
+  static constexpr int kResults = kDirect ? 0 : kHalves * kRows * kPitch * 4;
   static constexpr int kCtas = RP == 16 && kChunks == 32 ? 3 : 2;  // of an SM
   static constexpr int kStages = kCtas * (4 * kStage + kResults) <= 220 * 1024 ? 4 : 3;
   static constexpr int kSmem = kStages * kStage + kResults;
 };
 
+__device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
@@ -663,7 +666,7 @@ template <bool F32, int RP, bool VEC, bool NEAR, bool SHIFT>
 __global__ void __launch_bounds__(kUpThreads, (Up<F32, RP, SHIFT>::kCtas))
     k_adapters_up(const AdapterArgs g, const Head* head, const Tile* tiles, const uint8_t* t_in, int blocks) {
   using U = Up<F32, RP, SHIFT>;
-  constexpr int E = U::E, kSize = F32 ? 4 : 2, PARTS = F32 ? 3 : 2, STEPS = RP / 16, S = U::kStages, W = U::kChunks;
+  constexpr int E = U::E, kSize = F32 ? 4 : 2, PARTS = F32 ? 3 : 2, STEPS = RP / 16 / U::kHalves, S = U::kStages, W = U::kChunks;
   constexpr int kLoad = RP == 16 ? 4 : 8;  // weights of a lane and load: one instruction's, or two's
   constexpr int kTurns = (kRows * W + kUpThreads - 1) / kUpThreads;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -758,7 +761,8 @@ __global__ void __launch_bounds__(kUpThreads, (Up<F32, RP, SHIFT>::kCtas))
   const char* from_base[kTurns];  // without NEAR
   int shift[kTurns];
   const uint4* t4 = nullptr;
-  uint4 t[RP <= 64 ? STEPS : 1][PARTS];
+  uint4 t[STEPS][PARTS];
+  const int strand = wid % U::kWarps, half = wid / U::kWarps;  // of the warp's channels, of its ranks
   for (long long item = lo; item < hi; ++item) {
     asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
     __syncthreads();
@@ -787,12 +791,10 @@ __global__ void __launch_bounds__(kUpThreads, (Up<F32, RP, SHIFT>::kCtas))
         from_base[k] = base + (row * g.ldb + my_chunk - shift[k]) * kSize;
       }
       if (a >= 0) {
-        if constexpr (RP <= 64) {
 #pragma unroll
-          for (int s = 0; s < STEPS; ++s)
+        for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-            for (int p = 0; p < PARTS; ++p) t[s][p] = t4[(s * 3 + p) * 32];
-        }
+          for (int p = 0; p < PARTS; ++p) t[s][p] = t4[((half * STEPS + s) * 3 + p) * 32];
         dc0 = gq < count ? shift_of(tile.rows[gq]) : 0;
         dc1 = gq + 8 < count ? shift_of(tile.rows[gq + 8]) : 0;
       }
@@ -879,25 +881,18 @@ __global__ void __launch_bounds__(kUpThreads, (Up<F32, RP, SHIFT>::kCtas))
         const unsigned char* row = w + (there ? n * 8 * row_bytes : 0);
         d[0] = d[1] = d[2] = d[3] = 0.f;
 #pragma unroll
-        for (int h = 0; h < RP / (4 * kLoad); ++h) {
+        for (int h = 0; h < STEPS * 4 / kLoad; ++h) {
           uint32_t b[kLoad / 2];
-          shared_weights<kLoad, VEC>(row, 4 * kLoad * h + kLoad * q, there ? g.R : 0, b);
+          shared_weights<kLoad, VEC>(row, 16 * STEPS * half + 4 * kLoad * h + kLoad * q, there ? g.R : 0, b);
 #pragma unroll
-          for (int i = 0; i < kLoad / 4; ++i) {
-            const int s = h * (kLoad / 4) + i;
+          for (int i = 0; i < kLoad / 4; ++i)
 #pragma unroll
-            for (int p = PARTS - 1; p >= 0; --p) {
-              if constexpr (RP <= 64)
-                mma(d, t[s][p], b[2 * i], b[2 * i + 1]);
-              else
-                mma(d, t4[(s * 3 + p) * 32], b[2 * i], b[2 * i + 1]);
-            }
-          }
+            for (int p = PARTS - 1; p >= 0; --p) mma(d, t[h * (kLoad / 4) + i][p], b[2 * i], b[2 * i + 1]);
         }
       };
       // this lane's two sums of a group of 8 channels go here, the group's place added
-      float* to0 = results + gq * U::kPitch + 2 * q + dc0;
-      float* to1 = results + (gq + 8) * U::kPitch + 2 * q + dc1;
+      float* to0 = results + (half * kRows + gq) * U::kPitch + 2 * q + dc0;
+      float* to1 = results + (half * kRows + gq + 8) * U::kPitch + 2 * q + dc1;
       auto put = [&](int n, const float (&d)[4]) {
         // up to 7 places behind the last chunk: the pitch has room, nobody reads them
         if constexpr (SHIFT) {
@@ -915,18 +910,18 @@ __global__ void __launch_bounds__(kUpThreads, (Up<F32, RP, SHIFT>::kCtas))
           }
         }
       };
-      static_assert(U::kGroups % 8 == 0, "the same number for each");
+      static_assert(U::kGroups % U::kWarps == 0, "the same number for each");
       float d[kMine][4];
       if (left >= U::kChannels) {
 #pragma unroll
-        for (int j = 0; j < kMine; ++j) multiply(wid + 8 * j, true, d[j]);
+        for (int j = 0; j < kMine; ++j) multiply(strand + U::kWarps * j, true, d[j]);
       } else {
 #pragma unroll
-        for (int j = 0; j < kMine; ++j) multiply(wid + 8 * j, 8 * (wid + 8 * j) + gq < left, d[j]);
+        for (int j = 0; j < kMine; ++j) multiply(strand + U::kWarps * j, 8 * (strand + U::kWarps * j) + gq < left, d[j]);
       }
 #pragma unroll
-      for (int j = 0; j < kMine; ++j) put(wid + 8 * j, d[j]);
-      if (SHIFT && wid == 7) {  // the last channels in front of the block, where a row's chunks start earlier
+      for (int j = 0; j < kMine; ++j) put(strand + U::kWarps * j, d[j]);
+      if (SHIFT && strand == U::kWarps - 1) {  // the last channels in front of the block, where a row's chunks start earlier
         multiply(-1, f > 0 && gq - 8 < left, d[0]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -964,11 +959,13 @@ __global__ void __launch_bounds__(kUpThreads, (Up<F32, RP, SHIFT>::kCtas))
         } else if (a >= 0) {
           const float4* s = reinterpret_cast<const float4*>(results + (my_row + kPerTurn * k) * U::kPitch + my_chunk);
           if constexpr (F32) {
-            const float4 f = s[0];
+            float4 f = s[0];
+            if constexpr (U::kHalves == 2) f = add4(f, s[kRows * U::kPitch / 4]);
             z = make_uint4(__float_as_uint(__uint_as_float(z.x) + f.x), __float_as_uint(__uint_as_float(z.y) + f.y),
                            __float_as_uint(__uint_as_float(z.z) + f.z), __float_as_uint(__uint_as_float(z.w) + f.w));
           } else {
-            const float4 f = s[0], h = s[1];
+            float4 f = s[0], h = s[1];
+            if constexpr (U::kHalves == 2) f = add4(f, s[kRows * U::kPitch / 4]), h = add4(h, s[kRows * U::kPitch / 4 + 1]);
             z = make_uint4(pack_bf(bf_lo(z.x) + f.x, bf_hi(z.x) + f.y), pack_bf(bf_lo(z.y) + f.z, bf_hi(z.y) + f.w),
                            pack_bf(bf_lo(z.z) + h.x, bf_hi(z.z) + h.y), pack_bf(bf_lo(z.w) + h.z, bf_hi(z.w) + h.w));
           }
