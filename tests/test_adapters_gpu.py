@@ -228,6 +228,18 @@ def test_offsets_beyond_32_bits():
     _check(got, base, hidden, one, torch.where(ids < 0, -1, 0).to(torch.int32))
 
 
+def test_a_row_in_other_batches():
+    """A row's result does not depend on the rows beside it, nor on the order of the call's work: bit for bit."""
+    base, hidden, ad, ids, gain = _inputs(400, 2003, 320, 24, 40, "f32", norm=True)
+    whole = pkg.add_adapters(base, hidden, ad, ids, gain=gain, eps=EPS)
+    for i, n in ((0, 1), (5, 20), (100, 33), (0, 300), (0, 400)):
+        part = pkg.add_adapters(base[i:i + n], hidden[i:i + n], ad, ids[i:i + n], gain=gain, eps=EPS)
+        assert torch.equal(part, whole[i:i + n])
+    many = [t.repeat(21, 1) for t in (base, hidden)]  # more rows than the down kernel's CTAs plan for themselves
+    got = pkg.add_adapters(*many, ad, ids.repeat(21), gain=gain, eps=EPS)
+    assert torch.equal(got, whole.repeat(21, 1))
+
+
 def test_slots_are_read_at_the_call():
     """A program rewrites a slot in place: nothing is kept of what was there."""
     base, hidden, ad, ids, _ = _inputs(10, 500, 64, 16, 2, none=False)

@@ -149,6 +149,25 @@ def test_orders_and_ties(kind, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,team,share", [(3900, 32, 24), (3900, 32, 20), (9000, 128, 64), (9000, 128, 40), (22000, 256, 128),
+                                          (36000, 512, 128), (36000, 512, 256), (150001, 512, 128)])
+def test_largest_logits_in_few_threads(V, team, share, dtype):
+    """Chunks of 16 bytes go round a team of threads: rows whose largest logits are all in some threads' shares, so that a
+    bound from the threads' maxima lists thousands."""
+    E = 8 if dtype == "bf16" else 4
+    V = V * E // 8
+    x, tokens = _inputs(5, V, dtype, V + share)
+    # rows of a new tensor start on a chunk when V is a multiple of its logits: here the first one does
+    few = (torch.arange(V, device=_dev()) // E) % team < share
+    x[0] = torch.where(few, x[0].abs() + 20, x[0])
+    x[1] = x[0].flip(0)
+    x[2] = torch.where(few, torch.full_like(x[2], 9.0), x[2])
+    x[3] = torch.where(few, torch.round(x[3].float()).to(x.dtype) + 30, x[3])
+    for top in (20, 24, 32, 128):
+        _check(x, tokens, top, pkg.score_tokens(x, tokens, top=top))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("V", [40, 1025, 9001, 70001])
 def test_masks(V, dtype):
     """Masked by -inf or the type's lowest value: all but none, one, a few, half; whole leading and trailing parts."""
@@ -344,6 +363,19 @@ def test_grad_bad_rows():
 
 
 # ------------------------------------------------------------------ how it is called
+@pytest.mark.parametrize("V", [1025, 20011, 100003])
+def test_a_row_in_other_batches(V):
+    """Ranks and alternatives are the same whatever the batch; fp32 results within their own error."""
+    x, tokens = _inputs(320, V, "bf16", V)
+    whole = pkg.score_tokens(x, tokens, top=16)
+    for i, n in ((0, 1), (3, 2), (7, 40), (0, 320)):
+        part = pkg.score_tokens(x[i:i + n], tokens[i:i + n], top=16)
+        assert torch.equal(part.ranks, whole.ranks[i:i + n]) and torch.equal(part.top_ids, whole.top_ids[i:i + n])
+    again = pkg.score_tokens(x, tokens, top=16)
+    for a, b in zip(whole, again):
+        assert torch.equal(a, b)  # run to run: bit for bit
+
+
 def test_no_rows():
     x = torch.empty((0, 50), dtype=torch.bfloat16, device=_dev())
     none = torch.empty(0, dtype=torch.int32, device=_dev())
