@@ -835,7 +835,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
   }
   int listed = 0;
   u64 cut = 0;
-  if (top > 0) {
+  const bool dead = sh.total.m == -kInf;  // a slice of -inf alone: its first ones, without a look
+  if (top > 0 && !dead) {
     if (few) bound = sh.bound;
     const float bound_x = bound == 0 ? -kInf : logit_of_key(bound);
     // The logits that reach the bound: in the best batch of each thread whose maximum does,
@@ -909,7 +910,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
     rank_list<NT>(sh.list, listed, cut, [&](u64 key, int above) {
       if (above < top) sorted[above] = key;
     });
-    for (int i = listed + tid; i < top; i += NT) sorted[i] = 0;
+    const long long first = max(0LL, (long long)q_lo * E - x.dc), end = min((long long)a.V, (long long)q_hi * E - x.dc);
+    for (int i = listed + tid; i < top; i += NT) sorted[i] = dead && first + i < end ? order_of(-kInf, (int)(first + i)) : 0;
   }
   if (tid == 0) *cluster.map_shared_rank(&sh.slices[rank], 0) = sh.total;
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
