@@ -185,8 +185,8 @@ PyObject* head(PyObject*, PyObject* const* v, Py_ssize_t count) {
   END_HANDLE_TH_ERRORS
 }
 
-// A contiguous tensor [n] or [n][columns] of 4-byte elements within the memory of another: a quarter of what an
-// allocation takes.
+// A contiguous tensor [n] or [n][columns] within the memory of another of elements of the same size: a quarter of what
+// an allocation takes.
 at::Tensor within(const at::Tensor& memory, int64_t first, at::ScalarType type, int64_t n, int64_t columns = -1) {
   auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(memory.storage()), memory.key_set(),
                                                    c10::scalarTypeToTypeMeta(type));
@@ -273,13 +273,23 @@ PyObject* adapters(PyObject*, PyObject* const* v, Py_ssize_t count) {
   const double eps = PyFloat_AsDouble(v[7]);
   if (PyErr_Occurred()) return nullptr;
   const int32_t L = (int32_t)a->size(0), R = (int32_t)a->size(1);
-  at::Tensor out = at::empty({base.n, base.k}, on(base.device, t->scalar_type()));
   const int64_t need = p_adapters_ws((int32_t)base.n, L, R);
-  at::Tensor ws = at::empty({need}, on(base.device, at::kByte));
+  const int64_t size = c == DS_DTYPE_F32 ? 4 : 2, bytes = base.n * base.k * size, at = (bytes + 127) / 128 * 128;
+  at::Tensor out, ws;
+  void* work;
+  if (8 * need <= bytes) {  // a small workspace behind the result, in one allocation
+    ws = at::empty({(at + need) / size}, on(base.device, t->scalar_type()));
+    out = within(ws, 0, t->scalar_type(), base.n, base.k);
+    work = static_cast<char*>(ws.data_ptr()) + at;
+  } else {
+    out = at::empty({base.n, base.k}, on(base.device, t->scalar_type()));
+    ws = at::empty({need}, on(base.device, at::kByte));
+    work = ws.data_ptr();
+  }
   const ds_status rc =
       p_adapters(base.p, c, (int32_t)base.n, (int32_t)base.k, base.ld, x.p, xc, (int32_t)x.k, x.ld, (const float*)gain,
                  (float)eps, a->const_data_ptr(), b->const_data_ptr(), (const float*)s->const_data_ptr(), L, R,
-                 (const int32_t*)ids, out.data_ptr(), base.k, ws.data_ptr(), need, nullptr, stream(base.device));
+                 (const int32_t*)ids, out.data_ptr(), base.k, work, need, nullptr, stream(base.device));
   return rc != DS_OK ? PyLong_FromLong(rc) : THPVariable_Wrap(std::move(out));
   END_HANDLE_TH_ERRORS
 }
