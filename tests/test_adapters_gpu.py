@@ -1,5 +1,8 @@
 """ds_add_adapters against the definition in 64 bits, and the serving head with adapters."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -348,3 +351,12 @@ def test_head_samples_and_scores():
     # a row of one-hot minus p: its sum is 0 but for the bf16 rounding of each term, sizes adding up to 2 at most
     assert float(dx.double().sum(1).abs().max()) <= 2 * 2.0 ** -8
     assert int(status) == 0
+
+
+def test_example_with_adapters_and_alternatives():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, os.path.join(root, "examples", "next_token.py"), "--rows", "9", "--vocab", "3001",
+                        "--hidden", "128", "--steps", "2", "--adapters", "3", "--alternatives", "4"], capture_output=True,
+                       text=True, timeout=240)
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.count("step ") == 2 and r.stdout.count("alternatives") == 2
