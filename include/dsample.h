@@ -438,6 +438,7 @@ ds_status ds_head_i8(const void* x, int32_t dtype, int32_t n, int32_t K, int64_t
  *   entropy = -sum of p log p with p = exp(x - lse) (nats; p = 0 counts nothing),
  *   rank = how many tokens come before the given one in the order (0: the argmax),
  *   top alternatives = the first `top` of the order.
+ * Sums are fp32, each over less than V / 16384 + 200 additions.
  *
  * Arguments:
  *   logits       device [n][V] of dtype, rows ld elements apart (ld >= V), any
@@ -516,8 +517,8 @@ int64_t ds_add_adapters_workspace(int32_t n, int32_t L, int32_t R);
  *                alignment of the element type.
  *   dtype        DS_DTYPE_BF16 or DS_DTYPE_F32, of base and out.
  *   n, N         n >= 0 (0: nothing launched), 1 <= N <= 2^30.
- *   x            device [n][K] of x_dtype, rows ldx elements apart (ldx >= K), any
- *                alignment of the element type: the hidden states that the
+ *   x            device [n][K] of x_dtype, 1 <= K <= 2^30, rows ldx elements apart
+ *                (ldx >= K), any alignment of the element type: the hidden states that the
  *                projection was fed, before its norm when gain is given.
  *   gain, eps    as for ds_quantize_rows.
  *   a, b         device bf16 [L][R][K] and [L][N][R], dense; 2-byte alignment
@@ -538,8 +539,8 @@ int64_t ds_add_adapters_workspace(int32_t n, int32_t L, int32_t R);
  *   d_status     device uint32 or NULL.
  *   stream       cudaStream_t.
  * A row of x with a NaN or an infinity gives a row of NaN.
- * Returns DS_OK, DS_ERR_INVALID_ARG, DS_ERR_UNSUPPORTED (N, L, R, ldb, ldx or ldo too
- * large) or DS_ERR_CUDA.
+ * Returns DS_OK, DS_ERR_INVALID_ARG, DS_ERR_UNSUPPORTED (N, K, L, R, ldb, ldx or ldo
+ * too large) or DS_ERR_CUDA.
  */
 ds_status ds_add_adapters(const void* base, int32_t dtype, int32_t n, int32_t N, int64_t ldb, const void* x,
                           int32_t x_dtype, int32_t K, int64_t ldx, const float* gain, float eps, const void* a,

@@ -82,7 +82,8 @@ def test_add_adapters(lib):
                 dict(a=ODD), dict(b=ODD), dict(s=HALF), dict(ids=HALF), dict(gain=HALF), dict(st=HALF), dict(gain=FAKE, eps=-1.0),
                 dict(gain=FAKE, eps=float("nan")), dict(ldb=N + 1)):
         assert call(**bad) == INVALID, bad
-    for big in (dict(N=(1 << 30) + 1, ldb=1 << 31, ldo=1 << 31), dict(L=_lib.DS_ADAPTERS_MAX + 1), dict(R=_lib.DS_ADAPTERS_MAX_RANK + 1), dict(ldb=(1 << 40) + 1, ldo=(1 << 40) + 1),
+    for big in (dict(N=(1 << 30) + 1, ldb=1 << 31, ldo=1 << 31), dict(K=(1 << 30) + 1, ldx=1 << 31),
+                dict(L=_lib.DS_ADAPTERS_MAX + 1), dict(R=_lib.DS_ADAPTERS_MAX_RANK + 1), dict(ldb=(1 << 40) + 1, ldo=(1 << 40) + 1),
                 dict(ldx=(1 << 40) + 1), dict(ldo=(1 << 40) + 1)):
         assert call(**big) == UNSUPPORTED, big
     for bad in ((0, 5, 5), (5, 0, 5), (5, 5, 0), (5, _lib.DS_ADAPTERS_MAX + 1, 5), (5, 5, _lib.DS_ADAPTERS_MAX_RANK + 1)):

@@ -246,6 +246,47 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(x.contiguous(), dx)
 
 
+@pytest.mark.parametrize("dtype,V", [("bf16", 2 ** 31 - 1), ("f32", 2 ** 30 + 3)])
+def test_one_row_of_the_longest(V, dtype):
+    """Positions and byte offsets beyond 32 bits within a row; its sums are known: all logits are 0 but three."""
+    x = torch.zeros((1, V), dtype=DT[dtype], device=_dev())
+    x[0, V - 1], x[0, 5], x[0, V // 2] = 3, 2, -math.inf
+    tokens = torch.tensor([V - 1], dtype=torch.int32, device=_dev())
+    r = pkg.score_tokens(x, tokens, top=4)
+    assert r.top_ids[0].tolist() == [V - 1, 5, 0, 1] and int(r.ranks[0]) == 0
+    lse = math.log(V - 3 + math.exp(3) + math.exp(2))
+    # a thread's chain of at most V / 16384 + 200 additions, each off by 2^-24 at most
+    tol = (V / 16384 + 200) * 2.0 ** -24 + lse * 2.0 ** -23
+    assert abs(float(r.lse[0]) - lse) <= tol and abs(float(r.logprobs[0]) - (3 - lse)) <= tol
+    p3, p2 = math.exp(3 - lse), math.exp(2 - lse)
+    entropy = lse - 3 * p3 - 2 * p2
+    assert abs(float(r.entropy[0]) - entropy) <= (2 + 2 * lse) * tol
+    tokens[0] = V - 2
+    r = pkg.score_tokens(x, tokens, top=1)
+    assert int(r.ranks[0]) == V - 2  # the three others are V - 1, 5 and -inf: V - 3 zeros, of which it is the last
+    gl = torch.ones(1, device=_dev())
+    out = pkg.score_tokens_grad(x, tokens, r.lse, g_logprobs=gl, out=x)
+    # 0 - lse has lse's own half ulp in it, the exponential 2^-22, and bf16 half a step
+    p = math.exp(-float(r.lse[0]))
+    rel = (3 * lse + 10) * 2.0 ** -24 + (2.0 ** -8 if dtype == "bf16" else 0)
+    for i, want in ((0, -p), (5, -p * math.exp(2)), (V - 1, -p * math.exp(3)), (V // 2, 0.0), (V - 2, 1 - p), (V - 3, -p)):
+        assert abs(float(out[0, i]) - want) <= abs(want) * rel, i
+
+
+def test_results_can_be_saved(tmp_path):
+    """Results share their memory by type; what a program does with tensors works on them."""
+    x, tokens = _inputs(3, 100, "f32", 1)
+    for top in (0, 4):
+        r = pkg.score_tokens(x, tokens, top=top)
+        torch.save(tuple(r), tmp_path / "scores.pt")
+        for a, b in zip(r, torch.load(tmp_path / "scores.pt")):
+            assert torch.equal(a, b)
+        kept = [t.clone() for t in r]
+        for t in r[:3]:
+            t.add_(1)
+        assert torch.equal(r.ranks, kept[3]) and torch.equal(r.top_ids, kept[4]) and torch.equal(r.logprobs, kept[0] + 1)
+
+
 # ------------------------------------------------------------------ gradient
 def _grad_reference(x, tokens, lse, entropy, gl, gh):
     x, t, z = x.double(), tokens.long(), lse.double()[:, None]

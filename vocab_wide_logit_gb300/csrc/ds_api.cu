@@ -415,7 +415,7 @@ ds_status ds_add_adapters(const void* base, int32_t dtype, int32_t n, int32_t N,
   if (dtype != DS_DTYPE_F32 && dtype != DS_DTYPE_BF16) return DS_ERR_INVALID_ARG;
   if (x_dtype != DS_DTYPE_F32 && x_dtype != DS_DTYPE_BF16) return DS_ERR_INVALID_ARG;
   if (gain && !(eps >= 0.f && eps < INFINITY)) return DS_ERR_INVALID_ARG;
-  if (N > (1 << 30) || L > DS_ADAPTERS_MAX || R > DS_ADAPTERS_MAX_RANK || ldb > (1LL << 40) || ldx > (1LL << 40) || ldo > (1LL << 40))
+  if (N > (1 << 30) || K > (1 << 30) || L > DS_ADAPTERS_MAX || R > DS_ADAPTERS_MAX_RANK || ldb > (1LL << 40) || ldx > (1LL << 40) || ldo > (1LL << 40))
     return DS_ERR_UNSUPPORTED;
   if (n == 0) return DS_OK;
   if (!base || !x || !a || !b || !scale || !ids || !out) return DS_ERR_INVALID_ARG;

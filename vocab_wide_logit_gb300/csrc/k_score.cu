@@ -750,8 +750,12 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
           if (q + u * NT < q_hi) before += count_before<F32>(v[u], q + u * NT < g.chunk, g.x);
     }
     if (usual) {
+      // a batch's sums apart: a thread's chain of additions is as long as its batches
+      float2 bs = make_float2(0.f, 0.f), bt = bs;
 #pragma unroll
-      for (int u = 0; u < U; ++u) add_sums<F32>(v[u], m, low2, s, t);
+      for (int u = 0; u < U; ++u) add_sums<F32>(v[u], m, low2, bs, bt);
+      s = __fadd2_rn(s, bs);
+      t = __fadd2_rn(t, bt);
     } else if (m != -kInf) {
       for (int u = 0; u < U; ++u) add_sums_low<F32>(v[u], m, s, t);
     } else {  // -inf and NaN alone: s shows the NaN

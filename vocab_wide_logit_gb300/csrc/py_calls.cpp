@@ -185,8 +185,8 @@ PyObject* head(PyObject*, PyObject* const* v, Py_ssize_t count) {
   END_HANDLE_TH_ERRORS
 }
 
-// A contiguous tensor [n] or [n][columns] within the memory of another of elements of the same size: a quarter of what
-// an allocation takes.
+// A contiguous tensor [n] or [n][columns] within the memory of another of the same type: a quarter of what an allocation
+// takes.
 at::Tensor within(const at::Tensor& memory, int64_t first, at::ScalarType type, int64_t n, int64_t columns = -1) {
   auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(memory.storage()), memory.key_set(),
                                                    c10::scalarTypeToTypeMeta(type));
@@ -196,8 +196,8 @@ at::Tensor within(const at::Tensor& memory, int64_t first, at::ScalarType type, 
   return at::Tensor(std::move(impl));
 }
 
-// score(logits, tokens, top) -> (logprobs, lse, entropy, ranks, top ids, top logprobs); the first four share their
-// memory, and the last two, so that a program that keeps the former does not keep the latter
+// score(logits, tokens, top) -> (logprobs, lse, entropy, ranks, top ids, top logprobs). Results of a type share their
+// memory, the alternatives only where they are few: a program that keeps the log-probabilities alone keeps what is with them.
 PyObject* score(PyObject*, PyObject* const* v, Py_ssize_t count) {
   HANDLE_TH_ERRORS
   Rows x;
@@ -212,11 +212,16 @@ PyObject* score(PyObject*, PyObject* const* v, Py_ssize_t count) {
     PyErr_Clear();
     Py_RETURN_NONE;
   }
-  const at::Tensor four = at::empty({4 * x.n}, on(x.device, at::kFloat));
-  const at::Tensor two = top > 0 ? at::empty({2 * x.n * top}, on(x.device, at::kInt)) : four;
-  at::Tensor r[6] = {within(four, 0, at::kFloat, x.n),       within(four, x.n, at::kFloat, x.n),
-                     within(four, 2 * x.n, at::kFloat, x.n), within(four, 3 * x.n, at::kInt, x.n),
-                     within(two, 0, at::kInt, x.n, top),     within(two, top > 0 ? x.n * top : 0, at::kFloat, x.n, top)};
+  const at::TensorOptions f = on(x.device, at::kFloat), i = on(x.device, at::kInt);
+  const int64_t more = x.n * top;
+  const bool few = more <= 2048;
+  const at::Tensor fs = at::empty({3 * x.n + (few ? more : 0)}, f), is = at::empty({x.n + (few ? more : 0)}, i);
+  at::Tensor r[6] = {within(fs, 0, at::kFloat, x.n),
+                     within(fs, x.n, at::kFloat, x.n),
+                     within(fs, 2 * x.n, at::kFloat, x.n),
+                     within(is, 0, at::kInt, x.n),
+                     few ? within(is, x.n, at::kInt, x.n, top) : at::empty({x.n, top}, i),
+                     few ? within(fs, 3 * x.n, at::kFloat, x.n, top) : at::empty({x.n, top}, f)};
   const ds_status rc = p_score(x.p, c, (int32_t)x.n, (int32_t)x.k, x.ld, (const int32_t*)tokens, (int32_t)top,
                                (float*)r[0].data_ptr(), (float*)r[1].data_ptr(), (float*)r[2].data_ptr(),
                                (int32_t*)r[3].data_ptr(), (int32_t*)r[4].data_ptr(), (float*)r[5].data_ptr(), nullptr,
@@ -255,19 +260,25 @@ PyObject* score_grad(PyObject*, PyObject* const* v, Py_ssize_t count) {
   END_HANDLE_TH_ERRORS
 }
 
-// adapters(base, hidden, a, b, scale, ids, gain, eps) -> base with the adapters' part; a, b and scale as the
-// Adapters that hold them were checked
+// A stack of adapters' factors on the device.
+bool stack(const at::Tensor& t, int device) {
+  return t.is_cuda() && t.get_device() == device && t.dim() == 3 && t.scalar_type() == at::kBFloat16 && t.is_contiguous() &&
+         t.numel() > 0;
+}
+
+// adapters(base, hidden, a, b, scale, ids, gain, eps) -> base with the adapters' part
 PyObject* adapters(PyObject*, PyObject* const* v, Py_ssize_t count) {
   HANDLE_TH_ERRORS
   Rows base, x;
   int32_t c, xc;
-  void *ids, *gain;
+  void *ids, *gain, *scale;
   const bool all = count == 8 && p_adapters;
   const at::Tensor *t = all ? tensor(v[0]) : nullptr, *h = all ? tensor(v[1]) : nullptr, *a = all ? tensor(v[2]) : nullptr,
-                   *b = all ? tensor(v[3]) : nullptr, *s = all ? tensor(v[4]) : nullptr;
-  if (!rows(t, &base) || !code(t->scalar_type(), &c) || !rows(h, &x) || !code(h->scalar_type(), &xc) || !a || !b || !s ||
-      a->dim() != 3 || b->dim() != 3 || a->get_device() != base.device || x.n != base.n || x.k != a->size(2) ||
-      base.k != b->size(1) || !vec(v[5], base.n, at::kInt, base.device, false, &ids) ||
+                   *b = all ? tensor(v[3]) : nullptr;
+  if (!rows(t, &base) || !code(t->scalar_type(), &c) || !rows(h, &x) || !code(h->scalar_type(), &xc) || !a || !b ||
+      !stack(*a, base.device) || !stack(*b, base.device) || a->size(0) != b->size(0) || a->size(1) != b->size(2) ||
+      x.n != base.n || x.k != a->size(2) || base.k != b->size(1) || a->size(0) > DS_ADAPTERS_MAX ||
+      a->size(1) > DS_ADAPTERS_MAX_RANK || !vec(v[4], a->size(0), at::kFloat, base.device, false, &scale) || !vec(v[5], base.n, at::kInt, base.device, false, &ids) ||
       !vec(v[6], x.k, at::kFloat, base.device, true, &gain))
     Py_RETURN_NONE;
   const double eps = PyFloat_AsDouble(v[7]);
@@ -288,7 +299,7 @@ PyObject* adapters(PyObject*, PyObject* const* v, Py_ssize_t count) {
   }
   const ds_status rc =
       p_adapters(base.p, c, (int32_t)base.n, (int32_t)base.k, base.ld, x.p, xc, (int32_t)x.k, x.ld, (const float*)gain,
-                 (float)eps, a->const_data_ptr(), b->const_data_ptr(), (const float*)s->const_data_ptr(), L, R,
+                 (float)eps, a->const_data_ptr(), b->const_data_ptr(), (const float*)scale, L, R,
                  (const int32_t*)ids, out.data_ptr(), base.k, work, need, nullptr, stream(base.device));
   return rc != DS_OK ? PyLong_FromLong(rc) : THPVariable_Wrap(std::move(out));
   END_HANDLE_TH_ERRORS

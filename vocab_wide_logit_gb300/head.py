@@ -213,6 +213,24 @@ def _like(out, given, ld, index):
     return out, ldo
 
 
+def _stacks(a, b, scale):
+    """(L, R, K, N) of the stacks of Adapters."""
+    for name, t, what in (("a", a, "[L, R, K]"), ("b", b, "[L, N, R]")):
+        if t.dim() != 3 or t.dtype != _BF16 or not t.is_cuda or not t.is_contiguous() or not t.numel():
+            _bad(name, "a contiguous cuda bfloat16 tensor %s" % what, t)
+    L, R, K = a.shape
+    N = b.shape[1]
+    if b.shape[0] != L or b.shape[2] != R or b.get_device() != a.get_device():
+        _bad("b", "[%d, N, %d] on %s" % (L, R, a.device), b)
+    if scale is None:
+        raise ValueError("scale is needed")
+    _vec("scale", scale, L, _F32, a.get_device())
+    if L > _lib.DS_ADAPTERS_MAX or R > _lib.DS_ADAPTERS_MAX_RANK or max(N, K) > _INT_MAX:
+        raise ValueError("at most %d adapters of rank %d at most, got %d of rank %d" % (
+            _lib.DS_ADAPTERS_MAX, _lib.DS_ADAPTERS_MAX_RANK, L, R))
+    return L, R, K, N
+
+
 class Adapters:
     """Low-rank adapters of one projection, in stacks: a bfloat16 [L, R, K], b bfloat16 [L, N, R], scale float32 [L], all
     contiguous on one device. Adapter i adds scale[i] * b[i] @ (a[i] @ y) to the projection of y. The tensors are used as
@@ -220,19 +238,7 @@ class Adapters:
     zeros. Holds no workspace: calls on several streams may share it."""
 
     def __init__(self, a, b, scale):
-        for name, t, what in (("a", a, "[L, R, K]"), ("b", b, "[L, N, R]")):
-            if t.dim() != 3 or t.dtype != _BF16 or not t.is_cuda or not t.is_contiguous() or not t.numel():
-                _bad(name, "a contiguous cuda bfloat16 tensor %s" % what, t)
-        self.L, self.R, self.K = a.shape
-        self.N = b.shape[1]
-        if b.shape[0] != self.L or b.shape[2] != self.R or b.get_device() != a.get_device():
-            _bad("b", "[%d, N, %d] on %s" % (self.L, self.R, a.device), b)
-        if scale is None:
-            raise ValueError("scale is needed")
-        _vec("scale", scale, self.L, _F32, a.get_device())
-        if self.L > _lib.DS_ADAPTERS_MAX or self.R > _lib.DS_ADAPTERS_MAX_RANK or max(self.N, self.K) > _INT_MAX:
-            raise ValueError("at most %d adapters of rank %d at most, got %d of rank %d" % (
-                _lib.DS_ADAPTERS_MAX, _lib.DS_ADAPTERS_MAX_RANK, self.L, self.R))
+        self.L, self.R, self.K, self.N = _stacks(a, b, scale)
         self.a, self.b, self.scale = a, b, scale
 
 
@@ -251,10 +257,11 @@ def add_adapters(base, hidden, adapters, ids, gain=None, eps=1e-6, out=None, d_s
             return _check("ds_add_adapters", r) if type(r) is int else r
     n, N, ldb, index = _rows("base", base, _CODE)
     rows, K, ldx, at = _rows("hidden", hidden, _CODE)
-    if rows != n or K != adapters.K or at != index:
-        _bad("hidden", "[%d, %d] on cuda:%d" % (n, adapters.K, index), hidden)
-    if N != adapters.N or adapters.a.get_device() != index:
-        _bad("base", "[n, %d] on %s" % (adapters.N, adapters.a.device), base)
+    L, R, inputs, channels = _stacks(adapters.a, adapters.b, adapters.scale)  # as they are now
+    if rows != n or K != inputs or at != index:
+        _bad("hidden", "[%d, %d] on cuda:%d" % (n, inputs, index), hidden)
+    if N != channels or adapters.a.get_device() != index:
+        _bad("base", "[n, %d] on %s" % (channels, adapters.a.device), base)
     if ids is None:
         raise ValueError("ids are needed")
     ip = _vec("ids", ids, n, _I32, index)
@@ -262,11 +269,11 @@ def add_adapters(base, hidden, adapters, ids, gain=None, eps=1e-6, out=None, d_s
     st = _status(d_status, index)
     out, ldo = _like(out, base, ldb, index)
     lib = _lib.load()
-    need = lib.ds_add_adapters_workspace(n, adapters.L, adapters.R)
+    need = lib.ds_add_adapters_workspace(n, L, R)
     ws = torch.empty(need, dtype=_U8, device=base.device)
     _check("ds_add_adapters", lib.ds_add_adapters(
         base.data_ptr(), _CODE[base.dtype], n, N, ldb, hidden.data_ptr(), _CODE[hidden.dtype], K, ldx, gp, eps,
-        adapters.a.data_ptr(), adapters.b.data_ptr(), adapters.scale.data_ptr(), adapters.L, adapters.R, ip,
+        adapters.a.data_ptr(), adapters.b.data_ptr(), adapters.scale.data_ptr(), L, R, ip,
         out.data_ptr(), ldo, ws.data_ptr(), need, st, _lib.raw_stream()))
     return out
 
