@@ -508,7 +508,7 @@ int64_t ds_add_adapters_workspace(int32_t n, int32_t L, int32_t R);
  *   out[i] = base[i] + scale[q] * B[q] (A[q] y[i]),  q = ids[i],
  *   y = x, or x * rsqrt(mean(x^2) + eps) * gain when gain is given
  * with sums in fp32, rounded once to dtype. y and t = A y meet the adapters' bf16 as
- * sums of bf16 parts, of which 2^-27 is lost (fp32 logits) or 2^-18 (bf16 logits). x
+ * sums of bf16 parts, of which 2^-24 is lost (fp32 logits) or 2^-16 (bf16 logits). x
  * is meant to be within 1e-28 and 1e35 in size, or 0: beyond, products of it with the
  * adapters may leave fp32's range before the norm is applied.
  *

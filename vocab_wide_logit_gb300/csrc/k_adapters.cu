@@ -14,22 +14,20 @@
 //                    pairs: t B^T by matrix instructions (16 rows x 8 channels x 16
 //                    ranks), then base and result in whole 16-byte chunks a row.
 // The adapters' bf16 goes into the instructions as it is. The fp32 operand goes in as a
-// sum of bf16 parts, each the rest that the parts before it left: three of them (2^-27
-// of it is lost) for fp32 logits, two (2^-18) for bf16 logits, whose own rounding is
-// 2^-9. Sums are fp32.
+// sum of bf16 parts, each the rest that the parts before it left, off by 2^-8 of it at
+// most: three of them (2^-24 is lost) for fp32 logits, two (2^-16) for bf16 logits, whose
+// own rounding is 2^-8. Sums are fp32.
 //
 // What bounds it is HBM: base, result and the weights once. The weights of a block of
 // channels are one run of bytes whatever the rank, and come to shared memory with the
 // base's chunks by asynchronous copies of 16 bytes, two or three blocks ahead: with the
 // loads of a block in registers instead, 16 warps of 100 registers an SM left the memory
 // idle two thirds of the time. 256 rows x 248320 of rank 64 and 32 adapters: 200 us,
-// 6.4 TB/s; 24 rows of rank 16 and 8 adapters: 26 us, 6 of them for t. A lane takes the ranks that lie together, 8 or 16 bytes,
-// as "its" four of an instruction's 16 (any order of the ranks is right that both operands
-// share). Rows start at any element: a block of channels starts for each row at that
-// row's own 16-byte boundary, for which eight channels in front of the block are
-// computed twice.
-#include <cuda_bf16.h>
-
+// 6.4 TB/s; 24 rows of rank 16 and 8 adapters: 26 us, 6 of them for t. A lane takes the
+// ranks that lie together, 8 or 16 bytes, as "its" four of an instruction's 16 (any order
+// of the ranks is right that both operands share). Rows start at any element: a block of
+// channels starts for each row at that row's own 16-byte boundary, for which eight
+// channels in front of the block are computed twice.
 #include "ds_device.cuh"
 #include "ds_launch.h"
 
