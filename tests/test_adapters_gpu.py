@@ -79,7 +79,8 @@ SIZES = [(1, 1, 1, 1, 1), (1, 1025, 64, 16, 1), (2, 3, 5, 2, 2), (3, 31, 33, 3, 
          (24, 5003, 2048, 16, 8), (31, 640, 1024, 32, 40), (33, 513, 96, 33, 3), (64, 2000, 333, 64, 9), (65, 8200, 1024, 8, 5),
          (100, 300, 200, 100, 7), (128, 1024, 128, 128, 3), (37, 701, 1001, 13, 6), (257, 1025, 512, 24, 6), (600, 264, 160, 48, 2),
          (1939, 1025, 256, 8, 5), (40, 333, 5000, 127, 3), (1030, 77, 64, 1, 300), (4, 70001, 64, 16, 2),
-         (32, 90, 40, 16, 3), (33, 90, 40, 16, 40), (8192, 33, 24, 5, 50), (8193, 33, 24, 5, 50), (20000, 17, 40, 16, 3)]
+         (32, 90, 40, 16, 3), (33, 90, 40, 16, 40), (8192, 33, 24, 5, 50), (8193, 33, 24, 5, 50), (20000, 17, 40, 16, 3), (30, 400, 64, 12, 3),
+         (19, 1025, 64, 20, 3), (21, 600, 48, 36, 4), (18, 300, 64, 68, 3)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -198,14 +199,15 @@ def test_strides(N, pads, offset, dtype):
     assert float((bbuf == 7.0).sum()) == offset + 7 + n * pads[0]
 
 
-@pytest.mark.parametrize("R", [5, 8, 16])
-def test_misaligned_adapters(R):
-    """Stacks that start 2 bytes behind a 16-byte boundary."""
-    base, hidden, ad, ids, _ = _inputs(20, 300, 70, R, 3)
+@pytest.mark.parametrize("R", [5, 8, 16, 32, 40, 128])
+@pytest.mark.parametrize("behind", [1, 2, 4])
+def test_misaligned_adapters(R, behind):
+    """Stacks that start 2, 4 or 8 bytes behind a 16-byte boundary."""
+    base, hidden, ad, ids, _ = _inputs(20, 300, 72, R, 3)
     shifted = []
     for t in (ad.a, ad.b):
-        buf = torch.empty(t.numel() + 1, dtype=t.dtype, device=_dev())
-        shifted.append(buf[1:].view(t.shape))
+        buf = torch.empty(t.numel() + behind, dtype=t.dtype, device=_dev())
+        shifted.append(buf[behind:].view(t.shape))
         shifted[-1].copy_(t)
     got = pkg.add_adapters(base, hidden, pkg.Adapters(*shifted, ad.scale), ids)
     _check(got, base, hidden, ad, ids)

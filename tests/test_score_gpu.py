@@ -311,7 +311,8 @@ def _check_grad(got, x, tokens, lse, entropy, gl, gh):
     # p: exponential 2^-22, its argument three roundings of |log p|; five roundings of terms and sums; the type's own
     # half step; a p below fp32's normal range is 0
     d = logp.abs().clamp(max=110)
-    tol = size * (4 + 3 * d + 6) * 2.0 ** -24 + 2.0 ** -126 * (1 + size)
+    scale = torch.zeros_like(lse) if gl is None else gl.abs().nan_to_num(0)
+    tol = size * (4 + 3 * d + 6) * 2.0 ** -24 + 2.0 ** -126 * (1 + scale.double()[:, None])
     if gh is not None:
         tol = tol + gh.double().abs()[:, None] * 2.0 ** -126 * 256
     if got.dtype == torch.bfloat16:

@@ -42,6 +42,7 @@ constexpr int kDownWarps = kDownThreads / 32;
 constexpr int kDownRanks = 32;     // ranks of a CTA
 constexpr int kPlanThreads = 1024;
 constexpr int kUpThreads = 256;
+constexpr int kWideShare = 10;     // blocks a CTA from which they are wide
 constexpr int kNone = -1, kBad = -2;  // a tile of rows without an adapter, of ids beyond the stack
 
 // Rows of one adapter; count 0: no tile.
@@ -600,11 +601,12 @@ __global__ void __launch_bounds__(kDownThreads) k_adapters_down(const AdapterArg
 }
 
 // ---------------------------------------------------------------- base + t B^T
-// The kernel's sizes. RP: padded ranks.
-template <bool F32, int RP, bool SHIFT>
+// The kernel's sizes. RP: padded ranks. WIDE: blocks of 64 chunks of a row instead of 32,
+// with 16 ranks.
+template <bool F32, int RP, bool SHIFT, bool WIDE>
 struct Up {
   static constexpr int E = F32 ? 4 : 8;                          // logits of a chunk
-  static constexpr int kChunks = RP == 16 && (F32 || !SHIFT) ? 64 : (F32 ? RP <= 64 : RP <= 32) ? 32 : F32 || RP <= 64 ? 16 : 8;  // of a row and block
+  static constexpr int kChunks = WIDE ? 64 : (F32 ? RP <= 64 : RP <= 32) ? 32 : F32 || RP <= 64 ? 16 : 8;  // of a row and block
   static constexpr int kChannels = kChunks * E;                  // of a block
   static constexpr int kGroups = kChannels / 8;                  // of 8 channels
   static constexpr int kFront = SHIFT ? 8 : 0;                   // channels in front of the block
@@ -635,19 +637,18 @@ __device__ __forceinline__ void st16(void* p, uint4 v) {
                : "memory");
 }
 
-// `COUNT` (4 or 8) weights in shared memory from rank i on, zeros from `end` on.
-template <int COUNT, bool VEC>
+// `COUNT` (4 or 8) weights in shared memory from rank i on, zeros from `end` on, PIECE (8, 4
+// or 1) of them a load.
+template <int COUNT, int PIECE>
 __device__ __forceinline__ void shared_weights(const unsigned char* row, int i, int end, uint32_t* w) {
-  if constexpr (VEC) {
-    if (i >= end) {
+  if constexpr (PIECE == 8 && COUNT == 8) {
+    const uint4 v = i < end ? *reinterpret_cast<const uint4*>(row + 2 * i) : make_uint4(0, 0, 0, 0);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (PIECE >= 4) {
 #pragma unroll
-      for (int j = 0; j < COUNT / 2; ++j) w[j] = 0;
-    } else if constexpr (COUNT == 8) {
-      const uint4 v = *reinterpret_cast<const uint4*>(row + 2 * i);
-      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    } else {
-      const uint2 v = *reinterpret_cast<const uint2*>(row + 2 * i);
-      w[0] = v.x, w[1] = v.y;
+    for (int j = 0; j < COUNT / 4; ++j) {
+      const uint2 v = i + 4 * j < end ? *reinterpret_cast<const uint2*>(row + 2 * i + 8 * j) : make_uint2(0, 0);
+      w[2 * j] = v.x, w[2 * j + 1] = v.y;
     }
   } else {
     const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
@@ -659,12 +660,12 @@ __device__ __forceinline__ void shared_weights(const unsigned char* row, int i, 
   }
 }
 
-// VEC: a lane's weights in one load. NEAR: base and result rows lie the same way to
+// PIECE: weights of a load. NEAR: base and result rows lie the same way to
 // 16 bytes. SHIFT: some row starts between two chunks.
-template <bool F32, int RP, bool VEC, bool NEAR, bool SHIFT>
-__global__ void __launch_bounds__(kUpThreads, (Up<F32, RP, SHIFT>::kCtas))
+template <bool F32, int RP, int PIECE, bool NEAR, bool SHIFT, bool WIDE>
+__global__ void __launch_bounds__(kUpThreads, (Up<F32, RP, SHIFT, WIDE>::kCtas))
     k_adapters_up(const AdapterArgs g, const Head* head, const Tile* tiles, const uint8_t* t_in, int blocks) {
-  using U = Up<F32, RP, SHIFT>;
+  using U = Up<F32, RP, SHIFT, WIDE>;
   constexpr int E = U::E, kSize = F32 ? 4 : 2, PARTS = F32 ? 3 : 2, STEPS = RP / 16 / U::kHalves, S = U::kStages, W = U::kChunks;
   constexpr int kLoad = RP == 16 ? 4 : 8;  // weights of a lane and load: one instruction's, or two's
   constexpr int kTurns = (kRows * W + kUpThreads - 1) / kUpThreads;
@@ -816,7 +817,7 @@ __global__ void __launch_bounds__(kUpThreads, (Up<F32, RP, SHIFT>::kCtas))
 #pragma unroll
             for (int h = 0; h < RP / (4 * kLoad); ++h) {
               uint32_t b[kLoad / 2];
-              shared_weights<kLoad, VEC>(row, 4 * kLoad * h + kLoad * q, there ? g.R : 0, b);
+              shared_weights<kLoad, PIECE>(row, 4 * kLoad * h + kLoad * q, there ? g.R : 0, b);
 #pragma unroll
               for (int i = 0; i < kLoad / 4; ++i)
 #pragma unroll
@@ -882,7 +883,7 @@ __global__ void __launch_bounds__(kUpThreads, (Up<F32, RP, SHIFT>::kCtas))
 #pragma unroll
         for (int h = 0; h < STEPS * 4 / kLoad; ++h) {
           uint32_t b[kLoad / 2];
-          shared_weights<kLoad, VEC>(row, 16 * STEPS * half + 4 * kLoad * h + kLoad * q, there ? g.R : 0, b);
+          shared_weights<kLoad, PIECE>(row, 16 * STEPS * half + 4 * kLoad * h + kLoad * q, there ? g.R : 0, b);
 #pragma unroll
           for (int i = 0; i < kLoad / 4; ++i)
 #pragma unroll
@@ -1032,42 +1033,56 @@ cudaError_t launch_down_as(const AdapterArgs& g, bool vec, long long most, Head*
              : launch_down<XF32, PARTS, false, 4>(g, most, head, tiles, t, parts, st);
 }
 
-template <bool F32, int RP, bool VEC, bool NEAR, bool SHIFT>
+template <bool F32, int RP, int PIECE, bool NEAR, bool SHIFT, bool WIDE>
 cudaError_t launch_up(const AdapterArgs& g, long long most, const Head* head, const Tile* tiles, const uint8_t* t,
                       cudaStream_t st) {
-  using U = Up<F32, RP, SHIFT>;
+  using U = Up<F32, RP, SHIFT, WIDE>;
   static_assert(U::kCtas * (U::kSmem + 1024) <= 228 * 1024, "CTAs an SM");
-  auto kern = k_adapters_up<F32, RP, VEC, NEAR, SHIFT>;
+  auto kern = k_adapters_up<F32, RP, PIECE, NEAR, SHIFT, WIDE>;
   const int sms = device_sms();
-  if (sms <= 0 || !allow_smem(kern, U::kSmem)) return cudaErrorUnknown;
-  cudaLaunchAttribute attr;
+  if (sms <= 0) return cudaErrorUnknown;
   const long long blocks = ((long long)g.N + (SHIFT ? U::E - 1 : 0) + U::kChannels - 1) / U::kChannels;
-  const long long items = most * blocks;
-  const long long ctas = (long long)U::kCtas * sms;
+  const long long items = most * blocks, ctas = (long long)U::kCtas * sms;
+  // wide blocks halve what each costs beside its bytes, and leave CTAs with a few of them
+  // in unequal shares: 24 x 248320 (14 a CTA) 25.6 us for 28.2, 1939 x 8200 (7) 22.9 for 22.2
+  if constexpr (WIDE && !F32)
+    if (items < kWideShare * ctas) return launch_up<F32, RP, PIECE, NEAR, SHIFT, false>(g, most, head, tiles, t, st);
+  if (!allow_smem(kern, U::kSmem)) return cudaErrorUnknown;
+  cudaLaunchAttribute attr;
   const dim3 grid((unsigned)(items < ctas ? items : ctas), 1, 1);
   const cudaLaunchConfig_t cfg = config(grid, kUpThreads, U::kSmem, st, &attr);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, g, head, tiles, t, (int)blocks);
   if (e == cudaSuccess) note_launch();
   return e;
 }
-template <bool F32, int RP, bool VEC>
+template <bool F32, int RP, int PIECE>
 cudaError_t launch_up_as(const AdapterArgs& g, bool near, bool shift, long long most, const Head* head, const Tile* tiles,
                          const uint8_t* t, cudaStream_t st) {
-  if (!near) return launch_up<F32, RP, VEC, false, true>(g, most, head, tiles, t, st);
-  return shift ? launch_up<F32, RP, VEC, true, true>(g, most, head, tiles, t, st)
-               : launch_up<F32, RP, VEC, true, false>(g, most, head, tiles, t, st);
+  constexpr bool kWide = RP == 16;  // (rows between chunks have their sums in shared memory: fp32's fit it)
+  if (!near) return launch_up<F32, RP, PIECE, false, true, kWide && F32>(g, most, head, tiles, t, st);
+  return shift ? launch_up<F32, RP, PIECE, true, true, kWide && F32>(g, most, head, tiles, t, st)
+               : launch_up<F32, RP, PIECE, true, false, kWide>(g, most, head, tiles, t, st);
 }
 template <bool F32>
-cudaError_t launch_up_ranks(const AdapterArgs& g, bool vec, bool near, bool shift, long long most, const Head* head,
+cudaError_t launch_up_ranks(const AdapterArgs& g, int piece, bool near, bool shift, long long most, const Head* head,
                             const Tile* tiles, const uint8_t* t, cudaStream_t st) {
-#define DS_UP(RP)                                                                    \
-  return vec ? launch_up_as<F32, RP, true>(g, near, shift, most, head, tiles, t, st) \
-             : launch_up_as<F32, RP, false>(g, near, shift, most, head, tiles, t, st)
+#define DS_UP(RP, PIECE) return launch_up_as<F32, RP, PIECE>(g, near, shift, most, head, tiles, t, st)
   switch (padded(g.R)) {
-    case 16: DS_UP(16);
-    case 32: DS_UP(32);
-    case 64: DS_UP(64);
-    default: DS_UP(128);
+    case 16:
+      if (piece == 1) DS_UP(16, 1);
+      DS_UP(16, 4);
+    case 32:
+      if (piece == 1) DS_UP(32, 1);
+      if (piece == 4) DS_UP(32, 4);
+      DS_UP(32, 8);
+    case 64:
+      if (piece == 1) DS_UP(64, 1);
+      if (piece == 4) DS_UP(64, 4);
+      DS_UP(64, 8);
+    default:
+      if (piece == 1) DS_UP(128, 1);
+      if (piece == 4) DS_UP(128, 4);
+      DS_UP(128, 8);
   }
 #undef DS_UP
 }
@@ -1104,13 +1119,14 @@ cudaError_t launch_add_adapters(const AdapterArgs& g, bool x_f32, bool f32, cuda
     e = f32 ? DS_DOWN(false, 3) : DS_DOWN(false, 2);
 #undef DS_DOWN
   if (e != cudaSuccess) return e;
-  // a lane's weights in one load: 8 bytes, every adapter's stack at such a boundary, or 16
-  const bool vec = padded(g.R) == 16 ? g.R % 4 == 0 && (reinterpret_cast<uintptr_t>(g.b) & 7) == 0 : g.R % 8 == 0 && at16(g.b);
+  // weights that lie together at 16 or 8 bytes in every row of every stack
+  const uintptr_t b = reinterpret_cast<uintptr_t>(g.b);
+  const int piece = g.R % 8 == 0 && (b & 15) == 0 ? 8 : g.R % 4 == 0 && (b & 7) == 0 ? 4 : 1;
   const bool near = ((reinterpret_cast<uintptr_t>(g.base) ^ reinterpret_cast<uintptr_t>(g.out)) & 15) == 0 &&
                     (g.ldb - g.ldo) * s % 16 == 0;
   const bool shift = !at16(g.out) || g.ldo * s % 16 != 0;
-  e = f32 ? launch_up_ranks<true>(g, vec, near, shift, most, head, tiles, t, st)
-          : launch_up_ranks<false>(g, vec, near, shift, most, head, tiles, t, st);
+  e = f32 ? launch_up_ranks<true>(g, piece, near, shift, most, head, tiles, t, st)
+          : launch_up_ranks<false>(g, piece, near, shift, most, head, tiles, t, st);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
