@@ -162,9 +162,10 @@ def test_values_that_are_not_finite_stay_where_they_are():
 
 @pytest.mark.parametrize("scale", [1e-30, 1e-18, 1e18, 1e30])
 @pytest.mark.parametrize("eps", [0.0, 1e-5])
-def test_norm_of_small_and_large_rows(scale, eps):
+@pytest.mark.parametrize("x_dtype,n", [("f32", 20), ("bf16", 20), ("bf16", 50)])
+def test_norm_of_small_and_large_rows(x_dtype, n, scale, eps):
     """Squares that leave fp32's range; a row of zeros."""
-    base, hidden, ad, ids, gain = _inputs(20, 100, 128, 8, 2, x_dtype="f32", norm=True, none=False)
+    base, hidden, ad, ids, gain = _inputs(n, 100, 128, 8, 2, x_dtype=x_dtype, norm=True, none=False)
     hidden *= scale
     hidden[3] = 0
     got = pkg.add_adapters(base, hidden, ad, ids, gain=gain, eps=eps)
@@ -236,7 +237,11 @@ def test_offsets_beyond_32_bits():
 
 def test_a_row_in_other_batches():
     """A row's result does not depend on the rows beside it, nor on the order of the call's work: bit for bit."""
-    base, hidden, ad, ids, gain = _inputs(400, 2003, 320, 24, 40, "f32", norm=True)
+    for R, dtype, norm in ((24, "f32", True), (16, "f32", True), (12, "bf16", True), (16, "bf16", False)):
+        _other_batches(*_inputs(400, 2003, 320, R, 40, dtype, norm=norm))
+
+
+def _other_batches(base, hidden, ad, ids, gain):
     whole = pkg.add_adapters(base, hidden, ad, ids, gain=gain, eps=EPS)
     for i, n in ((0, 1), (5, 20), (100, 33), (0, 300), (0, 400)):
         part = pkg.add_adapters(base[i:i + n], hidden[i:i + n], ad, ids[i:i + n], gain=gain, eps=EPS)
