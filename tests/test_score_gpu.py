@@ -83,7 +83,9 @@ def _inputs(n, V, dtype, seed, spread=3.0):
 
 
 # every launch rule, below and above; the sizes around a chunk, a warp's and a block's share
-SIZES = [(1, 1), (3, 2), (2, 7), (5, 8), (4, 9), (3, 31), (7, 33), (2, 64), (9, 127), (3, 255), (5, 257), (33, 1000), (1, 1025),
+# and a power of two with a few more
+SIZES = [(9, 505), (9, 512), (9, 516), (9, 540), (9, 541), (9, 545), (40, 770), (40, 1017), (40, 1024), (40, 1049), (40, 1050), (40, 1053),
+         (40, 1056), (1, 1), (3, 2), (2, 7), (5, 8), (4, 9), (3, 31), (7, 33), (2, 64), (9, 127), (3, 255), (5, 257), (33, 1000), (1, 1025),
          (700, 1025), (6, 2048), (5, 2049), (3, 4096), (4, 4097), (300, 4099), (2, 8191), (17, 8200), (1, 32000), (170, 32001),
          (37, 70001), (1, 248320), (3, 248319), (160, 248320), (1, 1000003)]
 
@@ -105,7 +107,7 @@ def test_alternatives(top, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("V", [129, 1025, 5000, 40001])
+@pytest.mark.parametrize("V", [129, 1025, 1040, 5000, 40001])
 @pytest.mark.parametrize("kind", ["constant", "zeros", "few", "ascending", "descending", "comb", "one block", "low", "huge",
                                   "tiny", "one", "late"])
 def test_orders_and_ties(kind, V, dtype):
@@ -188,7 +190,7 @@ def test_masks(V, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("V", [17, 1025, 9001, 248320])
+@pytest.mark.parametrize("V", [17, 520, 1025, 1045, 9001, 248320])
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
 def test_rows_that_are_not_numbers(V, bad, dtype):
     x, tokens = _inputs(5, V, dtype, V)

@@ -413,10 +413,13 @@ __device__ __forceinline__ int warp_keep(u64* list, int n, u64 cut) {
   return kept;
 }
 
-// MANY: more than kWarpTop alternatives.
-template <bool F32, int C, bool MANY>
+// MANY: more than kWarpTop alternatives. TAIL: up to 32 logits behind the 32 C chunks, one a
+// lane: vocabularies of a power of two and a few tokens more would have a turn of chunks
+// for one of them.
+template <bool F32, int C, bool MANY, bool TAIL>
 __global__ void __launch_bounds__(kWarps * 32) k_score_warp(const ScoreArgs a) {
   constexpr int E = Row<F32>::E, kWarpList = warp_list(MANY);
+  static_assert(!TAIL || (!MANY && C > 2 && C * E < 64), "a bit for the logit behind the chunks");
   __shared__ u64 lists[kWarps][kWarpList];
   pdl_release();
   pdl_wait();
@@ -431,6 +434,9 @@ __global__ void __launch_bounds__(kWarps * 32) k_score_warp(const ScoreArgs a) {
     const int q = lane + 32 * u;
     v[u] = q < x.nq ? x.chunk(q) : nothing<F32>();
   }
+  const int tail_id = 32 * C * E - x.dc + lane, tail_chunk = 32 * C + lane / E;
+  const bool has_tail = TAIL && tail_id < a.V;
+  const float tail = has_tail ? x.logit(tail_id) : -kInf;
   const Given g = given_token(a, row, x);
   const float near = in_front(x, g);
   // the row's first and last chunk reach beyond it
@@ -452,6 +458,11 @@ __global__ void __launch_bounds__(kWarps * 32) k_score_warp(const ScoreArgs a) {
     const int q = lane + 32 * u;
     if (q < x.nq) r.before += count_before<F32>(v[u], q < g.chunk, g.x);
   }
+  if (TAIL && tail > best) {
+    best = tail;
+    at = tail_chunk;
+  }
+  if (has_tail) r.before += tail_chunk < g.chunk ? tail >= g.x : tail > g.x;
   r.m = warp_max_r(best);
   float2 s = make_float2(0.f, 0.f), t = s;
   if (is_low(r.m)) {
@@ -463,12 +474,18 @@ __global__ void __launch_bounds__(kWarps * 32) k_score_warp(const ScoreArgs a) {
 #pragma unroll
     for (int u = 0; u < C; ++u) add_sums<F32>(v[u], r.m, low2, s, t);
   }
+  if (TAIL && r.m != -kInf) {
+    const float d = tail - r.m, e = ex2_approx(d * kLog2e);
+    s.x += e;
+    t.x += e > 0.f ? e * d : 0.f;
+  }
   r.s = warp_sum(s.x + s.y);
   r.t = warp_sum(t.x + t.y);
   if (r.m == -kInf) {  // a row of NaN and -inf alone: s shows the NaN
     float seen = 0.f;
 #pragma unroll
     for (int u = 0; u < C; ++u) seen += nan_of<F32>(v[u]);
+    if (tail != tail) seen = tail;
     r.s = warp_sum(seen);
   }
   r.before = warp_sum_i(r.before);
@@ -544,10 +561,13 @@ __global__ void __launch_bounds__(kWarps * 32) k_score_warp(const ScoreArgs a) {
     u64 reach = 0;
 #pragma unroll
     for (int u = 0; u < C; ++u) reach |= (u64)reaching<F32>(v[u], bound_x) << (E * u);
+    if (TAIL && tail >= bound_x) reach |= 1ull << (C * E & 63);
     if (!any) reach = 0;
     const int first = lane * E - x.dc;
     while (__any_sync(0xffffffffu, reach != 0)) {
-      const int i = reach ? __ffsll((long long)reach) - 1 : 0, q = lane + 32 * (i / E), id = first + 32 * E * (i / E) + i % E;
+      const int i = reach ? __ffsll((long long)reach) - 1 : 0;
+      int q = lane + 32 * (i / E), id = first + 32 * E * (i / E) + i % E;
+      if (TAIL && i == C * E) q = tail_chunk, id = tail_id;
       const bool in_row = reach && id >= 0 && id < a.V;
       const uint32_t k = order_key((in_row ? x.logit(id) : 0.f) + 0.f);
       const bool in = in_row && (((u64)k << 32) | (uint32_t)~q) >= cut;
@@ -1005,12 +1025,17 @@ cudaError_t launch_rows(const ScoreArgs& a, cudaStream_t st) {
   if (nq <= 32 * 16) {
     const long long blocks = ((long long)a.n + kWarps - 1) / kWarps;
     const int c = (int)((nq + 31) / 32);
-#define DS_WARP(C, MANY) return launch(k_score_warp<F32, C, MANY>, a, blocks, kWarps * 32, 1, st)
+#define DS_WARP(C, MANY) return launch(k_score_warp<F32, C, MANY, false>, a, blocks, kWarps * 32, 1, st)
+#define DS_TAIL(C)                                                                         \
+  if (c >= C && (long long)a.V + E - 1 <= 32 * C * E + 32 && a.top <= kWarpTop)             \
+    return launch(k_score_warp<F32, C, false, true>, a, blocks, kWarps * 32, 1, st)
     if (a.top > kWarpTop) {
       if (c <= 5) DS_WARP(5, true);
       if (c <= 9) DS_WARP(9, true);
       DS_WARP(16, true);
     }
+    DS_TAIL(4);
+    if constexpr (F32) DS_TAIL(8);
     if (c <= 1) DS_WARP(1, false);
     if (c <= 2) DS_WARP(2, false);
     if (c <= 3) DS_WARP(3, false);
@@ -1019,6 +1044,7 @@ cudaError_t launch_rows(const ScoreArgs& a, cudaStream_t st) {
     if (c <= 9) DS_WARP(9, false);
     if (c <= 12) DS_WARP(12, false);
     DS_WARP(16, false);
+#undef DS_TAIL
 #undef DS_WARP
   }
   const int sms = device_sms();
