@@ -368,3 +368,20 @@ def test_example_with_adapters_and_alternatives():
                        text=True, timeout=240)
     assert r.returncode == 0, r.stderr
     assert r.stdout.count("step ") == 2 and r.stdout.count("alternatives") == 2
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [64, 333, 1001])
+@pytest.mark.parametrize("R", [65, 72, 95, 96, 97])
+def test_ranks_that_fill_up_to_128(R, K, dtype):
+    """The last block of 32 ranks has none of R's (but of 97); the last adapter of the stack in use, stacks at a boundary of 16
+    bytes and 2 bytes behind one. What lies behind the stack is in no result."""
+    for n in (5, 40):
+        base, hidden, ad, ids, gain = _inputs(n, 130, K, R, 2, dtype, norm=True, none=False)
+        ids[0] = 1
+        for behind in (0, 1):
+            buf = torch.full((ad.a.numel() + behind + 64 * K,), math.nan, dtype=torch.bfloat16, device=_dev())
+            a = buf[behind:behind + ad.a.numel()].view(ad.a.shape)
+            a.copy_(ad.a)
+            moved = pkg.Adapters(a, ad.b, ad.scale)
+            _check(pkg.add_adapters(base, hidden, moved, ids, gain=gain, eps=EPS), base, hidden, moved, ids, gain)

@@ -1,0 +1,76 @@
+"""Index arithmetic of the kernels (csrc/ds_index.h) on the CPU: every address that it gives lies in what the call was
+given. The program is built so that a signed overflow ends it."""
+import subprocess
+
+import pytest
+
+from vocab_wide_logit_gb300 import build
+
+
+@pytest.fixture
+def run(tmp_path):
+    """Builds and runs a C++ program around the header; it returns 0 or prints what it found."""
+    def go(body):
+        src, exe = tmp_path / "t.cpp", str(tmp_path / "t")
+        src.write_text('#include <cstdio>\n#include <algorithm>\n#include "ds_index.h"\nusing namespace ds;\n' + body)
+        subprocess.run(["g++", "-std=c++17", "-O1", "-fsanitize=signed-integer-overflow",
+                        "-fsanitize-undefined-trap-on-error", "-I", build.CSRC, str(src), "-o", exe], check=True)
+        r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+        assert r.returncode == 0, r.stdout[-2000:] or r.returncode
+    return go
+
+
+def test_adapter_weights_by_words(run):
+    """k_adapters_down reads an adapter's weights by words where rows start anywhere: blocks of 32 ranks up to R filled up
+    to 16, 32, 64 or 128, eight inputs a lane and step. Every word holds an input that counts, every input is in one."""
+    run(r"""
+int main() {
+  int bad = 0;
+  for (int R = 1; R <= 128; ++R)
+    for (int K : {1, 5, 7, 8, 33, 40, 97})
+      for (int front = 0; front < 8; ++front)  // elements between a 16-byte boundary and the stack
+        for (int a = 0; a < 3; ++a) {
+          const int padded = R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128;
+          for (int rank = 0; rank < std::max(padded, 32); ++rank) {
+            const int end = rank < R ? K : 0;
+            for (int i = 0; i < (K + 31) / 32 * 32; i += 8) {
+              const long long at = front + rank_at(a, rank, R, K) + i, word = at >> 1;
+              const int odd = (int)(at & 1);
+              unsigned seen = 0;
+              for (int j = 0; j < 5; ++j) {
+                if (!word_wanted(i, j, odd, end)) continue;
+                int counts = 0;
+                for (int e = 0; e < 2; ++e) {
+                  const long long k = 2 * (word + j) + e - at;  // of the eight
+                  if (k >= 0 && k < 8 && i + k < end) ++counts, seen |= 1u << k;
+                }
+                if (!counts && bad++ < 5) printf("R %d K %d front %d a %d rank %d i %d: word %d\n", R, K, front, a, rank, i, j);
+              }
+              const int some = std::max(0, std::min(8, end - i));
+              if (seen != (1u << some) - 1 && bad++ < 5) printf("R %d K %d rank %d i %d: %x of %d\n", R, K, rank, i, seen, some);
+            }
+          }
+        }
+  return bad != 0;
+}
+""")
+
+
+def test_ranks_that_fill_up_stay_in_the_stack(run):
+    """Where a rank's inputs start is within the stack for every rank that a launch has, and exact beyond 32 bits."""
+    run(r"""
+int main() {
+  int bad = 0;
+  for (int R = 1; R <= 128; ++R)
+    for (int K : {1, 1001, 1 << 30})
+      for (int L : {1, 2, 8192}) {
+        const int padded = R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128;
+        for (int rank = 0; rank < std::max(padded, 32); ++rank) {
+          const long long at = rank_at(L - 1, rank, R, K), first = (long long)(L - 1) * R * K;
+          if ((at < first || at >= first + (long long)R * K || (rank < R && at != first + (long long)rank * K)) && bad++ < 5)
+            printf("R %d K %d L %d rank %d: %lld\n", R, K, L, rank, at);
+        }
+      }
+  return bad != 0;
+}
+""")

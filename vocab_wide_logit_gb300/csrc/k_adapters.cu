@@ -29,6 +29,7 @@
 // channels starts for each row at that row's own 16-byte boundary, for which eight
 // channels in front of the block are computed twice.
 #include "ds_device.cuh"
+#include "ds_index.h"
 #include "ds_launch.h"
 
 namespace ds {
@@ -367,14 +368,14 @@ struct Raw {
 };
 
 // Eight bf16 from i on that start at any 2 bytes, as they are; zeros from `end` on: words
-// of 4 bytes, each of which has one of them.
+// of 4 bytes, each of which has one of those in front of `end`.
 __device__ __forceinline__ void load_any(const uint16_t* row, int i, int end, uint32_t (&w)[4]) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(row + i);
   const int odd = (int)(at >> 1) & 1;
   const uint32_t* p = reinterpret_cast<const uint32_t*>(at & ~(uintptr_t)3);
   uint32_t f[5];
 #pragma unroll
-  for (int j = 0; j < 5; ++j) f[j] = i + 2 * j - odd < end && (j < 4 || odd) ? __ldg(p + j) : 0u;
+  for (int j = 0; j < 5; ++j) f[j] = word_wanted(i, j, odd, end) ? __ldg(p + j) : 0u;
 #pragma unroll
   for (int j = 0; j < 4; ++j) w[j] = odd ? __funnelshift_r(f[j], f[j + 1], 16) : f[j];
   if (i + 8 > end) {
@@ -428,14 +429,13 @@ __global__ void __launch_bounds__(kDownThreads) k_adapters_down(const AdapterArg
   const char* x1 = x + rows[gq + 8] * g.ldx * kSize;
   const int K0 = has0 ? g.K : 0, K1 = has1 ? g.K : 0;
   const int rank0 = blockIdx.y * kDownRanks;
-  const uint16_t* w = g.a + ((long long)a * g.R + rank0) * g.K;
   const uint16_t* wr[GROUPS];
   int Kw[GROUPS];
 #pragma unroll
   for (int j = 0; j < GROUPS; ++j) {
-    const int r = 8 * j + gq;
-    Kw[j] = rank0 + r < g.R ? g.K : 0;
-    wr[j] = w + (Kw[j] ? (long long)r * g.K : 0);
+    const int r = rank0 + 8 * j + gq;
+    Kw[j] = r < g.R ? g.K : 0;  // (of 65 to 96 ranks filled up to 128 the last block has none)
+    wr[j] = g.a + rank_at(a, r, g.R, g.K);
   }
 
   float d[GROUPS][4] = {};
