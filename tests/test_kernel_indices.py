@@ -74,3 +74,29 @@ int main() {
   return bad != 0;
 }
 """)
+
+
+def test_logits_in_front_of_a_token(run):
+    """The ties in front of a token in its own chunk, a lane each: the right ones and none beside the row, for the last tokens
+    of rows of every length up to the largest and every place of a row in its first chunk, and without a token."""
+    run(r"""
+int main() {
+  int bad = 0;
+  for (int E : {4, 8})
+    for (int dc = 0; dc < E; ++dc)
+      for (long long V : {1LL, 2LL, 40LL, 1025LL, 1LL << 30, (1LL << 31) - 64, (1LL << 31) - 33, (1LL << 31) - 9, (1LL << 31) - 8, (1LL << 31) - 2,
+                          (1LL << 31) - 1})
+        for (long long t = std::max(-1LL, V - 70); t < V; ++t) {
+          const int token = (int)t, chunk = token < 0 ? 0 : chunk_of(token, E, dc);
+          const int first = first_in_chunk(chunk, E, dc);
+          const long long start = std::max(0LL, (long long)chunk * E - dc);
+          bool wrong = first != start || (token >= 0 && (token < start || token >= (long long)(chunk + 1LL) * E - dc));
+          for (int lane = 0; lane < 32; ++lane) {
+            const bool in = in_front_of(token, first, lane);
+            wrong |= in != (start + lane < token) || (in && start + lane >= V);
+          }
+          if (wrong && bad++ < 5) printf("E %d dc %d V %lld token %lld\n", E, dc, V, t);
+        }
+  return bad != 0;
+}
+""")

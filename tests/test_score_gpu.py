@@ -275,6 +275,21 @@ def test_one_row_of_the_longest(V, dtype):
         assert abs(float(out[0, i]) - want) <= abs(want) * rel, i
 
 
+@pytest.mark.parametrize("dtype,V", [("bf16", 2 ** 31 - 1), ("bf16", 2 ** 31 - 20), ("f32", 2 ** 31 - 1)])
+def test_last_tokens_of_the_longest_rows(V, dtype):
+    """All logits tie: a token's rank is its number, for the last ones of two rows, the second of which starts between two
+    chunks; the sum of ones is V itself."""
+    x = torch.zeros((2, V), dtype=DT[dtype], device=_dev())
+    for back in (1, 2, 7, 8, 9, 16, 31, 32, 33):
+        tokens = torch.tensor([V - back, V - back - 1], dtype=torch.int32, device=_dev())
+        r = pkg.score_tokens(x, tokens)
+        assert r.ranks.tolist() == tokens.tolist()
+        # V ones in sums of less than V / 16384 + 200 additions, then the logarithm and its sum
+        tol = (V / 16384 + 200) * 2.0 ** -24 + math.log(V) * 2.0 ** -22
+        assert float((r.lse.double() - math.log(V)).abs().max()) <= tol
+        assert float((r.logprobs.double() + math.log(V)).abs().max()) <= tol
+
+
 def test_results_can_be_saved(tmp_path):
     """Results share their memory by type; what a program does with tensors works on them."""
     x, tokens = _inputs(3, 100, "f32", 1)

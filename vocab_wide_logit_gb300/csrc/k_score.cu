@@ -23,6 +23,7 @@
 #include <cooperative_groups.h>
 
 #include "ds_device.cuh"
+#include "ds_index.h"
 #include "ds_launch.h"
 
 namespace cg = cooperative_groups;
@@ -272,15 +273,15 @@ __device__ __forceinline__ Given given_token(const ScoreArgs& a, int row, const 
   if (tok >= 0 && tok < a.V) {
     g.token = tok;
     g.x = x.logit(tok);
-    g.chunk = (int)(((long long)tok + x.dc) / Row<F32>::E);
+    g.chunk = chunk_of(tok, Row<F32>::E, x.dc);
   }
   return g;
 }
 // Lane i: logit i of the token's chunk when that is in front of the token, else NaN.
 template <bool F32>
 __device__ __forceinline__ float in_front(const Row<F32>& x, const Given& g) {
-  const int id = max(0, (int)((long long)g.chunk * Row<F32>::E - x.dc)) + (int)(threadIdx.x & 31);
-  return id < g.token ? x.logit(id) : __int_as_float(0x7fffffff);
+  const int first = first_in_chunk(g.chunk, Row<F32>::E, x.dc), place = (int)(threadIdx.x & 31);
+  return in_front_of(g.token, first, place) ? x.logit(first + place) : __int_as_float(0x7fffffff);
 }
 // What `before` lacks or has too much: ties in front of the token in its own chunk;
 // the padding in front of the row, which ties with a token of -inf. For a whole warp.
