@@ -100,3 +100,40 @@ int main() {
   return bad != 0;
 }
 """)
+
+
+def test_logits_of_a_rows_chunks(run):
+    """Which chunks a row has, what of a chunk is the row's, and where in it the token is: the first and last chunks of rows of
+    every length up to the largest, at every place of a row in its first chunk; one chunk behind the row as a launch may have."""
+    run(r"""
+int main() {
+  int bad = 0;
+  for (int E : {4, 8})
+    for (int dc = 0; dc < E; ++dc)
+      for (long long back = 0; back < 64; ++back)
+        for (long long V : {1 + back, (1LL << 30) - back, (1LL << 31) - 1 - back}) {
+          const long long chunks = (V + 2 * E - 2) / E;  // of a launch
+          for (long long q = 0; q < chunks; q = q == 4 && chunks > 9 ? chunks - 5 : q + 1) {
+            const long long id = q * E - dc;
+            bool wrong = (q < chunks_of((int)V, E, dc)) != (id < V);
+            if (id < V) {
+              const int first = first_of_chunk((unsigned)q, E, dc);
+              int all = 0;
+              for (int i = 0; i < E; ++i) {
+                const bool in = id + i >= 0 && id + i < V;
+                all += in;
+                wrong |= in_row(first, i, (int)V) != in;
+              }
+              wrong |= first != id || all_in_row(first, E, (int)V) != (all == E);
+              for (long long t : {0LL, 1LL, V / 2, V - 9, V - 8, V - 2, V - 1})
+                if (t >= 0) {
+                  const unsigned place = place_of((int)t, first);
+                  wrong |= t >= id && t < id + E ? place != t - id : place < (unsigned)E;
+                }
+            }
+            if (wrong && bad++ < 5) printf("E %d dc %d V %lld chunk %lld\n", E, dc, V, q);
+          }
+        }
+  return bad != 0;
+}
+""")

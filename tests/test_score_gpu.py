@@ -409,6 +409,34 @@ def test_grad_strides(V, pad, offset, opad, ooffset, dtype):
     assert float((buf == 7.0).sum()) == offset + n * pad
 
 
+@pytest.mark.parametrize("bend", [False, True])
+@pytest.mark.parametrize("dtype,V", [("bf16", 2 ** 31 - 1), ("bf16", 2 ** 31 - 8), ("f32", 2 ** 31 - 1)])
+def test_grad_of_the_longest_rows(V, dtype, bend):
+    """Two rows of tied logits, the second of which starts between two chunks: every gradient is written, the first ones and
+    the last ones of both."""
+    lse = torch.full((2,), math.log(V), device=_dev())
+    gl, gh = torch.tensor([1.0, -2.0], device=_dev()), torch.tensor([0.5, 0.25], device=_dev())
+    for tokens in ((V - 1, 3), (0, V - 1)):
+        x = torch.zeros((2, V), dtype=DT[dtype], device=_dev())
+        out = torch.full((2, V), math.nan, dtype=DT[dtype], device=_dev())
+        t = torch.tensor(tokens, dtype=torch.int32, device=_dev())
+        pkg.score_tokens_grad(x, t, lse, lse if bend else None, gl, gh if bend else None, out=out)
+        del x
+        p = math.exp(-float(lse[0]))  # log p + H is 0
+        # p: exponential 2^-22, its argument three roundings of log V; five roundings of terms of up to |gl| + |gh| log V
+        rel = (4 + 3 * math.log(V) + 6) * 2.0 ** -24
+        half = 2.0 ** -8 if dtype == "bf16" else 0.0
+        for i in range(2):
+            want = -p * float(gl[i])
+            tol = p * (abs(float(gl[i])) + (float(gh[i]) * 2 * math.log(V) if bend else 0)) * rel + abs(want) * half * (1 + 2.0 ** -10)
+            hit = float(out[i, tokens[i]])
+            assert abs(hit - float(gl[i]) * (1 - p)) <= abs(float(gl[i])) * (half + 2.0 ** -22)
+            out[i, tokens[i]] = want  # (rounded to the type it stays within the tolerance)
+            least, most = float(out[i].amin()), float(out[i].amax())  # a NaN shows in both
+            assert abs(least - want) <= tol and abs(most - want) <= tol, (i, least, most, want)
+        del out
+
+
 def test_grad_bad_rows():
     x, tokens = _inputs(4, 100, "f32", 1)
     x[1, 5] = math.nan

@@ -27,5 +27,14 @@ constexpr int first_in_chunk(int chunk, int E, int dc) {
 }
 // Whether the logit `place` behind the first one of the token's chunk is in front of the token (-1, in chunk 0: none is).
 constexpr bool in_front_of(int token, int first, int place) { return place < token - first; }
+// Chunks that hold a row of V.
+constexpr unsigned chunks_of(int V, int E, int dc) { return ((unsigned)V + dc + E - 1) / E; }
+// The number of a chunk's first logit, below 0 in front of a row that starts within a chunk. Of a chunk that the row has.
+constexpr int first_of_chunk(unsigned chunk, int E, int dc) { return (int)(chunk * E - dc); }
+// Whether logit i of the chunk whose first one is number `first` is the row's, and whether all E of them are.
+constexpr bool in_row(int first, int i, int V) { return (unsigned)first + i < (unsigned)V; }
+constexpr bool all_in_row(int first, int E, int V) { return first >= 0 && V - first >= E; }
+// Where the token is among the logits from number `first` on: below E if it is in that chunk. Of a token >= 0.
+constexpr unsigned place_of(int token, int first) { return (unsigned)token - (unsigned)first; }
 
 }  // namespace ds

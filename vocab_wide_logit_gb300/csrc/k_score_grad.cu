@@ -18,6 +18,7 @@
 // A row whose lse is -inf (nothing in it) gets zeros; a logit of probability zero
 // gets exactly zero from the entropy, -inf among them.
 #include "ds_device.cuh"
+#include "ds_index.h"
 #include "ds_launch.h"
 
 namespace ds {
@@ -105,8 +106,8 @@ __device__ __forceinline__ uint4 chunk_grad(const uint4& v, const RowGrad& g, in
       f[i] = __fmul2_rn(p, nc);
     }
   }
-  const int at = g.token - first;  // the given token's own part
-  if (g.token >= 0 && (unsigned)at < (unsigned)E) {
+  const unsigned at = place_of(g.token, first);  // the given token's own part
+  if (g.token >= 0 && at < E) {
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) {
       if (at == 2 * i) f[i].x += g.gl;
@@ -129,13 +130,13 @@ __global__ void __launch_bounds__(kThreads) k_score_grad(const ScoreGradArgs a, 
   const long long row0 = first / nq;
   const uint32_t rem = (uint32_t)(first - row0 * nq);
   auto write = [&](char* out, int id0, const uint4& z) {
-    if (id0 >= 0 && a.V - id0 >= E && (reinterpret_cast<uintptr_t>(out) & 15) == 0) {
+    if (all_in_row(id0, E, a.V) && (reinterpret_cast<uintptr_t>(out) & 15) == 0) {
       st16(out, z);
     } else {
       const uint32_t w[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        if (id0 + i < 0 || i >= a.V - id0) continue;
+        if (!in_row(id0, i, a.V)) continue;
         if constexpr (F32)
           reinterpret_cast<uint32_t*>(out)[i] = w[i];
         else
@@ -147,17 +148,18 @@ __global__ void __launch_bounds__(kThreads) k_score_grad(const ScoreGradArgs a, 
     // one row
     const char* x = static_cast<const char*>(a.x) + row0 * a.ld * kSize;
     const int dc = (int)(reinterpret_cast<uintptr_t>(x) & 15) / kSize;
-    const int id0 = (int)((long long)(rem + threadIdx.x) * E - dc);
+    const uint32_t q = rem + threadIdx.x, chunks = chunks_of(a.V, E, dc);
+    const int id0 = first_of_chunk(q, E, dc);
     x += (long long)id0 * kSize;
     uint4 v[kChunks];
 #pragma unroll
     for (int u = 0; u < kChunks; ++u)
-      if (u * kThreads * E < a.V - id0) v[u] = ld16(x + u * kThreads * 16);
+      if (q + u * kThreads < chunks) v[u] = ld16(x + u * kThreads * 16);
     const RowGrad g = row_grad<ENT>(a, (int)row0);
     char* out = static_cast<char*>(a.out) + (row0 * a.ldo + id0) * kSize;
 #pragma unroll
     for (int u = 0; u < kChunks; ++u)
-      if (u * kThreads * E < a.V - id0)
+      if (q + u * kThreads < chunks)
         write(out + u * kThreads * 16, id0 + u * kThreads * E, chunk_grad<F32, ENT>(v[u], g, id0 + u * kThreads * E));
     if (rem == 0 && threadIdx.x == 0 && a.tokens[row0] >= a.V) report(a.d_status, DS_DEV_ERR_PARAM);
     return;
