@@ -438,7 +438,8 @@ ds_status ds_head_i8(const void* x, int32_t dtype, int32_t n, int32_t K, int64_t
  *   entropy = -sum of p log p with p = exp(x - lse) (nats; p = 0 counts nothing),
  *   rank = how many tokens come before the given one in the order (0: the argmax),
  *   top alternatives = the first `top` of the order.
- * Sums are fp32, each over less than V / 16384 + 200 additions.
+ * Sums are fp32, each over less than V / 16384 + 200 additions (more, of ones, which
+ * are exact, where no logit is above -1e38).
  *
  * Arguments:
  *   logits       device [n][V] of dtype, rows ld elements apart (ld >= V), any

@@ -290,6 +290,26 @@ def test_last_tokens_of_the_longest_rows(V, dtype):
         assert float((r.logprobs.double() + math.log(V)).abs().max()) <= tol
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("at_once", [8, 16, 32])
+def test_sums_of_long_rows_in_a_large_batch(at_once, dtype):
+    """More rows than SMs, each long: one logit of 0, the others so low that `at_once` of their exponentials are below half a
+    step of a sum of 1. An addition of no more of them is lost where the sum has the 0; the stated number of additions bounds
+    what is."""
+    n, V = torch.cuda.get_device_properties(0).multi_processor_count + 8, 1 << 24
+    low = torch.tensor(-math.log(at_once) - 24.05 * math.log(2)).to(DT[dtype])
+    e = math.exp(float(low))
+    assert at_once * e < 2.0 ** -24
+    x = torch.full((n, V), float(low), dtype=DT[dtype], device=_dev())
+    x[:, 0] = 0
+    s = 1 + (V - 1) * e
+    r = pkg.score_tokens(x, torch.zeros(n, dtype=torch.int32, device=_dev()))
+    # additions, the exponentials (2^-22, three roundings of their argument), the logarithm and its sum
+    tol = (V / 16384 + 200 + 4 + 3 * abs(float(low)) + 8) * 2.0 ** -24
+    off = max(float((r.lse.double() - math.log(s)).abs().max()), float((r.logprobs.double() + math.log(s)).abs().max()))
+    assert off <= tol, off / tol
+
+
 def test_results_can_be_saved(tmp_path):
     """Results share their memory by type; what a program does with tensors works on them."""
     x, tokens = _inputs(3, 100, "f32", 1)

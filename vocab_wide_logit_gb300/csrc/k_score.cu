@@ -182,7 +182,8 @@ __device__ __forceinline__ void add_sums(const uint4& v, float m, uint32_t low2,
     }
   }
 }
-// The same where m is so low that nothing finite lies 256 below it.
+// The same where m is so low that nothing finite lies 256 below it: logits are 1e31 apart
+// there, each exponential is 0 or 1 and the sums are counts, exact up to 2^24.
 template <bool F32>
 __device__ __noinline__ void add_sums_low(uint4 v, float m, float2& s, float2& t) {
   for (int i = 0; i < Row<F32>::E; ++i) {
@@ -777,12 +778,18 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_block(const ScoreArgs a
           if (q + u * NT < q_hi) before += count_before<F32>(v[u], q + u * NT < g.chunk, g.x);
     }
     if (usual) {
-      // a batch's sums apart: a thread's chain of additions is as long as its batches
+      // a batch's sums apart: a thread's chain of additions is as long as its batches, for fp32
+      // half as long (a batch has half the logits, and its two sums go to one of s.x and s.y in turn)
       float2 bs = make_float2(0.f, 0.f), bt = bs;
 #pragma unroll
       for (int u = 0; u < U; ++u) add_sums<F32>(v[u], m, low2, bs, bt);
-      s = __fadd2_rn(s, bs);
-      t = __fadd2_rn(t, bt);
+      if constexpr (F32) {
+        s = make_float2(s.y, s.x + (bs.x + bs.y));
+        t = make_float2(t.y, t.x + (bt.x + bt.y));
+      } else {
+        s = __fadd2_rn(s, bs);
+        t = __fadd2_rn(t, bt);
+      }
     } else if (m != -kInf) {
       for (int u = 0; u < U; ++u) add_sums_low<F32>(v[u], m, s, t);
     } else {  // -inf and NaN alone: s shows the NaN
