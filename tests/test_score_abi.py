@@ -170,6 +170,35 @@ def test_wrong_tensors_are_refused(launched):
     assert not launched
 
 
+def test_the_head_checks_adapters_before_the_projection(launched):
+    """Stacks that were replaced by others than those that the Adapters were made of: the projection has not run, so that an
+    `out` that was given is as it was."""
+    n, V, K = 4, 16, 32
+
+    def t(*shape, dtype=F32, index=0):
+        return Tensor(shape, dtype, index)
+    head, ids, hidden = _head(V, K, 0), t(n, dtype=I32), t(n, K)
+    for name, stack in (("b", t(3, V, 9, dtype=BF16)), ("b", t(3, V + 1, 8, dtype=BF16)), ("b", t(3, V, 8, dtype=BF16, index=1)),
+                        ("b", t(3, V, 8)), ("a", t(2, 8, K, dtype=BF16)), ("a", t(3, 8, K + 1, dtype=BF16)), ("scale", t(2)),
+                        ("scale", None)):
+        ad = _adapters(3, 8, K, V, 0)
+        setattr(ad, name, stack)
+        for call in (lambda: head.logits(hidden, out=t(n, V, dtype=BF16), adapters=ad, adapter_ids=ids),
+                     lambda: head.sample(hidden, t(n), t(n), adapters=ad, adapter_ids=ids),
+                     lambda: head.score(hidden, ids, adapters=ad, adapter_ids=ids)):
+            with pytest.raises(ValueError):
+                call()
+            assert not launched, name
+
+
+def test_stacks_larger_than_the_library_takes():
+    """2^30 inputs and channels at most: refused when the stacks are put together, not at the first call."""
+    big = (1 << 30) + 1
+    for a, b in (((1, 1, big), (1, 4, 1)), ((1, 1, 4), (1, big, 1))):
+        with pytest.raises(ValueError, match="1073741824"):
+            pkg.Adapters(Tensor(a, BF16), Tensor(b, BF16), Tensor((1,), F32))
+
+
 def test_results_beside_the_input_are_taken(launched):
     """Rows side by side in one buffer, and right behind the input."""
     n, V = 4, 16

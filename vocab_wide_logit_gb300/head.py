@@ -13,6 +13,7 @@ from . import _lib
 
 _F32, _I32, _I8, _U8, _BF16 = torch.float32, torch.int32, torch.int8, torch.uint8, torch.bfloat16
 _INT_MAX = 2 ** 31 - 1
+_ADAPTERS_MAX_SIZE = 2 ** 30
 _CODE = {_F32: _lib.DS_DTYPE_F32, _BF16: _lib.DS_DTYPE_BF16}
 
 
@@ -225,9 +226,9 @@ def _stacks(a, b, scale):
     if scale is None:
         raise ValueError("scale is needed")
     _vec("scale", scale, L, _F32, a.get_device())
-    if L > _lib.DS_ADAPTERS_MAX or R > _lib.DS_ADAPTERS_MAX_RANK or max(N, K) > _INT_MAX:
-        raise ValueError("at most %d adapters of rank %d at most, got %d of rank %d" % (
-            _lib.DS_ADAPTERS_MAX, _lib.DS_ADAPTERS_MAX_RANK, L, R))
+    if L > _lib.DS_ADAPTERS_MAX or R > _lib.DS_ADAPTERS_MAX_RANK or max(N, K) > _ADAPTERS_MAX_SIZE:
+        raise ValueError("at most %d adapters of rank %d at most on at most %d inputs and channels, got %d of rank %d on %d and %d" % (
+            _lib.DS_ADAPTERS_MAX, _lib.DS_ADAPTERS_MAX_RANK, _ADAPTERS_MAX_SIZE, L, R, K, N))
     return L, R, K, N
 
 
@@ -240,6 +241,34 @@ class Adapters:
     def __init__(self, a, b, scale):
         self.L, self.R, self.K, self.N = _stacks(a, b, scale)
         self.a, self.b, self.scale = a, b, scale
+
+
+def _adapter_inputs(n, N, index, hidden, adapters, ids, gain, d_status):
+    """Checks what goes with a base [n, N] on a device: (elements between hidden's rows, L, R, and the addresses of ids, gain and
+    status)."""
+    rows, K, ldx, at = _rows("hidden", hidden, _CODE)
+    L, R, inputs, channels = _stacks(adapters.a, adapters.b, adapters.scale)  # as they are now
+    if rows != n or K != inputs or at != index:
+        _bad("hidden", "[%d, %d] on cuda:%d" % (n, inputs, index), hidden)
+    if N != channels or adapters.a.get_device() != index:
+        _bad("adapters", "of a projection [%d, %d] on cuda:%d" % (N, K, index), adapters.b)
+    if ids is None:
+        raise ValueError("ids are needed")
+    return (ldx, L, R, _vec("ids", ids, n, _I32, index), _vec("gain", gain, K, _F32, index), _status(d_status, index))
+
+
+def _add_adapters(base, ldb, hidden, adapters, inputs, eps, out, ldo):
+    """The launch, of checked tensors; inputs: what _adapter_inputs() returned."""
+    ldx, L, R, ids, gain, status = inputs
+    n, N = base.shape
+    lib = _lib.load()
+    need = lib.ds_add_adapters_workspace(n, L, R)
+    ws = torch.empty(need, dtype=_U8, device=base.device)
+    _check("ds_add_adapters", lib.ds_add_adapters(
+        base.data_ptr(), _CODE[base.dtype], n, N, ldb, hidden.data_ptr(), _CODE[hidden.dtype], hidden.shape[1], ldx, gain, eps,
+        adapters.a.data_ptr(), adapters.b.data_ptr(), adapters.scale.data_ptr(), L, R, ids,
+        out.data_ptr(), ldo, ws.data_ptr(), need, status, _lib.raw_stream()))
+    return out
 
 
 def add_adapters(base, hidden, adapters, ids, gain=None, eps=1e-6, out=None, d_status=None, stream=None):
@@ -256,26 +285,9 @@ def add_adapters(base, hidden, adapters, ids, gain=None, eps=1e-6, out=None, d_s
         if r is not None:
             return _check("ds_add_adapters", r) if type(r) is int else r
     n, N, ldb, index = _rows("base", base, _CODE)
-    rows, K, ldx, at = _rows("hidden", hidden, _CODE)
-    L, R, inputs, channels = _stacks(adapters.a, adapters.b, adapters.scale)  # as they are now
-    if rows != n or K != inputs or at != index:
-        _bad("hidden", "[%d, %d] on cuda:%d" % (n, inputs, index), hidden)
-    if N != channels or adapters.a.get_device() != index:
-        _bad("base", "[n, %d] on %s" % (channels, adapters.a.device), base)
-    if ids is None:
-        raise ValueError("ids are needed")
-    ip = _vec("ids", ids, n, _I32, index)
-    gp = _vec("gain", gain, K, _F32, index)
-    st = _status(d_status, index)
+    inputs = _adapter_inputs(n, N, index, hidden, adapters, ids, gain, d_status)
     out, ldo = _like(out, base, ldb, index)
-    lib = _lib.load()
-    need = lib.ds_add_adapters_workspace(n, L, R)
-    ws = torch.empty(need, dtype=_U8, device=base.device)
-    _check("ds_add_adapters", lib.ds_add_adapters(
-        base.data_ptr(), _CODE[base.dtype], n, N, ldb, hidden.data_ptr(), _CODE[hidden.dtype], K, ldx, gp, eps,
-        adapters.a.data_ptr(), adapters.b.data_ptr(), adapters.scale.data_ptr(), L, R, ip,
-        out.data_ptr(), ldo, ws.data_ptr(), need, st, _lib.raw_stream()))
-    return out
+    return _add_adapters(base, ldb, hidden, adapters, inputs, eps, out, ldo)
 
 
 class Int8Head:
@@ -304,12 +316,11 @@ class Int8Head:
             # checked before the projection runs: a refused call leaves out as it was
             if adapter_ids is None:
                 raise ValueError("adapter_ids are needed")
-            n, K, _, index = _rows("hidden", hidden, _CODE)
-            _vec("adapter_ids", adapter_ids, n, _I32, index)
-            if adapters.N != self.weight.N or adapters.K != self.weight.K or adapters.a.get_device() != index:
-                _bad("adapters", "of a projection [%d, %d] on cuda:%d" % (self.weight.N, self.weight.K, index), adapters.b)
+            n, _, _, index = _rows("hidden", hidden, _CODE)
+            inputs = _adapter_inputs(n, self.weight.N, index, hidden, adapters, adapter_ids, self.gain, d_status)
             out = self.logits(hidden, out, dtype, d_status)
-            return add_adapters(out, hidden, adapters, adapter_ids, self.gain, self.eps, out, d_status)
+            ldo = out.stride(0) if n > 1 else self.weight.N
+            return _add_adapters(out, ldo, hidden, adapters, inputs, self.eps, out, ldo)
         if adapter_ids is not None:
             raise ValueError("adapter_ids without adapters")
         if out is None and d_status is None and dtype in _CODE:
