@@ -483,6 +483,24 @@ def test_a_row_in_other_batches(V):
         assert torch.equal(a, b)  # run to run: bit for bit
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [1025, 20011, 100003])
+def test_float_results_in_other_batches(V, dtype):
+    """The batch decides how many threads and CTAs a row has: log-probabilities, sums and entropies of each batch are as near
+    to the definition, so that those of two batches differ by twice that at most."""
+    x, tokens = _inputs(320, V, dtype, V)
+    whole = pkg.score_tokens(x, tokens, top=16)
+    _check(x, tokens, 16, whole)
+    rel = _sum_tolerance(V, math.log(V))
+    z = rel + (whole.lse.double().abs() + math.log(V)) * 2.0 ** -22  # as in _check()
+    for i, n in ((0, 1), (3, 2), (7, 40), (20, 100), (100, 160)):
+        part = pkg.score_tokens(x[i:i + n], tokens[i:i + n], top=16)
+        _check(x[i:i + n], tokens[i:i + n], 16, part)
+        for a, b, tol in ((part.lse, whole.lse, z), (part.entropy, whole.entropy, (2 + 2 * math.log(V)) * rel + 0 * z),
+                          (part.logprobs, whole.logprobs, z + whole.logprobs.double().abs() * 2.0 ** -24)):
+            assert bool(((a.double() - b[i:i + n].double()).abs() <= 2 * tol[i:i + n]).all())
+
+
 def test_no_rows():
     x = torch.empty((0, 50), dtype=torch.bfloat16, device=_dev())
     none = torch.empty(0, dtype=torch.int32, device=_dev())
