@@ -93,47 +93,15 @@ __device__ __forceinline__ float load(const void* p, long long i) {
     return __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p) + i) << 16);
 }
 
-// Eight inputs from k on, zeros from K on. VEC: at a 16-byte boundary, K a multiple of 8.
-template <bool F32, bool VEC>
+// Eight fp32 from k on that start at any 4 bytes, zeros from K on.
 __device__ __forceinline__ void load8(const void* row, int k, int K, float (&f)[8]) {
-  if constexpr (VEC) {
-    if (k >= K) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = 0.f;
-    } else if constexpr (F32) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(row) + k));
-      const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(row) + k) + 1);
-      f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-    } else {
-      unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + k)), f);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = k + i < K ? load<F32>(row, k + i) : 0.f;
-  }
+  for (int i = 0; i < 8; ++i) f[i] = k + i < K ? load<true>(row, k + i) : 0.f;
 }
-// `count` (4 or 8) weights as they are, from i on, zeros from `end` on.
-template <int COUNT, bool VEC>
-__device__ __forceinline__ void load_weights(const uint16_t* row, int i, int end, uint32_t (&w)[COUNT / 2]) {
-  if constexpr (VEC) {
-    if (i >= end) {
-#pragma unroll
-      for (int j = 0; j < COUNT / 2; ++j) w[j] = 0;
-    } else if constexpr (COUNT == 8) {
-      const uint4 v = ld_stream16(row + i);
-      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    } else {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + i));
-      w[0] = v.x, w[1] = v.y;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < COUNT / 2; ++j) {
-      const uint32_t lo = i + 2 * j < end ? __ldg(row + i + 2 * j) : 0u;
-      const uint32_t hi = i + 2 * j + 1 < end ? __ldg(row + i + 2 * j + 1) : 0u;
-      w[j] = lo | (hi << 16);
-    }
-  }
+// Eight weights of 16 bytes as they are, zeros from `end` on.
+__device__ __forceinline__ void load_weights(const uint16_t* row, int i, int end, uint32_t (&w)[4]) {
+  const uint4 v = i < end ? ld_stream16(row + i) : make_uint4(0, 0, 0, 0);
+  w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
 }
 
 // ---------------------------------------------------------------- tiles
@@ -494,7 +462,7 @@ __global__ void __launch_bounds__(kDownThreads) k_adapters_down(const AdapterArg
         r0[i].load(x0, k, K0);
         r1[i].load(x1, k, K1);
 #pragma unroll
-        for (int j = 0; j < GROUPS; ++j) load_weights<8, true>(wr[j], k, Kw[j], b[i][j]);
+        for (int j = 0; j < GROUPS; ++j) load_weights(wr[j], k, Kw[j], b[i][j]);
         if (g.gain) rn[i].load(reinterpret_cast<const char*>(g.gain), k, g.K);
       }
 #pragma unroll
@@ -514,8 +482,8 @@ __global__ void __launch_bounds__(kDownThreads) k_adapters_down(const AdapterArg
       float f0[8], f1[8], n8[8];
       uint32_t b[GROUPS][4];
       if constexpr (XF32) {
-        load8<true, false>(x0, k, K0, f0);
-        load8<true, false>(x1, k, K1, f1);
+        load8(x0, k, K0, f0);
+        load8(x1, k, K1, f1);
       } else {
         uint32_t w0[4], w1[4];
         load_any(reinterpret_cast<const uint16_t*>(x0), k, K0, w0);
@@ -525,7 +493,7 @@ __global__ void __launch_bounds__(kDownThreads) k_adapters_down(const AdapterArg
       }
 #pragma unroll
       for (int j = 0; j < GROUPS; ++j) load_any(wr[j], k, Kw[j], b[j]);
-      load8<true, false>(g.gain, k, g.gain ? g.K : 0, n8);
+      load8(g.gain, k, g.gain ? g.K : 0, n8);
       take(f0, f1, n8, b);
     }
   }

@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_score_warp(const ScoreArgs a) {
 // 20 alternatives (3.6 TB/s): 22.5 us are loads and maxima, 3 the exponentials, up to 4
 // the rank of unlikely tokens, 5.5 the alternatives. 37 x 70001 fp32, four CTAs a row:
 // 12 us, latency.
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = 8;
 // Candidates a slice may list: `top` chunks of 8 logits for each thread of a group.
 __host__ __device__ constexpr int list_size(int threads) { return threads >= 512 ? 2048 : 1024; }
 constexpr int kLong = 160;     // entries from which the exact cut is cheaper than ranking all
@@ -1064,7 +1064,7 @@ cudaError_t launch_rows(const ScoreArgs& a, cudaStream_t st) {
   }
   // slices of at least 4.5 chunks a thread while all CTAs run at once
   int cs = 1;
-  while (cs < 8 && nq / (2 * cs) >= 2304 && 2LL * a.n * cs <= 2LL * sms) cs *= 2;
+  while (cs < kMaxCluster && nq / (2 * cs) >= 2304 && 2LL * a.n * cs <= 2LL * sms) cs *= 2;
   return launch(k_score_block<F32, 512>, a, (long long)a.n * cs, 512, cs, st);
 }
 
