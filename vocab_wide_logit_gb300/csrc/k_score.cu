@@ -202,8 +202,9 @@ __device__ __noinline__ float nan_of(uint4 v) {
   }
   return n;
 }
-// What the clamp of bf16 logits may not fall below: more than 200 under m, whatever
-// the rounding to bf16 (2^-9 of it, an eighth of the distance for large m).
+// What the clamp of bf16 logits may not fall below: 192 under m or more, whatever the
+// rounding to bf16 (up to 2^-8 of it, a quarter of the distance for large m). The
+// exponential of -104 is 0 already.
 __device__ __forceinline__ uint32_t low_of(float m) { return bf2(m - fmaxf(256.f, fabsf(m) * 0.015625f)); }
 __device__ __forceinline__ bool is_low(float m) { return m < -1e38f; }
 
@@ -415,8 +416,11 @@ __device__ __forceinline__ int warp_keep(u64* list, int n, u64 cut) {
 }
 
 // MANY: more than kWarpTop alternatives. TAIL: up to 32 logits behind the 32 C chunks, one a
-// lane: vocabularies of a power of two and a few tokens more would have a turn of chunks
-// for one of them.
+// lane, where lengths just above 32 C chunks would have a turn of chunks for a few of them.
+// Launched for bf16 rows of 762 to 1049 logits (C = 4) and fp32 rows of 382 to 541 (C = 4) and
+// 894 to 1053 (C = 8); other lengths take the next C that holds them. It needs the loop
+// over a lane's bits (C > 2) and a bit of the 64 beside theirs (C E < 64): there is none for
+// 513 bf16 logits, nor for 2049.
 template <bool F32, int C, bool MANY, bool TAIL>
 __global__ void __launch_bounds__(kWarps * 32) k_score_warp(const ScoreArgs a) {
   constexpr int E = Row<F32>::E, kWarpList = warp_list(MANY);

@@ -70,7 +70,8 @@ __device__ __forceinline__ RowGrad row_grad(const ScoreGradArgs& a, int r) {
   if constexpr (ENT) {
     g.h = a.g_entropy[r];
     g.c = __fmaf_rn(g.h, a.entropy[r], g.gl);
-    // more than 200 below lse whatever the rounding to bf16 (2^-9 of it, an eighth of the distance for large lse)
+    // 192 below lse or more whatever the rounding to bf16 (up to 2^-8 of it, a quarter of the distance for large lse): the
+    // exponential is 0 there
     const float low = g.lse - fmaxf(256.f, fabsf(g.lse) * 0.015625f);
     g.low2 = pack_bf(low, low);
   }

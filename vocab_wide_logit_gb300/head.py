@@ -274,9 +274,11 @@ def _add_adapters(base, ldb, hidden, adapters, inputs, eps, out, ldo):
 def add_adapters(base, hidden, adapters, ids, gain=None, eps=1e-6, out=None, d_status=None, stream=None):
     """Each row's low-rank adapter added to the logits of a projection that all rows share: base [n, N] (bfloat16 or
     float32) + scale B (A y) with the Adapters entry ids[row] (int32 [n], any order, -1 for none), y the hidden states
-    [n, K] (bfloat16 or float32), RMS-normed with gain (float32 [K]) and eps when that is given. Computed in float32 and
-    rounded once to base's type. out: such a tensor (rows may lie apart), base itself to add in place; allocated when
-    None. An id beyond the stack gives a row of NaN and a bit in d_status."""
+    [n, K] (bfloat16 or float32), RMS-normed with gain (float32 [K]) and eps when that is given. Sums are float32, rounded once
+    to base's type; y and A y meet the adapters' bfloat16 as sums of bfloat16 parts that lose 2^-24 of them for float32 base
+    and 2^-16 for bfloat16. out: such a tensor (rows may lie apart), base itself to add in place; allocated when None, up to
+    an eighth of it more in memory than it shows (the workspace lies behind it). An id beyond the stack gives a row of NaN and
+    a bit in d_status. Not recorded by autograd."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return add_adapters(base, hidden, adapters, ids, gain, eps, out, d_status)

@@ -2,8 +2,8 @@
 alternatives, and the gradient of what was scored with respect to the logits.
 
 Functions check their tensors and allocate their outputs on the stream that the call runs on, as those of the serving
-head do, and the usual calls go through _lib.calls() as theirs; the compute is in the library. Nothing here is recorded by autograd: score_tokens_grad() is the backward pass,
-called with what the forward pass returned.
+head do, and the usual calls go through _lib.calls() as theirs; the compute is in the library. Nothing here is recorded by
+autograd: score_tokens_grad() is the backward pass, called with what the forward pass returned.
 """
 from typing import NamedTuple
 
@@ -34,7 +34,9 @@ def score_tokens(logits, tokens, top=0, d_status=None, stream=None):
     """Scores of one given token per row of logits [n, V] (bfloat16 or float32, cuda, rows may lie apart): its
     log-probability and its rank (0: the argmax), the row's log-sum-exp and entropy, and the `top` most likely tokens with
     their log-probabilities. tokens: int32 [n], -1 for none (logprob NaN, rank -1). Returns TokenScores; a row with
-    nothing in it, a NaN or +inf gives NaN and -1, the last two and a token >= V with a bit in d_status."""
+    nothing in it (lse -inf), a NaN or +inf gives NaN and -1, the last two and a token >= V with a bit in d_status. Not recorded by
+    autograd, whether or not logits require a gradient: score_tokens_grad() makes it. Results may share their memory by
+    type: one that is kept or saved keeps or saves those beside it, unless it is cloned."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return score_tokens(logits, tokens, top, d_status)
